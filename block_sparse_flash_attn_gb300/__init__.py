@@ -29,6 +29,7 @@ BLOCK = 128
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_OOM, ERR_TIMEOUT, ERR_INTERNAL = range(7)
 ERR_SCRATCH_LIMIT = 7
 ERR_RANGE = 8
+ERR_PAGE = 9
 CAUSAL, OUT_F32, MASK_SHARED_HEADS, KEY_BLOCK_64 = 1, 2, 4, 8
 
 EXPORTS = ["bsattn_plan", "bsattn_plan_csr", "bsattn_plan_schedule", "bsattn_fwd",
@@ -36,7 +37,11 @@ EXPORTS = ["bsattn_plan", "bsattn_plan_csr", "bsattn_plan_schedule", "bsattn_fwd
            "bsattn_selftest_wait_timeout", "bsattn_fwd_noalloc", "bsattn_pipeline_create",
            "bsattn_pipeline_run", "bsattn_pipeline_status", "bsattn_pipeline_free",
            "bsattn_plan_csc", "bsattn_bwd", "bsattn_fwd_gqa", "bsattn_bwd_gqa",
-           "bsattn_fwd_fp8", "bsattn_plan_v16"]
+           "bsattn_fwd_fp8", "bsattn_plan_v16", "bsattn_rope_table", "bsattn_qk_norm_rope",
+           "bsattn_qk_norm_rope_bwd", "bsattn_qk_norm_rope_bwd_workspace",
+           "bsattn_select_blocks", "bsattn_select_blocks_workspace", "bsattn_kv4_append",
+           "bsattn_kv4_read", "bsattn_kv4_select", "bsattn_kv4_select_workspace",
+           "bsattn_kv4_attn", "bsattn_kv4_attn_workspace", "bsattn_kv4_status"]
 
 
 class BsattnError(RuntimeError):
@@ -111,6 +116,29 @@ def load():
     lib.bsattn_pipeline_status.restype = i32
     lib.bsattn_pipeline_free.argtypes = [vp]
     lib.bsattn_pipeline_free.restype = None
+    f32, size = ctypes.c_float, ctypes.c_size_t
+    table = [vp, i64, i32]  # block table, row stride, columns
+    rope = [vp, vp, vp, i32, i32, vp, f32, u32]  # weights, angle table, its sizes, positions, eps, flags
+    for name, args, res in (
+            ("rope_table", [vp, i32, i32, vp, vp], i32),
+            ("qk_norm_rope", [vp, i64, i64] + [i32] * 5 + rope + [vp] * 4, i32),
+            ("qk_norm_rope_bwd", [vp, i64, i64, vp, vp, vp] + [i32] * 5 + rope
+             + [vp, i64, i64, vp, vp, vp, size, vp], i32),
+            ("qk_norm_rope_bwd_workspace", [i32] * 5, size),
+            ("select_blocks", [vp, vp] + [i32] * 8 + [u32, vp, i32, vp, vp, size, vp], i32),
+            ("select_blocks_workspace", [i32] * 5 + [u32], size),
+            ("kv4_append", [vp, vp, i64, i64, i64, vp, i64, i64, i64, i32, i32] + table
+             + [vp, vp, vp], i32),
+            ("kv4_read", [vp, i32, i32] + table + [vp] * 5, i32),
+            ("kv4_select", [vp, vp, i32, i32, i32] + table + [vp, i32, i32, i32, vp, vp, size, vp],
+             i32),
+            ("kv4_select_workspace", [i32] * 3, size),
+            ("kv4_attn", [vp, vp, i32, i32, i32] + table + [vp, vp, i32, f32, u32, vp, vp, vp, size,
+                                                            vp], i32),
+            ("kv4_attn_workspace", [i32] * 5, size),
+            ("kv4_status", [vp, vp], i32)):
+        fn = getattr(lib, "bsattn_" + name)
+        fn.argtypes, fn.restype = args, res
     _lib = lib
     return lib
 
@@ -501,3 +529,10 @@ def attention(q, k, v, mask, causal: bool = False, scale: float | None = None,
     finally:
         torch.cuda.current_stream().synchronize()
         p.close()
+
+
+# the operators around the attention (they use the names above)
+from .blocks import select_blocks  # noqa: E402
+from .kv4 import (Kv4Cache, kv4_append, kv4_attn, kv4_read, kv4_select,  # noqa: E402
+                  kv4_status)
+from .rope import qk_norm_rope, qk_norm_rope_bwd, rope_table  # noqa: E402

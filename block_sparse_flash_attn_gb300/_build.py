@@ -18,8 +18,9 @@ _INC = os.path.join(_ROOT, "include")
 LIBDIR = os.path.join(_PKG, "_lib")
 LIB = os.path.join(LIBDIR, "libbsattn.so")
 
-SOURCES = ["api.cu", "plan.cu", "fwd_sm103.cu", "bwd_sm103.cu", "noalloc.cu", "pipeline.cu"]
-HEADERS = ["ptx.cuh", "internal.h", "bwd.h"]
+SOURCES = ["api.cu", "plan.cu", "fwd_sm103.cu", "bwd_sm103.cu", "noalloc.cu", "pipeline.cu",
+           "rope.cu", "select.cu", "kv4.cu", "kv4_attn.cu"]
+HEADERS = ["ptx.cuh", "internal.h", "bwd.h", "ops.cuh", "kv4.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

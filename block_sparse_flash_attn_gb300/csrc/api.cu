@@ -246,6 +246,7 @@ const char* bsattn_status_string(bsattn_status s) {
     case BSATTN_ERR_INTERNAL: return "internal error detected on device";
     case BSATTN_ERR_SCRATCH_LIMIT: return "problem exceeds the no-allocation scratch size";
     case BSATTN_ERR_RANGE: return "input value out of the supported range (D = 64: |V| <= 65504)";
+    case BSATTN_ERR_PAGE: return "a page outside the cache or the table, or a page list out of order";
   }
   return "unknown status";
 }

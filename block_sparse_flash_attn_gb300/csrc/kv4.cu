@@ -1,0 +1,614 @@
+// The paged key/value cache in 4 bits: writing new tokens into it, reading
+// tokens back, and choosing pages for a query.  (Attention over it:
+// kv4_attn.cu.)
+//
+// Per (token, head) row and group of g channels (g = 32, 64 or 128):
+//   minimum = min x,  step = bf16((max x - min x) / 15),
+//   code = (x - minimum) / step rounded to the nearest whole number, half to even,
+//   value = step * code + minimum.
+// The minimum is one of the inputs, so bf16 holds it exactly; the step's
+// rounding is part of the format (codes are taken with the rounded step).  A
+// group whose step is below 2^-100 counts as constant (codes 0); a group with
+// a NaN or an infinity, or whose range overflows, decodes to NaN.
+#include <cmath>
+#include <cstdint>
+
+#include "kv4.cuh"
+
+namespace bsattn {
+namespace {
+
+constexpr int kRowThreads = 128;  // write_rounded_mean takes a CTA of 128
+constexpr int kRowWarps = kRowThreads / 32;
+constexpr int kReadRows = 4;      // rows a lane group reads back at once
+constexpr float kLeastStep = 7.888609e-31f;  // 2^-100
+
+struct AppendParams {
+  Kv4View c;
+  const uint16_t* k;  // [B][Hkv][T][D], strides in elements
+  const uint16_t* v;
+  int64_t kb, kh, kt, vb, vh, vt;
+  const int* table;
+  int64_t table_stride;
+  int columns;
+  const int* lengths;
+  const int* counts;  // null: T each
+  int T;
+};
+
+// Eight channels of one group's row -> codes (a nibble each, the first
+// lowest), and the group's step and minimum.  GL lanes hold a group.
+//
+// (x - minimum) / step is first estimated with the reciprocal, then settled
+// by its exact remainder: r = d - n step is exact in 32 bits (|r| <= step),
+// and |r| against step / 2 says whether n is the nearest, so codes do not
+// depend on how a division rounds.
+template <int GL>
+__device__ __forceinline__ uint32_t quantise(const float (&x)[8], float& step, float& least) {
+  float mn = x[0], mx = x[0], z = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    mn = fminf(mn, x[i]);
+    mx = fmaxf(mx, x[i]);
+    z += x[i] * 0.0f;  // NaN for a value that is not finite
+  }
+  if (z != 0.0f) mx = INFINITY;
+#pragma unroll
+  for (int o = 1; o < GL; o <<= 1) {
+    mn = fminf(mn, __shfl_xor_sync(0xFFFFFFFFu, mn, o));
+    mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+  }
+  const float range = mx - mn;
+  step = __bfloat162float(__float2bfloat16_rn(__fdiv_rn(range, 15.0f)));
+  least = mn;
+  if (!(range <= 3.4028234e38f)) {
+    step = least = __int_as_float(0x7FC00000);
+    return 0u;
+  }
+  if (step < kLeastStep) {
+    step = 0.0f;
+    return 0u;
+  }
+  const float inv = __frcp_rn(step), half = 0.5f * step;
+  uint32_t codes = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float d = x[i] - mn;
+    int n = __float2int_rn(d * inv);
+    const float r = fmaf(-(float)n, step, d);
+    if (r > half || (r == half && (n & 1))) n += 1;
+    if (r < -half || (r == -half && (n & 1))) n -= 1;
+    codes |= (uint32_t)min(max(n, 0), 15) << (4 * i);
+  }
+  return codes;
+}
+
+__device__ __forceinline__ void decode8(uint32_t codes, float step, float least, float (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = fmaf(step, (float)((codes >> (4 * i)) & 15u), least);
+}
+
+// One CTA: one page of one sequence and head, the tokens of this call that
+// fall into it.  Rows of K come first, then rows of V; a row is held by D / 8
+// lanes.  When the call fills the page the CTA adds up the page's decoded
+// keys (those of earlier calls are read back) and writes their rounded mean.
+template <int D, int GL>
+__global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const AppendParams p) {
+  constexpr int L = D / 8, R = 32 / L, NG = L / GL;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int h = blockIdx.y, b = blockIdx.z;
+  const int len = p.lengths[b];
+  int cnt = p.T;
+  if (p.counts) cnt = min(max(p.counts[b], 0), p.T);
+  if (cnt == 0) return;
+  if (len < 0) {
+    if (threadIdx.x == 0) p.c.report();
+    return;
+  }
+  const int64_t page = p.c.page;
+  const int64_t logical = (len >> p.c.log_page) + (int64_t)blockIdx.x;
+  const int64_t end = min((int64_t)len + cnt, (logical + 1) * page);
+  const int64_t begin = max((int64_t)len, logical * page);
+  if (begin >= end) return;
+  const int pg = page_at(p.c, p.table + b * p.table_stride, p.columns, logical);
+  if (pg < 0) return;
+  const bool fills = end == (logical + 1) * page;
+  const int n = (int)(end - begin), place0 = (int)(begin - logical * page);
+  const int t0 = (int)(begin - len);
+  const int sub = lane / L, cl = lane % L;
+  const uint16_t* k = p.k + b * p.kb + h * p.kh + cl * 8;
+  const uint16_t* v = p.v + b * p.vb + h * p.vh + cl * 8;
+  const int64_t row0 = p.c.row(pg, h, 0);
+
+  Sum2 s[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s[i] = Sum2{0.0f, 0.0f};
+  for (int i0 = warp * R; i0 < 2 * n; i0 += kRowWarps * R) {
+    const int i = i0 + sub;
+    const bool is_k = i < n;
+    const int r = is_k ? i : i - n;
+    uint4 raw = make_uint4(0, 0, 0, 0);
+    if (i < 2 * n)
+      raw = __ldg(reinterpret_cast<const uint4*>(is_k ? k + (t0 + r) * p.kt : v + (t0 + r) * p.vt));
+    float x[8], step, least;
+    unpack8(raw, x);
+    const uint32_t codes = quantise<GL>(x, step, least);
+    if (i < 2 * n) {
+      const int64_t row = row0 + place0 + r;
+      reinterpret_cast<uint32_t*>(is_k ? p.c.k_codes : p.c.v_codes)[row * L + cl] = codes;
+      if (cl % GL == 0)
+        reinterpret_cast<uint32_t*>(is_k ? p.c.k_scales : p.c.v_scales)[row * NG + cl / GL] =
+            pack_bf16(step, least);
+      if (is_k && fills) {
+        decode8(codes, step, least, x);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) add_exact(s[c], x[c]);
+      }
+    }
+  }
+  if (!fills) return;
+  for (int r = warp * R + sub; r < place0; r += kRowWarps * R) {
+    const int64_t row = row0 + r;
+    const uint32_t codes = reinterpret_cast<const uint32_t*>(p.c.k_codes)[row * L + cl];
+    const uint32_t sc = reinterpret_cast<const uint32_t*>(p.c.k_scales)[row * NG + cl / GL];
+    float x[8];
+    decode8(codes, bf16_lo(sc), bf16_hi(sc), x);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) add_exact(s[c], x[c]);
+  }
+  write_rounded_mean<D>(s, p.c.page, false, p.c.k_means + ((int64_t)pg * p.c.Hkv + h) * D);
+}
+
+struct ReadParams {
+  Kv4View c;
+  const int* table;
+  int64_t table_stride;
+  int columns;
+  const int* start;
+  const int* counts;
+  int T, rows;  // rows = B * Hkv * T
+  uint16_t* k;
+  uint16_t* v;
+};
+
+// A lane group (D / 8 lanes) decodes kReadRows consecutive rows of K and V.
+// Rows behind a sequence's count are zero.
+template <int D, int GL>
+__global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const ReadParams p) {
+  constexpr int L = D / 8, R = 32 / L, NG = L / GL;
+  const int lane = threadIdx.x & 31, cl = lane % L;
+  const int group = (blockIdx.x * kRowWarps + (threadIdx.x >> 5)) * R + lane / L;
+  uint32_t code[kReadRows][2], sc[kReadRows][2];
+  const int64_t first = (int64_t)group * kReadRows;
+#pragma unroll
+  for (int u = 0; u < kReadRows; ++u) {
+    code[u][0] = code[u][1] = sc[u][0] = sc[u][1] = 0u;
+    const int64_t r = first + u;
+    if (r >= p.rows) continue;
+    const int bh = (int)(r / p.T), t = (int)(r - (int64_t)bh * p.T);
+    const int b = bh / p.c.Hkv, h = bh - b * p.c.Hkv;
+    if (p.counts && t >= __ldg(p.counts + b)) continue;
+    const int64_t pos = (int64_t)__ldg(p.start + b) + t;
+    const int pg = page_at(p.c, p.table + b * p.table_stride, p.columns, pos >> p.c.log_page);
+    if (pg < 0) continue;
+    const int64_t row = p.c.row(pg, h, (int)(pos & (p.c.page - 1)));
+    code[u][0] = reinterpret_cast<const uint32_t*>(p.c.k_codes)[row * L + cl];
+    code[u][1] = reinterpret_cast<const uint32_t*>(p.c.v_codes)[row * L + cl];
+    sc[u][0] = reinterpret_cast<const uint32_t*>(p.c.k_scales)[row * NG + cl / GL];
+    sc[u][1] = reinterpret_cast<const uint32_t*>(p.c.v_scales)[row * NG + cl / GL];
+  }
+#pragma unroll
+  for (int u = 0; u < kReadRows; ++u) {
+    const int64_t r = first + u;
+    if (r >= p.rows) continue;
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      float x[8];
+      decode8(code[u][kv], bf16_lo(sc[u][kv]), bf16_hi(sc[u][kv]), x);
+      *reinterpret_cast<uint4*>((kv ? p.v : p.k) + r * D + cl * 8) = pack8(x);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Choosing pages: the single-token form of the block choice in select.cu.
+// The queries of one key/value head (G heads, T tokens) are rounded to 7 bits
+// beside their largest entry (whole numbers t); a page's score is the largest
+// of t . mean over those queries: a whole number times the page's power of
+// two, exact in 32 bits.  The last `recent` pages and the first `sink` are
+// always taken; of the others the best, the lowest index first among equals.
+// ---------------------------------------------------------------------------
+constexpr int kScoreThreads = 256;
+constexpr int kScorePages = 64;  // a CTA: 8 warps, 8 pages each
+constexpr int kMostRows = 128;   // G * T
+constexpr uint32_t kForcedPage = 0xFFFFFFFFu;
+constexpr uint32_t kNoPage = 0u;
+
+struct PagesParams {
+  Kv4View c;
+  const uint16_t* q;  // [B][H][T][D]
+  const int* table;
+  int64_t table_stride;
+  int columns;
+  const int* lengths;
+  int rows;  // G * T
+  int keep, sink, recent;
+  uint32_t* keys;  // [B * Hkv][columns]
+  int* out;        // [B * Hkv][keep]
+};
+
+__device__ __forceinline__ int pages_of(const PagesParams& p, int b) {
+  const int64_t n = ((int64_t)max(p.lengths[b], 0) + p.c.page - 1) >> p.c.log_page;
+  return (int)min(n, (int64_t)p.columns);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kScoreThreads) page_scores_kernel(const PagesParams p) {
+  constexpr int C = D / 32;
+  __shared__ __align__(16) uint16_t whole[kMostRows * D];
+  __shared__ int top[kScoreThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int h = blockIdx.y, b = blockIdx.z;
+  const int n = pages_of(p, b);
+  const int first = blockIdx.x * kScorePages;
+  if (first >= n) return;
+  allow_next_launch();
+  const int tiles = (p.rows + 15) / 16;
+  const int64_t bh = (int64_t)b * p.c.Hkv + h;
+  const uint16_t* q = p.q + bh * p.rows * D;
+
+  int e = kNoExponent;
+  for (int i = threadIdx.x; i < p.rows * D; i += kScoreThreads)
+    e = max(e, exponent_of(Sum2{__uint_as_float((uint32_t)__ldg(q + i) << 16), 0.0f}));
+  e = __reduce_max_sync(0xFFFFFFFFu, e);
+  if (lane == 0) top[warp] = e;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kScoreThreads / 32; ++w) e = max(e, top[w]);
+  for (int i = threadIdx.x; i < tiles * 16 * D; i += kScoreThreads) {
+    float t = 0.0f;
+    if (i < p.rows * D && e != kNoExponent)
+      t = rint_scaled(Sum2{__uint_as_float((uint32_t)__ldg(q + i) << 16), 0.0f}, 6 - e);
+    whole[i] = (uint16_t)(__float_as_uint(t) >> 16);
+  }
+  __syncthreads();
+
+  const int g = lane >> 2, j = lane & 3;
+  const int my_page = first + warp * 8 + g;
+  int pg = -1;
+  if (my_page < n) pg = page_at(p.c, p.table + b * p.table_stride, p.columns, my_page);
+  uint4 w[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+    w[c] = pg < 0 ? make_uint4(0, 0, 0, 0)
+                  : reinterpret_cast<const uint4*>(
+                        p.c.k_means + ((int64_t)pg * p.c.Hkv + h) * D)[4 * c + j];
+  float best[2] = {-INFINITY, -INFINITY};  // of pages 2j and 2j + 1, over the rows
+  for (int m = 0; m < tiles; ++m) {
+    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    const uint4* a = reinterpret_cast<const uint4*>(whole + (m * 16 + g) * D);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const uint4 lo = a[4 * c + j], hi = a[D + 4 * c + j];  // row g + 8: 8 * D / 8 pieces on
+      const uint32_t a0[4] = {lo.x, hi.x, lo.y, hi.y};
+      const uint32_t a1[4] = {lo.z, hi.z, lo.w, hi.w};
+      mma_bf16(acc, a0, w[c].x, w[c].y);
+      mma_bf16(acc, a1, w[c].z, w[c].w);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (m * 16 + g + 8 * (i >> 1) < p.rows) best[i & 1] = fmaxf(best[i & 1], acc[i]);
+  }
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) {
+    best[0] = fmaxf(best[0], __shfl_xor_sync(0xFFFFFFFFu, best[0], o));
+    best[1] = fmaxf(best[1], __shfl_xor_sync(0xFFFFFFFFu, best[1], o));
+  }
+  // lane (g, j) writes page g: its score sits in lanes with j = g / 2
+  const float lo = __shfl_sync(0xFFFFFFFFu, best[0], g >> 1);
+  const float hi = __shfl_sync(0xFFFFFFFFu, best[1], g >> 1);
+  if (j == 0 && my_page < n) {
+    const bool forced = my_page < p.sink || my_page >= n - p.recent;
+    p.keys[bh * p.columns + my_page] =
+        pg < 0 ? kNoPage : forced ? kForcedPage : ordered_bits(g & 1 ? hi : lo);
+  }
+}
+
+// Sum over the CTA of one number a thread (two uses in a row need other slots).
+__device__ __forceinline__ int block_sum(int v, int* slots) {
+  v = __reduce_add_sync(0xFFFFFFFFu, v);
+  if ((threadIdx.x & 31) == 0) slots[threadIdx.x >> 5] = v;
+  __syncthreads();
+  int s = 0;
+#pragma unroll
+  for (int w = 0; w < kScoreThreads / 32; ++w) s += slots[w];
+  return s;
+}
+
+// Exclusive prefix over the CTA's threads.
+__device__ __forceinline__ int block_prefix(int v, int* slots) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int s = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(0xFFFFFFFFu, s, o);
+    if (lane >= o) s += t;
+  }
+  if (lane == 31) slots[warp] = s;
+  __syncthreads();
+  int before = 0;
+  for (int w = 0; w < warp; ++w) before += slots[w];
+  return before + s - v;
+}
+
+// One CTA per (sequence, head): thread i holds KP consecutive keys (KP = 0:
+// reads them again each time, for more pages than registers hold).
+template <int KP>
+__device__ __forceinline__ void choose_pages(const PagesParams& p, const uint32_t* keys, int n,
+                                             int* out, int (*slots)[kScoreThreads / 32]) {
+  const int per = KP > 0 ? KP : (n + kScoreThreads - 1) / kScoreThreads;
+  const int64_t base = (int64_t)threadIdx.x * per;
+  uint32_t k[KP > 0 ? KP : 1];
+  if (KP > 0) {
+#pragma unroll
+    for (int i = 0; i < KP; ++i) k[i] = base + i < n ? __ldcg(keys + base + i) : kNoPage;
+  }
+  auto key = [&](int i) -> uint32_t {
+    if (KP > 0) return k[i];
+    return base + i < n ? __ldcg(keys + base + i) : kNoPage;
+  };
+  int turn = 0;
+  auto at_least = [&](uint32_t t) {
+    int c = 0;
+    if (KP > 0) {
+#pragma unroll
+      for (int i = 0; i < KP; ++i) c += k[i] >= t ? 1 : 0;
+    } else {
+      for (int i = 0; i < per; ++i) c += key(i) >= t ? 1 : 0;
+    }
+    turn ^= 1;
+    return block_sum(c, slots[turn]);
+  };
+  const int there = at_least(1u);
+  const int want = min(p.keep, there);
+  uint32_t t = 1u;
+  int have = there;
+  if (want < there) {
+    t = 0u;
+    for (int bit = 31; bit >= 0; --bit) {
+      const uint32_t c = t | (1u << bit);
+      const int cnt = at_least(c);
+      if (cnt >= want) {
+        t = c;
+        have = cnt;
+        if (cnt == want) break;
+      }
+    }
+  }
+  // all of those above t, and the first of those equal to it
+  const bool all = have == want;
+  int above = 0, equal = 0;
+  for (int i = 0; i < per; ++i) {
+    const uint32_t x = key(i);
+    above += (all ? x >= t : x > t) ? 1 : 0;
+    equal += (!all && x == t) ? 1 : 0;
+  }
+  const int before = block_prefix(above, slots[2]);
+  const int equal_before = block_prefix(equal, slots[3]);
+  turn ^= 1;
+  const int ties = all ? 0 : want - block_sum(above, slots[turn]);
+  int taken = min(equal_before, ties), pos = before + taken;
+  for (int i = 0; i < per; ++i) {
+    const uint32_t x = key(i);
+    bool take = all ? x >= t : x > t;
+    if (!all && x == t && taken < ties) {
+      take = true;
+      ++taken;
+    }
+    if (take) out[pos++] = (int)(base + i);
+  }
+  for (int i = want + threadIdx.x; i < p.keep; i += kScoreThreads) out[i] = -1;
+}
+
+__global__ void __launch_bounds__(kScoreThreads) choose_pages_kernel(const PagesParams p) {
+  __shared__ int slots[4][kScoreThreads / 32];
+  const int64_t bh = blockIdx.x;
+  const int n = pages_of(p, (int)(bh / p.c.Hkv));
+  const uint32_t* keys = p.keys + bh * p.columns;
+  int* out = p.out + bh * p.keep;
+  wait_for_previous_launch();
+  if (n <= 4 * kScoreThreads)
+    choose_pages<4>(p, keys, n, out, slots);
+  else if (n <= 16 * kScoreThreads)
+    choose_pages<16>(p, keys, n, out, slots);
+  else
+    choose_pages<0>(p, keys, n, out, slots);
+}
+
+bool strides_ok(const int64_t (&s)[6]) {
+  for (int64_t x : s)
+    if (x < 0 || x % 8 != 0) return false;
+  return true;
+}
+
+bool ints_ok(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Dispatch over head_dim and group: f<D, lanes a group>.
+#define BSATTN_KV4_DISPATCH(c, CALL)                                \
+  do {                                                              \
+    if ((c)->head_dim == 64) {                                      \
+      if ((c)->group == 32) { CALL(64, 4); } else { CALL(64, 8); }  \
+    } else {                                                        \
+      if ((c)->group == 32) { CALL(128, 4); }                       \
+      else if ((c)->group == 64) { CALL(128, 8); }                  \
+      else { CALL(128, 16); }                                       \
+    }                                                               \
+  } while (0)
+
+}  // namespace
+
+bsattn_status check_cache(const bsattn_kv4_cache* c, Kv4View* view) {
+  if (!c || !c->k_codes || !c->v_codes || !c->k_scales || !c->v_scales || !c->k_means || !c->status)
+    return BSATTN_ERR_INVALID_ARG;
+  if (!aligned16(c->k_codes) || !aligned16(c->v_codes) || !aligned16(c->k_scales) ||
+      !aligned16(c->v_scales) || !aligned16(c->k_means) || !ints_ok(c->status))
+    return BSATTN_ERR_INVALID_ARG;
+  if (c->pages <= 0 || c->kv_heads <= 0) return BSATTN_ERR_INVALID_ARG;
+  if (c->head_dim != 64 && c->head_dim != 128) return BSATTN_ERR_UNSUPPORTED;
+  if (c->group != 32 && c->group != 64 && c->group != 128) return BSATTN_ERR_UNSUPPORTED;
+  if (c->group > c->head_dim) return BSATTN_ERR_INVALID_ARG;
+  const int ps = c->page_size;
+  if (ps < 16 || ps > 256 || (ps & (ps - 1)) != 0) return BSATTN_ERR_UNSUPPORTED;
+  if (c->kv_heads > 65535) return BSATTN_ERR_UNSUPPORTED;
+  view->k_codes = static_cast<uint8_t*>(c->k_codes);
+  view->v_codes = static_cast<uint8_t*>(c->v_codes);
+  view->k_scales = static_cast<uint16_t*>(c->k_scales);
+  view->v_scales = static_cast<uint16_t*>(c->v_scales);
+  view->k_means = static_cast<uint16_t*>(c->k_means);
+  view->status = c->status;
+  view->pages = c->pages;
+  view->Hkv = c->kv_heads;
+  view->page = ps;
+  view->log_page = __builtin_ctz((unsigned)ps);
+  return BSATTN_OK;
+}
+
+}  // namespace bsattn
+
+using namespace bsattn;
+
+extern "C" {
+
+bsattn_status bsattn_kv4_append(const bsattn_kv4_cache* cache, const void* k, int64_t k_batch,
+                                int64_t k_head, int64_t k_token, const void* v, int64_t v_batch,
+                                int64_t v_head, int64_t v_token, int B, int T,
+                                const int32_t* block_table, int64_t table_stride, int columns,
+                                const int32_t* lengths, const int32_t* counts, void* stream) {
+  AppendParams p{};
+  const bsattn_status rc = check_cache(cache, &p.c);
+  if (rc != BSATTN_OK) return rc;
+  if (!k || !v || !aligned16(k) || !aligned16(v)) return BSATTN_ERR_INVALID_ARG;
+  if (!ints_ok(block_table) || !ints_ok(lengths) || (counts && !ints_ok(counts)))
+    return BSATTN_ERR_INVALID_ARG;
+  if (B <= 0 || T <= 0 || columns <= 0 || table_stride < 0) return BSATTN_ERR_INVALID_ARG;
+  if (B > 65535) return BSATTN_ERR_UNSUPPORTED;
+  if (!strides_ok({k_batch, k_head, k_token, v_batch, v_head, v_token}))
+    return BSATTN_ERR_INVALID_ARG;
+  p.k = static_cast<const uint16_t*>(k);
+  p.v = static_cast<const uint16_t*>(v);
+  p.kb = k_batch;
+  p.kh = k_head;
+  p.kt = k_token;
+  p.vb = v_batch;
+  p.vh = v_head;
+  p.vt = v_token;
+  p.table = block_table;
+  p.table_stride = table_stride;
+  p.columns = columns;
+  p.lengths = lengths;
+  p.counts = counts;
+  p.T = T;
+  // T tokens touch at most this many pages
+  const int touched = (T + cache->page_size - 2) / cache->page_size + 1;
+  const dim3 grid(touched, cache->kv_heads, B);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+#define BSATTN_CALL(D, GL) kv4_append_kernel<D, GL><<<grid, kRowThreads, 0, st>>>(p)
+  BSATTN_KV4_DISPATCH(cache, BSATTN_CALL);
+#undef BSATTN_CALL
+  return from_cuda(cudaGetLastError());
+}
+
+bsattn_status bsattn_kv4_read(const bsattn_kv4_cache* cache, int B, int T,
+                              const int32_t* block_table, int64_t table_stride, int columns,
+                              const int32_t* start, const int32_t* counts, void* k, void* v,
+                              void* stream) {
+  ReadParams p{};
+  const bsattn_status rc = check_cache(cache, &p.c);
+  if (rc != BSATTN_OK) return rc;
+  if (!k || !v || !aligned16(k) || !aligned16(v)) return BSATTN_ERR_INVALID_ARG;
+  if (!ints_ok(block_table) || !ints_ok(start) || (counts && !ints_ok(counts)))
+    return BSATTN_ERR_INVALID_ARG;
+  if (B <= 0 || T <= 0 || columns <= 0 || table_stride < 0) return BSATTN_ERR_INVALID_ARG;
+  const int64_t rows = (int64_t)B * cache->kv_heads * T;
+  if (rows >= (1ll << 31) - 4096) return BSATTN_ERR_UNSUPPORTED;
+  p.table = block_table;
+  p.table_stride = table_stride;
+  p.columns = columns;
+  p.start = start;
+  p.counts = counts;
+  p.T = T;
+  p.rows = (int)rows;
+  p.k = static_cast<uint16_t*>(k);
+  p.v = static_cast<uint16_t*>(v);
+  const int per_cta = kRowWarps * (256 / cache->head_dim) * kReadRows;
+  const int grid = (int)((rows + per_cta - 1) / per_cta);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+#define BSATTN_CALL(D, GL) kv4_read_kernel<D, GL><<<grid, kRowThreads, 0, st>>>(p)
+  BSATTN_KV4_DISPATCH(cache, BSATTN_CALL);
+#undef BSATTN_CALL
+  return from_cuda(cudaGetLastError());
+}
+
+size_t bsattn_kv4_select_workspace(int B, int kv_heads, int columns) {
+  if (B <= 0 || kv_heads <= 0 || columns <= 0) return 0;
+  return (size_t)B * kv_heads * columns * sizeof(uint32_t);
+}
+
+bsattn_status bsattn_kv4_select(const bsattn_kv4_cache* cache, const void* q, int B, int H, int T,
+                                const int32_t* block_table, int64_t table_stride, int columns,
+                                const int32_t* lengths, int keep, int sink, int recent,
+                                int32_t* selected, void* workspace, size_t workspace_bytes,
+                                void* stream) {
+  PagesParams p{};
+  const bsattn_status rc = check_cache(cache, &p.c);
+  if (rc != BSATTN_OK) return rc;
+  if (!q || !aligned16(q) || !ints_ok(block_table) || !ints_ok(lengths) || !ints_ok(selected) ||
+      !ints_ok(workspace))
+    return BSATTN_ERR_INVALID_ARG;
+  if (B <= 0 || H <= 0 || T <= 0 || columns <= 0 || table_stride < 0 || H % cache->kv_heads != 0)
+    return BSATTN_ERR_INVALID_ARG;
+  if (sink < 0 || recent < 1 || (int64_t)sink + recent > keep) return BSATTN_ERR_INVALID_ARG;
+  const int64_t rows = (int64_t)(H / cache->kv_heads) * T;
+  if (rows > kMostRows || B > 65535 || (int64_t)B * cache->kv_heads >= (1ll << 31))
+    return BSATTN_ERR_UNSUPPORTED;
+  if (workspace_bytes < bsattn_kv4_select_workspace(B, cache->kv_heads, columns))
+    return BSATTN_ERR_INVALID_ARG;
+  p.q = static_cast<const uint16_t*>(q);
+  p.table = block_table;
+  p.table_stride = table_stride;
+  p.columns = columns;
+  p.lengths = lengths;
+  p.rows = (int)rows;
+  p.keep = keep;
+  p.sink = sink;
+  p.recent = recent;
+  p.keys = static_cast<uint32_t*>(workspace);
+  p.out = selected;
+  const dim3 grid((columns + kScorePages - 1) / kScorePages, cache->kv_heads, B);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (cache->head_dim == 64)
+    page_scores_kernel<64><<<grid, kScoreThreads, 0, st>>>(p);
+  else
+    page_scores_kernel<128><<<grid, kScoreThreads, 0, st>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return from_cuda(e);
+  e = launch_dependent(choose_pages_kernel, dim3(B * cache->kv_heads), dim3(kScoreThreads), 0, st,
+                       p);
+  return from_cuda(e);
+}
+
+bsattn_status bsattn_kv4_status(const bsattn_kv4_cache* cache, void* stream) {
+  Kv4View view{};
+  const bsattn_status rc = check_cache(cache, &view);
+  if (rc != BSATTN_OK) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int word = 0;
+  if (cudaMemcpyAsync(&word, view.status, sizeof(word), cudaMemcpyDeviceToHost, st) !=
+          cudaSuccess ||
+      cudaMemsetAsync(view.status, 0, sizeof(word), st) != cudaSuccess ||
+      cudaStreamSynchronize(st) != cudaSuccess)
+    return BSATTN_ERR_CUDA;
+  return (word & kStatusPage) ? BSATTN_ERR_PAGE : BSATTN_OK;
+}
+
+}  // extern "C"

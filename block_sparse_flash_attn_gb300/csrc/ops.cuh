@@ -1,0 +1,186 @@
+// Small device helpers shared by the operators around the attention kernels
+// (rope.cu, select.cu, kv4.cu): bf16 packing, exact sums, block floating point.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+namespace bsattn {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// two bf16 of a 32-bit word, the lower half first
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
+  f[0] = bf16_lo(v.x), f[1] = bf16_hi(v.x), f[2] = bf16_lo(v.y), f[3] = bf16_hi(v.y);
+  f[4] = bf16_lo(v.z), f[5] = bf16_hi(v.z), f[6] = bf16_lo(v.w), f[7] = bf16_hi(v.w);
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
+                    pack_bf16(f[6], f[7]));
+}
+
+// A programmatic dependent waits here for the launch before it (griddepcontrol
+// is a no-op in a kernel launched without the attribute).
+__device__ __forceinline__ void wait_for_previous_launch() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void allow_next_launch() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// Launch with programmatic stream serialisation: the kernel may start while
+// the one before it in the stream drains, and waits for it itself.
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_dependent(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                                    cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, KArgs(args)...);
+}
+
+// ---------------------------------------------------------------------------
+// Exact sums of bf16 (or 32-bit) values: hi + lo with lo the exact error of
+// hi (Knuth's two-sum), about 48 bits in all.
+// ---------------------------------------------------------------------------
+struct Sum2 {
+  float hi, lo;
+};
+
+__device__ __forceinline__ void add_exact(Sum2& s, float x) {
+  const float t = __fadd_rn(s.hi, x);
+  const float z = __fadd_rn(t, -s.hi);
+  const float e = __fadd_rn(__fadd_rn(s.hi, -__fadd_rn(t, -z)), __fadd_rn(x, -z));
+  s.hi = t;
+  s.lo = __fadd_rn(s.lo, e);
+}
+
+__device__ __forceinline__ void add_exact(Sum2& s, const Sum2& o) {
+  add_exact(s, o.hi);
+  s.lo = __fadd_rn(s.lo, o.lo);
+}
+
+// hi takes everything it can hold: |lo| <= half a step of hi
+__device__ __forceinline__ Sum2 renormalised(const Sum2& s) {
+  Sum2 r{s.hi, 0.0f};
+  add_exact(r, s.lo);
+  return r;
+}
+
+// floor(log2 |hi + lo|) of a renormalised sum; a very low number for zero and
+// for a sum that is not finite (both count as zero).
+constexpr int kNoExponent = -100000;
+__device__ __forceinline__ int exponent_of(const Sum2& s) {
+  const float a = fabsf(s.hi);
+  if (!(a > 0.0f) || !(a <= 3.0e38f)) return kNoExponent;
+  int e = ilogbf(a);
+  // a power of two with a negative rest lies just below it
+  const bool pow2 = a == ldexpf(1.0f, e);
+  if (pow2 && (s.hi > 0.0f ? s.lo < 0.0f : s.lo > 0.0f)) e -= 1;
+  return e;
+}
+
+// rint((hi + lo) * 2^shift), half to even, exactly: a whole number of at most
+// 8 bits (the caller's shift puts the largest below 2^7).
+__device__ __forceinline__ float rint_scaled(const Sum2& s, int shift) {
+  const float h = ldexpf(s.hi, shift);
+  if (!(fabsf(h) <= 256.0f)) return 0.0f;  // not finite: counts as zero
+  float n = rintf(h);
+  const float r = h - n;  // exact
+  // hi lies on a border: the sign of lo says which side the sum is on
+  if (r == 0.5f && s.lo > 0.0f) n += 1.0f;
+  if (r == -0.5f && s.lo < 0.0f) n -= 1.0f;
+  return n;
+}
+
+// The mean of `rows` rows of a block (rows a power of two), rounded to 7 bits
+// beside its largest entry, by a CTA of 128 threads: s[i] is this thread's sum
+// of channel (lane % (D/8)) * 8 + i over the rows that it saw.  Writes, as
+// bf16, the whole numbers t = rint(mean 2^(6 - E)) or the values t 2^(E - 6).
+template <int D>
+__device__ __forceinline__ void write_rounded_mean(Sum2 (&s)[8], int rows, bool whole,
+                                                   uint16_t* out) {
+  constexpr int L = D / 8, W = 4;
+  __shared__ Sum2 part[W][D];
+  __shared__ int top[W];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+#pragma unroll
+    for (int o = L; o < 32; o <<= 1) {
+      Sum2 other;
+      other.hi = __shfl_xor_sync(0xFFFFFFFFu, s[i].hi, o);
+      other.lo = __shfl_xor_sync(0xFFFFFFFFu, s[i].lo, o);
+      add_exact(s[i], other);
+    }
+    if (lane < L) part[warp][lane * 8 + i] = s[i];
+  }
+  __syncthreads();
+  const int c = threadIdx.x;
+  Sum2 t{0.0f, 0.0f};
+  int e = kNoExponent;
+  if (c < D) {
+#pragma unroll
+    for (int w = 0; w < W; ++w) add_exact(t, part[w][c]);
+    t = renormalised(t);
+    e = exponent_of(t);
+  }
+  e = __reduce_max_sync(0xFFFFFFFFu, e);
+  if (lane == 0) top[warp] = e;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < W; ++w) e = max(e, top[w]);
+  if (c < D) {
+    // the mean's exponent is e - log2(rows): t = rint(sum 2^(6 - e))
+    const bool none = e == kNoExponent;
+    const float n = none ? 0.0f : rint_scaled(t, 6 - e);
+    const int shift = none || whole ? 0 : e - 6 - (31 - __clz(rows));
+    out[c] = (uint16_t)(__float_as_uint(ldexpf(n, shift)) >> 16);
+  }
+}
+
+// Order-preserving map of a finite float to uint32 (larger float, larger
+// number; 0 and 0xFFFFFFFF are not images of a finite float).
+__device__ __forceinline__ uint32_t ordered_bits(float x) {
+  const uint32_t u = __float_as_uint(x + 0.0f);  // -0 becomes +0
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+// D += A B, 16 x 8 x 16: bf16 in, 32-bit sums (A row-major, B column-major)
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+}  // namespace bsattn

@@ -44,6 +44,7 @@
 #ifndef BSATTN_H_
 #define BSATTN_H_
 
+#include <stddef.h>
 #include <stdint.h>
 
 #ifdef __cplusplus
@@ -59,10 +60,14 @@ typedef enum {
   BSATTN_ERR_TIMEOUT = 5,      /* a kernel gave up waiting (bounded wait ran out) */
   BSATTN_ERR_INTERNAL = 6,     /* a kernel detected an inconsistent state */
   BSATTN_ERR_SCRATCH_LIMIT = 7, /* problem too large for bsattn_fwd_noalloc's fixed scratch */
-  BSATTN_ERR_RANGE = 8         /* an input value outside what the kernel's arithmetic holds:
+  BSATTN_ERR_RANGE = 8,        /* an input value outside what the kernel's arithmetic holds:
                                   at D = 64 the forward pass multiplies P by V in fp16, so
                                   every V entry must be finite with |v| <= 65504; reported
                                   after the launch, by the status calls */
+  BSATTN_ERR_PAGE = 9          /* bsattn_kv4_*: a block table names a page outside the cache,
+                                  a position lies behind the table, a length is negative, or
+                                  a page list is out of order; reported after the launch, by
+                                  bsattn_kv4_status */
 } bsattn_status;
 
 /* Opaque plan: the per-query-tile list of live key blocks and the tile order. */
@@ -362,6 +367,224 @@ bsattn_status bsattn_pipeline_run(bsattn_pipeline_t pipe, const void* hq, const 
                                   void* stream);
 bsattn_status bsattn_pipeline_status(bsattn_pipeline_t pipe);
 void bsattn_pipeline_free(bsattn_pipeline_t pipe);
+
+/*
+ * Around the attention: from a model's projection to Q, K, V and back, block
+ * masks chosen by a cheap score, and a 4-bit key/value cache for serving.
+ * The pages have no counterpart.  Every call is stream-ordered, synchronises
+ * nothing (bsattn_kv4_status excepted), allocates nothing and may be captured
+ * into a graph; workspaces belong to one call at a time (two captured graphs
+ * that may run at once need one each) and need no initial contents.
+ */
+
+/* Flags of bsattn_qk_norm_rope and its gradient. */
+enum {
+  BSATTN_ROPE_INTERLEAVED = 1u, /* channel pairs (2i, 2i + 1) instead of (i, i + rotary_dim/2) */
+  BSATTN_WEIGHT_F32 = 2u        /* the norm weights are fp32 instead of bf16 */
+};
+
+/*
+ * bsattn_rope_table -- cos and sin of position * inv_freq[i], evaluated in 64
+ * bits and rounded to fp32.
+ *   inv_freq   device double [rotary_dim/2].
+ *   table      device fp32 [n_pos][rotary_dim/2][2] (cos, sin), 16-byte aligned.
+ *   rotary_dim a positive multiple of 16, at most 128.
+ * Errors: INVALID_ARG, UNSUPPORTED (rotary_dim), CUDA.
+ */
+bsattn_status bsattn_rope_table(const double* inv_freq, int n_pos, int rotary_dim, float* table,
+                                void* stream);
+
+/*
+ * bsattn_qk_norm_rope -- Q, K, V of bsattn_fwd from one projection.
+ *
+ * Per (token, head) row x of a query or key head:
+ *   n = x / sqrt(mean(x^2) + eps) * weight       (weight null: n = x)
+ *   y_i = n_i cos - n_j sin, y_j = n_j cos + n_i sin for the channel pairs
+ *   (i, j) of the first rotary_dim channels, the angles taken from the table at
+ *   the token's position (table null: y = n); the other channels y = n.
+ * V rows are copied.  32-bit arithmetic, one rounding to bf16.
+ *
+ *   x          device bf16 [B][S][H + 2 Hkv][D]: heads of Q, then K, then V; rows of
+ *              one token contiguous, token and batch strides in elements, multiples
+ *              of 8; 16-byte aligned.
+ *   q_weight, k_weight  device [D], bf16 (fp32 with BSATTN_WEIGHT_F32), 16-byte
+ *              aligned; both or neither.
+ *   table      bsattn_rope_table's, or null.  n_pos: its positions.
+ *   rotary_dim a positive multiple of 16, at most D.
+ *   positions  device int32 [B][S], or null: token s at position s (S <= n_pos).  A
+ *              token whose position is outside [0, n_pos) gets NaN in its rotated
+ *              channels.
+ *   q, k, v    device bf16 [B][H][S][D], [B][Hkv][S][D] twice, 16-byte aligned.
+ *   S          any positive length.  D: 64 or 128.
+ * Errors: INVALID_ARG, UNSUPPORTED (D, rotary_dim, B*S*(H + 2 Hkv) >= 2^31), CUDA.
+ */
+bsattn_status bsattn_qk_norm_rope(const void* x, int64_t x_batch_stride, int64_t x_token_stride,
+                                  int B, int S, int H, int Hkv, int D, const void* q_weight,
+                                  const void* k_weight, const float* table, int n_pos,
+                                  int rotary_dim, const int32_t* positions, float eps,
+                                  unsigned flags, void* q, void* k, void* v, void* stream);
+
+/*
+ * bsattn_qk_norm_rope_bwd -- the gradient of bsattn_qk_norm_rope.
+ *
+ *   x .. flags  the forward call's.
+ *   dq, dk, dv device fp32 [B][H][S][D], [B][Hkv][S][D] twice (as bsattn_bwd_gqa
+ *              writes them), 16-byte aligned.
+ *   dx         device bf16, shaped like x, with strides of its own (multiples of 8;
+ *              tokens must not overlap); may be x itself.
+ *   dq_weight, dk_weight  device fp32 [D], written in full; ignored without weights.
+ *   workspace  bsattn_qk_norm_rope_bwd_workspace bytes, 16-byte aligned; ignored
+ *              without weights.
+ * The weight gradients are added up in a fixed order: repeated calls agree bit
+ * for bit.
+ * Errors: as bsattn_qk_norm_rope.
+ */
+size_t bsattn_qk_norm_rope_bwd_workspace(int B, int S, int H, int Hkv, int D);
+bsattn_status bsattn_qk_norm_rope_bwd(const void* x, int64_t x_batch_stride, int64_t x_token_stride,
+                                      const float* dq, const float* dk, const float* dv, int B,
+                                      int S, int H, int Hkv, int D, const void* q_weight,
+                                      const void* k_weight, const float* table, int n_pos,
+                                      int rotary_dim, const int32_t* positions, float eps,
+                                      unsigned flags, void* dx, int64_t dx_batch_stride,
+                                      int64_t dx_token_stride, float* dq_weight, float* dk_weight,
+                                      void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * bsattn_select_blocks -- the block mask of bsattn_plan, chosen by block means.
+ *
+ * Per query block (128 tokens) and key block (128 tokens, 64 with
+ * BSATTN_KEY_BLOCK_64) the mean over the tokens, per channel, is rounded to 7
+ * bits beside the block's largest entry: E = floor(log2 max |mean|), t =
+ * rint(mean 2^(6 - E)), half to even; entries that are not finite count as
+ * zero.  The score of a pair is sum_d tq_d tk_d 2^(Ek - 6), exact in 32 bits.
+ * Each query block keeps its `keep` best key blocks (fewer if fewer are
+ * allowed); of equal scores the lower index goes first.
+ *   causal     (BSATTN_CAUSAL) only key blocks that start at or before the query
+ *              block's last token.
+ *   allow      device uint8 [B][allow_heads][S/128][S/128 (S/64)], nonzero = may be
+ *              kept, or null: all.  allow_heads: H, or 1 for one mask a batch entry.
+ *   sink       the first `sink` key blocks are kept where allowed;
+ *   local      key blocks of the 128-token blocks fewer than `local` away from the
+ *              query block are kept where allowed (1: its own).  These count
+ *              towards `keep`; if they are more than `keep` they are all kept.
+ *   q, k       device bf16 [B][H][S][D], [B][Hkv][S][D], as for bsattn_fwd_gqa
+ *              (query head h scores against key head h / (H / Hkv)).  Sums of a
+ *              block's entries must stay below 3e38 in magnitude.
+ *   mask       device uint8 [B][H][S/128][S/128 (S/64)], written in full.
+ *   workspace  bsattn_select_blocks_workspace bytes, 16-byte aligned.
+ * Errors: INVALID_ARG, UNSUPPORTED (D, sizes as bsattn_plan), CUDA.
+ */
+size_t bsattn_select_blocks_workspace(int B, int H, int Hkv, int S, int D, unsigned flags);
+bsattn_status bsattn_select_blocks(const void* q, const void* k, int B, int H, int Hkv, int S,
+                                   int D, int keep, int sink, int local, unsigned flags,
+                                   const uint8_t* allow, int allow_heads, uint8_t* mask,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * A paged key/value cache in 4 bits, owned by the caller (all device memory).
+ *
+ * Per (token, head) row and group of `group` channels: the least value, a step
+ * = bf16((largest - least) / 15), and a code 0..15 per channel, (x - least) /
+ * step rounded to nearest, half to even; the row stands for step * code + least.
+ * A group whose step is below 2^-100 is constant; a group with a value that is
+ * not finite, or whose range overflows, stands for NaN.  Position p of a
+ * sequence lives in page block_table[p / page_size] at place p % page_size.
+ */
+typedef struct {
+  void* k_codes;   /* uint8 [pages][kv_heads][page_size][head_dim/2], even channel in the low bits */
+  void* v_codes;
+  void* k_scales;  /* bf16 [pages][kv_heads][page_size][head_dim/group][2] (step, least) */
+  void* v_scales;
+  void* k_means;   /* bf16 [pages][kv_heads][head_dim]: a full page's mean key, rounded as in
+                      bsattn_select_blocks; untouched while a page is not full */
+  int32_t* status; /* one word, zero at first: see bsattn_kv4_status */
+  int pages, kv_heads;
+  int page_size;   /* 16, 32, 64, 128 or 256 tokens */
+  int head_dim;    /* 64 or 128 */
+  int group;       /* 32, 64 or 128, at most head_dim */
+} bsattn_kv4_cache;
+
+/*
+ * Arguments that the bsattn_kv4_* calls share:
+ *   block_table device int32, `columns` pages a sequence, rows table_stride apart.
+ *   lengths     device int32 [B].
+ *   counts      device int32 [B] (taken as 0 below 0, T above T), or null: T each.
+ * A page that the table does not have, or that lies outside the cache, is
+ * skipped (its tokens are not written, read as zero, not attended to) and
+ * reported by bsattn_kv4_status.
+ *
+ * bsattn_kv4_append -- write T new tokens a sequence at positions lengths[b] ..
+ * lengths[b] + counts[b] - 1 (lengths before the call; not changed).  Sequences
+ * must not write to one page at once.  When a page's last place is written its
+ * mean key is written too, from the page's decoded keys.
+ *   k, v       device bf16 [B][kv_heads][T][head_dim], 16-byte aligned, strides in
+ *              elements (multiples of 8), channels contiguous.
+ * bsattn_kv4_read -- positions start[b] .. start[b] + T - 1 as bf16, into k, v
+ * [B][kv_heads][T][head_dim] (contiguous); rows from counts[b] on are zero.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA.
+ */
+bsattn_status bsattn_kv4_append(const bsattn_kv4_cache* cache, const void* k, int64_t k_batch,
+                                int64_t k_head, int64_t k_token, const void* v, int64_t v_batch,
+                                int64_t v_head, int64_t v_token, int B, int T,
+                                const int32_t* block_table, int64_t table_stride, int columns,
+                                const int32_t* lengths, const int32_t* counts, void* stream);
+bsattn_status bsattn_kv4_read(const bsattn_kv4_cache* cache, int B, int T,
+                              const int32_t* block_table, int64_t table_stride, int columns,
+                              const int32_t* start, const int32_t* counts, void* k, void* v,
+                              void* stream);
+
+/*
+ * bsattn_kv4_select -- the pages that each key/value head's queries attend to:
+ * the single-token form of bsattn_select_blocks.
+ *
+ * The queries of one key/value head (H / kv_heads heads, T tokens) are rounded
+ * to 7 bits beside their largest entry; a page scores the largest of query . page
+ * mean over them.  The first `sink` and the last `recent` pages of the sequence
+ * are always taken, the best others fill up to `keep`, the lower page first
+ * among equals.
+ *   q          device bf16 [B][H][T][head_dim]; (H / kv_heads) * T <= 128.
+ *   lengths    cached tokens, the T new ones included.
+ *   keep       >= sink + recent;  sink >= 0;  recent >= 1.
+ *   selected   device int32 [B][kv_heads][keep]: pages (p / page_size) ascending, then -1.
+ *   workspace  bsattn_kv4_select_workspace bytes, 16-byte aligned.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA.
+ */
+size_t bsattn_kv4_select_workspace(int B, int kv_heads, int columns);
+bsattn_status bsattn_kv4_select(const bsattn_kv4_cache* cache, const void* q, int B, int H, int T,
+                                const int32_t* block_table, int64_t table_stride, int columns,
+                                const int32_t* lengths, int keep, int sink, int recent,
+                                int32_t* selected, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
+/*
+ * bsattn_kv4_attn -- O, LSE of T new tokens a sequence against the cache.
+ *
+ * Query t of a sequence of length n sits at position n - T + t and sees the
+ * cached tokens at positions up to its own: all, or those of the listed pages.
+ * A query that sees none gets O = 0, LSE = -inf.
+ *   q          device bf16 [B][H][T][head_dim], 16-byte aligned; query head h reads
+ *              key/value head h / (H / kv_heads); (H / kv_heads) * T <= 128.
+ *   lengths    cached tokens, the T new ones included.
+ *   selected   device int32 [B][kv_heads][n_selected], strictly ascending pages, then
+ *              negative entries (as bsattn_kv4_select writes it), or null with
+ *              n_selected 0.  A page not above the one before it is skipped and
+ *              reported; pages behind the length are skipped.
+ *   scale      finite; multiplies q.k.
+ *   flags      BSATTN_OUT_F32.
+ *   out        device bf16 (fp32) [B][H][T][head_dim];  lse  device fp32 [B][H][T].
+ *   workspace  bsattn_kv4_attn_workspace bytes, 16-byte aligned.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA.
+ */
+size_t bsattn_kv4_attn_workspace(int B, int H, int kv_heads, int T, int D);
+bsattn_status bsattn_kv4_attn(const bsattn_kv4_cache* cache, const void* q, int B, int H, int T,
+                              const int32_t* block_table, int64_t table_stride, int columns,
+                              const int32_t* lengths, const int32_t* selected, int n_selected,
+                              float scale, unsigned flags, void* out, float* lse, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/* Wait for `stream`, then report and clear the cache's status word: OK or PAGE
+   (CUDA if the wait failed). */
+bsattn_status bsattn_kv4_status(const bsattn_kv4_cache* cache, void* stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,417 @@
+"""The 4-bit cache: appended codes, scales and page means equal to the 64-bit
+restatement; reading back, choosing pages and attention against it.
+
+Tolerances: reading back is one 32-bit and one bf16 rounding.  Attention: the
+bounds that _ops_ref.attn derives from 32-bit sums, plus the output's rounding."""
+import pytest
+import torch
+
+import _ops_ref as ref
+from _ops_ref import U32, UBF
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def bs():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import __graft_entry__
+    __graft_entry__.build()
+    import block_sparse_flash_attn_gb300 as bs
+    bs.load()
+    return bs
+
+
+def _i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def _state(cache):
+    return [t.clone() for t in (cache.k_codes, cache.v_codes, cache.k_scales, cache.v_scales, cache.k_means)]
+
+
+def _append_ref(cache, state, k, v, table, lengths, counts):
+    """What the cache's tensors must hold after the call."""
+    kc, vc, ks, vs, km = [t.clone() for t in state]
+    page = cache.page_size
+    full = []
+    for b, (n, c) in enumerate(zip(lengths, counts)):
+        for x, codes, scales in ((k, kc, ks), (v, vc, vs)):
+            code, sc = ref.quantise(x[b, :, :c], cache.group)
+            pos = torch.arange(n, n + c, device="cuda")
+            pg, place = table[b, pos // page].long(), pos % page
+            codes[pg, :, place] = ref.pack(code).transpose(0, 1)
+            scales[pg, :, place] = sc.transpose(0, 1).bfloat16()
+        full += [int(table[b, p]) for p in range(n // page, (n + c) // page)]
+    if full:
+        val = ref.values(kc[full], ks[full]).float().double()
+        t, e = ref.round7(val.mean(-2))
+        km[full] = (t * torch.exp2(e)).bfloat16()
+    return [kc, vc, ks, vs, km]
+
+
+#        Hkv D    page group T    lengths            counts
+APPENDS = [
+    (2, 64, 16, 32, 1, [0, 15, 16, 100], None),
+    (2, 64, 16, 64, 40, [0, 7, 33], [40, 0, 13]),
+    (1, 128, 64, 128, 1, [63, 64, 0], [1, 1, 0]),
+    (3, 128, 32, 32, 70, [5, 0], [70, 69]),
+    (8, 128, 128, 64, 129, [0, 127], None),
+    (1, 64, 256, 64, 600, [1, 255], [600, 513]),
+]
+
+
+@pytest.mark.parametrize("case", APPENDS, ids=str)
+def test_append_and_read(bs, case):
+    Hkv, D, page, group, T, lengths, counts = case
+    B = len(lengths)
+    done = counts or [T] * B
+    ends = [n + c for n, c in zip(lengths, done)]
+    columns = max(-(-e // page) for e in ends) + 1
+    cache = bs.Kv4Cache(sum(-(-e // page) for e in ends) + 2, Hkv, D, page_size=page, group=group)
+    ref.fill(cache, 11)
+    table = ref.table(cache, ends, columns, 5)
+    g = ref.gen(6)
+    k, v = ((torch.randn(B, Hkv, T, D, generator=g, device="cuda") * (1 + i)).bfloat16() for i in range(2))
+    before = _state(cache)
+    n, c = _i32(lengths), None if counts is None else _i32(counts)
+    bs.kv4_append(cache, k, v, table, n, c)
+    bs.kv4_status(cache)
+    for got, want in zip(_state(cache), _append_ref(cache, before, k, v, table, lengths, done)):
+        assert torch.equal(got, want)
+    # read back what was written, and what was there before
+    rk, rv = bs.kv4_read(cache, table, n, T, c)
+    start = [max(x - 20, 0) for x in lengths]
+    back = max(e - s for e, s in zip(ends, start))
+    rk2, rv2 = bs.kv4_read(cache, table, _i32(start), back, _i32([e - s for e, s in zip(ends, start)]))
+    bs.kv4_status(cache)
+    for first, width, pairs in ((lengths, T, ((rk, "k"), (rv, "v"))), (start, back, ((rk2, "k"), (rv2, "v")))):
+        for got, m in pairs:
+            assert got.shape == (B, Hkv, width, D)
+            for b in range(B):
+                pos = torch.arange(first[b], ends[b], device="cuda")
+                pg, place = table[b, pos // page].long(), pos % page
+                codes = getattr(cache, m + "_codes")[pg, :, place].transpose(0, 1)
+                sc = getattr(cache, m + "_scales")[pg, :, place].transpose(0, 1)
+                want = ref.values(codes, sc)
+                size = want.abs() + 2 * sc[..., 1].double().abs().repeat_interleave(group, -1)
+                err = (got[b, :, :pos.numel()].double() - want).abs()
+                assert bool((err <= UBF * want.abs() + 2 * U32 * size).all())
+                assert not bool(got[b, :, pos.numel():].any())
+
+
+def test_append_token_by_token_equals_a_prompt(bs):
+    """The same tokens one at a time, in pieces and at once: the same cache, means included."""
+    Hkv, D, T, page = 2, 128, 75, 16
+    g = ref.gen(3)
+    k, v = (torch.randn(2, Hkv, T, D, generator=g, device="cuda").bfloat16() for _ in "kv")
+    caches = []
+    for pieces in ([1] * T, [T], [13, 3, 16, 43]):
+        cache = bs.Kv4Cache(12, Hkv, D, page_size=page, group=32)
+        table = ref.table(cache, [T, T], 5, 2)
+        at = 0
+        for n in pieces:  # (slices of k, v: strided)
+            bs.kv4_append(cache, k[:, :, at:at + n], v[:, :, at:at + n], table, _i32([at, at]))
+            at += n
+        caches.append(_state(cache))
+    for other in caches[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(caches[0], other))
+
+
+def test_append_extreme_values(bs):
+    """Constant groups, steps on borders, tiny and huge ranges, NaN and infinities."""
+    D, page = 64, 16
+    k = torch.randn(1, 1, 16, D, generator=ref.gen(1), device="cuda").bfloat16()
+    k[0, 0, 0] = 0
+    k[0, 0, 1] = -3.25
+    k[0, 0, 2] = (torch.arange(D, device="cuda") % 31).bfloat16() / 2    # halves of a step
+    k[0, 0, 3] *= 1e-38
+    k[0, 0, 4] *= 1e37
+    k[0, 0, 5, 7] = float("nan")
+    k[0, 0, 6, 40] = float("inf")
+    k[0, 0, 7, 3] = float("-inf")
+    k[0, 0, 8, 0], k[0, 0, 8, 1] = 3e38, -3e38
+    k[0, 0, 9] = torch.tensor([1.0] * 63 + [1.0078125])
+    k[0, 0, 10, ::2] = 0.0
+    k[0, 0, 10, 1::2] = -0.0
+    for group in (32, 64):
+        cache = bs.Kv4Cache(2, 1, D, page_size=page, group=group)
+        table = _i32([[1]])
+        bs.kv4_append(cache, k, k, table, _i32([0]))
+        code, scales = ref.quantise(k[0, 0], group)
+        for m in "kv":
+            assert torch.equal(getattr(cache, m + "_codes")[1, 0], ref.pack(code))
+            got = getattr(cache, m + "_scales")[1, 0].double()
+            want = scales.bfloat16().double()
+            assert torch.equal(got.nan_to_num(1e5), want.nan_to_num(1e5))
+        rk, _ = bs.kv4_read(cache, table, _i32([0]), 16)
+        assert bool(rk[0, 0, 5, :32].isnan().all()) and not bool(rk[0, 0, 0].any())
+        if group == 32:
+            assert not bool(rk[0, 0, 5, 32:].isnan().any())
+
+
+#         Hkv G  D    page group T  lengths
+ATTNS = [
+    (1, 1, 64, 16, 64, 1, [1]),
+    (2, 4, 128, 64, 128, 1, [0, 1, 63, 64, 65, 700]),
+    (2, 8, 64, 16, 32, 1, [777, 16, 300]),
+    (1, 5, 128, 32, 64, 3, [2, 3, 40, 555]),
+    (4, 1, 128, 128, 32, 1, [1000, 129]),
+    (2, 16, 128, 64, 128, 1, [333, 128]),
+    (1, 8, 64, 256, 64, 5, [1500, 4, 0]),
+    (8, 4, 128, 64, 128, 1, [5000]),
+    (1, 40, 64, 16, 32, 3, [200, 31]),
+    (1, 3, 128, 16, 128, 1, [900] + list(range(60))),
+]
+
+
+def _attn_case(bs, case, seed=21):
+    Hkv, G, D, page, group, T, lengths = case
+    B = len(lengths)
+    columns = max(1, max(-(-n // page) for n in lengths))
+    cache = bs.Kv4Cache(sum(-(-n // page) for n in lengths) + 2, Hkv, D, page_size=page, group=group)
+    ref.fill(cache, seed)
+    table = ref.table(cache, lengths, columns, seed + 1)
+    q = (torch.randn(B, Hkv * G, T, D, generator=ref.gen(seed + 2), device="cuda") * 1.5).bfloat16()
+    return cache, table, q, _i32(lengths)
+
+
+def _check_attn(o, lse, want, out_f32):
+    o_ref, l_ref, tol_o, tol_l = want
+    assert torch.equal(lse.isneginf(), l_ref.isneginf())
+    dead = l_ref.isneginf()
+    assert not bool(o[dead].any())
+    err = (lse.double() - l_ref).abs()[~dead]
+    # the LSE's own rounding to 32 bits and log2's 2 ulp: 4 U32 of its size
+    assert bool((err <= tol_l[~dead] + 4 * U32 * (1 + l_ref[~dead].abs())).all()), float(err.max())
+    tol = tol_o[..., None] + (U32 if out_f32 else UBF) * o_ref.abs()
+    err = (o.double() - o_ref).abs()
+    assert bool((err <= tol).all()), (float(err.max()), float((err / (tol + 1e-300)).max()))
+
+
+@pytest.mark.parametrize("out_f32", [True, False], ids=["f32", "bf16"])
+@pytest.mark.parametrize("case", ATTNS, ids=str)
+def test_attn(bs, case, out_f32):
+    cache, table, q, n = _attn_case(bs, case)
+    o, lse = bs.kv4_attn(cache, q, table, n, out_f32=out_f32)
+    bs.kv4_status(cache)
+    _check_attn(o, lse, ref.attn(cache, q, table, case[-1]), out_f32)
+    again = bs.kv4_attn(cache, q, table, n, out_f32=out_f32)
+    assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3, 2.0])
+def test_attn_scale(bs, scale):
+    case = (2, 4, 64, 16, 32, 1, [150, 31])
+    cache, table, q, n = _attn_case(bs, case)
+    o, lse = bs.kv4_attn(cache, q, table, n, scale=scale, out_f32=True)
+    _check_attn(o, lse, ref.attn(cache, q, table, case[-1], scale=scale), True)
+
+
+def test_attn_wide_steps(bs):
+    """Values of one head far larger than another token's, steps from 2^-40 to 2^20."""
+    case = (1, 4, 128, 16, 32, 1, [300])
+    cache, table, q, n = _attn_case(bs, case)
+    f = torch.exp2(torch.randint(-40, 21, (cache.pages, 1, 16, 1, 1), generator=ref.gen(1), device="cuda").float())
+    cache.v_scales.mul_(f.bfloat16())
+    o, lse = bs.kv4_attn(cache, q, table, n, out_f32=True)
+    _check_attn(o, lse, ref.attn(cache, q, table, case[-1]), True)
+
+
+def test_attn_growing_scores(bs):
+    """Scores that rise along the sequence by far more than a running maximum may lag, and fall."""
+    case = (1, 2, 64, 16, 64, 1, [400])
+    for sign in (1, -1):
+        cache, table, q, n = _attn_case(bs, case)
+        q[:] = 1.0
+        order = table[0].long()
+        for i in range(25):
+            cache.k_scales[order[i], ..., 1] = sign * (i - 12) * 2.0
+        o, lse = bs.kv4_attn(cache, q, table, n, out_f32=True)
+        _check_attn(o, lse, ref.attn(cache, q, table, case[-1]), True)
+
+
+def test_attn_never_reads_what_is_not_there(bs):
+    """NaN scales in unused places, pages and heads' other tokens change nothing."""
+    case = (2, 4, 128, 64, 128, 2, [70, 0, 1])
+    cache, table, q, n = _attn_case(bs, case)
+    want = bs.kv4_attn(cache, q, table, n)
+    used = torch.zeros(cache.pages, cache.page_size, dtype=torch.bool, device="cuda")
+    for b, length in enumerate(case[-1]):
+        pos = torch.arange(length, device="cuda")
+        used[table[b, pos // 64].long(), pos % 64] = True
+    dead = ~used[:, None].expand(-1, 2, -1)
+    for t in (cache.k_scales, cache.v_scales):
+        t[dead] = float("nan")
+    for t in (cache.k_codes, cache.v_codes):
+        t[dead] = 255
+    got = bs.kv4_attn(cache, q, table, n)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+SELECTED = [
+    (2, 4, 128, 64, 128, 1, [700, 65, 1, 0], 4),
+    (1, 8, 64, 16, 32, 3, [900, 17], 9),
+    (4, 2, 128, 32, 64, 1, [2000], 64),
+]
+
+
+@pytest.mark.parametrize("case", SELECTED, ids=str)
+def test_selected_pages(bs, case):
+    *rest, keep = case
+    cache, table, q, n = _attn_case(bs, tuple(rest))
+    lengths = rest[-1]
+    sel = bs.kv4_select(cache, q, table, n, keep, sink=1, recent=2)
+    assert torch.equal(sel, ref.select_pages(cache, q, table, lengths, keep, 1, 2))
+    o, lse = bs.kv4_attn(cache, q, table, n, sel, out_f32=True)
+    bs.kv4_status(cache)
+    _check_attn(o, lse, ref.attn(cache, q, table, lengths, sel), True)
+    # a list of all pages is the whole cache
+    most = table.shape[1]
+    every = torch.arange(most, dtype=torch.int32, device="cuda").expand(len(lengths), cache.kv_heads, most).contiguous()
+    whole = bs.kv4_attn(cache, q, table, n, every, out_f32=True)
+    bs.kv4_status(cache)
+    _check_attn(*whole, ref.attn(cache, q, table, lengths), True)
+
+
+@pytest.mark.parametrize("pages", [1, 63, 64, 65, 1030, 4100, 17000])
+def test_select_many_pages(bs, pages):
+    """Lists on both sides of what a CTA holds in registers; ties among equal means."""
+    page, D = 16, 64
+    cache = bs.Kv4Cache(64, 1, D, page_size=page, group=64)
+    ref.fill(cache, 4)
+    g = ref.gen(5)
+    table = torch.randint(0, 64, (2, pages), generator=g, device="cuda").to(torch.int32)  # pages repeat: ties
+    lengths = [pages * page, max(1, pages * page // 3)]
+    q = torch.randn(2, 4, 2, D, generator=g, device="cuda").bfloat16()
+    for keep in (3, 40, 700):
+        got = bs.kv4_select(cache, q, table, _i32(lengths), keep, sink=1, recent=2)
+        assert torch.equal(got, ref.select_pages(cache, q, table, lengths, keep, 1, 2))
+    got = bs.kv4_select(cache, q, table, _i32(lengths), 1, sink=0, recent=1)
+    assert torch.equal(got, ref.select_pages(cache, q, table, lengths, 1, 0, 1))
+
+
+def test_select_zero_queries(bs):
+    cache, table, q, n = _attn_case(bs, (2, 4, 128, 16, 128, 1, [300, 40]))
+    q.zero_()
+    got = bs.kv4_select(cache, q, table, n, 5)
+    assert got[0, 0].tolist() == [0, 1, 2, 3, 18] and got[1, 1].tolist() == [0, 1, 2, -1, -1]
+
+
+def test_bad_pages_are_skipped_and_reported(bs):
+    case = (1, 4, 64, 16, 64, 1, [100])
+    cache, table, q, n = _attn_case(bs, case)
+    good = bs.kv4_attn(cache, q, table, n, _i32([[[0, 1, 3, 4, 5, 6]]]), out_f32=True)
+    bs.kv4_status(cache)
+    for bad in (-1, cache.pages, 2 ** 31 - 1, -2 ** 31):
+        broken = table.clone()
+        broken[0, 2] = bad
+        got = bs.kv4_attn(cache, q, broken, n, out_f32=True)
+        with pytest.raises(bs.BsattnError, match="page"):
+            bs.kv4_status(cache)
+        bs.kv4_status(cache)  # reported once
+        _check_attn(*got, ref.attn(cache, q, table, [100], _i32([[[0, 1, 3, 4, 5, 6]]])), True)
+        before = _state(cache)
+        k = torch.randn(1, 1, 5, 64, device="cuda").bfloat16()
+        bs.kv4_append(cache, k, k, broken, _i32([33]))
+        with pytest.raises(bs.BsattnError):
+            bs.kv4_status(cache)
+        assert all(torch.equal(a, b) for a, b in zip(before, _state(cache)))
+        rk, _ = bs.kv4_read(cache, broken, _i32([30]), 20)
+        with pytest.raises(bs.BsattnError):
+            bs.kv4_status(cache)
+        assert bool((rk[0, 0, 2:18] == 0).all()) and bool(rk[0, 0, 18:].any()) and bool(rk[0, 0, :2].any())
+        sel = bs.kv4_select(cache, q, broken, n, 7)
+        with pytest.raises(bs.BsattnError):
+            bs.kv4_status(cache)
+        assert sel[0, 0].tolist() == [0, 1, 3, 4, 5, 6, -1]
+    # behind the table, negative lengths, lists out of order
+    k = torch.randn(1, 1, 5, 64, device="cuda").bfloat16()
+    for length in (7 * 16 - 2, -3, 2 ** 31 - 2):
+        bs.kv4_append(cache, k, k, table, _i32([length]))
+        with pytest.raises(bs.BsattnError):
+            bs.kv4_status(cache)
+    bs.kv4_read(cache, table, _i32([-3]), 2)
+    with pytest.raises(bs.BsattnError):
+        bs.kv4_status(cache)
+    got = bs.kv4_attn(cache, q, table, n, _i32([[[0, 1, 1, 3, 2, 4, 5, 6]]]), out_f32=True)
+    with pytest.raises(bs.BsattnError):
+        bs.kv4_status(cache)
+    assert bool(torch.isfinite(got[0]).all()) and bool(torch.isfinite(good[0]).all())
+    neg = bs.kv4_attn(cache, q, table, _i32([-7]))
+    assert not bool(neg[0].any()) and bool(neg[1].isneginf().all())
+    bs.kv4_status(cache)
+
+
+def test_empty_calls(bs):
+    cache = bs.Kv4Cache(2, 1, 64)
+    table, n = torch.zeros(0, 1, dtype=torch.int32, device="cuda"), _i32([])
+    q = torch.zeros(0, 2, 1, 64, dtype=torch.bfloat16, device="cuda")
+    assert bs.kv4_attn(cache, q, table, n)[0].shape == q.shape
+    assert bs.kv4_select(cache, q, table, n, 2).shape == (0, 1, 2)
+    bs.kv4_append(cache, q[:, :1], q[:, :1], table, n)
+    one, z = _i32([[0]]), torch.zeros(1, 1, 0, 64, dtype=torch.bfloat16, device="cuda")
+    bs.kv4_append(cache, z, z, one, _i32([0]))
+    assert bs.kv4_read(cache, one, _i32([0]), 0)[0].shape == (1, 1, 0, 64)
+    bs.kv4_status(cache)
+
+
+def test_offsets_past_32_bits(bs):
+    """A cache whose code arrays pass 2^32 bytes: pages at its far end."""
+    Hkv, D, page = 8, 128, 256
+    pages = (1 << 32) // (Hkv * page * D // 2) + 40
+    cache = bs.Kv4Cache(pages, Hkv, D, page_size=page, group=128)
+    table = _i32([[pages - 1, 3, pages - 2]])
+    T = 600
+    g = ref.gen(2)
+    k, v = (torch.randn(1, Hkv, T, D, generator=g, device="cuda").bfloat16() for _ in "kv")
+    bs.kv4_append(cache, k, v, table, _i32([0]))
+    rk, rv = bs.kv4_read(cache, table, _i32([0]), T)
+    for got, x in ((rk, k), (rv, v)):
+        code, sc = ref.quantise(x, 128)
+        assert float((got.double() - ref.values(ref.pack(code), sc)).abs().max()) < 0.02
+    q = torch.randn(1, 32, 1, D, generator=g, device="cuda").bfloat16()
+    o, lse = bs.kv4_attn(cache, q, table, _i32([T]), out_f32=True)
+    _check_attn(o, lse, ref.attn(cache, q, table, [T]), True)
+    bs.kv4_status(cache)
+
+
+def test_refusals(bs):
+    cache = bs.Kv4Cache(4, 2, 64, page_size=16)
+    table, n = _i32([[0, 1]]), _i32([3])
+    q = torch.zeros(1, 4, 1, 64, dtype=torch.bfloat16, device="cuda")
+    k = torch.zeros(1, 2, 1, 64, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError, match="group"):
+        bs.Kv4Cache(4, 2, 64, group=128)
+    with pytest.raises(ValueError, match="page_size"):
+        bs.Kv4Cache(4, 2, 64, page_size=48)
+    with pytest.raises(TypeError, match="Kv4Cache"):
+        bs.kv4_attn(None, q, table, n)
+    with pytest.raises(TypeError, match="int32"):
+        bs.kv4_attn(cache, q, table.long(), n)
+    with pytest.raises(ValueError, match="block_table"):
+        bs.kv4_attn(cache, q, table[0], n)
+    with pytest.raises(ValueError, match="lengths"):
+        bs.kv4_attn(cache, q, table, _i32([3, 4]))
+    with pytest.raises(ValueError, match="kv_heads"):
+        bs.kv4_attn(cache, q[:, :3].contiguous(), table, n)
+    with pytest.raises(ValueError, match="128 query rows"):
+        bs.kv4_attn(cache, q.expand(1, 4, 65, 64).contiguous(), table, n)
+    with pytest.raises(ValueError, match="selected"):
+        bs.kv4_attn(cache, q, table, n, _i32([[0]]))
+    with pytest.raises(ValueError, match="keep"):
+        bs.kv4_select(cache, q, table, n, 1, sink=1, recent=1)
+    with pytest.raises(ValueError, match="recent"):
+        bs.kv4_select(cache, q, table, n, 3, recent=0)
+    with pytest.raises(ValueError, match="k, v"):
+        bs.kv4_append(cache, k[..., :32], k, table, n)
+    with pytest.raises(ValueError, match="contiguous"):
+        wide = torch.zeros(1, 2, 64, 2, dtype=torch.bfloat16, device="cuda").transpose(2, 3)[:, :, :1]
+        bs.kv4_append(cache, wide, wide, table, n)
+    with pytest.raises(TypeError, match="cuda"):
+        bs.kv4_append(cache, k.cpu(), k.cpu(), table, n)
+    with pytest.raises(ValueError, match="counts"):
+        bs.kv4_read(cache, table, n, 1, _i32([1, 2]))
+    with pytest.raises(bs.BsattnError):
+        bs.kv4_attn(cache, q, table, n, scale=float("inf"))

@@ -2,11 +2,41 @@
 //
 // Query t of T of a sequence of length n sits at position n - T + t and sees
 // the cached tokens up to its own position (all of them, or those of a list of
-// pages).  With K and V rows decoded as step * code + minimum (kv4.cu):
+// pages).  With K and V rows decoded as step * code + least (kv4.cu):
 //   s_i = scale q . k_i,  p = softmax(s),  o = sum_i p_i v_i,
 //   lse = ln sum_i exp(s_i);  a query that sees nothing: o = 0, lse = -inf.
+//
+// The codes are never expanded to values.  With n_i the codes of a token,
+//   q . k_i = step_i (q . n_i) + least_i sum(q)           (per group of channels)
+//   sum_i p_i v_i = sum_i (p_i step_i) n_i + sum_i p_i least_i
+// so both products run on the codes themselves, and steps and minima touch
+// one number a (token, query, group).  A code masked out of a 32-bit word IS an
+// fp16 number: the bits 0x000F hold n as the subnormal n 2^-24, the bits
+// 0x00F0 as 16 n 2^-24, both exact operands of an fp16 MMA.  One AND makes two
+// operands; the factor 16 goes into the queries (divided by 16) and the
+// output, the 2^-24 into a final factor.
+//
+// Tokens are the MMA's M (16 a tile), queries its N (8 a tile): S^T = K Q^T and
+// O^T = V^T P^T, since a key/value head has few query rows (G T <= 16 a tile).
+// P goes from S^T's accumulator layout to O^T's operand layout with movmatrix,
+// as an fp16 pair hi + lo (22 bits), so its rounding is below fp32 sums' own.
+//
+// Bound: memory.  D + 8 bytes (groups of D) a token and head for 4 D G T
+// operations: at G T = 8 some 30 operations a byte, a tenth of the card's
+// tensor-to-memory ratio; mma.sync (no TMEM round trip, operands straight from
+// registers) is ample.  Each warp streams 16-token tiles through its own ring
+// of cp.async stages, with no CTA barrier in the loop.
+//
+// Work: the (sequence, head, 128-token step) units in order are cut into equal
+// ranges, one a CTA, from the device's lengths (so a captured graph follows
+// them).  A range that ends inside a sequence's head leaves a partial result
+// (maximum, sum, O) in the workspace, and a second launch joins those in a fixed
+// order: ragged batches and single long sequences fill the machine alike, and
+// results repeat bit for bit.
 #include <cmath>
 #include <cstdint>
+
+#include <cuda_fp16.h>
 
 #include "kv4.cuh"
 
@@ -15,6 +45,13 @@ namespace {
 
 constexpr int kAttnThreads = 256;
 constexpr int kAttnWarps = kAttnThreads / 32;
+constexpr int kTile = 16;                      // tokens a warp takes at once
+constexpr int kStep = kTile * kAttnWarps;      // tokens a CTA takes at once
+constexpr int kStages = 4;                     // tiles in a warp's ring
+constexpr int kMostSequences = 4096;
+constexpr int kJoinThreads = 256;
+constexpr float kNoMax = -1e30f;               // running maximum before any score
+constexpr float kLag = 8.0f;                   // a score may pass the running maximum by 2^8
 
 struct AttnParams {
   Kv4View c;
@@ -25,20 +62,70 @@ struct AttnParams {
   const int* lengths;
   const int* selected;  // [B][Hkv][n_selected] ascending pages, or null
   int n_selected;
-  int T, rows;  // rows = G * T
+  int B, T, rows;  // rows = G * T
+  int mt;          // row tiles a head
   float scale_log2;
   void* out;
   float* lse;
   int out_f32;
+  int* prefix;     // [B + 1] steps before each sequence (written by CTA 0 for the join)
+  float* partial;  // [2 * CTAs][RP * (D + 2)]
+  int ctas;
 };
 
-// The page of list entry e of a (sequence, head), and the position of its
-// first token; -1 for nothing.  Without a list entry e is page e.
-__device__ __forceinline__ int listed_page(const AttnParams& p, int b, int h, int64_t e, int len,
-                                           int64_t& first) {
-  int64_t logical = e;
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 unpack_half(uint32_t x) {
+  return __half22float2(*reinterpret_cast<__half2*>(&x));
+}
+
+// Where each CTA's range of units begins.
+__device__ __forceinline__ int64_t range_begin(int64_t units, int ctas, int c) {
+  return units * c / ctas;
+}
+// The CTA whose range holds unit u.
+__device__ __forceinline__ int range_of(int64_t units, int ctas, int64_t u) {
+  int c = (int)((u * ctas) / units);
+  while (c + 1 < ctas && range_begin(units, ctas, c + 1) <= u) ++c;
+  while (c > 0 && range_begin(units, ctas, c) > u) --c;
+  return c;
+}
+
+// The page of the tile that starts at token v0 of a (sequence, head)'s list,
+// and that tile's first position; -1 when it holds nothing to see.
+__device__ __forceinline__ int tile_page(const AttnParams& p, int b, int h, int64_t v0, int len,
+                                         int& pos) {
+  int64_t logical = v0 >> p.c.log_page;
+  const int place = (int)(v0 & (p.c.page - 1));
   if (p.selected) {
+    if (logical >= p.n_selected) return -1;
     const int* sel = p.selected + ((int64_t)b * p.c.Hkv + h) * p.n_selected;
+    const int64_t e = logical;
     logical = __ldg(sel + e);
     if (logical < 0) return -1;
     if (e > 0 && logical <= __ldg(sel + e - 1)) {  // a page named twice, or out of order
@@ -46,78 +133,591 @@ __device__ __forceinline__ int listed_page(const AttnParams& p, int b, int h, in
       return -1;
     }
   }
-  first = logical << p.c.log_page;
+  const int64_t first = (logical << p.c.log_page) + place;
   if (first >= len) return -1;
+  pos = (int)first;
   return page_at(p.c, p.table + b * p.table_stride, p.columns, logical);
 }
 
-// One CTA per (query row, head, sequence); each warp takes every eighth token
-// of the list and keeps its own running maximum and sums, which are joined
-// at the end.
-template <int D, int GL>
-__global__ void __launch_bounds__(kAttnThreads) kv4_attn_kernel(const AttnParams p) {
-  constexpr int V = D / 32, NG = D / 8 / GL;  // channels a lane
-  __shared__ float sm[kAttnWarps], sl[kAttnWarps], so[kAttnWarps][D];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int r = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
-  const int len = max(p.lengths[b], 0);
-  const int64_t last = (int64_t)len - p.T + r % p.T;
-  const int64_t row = ((int64_t)b * p.c.Hkv + h) * p.rows + r;
-  float q[V], o[V], m = -INFINITY, l = 0.0f;
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    q[i] = __uint_as_float((uint32_t)p.q[row * D + lane * V + i] << 16);
-    o[i] = 0.0f;
+// One CTA: a range of units.  NG groups of channels share a step each, NT
+// tiles of 8 query rows.
+template <int D, int NG, int NT>
+struct Attn {
+  static constexpr int C = D / 32;        // 16-byte pieces (32 channels) of a row of codes
+  static constexpr int CG = C / NG;       // pieces a group
+  static constexpr int RB = D / 2;        // bytes of a row of codes
+  static constexpr int RP = 8 * NT;       // query rows a tile
+  static constexpr int kCodes = kTile * RB;
+  static constexpr int kScales = kTile * NG * 4;
+  static constexpr int kStage = 2 * kCodes + 2 * kScales;  // K, V codes, K, V scales
+  static constexpr int kRing = kAttnWarps * kStages * kStage;
+  static constexpr int kJoin = kAttnWarps * RP * (D + 2) * 4 + kAttnWarps * RP * 4;
+  static constexpr int kSmem = (kRing > kJoin ? kRing : kJoin);
+  static constexpr int kSlot = RP * (D + 2);  // floats of a partial result
+
+  // pieces of a row are stored permuted by its token, so that the 32-bit reads
+  // of both products meet 32 banks
+  static __device__ __forceinline__ int swizzle(int token) {
+    return D == 128 ? (token >> 1) & 3 : (token >> 2) & 1;
   }
-  const int64_t entries = p.selected ? p.n_selected : ((int64_t)len + p.c.page - 1) >> p.c.log_page;
-  for (int64_t e = 0; e < entries; ++e) {
-    int64_t first = 0;
-    const int pg = listed_page(p, b, h, e, len, first);
-    if (pg < 0) continue;
-    for (int t = warp; t < p.c.page && first + t <= last; t += kAttnWarps) {
-      const int64_t cr = p.c.row(pg, h, t);
-      float dot = 0.0f, v[V];
-      const int ch = lane * V;
-      const uint32_t ks = reinterpret_cast<const uint32_t*>(p.c.k_scales)[cr * NG + ch / (8 * GL)];
-      const uint32_t vs = reinterpret_cast<const uint32_t*>(p.c.v_scales)[cr * NG + ch / (8 * GL)];
+};
+
+template <int D, int NG, int NT>
+__global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1)
+    kv4_attn_kernel(const AttnParams p) {
+  using A = Attn<D, NG, NT>;
+  constexpr int C = A::C, RB = A::RB, RP = A::RP;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ int warp_sums[kAttnWarps];
+  __shared__ int tile_pos[kAttnWarps][kStages];
+  int* prefix = reinterpret_cast<int*>(smem + A::kSmem);  // [B + 1]
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, j = lane & 3;
+
+  // steps before each sequence
+  {
+    const int per = (p.B + kAttnThreads - 1) / kAttnThreads;
+    const int b0 = tid * per;
+    const int64_t most = (int64_t)p.columns * p.c.page;
+    auto steps_of = [&](int b) -> int {
+      if (p.selected) return (int)(((int64_t)p.n_selected * p.c.page + kStep - 1) / kStep);
+      int64_t n = max(__ldg(p.lengths + b), 0);
+      if (n > most) {
+        p.c.report();
+        n = most;
+      }
+      return (int)((n + kStep - 1) / kStep);
+    };
+    int sum = 0;
+    for (int i = 0; i < per; ++i)
+      if (b0 + i < p.B) sum += steps_of(b0 + i);
+    int s = sum;
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int sh = 4 * (i & 1);
-        const int kc = (p.c.k_codes[cr * (D / 2) + (ch + i) / 2] >> sh) & 15;
-        const int vc = (p.c.v_codes[cr * (D / 2) + (ch + i) / 2] >> sh) & 15;
-        dot += q[i] * fmaf(bf16_lo(ks), (float)kc, bf16_hi(ks));
-        v[i] = fmaf(bf16_lo(vs), (float)vc, bf16_hi(vs));
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xFFFFFFFFu, s, o);
+      if (lane >= o) s += t;
+    }
+    if (lane == 31) warp_sums[warp] = s;
+    __syncthreads();
+    int at = s - sum;
+    for (int w = 0; w < warp; ++w) at += warp_sums[w];
+    for (int i = 0; i < per; ++i)
+      if (b0 + i < p.B) {
+        prefix[b0 + i] = at;
+        at += steps_of(b0 + i);
+        if (b0 + i == p.B - 1) prefix[p.B] = at;
+      }
+    __syncthreads();
+    if (blockIdx.x == 0)
+      for (int i = tid; i <= p.B; i += kAttnThreads) p.prefix[i] = prefix[i];
+  }
+  allow_next_launch();
+  const int heads = p.c.Hkv * p.mt;
+  const int64_t units = (int64_t)prefix[p.B] * heads;
+  if (units == 0) return;
+  const int ctas = (int)min((int64_t)p.ctas, units);
+  if ((int)blockIdx.x >= ctas) return;
+  int64_t u = range_begin(units, ctas, blockIdx.x);
+  const int64_t u_end = range_begin(units, ctas, blockIdx.x + 1);
+  bool first_segment = true;
+
+  const uint32_t ring =
+      (uint32_t)__cvta_generic_to_shared(smem) + warp * (kStages * A::kStage);
+  int* my_pos = tile_pos[warp];
+
+  while (u < u_end) {
+    // the segment: steps [s0, s1) of row tile m of head h of sequence b
+    int lo = 0, hi = p.B;  // last b with prefix[b] * heads <= u
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if ((int64_t)prefix[mid] * heads <= u) lo = mid; else hi = mid;
+    }
+    const int b = lo;
+    const int steps = prefix[b + 1] - prefix[b];
+    const int64_t off = u - (int64_t)prefix[b] * heads;
+    const int hm = (int)(off / steps);
+    const int s0 = (int)(off - (int64_t)hm * steps);
+    const int s1 = (int)min((int64_t)steps, s0 + (u_end - u));
+    const int h = hm / p.mt, row0 = (hm - h * p.mt) * RP;
+    const int len = max(__ldg(p.lengths + b), 0);
+    const int64_t bh = (int64_t)b * p.c.Hkv + h;
+    const int n_tiles = s1 - s0;  // this warp's, one a step
+
+    // ---- tiles: pages are looked up 32 steps at a time, one batch ahead
+    int page_cur = -1, pos_cur = 0, page_next = -1, pos_next = 0;
+    auto look_up = [&](int batch, int& pg, int& pos) {
+      pg = -1;
+      pos = 0;
+      const int i = batch * 32 + lane;
+      if (i < n_tiles)
+        pg = tile_page(p, b, h, ((int64_t)(s0 + i) * kAttnWarps + warp) * kTile, len, pos);
+    };
+    auto issue = [&](int i) {
+      if (i < n_tiles) {
+        if ((i & 31) == 0) {
+          if (i == 0) {
+            look_up(0, page_cur, pos_cur);
+          } else {
+            page_cur = page_next;
+            pos_cur = pos_next;
+          }
+          look_up(i / 32 + 1, page_next, pos_next);
+        }
+        const int pg = __shfl_sync(0xFFFFFFFFu, page_cur, i & 31);
+        const int pos = __shfl_sync(0xFFFFFFFFu, pos_cur, i & 31);
+        const int st = i % kStages;
+        if (lane == 0) my_pos[st] = pg < 0 ? -1 : pos;
+        if (pg >= 0) {
+          const uint32_t dst = ring + st * A::kStage;
+          const int64_t row = p.c.row(pg, h, pos & (p.c.page - 1));
+          const uint8_t* kc = p.c.k_codes + row * RB;
+          const uint8_t* vc = p.c.v_codes + row * RB;
+#pragma unroll
+          for (int x = 0; x < kTile * C / 32; ++x) {
+            const int piece = x * 32 + lane, token = piece / C, c = piece % C;
+            const uint32_t at = token * RB + 16 * (c ^ A::swizzle(token));
+            copy16(dst + at, kc + piece * 16);
+            copy16(dst + A::kCodes + at, vc + piece * 16);
+          }
+          if (lane < 8 * NG) {
+            const int kv = lane / (4 * NG), piece = lane % (4 * NG);
+            const uint8_t* sc = reinterpret_cast<const uint8_t*>(kv ? p.c.v_scales : p.c.k_scales);
+            copy16(dst + 2 * A::kCodes + kv * A::kScales + piece * 16,
+                   sc + row * (NG * 4) + piece * 16);
+          }
+        }
+      }
+      copy_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) issue(i);
+
+    // ---- queries: operands, the factor of the code product, the group sums
+    uint32_t qf[NT][C][4];
+    float mul[NT][2], qs[NT][NG][2];
+    int lim[NT][2];  // last position that the row sees
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = row0 + nt * 8 + g;
+      float x[C][8], top = 0.0f, sum[NG];
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        uint4 raw = make_uint4(0, 0, 0, 0);
+        if (r < p.rows)
+          raw = __ldg(reinterpret_cast<const uint4*>(p.q + (bh * p.rows + r) * D) + 4 * c + j);
+        unpack8(raw, x[c]);
+        if (c % A::CG == 0) sum[c / A::CG] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          top = fmaxf(top, fabsf(x[c][i]));
+          sum[c / A::CG] += x[c][i];
+        }
       }
 #pragma unroll
-      for (int s = 16; s > 0; s >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, s);
-      const float x = dot * p.scale_log2;
-      const float nm = fmaxf(m, x);
-      const float a = exp2f(m - nm), w = exp2f(x - nm);
-      m = nm;
-      l = l * a + w;
+      for (int o = 1; o < 4; o <<= 1) {
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
 #pragma unroll
-      for (int i = 0; i < V; ++i) o[i] = o[i] * a + w * v[i];
+        for (int n = 0; n < NG; ++n) sum[n] += __shfl_xor_sync(0xFFFFFFFFu, sum[n], o);
+      }
+      // the row's largest query goes to [2^13, 2^14): fp16 then holds bf16
+      // queries 2^27 times smaller exactly, a sixteenth of them included
+      int sh = 0;
+      if (top > 0.0f && top <= 3.4e38f) sh = min(13 - ilogbf(top), 120);
+      const float f = ldexpf(1.0f, sh), f16 = f * 0.0625f;
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        qf[nt][c][0] = pack_half(x[c][0] * f, x[c][4] * f);
+        qf[nt][c][1] = pack_half(x[c][2] * f, x[c][6] * f);
+        qf[nt][c][2] = pack_half(x[c][1] * f16, x[c][5] * f16);
+        qf[nt][c][3] = pack_half(x[c][3] * f16, x[c][7] * f16);
+      }
+      const float m = p.scale_log2 * ldexpf(1.0f, 24 - sh);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {  // rows 2j, 2j + 1 of the accumulators
+        const int src = 8 * j + 4 * e;
+        mul[nt][e] = __shfl_sync(0xFFFFFFFFu, m, src);
+#pragma unroll
+        for (int n = 0; n < NG; ++n)
+          qs[nt][n][e] = __shfl_sync(0xFFFFFFFFu, sum[n], src) * p.scale_log2;
+        const int rr = row0 + nt * 8 + 2 * j + e;
+        lim[nt][e] = rr < p.rows ? len - p.T + rr % p.T : -1;
+      }
     }
-  }
-  if (lane == 0) sm[warp] = m, sl[warp] = l;
+
+    float mx[NT][2], l[NT][2], vm[NT][NG][2], o[C][2][NT][4];
 #pragma unroll
-  for (int i = 0; i < V; ++i) so[warp][lane * V + i] = o[i];
-  __syncthreads();
-  float top = -INFINITY, sum = 0.0f;
-  for (int w = 0; w < kAttnWarps; ++w) top = fmaxf(top, sm[w]);
-  const float ref = top == -INFINITY ? 0.0f : top;
-  for (int w = 0; w < kAttnWarps; ++w) sum += sl[w] * exp2f(sm[w] - ref);
-  if (threadIdx.x == 0) p.lse[row] = (ref + log2f(sum)) * kLn2;
-  for (int c = threadIdx.x; c < D; c += kAttnThreads) {
-    float t = 0.0f;
-    for (int w = 0; w < kAttnWarps; ++w) t += so[w][c] * exp2f(sm[w] - ref);
-    t = sum > 0.0f ? t / sum : (sum == 0.0f ? 0.0f : sum);
-    if (p.out_f32)
-      static_cast<float*>(p.out)[row * D + c] = t;
-    else
-      static_cast<__nv_bfloat16*>(p.out)[row * D + c] = __float2bfloat16_rn(t);
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        mx[nt][e] = kNoMax;
+        l[nt][e] = 0.0f;
+#pragma unroll
+        for (int n = 0; n < NG; ++n) vm[nt][n][e] = 0.0f;
+      }
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[c][t][nt][e] = 0.0f;
+    }
+    // steps are held beside a power of two not below any seen, so that p step
+    // stays inside fp16 (|p| <= 2^8)
+    float top_step = 7.888609e-31f;  // 2^-100
+    float inv_top = 1.2676506e30f;   // 2^100
+
+    for (int i = 0; i < n_tiles; ++i) {
+      copy_wait<kStages - 2>();
+      __syncwarp();
+      issue(i + kStages - 1);
+      const int st = i % kStages;
+      const int pos = my_pos[st];
+      if (pos < 0) continue;
+      const uint32_t kt = ring + st * A::kStage;
+      const uint32_t vt = kt + A::kCodes, kst = kt + 2 * A::kCodes, vst = kst + A::kScales;
+
+      // ---- scores (base 2): tokens g and g + 8, rows 2j and 2j + 1
+      float s[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[nt][e] = 0.0f;
+      const uint32_t kw = kt + g * RB + 4 * j;
+      const int sw = A::swizzle(g);
+#pragma unroll
+      for (int n = 0; n < NG; ++n) {
+        float acc[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[nt][e] = 0.0f;
+#pragma unroll
+        for (int c = n * A::CG; c < (n + 1) * A::CG; ++c) {
+          const uint32_t w0 = lds32(kw + 16 * (c ^ sw)), w1 = lds32(kw + 8 * RB + 16 * (c ^ sw));
+          const uint32_t y0 = w0 >> 8, y1 = w1 >> 8;
+          const uint32_t a[4] = {w0 & 0x000F000Fu, w1 & 0x000F000Fu, y0 & 0x000F000Fu,
+                                 y1 & 0x000F000Fu};
+          const uint32_t a16[4] = {w0 & 0x00F000F0u, w1 & 0x00F000F0u, y0 & 0x00F000F0u,
+                                   y1 & 0x00F000F0u};
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma_f16(acc[nt], a, qf[nt][c][0], qf[nt][c][1]);
+            mma_f16(acc[nt], a16, qf[nt][c][2], qf[nt][c][3]);
+          }
+        }
+        const uint32_t k0 = lds32(kst + (g * NG + n) * 4), k1 = lds32(kst + ((g + 8) * NG + n) * 4);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t sc = e < 2 ? k0 : k1;
+            s[nt][e] = fmaf(acc[nt][e] * bf16_lo(sc), mul[nt][e & 1],
+                            fmaf(bf16_hi(sc), qs[nt][n][e & 1], s[nt][e]));
+          }
+      }
+      // ---- V's steps and minima; what a row does not see weighs nothing
+      float vs[NG][NT][4], vl[NG][NT][4], most = 0.0f;
+#pragma unroll
+      for (int n = 0; n < NG; ++n) {
+        const uint32_t v0 = lds32(vst + (g * NG + n) * 4), v1 = lds32(vst + ((g + 8) * NG + n) * 4);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            vs[n][nt][e] = bf16_lo(e < 2 ? v0 : v1);
+            vl[n][nt][e] = bf16_hi(e < 2 ? v0 : v1);
+          }
+      }
+      if (pos + kTile - 1 > len - p.T) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (pos + g + (e < 2 ? 0 : 8) > lim[nt][e & 1]) {
+              s[nt][e] = -INFINITY;
+#pragma unroll
+              for (int n = 0; n < NG; ++n) vs[n][nt][e] = vl[n][nt][e] = 0.0f;
+            }
+      }
+      float over = kNoMax;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          over = fmaxf(over, s[nt][e] - mx[nt][e & 1]);
+#pragma unroll
+          for (int n = 0; n < NG; ++n) most = fmaxf(most, vs[n][nt][e]);
+        }
+      // ---- rare: a score far above the running maximum, or a larger step
+      if (__any_sync(0xFFFFFFFFu, over > kLag || most > top_step)) {
+#pragma unroll
+        for (int sft = 16; sft > 0; sft >>= 1)
+          most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, sft));
+        float fs = 1.0f;
+        if (most > top_step) {
+          // the next power of two (2^127 at most: p step then passes 2^8 by 2)
+          uint32_t bits = (__float_as_uint(most) + 0x007FFFFFu) & 0x7F800000u;
+          bits = min(bits, 0x7F000000u);
+          const float t = __uint_as_float(bits);
+          fs = top_step / t;
+          top_step = t;
+          inv_top = 1.0f / t;
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float t = fmaxf(s[nt][e], s[nt][e + 2]);
+#pragma unroll
+            for (int sft = 4; sft < 32; sft <<= 1)
+              t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, sft));
+            t = fmaxf(t, mx[nt][e]);
+            const float f = exp2_fast(mx[nt][e] - t);
+            mx[nt][e] = t;
+            l[nt][e] *= f;
+#pragma unroll
+            for (int n = 0; n < NG; ++n) vm[nt][n][e] *= f;
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                o[c][k][nt][e] *= f * fs;
+                o[c][k][nt][e + 2] *= f * fs;
+              }
+          }
+      }
+      // ---- weights p step, as fp16 hi + lo, turned to the operand layout
+      uint32_t wh[NG][NT][2], wl[NG][NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float pr[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          pr[e] = exp2_fast(s[nt][e] - mx[nt][e & 1]);
+          l[nt][e & 1] += pr[e];
+        }
+#pragma unroll
+        for (int n = 0; n < NG; ++n) {
+          float w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            vm[nt][n][e & 1] = fmaf(pr[e], vl[n][nt][e], vm[nt][n][e & 1]);
+            w[e] = pr[e] * (vs[n][nt][e] * inv_top);
+          }
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const uint32_t hi16 = pack_half(w[2 * t], w[2 * t + 1]);
+            const float2 back = unpack_half(hi16);
+            wh[n][nt][t] = transpose8x8(hi16);
+            wl[n][nt][t] = transpose8x8(pack_half(w[2 * t] - back.x, w[2 * t + 1] - back.y));
+          }
+        }
+      }
+      // ---- O^T += V^T P^T: a piece's 32 channels are two M tiles, codes 0 and
+      // 2 (1 and 3) of each lane's half word for rows g and g + 8
+      const uint32_t vw = vt + 2 * j * RB + 4 * (g & 3);
+      const int vsw = A::swizzle(2 * j);
+      const uint32_t half = g < 4 ? 0x5410u : 0x7632u;
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const uint32_t at = vw + 16 * (c ^ vsw);
+        const uint32_t x0 = __byte_perm(lds32(at), lds32(at + RB), half);
+        const uint32_t x1 = __byte_perm(lds32(at + 8 * RB), lds32(at + 9 * RB), half);
+        const uint32_t y0 = x0 >> 8, y1 = x1 >> 8;
+        const uint32_t a[4] = {x0 & 0x000F000Fu, y0 & 0x000F000Fu, x1 & 0x000F000Fu,
+                               y1 & 0x000F000Fu};
+        const uint32_t a16[4] = {x0 & 0x00F000F0u, y0 & 0x00F000F0u, x1 & 0x00F000F0u,
+                                 y1 & 0x00F000F0u};
+        const int n = c / A::CG;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma_f16(o[c][0][nt], a, wh[n][nt][0], wh[n][nt][1]);
+          mma_f16(o[c][0][nt], a, wl[n][nt][0], wl[n][nt][1]);
+          mma_f16(o[c][1][nt], a16, wh[n][nt][0], wh[n][nt][1]);
+          mma_f16(o[c][1][nt], a16, wl[n][nt][0], wl[n][nt][1]);
+        }
+      }
+    }
+    copy_wait<0>();
+
+    // ---- join the warps (the ring is free): maxima, sums, O in 32 bits
+    __syncthreads();
+    float* sm = reinterpret_cast<float*>(smem);  // [warp][RP] maxima
+    float* sl = sm + kAttnWarps * RP;            // [warp][RP] sums
+    float* so = sl + kAttnWarps * RP;            // [warp][RP][D]
+    float* sf = so + kAttnWarps * RP * D;        // [warp][RP] factors
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = nt * 8 + 2 * j + e;
+#pragma unroll
+        for (int sft = 4; sft < 32; sft <<= 1) {
+          l[nt][e] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][e], sft);
+#pragma unroll
+          for (int n = 0; n < NG; ++n)
+            vm[nt][n][e] += __shfl_xor_sync(0xFFFFFFFFu, vm[nt][n][e], sft);
+        }
+        if (g == 0) {
+          sm[warp * RP + r] = mx[nt][e];
+          sl[warp * RP + r] = l[nt][e];
+        }
+        const float f = 16777216.0f * top_step, f16 = 1048576.0f * top_step;  // 2^24, 2^20
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          float* dst = so + (warp * RP + r) * D + 32 * c + 8 * (g & 3) + 4 * (g >> 2);
+          const float base = vm[nt][c / A::CG][e];
+          dst[0] = fmaf(o[c][0][nt][e], f, base);
+          dst[1] = fmaf(o[c][1][nt][e], f16, base);
+          dst[2] = fmaf(o[c][0][nt][e + 2], f, base);
+          dst[3] = fmaf(o[c][1][nt][e + 2], f16, base);
+        }
+      }
+    __syncthreads();
+    if (tid < RP) {
+      float top = kNoMax, sum = 0.0f;
+      for (int w = 0; w < kAttnWarps; ++w) top = fmaxf(top, sm[w * RP + tid]);
+      for (int w = 0; w < kAttnWarps; ++w) {
+        const float f = exp2_fast(sm[w * RP + tid] - top);
+        sf[w * RP + tid] = f;
+        sum += sl[w * RP + tid] * f;
+      }
+      sm[tid] = top;  // (this thread's column only)
+      sl[tid] = sum;
+    }
+    __syncthreads();
+    const bool whole = s0 == 0 && s1 == steps;
+    float* slot = p.partial + (int64_t)(2 * blockIdx.x + (first_segment ? 0 : 1)) * A::kSlot;
+    for (int x = tid; x < RP * D; x += kAttnThreads) {
+      const int r = x / D, ch = x % D;
+      float t = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kAttnWarps; ++w) t = fmaf(so[(w * RP + r) * D + ch], sf[w * RP + r], t);
+      if (!whole) {
+        slot[2 * RP + x] = t;
+      } else if (row0 + r < p.rows) {
+        const float sum = sl[r];
+        t = sum == 0.0f ? 0.0f : t / sum;
+        const int64_t at = (bh * p.rows + row0 + r) * D + ch;
+        if (p.out_f32)
+          static_cast<float*>(p.out)[at] = t;
+        else
+          static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(t);
+      }
+    }
+    if (tid < RP) {
+      if (!whole) {
+        slot[tid] = sm[tid];
+        slot[RP + tid] = sl[tid];
+      } else if (row0 + tid < p.rows) {
+        p.lse[bh * p.rows + row0 + tid] = (sm[tid] + log2f(sl[tid])) * kLn2;
+      }
+    }
+    __syncthreads();
+    u += n_tiles;
+    first_segment = false;
   }
 }
+
+// One CTA per (row of a tile, row tile, head, sequence): joins the partial
+// results of a head that several CTAs shared, in their order; writes the empty
+// result where there is nothing to see.
+template <int D, int NT>
+__global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const AttnParams p) {
+  constexpr int RP = 8 * NT, kSlot = RP * (D + 2);
+  constexpr int kParts = kJoinThreads / D;  // slots read at once
+  __shared__ float red[kJoinThreads];
+  __shared__ float tops[kJoinThreads / 32];
+  const int heads = p.c.Hkv * p.mt;
+  const int64_t hh = blockIdx.x;
+  const int b = (int)(hh / heads), hm = (int)(hh - (int64_t)b * heads);
+  const int h = hm / p.mt, r = blockIdx.y;
+  const int row = (hm - h * p.mt) * RP + r;
+  if (row >= p.rows) return;
+  wait_for_previous_launch();
+  const int64_t before = __ldcg(p.prefix + b), steps = __ldcg(p.prefix + b + 1) - before;
+  const int64_t units = (int64_t)__ldcg(p.prefix + p.B) * heads;
+  const int64_t out_row = ((int64_t)b * p.c.Hkv + h) * p.rows + row;
+  const int ch = threadIdx.x % D, part = threadIdx.x / D;
+  if (steps == 0) {
+    if (part == 0) {
+      if (p.out_f32)
+        static_cast<float*>(p.out)[out_row * D + ch] = 0.0f;
+      else
+        static_cast<uint16_t*>(p.out)[out_row * D + ch] = 0;
+    }
+    if (threadIdx.x == 0) p.lse[out_row] = -INFINITY;
+    return;
+  }
+  const int ctas = (int)min((int64_t)p.ctas, units);
+  const int64_t u0 = before * heads + hm * steps;
+  const int c0 = range_of(units, ctas, u0), c1 = range_of(units, ctas, u0 + steps - 1);
+  if (c0 == c1) return;  // one CTA had it all and wrote the result
+  // the head is CTA c's first segment unless c's range began before it
+  auto slot_of = [&](int c) -> const float* {
+    const bool first = range_begin(units, ctas, c) >= u0;
+    return p.partial + (int64_t)(2 * c + (first ? 0 : 1)) * kSlot;
+  };
+  float top = kNoMax;
+  for (int c = c0 + threadIdx.x; c <= c1; c += kJoinThreads) top = fmaxf(top, __ldcg(slot_of(c) + r));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+  if ((threadIdx.x & 31) == 0) tops[threadIdx.x / 32] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kJoinThreads / 32; ++w) top = fmaxf(top, tops[w]);
+  float t = 0.0f, sum = 0.0f;
+#pragma unroll 4
+  for (int c = c0 + part; c <= c1; c += kParts) {
+    const float* s = slot_of(c);
+    const float f = exp2_fast(__ldcg(s + r) - top);
+    sum = fmaf(__ldcg(s + RP + r), f, sum);
+    t = fmaf(__ldcg(s + 2 * RP + r * D + ch), f, t);
+  }
+  red[threadIdx.x] = t;
+  __syncthreads();
+  float total = 0.0f;
+  for (int w = 0; w < kParts; ++w) total += red[w * D + ch];
+  __syncthreads();
+  red[threadIdx.x] = sum;
+  __syncthreads();
+  sum = 0.0f;
+  for (int w = 0; w < kParts; ++w) sum += red[w * D + ch];
+  if (part == 0) {
+    const float v = sum == 0.0f ? 0.0f : total / sum;
+    if (p.out_f32)
+      static_cast<float*>(p.out)[out_row * D + ch] = v;
+    else
+      static_cast<__nv_bfloat16*>(p.out)[out_row * D + ch] = __float2bfloat16_rn(v);
+  }
+  if (threadIdx.x == 0) p.lse[out_row] = (top + log2f(sum)) * kLn2;
+}
+
+// CTAs of the attention launch: as many as run at once
+int attn_ctas(int nt, int sms) { return nt == 1 ? 2 * sms : sms; }
+
+template <int D, int NG, int NT>
+cudaError_t launch_attn(const AttnParams& p, int grid, cudaStream_t st) {
+  using A = Attn<D, NG, NT>;
+  const size_t smem = A::kSmem + (size_t)(p.B + 1) * sizeof(int);
+  constexpr size_t most = A::kSmem + (size_t)(kMostSequences + 1) * sizeof(int);
+  static_assert(most <= 227 * 1024, "shared memory");
+  cudaError_t e = cudaFuncSetAttribute(kv4_attn_kernel<D, NG, NT>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+  if (e != cudaSuccess) return e;
+  kv4_attn_kernel<D, NG, NT><<<grid, kAttnThreads, smem, st>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  const int rows = p.rows < 8 * NT ? p.rows : 8 * NT;
+  return launch_dependent(kv4_join_kernel<D, NT>, dim3(p.B * p.c.Hkv * p.mt, rows),
+                          dim3(kJoinThreads), 0, st, p);
+}
+
+template <int D, int NG>
+cudaError_t launch_attn(const AttnParams& p, int nt, int grid, cudaStream_t st) {
+  return nt == 1 ? launch_attn<D, NG, 1>(p, grid, st) : launch_attn<D, NG, 2>(p, grid, st);
+}
+
+size_t prefix_bytes(int B) { return ((size_t)(B + 1) * sizeof(int) + 15) / 16 * 16; }
 
 }  // namespace
 }  // namespace bsattn
@@ -129,7 +729,11 @@ extern "C" {
 size_t bsattn_kv4_attn_workspace(int B, int H, int kv_heads, int T, int D) {
   if (B <= 0 || H <= 0 || kv_heads <= 0 || T <= 0 || H % kv_heads != 0 || (D != 64 && D != 128))
     return 0;
-  return 16;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  const int nt = (int64_t)(H / kv_heads) * T <= 8 ? 1 : 2;
+  return prefix_bytes(B) +
+         (size_t)2 * attn_ctas(nt, device_sm_count(dev)) * 8 * nt * (D + 2) * sizeof(float);
 }
 
 bsattn_status bsattn_kv4_attn(const bsattn_kv4_cache* cache, const void* q, int B, int H, int T,
@@ -153,9 +757,18 @@ bsattn_status bsattn_kv4_attn(const bsattn_kv4_cache* cache, const void* q, int 
   if (flags & ~(unsigned)BSATTN_OUT_F32) return BSATTN_ERR_INVALID_ARG;
   if (!std::isfinite(scale)) return BSATTN_ERR_INVALID_ARG;
   const int64_t rows = (int64_t)(H / cache->kv_heads) * T;
-  if (rows > 128 || B > 65535) return BSATTN_ERR_UNSUPPORTED;
-  if (workspace_bytes < bsattn_kv4_attn_workspace(B, H, cache->kv_heads, T, cache->head_dim))
+  const int64_t listed = selected ? n_selected : columns;  // pages a sequence
+  const int64_t steps = (listed * cache->page_size + kStep - 1) / kStep;
+  const int nt = rows <= 8 ? 1 : 2;
+  const int mt = (int)((rows + 8 * nt - 1) / (8 * nt));
+  if (rows > 128 || B > kMostSequences || steps * B >= (1ll << 31) ||
+      (int64_t)B * cache->kv_heads * mt >= (1ll << 31))
+    return BSATTN_ERR_UNSUPPORTED;
+  if (workspace_bytes < bsattn_kv4_attn_workspace(B, H, cache->kv_heads, T, cache->head_dim) ||
+      workspace_bytes == 0)
     return BSATTN_ERR_INVALID_ARG;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return BSATTN_ERR_CUDA;
   p.q = static_cast<const uint16_t*>(q);
   p.table = block_table;
   p.table_stride = table_stride;
@@ -163,28 +776,30 @@ bsattn_status bsattn_kv4_attn(const bsattn_kv4_cache* cache, const void* q, int 
   p.lengths = lengths;
   p.selected = selected;
   p.n_selected = n_selected;
+  p.B = B;
   p.T = T;
   p.rows = (int)rows;
+  p.mt = mt;
   p.scale_log2 = (float)((double)scale * 1.4426950408889634074);
   p.out = out;
   p.lse = lse;
   p.out_f32 = (flags & BSATTN_OUT_F32) ? 1 : 0;
-  const dim3 grid((int)rows, cache->kv_heads, B);
+  p.prefix = static_cast<int*>(workspace);
+  p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + prefix_bytes(B));
+  p.ctas = attn_ctas(nt, device_sm_count(dev));
+  const int64_t most = steps * B * cache->kv_heads * mt;  // units, at most
+  const int grid = (int)(most < p.ctas ? most : p.ctas);
+  p.ctas = grid;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (cache->head_dim == 64) {
-    if (cache->group == 32)
-      kv4_attn_kernel<64, 4><<<grid, kAttnThreads, 0, st>>>(p);
-    else
-      kv4_attn_kernel<64, 8><<<grid, kAttnThreads, 0, st>>>(p);
-  } else {
-    if (cache->group == 32)
-      kv4_attn_kernel<128, 4><<<grid, kAttnThreads, 0, st>>>(p);
-    else if (cache->group == 64)
-      kv4_attn_kernel<128, 8><<<grid, kAttnThreads, 0, st>>>(p);
-    else
-      kv4_attn_kernel<128, 16><<<grid, kAttnThreads, 0, st>>>(p);
-  }
-  return from_cuda(cudaGetLastError());
+  const int groups = cache->head_dim / cache->group;
+  cudaError_t e;
+  if (cache->head_dim == 64)
+    e = groups == 1 ? launch_attn<64, 1>(p, nt, grid, st) : launch_attn<64, 2>(p, nt, grid, st);
+  else
+    e = groups == 1   ? launch_attn<128, 1>(p, nt, grid, st)
+        : groups == 2 ? launch_attn<128, 2>(p, nt, grid, st)
+                      : launch_attn<128, 4>(p, nt, grid, st);
+  return from_cuda(e);
 }
 
 }  // extern "C"

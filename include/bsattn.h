@@ -563,7 +563,7 @@ bsattn_status bsattn_kv4_select(const bsattn_kv4_cache* cache, const void* q, in
  * cached tokens at positions up to its own: all, or those of the listed pages.
  * A query that sees none gets O = 0, LSE = -inf.
  *   q          device bf16 [B][H][T][head_dim], 16-byte aligned; query head h reads
- *              key/value head h / (H / kv_heads); (H / kv_heads) * T <= 128.
+ *              key/value head h / (H / kv_heads); (H / kv_heads) * T <= 128; B <= 4096.
  *   lengths    cached tokens, the T new ones included.
  *   selected   device int32 [B][kv_heads][n_selected], strictly ascending pages, then
  *              negative entries (as bsattn_kv4_select writes it), or null with

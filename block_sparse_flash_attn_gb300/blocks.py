@@ -5,11 +5,18 @@
 """
 from __future__ import annotations
 
+import functools
+
 import torch
 
 import block_sparse_flash_attn_gb300 as _bs
 
 from ._args import launch_on, pointer, tensor
+
+
+@functools.lru_cache(maxsize=256)
+def _workspace(*sizes):  # a function of the sizes
+    return _bs.load().bsattn_select_blocks_workspace(*sizes)
 
 
 def select_blocks(q: torch.Tensor, k: torch.Tensor, keep: int, causal: bool = False,
@@ -51,16 +58,16 @@ def select_blocks(q: torch.Tensor, k: torch.Tensor, keep: int, causal: bool = Fa
             raise ValueError(f"allow must be [B, H or 1, S/128, S/{key_block}]")
         allow_heads = allow.shape[1]
     flags = (_bs.CAUSAL if causal else 0) | (_bs.KEY_BLOCK_64 if key_block == 64 else 0)
-    with launch_on(q.device, stream):
+    with launch_on(q.device, stream) as on:
         if out is None:
             out = torch.empty((B, H, nb, nk), dtype=torch.uint8, device=q.device)
         else:
             tensor("out", out, (torch.uint8,), (B, H, nb, nk), q.device)
         lib = _bs.load()
-        nbytes = lib.bsattn_select_blocks_workspace(B, H, Hkv, S, D, flags)
+        nbytes = _workspace(B, H, Hkv, S, D, flags)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
         _bs._check(lib.bsattn_select_blocks(
             q.data_ptr(), k.data_ptr(), B, H, Hkv, S, D, keep, sink, local, flags, pointer(allow),
-            allow_heads, out.data_ptr(), ws.data_ptr(), nbytes, _bs._stream_handle(None)),
+            allow_heads, out.data_ptr(), ws.data_ptr(), nbytes, on),
             "bsattn_select_blocks")
     return out

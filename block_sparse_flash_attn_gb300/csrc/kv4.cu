@@ -36,56 +36,93 @@ struct AppendParams {
   int T;
 };
 
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {  // of bf16 pairs; NaN stays
+  __nv_bfloat162 r = __hmin2_nan(*reinterpret_cast<__nv_bfloat162*>(&a),
+                                 *reinterpret_cast<__nv_bfloat162*>(&b));
+  return *reinterpret_cast<uint32_t*>(&r);
+}
+
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<__nv_bfloat162*>(&a),
+                                 *reinterpret_cast<__nv_bfloat162*>(&b));
+  return *reinterpret_cast<uint32_t*>(&r);
+}
+
 // Eight channels of one group's row -> codes (a nibble each, the first
-// lowest), and the group's step and minimum.  GL lanes hold a group.
+// lowest; n[i]: channels 2i, 2i + 1 as floats), and the group's step and least.
+// GL lanes hold a group.
 //
-// (x - minimum) / step is first estimated with the reciprocal, then settled
-// by its exact remainder: r = d - n step is exact in 32 bits (|r| <= step),
-// and |r| against step / 2 says whether n is the nearest, so codes do not
-// depend on how a division rounds.
+// (x - least) / step is first estimated with the reciprocal and rounded by
+// adding 1.5 2^23 (no conversion instruction), then settled by its exact
+// remainder: r = d - n step is exact in 32 bits (|r| <= step), and |r| against
+// step / 2 says whether n is the nearest (at the half itself: whether n is
+// even), so codes do not depend on how a division rounds.
 template <int GL>
-__device__ __forceinline__ uint32_t quantise(const float (&x)[8], float& step, float& least) {
-  float mn = x[0], mx = x[0], z = 0.0f;
+__device__ __forceinline__ uint32_t quantise(const uint4& raw, F2 (&n)[4], float& step,
+                                             float& least) {
+  uint32_t lo = min2(min2(raw.x, raw.y), min2(raw.z, raw.w));
+  uint32_t hi = max2(max2(raw.x, raw.y), max2(raw.z, raw.w));
+  lo = min2(lo, __byte_perm(lo, lo, 0x1032));
+  hi = max2(hi, __byte_perm(hi, hi, 0x1032));
+  // (least, -most) in one word: one shuffle a level
+  uint32_t both = (lo & 0x0000FFFFu) | ((hi ^ 0x80000000u) & 0xFFFF0000u);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    mn = fminf(mn, x[i]);
-    mx = fmaxf(mx, x[i]);
-    z += x[i] * 0.0f;  // NaN for a value that is not finite
-  }
-  if (z != 0.0f) mx = INFINITY;
-#pragma unroll
-  for (int o = 1; o < GL; o <<= 1) {
-    mn = fminf(mn, __shfl_xor_sync(0xFFFFFFFFu, mn, o));
-    mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-  }
-  const float range = mx - mn;
+  for (int o = 1; o < GL; o <<= 1) both = min2(both, __shfl_xor_sync(0xFFFFFFFFu, both, o));
+  least = bf16_lo(both);
+  const float range = -bf16_hi(both) - least;  // NaN or infinite for a group that is not finite
   step = __bfloat162float(__float2bfloat16_rn(__fdiv_rn(range, 15.0f)));
-  least = mn;
-  if (!(range <= 3.4028234e38f)) {
-    step = least = __int_as_float(0x7FC00000);
-    return 0u;
-  }
-  if (step < kLeastStep) {
-    step = 0.0f;
-    return 0u;
-  }
-  const float inv = __frcp_rn(step), half = 0.5f * step;
-  uint32_t codes = 0;
+  const bool finite = range <= 3.4028234e38f, flat = step < kLeastStep;
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(step));
+  const uint32_t half = __float_as_uint(0.5f * step);
+  const F2 vinv = f2(inv), vstep = f2(-step), vleast = f2(-least);
+  const F2 magic = f2(12582912.0f), unmagic = f2(-12582912.0f);
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float d = x[i] - mn;
-    int n = __float2int_rn(d * inv);
-    const float r = fmaf(-(float)n, step, d);
-    if (r > half || (r == half && (n & 1))) n += 1;
-    if (r < -half || (r == -half && (n & 1))) n -= 1;
-    codes |= (uint32_t)min(max(n, 0), 15) << (4 * i);
+  for (int i = 0; i < 4; ++i) {
+    const F2 d = bf16_pair(w[i]) + vleast;
+    const F2 t = fma2(d, vinv, magic);
+    const F2 nf = t + unmagic;
+    const float2 r = split(fma2(nf, vstep, d)), tt = split(t);
+    float2 k = split(nf);
+    // too far: above half a step, or at it with n odd
+    if (fabsf(r.x) > __uint_as_float(half - (__float_as_uint(tt.x) & 1u))) k.x += copysignf(1.0f, r.x);
+    if (fabsf(r.y) > __uint_as_float(half - (__float_as_uint(tt.y) & 1u))) k.y += copysignf(1.0f, r.y);
+    n[i] = f2(k.x, k.y);
+  }
+  // four codes a sum: n0 + 16 n1 + 256 n2 + 4096 n3 (exact), both halves at once
+  const float2 a = split(n[0]), b = split(n[1]), c = split(n[2]), e = split(n[3]);
+  F2 sum = fma2(f2(b.y, e.y), f2(4096.0f), f2(8388608.0f));
+  sum = fma2(f2(b.x, e.x), f2(256.0f), sum);
+  sum = fma2(f2(a.y, c.y), f2(16.0f), sum);
+  sum = sum + f2(a.x, c.x);
+  const float2 s = split(sum);
+  uint32_t codes = __byte_perm(__float_as_uint(s.x), __float_as_uint(s.y), 0x5410);
+  if (!finite) step = least = __int_as_float(0x7FC00000);
+  if (flat) step = 0.0f;
+  if (!finite || flat) {
+    codes = 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) n[i] = f2(0.0f);
   }
   return codes;
 }
 
-__device__ __forceinline__ void decode8(uint32_t codes, float step, float least, float (&x)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = fmaf(step, (float)((codes >> (4 * i)) & 15u), least);
+// The values of eight codes.  Code i is read as (2^23 + code 16^i) - 2^23 in
+// place (codes 5 to 7 after one shift) and multiplied by step 16^-i: the same
+// product, exactly, as step * code.
+__device__ __forceinline__ void decode8(uint32_t codes, float step, float least, F2 (&x)[4]) {
+  const uint32_t up = codes >> 20;
+  const F2 off = f2(-8388608.0f), l = f2(least);
+  auto field = [](uint32_t v, int bit) {
+    return __uint_as_float((v & (15u << bit)) | 0x4B000000u);
+  };
+  const float s1 = step * 0.0625f, s2 = step * 0.00390625f;
+  const float s3 = step * 2.44140625e-4f, s4 = step * 1.52587890625e-5f;
+  x[0] = fma2(f2(field(codes, 0), field(codes, 4)) + off, f2(step, s1), l);
+  x[1] = fma2(f2(field(codes, 8), field(codes, 12)) + off, f2(s2, s3), l);
+  x[2] = fma2(f2(field(codes, 16), field(up, 0)) + off, f2(s4, step), l);
+  x[3] = fma2(f2(field(up, 4), field(up, 8)) + off, f2(s1, s2), l);
 }
 
 // One CTA: one page of one sequence and head, the tokens of this call that
@@ -120,9 +157,9 @@ __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const AppendPar
   const uint16_t* v = p.v + b * p.vb + h * p.vh + cl * 8;
   const int64_t row0 = p.c.row(pg, h, 0);
 
-  Sum2 s[8];
+  Sum2x2 s[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) s[i] = Sum2{0.0f, 0.0f};
+  for (int i = 0; i < 4; ++i) s[i].hi = s[i].lo = f2(0.0f);
   for (int i0 = warp * R; i0 < 2 * n; i0 += kRowWarps * R) {
     const int i = i0 + sub;
     const bool is_k = i < n;
@@ -130,9 +167,9 @@ __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const AppendPar
     uint4 raw = make_uint4(0, 0, 0, 0);
     if (i < 2 * n)
       raw = __ldg(reinterpret_cast<const uint4*>(is_k ? k + (t0 + r) * p.kt : v + (t0 + r) * p.vt));
-    float x[8], step, least;
-    unpack8(raw, x);
-    const uint32_t codes = quantise<GL>(x, step, least);
+    F2 x[4];
+    float step, least;
+    const uint32_t codes = quantise<GL>(raw, x, step, least);
     if (i < 2 * n) {
       const int64_t row = row0 + place0 + r;
       reinterpret_cast<uint32_t*>(is_k ? p.c.k_codes : p.c.v_codes)[row * L + cl] = codes;
@@ -140,9 +177,8 @@ __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const AppendPar
         reinterpret_cast<uint32_t*>(is_k ? p.c.k_scales : p.c.v_scales)[row * NG + cl / GL] =
             pack_bf16(step, least);
       if (is_k && fills) {
-        decode8(codes, step, least, x);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) add_exact(s[c], x[c]);
+        for (int c = 0; c < 4; ++c) add_exact(s[c], fma2(x[c], f2(step), f2(least)));
       }
     }
   }
@@ -151,10 +187,10 @@ __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const AppendPar
     const int64_t row = row0 + r;
     const uint32_t codes = reinterpret_cast<const uint32_t*>(p.c.k_codes)[row * L + cl];
     const uint32_t sc = reinterpret_cast<const uint32_t*>(p.c.k_scales)[row * NG + cl / GL];
-    float x[8];
+    F2 x[4];
     decode8(codes, bf16_lo(sc), bf16_hi(sc), x);
 #pragma unroll
-    for (int c = 0; c < 8; ++c) add_exact(s[c], x[c]);
+    for (int c = 0; c < 4; ++c) add_exact(s[c], x[c]);
   }
   write_rounded_mean<D>(s, p.c.page, false, p.c.k_means + ((int64_t)pg * p.c.Hkv + h) * D);
 }
@@ -166,46 +202,49 @@ struct ReadParams {
   int columns;
   const int* start;
   const int* counts;
-  int T, rows;  // rows = B * Hkv * T
+  int T;
   uint16_t* k;
   uint16_t* v;
 };
 
-// A lane group (D / 8 lanes) decodes kReadRows consecutive rows of K and V.
-// Rows behind a sequence's count are zero.
+// One CTA: consecutive rows of one sequence and head; a lane group (D / 8
+// lanes) decodes kReadRows of them, K and V.  Rows behind the count are zero.
 template <int D, int GL>
 __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const ReadParams p) {
-  constexpr int L = D / 8, R = 32 / L, NG = L / GL;
-  const int lane = threadIdx.x & 31, cl = lane % L;
-  const int group = (blockIdx.x * kRowWarps + (threadIdx.x >> 5)) * R + lane / L;
+  constexpr int L = D / 8, NG = L / GL;
+  constexpr int kGroups = kRowThreads / L;
+  const int cl = threadIdx.x % L, group = threadIdx.x / L;
+  const int h = blockIdx.y, b = blockIdx.z;
+  const int t0 = blockIdx.x * (kGroups * kReadRows) + group;
+  const int count = p.counts ? __ldg(p.counts + b) : p.T;
+  const int64_t start = __ldg(p.start + b);
+  const int* table = p.table + b * p.table_stride;
   uint32_t code[kReadRows][2], sc[kReadRows][2];
-  const int64_t first = (int64_t)group * kReadRows;
 #pragma unroll
   for (int u = 0; u < kReadRows; ++u) {
+    const int t = t0 + u * kGroups;
     code[u][0] = code[u][1] = sc[u][0] = sc[u][1] = 0u;
-    const int64_t r = first + u;
-    if (r >= p.rows) continue;
-    const int bh = (int)(r / p.T), t = (int)(r - (int64_t)bh * p.T);
-    const int b = bh / p.c.Hkv, h = bh - b * p.c.Hkv;
-    if (p.counts && t >= __ldg(p.counts + b)) continue;
-    const int64_t pos = (int64_t)__ldg(p.start + b) + t;
-    const int pg = page_at(p.c, p.table + b * p.table_stride, p.columns, pos >> p.c.log_page);
+    if (t >= p.T || t >= count) continue;
+    const int64_t pos = start + t;
+    const int pg = page_at(p.c, table, p.columns, pos >> p.c.log_page);
     if (pg < 0) continue;
     const int64_t row = p.c.row(pg, h, (int)(pos & (p.c.page - 1)));
-    code[u][0] = reinterpret_cast<const uint32_t*>(p.c.k_codes)[row * L + cl];
-    code[u][1] = reinterpret_cast<const uint32_t*>(p.c.v_codes)[row * L + cl];
-    sc[u][0] = reinterpret_cast<const uint32_t*>(p.c.k_scales)[row * NG + cl / GL];
-    sc[u][1] = reinterpret_cast<const uint32_t*>(p.c.v_scales)[row * NG + cl / GL];
+    code[u][0] = __ldg(reinterpret_cast<const uint32_t*>(p.c.k_codes) + row * L + cl);
+    code[u][1] = __ldg(reinterpret_cast<const uint32_t*>(p.c.v_codes) + row * L + cl);
+    sc[u][0] = __ldg(reinterpret_cast<const uint32_t*>(p.c.k_scales) + row * NG + cl / GL);
+    sc[u][1] = __ldg(reinterpret_cast<const uint32_t*>(p.c.v_scales) + row * NG + cl / GL);
   }
+  const int64_t out = (((int64_t)b * p.c.Hkv + h) * p.T) * D + cl * 8;
 #pragma unroll
   for (int u = 0; u < kReadRows; ++u) {
-    const int64_t r = first + u;
-    if (r >= p.rows) continue;
+    const int t = t0 + u * kGroups;
+    if (t >= p.T) continue;
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
-      float x[8];
+      F2 x[4];
       decode8(code[u][kv], bf16_lo(sc[u][kv]), bf16_hi(sc[u][kv]), x);
-      *reinterpret_cast<uint4*>((kv ? p.v : p.k) + r * D + cl * 8) = pack8(x);
+      *reinterpret_cast<uint4*>((kv ? p.v : p.k) + out + (int64_t)t * D) = make_uint4(
+          pack_bf16(x[0]), pack_bf16(x[1]), pack_bf16(x[2]), pack_bf16(x[3]));
     }
   }
 }
@@ -529,19 +568,17 @@ bsattn_status bsattn_kv4_read(const bsattn_kv4_cache* cache, int B, int T,
   if (!ints_ok(block_table) || !ints_ok(start) || (counts && !ints_ok(counts)))
     return BSATTN_ERR_INVALID_ARG;
   if (B <= 0 || T <= 0 || columns <= 0 || table_stride < 0) return BSATTN_ERR_INVALID_ARG;
-  const int64_t rows = (int64_t)B * cache->kv_heads * T;
-  if (rows >= (1ll << 31) - 4096) return BSATTN_ERR_UNSUPPORTED;
+  if (B > 65535 || T > (1 << 30)) return BSATTN_ERR_UNSUPPORTED;
   p.table = block_table;
   p.table_stride = table_stride;
   p.columns = columns;
   p.start = start;
   p.counts = counts;
   p.T = T;
-  p.rows = (int)rows;
   p.k = static_cast<uint16_t*>(k);
   p.v = static_cast<uint16_t*>(v);
-  const int per_cta = kRowWarps * (256 / cache->head_dim) * kReadRows;
-  const int grid = (int)((rows + per_cta - 1) / per_cta);
+  const int per_cta = kRowThreads / (cache->head_dim / 8) * kReadRows;
+  const dim3 grid((T + per_cta - 1) / per_cta, cache->kv_heads, B);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
 #define BSATTN_CALL(D, GL) kv4_read_kernel<D, GL><<<grid, kRowThreads, 0, st>>>(p)
   BSATTN_KV4_DISPATCH(cache, BSATTN_CALL);

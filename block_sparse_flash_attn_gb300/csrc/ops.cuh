@@ -30,6 +30,45 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
                     pack_bf16(f[6], f[7]));
 }
 
+// ---------------------------------------------------------------------------
+// Two 32-bit floats a register pair: sm_103a adds, multiplies and fuses both
+// with one instruction, each rounded as the single instruction rounds.
+// ---------------------------------------------------------------------------
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ F2 f2(float both) { return f2(both, both); }
+__device__ __forceinline__ float2 split(F2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+  return r;
+}
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 bf16_pair(uint32_t w) { return f2(bf16_lo(w), bf16_hi(w)); }
+__device__ __forceinline__ uint32_t pack_bf16(F2 a) {
+  const float2 s = split(a);
+  return pack_bf16(s.x, s.y);
+}
+
 // A programmatic dependent waits here for the launch before it (griddepcontrol
 // is a no-op in a kernel launched without the attribute).
 __device__ __forceinline__ void wait_for_previous_launch() {
@@ -73,6 +112,20 @@ __device__ __forceinline__ void add_exact(Sum2& s, float x) {
   s.lo = __fadd_rn(s.lo, e);
 }
 
+// The same for two sums at once; a - b is taken as fma(b, -1, a), exact alike.
+struct Sum2x2 {
+  F2 hi, lo;
+};
+
+__device__ __forceinline__ void add_exact(Sum2x2& s, F2 x) {
+  const F2 neg = f2(-1.0f);
+  const F2 t = s.hi + x;
+  const F2 z = fma2(s.hi, neg, t);
+  const F2 e = fma2(fma2(z, neg, t), neg, s.hi) + fma2(z, neg, x);
+  s.hi = t;
+  s.lo = s.lo + e;
+}
+
 __device__ __forceinline__ void add_exact(Sum2& s, const Sum2& o) {
   add_exact(s, o.hi);
   s.lo = __fadd_rn(s.lo, o.lo);
@@ -112,16 +165,23 @@ __device__ __forceinline__ float rint_scaled(const Sum2& s, int shift) {
 }
 
 // The mean of `rows` rows of a block (rows a power of two), rounded to 7 bits
-// beside its largest entry, by a CTA of 128 threads: s[i] is this thread's sum
-// of channel (lane % (D/8)) * 8 + i over the rows that it saw.  Writes, as
+// beside its largest entry, by a CTA of 128 threads: pairs[i] are this thread's
+// sums of channels (lane % (D/8)) * 8 + 2i, 2i + 1 over the rows that it saw.  Writes, as
 // bf16, the whole numbers t = rint(mean 2^(6 - E)) or the values t 2^(E - 6).
 template <int D>
-__device__ __forceinline__ void write_rounded_mean(Sum2 (&s)[8], int rows, bool whole,
+__device__ __forceinline__ void write_rounded_mean(const Sum2x2 (&pairs)[4], int rows, bool whole,
                                                    uint16_t* out) {
   constexpr int L = D / 8, W = 4;
   __shared__ Sum2 part[W][D];
   __shared__ int top[W];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  Sum2 s[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 hi = split(pairs[i].hi), lo = split(pairs[i].lo);
+    s[2 * i] = Sum2{hi.x, lo.x};
+    s[2 * i + 1] = Sum2{hi.y, lo.y};
+  }
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
 #pragma unroll

@@ -11,11 +11,15 @@
 // V rows are copied.
 //
 // Both read each input once and write each output once and do some 10 (25)
-// operations an element: memory bound.  A row is held by D / 8 lanes, 16
-// bytes each, so the norm's sum and the exchange between the two halves of a
-// rotated row are shuffles inside the lane group; a warp takes rows of one
-// token, so the token's angles are loaded once for all its rows, and has all
-// its rows' loads in flight at once.
+// operations an element: memory bound, if few enough instructions go into an
+// element.  A row is held by D / 8 lanes, 16 bytes each, so the norm's sum and
+// the exchange between the two halves of a rotated row are shuffles inside the
+// lane group.  A warp takes rows of one token and one kind (Q, K or V): weights
+// and angles are multiplied once for all its rows,
+//   y = r (x (w cos) + x_partner (w_partner sin)),
+// and all its rows' loads are in flight at once.  A CTA's eight warps take
+// eight consecutive tokens of the same heads, 2 KB and more of every head-major
+// row run.  The arithmetic is on register pairs (two floats an instruction).
 #include <cmath>
 #include <cstdint>
 
@@ -27,14 +31,21 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 constexpr int kRopeWarps = kRopeThreads / 32;
+#ifndef BWDW
+#define BWDW 4
+#endif
+#ifndef BWDP
+#define BWDP 5
+#endif
+constexpr int kBwdWarps = BWDW;   // the backward kernel: warps a CTA
+constexpr int kBwdPerSm = BWDP;   // and CTAs an SM (its registers' limit)
 
 struct RopeParams {
   const uint16_t* x;  // [B][S][heads][D], strides xb and xs (elements)
   int64_t xb, xs;
-  int S, H, Hkv, heads;  // heads = H + 2 Hkv
-  int chunks;            // tasks a token: chunks of heads
-  int tasks;             // tokens * chunks
-  const void* wq;        // [D] bf16 or fp32, null: no norm
+  int tokens, S, H, Hkv;
+  int q_chunks, k_chunks;  // warps' worth of heads of Q, and of K (and of V)
+  const void* wq;          // [D] bf16 or fp32, null: no norm
   const void* wk;
   int w_f32;
   const float2* table;  // [n_pos][half] (cos, sin), null: no rotation
@@ -47,33 +58,49 @@ struct RopeParams {
   void* v;
   uint16_t* dx;
   int64_t dxb, dxs;
-  float* partial;  // backward: [CTAs][2][D] weight gradients
+  float* partial;  // backward: [(q_chunks + k_chunks) * groups][D] weight gradients
+  int groups;      // backward: CTAs a chunk
 };
 
-template <int D>
+// The heads of one chunk: kind 0, 1, 2 = Q, K, V; heads [first, end) of the
+// kind; `row` is the first one's place in a token of x.
+struct Chunk {
+  int kind, first, end, row;
+};
+__device__ __forceinline__ Chunk chunk_of(const RopeParams& p, int chunk, int rows) {
+  Chunk c;
+  c.kind = chunk < p.q_chunks ? 0 : chunk < p.q_chunks + p.k_chunks ? 1 : 2;
+  const int at = chunk - (c.kind == 0 ? 0 : c.kind == 1 ? p.q_chunks : p.q_chunks + p.k_chunks);
+  const int heads = c.kind == 0 ? p.H : p.Hkv;
+  c.first = at * rows;
+  c.end = min(heads, c.first + rows);
+  c.row = c.first + (c.kind == 0 ? 0 : c.kind == 1 ? p.H : p.H + p.Hkv);
+  return c;
+}
+
 __device__ __forceinline__ void load_weights(const void* w, int f32, int c0, float (&out)[8]) {
   if (w == nullptr) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) out[i] = 1.0f;
   } else if (f32) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) out[i] = __ldg(static_cast<const float*>(w) + c0 + i);
+    const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(w) + c0);
+    const float4 a = __ldg(f), b = __ldg(f + 1);
+    out[0] = a.x, out[1] = a.y, out[2] = a.z, out[3] = a.w;
+    out[4] = b.x, out[5] = b.y, out[6] = b.z, out[7] = b.w;
   } else {
     unpack8(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(w) + c0)), out);
   }
 }
 
-// cos and sin of this lane's 8 channels.  Pairs side by side: 4 pairs, the
-// first four entries.  Pairs half a row apart: one entry a channel, the sine
-// negative in the first half, so that y = n cos + n_partner sin in both.
-// Channels behind the rotated ones: cos 1, sin 0.  A position outside the
-// table: NaN.
+// cos and sin of this lane's 8 channels, the sine with the sign it has in
+// y = n cos + n_partner sin.  Channels behind the rotated ones: cos 1, sin 0.
+// A position outside the table: NaN.
 template <bool INTER>
 __device__ __forceinline__ void load_angles(const RopeParams& p, int token, int s, int c0,
                                             float (&cs)[8], float (&sn)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) cs[i] = 1.0f, sn[i] = 0.0f;
-  if (p.table == nullptr || c0 >= 2 * p.half) return;
+  if (c0 >= 2 * p.half) return;
   const int pos = p.pos ? __ldg(p.pos + token) : s;
   if (pos < 0 || pos >= p.n_pos) {
 #pragma unroll
@@ -81,34 +108,19 @@ __device__ __forceinline__ void load_angles(const RopeParams& p, int token, int 
     return;
   }
   const int first = INTER ? c0 / 2 : (c0 < p.half ? c0 : c0 - p.half);
-  const float4* t =
-      reinterpret_cast<const float4*>(p.table + (size_t)pos * p.half + first);
-  const float sign = (!INTER && c0 < p.half) ? -1.0f : 1.0f;
+  const float4* t = reinterpret_cast<const float4*>(p.table + (size_t)pos * p.half + first);
+  const float sign = c0 < p.half ? -1.0f : 1.0f;
 #pragma unroll
   for (int i = 0; i < (INTER ? 2 : 4); ++i) {
     const float4 f = __ldg(t + i);
-    cs[2 * i] = f.x, sn[2 * i] = sign * f.y;
-    cs[2 * i + 1] = f.z, sn[2 * i + 1] = sign * f.w;
-  }
-}
-
-// Rotate this lane's 8 values (dir = 1), or turn them back (dir = -1).
-// `partner`: the lane that holds the other half (this lane: nothing to swap).
-template <bool INTER>
-__device__ __forceinline__ void rotate(float (&y)[8], const float (&cs)[8], const float (&sn)[8],
-                                       float dir, int partner) {
-  if (INTER) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float a = y[2 * i], b = y[2 * i + 1], s = dir * sn[i];
-      y[2 * i] = a * cs[i] - b * s;
-      y[2 * i + 1] = b * cs[i] + a * s;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float o = __shfl_sync(0xFFFFFFFFu, y[i], partner);
-      y[i] = y[i] * cs[i] + o * (dir * sn[i]);
+    if (INTER) {  // two pairs of channels
+      cs[4 * i] = cs[4 * i + 1] = f.x;
+      cs[4 * i + 2] = cs[4 * i + 3] = f.z;
+      sn[4 * i] = -f.y, sn[4 * i + 1] = f.y;
+      sn[4 * i + 2] = -f.w, sn[4 * i + 3] = f.w;
+    } else {
+      cs[2 * i] = f.x, sn[2 * i] = sign * f.y;
+      cs[2 * i + 1] = f.z, sn[2 * i + 1] = sign * f.w;
     }
   }
 }
@@ -120,191 +132,226 @@ __device__ __forceinline__ float group_sum(float v) {
   return v;
 }
 
-__device__ __forceinline__ int rotation_partner(const RopeParams& p, int lane, int c0, bool inter) {
-  if (inter || p.table == nullptr || c0 >= 2 * p.half) return lane;
-  return c0 < p.half ? lane + p.half / 8 : lane - p.half / 8;
+// The channel offset (0, or +-half a rotated row) of the partner's channels
+// when pairs lie half a row apart; the partner lane is that / 8 away.
+__device__ __forceinline__ int partner_offset(const RopeParams& p, int c0) {
+  if (c0 >= 2 * p.half) return 0;
+  return c0 < p.half ? p.half : -p.half;
 }
 
-// One warp: U * (32 / L) consecutive heads of one token.
+// One warp: up to U * (32 / L) heads of one kind of one token.
 template <int D, bool INTER, int U>
 __global__ void __launch_bounds__(kRopeThreads) rope_fwd_kernel(const RopeParams p) {
-  constexpr int L = D / 8;    // lanes a row
-  constexpr int R = 32 / L;   // rows a warp holds at once
+  constexpr int L = D / 8;   // lanes a row
+  constexpr int R = 32 / L;  // rows a warp holds at once
   const int lane = threadIdx.x & 31;
-  const unsigned task = blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
-  if (task >= (unsigned)p.tasks) return;
-  const int token = task / (unsigned)p.chunks;
-  const int h0 = (int)(task - (unsigned)token * p.chunks) * (U * R) + lane / L;
-  const int b = token / p.S, s = token - b * p.S;
-  const int c0 = (lane % L) * 8;
+  const unsigned chunks = p.q_chunks + 2 * p.k_chunks;
+  const unsigned block = blockIdx.x / chunks;
+  const Chunk c = chunk_of(p, blockIdx.x - block * chunks, U * R);
+  const unsigned token = block * kRopeWarps + (threadIdx.x >> 5);
+  if (token >= (unsigned)p.tokens) return;
+  const int b = token / (unsigned)p.S, s = token - b * p.S;
+  const int c0 = (lane % L) * 8, h0 = c.first + lane / L;
 
-  const uint16_t* xr = p.x + b * p.xb + s * p.xs + c0;
+  const uint16_t* xr = p.x + b * p.xb + s * p.xs + (c.row + lane / L) * D + c0;
   uint4 raw[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int h = h0 + u * R;
     raw[u] = make_uint4(0, 0, 0, 0);
-    if (h < p.heads) raw[u] = __ldg(reinterpret_cast<const uint4*>(xr + h * D));
+    if (h0 + u * R < c.end) raw[u] = __ldg(reinterpret_cast<const uint4*>(xr + u * R * D));
   }
-  float cs[8], sn[8], wq[8], wk[8];
-  load_angles<INTER>(p, token, s, c0, cs, sn);
-  load_weights<D>(p.wq, p.w_f32, c0, wq);
-  load_weights<D>(p.wk, p.w_f32, c0, wk);
-  const int partner = rotation_partner(p, lane, c0, INTER);
+  const int heads = c.kind == 0 ? p.H : p.Hkv;
+  uint16_t* out = static_cast<uint16_t*>(c.kind == 0 ? p.q : c.kind == 1 ? p.k : p.v) +
+                  (((int64_t)b * heads + h0) * p.S + s) * D + c0;
+  const int64_t next = (int64_t)R * p.S * D;
+  const bool norm = p.wq != nullptr;
+  if (c.kind == 2 || (!norm && p.half == 0)) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (h0 + u * R < c.end) *reinterpret_cast<uint4*>(out + u * next) = raw[u];
+    return;
+  }
+  F2 wc[4], ws[4];  // w cos, w_partner sin
+  const int off = INTER ? 0 : partner_offset(p, c0);
+  {
+    float cs[8], sn[8], w[8];
+    load_angles<INTER>(p, token, s, c0, cs, sn);
+    const void* weight = c.kind == 0 ? p.wq : p.wk;
+    load_weights(weight, p.w_f32, c0, w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) wc[i] = f2(w[2 * i] * cs[2 * i], w[2 * i + 1] * cs[2 * i + 1]);
+    if (!INTER) load_weights(weight, p.w_f32, c0 + off, w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      ws[i] = INTER ? f2(w[2 * i + 1] * sn[2 * i], w[2 * i] * sn[2 * i + 1])
+                    : f2(w[2 * i] * sn[2 * i], w[2 * i + 1] * sn[2 * i + 1]);
+  }
+  const int partner = lane + off / 8;
+  const uint32_t turns = c0 < 2 * p.half ? 0xFFFFFFFFu : 0u;  // an infinity stays one elsewhere
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int h = h0 + u * R;
-    float y[8];
-    unpack8(raw[u], y);
-    if (p.wq != nullptr) {
-      float ss = 0.0f;
+    const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+    F2 x[4], ss = f2(0.0f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss += y[i] * y[i];
-      const float r = rsqrtf(group_sum<L>(ss) * (1.0f / D) + p.eps);
+    for (int i = 0; i < 4; ++i) {
+      x[i] = bf16_pair(w[i]);
+      ss = fma2(x[i], x[i], ss);
+    }
+    F2 r = f2(1.0f);
+    if (norm) {
+      const float2 t = split(ss);
+      r = f2(rsqrtf(group_sum<L>(t.x + t.y) * (1.0f / D) + p.eps));
+    }
+    uint32_t y[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] *= r * (h < p.H ? wq[i] : wk[i]);
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t o = INTER ? __byte_perm(w[i], w[i], 0x1032)
+                               : __shfl_sync(0xFFFFFFFFu, w[i], partner);
+      y[i] = pack_bf16(fma2(bf16_pair(o & turns), ws[i], x[i] * wc[i]) * r);
     }
-    rotate<INTER>(y, cs, sn, 1.0f, partner);
-    if (h < p.H) {
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.q) +
-                                (((int64_t)b * p.H + h) * p.S + s) * D + c0) = pack8(y);
-    } else if (h < p.H + p.Hkv) {
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.k) +
-                                (((int64_t)b * p.Hkv + h - p.H) * p.S + s) * D + c0) = pack8(y);
-    } else if (h < p.heads) {
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.v) +
-                                (((int64_t)b * p.Hkv + h - p.H - p.Hkv) * p.S + s) * D + c0) =
-          raw[u];
-    }
+    if (h0 + u * R < c.end)
+      *reinterpret_cast<uint4*>(out + u * next) = make_uint4(y[0], y[1], y[2], y[3]);
   }
 }
 
-// The gradient: the same split, each warp walking over tasks; the two weight
-// gradients stay in registers (32-bit sums of the rows a lane sees), are
-// added up over the CTA in a fixed order and written as one partial row a
-// CTA, which rope_weight_kernel adds up: no atomics, so results repeat.
+// The gradient.  A CTA keeps to one chunk of heads and walks over tokens, so
+// the weights and one weight gradient stay in registers: 32-bit sums of the
+// rows a lane sees, added up over the CTA in a fixed order and written as one
+// partial row a CTA, which rope_weight_kernel adds up.  No atomics: results
+// repeat bit for bit.
 template <int D, bool INTER, int U>
-__global__ void __launch_bounds__(kRopeThreads) rope_bwd_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(32 * kBwdWarps, kBwdPerSm) rope_bwd_kernel(const RopeParams p) {
   constexpr int L = D / 8;
   constexpr int R = 32 / L;
-  __shared__ float red[kRopeWarps][2][D];
+  __shared__ float red[kBwdWarps][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c0 = (lane % L) * 8;
-  const int partner = rotation_partner(p, lane, c0, INTER);
-  float wq[8], wk[8], aq[8], ak[8];
-  load_weights<D>(p.wq, p.w_f32, c0, wq);
-  load_weights<D>(p.wk, p.w_f32, c0, wk);
+  const int chunk = blockIdx.x / p.groups, group = blockIdx.x - chunk * p.groups;
+  const Chunk c = chunk_of(p, chunk, U * R);
+  const int c0 = (lane % L) * 8, h0 = c.first + lane / L;
+  const int heads = c.kind == 0 ? p.H : p.Hkv;
+  const float* up = static_cast<const float*>(c.kind == 0 ? p.q : c.kind == 1 ? p.k : p.v);
+  const int64_t next = (int64_t)R * p.S * D;
+  const int off = INTER ? 0 : partner_offset(p, c0);
+  const int partner = lane + off / 8;
+  const bool norm = p.wq != nullptr && c.kind != 2, turned = p.half != 0 && c.kind != 2;
+  const bool turns = c0 < 2 * p.half;
+  F2 w[4], acc[4];
+  {
+    float f[8];
+    load_weights(c.kind == 0 ? p.wq : c.kind == 1 ? p.wk : nullptr, p.w_f32, c0, f);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) aq[i] = ak[i] = 0.0f;
-
-  for (unsigned task = blockIdx.x * kRopeWarps + warp; task < (unsigned)p.tasks;
-       task += gridDim.x * kRopeWarps) {
-    const int token = task / (unsigned)p.chunks;
-    const int h0 = (int)(task - (unsigned)token * p.chunks) * (U * R) + lane / L;
-    const int b = token / p.S, s = token - b * p.S;
-    const uint16_t* xr = p.x + b * p.xb + s * p.xs + c0;
+    for (int i = 0; i < 4; ++i) w[i] = f2(f[2 * i], f[2 * i + 1]), acc[i] = f2(0.0f);
+  }
+  for (unsigned token = group * kBwdWarps + warp; token < (unsigned)p.tokens;
+       token += p.groups * kBwdWarps) {
+    const int b = token / (unsigned)p.S, s = token - b * p.S;
+    const int64_t row = (c.row + lane / L) * D + c0;
+    const uint16_t* xr = p.x + b * p.xb + s * p.xs + row;
+    const float* d = up + (((int64_t)b * heads + h0) * p.S + s) * D + c0;
     uint4 raw[U];
     float4 dy[U][2];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int h = h0 + u * R;
       raw[u] = make_uint4(0, 0, 0, 0);
       dy[u][0] = dy[u][1] = make_float4(0, 0, 0, 0);
-      const float* d = nullptr;
-      if (h < p.H)
-        d = static_cast<const float*>(p.q) + (((int64_t)b * p.H + h) * p.S + s) * D;
-      else if (h < p.H + p.Hkv)
-        d = static_cast<const float*>(p.k) + (((int64_t)b * p.Hkv + h - p.H) * p.S + s) * D;
-      else if (h < p.heads)
-        d = static_cast<const float*>(p.v) +
-            (((int64_t)b * p.Hkv + h - p.H - p.Hkv) * p.S + s) * D;
-      if (d != nullptr) {
-        dy[u][0] = __ldg(reinterpret_cast<const float4*>(d + c0));
-        dy[u][1] = __ldg(reinterpret_cast<const float4*>(d + c0) + 1);
+      if (h0 + u * R < c.end) {
+        dy[u][0] = __ldg(reinterpret_cast<const float4*>(d + u * next));
+        dy[u][1] = __ldg(reinterpret_cast<const float4*>(d + u * next) + 1);
+        if (norm) raw[u] = __ldg(reinterpret_cast<const uint4*>(xr + u * R * D));
       }
-      if (h < p.H + p.Hkv && p.wq != nullptr)  // without a norm x is not needed
-        raw[u] = __ldg(reinterpret_cast<const uint4*>(xr + h * D));
     }
     float cs[8], sn[8];
-    load_angles<INTER>(p, token, s, c0, cs, sn);
+    if (turned) load_angles<INTER>(p, token, s, c0, cs, sn);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int h = h0 + u * R;
       const float4 d0 = dy[u][0], d1 = dy[u][1];
-      const float up[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
-      float g[8];
+      F2 g[4] = {f2(d0.x, d0.y), f2(d0.z, d0.w), f2(d1.x, d1.y), f2(d1.z, d1.w)};
+      if (turned) {
+        // turned back: the sine changes its sign
+        const float e[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
+        float o[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) g[i] = up[i];
-      rotate<INTER>(g, cs, sn, -1.0f, partner);
-      if (p.wq != nullptr) {
-        float x[8], ss = 0.0f, dot = 0.0f;
-        unpack8(raw[u], x);
+        for (int i = 0; i < 8; ++i)
+          o[i] = INTER ? e[i ^ 1] : __shfl_sync(0xFFFFFFFFu, e[i], partner);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          ss += x[i] * x[i];
-          dot += g[i] * (h < p.H ? wq[i] : wk[i]) * x[i];
-        }
-        const float r = rsqrtf(group_sum<L>(ss) * (1.0f / D) + p.eps);
-        const float m = group_sum<L>(dot) * (1.0f / D) * r * r;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float t = g[i] * x[i] * r;
-          if (h < p.H)
-            aq[i] += t;
-          else if (h < p.H + p.Hkv)
-            ak[i] += t;
-          g[i] = r * (g[i] * (h < p.H ? wq[i] : wk[i]) - x[i] * m);
+        for (int i = 0; i < 4; ++i) {
+          const F2 t = f2(o[2 * i] * -sn[2 * i], o[2 * i + 1] * -sn[2 * i + 1]);
+          if (turns) g[i] = fma2(g[i], f2(cs[2 * i], cs[2 * i + 1]), t);
         }
       }
-      if (h < p.heads) {
+      if (norm) {
+        const uint32_t v[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+        F2 x[4], t[4], ss = f2(0.0f), dot = f2(0.0f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) g[i] = h < p.H + p.Hkv ? g[i] : up[i];
-        *reinterpret_cast<uint4*>(p.dx + b * p.dxb + s * p.dxs + h * D + c0) = pack8(g);
+        for (int i = 0; i < 4; ++i) {
+          x[i] = bf16_pair(v[i]);
+          ss = fma2(x[i], x[i], ss);
+          t[i] = g[i] * x[i];
+          dot = fma2(t[i], w[i], dot);
+        }
+        const float2 a = split(ss), m = split(dot);
+        F2 sums = f2(a.x + a.y, m.x + m.y);
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1) {
+          const float2 t2 = split(sums);
+          sums = sums + f2(__shfl_xor_sync(0xFFFFFFFFu, t2.x, o),
+                           __shfl_xor_sync(0xFFFFFFFFu, t2.y, o));
+        }
+        const float2 total = split(sums);
+        const float r = rsqrtf(total.x * (1.0f / D) + p.eps);
+        const F2 r2 = f2(r), m2 = f2(-total.y * (1.0f / D) * r * r * r);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          acc[i] = fma2(t[i], r2, acc[i]);
+          g[i] = fma2(x[i], m2, g[i] * w[i] * r2);
+        }
       }
+      if (h0 + u * R < c.end)
+        *reinterpret_cast<uint4*>(p.dx + b * p.dxb + s * p.dxs + row + u * R * D) =
+            make_uint4(pack_bf16(g[0]), pack_bf16(g[1]), pack_bf16(g[2]), pack_bf16(g[3]));
     }
   }
-  if (p.partial == nullptr) return;
+  allow_next_launch();
+  if (!norm) return;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
+    const float2 a = split(acc[i]);
+    float t[2] = {a.x, a.y};
 #pragma unroll
-    for (int o = L; o < 32; o <<= 1) {
-      aq[i] += __shfl_xor_sync(0xFFFFFFFFu, aq[i], o);
-      ak[i] += __shfl_xor_sync(0xFFFFFFFFu, ak[i], o);
-    }
-    if (lane < L) {
-      red[warp][0][c0 + i] = aq[i];
-      red[warp][1][c0 + i] = ak[i];
+    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+      for (int o = L; o < 32; o <<= 1) t[e] += __shfl_xor_sync(0xFFFFFFFFu, t[e], o);
+      if (lane < L) red[warp][c0 + 2 * i + e] = t[e];
     }
   }
   __syncthreads();
-  allow_next_launch();
-  for (int c = threadIdx.x; c < 2 * D; c += kRopeThreads) {
+  for (int i = threadIdx.x; i < D; i += 32 * kBwdWarps) {
     float t = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kRopeWarps; ++w) t += red[w][c / D][c % D];
-    p.partial[(size_t)blockIdx.x * 2 * D + c] = t;
+    for (int k = 0; k < kBwdWarps; ++k) t += red[k][i];
+    p.partial[(size_t)blockIdx.x * D + i] = t;
   }
 }
 
-// Adds up the CTAs' partial weight gradients in a fixed order: 32 columns a
-// CTA, 32 rows at a time.  (The sums of a few hundred rows, in 64 bits.)
+// Adds up the CTAs' partial weight gradients in a fixed order: 32 channels of
+// one weight a CTA, 32 rows at a time.  (A few hundred rows, in 64 bits.)
 __global__ void __launch_bounds__(1024)
-    rope_weight_kernel(const float* __restrict__ partial, int rows, int D, float* __restrict__ dwq,
-                       float* __restrict__ dwk) {
+    rope_weight_kernel(const float* __restrict__ partial, int q_rows, int k_rows, int D,
+                       float* __restrict__ dwq, float* __restrict__ dwk) {
   __shared__ double sh[32][33];
   wait_for_previous_launch();
   const int col = blockIdx.x * 32 + threadIdx.x;
+  const bool is_q = blockIdx.y == 0;
+  const float* from = partial + (is_q ? 0 : (size_t)q_rows * D) + col;
+  const int rows = is_q ? q_rows : k_rows;
   double t = 0.0;
-  for (int r = threadIdx.y; r < rows; r += 32) t += partial[(size_t)r * 2 * D + col];
+  for (int r = threadIdx.y; r < rows; r += 32) t += __ldcg(from + (size_t)r * D);
   sh[threadIdx.y][threadIdx.x] = t;
   __syncthreads();
   if (threadIdx.y == 0) {
     double s = 0.0;
     for (int r = 0; r < 32; ++r) s += sh[r][threadIdx.x];
-    if (col < D)
-      dwq[col] = (float)s;
-    else
-      dwk[col - D] = (float)s;
+    (is_q ? dwq : dwk)[col] = (float)s;
   }
 }
 
@@ -322,10 +369,31 @@ __global__ void rope_table_kernel(const double* __restrict__ inv_freq, int n_pos
 
 bool multiple8(int64_t v) { return v % 8 == 0; }
 
-// CTAs of the backward kernel, and rows of its workspace
-int bwd_ctas(int tasks, int sms) {
-  const int all = tasks / kRopeWarps + (tasks % kRopeWarps != 0);
-  return all < 4 * sms ? all : 4 * sms;
+// Rows a lane holds at once: as many as the larger kind of heads fills, at most
+// `most` (4; 2 in the backward pass, whose rows take three times the registers).
+int rows_per_lane(int H, int D, int most) {
+  const int at_once = 256 / D;
+  int u = 1;
+  while (u < most && u * at_once < H) u *= 2;
+  return u;
+}
+
+// The backward pass's split: CTAs a chunk, so that kBwdPerSm CTAs run on each SM
+// and none is without tokens.
+struct BwdSplit {
+  int u, q_chunks, k_chunks, groups;
+};
+BwdSplit bwd_split(int tokens, int H, int Hkv, int D, int sms) {
+  BwdSplit s;
+  s.u = rows_per_lane(H, D, 2);
+  const int rows = s.u * 256 / D;
+  s.q_chunks = (H + rows - 1) / rows;
+  s.k_chunks = (Hkv + rows - 1) / rows;
+  const int chunks = s.q_chunks + 2 * s.k_chunks;
+  const int most = tokens / kBwdWarps + (tokens % kBwdWarps != 0);
+  s.groups = (kBwdPerSm * sms + chunks - 1) / chunks;
+  if (s.groups > most) s.groups = most;
+  return s;
 }
 
 // The argument checks that both directions share.
@@ -353,19 +421,17 @@ bsattn_status check_rope(const void* x, int64_t xb, int64_t xs, int B, int S, in
   return BSATTN_OK;
 }
 
-RopeParams rope_params(const void* x, int64_t xb, int64_t xs, int B, int S, int H, int Hkv, int D,
+RopeParams rope_params(const void* x, int64_t xb, int64_t xs, int B, int S, int H, int Hkv,
                        const void* wq, const void* wk, unsigned flags, const float* table,
-                       int n_pos, int rotary_dim, const int32_t* pos, float eps, int rows) {
+                       int n_pos, int rotary_dim, const int32_t* pos, float eps) {
   RopeParams p{};
   p.x = static_cast<const uint16_t*>(x);
   p.xb = xb;
   p.xs = xs;
+  p.tokens = B * S;
   p.S = S;
   p.H = H;
   p.Hkv = Hkv;
-  p.heads = H + 2 * Hkv;
-  p.chunks = (p.heads + rows - 1) / rows;
-  p.tasks = B * S * p.chunks;  // at most B * S * heads
   p.wq = wq;
   p.wk = wk;
   p.w_f32 = (flags & BSATTN_WEIGHT_F32) ? 1 : 0;
@@ -377,18 +443,14 @@ RopeParams rope_params(const void* x, int64_t xb, int64_t xs, int B, int S, int 
   return p;
 }
 
-// Rows a lane holds at once: as many as the heads fill, at most 4 (2 in the
-// backward pass, whose rows take three times the registers).
-int rows_per_lane(int heads, int D, int most) {
-  const int at_once = 256 / D;
-  int u = 1;
-  while (u < most && u * at_once < heads) u *= 2;
-  return u;
-}
-
 template <int D, bool INTER>
-void launch_rope_fwd(const RopeParams& p, int u, cudaStream_t st) {
-  const int grid = p.tasks / kRopeWarps + (p.tasks % kRopeWarps != 0);
+void launch_rope_fwd(RopeParams& p, cudaStream_t st) {
+  const int u = rows_per_lane(p.H, D, 4), rows = u * 256 / D;
+  p.q_chunks = (p.H + rows - 1) / rows;
+  p.k_chunks = (p.Hkv + rows - 1) / rows;
+  // at most B * S * heads CTAs: below 2^31
+  const int blocks = p.tokens / kRopeWarps + (p.tokens % kRopeWarps != 0);
+  const int grid = blocks * (p.q_chunks + 2 * p.k_chunks);
   if (u == 1)
     rope_fwd_kernel<D, INTER, 1><<<grid, kRopeThreads, 0, st>>>(p);
   else if (u == 2)
@@ -398,11 +460,12 @@ void launch_rope_fwd(const RopeParams& p, int u, cudaStream_t st) {
 }
 
 template <int D, bool INTER>
-void launch_rope_bwd(const RopeParams& p, int u, int grid, cudaStream_t st) {
+void launch_rope_bwd(const RopeParams& p, int u, cudaStream_t st) {
+  const int grid = (p.q_chunks + 2 * p.k_chunks) * p.groups;
   if (u == 1)
-    rope_bwd_kernel<D, INTER, 1><<<grid, kRopeThreads, 0, st>>>(p);
+    rope_bwd_kernel<D, INTER, 1><<<grid, 32 * kBwdWarps, 0, st>>>(p);
   else
-    rope_bwd_kernel<D, INTER, 2><<<grid, kRopeThreads, 0, st>>>(p);
+    rope_bwd_kernel<D, INTER, 2><<<grid, 32 * kBwdWarps, 0, st>>>(p);
 }
 
 }  // namespace
@@ -435,18 +498,17 @@ bsattn_status bsattn_qk_norm_rope(const void* x, int64_t x_batch_stride, int64_t
   if (rc != BSATTN_OK) return rc;
   if (!q || !k || !v || !aligned16(q) || !aligned16(k) || !aligned16(v))
     return BSATTN_ERR_INVALID_ARG;
-  const int u = rows_per_lane(H + 2 * Hkv, D, 4);
-  RopeParams p = rope_params(x, x_batch_stride, x_token_stride, B, S, H, Hkv, D, q_weight, k_weight,
-                             flags, table, n_pos, rotary_dim, positions, eps, u * 256 / D);
+  RopeParams p = rope_params(x, x_batch_stride, x_token_stride, B, S, H, Hkv, q_weight, k_weight,
+                             flags, table, n_pos, rotary_dim, positions, eps);
   p.q = q;
   p.k = k;
   p.v = v;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool inter = (flags & BSATTN_ROPE_INTERLEAVED) != 0;
   if (D == 64)
-    inter ? launch_rope_fwd<64, true>(p, u, st) : launch_rope_fwd<64, false>(p, u, st);
+    inter ? launch_rope_fwd<64, true>(p, st) : launch_rope_fwd<64, false>(p, st);
   else
-    inter ? launch_rope_fwd<128, true>(p, u, st) : launch_rope_fwd<128, false>(p, u, st);
+    inter ? launch_rope_fwd<128, true>(p, st) : launch_rope_fwd<128, false>(p, st);
   return from_cuda(cudaGetLastError());
 }
 
@@ -454,7 +516,9 @@ size_t bsattn_qk_norm_rope_bwd_workspace(int B, int S, int H, int Hkv, int D) {
   if (B <= 0 || S <= 0 || H <= 0 || Hkv <= 0 || (D != 64 && D != 128)) return 0;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  return (size_t)4 * device_sm_count(dev) * 2 * D * sizeof(float);
+  if ((int64_t)B * S >= (1ll << 31)) return 0;
+  const BwdSplit s = bwd_split(B * S, H, Hkv, D, device_sm_count(dev));
+  return (size_t)(s.q_chunks + s.k_chunks) * s.groups * D * sizeof(float);
 }
 
 bsattn_status bsattn_qk_norm_rope_bwd(const void* x, int64_t x_batch_stride, int64_t x_token_stride,
@@ -477,13 +541,15 @@ bsattn_status bsattn_qk_norm_rope_bwd(const void* x, int64_t x_batch_stride, int
     return BSATTN_ERR_INVALID_ARG;
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) return BSATTN_ERR_CUDA;
-  const int u = rows_per_lane(H + 2 * Hkv, D, 2);
-  RopeParams p = rope_params(x, x_batch_stride, x_token_stride, B, S, H, Hkv, D, q_weight, k_weight,
-                             flags, table, n_pos, rotary_dim, positions, eps, u * 256 / D);
-  const int grid = bwd_ctas(p.tasks, device_sm_count(dev));
+  const BwdSplit split = bwd_split(B * S, H, Hkv, D, device_sm_count(dev));
+  RopeParams p = rope_params(x, x_batch_stride, x_token_stride, B, S, H, Hkv, q_weight, k_weight,
+                             flags, table, n_pos, rotary_dim, positions, eps);
+  p.q_chunks = split.q_chunks;
+  p.k_chunks = split.k_chunks;
+  p.groups = split.groups;
   if (q_weight) {
     if (!dq_weight || !dk_weight || !workspace || !aligned16(workspace) ||
-        workspace_bytes < (size_t)grid * 2 * D * sizeof(float))
+        workspace_bytes < bsattn_qk_norm_rope_bwd_workspace(B, S, H, Hkv, D))
       return BSATTN_ERR_INVALID_ARG;
     p.partial = static_cast<float*>(workspace);
   }
@@ -497,13 +563,15 @@ bsattn_status bsattn_qk_norm_rope_bwd(const void* x, int64_t x_batch_stride, int
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool inter = (flags & BSATTN_ROPE_INTERLEAVED) != 0;
   if (D == 64)
-    inter ? launch_rope_bwd<64, true>(p, u, grid, st) : launch_rope_bwd<64, false>(p, u, grid, st);
+    inter ? launch_rope_bwd<64, true>(p, split.u, st) : launch_rope_bwd<64, false>(p, split.u, st);
   else
-    inter ? launch_rope_bwd<128, true>(p, u, grid, st) : launch_rope_bwd<128, false>(p, u, grid, st);
+    inter ? launch_rope_bwd<128, true>(p, split.u, st)
+          : launch_rope_bwd<128, false>(p, split.u, st);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !q_weight) return from_cuda(e);
-  e = launch_dependent(rope_weight_kernel, dim3(2 * D / 32), dim3(32, 32), 0, st,
-                       (const float*)p.partial, grid, D, dq_weight, dk_weight);
+  e = launch_dependent(rope_weight_kernel, dim3(D / 32, 2), dim3(32, 32), 0, st,
+                       (const float*)p.partial, split.q_chunks * split.groups,
+                       split.k_chunks * split.groups, D, dq_weight, dk_weight);
   return from_cuda(e);
 }
 

@@ -47,9 +47,9 @@ __global__ void __launch_bounds__(kPoolThreads)
   const int rows = is_q ? kBlock : key_block;
   const uint16_t* src = (is_q ? q : k) + blk * rows * D + (lane % L) * 8;
 
-  Sum2 s[8];
+  Sum2x2 s[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) s[i] = Sum2{0.0f, 0.0f};
+  for (int i = 0; i < 4; ++i) s[i].hi = s[i].lo = f2(0.0f);
   constexpr int U = 4;
   for (int r0 = warp * R + lane / L; r0 < rows; r0 += U * kPoolWarps * R) {
     uint4 raw[U];
@@ -58,10 +58,10 @@ __global__ void __launch_bounds__(kPoolThreads)
       raw[u] = __ldg(reinterpret_cast<const uint4*>(src + (r0 + u * kPoolWarps * R) * D));
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      float x[8];
-      unpack8(raw[u], x);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) add_exact(s[i], x[i]);
+      add_exact(s[0], bf16_pair(raw[u].x));
+      add_exact(s[1], bf16_pair(raw[u].y));
+      add_exact(s[2], bf16_pair(raw[u].z));
+      add_exact(s[3], bf16_pair(raw[u].w));
     }
   }
   allow_next_launch();

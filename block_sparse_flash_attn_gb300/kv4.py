@@ -11,6 +11,7 @@
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 
 import torch
@@ -70,6 +71,11 @@ class Kv4Cache:
         self._ref = ctypes.byref(self._struct)
 
 
+@functools.lru_cache(maxsize=256)
+def _attn_workspace(device, *sizes):  # a function of the sizes and the (current) device
+    return _bs.load().bsattn_kv4_attn_workspace(*sizes)
+
+
 def _cache(cache) -> Kv4Cache:
     if not isinstance(cache, Kv4Cache):
         raise TypeError("cache must be a Kv4Cache")
@@ -119,11 +125,11 @@ def kv4_append(cache: Kv4Cache, k: torch.Tensor, v: torch.Tensor, block_table: t
     T = k.shape[2]
     if B * T == 0:
         return
-    with launch_on(cache.device, stream):
+    with launch_on(cache.device, stream) as on:
         _bs._check(_bs.load().bsattn_kv4_append(
             cache._ref, k.data_ptr(), *k.stride()[:3], v.data_ptr(), *v.stride()[:3], B, T,
             block_table.data_ptr(), stride, columns, lengths.data_ptr(), pointer(counts),
-            _bs._stream_handle(None)), "bsattn_kv4_append")
+            on), "bsattn_kv4_append")
 
 
 def kv4_read(cache: Kv4Cache, block_table: torch.Tensor, start: torch.Tensor, tokens: int,
@@ -136,7 +142,7 @@ def kv4_read(cache: Kv4Cache, block_table: torch.Tensor, start: torch.Tensor, to
     if tokens < 0:
         raise ValueError("tokens must not be negative")
     shape = (B, cache.kv_heads, tokens, cache.head_dim)
-    with launch_on(cache.device, stream):
+    with launch_on(cache.device, stream) as on:
         outs = []
         for name, t in (("k", k), ("v", v)):
             if t is None:
@@ -147,7 +153,7 @@ def kv4_read(cache: Kv4Cache, block_table: torch.Tensor, start: torch.Tensor, to
         if B * tokens:
             _bs._check(_bs.load().bsattn_kv4_read(
                 cache._ref, B, tokens, block_table.data_ptr(), stride, columns, start.data_ptr(),
-                pointer(counts), outs[0].data_ptr(), outs[1].data_ptr(), _bs._stream_handle(None)),
+                pointer(counts), outs[0].data_ptr(), outs[1].data_ptr(), on),
                 "bsattn_kv4_read")
     return outs[0], outs[1]
 
@@ -164,19 +170,19 @@ def kv4_select(cache: Kv4Cache, q: torch.Tensor, block_table: torch.Tensor, leng
     H, T = _queries(cache, q, B)
     if sink < 0 or recent < 1 or keep < sink + recent:
         raise ValueError("sink must not be negative, recent at least 1, keep at least sink + recent")
-    with launch_on(cache.device, stream):
+    with launch_on(cache.device, stream) as on:
         if out is None:
             out = torch.empty((B, cache.kv_heads, keep), dtype=_I32, device=cache.device)
         else:
             tensor("out", out, (_I32,), (B, cache.kv_heads, keep), cache.device)
         if B:
             lib = _bs.load()
-            nbytes = lib.bsattn_kv4_select_workspace(B, cache.kv_heads, columns)
+            nbytes = 4 * B * cache.kv_heads * columns  # bsattn_kv4_select_workspace
             ws = torch.empty(nbytes, dtype=torch.uint8, device=cache.device)
             _bs._check(lib.bsattn_kv4_select(
                 cache._ref, q.data_ptr(), B, H, T, block_table.data_ptr(), stride, columns,
                 lengths.data_ptr(), keep, sink, recent, out.data_ptr(), ws.data_ptr(), nbytes,
-                _bs._stream_handle(None)), "bsattn_kv4_select")
+                on), "bsattn_kv4_select")
     return out
 
 
@@ -203,7 +209,7 @@ def kv4_attn(cache: Kv4Cache, q: torch.Tensor, block_table: torch.Tensor, length
     if scale is None:
         scale = 1.0 / math.sqrt(cache.head_dim)
     odt = torch.float32 if out_f32 else _BF16
-    with launch_on(cache.device, stream):
+    with launch_on(cache.device, stream) as on:
         if out is None:
             out = torch.empty(q.shape, dtype=odt, device=cache.device)
         else:
@@ -214,19 +220,19 @@ def kv4_attn(cache: Kv4Cache, q: torch.Tensor, block_table: torch.Tensor, length
             tensor("lse", lse, (torch.float32,), q.shape[:3], cache.device)
         if B:
             lib = _bs.load()
-            nbytes = lib.bsattn_kv4_attn_workspace(B, H, cache.kv_heads, T, cache.head_dim)
+            nbytes = _attn_workspace(cache.device.index, B, H, cache.kv_heads, T, cache.head_dim)
             ws = torch.empty(nbytes, dtype=torch.uint8, device=cache.device)
             _bs._check(lib.bsattn_kv4_attn(
                 cache._ref, q.data_ptr(), B, H, T, block_table.data_ptr(), stride, columns,
                 lengths.data_ptr(), pointer(selected), n_selected, float(scale),
                 _bs.OUT_F32 if out_f32 else 0, out.data_ptr(), lse.data_ptr(), ws.data_ptr(),
-                nbytes, _bs._stream_handle(None)), "bsattn_kv4_attn")
+                nbytes, on), "bsattn_kv4_attn")
     return out, lse
 
 
 def kv4_status(cache: Kv4Cache, stream=None) -> None:
     """Wait for the stream; raise if a call met a bad page or page list since the last check."""
     _cache(cache)
-    with launch_on(cache.device, stream):
-        _bs._check(_bs.load().bsattn_kv4_status(cache._ref, _bs._stream_handle(None)),
+    with launch_on(cache.device, stream) as on:
+        _bs._check(_bs.load().bsattn_kv4_status(cache._ref, on),
                    "kv4 status")

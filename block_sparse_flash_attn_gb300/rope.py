@@ -9,6 +9,8 @@ head-major layout of the forward pass in one kernel, and its gradient.
 """
 from __future__ import annotations
 
+import functools
+
 import torch
 
 import block_sparse_flash_attn_gb300 as _bs
@@ -37,13 +39,18 @@ def rope_table(positions: int, rotary_dim: int, theta: float = 10000.0,
         raise ValueError("inv_freq must be a tensor of rotary_dim / 2 frequencies")
     if device.index is None:
         device = torch.device("cuda", torch.cuda.current_device())
-    with launch_on(device, stream):
+    with launch_on(device, stream) as on:
         inv = inv_freq.to(device=device, dtype=torch.float64).contiguous()
         table = torch.empty((positions, rotary_dim // 2, 2), dtype=_F32, device=device)
         _bs._check(_bs.load().bsattn_rope_table(inv.data_ptr(), positions, rotary_dim,
-                                                table.data_ptr(), _bs._stream_handle(None)),
+                                                table.data_ptr(), on),
                    "bsattn_rope_table")
     return table
+
+
+@functools.lru_cache(maxsize=256)
+def _workspace(device, *sizes):  # a function of the sizes and the (current) device
+    return _bs.load().bsattn_qk_norm_rope_bwd_workspace(*sizes)
 
 
 def _common(x, heads, kv_heads, q_weight, k_weight, table, positions, interleaved):
@@ -102,7 +109,7 @@ def qk_norm_rope(x: torch.Tensor, heads: int, kv_heads: int, q_weight: torch.Ten
     multiple of 128 here."""
     B, S, D, n_pos, rotary, flags = _common(x, heads, kv_heads, q_weight, k_weight, table,
                                             positions, interleaved)
-    with launch_on(x.device, stream):
+    with launch_on(x.device, stream) as on:
         outs = []
         for name, t, h in (("q", q, heads), ("k", k, kv_heads), ("v", v, kv_heads)):
             if t is None:
@@ -116,7 +123,7 @@ def qk_norm_rope(x: torch.Tensor, heads: int, kv_heads: int, q_weight: torch.Ten
                 x.data_ptr(), x.stride(0), x.stride(1), B, S, heads, kv_heads, D,
                 pointer(q_weight), pointer(k_weight), pointer(table), n_pos, rotary,
                 pointer(positions), float(eps), flags, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                _bs._stream_handle(None)), "bsattn_qk_norm_rope")
+                on), "bsattn_qk_norm_rope")
     return q, k, v
 
 
@@ -129,8 +136,9 @@ def qk_norm_rope_bwd(x: torch.Tensor, dq: torch.Tensor, dk: torch.Tensor, dv: to
     the gradient of qk_norm_rope, from dq [B, H, S, D], dk, dv [B, Hkv, S, D]
     (CUDA fp32, as bwd returns them) and the forward call's other arguments.
     Repeated calls give the same bits."""
-    for name, t in (("dq", dq), ("dk", dk), ("dv", dv)):
-        tensor(name, t, (_F32,))
+    for name, t in (("dq", dq), ("dk", dk)):
+        if not isinstance(t, torch.Tensor) or t.dtype != _F32:
+            raise TypeError(f"{name} must be a tensor of {_F32}")
         if t.dim() != 4:
             raise ValueError(f"{name} must be [B, H, S, D]")
     heads, kv_heads = dq.shape[1], dk.shape[1]
@@ -138,7 +146,7 @@ def qk_norm_rope_bwd(x: torch.Tensor, dq: torch.Tensor, dk: torch.Tensor, dv: to
                                             positions, interleaved)
     for name, t, h in (("dq", dq, heads), ("dk", dk, kv_heads), ("dv", dv, kv_heads)):
         tensor(name, t, (_F32,), (B, h, S, D), x.device)
-    with launch_on(x.device, stream):
+    with launch_on(x.device, stream) as on:
         if dx is None:
             dx = torch.empty(x.shape, dtype=_BF16, device=x.device)
         else:
@@ -146,18 +154,19 @@ def qk_norm_rope_bwd(x: torch.Tensor, dq: torch.Tensor, dk: torch.Tensor, dv: to
         dwq = dwk = ws = None
         lib = _bs.load()
         if q_weight is not None:
-            dwq, dwk = torch.empty((2, D), dtype=_F32, device=x.device).unbind(0)
+            dwq = torch.empty(D, dtype=_F32, device=x.device)
+            dwk = torch.empty(D, dtype=_F32, device=x.device)
             if B * S == 0:
                 dwq.zero_(), dwk.zero_()
         if B * S:
             nbytes = 0
             if q_weight is not None:
-                nbytes = lib.bsattn_qk_norm_rope_bwd_workspace(B, S, heads, kv_heads, D)
+                nbytes = _workspace(x.device.index, B, S, heads, kv_heads, D)
                 ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
             _bs._check(lib.bsattn_qk_norm_rope_bwd(
                 x.data_ptr(), x.stride(0), x.stride(1), dq.data_ptr(), dk.data_ptr(),
                 dv.data_ptr(), B, S, heads, kv_heads, D, pointer(q_weight), pointer(k_weight),
                 pointer(table), n_pos, rotary, pointer(positions), float(eps), flags,
                 dx.data_ptr(), dx.stride(0), dx.stride(1), pointer(dwq), pointer(dwk),
-                pointer(ws), nbytes, _bs._stream_handle(None)), "bsattn_qk_norm_rope_bwd")
+                pointer(ws), nbytes, on), "bsattn_qk_norm_rope_bwd")
     return dx, dwq, dwk

@@ -124,7 +124,7 @@ def test_caches(bs, change, status):
     ("append", APPEND, dict(lengths=None), 1), ("append", APPEND, dict(counts=vp(0x10001)), 1),
     ("append", APPEND, dict(B=65536), 2), ("append", APPEND, dict(stride=-4), 1),
     ("read", READ, dict(k=None), 1), ("read", READ, dict(v=ODD), 1), ("read", READ, dict(start=None), 1),
-    ("read", READ, dict(T=0), 1), ("read", READ, dict(B=1 << 15, T=1 << 15), 2),
+    ("read", READ, dict(T=0), 1), ("read", READ, dict(B=1 << 16), 2), ("read", READ, dict(T=(1 << 30) + 1), 2),
     ("select", PAGES, dict(q=ODD), 1), ("select", PAGES, dict(H=3), 1), ("select", PAGES, dict(T=65), 2),
     ("select", PAGES, dict(keep=1), 1), ("select", PAGES, dict(recent=0), 1), ("select", PAGES, dict(sink=-1), 1),
     ("select", PAGES, dict(nbytes=8), 1), ("select", PAGES, dict(out=None), 1),

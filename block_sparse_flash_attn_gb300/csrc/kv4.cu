@@ -19,7 +19,6 @@ namespace bsattn {
 namespace {
 
 constexpr int kRowThreads = 128;  // write_rounded_mean takes a CTA of 128
-constexpr int kRowWarps = kRowThreads / 32;
 constexpr int kReadRows = 4;      // rows a lane group reads back at once
 constexpr float kLeastStep = 7.888609e-31f;  // 2^-100
 
@@ -48,20 +47,25 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
   return *reinterpret_cast<uint32_t*>(&r);
 }
 
-// Eight channels of one group's row -> codes (a nibble each, the first
+// Sixteen channels of one group's row -> codes (a nibble each, the first
 // lowest; n[i]: channels 2i, 2i + 1 as floats), and the group's step and least.
 // GL lanes hold a group.
 //
-// (x - least) / step is first estimated with the reciprocal and rounded by
-// adding 1.5 2^23 (no conversion instruction), then settled by its exact
-// remainder: r = d - n step is exact in 32 bits (|r| <= step), and |r| against
-// step / 2 says whether n is the nearest (at the half itself: whether n is
-// even), so codes do not depend on how a division rounds.
+// d / step, d = x - least, is estimated with the reciprocal and corrected by its
+// exact remainder: q = q0 + (d - q0 step) / step, good to 2^-46 before its one
+// rounding; adding 1.5 2^23 then rounds it half to even with no conversion
+// instruction.  The codes are those of the real quotient: at a border it is
+// k + 1/2 exactly, which 32 bits hold, and next to one d differs from
+// (k + 1/2) step, a number of 13 bits, by a step of d at least, so the quotient
+// by more than its own rounding.  The step's (most - least) / 15 is taken the
+// same way, and is the 32-bit quotient: no a / 15 comes closer to the middle
+// between two floats than 2^-29 of itself.
 template <int GL>
-__device__ __forceinline__ uint32_t quantise(const uint4& raw, F2 (&n)[4], float& step,
-                                             float& least) {
-  uint32_t lo = min2(min2(raw.x, raw.y), min2(raw.z, raw.w));
-  uint32_t hi = max2(max2(raw.x, raw.y), max2(raw.z, raw.w));
+__device__ __forceinline__ uint2 quantise(const uint32_t (&w)[8], F2 (&n)[8], float& step,
+                                          float& least) {
+  uint32_t lo = w[0], hi = w[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) lo = min2(lo, w[i]), hi = max2(hi, w[i]);
   lo = min2(lo, __byte_perm(lo, lo, 0x1032));
   hi = max2(hi, __byte_perm(hi, hi, 0x1032));
   // (least, -most) in one word: one shuffle a level
@@ -70,127 +74,146 @@ __device__ __forceinline__ uint32_t quantise(const uint4& raw, F2 (&n)[4], float
   for (int o = 1; o < GL; o <<= 1) both = min2(both, __shfl_xor_sync(0xFFFFFFFFu, both, o));
   least = bf16_lo(both);
   const float range = -bf16_hi(both) - least;  // NaN or infinite for a group that is not finite
-  step = __bfloat162float(__float2bfloat16_rn(__fdiv_rn(range, 15.0f)));
+  constexpr float kFifteenth = 1.0f / 15.0f;
+  const float r0 = range * kFifteenth;
+  step = __bfloat162float(__float2bfloat16_rn(fmaf(fmaf(-15.0f, r0, range), kFifteenth, r0)));
   const bool finite = range <= 3.4028234e38f, flat = step < kLeastStep;
   float inv;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(step));
-  const uint32_t half = __float_as_uint(0.5f * step);
   const F2 vinv = f2(inv), vstep = f2(-step), vleast = f2(-least);
   const F2 magic = f2(12582912.0f), unmagic = f2(-12582912.0f);
-  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const F2 d = bf16_pair(w[i]) + vleast;
+    const F2 q0 = d * vinv;
+    n[i] = fma2(fma2(q0, vstep, d), vinv, q0) + magic + unmagic;
+  }
+  if (!finite || flat) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) n[i] = f2(0.0f);
+    step = finite ? 0.0f : __int_as_float(0x7FC00000);
+    least = finite ? least : step;
+  }
+  // four codes a sum, exactly: (n0, n1) + 256 (n2, n3), then n0 + 16 n1
+  uint32_t half[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const F2 d = bf16_pair(w[i]) + vleast;
-    const F2 t = fma2(d, vinv, magic);
-    const F2 nf = t + unmagic;
-    const float2 r = split(fma2(nf, vstep, d)), tt = split(t);
-    float2 k = split(nf);
-    // too far: above half a step, or at it with n odd
-    if (fabsf(r.x) > __uint_as_float(half - (__float_as_uint(tt.x) & 1u))) k.x += copysignf(1.0f, r.x);
-    if (fabsf(r.y) > __uint_as_float(half - (__float_as_uint(tt.y) & 1u))) k.y += copysignf(1.0f, r.y);
-    n[i] = f2(k.x, k.y);
+    const float2 s = split(fma2(n[2 * i + 1], f2(256.0f), n[2 * i]));
+    half[i] = __float_as_uint(fmaf(s.y, 16.0f, s.x) + 8388608.0f);
   }
-  // four codes a sum: n0 + 16 n1 + 256 n2 + 4096 n3 (exact), both halves at once
-  const float2 a = split(n[0]), b = split(n[1]), c = split(n[2]), e = split(n[3]);
-  F2 sum = fma2(f2(b.y, e.y), f2(4096.0f), f2(8388608.0f));
-  sum = fma2(f2(b.x, e.x), f2(256.0f), sum);
-  sum = fma2(f2(a.y, c.y), f2(16.0f), sum);
-  sum = sum + f2(a.x, c.x);
-  const float2 s = split(sum);
-  uint32_t codes = __byte_perm(__float_as_uint(s.x), __float_as_uint(s.y), 0x5410);
-  if (!finite) step = least = __int_as_float(0x7FC00000);
-  if (flat) step = 0.0f;
-  if (!finite || flat) {
-    codes = 0u;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) n[i] = f2(0.0f);
-  }
-  return codes;
+  return make_uint2(__byte_perm(half[0], half[1], 0x5410), __byte_perm(half[2], half[3], 0x5410));
 }
 
 // The values of eight codes.  Code i is read as (2^23 + code 16^i) - 2^23 in
 // place (codes 5 to 7 after one shift) and multiplied by step 16^-i: the same
 // product, exactly, as step * code.
-__device__ __forceinline__ void decode8(uint32_t codes, float step, float least, F2 (&x)[4]) {
-  const uint32_t up = codes >> 20;
-  const F2 off = f2(-8388608.0f), l = f2(least);
-  auto field = [](uint32_t v, int bit) {
-    return __uint_as_float((v & (15u << bit)) | 0x4B000000u);
-  };
-  const float s1 = step * 0.0625f, s2 = step * 0.00390625f;
-  const float s3 = step * 2.44140625e-4f, s4 = step * 1.52587890625e-5f;
-  x[0] = fma2(f2(field(codes, 0), field(codes, 4)) + off, f2(step, s1), l);
-  x[1] = fma2(f2(field(codes, 8), field(codes, 12)) + off, f2(s2, s3), l);
-  x[2] = fma2(f2(field(codes, 16), field(up, 0)) + off, f2(s4, step), l);
-  x[3] = fma2(f2(field(up, 4), field(up, 8)) + off, f2(s1, s2), l);
-}
+struct Decoder {
+  F2 s01, s23, s4, s12, least;
+
+  __device__ __forceinline__ Decoder(float step, float l) {
+    const float s1 = step * 0.0625f, s2 = step * 0.00390625f;
+    s01 = f2(step, s1);
+    s23 = f2(s2, step * 2.44140625e-4f);
+    s4 = f2(step * 1.52587890625e-5f, step);
+    s12 = f2(s1, s2);
+    least = f2(l);
+  }
+  __device__ __forceinline__ void decode8(uint32_t codes, F2* x) const {
+    const uint32_t up = codes >> 20;
+    const F2 off = f2(-8388608.0f);
+    auto field = [](uint32_t v, int bit) {
+      return __uint_as_float((v & (15u << bit)) | 0x4B000000u);
+    };
+    x[0] = fma2(f2(field(codes, 0), field(codes, 4)) + off, s01, least);
+    x[1] = fma2(f2(field(codes, 8), field(codes, 12)) + off, s23, least);
+    x[2] = fma2(f2(field(codes, 16), field(up, 0)) + off, s4, least);
+    x[3] = fma2(f2(field(up, 4), field(up, 8)) + off, s12, least);
+  }
+};
 
 // One CTA: one page of one sequence and head, the tokens of this call that
-// fall into it.  Rows of K come first, then rows of V; a row is held by D / 8
-// lanes.  When the call fills the page the CTA adds up the page's decoded
-// keys (those of earlier calls are read back) and writes their rounded mean.
+// fall into it, K then V.  A row is held by D / 16 lanes, and the next row's
+// load is in flight while one is quantised.  When the call fills the page the
+// CTA adds up the page's decoded keys (those of earlier calls are read back)
+// and writes their rounded mean.
 template <int D, int GL>
 __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const AppendParams p) {
-  constexpr int L = D / 8, R = 32 / L, NG = L / GL;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int L = D / 16, NG = L / GL, kRows = kRowThreads / L;  // rows the CTA holds at once
   const int h = blockIdx.y, b = blockIdx.z;
-  const int len = p.lengths[b];
+  wait_for_previous_launch();
+  allow_next_launch();
+  const int len = __ldg(p.lengths + b);
   int cnt = p.T;
-  if (p.counts) cnt = min(max(p.counts[b], 0), p.T);
+  if (p.counts) cnt = min(max(__ldg(p.counts + b), 0), p.T);
   if (cnt == 0) return;
   if (len < 0) {
     if (threadIdx.x == 0) p.c.report();
     return;
   }
-  const int64_t page = p.c.page;
   const int64_t logical = (len >> p.c.log_page) + (int64_t)blockIdx.x;
-  const int64_t end = min((int64_t)len + cnt, (logical + 1) * page);
-  const int64_t begin = max((int64_t)len, logical * page);
+  const int64_t end = min((int64_t)len + cnt, (logical + 1) << p.c.log_page);
+  const int64_t begin = max((int64_t)len, logical << p.c.log_page);
   if (begin >= end) return;
   const int pg = page_at(p.c, p.table + b * p.table_stride, p.columns, logical);
   if (pg < 0) return;
-  const bool fills = end == (logical + 1) * page;
-  const int n = (int)(end - begin), place0 = (int)(begin - logical * page);
+  const bool fills = end == (logical + 1) << p.c.log_page;
+  const int n = (int)(end - begin), place0 = (int)(begin & (p.c.page - 1));
   const int t0 = (int)(begin - len);
-  const int sub = lane / L, cl = lane % L;
-  const uint16_t* k = p.k + b * p.kb + h * p.kh + cl * 8;
-  const uint16_t* v = p.v + b * p.vb + h * p.vh + cl * 8;
+  const int sub = threadIdx.x / L, cl = threadIdx.x % L;
   const int64_t row0 = p.c.row(pg, h, 0);
 
-  Sum2x2 s[4];
+  Sum2x2 s[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) s[i].hi = s[i].lo = f2(0.0f);
-  for (int i0 = warp * R; i0 < 2 * n; i0 += kRowWarps * R) {
-    const int i = i0 + sub;
-    const bool is_k = i < n;
-    const int r = is_k ? i : i - n;
-    uint4 raw = make_uint4(0, 0, 0, 0);
-    if (i < 2 * n)
-      raw = __ldg(reinterpret_cast<const uint4*>(is_k ? k + (t0 + r) * p.kt : v + (t0 + r) * p.vt));
-    F2 x[4];
-    float step, least;
-    const uint32_t codes = quantise<GL>(raw, x, step, least);
-    if (i < 2 * n) {
-      const int64_t row = row0 + place0 + r;
-      reinterpret_cast<uint32_t*>(is_k ? p.c.k_codes : p.c.v_codes)[row * L + cl] = codes;
-      if (cl % GL == 0)
-        reinterpret_cast<uint32_t*>(is_k ? p.c.k_scales : p.c.v_scales)[row * NG + cl / GL] =
-            pack_bf16(step, least);
-      if (is_k && fills) {
+  for (int i = 0; i < 8; ++i) s[i].hi = s[i].lo = f2(0.0f);
+  const int rounds = (n + kRows - 1) / kRows;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) add_exact(s[c], fma2(x[c], f2(step), f2(least)));
+  for (int kv = 0; kv < 2; ++kv) {
+    const int64_t stride = kv ? p.vt : p.kt;
+    const uint16_t* src = (kv ? p.v + b * p.vb + h * p.vh : p.k + b * p.kb + h * p.kh) +
+                          (t0 + sub) * stride + cl * 16;
+    const int64_t row = row0 + place0 + sub;
+    uint2* codes = reinterpret_cast<uint2*>(kv ? p.c.v_codes : p.c.k_codes) + row * L + cl;
+    uint32_t* scales =
+        reinterpret_cast<uint32_t*>(kv ? p.c.v_scales : p.c.k_scales) + row * NG + cl / GL;
+    uint4 a = make_uint4(0, 0, 0, 0), c = a;
+    if (sub < n) {
+      a = __ldg(reinterpret_cast<const uint4*>(src));
+      c = __ldg(reinterpret_cast<const uint4*>(src) + 1);
+    }
+    for (int i = 0; i < rounds; ++i) {  // (as many for every lane: shuffles)
+      const bool there = i * kRows + sub < n;
+      const uint32_t w[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+      src += kRows * stride;
+      if ((i + 1) * kRows + sub < n) {
+        a = __ldg(reinterpret_cast<const uint4*>(src));
+        c = __ldg(reinterpret_cast<const uint4*>(src) + 1);
       }
+      F2 x[8];
+      float step, least;
+      const uint2 packed = quantise<GL>(w, x, step, least);
+      if (there) {
+        *codes = packed;
+        if (cl % GL == 0) *scales = pack_bf16(step, least);
+        if (kv == 0 && fills) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) add_exact(s[k], fma2(x[k], f2(step), f2(least)));
+        }
+      }
+      codes += kRows * L;
+      scales += kRows * NG;
     }
   }
   if (!fills) return;
-  for (int r = warp * R + sub; r < place0; r += kRowWarps * R) {
+  for (int r = sub; r < place0; r += kRows) {
     const int64_t row = row0 + r;
-    const uint32_t codes = reinterpret_cast<const uint32_t*>(p.c.k_codes)[row * L + cl];
+    const uint2 codes = reinterpret_cast<const uint2*>(p.c.k_codes)[row * L + cl];
     const uint32_t sc = reinterpret_cast<const uint32_t*>(p.c.k_scales)[row * NG + cl / GL];
-    F2 x[4];
-    decode8(codes, bf16_lo(sc), bf16_hi(sc), x);
+    const Decoder dec(bf16_lo(sc), bf16_hi(sc));
+    F2 x[8];
+    dec.decode8(codes.x, x);
+    dec.decode8(codes.y, x + 4);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) add_exact(s[c], x[c]);
+    for (int k = 0; k < 8; ++k) add_exact(s[k], x[k]);
   }
   write_rounded_mean<D>(s, p.c.page, false, p.c.k_means + ((int64_t)pg * p.c.Hkv + h) * D);
 }
@@ -205,46 +228,54 @@ struct ReadParams {
   int T;
   uint16_t* k;
   uint16_t* v;
+  int wide;  // k and v are aligned to 32 bytes
 };
 
-// One CTA: consecutive rows of one sequence and head; a lane group (D / 8
+// One CTA: consecutive rows of one sequence and head; a lane group (D / 16
 // lanes) decodes kReadRows of them, K and V.  Rows behind the count are zero.
 template <int D, int GL>
 __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const ReadParams p) {
-  constexpr int L = D / 8, NG = L / GL;
+  constexpr int L = D / 16, NG = L / GL;
   constexpr int kGroups = kRowThreads / L;
   const int cl = threadIdx.x % L, group = threadIdx.x / L;
   const int h = blockIdx.y, b = blockIdx.z;
   const int t0 = blockIdx.x * (kGroups * kReadRows) + group;
-  const int count = p.counts ? __ldg(p.counts + b) : p.T;
+  wait_for_previous_launch();
+  allow_next_launch();
+  const int count = p.counts ? min(__ldg(p.counts + b), p.T) : p.T;
   const int64_t start = __ldg(p.start + b);
   const int* table = p.table + b * p.table_stride;
-  uint32_t code[kReadRows][2], sc[kReadRows][2];
+  uint2 code[kReadRows][2];
+  uint32_t sc[kReadRows][2];
 #pragma unroll
   for (int u = 0; u < kReadRows; ++u) {
     const int t = t0 + u * kGroups;
-    code[u][0] = code[u][1] = sc[u][0] = sc[u][1] = 0u;
-    if (t >= p.T || t >= count) continue;
+    code[u][0] = code[u][1] = make_uint2(0, 0);
+    sc[u][0] = sc[u][1] = 0u;
+    if (t >= count) continue;
     const int64_t pos = start + t;
     const int pg = page_at(p.c, table, p.columns, pos >> p.c.log_page);
     if (pg < 0) continue;
     const int64_t row = p.c.row(pg, h, (int)(pos & (p.c.page - 1)));
-    code[u][0] = __ldg(reinterpret_cast<const uint32_t*>(p.c.k_codes) + row * L + cl);
-    code[u][1] = __ldg(reinterpret_cast<const uint32_t*>(p.c.v_codes) + row * L + cl);
-    sc[u][0] = __ldg(reinterpret_cast<const uint32_t*>(p.c.k_scales) + row * NG + cl / GL);
-    sc[u][1] = __ldg(reinterpret_cast<const uint32_t*>(p.c.v_scales) + row * NG + cl / GL);
+    code[u][0] = reinterpret_cast<const uint2*>(p.c.k_codes)[row * L + cl];
+    code[u][1] = reinterpret_cast<const uint2*>(p.c.v_codes)[row * L + cl];
+    sc[u][0] = reinterpret_cast<const uint32_t*>(p.c.k_scales)[row * NG + cl / GL];
+    sc[u][1] = reinterpret_cast<const uint32_t*>(p.c.v_scales)[row * NG + cl / GL];
   }
-  const int64_t out = (((int64_t)b * p.c.Hkv + h) * p.T) * D + cl * 8;
+  const int64_t out = (((int64_t)b * p.c.Hkv + h) * p.T + t0) * D + cl * 16;
 #pragma unroll
   for (int u = 0; u < kReadRows; ++u) {
-    const int t = t0 + u * kGroups;
-    if (t >= p.T) continue;
+    if (t0 + u * kGroups >= p.T) continue;
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
-      F2 x[4];
-      decode8(code[u][kv], bf16_lo(sc[u][kv]), bf16_hi(sc[u][kv]), x);
-      *reinterpret_cast<uint4*>((kv ? p.v : p.k) + out + (int64_t)t * D) = make_uint4(
-          pack_bf16(x[0]), pack_bf16(x[1]), pack_bf16(x[2]), pack_bf16(x[3]));
+      const Decoder dec(bf16_lo(sc[u][kv]), bf16_hi(sc[u][kv]));
+      F2 x[8];
+      dec.decode8(code[u][kv].x, x);
+      dec.decode8(code[u][kv].y, x + 4);
+      uint32_t y[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = pack_bf16(x[i]);
+      store32((kv ? p.v : p.k) + out + u * kGroups * D, y, p.wide != 0);
     }
   }
 }
@@ -288,10 +319,11 @@ __global__ void __launch_bounds__(kScoreThreads) page_scores_kernel(const PagesP
   __shared__ int top[kScoreThreads / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int h = blockIdx.y, b = blockIdx.z;
+  wait_for_previous_launch();
+  allow_next_launch();
   const int n = pages_of(p, b);
   const int first = blockIdx.x * kScorePages;
   if (first >= n) return;
-  allow_next_launch();
   const int tiles = (p.rows + 15) / 16;
   const int64_t bh = (int64_t)b * p.c.Hkv + h;
   const uint16_t* q = p.q + bh * p.rows * D;
@@ -451,11 +483,12 @@ __device__ __forceinline__ void choose_pages(const PagesParams& p, const uint32_
 
 __global__ void __launch_bounds__(kScoreThreads) choose_pages_kernel(const PagesParams p) {
   __shared__ int slots[4][kScoreThreads / 32];
+  wait_for_previous_launch();
+  allow_next_launch();
   const int64_t bh = blockIdx.x;
   const int n = pages_of(p, (int)(bh / p.c.Hkv));
   const uint32_t* keys = p.keys + bh * p.columns;
   int* out = p.out + bh * p.keep;
-  wait_for_previous_launch();
   if (n <= 4 * kScoreThreads)
     choose_pages<4>(p, keys, n, out, slots);
   else if (n <= 16 * kScoreThreads)
@@ -476,11 +509,11 @@ bool ints_ok(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 3u) 
 #define BSATTN_KV4_DISPATCH(c, CALL)                                \
   do {                                                              \
     if ((c)->head_dim == 64) {                                      \
-      if ((c)->group == 32) { CALL(64, 4); } else { CALL(64, 8); }  \
+      if ((c)->group == 32) { CALL(64, 2); } else { CALL(64, 4); }  \
     } else {                                                        \
-      if ((c)->group == 32) { CALL(128, 4); }                       \
-      else if ((c)->group == 64) { CALL(128, 8); }                  \
-      else { CALL(128, 16); }                                       \
+      if ((c)->group == 32) { CALL(128, 2); }                       \
+      else if ((c)->group == 64) { CALL(128, 4); }                  \
+      else { CALL(128, 8); }                                        \
     }                                                               \
   } while (0)
 
@@ -551,10 +584,12 @@ bsattn_status bsattn_kv4_append(const bsattn_kv4_cache* cache, const void* k, in
   const int touched = (T + cache->page_size - 2) / cache->page_size + 1;
   const dim3 grid(touched, cache->kv_heads, B);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-#define BSATTN_CALL(D, GL) kv4_append_kernel<D, GL><<<grid, kRowThreads, 0, st>>>(p)
+#define BSATTN_CALL(D, GL) \
+  e = launch_dependent(kv4_append_kernel<D, GL>, grid, dim3(kRowThreads), 0, st, p)
+  cudaError_t e;
   BSATTN_KV4_DISPATCH(cache, BSATTN_CALL);
 #undef BSATTN_CALL
-  return from_cuda(cudaGetLastError());
+  return from_cuda(e);
 }
 
 bsattn_status bsattn_kv4_read(const bsattn_kv4_cache* cache, int B, int T,
@@ -577,13 +612,16 @@ bsattn_status bsattn_kv4_read(const bsattn_kv4_cache* cache, int B, int T,
   p.T = T;
   p.k = static_cast<uint16_t*>(k);
   p.v = static_cast<uint16_t*>(v);
-  const int per_cta = kRowThreads / (cache->head_dim / 8) * kReadRows;
+  p.wide = ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 31u) == 0;
+  const int per_cta = kRowThreads / (cache->head_dim / 16) * kReadRows;
   const dim3 grid((T + per_cta - 1) / per_cta, cache->kv_heads, B);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-#define BSATTN_CALL(D, GL) kv4_read_kernel<D, GL><<<grid, kRowThreads, 0, st>>>(p)
+#define BSATTN_CALL(D, GL) \
+  e = launch_dependent(kv4_read_kernel<D, GL>, grid, dim3(kRowThreads), 0, st, p)
+  cudaError_t e;
   BSATTN_KV4_DISPATCH(cache, BSATTN_CALL);
 #undef BSATTN_CALL
-  return from_cuda(cudaGetLastError());
+  return from_cuda(e);
 }
 
 size_t bsattn_kv4_select_workspace(int B, int kv_heads, int columns) {
@@ -623,11 +661,9 @@ bsattn_status bsattn_kv4_select(const bsattn_kv4_cache* cache, const void* q, in
   p.out = selected;
   const dim3 grid((columns + kScorePages - 1) / kScorePages, cache->kv_heads, B);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (cache->head_dim == 64)
-    page_scores_kernel<64><<<grid, kScoreThreads, 0, st>>>(p);
-  else
-    page_scores_kernel<128><<<grid, kScoreThreads, 0, st>>>(p);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_dependent(
+      cache->head_dim == 64 ? page_scores_kernel<64> : page_scores_kernel<128>, grid,
+      dim3(kScoreThreads), 0, st, p);
   if (e != cudaSuccess) return from_cuda(e);
   e = launch_dependent(choose_pages_kernel, dim3(B * cache->kv_heads), dim3(kScoreThreads), 0, st,
                        p);

@@ -47,7 +47,14 @@ constexpr int kAttnThreads = 256;
 constexpr int kAttnWarps = kAttnThreads / 32;
 constexpr int kTile = 16;                      // tokens a warp takes at once
 constexpr int kStep = kTile * kAttnWarps;      // tokens a CTA takes at once
-constexpr int kStages = 4;                     // tiles in a warp's ring
+#ifndef ATTS
+#define ATTS 4
+#endif
+#ifndef ATTP
+#define ATTP 2
+#endif
+constexpr int kStages = ATTS;                     // tiles in a warp's ring
+constexpr int kPerSm = ATTP;  // CTAs an SM, 8 query rows
 constexpr int kMostSequences = 4096;
 constexpr int kJoinThreads = 256;
 constexpr float kNoMax = -1e30f;               // running maximum before any score
@@ -73,18 +80,20 @@ struct AttnParams {
   int ctas;
 };
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ uint32_t word(const uint8_t* shared) {
+  return *reinterpret_cast<const uint32_t*>(shared);
 }
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
+__device__ __forceinline__ void load_words(const uint8_t* shared, uint32_t (&w)[N]) {
+  if constexpr (N == 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(shared);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  } else if constexpr (N == 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(shared);
+    w[0] = v.x, w[1] = v.y;
+  } else {
+    w[0] = word(shared);
+  }
 }
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
@@ -163,17 +172,20 @@ struct Attn {
 };
 
 template <int D, int NG, int NT>
-__global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1)
+__global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
     kv4_attn_kernel(const AttnParams p) {
   using A = Attn<D, NG, NT>;
-  constexpr int C = A::C, RB = A::RB, RP = A::RP;
-  extern __shared__ __align__(16) uint8_t smem[];
+  constexpr int C = A::C, RB = A::RB, RP = A::RP, KW = A::CG;
+  constexpr bool kWide = D / NG >= 64;
+  extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int warp_sums[kAttnWarps];
-  __shared__ int tile_pos[kAttnWarps][kStages];
+  __shared__ uint4 queries[NT][C][32];        // operands of S^T = K Q^T, a lane's four words
+  __shared__ int2 tiles[kAttnWarps][4][32];  // (row / 16, position) of four batches of tiles
   int* prefix = reinterpret_cast<int*>(smem + A::kSmem);  // [B + 1]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, j = lane & 3;
 
+  wait_for_previous_launch();
   // steps before each sequence
   {
     const int per = (p.B + kAttnThreads - 1) / kAttnThreads;
@@ -221,9 +233,27 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1)
   const int64_t u_end = range_begin(units, ctas, blockIdx.x + 1);
   bool first_segment = true;
 
-  const uint32_t ring =
-      (uint32_t)__cvta_generic_to_shared(smem) + warp * (kStages * A::kStage);
-  int* my_pos = tile_pos[warp];
+  const uint32_t ring = shared_address(smem) + warp * (kStages * A::kStage);
+  const uint8_t* my_ring = smem + warp * (kStages * A::kStage);
+  // Where this lane's words begin.  K: tokens g and g + 8, words j KW .. j KW +
+  // KW - 1 of each group.  V: tokens 2j, 2j + 1 and 8 on, word g of each 64
+  // channels; where a group has 32 channels, word g mod 4 of each 32, its half
+  // g / 4.  A row's 16-byte piece c is at the offset with 16 c in its swizzled
+  // bits.
+  const uint32_t k_at = g * RB + (4 * KW * j & 15) + 16 * (A::swizzle(g) ^ (KW * j / 4));
+  const uint32_t v_at = 2 * j * RB + 4 * (g & 3) + 16 * (A::swizzle(2 * j) ^ (kWide ? g >> 2 : 0));
+  const uint32_t half = g < 4 ? 0x5410u : 0x7632u;
+  int2(*my_tiles)[32] = tiles[warp];
+  // this lane's pieces of a tile: codes (token, piece) = lane / C, lane % C, and
+  // for D = 128 eight tokens on; one piece of the scales
+  const uint32_t code_at = ring + lane / C * RB + 16 * ((lane % C) ^ A::swizzle(lane / C));
+  const uint8_t* k_src = p.c.k_codes + lane * 16;
+  const uint8_t* v_src = p.c.v_codes + lane * 16;
+  const int scale_kv = lane / (4 * NG), scale_piece = lane % (4 * NG);
+  const uint32_t scale_at =
+      ring + 2 * A::kCodes + scale_kv * A::kScales + scale_piece * 16;
+  const uint8_t* scale_src =
+      reinterpret_cast<const uint8_t*>(scale_kv ? p.c.v_scales : p.c.k_scales) + scale_piece * 16;
 
   while (u < u_end) {
     // the segment: steps [s0, s1) of row tile m of head h of sequence b
@@ -242,50 +272,41 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1)
     const int len = max(__ldg(p.lengths + b), 0);
     const int64_t bh = (int64_t)b * p.c.Hkv + h;
     const int n_tiles = s1 - s0;  // this warp's, one a step
+    const int seen_by_all = len - p.T - (kTile - 1);  // tiles that begin later need the mask
 
-    // ---- tiles: pages are looked up 32 steps at a time, one batch ahead
-    int page_cur = -1, pos_cur = 0, page_next = -1, pos_next = 0;
-    auto look_up = [&](int batch, int& pg, int& pos) {
-      pg = -1;
-      pos = 0;
+    // ---- tiles: pages are looked up 32 steps at a time, one batch ahead (the
+    // next batch's loads are in flight while this one's tiles run)
+    int2 next_tile;
+    auto look_up = [&](int batch) {
+      next_tile = make_int2(-1, -1);
       const int i = batch * 32 + lane;
-      if (i < n_tiles)
-        pg = tile_page(p, b, h, ((int64_t)(s0 + i) * kAttnWarps + warp) * kTile, len, pos);
-    };
-    auto issue = [&](int i) {
       if (i < n_tiles) {
-        if ((i & 31) == 0) {
-          if (i == 0) {
-            look_up(0, page_cur, pos_cur);
-          } else {
-            page_cur = page_next;
-            pos_cur = pos_next;
-          }
-          look_up(i / 32 + 1, page_next, pos_next);
+        int pos = 0;
+        const int pg =
+            tile_page(p, b, h, ((int64_t)(s0 + i) * kAttnWarps + warp) * kTile, len, pos);
+        if (pg >= 0)
+          next_tile = make_int2((int)(p.c.row(pg, h, pos & (p.c.page - 1)) / kTile), pos);
+      }
+    };
+    look_up(0);
+    auto issue = [&](int i) {
+      if ((i & 31) == 0) {
+        my_tiles[(i >> 5) & 3][lane] = next_tile;
+        __syncwarp();
+        look_up((i >> 5) + 1);
+      }
+      const int row16 = my_tiles[(i >> 5) & 3][i & 31].x;
+      if (row16 >= 0) {
+        const uint32_t stage = (i % kStages) * A::kStage;
+        const uint8_t* kc = k_src + (int64_t)row16 * A::kCodes;
+        const uint8_t* vc = v_src + (int64_t)row16 * A::kCodes;
+        copy16(code_at + stage, kc);
+        copy16(code_at + stage + A::kCodes, vc);
+        if (D == 128) {
+          copy16(code_at + stage + 8 * RB, kc + 512);
+          copy16(code_at + stage + A::kCodes + 8 * RB, vc + 512);
         }
-        const int pg = __shfl_sync(0xFFFFFFFFu, page_cur, i & 31);
-        const int pos = __shfl_sync(0xFFFFFFFFu, pos_cur, i & 31);
-        const int st = i % kStages;
-        if (lane == 0) my_pos[st] = pg < 0 ? -1 : pos;
-        if (pg >= 0) {
-          const uint32_t dst = ring + st * A::kStage;
-          const int64_t row = p.c.row(pg, h, pos & (p.c.page - 1));
-          const uint8_t* kc = p.c.k_codes + row * RB;
-          const uint8_t* vc = p.c.v_codes + row * RB;
-#pragma unroll
-          for (int x = 0; x < kTile * C / 32; ++x) {
-            const int piece = x * 32 + lane, token = piece / C, c = piece % C;
-            const uint32_t at = token * RB + 16 * (c ^ A::swizzle(token));
-            copy16(dst + at, kc + piece * 16);
-            copy16(dst + A::kCodes + at, vc + piece * 16);
-          }
-          if (lane < 8 * NG) {
-            const int kv = lane / (4 * NG), piece = lane % (4 * NG);
-            const uint8_t* sc = reinterpret_cast<const uint8_t*>(kv ? p.c.v_scales : p.c.k_scales);
-            copy16(dst + 2 * A::kCodes + kv * A::kScales + piece * 16,
-                   sc + row * (NG * 4) + piece * 16);
-          }
-        }
+        if (lane < 8 * NG) copy16(scale_at + stage, scale_src + (int64_t)row16 * A::kScales);
       }
       copy_commit();
     };
@@ -293,7 +314,6 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1)
     for (int i = 0; i < kStages - 1; ++i) issue(i);
 
     // ---- queries: operands, the factor of the code product, the group sums
-    uint32_t qf[NT][C][4];
     float mul[NT][2], qs[NT][NG][2];
     int lim[NT][2];  // last position that the row sees
 #pragma unroll
@@ -304,7 +324,8 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1)
       for (int c = 0; c < C; ++c) {
         uint4 raw = make_uint4(0, 0, 0, 0);
         if (r < p.rows)
-          raw = __ldg(reinterpret_cast<const uint4*>(p.q + (bh * p.rows + r) * D) + 4 * c + j);
+          raw = __ldg(reinterpret_cast<const uint4*>(p.q + (bh * p.rows + r) * D) +
+                      (c / KW * 4 + j) * KW + c % KW);
         unpack8(raw, x[c]);
         if (c % A::CG == 0) sum[c / A::CG] = 0.0f;
 #pragma unroll
@@ -326,10 +347,10 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1)
       const float f = ldexpf(1.0f, sh), f16 = f * 0.0625f;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        qf[nt][c][0] = pack_half(x[c][0] * f, x[c][4] * f);
-        qf[nt][c][1] = pack_half(x[c][2] * f, x[c][6] * f);
-        qf[nt][c][2] = pack_half(x[c][1] * f16, x[c][5] * f16);
-        qf[nt][c][3] = pack_half(x[c][3] * f16, x[c][7] * f16);
+        if (warp == 0)  // (the same for all warps)
+          queries[nt][c][lane] = make_uint4(
+              pack_half(x[c][0] * f, x[c][4] * f), pack_half(x[c][2] * f, x[c][6] * f),
+              pack_half(x[c][1] * f16, x[c][5] * f16), pack_half(x[c][3] * f16, x[c][7] * f16));
       }
       const float m = p.scale_log2 * ldexpf(1.0f, 24 - sh);
 #pragma unroll
@@ -344,6 +365,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1)
       }
     }
 
+    __syncthreads();
     float mx[NT][2], l[NT][2], vm[NT][NG][2], o[C][2][NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -371,10 +393,9 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1)
       __syncwarp();
       issue(i + kStages - 1);
       const int st = i % kStages;
-      const int pos = my_pos[st];
+      const int pos = my_tiles[(i >> 5) & 3][i & 31].y;
       if (pos < 0) continue;
-      const uint32_t kt = ring + st * A::kStage;
-      const uint32_t vt = kt + A::kCodes, kst = kt + 2 * A::kCodes, vst = kst + A::kScales;
+      const uint8_t* stage = my_ring + st * A::kStage;
 
       // ---- scores (base 2): tokens g and g + 8, rows 2j and 2j + 1
       float s[NT][4];
@@ -382,36 +403,39 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1)
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[nt][e] = 0.0f;
-      const uint32_t kw = kt + g * RB + 4 * j;
-      const int sw = A::swizzle(g);
 #pragma unroll
       for (int n = 0; n < NG; ++n) {
-        float acc[NT][4];
+        float acc[NT][4], acc16[NT][4];  // (two chains of products, half as long)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[nt][e] = 0.0f;
+          for (int e = 0; e < 4; ++e) acc[nt][e] = acc16[nt][e] = 0.0f;
+        const uint8_t* at = stage + (k_at ^ (16 * KW * n));
+        uint32_t w0[KW], w1[KW];
+        load_words<KW>(at, w0);
+        load_words<KW>(at + 8 * RB, w1);
 #pragma unroll
-        for (int c = n * A::CG; c < (n + 1) * A::CG; ++c) {
-          const uint32_t w0 = lds32(kw + 16 * (c ^ sw)), w1 = lds32(kw + 8 * RB + 16 * (c ^ sw));
-          const uint32_t y0 = w0 >> 8, y1 = w1 >> 8;
-          const uint32_t a[4] = {w0 & 0x000F000Fu, w1 & 0x000F000Fu, y0 & 0x000F000Fu,
+        for (int k = 0; k < KW; ++k) {
+          const uint32_t y0 = w0[k] >> 8, y1 = w1[k] >> 8;
+          const uint32_t a[4] = {w0[k] & 0x000F000Fu, w1[k] & 0x000F000Fu, y0 & 0x000F000Fu,
                                  y1 & 0x000F000Fu};
-          const uint32_t a16[4] = {w0 & 0x00F000F0u, w1 & 0x00F000F0u, y0 & 0x00F000F0u,
+          const uint32_t a16[4] = {w0[k] & 0x00F000F0u, w1[k] & 0x00F000F0u, y0 & 0x00F000F0u,
                                    y1 & 0x00F000F0u};
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            mma_f16(acc[nt], a, qf[nt][c][0], qf[nt][c][1]);
-            mma_f16(acc[nt], a16, qf[nt][c][2], qf[nt][c][3]);
+            const uint4 qf = queries[nt][n * KW + k][lane];
+            mma_f16(acc[nt], a, qf.x, qf.y);
+            mma_f16(acc16[nt], a16, qf.z, qf.w);
           }
         }
-        const uint32_t k0 = lds32(kst + (g * NG + n) * 4), k1 = lds32(kst + ((g + 8) * NG + n) * 4);
+        const uint8_t* ks = stage + 2 * A::kCodes + (g * NG + n) * 4;
+        const uint32_t k0 = word(ks), k1 = word(ks + 8 * NG * 4);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const uint32_t sc = e < 2 ? k0 : k1;
-            s[nt][e] = fmaf(acc[nt][e] * bf16_lo(sc), mul[nt][e & 1],
+            s[nt][e] = fmaf((acc[nt][e] + acc16[nt][e]) * bf16_lo(sc), mul[nt][e & 1],
                             fmaf(bf16_hi(sc), qs[nt][n][e & 1], s[nt][e]));
           }
       }
@@ -419,7 +443,8 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1)
       float vs[NG][NT][4], vl[NG][NT][4], most = 0.0f;
 #pragma unroll
       for (int n = 0; n < NG; ++n) {
-        const uint32_t v0 = lds32(vst + (g * NG + n) * 4), v1 = lds32(vst + ((g + 8) * NG + n) * 4);
+        const uint8_t* sc = stage + 2 * A::kCodes + A::kScales + (g * NG + n) * 4;
+        const uint32_t v0 = word(sc), v1 = word(sc + 8 * NG * 4);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -427,8 +452,10 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1)
             vs[n][nt][e] = bf16_lo(e < 2 ? v0 : v1);
             vl[n][nt][e] = bf16_hi(e < 2 ? v0 : v1);
           }
+        most = fmaxf(most, fmaxf(bf16_lo(v0), bf16_lo(v1)));
       }
-      if (pos + kTile - 1 > len - p.T) {
+      if (pos > seen_by_all) {
+        most = 0.0f;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -437,17 +464,16 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1)
               s[nt][e] = -INFINITY;
 #pragma unroll
               for (int n = 0; n < NG; ++n) vs[n][nt][e] = vl[n][nt][e] = 0.0f;
+            } else {
+#pragma unroll
+              for (int n = 0; n < NG; ++n) most = fmaxf(most, vs[n][nt][e]);
             }
       }
       float over = kNoMax;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          over = fmaxf(over, s[nt][e] - mx[nt][e & 1]);
-#pragma unroll
-          for (int n = 0; n < NG; ++n) most = fmaxf(most, vs[n][nt][e]);
-        }
+        for (int e = 0; e < 4; ++e) over = fmaxf(over, s[nt][e] - mx[nt][e & 1]);
       // ---- rare: a score far above the running maximum, or a larger step
       if (__any_sync(0xFFFFFFFFu, over > kLag || most > top_step)) {
 #pragma unroll
@@ -513,28 +539,34 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1)
           }
         }
       }
-      // ---- O^T += V^T P^T: a piece's 32 channels are two M tiles, codes 0 and
-      // 2 (1 and 3) of each lane's half word for rows g and g + 8
-      const uint32_t vw = vt + 2 * j * RB + 4 * (g & 3);
-      const int vsw = A::swizzle(2 * j);
-      const uint32_t half = g < 4 ? 0x5410u : 0x7632u;
+      // ---- O^T += V^T P^T: of each half word, M tile 0 is made of codes 0 (rows
+      // g) and 2 (rows g + 8), M tile 1 of the whole bytes, codes 0 + 16 1 and
+      // 2 + 16 3, from which tile 0 is taken off at the end: a byte is one
+      // mask, a code by itself a shift and a mask
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        const uint32_t at = vw + 16 * (c ^ vsw);
-        const uint32_t x0 = __byte_perm(lds32(at), lds32(at + RB), half);
-        const uint32_t x1 = __byte_perm(lds32(at + 8 * RB), lds32(at + 9 * RB), half);
-        const uint32_t y0 = x0 >> 8, y1 = x1 >> 8;
-        const uint32_t a[4] = {x0 & 0x000F000Fu, y0 & 0x000F000Fu, x1 & 0x000F000Fu,
-                               y1 & 0x000F000Fu};
-        const uint32_t a16[4] = {x0 & 0x00F000F0u, y0 & 0x00F000F0u, x1 & 0x00F000F0u,
-                                 y1 & 0x00F000F0u};
+        uint32_t x0, x1;
+        if (kWide) {
+          const uint8_t* at = stage + A::kCodes + (v_at ^ (16 * (c & ~1)));
+          const uint32_t sel = c & 1 ? 0x7632u : 0x5410u;
+          x0 = __byte_perm(word(at), word(at + RB), sel);
+          x1 = __byte_perm(word(at + 8 * RB), word(at + 9 * RB), sel);
+        } else {
+          const uint8_t* at = stage + A::kCodes + (v_at ^ (16 * c));
+          x0 = __byte_perm(word(at), word(at + RB), half);
+          x1 = __byte_perm(word(at + 8 * RB), word(at + 9 * RB), half);
+        }
+        const uint32_t bytes[4] = {x0 & 0x00FF00FFu, __byte_perm(x0, 0u, 0x4341),
+                                   x1 & 0x00FF00FFu, __byte_perm(x1, 0u, 0x4341)};
+        const uint32_t a[4] = {x0 & 0x000F000Fu, bytes[1] & 0x000F000Fu, x1 & 0x000F000Fu,
+                               bytes[3] & 0x000F000Fu};
         const int n = c / A::CG;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           mma_f16(o[c][0][nt], a, wh[n][nt][0], wh[n][nt][1]);
+          mma_f16(o[c][1][nt], bytes, wh[n][nt][0], wh[n][nt][1]);
           mma_f16(o[c][0][nt], a, wl[n][nt][0], wl[n][nt][1]);
-          mma_f16(o[c][1][nt], a16, wh[n][nt][0], wh[n][nt][1]);
-          mma_f16(o[c][1][nt], a16, wl[n][nt][0], wl[n][nt][1]);
+          mma_f16(o[c][1][nt], bytes, wl[n][nt][0], wl[n][nt][1]);
         }
       }
     }
@@ -565,12 +597,14 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1)
         const float f = 16777216.0f * top_step, f16 = 1048576.0f * top_step;  // 2^24, 2^20
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-          float* dst = so + (warp * RP + r) * D + 32 * c + 8 * (g & 3) + 4 * (g >> 2);
+          const int ch = kWide ? 64 * (c / 2) + 8 * g + 4 * (c & 1)
+                               : 32 * c + 8 * (g & 3) + 4 * (g >> 2);
+          float* dst = so + (warp * RP + r) * D + ch;
           const float base = vm[nt][c / A::CG][e];
           dst[0] = fmaf(o[c][0][nt][e], f, base);
-          dst[1] = fmaf(o[c][1][nt][e], f16, base);
+          dst[1] = fmaf(o[c][1][nt][e] - o[c][0][nt][e], f16, base);
           dst[2] = fmaf(o[c][0][nt][e + 2], f, base);
-          dst[3] = fmaf(o[c][1][nt][e + 2], f16, base);
+          dst[3] = fmaf(o[c][1][nt][e + 2] - o[c][0][nt][e + 2], f16, base);
         }
       }
     __syncthreads();
@@ -628,13 +662,14 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const AttnParams
   constexpr int kParts = kJoinThreads / D;  // slots read at once
   __shared__ float red[kJoinThreads];
   __shared__ float tops[kJoinThreads / 32];
+  wait_for_previous_launch();
+  allow_next_launch();
   const int heads = p.c.Hkv * p.mt;
   const int64_t hh = blockIdx.x;
   const int b = (int)(hh / heads), hm = (int)(hh - (int64_t)b * heads);
   const int h = hm / p.mt, r = blockIdx.y;
   const int row = (hm - h * p.mt) * RP + r;
   if (row >= p.rows) return;
-  wait_for_previous_launch();
   const int64_t before = __ldcg(p.prefix + b), steps = __ldcg(p.prefix + b + 1) - before;
   const int64_t units = (int64_t)__ldcg(p.prefix + p.B) * heads;
   const int64_t out_row = ((int64_t)b * p.c.Hkv + h) * p.rows + row;
@@ -694,7 +729,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const AttnParams
 }
 
 // CTAs of the attention launch: as many as run at once
-int attn_ctas(int nt, int sms) { return nt == 1 ? 2 * sms : sms; }
+int attn_ctas(int nt, int sms) { return nt == 1 ? kPerSm * sms : sms; }
 
 template <int D, int NG, int NT>
 cudaError_t launch_attn(const AttnParams& p, int grid, cudaStream_t st) {
@@ -705,8 +740,8 @@ cudaError_t launch_attn(const AttnParams& p, int grid, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(kv4_attn_kernel<D, NG, NT>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
   if (e != cudaSuccess) return e;
-  kv4_attn_kernel<D, NG, NT><<<grid, kAttnThreads, smem, st>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  e = launch_dependent(kv4_attn_kernel<D, NG, NT>, dim3(grid), dim3(kAttnThreads), smem, st, p);
+  if (e != cudaSuccess) return e;
   const int rows = p.rows < 8 * NT ? p.rows : 8 * NT;
   return launch_dependent(kv4_join_kernel<D, NT>, dim3(p.B * p.c.Hkv * p.mt, rows),
                           dim3(kJoinThreads), 0, st, p);
@@ -762,7 +797,8 @@ bsattn_status bsattn_kv4_attn(const bsattn_kv4_cache* cache, const void* q, int 
   const int nt = rows <= 8 ? 1 : 2;
   const int mt = (int)((rows + 8 * nt - 1) / (8 * nt));
   if (rows > 128 || B > kMostSequences || steps * B >= (1ll << 31) ||
-      (int64_t)B * cache->kv_heads * mt >= (1ll << 31))
+      (int64_t)B * cache->kv_heads * mt >= (1ll << 31) ||
+      (int64_t)cache->pages * cache->kv_heads * cache->page_size / kTile >= (1ll << 31))
     return BSATTN_ERR_UNSUPPORTED;
   if (workspace_bytes < bsattn_kv4_attn_workspace(B, H, cache->kv_heads, T, cache->head_dim) ||
       workspace_bytes == 0)

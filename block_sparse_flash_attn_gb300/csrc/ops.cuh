@@ -31,6 +31,29 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
 }
 
 // ---------------------------------------------------------------------------
+// Asynchronous copies of 16 bytes into shared memory: bytes in flight that
+// hold no registers.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t shared_address(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+
+// ---------------------------------------------------------------------------
 // Two 32-bit floats a register pair: sm_103a adds, multiplies and fuses both
 // with one instruction, each rounded as the single instruction rounds.
 // ---------------------------------------------------------------------------
@@ -165,33 +188,29 @@ __device__ __forceinline__ float rint_scaled(const Sum2& s, int shift) {
 }
 
 // The mean of `rows` rows of a block (rows a power of two), rounded to 7 bits
-// beside its largest entry, by a CTA of 128 threads: pairs[i] are this thread's
-// sums of channels (lane % (D/8)) * 8 + 2i, 2i + 1 over the rows that it saw.  Writes, as
-// bf16, the whole numbers t = rint(mean 2^(6 - E)) or the values t 2^(E - 6).
-template <int D>
-__device__ __forceinline__ void write_rounded_mean(const Sum2x2 (&pairs)[4], int rows, bool whole,
+// beside its largest entry, by a CTA of 128 threads: a row is held by D / (2 N)
+// lanes, pairs[i] are this thread's sums of channels (lane % L) * 2N + 2i and
+// 2i + 1 over the rows that it saw.  Writes, as bf16, the whole numbers t =
+// rint(mean 2^(6 - E)) or the values t 2^(E - 6).
+template <int D, int N>
+__device__ __forceinline__ void write_rounded_mean(const Sum2x2 (&pairs)[N], int rows, bool whole,
                                                    uint16_t* out) {
-  constexpr int L = D / 8, W = 4;
+  constexpr int L = D / (2 * N), W = 4;
   __shared__ Sum2 part[W][D];
   __shared__ int top[W];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  Sum2 s[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 hi = split(pairs[i].hi), lo = split(pairs[i].lo);
-    s[2 * i] = Sum2{hi.x, lo.x};
-    s[2 * i + 1] = Sum2{hi.y, lo.y};
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 2 * N; ++i) {
+    const float2 hi = split(pairs[i / 2].hi), lo = split(pairs[i / 2].lo);
+    Sum2 s = i % 2 ? Sum2{hi.y, lo.y} : Sum2{hi.x, lo.x};
 #pragma unroll
     for (int o = L; o < 32; o <<= 1) {
       Sum2 other;
-      other.hi = __shfl_xor_sync(0xFFFFFFFFu, s[i].hi, o);
-      other.lo = __shfl_xor_sync(0xFFFFFFFFu, s[i].lo, o);
-      add_exact(s[i], other);
+      other.hi = __shfl_xor_sync(0xFFFFFFFFu, s.hi, o);
+      other.lo = __shfl_xor_sync(0xFFFFFFFFu, s.lo, o);
+      add_exact(s, other);
     }
-    if (lane < L) part[warp][lane * 8 + i] = s[i];
+    if (lane < L) part[warp][lane * 2 * N + i] = s;
   }
   __syncthreads();
   const int c = threadIdx.x;
@@ -224,10 +243,22 @@ __device__ __forceinline__ uint32_t ordered_bits(float x) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+// 32 bytes to global memory, in one store where they are aligned to 32
+__device__ __forceinline__ void store32(void* dst, const uint32_t (&v)[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  } else {
+    static_cast<uint4*>(dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    static_cast<uint4*>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
+}
+
 // D += A B, 16 x 8 x 16: bf16 in, 32-bit sums (A row-major, B column-major)
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -236,7 +267,7 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                         uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])

@@ -31,14 +31,16 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 constexpr int kRopeWarps = kRopeThreads / 32;
-#ifndef BWDW
-#define BWDW 4
+// The backward kernel: warps a CTA, CTAs an SM and rows a lane.  Many rows a
+// warp share one token's angles and read long runs of x, and four CTAs keep
+// enough in flight.  At 4 x 4096 tokens, 16 + 2 x 16 heads of 128: 4, 4, 4 take
+// 131 us; 2 rows a lane in 5 CTAs 151, in 6 (spilling) 188; 4 rows in 3 CTAs 147.
+constexpr int kBwdWarps = 4;
+constexpr int kBwdPerSm = 4;
+constexpr int kBwdRows = 4;
+#ifndef FWDU
+#define FWDU 8
 #endif
-#ifndef BWDP
-#define BWDP 5
-#endif
-constexpr int kBwdWarps = BWDW;   // the backward kernel: warps a CTA
-constexpr int kBwdPerSm = BWDP;   // and CTAs an SM (its registers' limit)
 
 struct RopeParams {
   const uint16_t* x;  // [B][S][heads][D], strides xb and xs (elements)
@@ -144,6 +146,8 @@ template <int D, bool INTER, int U>
 __global__ void __launch_bounds__(kRopeThreads) rope_fwd_kernel(const RopeParams p) {
   constexpr int L = D / 8;   // lanes a row
   constexpr int R = 32 / L;  // rows a warp holds at once
+  wait_for_previous_launch();
+  allow_next_launch();
   const int lane = threadIdx.x & 31;
   const unsigned chunks = p.q_chunks + 2 * p.k_chunks;
   const unsigned block = blockIdx.x / chunks;
@@ -224,6 +228,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, kBwdPerSm) rope_bwd_kernel(con
   constexpr int L = D / 8;
   constexpr int R = 32 / L;
   __shared__ float red[kBwdWarps][D];
+  wait_for_previous_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int chunk = blockIdx.x / p.groups, group = blockIdx.x - chunk * p.groups;
   const Chunk c = chunk_of(p, chunk, U * R);
@@ -369,8 +374,7 @@ __global__ void rope_table_kernel(const double* __restrict__ inv_freq, int n_pos
 
 bool multiple8(int64_t v) { return v % 8 == 0; }
 
-// Rows a lane holds at once: as many as the larger kind of heads fills, at most
-// `most` (4; 2 in the backward pass, whose rows take three times the registers).
+// Rows a lane holds at once: as many as the larger kind of heads fills, at most `most`.
 int rows_per_lane(int H, int D, int most) {
   const int at_once = 256 / D;
   int u = 1;
@@ -385,14 +389,15 @@ struct BwdSplit {
 };
 BwdSplit bwd_split(int tokens, int H, int Hkv, int D, int sms) {
   BwdSplit s;
-  s.u = rows_per_lane(H, D, 2);
+  s.u = rows_per_lane(H, D, kBwdRows);
   const int rows = s.u * 256 / D;
   s.q_chunks = (H + rows - 1) / rows;
   s.k_chunks = (Hkv + rows - 1) / rows;
   const int chunks = s.q_chunks + 2 * s.k_chunks;
   const int most = tokens / kBwdWarps + (tokens % kBwdWarps != 0);
-  s.groups = (kBwdPerSm * sms + chunks - 1) / chunks;
+  s.groups = kBwdPerSm * sms / chunks;  // one wave: a CTA more would run alone at the end
   if (s.groups > most) s.groups = most;
+  if (s.groups < 1) s.groups = 1;
   return s;
 }
 
@@ -444,28 +449,27 @@ RopeParams rope_params(const void* x, int64_t xb, int64_t xs, int B, int S, int 
 }
 
 template <int D, bool INTER>
-void launch_rope_fwd(RopeParams& p, cudaStream_t st) {
-  const int u = rows_per_lane(p.H, D, 4), rows = u * 256 / D;
+cudaError_t launch_rope_fwd(RopeParams& p, cudaStream_t st) {
+  const int u = rows_per_lane(p.H, D, FWDU), rows = u * 256 / D;
   p.q_chunks = (p.H + rows - 1) / rows;
   p.k_chunks = (p.Hkv + rows - 1) / rows;
   // at most B * S * heads CTAs: below 2^31
   const int blocks = p.tokens / kRopeWarps + (p.tokens % kRopeWarps != 0);
   const int grid = blocks * (p.q_chunks + 2 * p.k_chunks);
-  if (u == 1)
-    rope_fwd_kernel<D, INTER, 1><<<grid, kRopeThreads, 0, st>>>(p);
-  else if (u == 2)
-    rope_fwd_kernel<D, INTER, 2><<<grid, kRopeThreads, 0, st>>>(p);
-  else
-    rope_fwd_kernel<D, INTER, 4><<<grid, kRopeThreads, 0, st>>>(p);
+  return launch_dependent(u == 1   ? rope_fwd_kernel<D, INTER, 1>
+                          : u == 2 ? rope_fwd_kernel<D, INTER, 2>
+                          : u == 4 ? rope_fwd_kernel<D, INTER, 4>
+                                   : rope_fwd_kernel<D, INTER, 8>,
+                          dim3(grid), dim3(kRopeThreads), 0, st, (const RopeParams&)p);
 }
 
 template <int D, bool INTER>
-void launch_rope_bwd(const RopeParams& p, int u, cudaStream_t st) {
+cudaError_t launch_rope_bwd(const RopeParams& p, int u, cudaStream_t st) {
   const int grid = (p.q_chunks + 2 * p.k_chunks) * p.groups;
-  if (u == 1)
-    rope_bwd_kernel<D, INTER, 1><<<grid, 32 * kBwdWarps, 0, st>>>(p);
-  else
-    rope_bwd_kernel<D, INTER, 2><<<grid, 32 * kBwdWarps, 0, st>>>(p);
+  return launch_dependent(u == 1   ? rope_bwd_kernel<D, INTER, 1>
+                          : u == 2 ? rope_bwd_kernel<D, INTER, 2>
+                                   : rope_bwd_kernel<D, INTER, 4>,
+                          dim3(grid), dim3(32 * kBwdWarps), 0, st, p);
 }
 
 }  // namespace
@@ -506,10 +510,8 @@ bsattn_status bsattn_qk_norm_rope(const void* x, int64_t x_batch_stride, int64_t
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool inter = (flags & BSATTN_ROPE_INTERLEAVED) != 0;
   if (D == 64)
-    inter ? launch_rope_fwd<64, true>(p, st) : launch_rope_fwd<64, false>(p, st);
-  else
-    inter ? launch_rope_fwd<128, true>(p, st) : launch_rope_fwd<128, false>(p, st);
-  return from_cuda(cudaGetLastError());
+    return from_cuda(inter ? launch_rope_fwd<64, true>(p, st) : launch_rope_fwd<64, false>(p, st));
+  return from_cuda(inter ? launch_rope_fwd<128, true>(p, st) : launch_rope_fwd<128, false>(p, st));
 }
 
 size_t bsattn_qk_norm_rope_bwd_workspace(int B, int S, int H, int Hkv, int D) {
@@ -562,12 +564,11 @@ bsattn_status bsattn_qk_norm_rope_bwd(const void* x, int64_t x_batch_stride, int
   p.dxs = dx_token_stride;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool inter = (flags & BSATTN_ROPE_INTERLEAVED) != 0;
-  if (D == 64)
-    inter ? launch_rope_bwd<64, true>(p, split.u, st) : launch_rope_bwd<64, false>(p, split.u, st);
-  else
-    inter ? launch_rope_bwd<128, true>(p, split.u, st)
-          : launch_rope_bwd<128, false>(p, split.u, st);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e =
+      D == 64 ? (inter ? launch_rope_bwd<64, true>(p, split.u, st)
+                       : launch_rope_bwd<64, false>(p, split.u, st))
+              : (inter ? launch_rope_bwd<128, true>(p, split.u, st)
+                       : launch_rope_bwd<128, false>(p, split.u, st));
   if (e != cudaSuccess || !q_weight) return from_cuda(e);
   e = launch_dependent(rope_weight_kernel, dim3(D / 32, 2), dim3(32, 32), 0, st,
                        (const float*)p.partial, split.q_chunks * split.groups,

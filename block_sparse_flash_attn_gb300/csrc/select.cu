@@ -17,7 +17,7 @@
 // element costs one exact addition (6 operations).  The scores are one small
 // matrix product per head on bf16 tensor instructions (whole numbers up to 128
 // are exact in bf16), the rows' k-th best is found by bisection over the
-// scores' order-preserving bit patterns, held in registers.
+// scores' order-preserving bit patterns, held in registers, steered by the counts.
 #include <cstdint>
 
 #include "internal.h"
@@ -27,43 +27,51 @@ namespace bsattn {
 namespace {
 
 constexpr int kPoolThreads = 128;
-constexpr int kPoolWarps = kPoolThreads / 32;
 constexpr int kSelThreads = 256;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr uint32_t kForced = 0xFFFFFFFFu;  // key of a block that is always kept
 constexpr uint32_t kRuledOut = 0u;         // key of a block that never is
 
 // One CTA per block: its rows' mean, rounded.  The blocks of Q come first
-// (whole numbers t), then the blocks of K (t 2^(E - 6)).
+// (whole numbers t), then the blocks of K (t 2^(E - 6)).  A block is 8 to 32 KB
+// in a row: it is copied to shared memory at once, each thread the pieces that
+// it adds up itself, in two groups so that the first half is summed while the
+// second arrives.
 template <int D>
 __global__ void __launch_bounds__(kPoolThreads)
     block_mean_kernel(const uint16_t* __restrict__ q, const uint16_t* __restrict__ k, int q_blocks,
                       int key_block, uint16_t* __restrict__ mq, uint16_t* __restrict__ mk) {
-  constexpr int L = D / 8;
-  constexpr int R = 32 / L;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  extern __shared__ __align__(16) uint8_t block[];
+  wait_for_previous_launch();
   const bool is_q = (int)blockIdx.x < q_blocks;
   const int64_t blk = is_q ? blockIdx.x : blockIdx.x - q_blocks;
   const int rows = is_q ? kBlock : key_block;
-  const uint16_t* src = (is_q ? q : k) + blk * rows * D + (lane % L) * 8;
-
+  const uint4* src = reinterpret_cast<const uint4*>((is_q ? q : k) + blk * rows * D) + threadIdx.x;
+  const uint32_t dst = shared_address(block) + threadIdx.x * 16;
+  const int pieces = rows * (D / 8) / kPoolThreads;  // a thread's: 4, 8 or 16
   Sum2x2 s[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) s[i].hi = s[i].lo = f2(0.0f);
-  constexpr int U = 4;
-  for (int r0 = warp * R + lane / L; r0 < rows; r0 += U * kPoolWarps * R) {
-    uint4 raw[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      raw[u] = __ldg(reinterpret_cast<const uint4*>(src + (r0 + u * kPoolWarps * R) * D));
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      add_exact(s[0], bf16_pair(raw[u].x));
-      add_exact(s[1], bf16_pair(raw[u].y));
-      add_exact(s[2], bf16_pair(raw[u].z));
-      add_exact(s[3], bf16_pair(raw[u].w));
-    }
-  }
+  const int half = pieces / 2;
+#pragma unroll 4
+  for (int i = 0; i < half; ++i) copy16(dst + i * (kPoolThreads * 16), src + i * kPoolThreads);
+  copy_commit();
+#pragma unroll 4
+  for (int i = half; i < pieces; ++i) copy16(dst + i * (kPoolThreads * 16), src + i * kPoolThreads);
+  copy_commit();
+  auto add = [&](int i) {
+    const uint4 raw = lds128(dst + i * (kPoolThreads * 16));
+    add_exact(s[0], bf16_pair(raw.x));
+    add_exact(s[1], bf16_pair(raw.y));
+    add_exact(s[2], bf16_pair(raw.z));
+    add_exact(s[3], bf16_pair(raw.w));
+  };
+  copy_wait<1>();
+#pragma unroll 2
+  for (int i = 0; i < half; ++i) add(i);
+  copy_wait<0>();
+#pragma unroll 2
+  for (int i = half; i < pieces; ++i) add(i);
   allow_next_launch();
   write_rounded_mean<D>(s, rows, is_q, (is_q ? mq : mk) + blk * D);
 }
@@ -79,84 +87,138 @@ struct SelectParams {
   int rows;  // query blocks a CTA: 16, or 4 when 16 rows of keys do not fit
 };
 
-// The k-th largest of a row of n keys held by one warp (key i*32 + lane), as
-// (threshold, how many keys equal to it are taken, lowest index first).  KP >
-// 0: in registers, KP a lane; KP = 0: in shared memory.
+// A row of n keys held by one warp, four consecutive ones a lane and piece of
+// 128.  KP > 0: in registers, KP a lane; KP = 0: in shared memory.  (Keys behind
+// n are ruled out.)
 template <int KP>
 struct RowKeys {
   uint32_t k[KP > 0 ? KP : 1];
-  const uint32_t* sh;
-  int n, lane;
+  const uint4* sh;
+  int pieces, lane;
 
-  __device__ __forceinline__ void load(const uint32_t* row, int count, int ln) {
-    sh = row;
-    n = count;
+  __device__ __forceinline__ void load(const uint32_t* row, int n, int ln) {
+    sh = reinterpret_cast<const uint4*>(row);
+    pieces = (n + 127) / 128;
     lane = ln;
     if (KP > 0) {
 #pragma unroll
-      for (int i = 0; i < KP; ++i) k[i] = i * 32 + lane < n ? row[i * 32 + lane] : kRuledOut;
+      for (int i = 0; i < KP / 4; ++i) {
+        const uint4 v = piece_from_shared(i, n);
+        k[4 * i] = v.x, k[4 * i + 1] = v.y, k[4 * i + 2] = v.z, k[4 * i + 3] = v.w;
+      }
     }
   }
-  __device__ __forceinline__ int count_at_least(uint32_t t) const {
-    int c = 0;
+  __device__ __forceinline__ uint4 piece_from_shared(int i, int n) const {
+    return i * 128 + lane * 4 < n ? sh[i * 32 + lane] : make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ uint4 piece(int i, int n) const { return piece_from_shared(i, n); }
+
+  template <typename F>
+  __device__ __forceinline__ void each(int n, F f) const {
     if (KP > 0) {
 #pragma unroll
-      for (int i = 0; i < KP; ++i) c += k[i] >= t ? 1 : 0;
+      for (int i = 0; i < KP; ++i) f(k[i]);
     } else {
-      for (int i = lane; i < n; i += 32) c += sh[i] >= t ? 1 : 0;
+      for (int i = 0; i < pieces; ++i) {
+        const uint4 v = piece_from_shared(i, n);
+        f(v.x), f(v.y), f(v.z), f(v.w);
+      }
     }
-    return __reduce_add_sync(0xFFFFFFFFu, c);
   }
 };
 
+// Marks the best keys of a row: `keep` of them, or all that are forced if those
+// are more.  The threshold is searched between the row's least and largest key,
+// in turn by interpolating the counts (scores spread smoothly: a few steps
+// do) and by halving (so that it ends, in 64 steps at most).
 template <int KP>
 __device__ __forceinline__ void choose_row(const uint32_t* row, int n, int nk, int keep,
                                            uint8_t* out, int lane) {
   RowKeys<KP> keys;
   keys.load(row, n, lane);
-  const int allowed = keys.count_at_least(1u);
-  const int forced = keys.count_at_least(kForced);
+  // counts in one word: forced << 16 | allowed (n <= 8192); largest and least
+  // of the keys in between
+  uint32_t counts = 0, top = 0, least = kForced;
+  keys.each(n, [&](uint32_t x) {
+    counts += (x != kRuledOut ? 1u : 0u) + (x == kForced ? 65536u : 0u);
+    top = max(top, x == kForced ? 0u : x);
+    least = min(least, x - 1u);  // 0 wraps: never the least
+  });
+  counts = __reduce_add_sync(0xFFFFFFFFu, counts);
+  top = __reduce_max_sync(0xFFFFFFFFu, top);
+  least = __reduce_min_sync(0xFFFFFFFFu, least) + 1u;
+  const int allowed = counts & 0xFFFF, forced = counts >> 16;
   const int want = min(max(keep, forced), allowed);
-  // largest t with at least `want` keys >= t, bit by bit from the top
+  // at least `want` keys are >= t, fewer are >= hi; `have` of them are >= t
   uint32_t t = 1u;
-  int above = allowed;
-  if (want < allowed) {
-    t = 0u;
-    for (int bit = 31; bit >= 0; --bit) {
-      const uint32_t c = t | (1u << bit);
-      const int cnt = keys.count_at_least(c);
-      if (cnt >= want) {
-        t = c;
-        above = cnt;
-        if (cnt == want) break;
-      }
+  int have = allowed;
+  if (want == forced) {
+    t = kForced;
+    have = forced;
+  } else if (want < allowed) {
+    t = least;
+    uint32_t hi = top + 1u;
+    int over = forced;
+    bool halve = false;
+    while (have != want && hi - t > 1u) {
+      const float share = halve ? 0.5f : ((float)(have - want) + 0.5f) / (float)(have - over);
+      const uint32_t step = (uint32_t)((float)(hi - t) * share);
+      const uint32_t c = t + min(max(step, 1u), hi - t - 1u);
+      int cnt = 0;
+      keys.each(n, [&](uint32_t x) { cnt += x >= c ? 1 : 0; });
+      cnt = __reduce_add_sync(0xFFFFFFFFu, cnt);
+      if (cnt >= want)
+        t = c, have = cnt;
+      else
+        hi = c, over = cnt;
+      halve = !halve;
     }
   }
-  // keys > t all go in, and of those equal to t the first ones
-  int ties = want - (above == want ? 0 : keys.count_at_least(t + 1u));
-  if (above == want) ties = want;  // every key >= t: no border to settle
-  const bool all = above == want;
-  for (int i0 = 0; i0 < nk; i0 += 32) {
-    const int i = i0 + lane;
-    const uint32_t key = i < n ? row[i] : kRuledOut;
-    const bool eq = key == t && !all;
-    const unsigned eqs = __ballot_sync(0xFFFFFFFFu, eq);
-    const bool take = (all ? key >= t : key > t) || (eq && __popc(eqs & ((1u << lane) - 1u)) < ties);
-    ties -= __popc(eqs);
-    if (i < nk) out[i] = take && key != kRuledOut ? 1 : 0;
+  // more keys >= t than wanted: those equal to t go in from the left
+  int drop_from = 0x7FFFFFFF;  // column from which keys equal to t stay out
+  if (have != want) {
+    int above = 0;
+    keys.each(n, [&](uint32_t x) { above += x > t ? 1 : 0; });
+    int ties = want - __reduce_add_sync(0xFFFFFFFFu, above);  // >= 1
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      const unsigned eq = __ballot_sync(0xFFFFFFFFu, i0 + lane < n && row[i0 + lane] == t);
+      if (__popc(eq) >= ties) {
+        drop_from = i0 + __fns(eq, 0, ties) + 1;
+        break;
+      }
+      ties -= __popc(eq);
+    }
+  }
+  if (((nk | (int)reinterpret_cast<uintptr_t>(out)) & 3) == 0) {
+    for (int i = 0; i * 128 + lane * 4 < nk; ++i) {
+      const uint4 v = keys.piece(i, n);
+      const int col = i * 128 + lane * 4;
+      auto in = [&](uint32_t x, int at) {
+        return (x > t || (x == t && at < drop_from)) && at < n ? 1u : 0u;
+      };
+      *reinterpret_cast<uint32_t*>(out + col) = in(v.x, col) | in(v.y, col + 1) << 8 |
+                                                in(v.z, col + 2) << 16 | in(v.w, col + 3) << 24;
+    }
+  } else {
+    for (int i = lane; i < nk; i += 32) {
+      const uint32_t x = i < n ? row[i] : kRuledOut;
+      out[i] = x > t || (x == t && i < drop_from) ? 1 : 0;
+    }
   }
 }
 
 // One CTA: `rows` query blocks of one head.  Each warp scores 8 key blocks at
 // a time against all of them, then takes rows for the choice.
 template <int D>
-__global__ void __launch_bounds__(kSelThreads) choose_blocks_kernel(const SelectParams p) {
-  extern __shared__ uint32_t keys[];  // [rows][nk]
+__global__ void __launch_bounds__(kSelThreads, 4) choose_blocks_kernel(const SelectParams p) {
+  extern __shared__ __align__(16) uint32_t keys[];  // [rows][stride]
   constexpr int C = D / 32;           // 16-byte pieces a lane holds of a row
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int h = blockIdx.y, b = blockIdx.z;
-  const int q0 = blockIdx.x * p.rows;
+  // the rows with the most key blocks in reach first
+  const int q0 = (gridDim.x - 1 - blockIdx.x) * p.rows;
   const int rows = min(p.rows, p.nb - q0);
+  const int stride = (p.nk + 3) & ~3;
   const int g = lane >> 2, j = lane & 3;
   // key blocks that the tile's last row can reach
   const int reach = p.causal ? min(p.nk, (q0 + rows) * p.kdiv) : p.nk;
@@ -198,7 +260,7 @@ __global__ void __launch_bounds__(kSelThreads) choose_blocks_kernel(const Select
         bool ok = !p.causal || k128 <= q128;
         if (allow) ok = ok && allow[(int64_t)r * p.nk + col] != 0;
         const bool must = col < p.sink || abs(k128 - q128) < p.local;
-        keys[r * p.nk + col] = !ok ? kRuledOut : must ? kForced : ordered_bits(acc[i]);
+        keys[r * stride + col] = !ok ? kRuledOut : must ? kForced : ordered_bits(acc[i]);
       }
     }
   }
@@ -206,9 +268,13 @@ __global__ void __launch_bounds__(kSelThreads) choose_blocks_kernel(const Select
   for (int r = warp; r < rows; r += kSelWarps) {
     const int n = p.causal ? min(p.nk, (q0 + r + 1) * p.kdiv) : p.nk;
     uint8_t* out = p.mask + (((int64_t)b * p.H + h) * p.nb + q0 + r) * p.nk;
-    const uint32_t* row = keys + r * p.nk;
+    uint32_t* row = keys + r * stride;
+    if (lane < ((4 - (n & 3)) & 3)) row[n + lane] = kRuledOut;  // to a whole piece of four
+    __syncwarp();
     if (n <= 128)
       choose_row<4>(row, n, p.nk, p.keep, out, lane);
+    else if (n <= 256)
+      choose_row<8>(row, n, p.nk, p.keep, out, lane);
     else if (n <= 512)
       choose_row<16>(row, n, p.nk, p.keep, out, lane);
     else
@@ -219,23 +285,22 @@ __global__ void __launch_bounds__(kSelThreads) choose_blocks_kernel(const Select
 // 16 query blocks a CTA (the tensor instruction's rows) while their keys fit
 // 128 KB of shared memory, 4 above (4 rows of at most 8192 keys).
 constexpr int kSelKeyBytes = 128 << 10;
-int select_rows(int nk) { return 16 * nk * 4 <= kSelKeyBytes ? 16 : 4; }
+int select_rows(int nk) { return 16 * ((nk + 3) & ~3) * 4 <= kSelKeyBytes ? 16 : 4; }
 
 template <int D>
 cudaError_t launch_select(const void* q, const void* k, int q_blocks, int k_blocks, int key_block,
                           uint16_t* mq, uint16_t* mk, const SelectParams& p, int B,
                           cudaStream_t st) {
-  const size_t smem = (size_t)p.rows * p.nk * sizeof(uint32_t);
+  const size_t smem = (size_t)p.rows * ((p.nk + 3) & ~3) * sizeof(uint32_t);
   cudaError_t e = cudaSuccess;
   if (smem > (48 << 10)) {
     e = cudaFuncSetAttribute(choose_blocks_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kSelKeyBytes);
     if (e != cudaSuccess) return e;
   }
-  block_mean_kernel<D><<<q_blocks + k_blocks, kPoolThreads, 0, st>>>(
-      static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k), q_blocks, key_block, mq,
-      mk);
-  e = cudaGetLastError();
+  e = launch_dependent(block_mean_kernel<D>, dim3(q_blocks + k_blocks), dim3(kPoolThreads),
+                       (size_t)kBlock * D * 2, st, static_cast<const uint16_t*>(q),
+                       static_cast<const uint16_t*>(k), q_blocks, key_block, mq, mk);
   if (e != cudaSuccess) return e;
   return launch_dependent(choose_blocks_kernel<D>, dim3((p.nb + p.rows - 1) / p.rows, p.H, B),
                           dim3(kSelThreads), smem, st, p);

@@ -19,7 +19,10 @@ namespace bsattn {
 namespace {
 
 constexpr int kRowThreads = 128;  // write_rounded_mean takes a CTA of 128
-constexpr int kReadRows = 4;      // rows a lane group reads back at once
+#ifndef RDR
+#define RDR 2
+#endif
+constexpr int kReadRows = RDR;      // rows a lane group reads back at once
 constexpr float kLeastStep = 7.888609e-31f;  // 2^-100
 
 struct AppendParams {
@@ -131,15 +134,16 @@ struct Decoder {
   }
 };
 
-// One CTA: one page of one sequence and head, the tokens of this call that
-// fall into it, K then V.  A row is held by D / 16 lanes, and the next row's
-// load is in flight while one is quantised.  When the call fills the page the
-// CTA adds up the page's decoded keys (those of earlier calls are read back)
-// and writes their rounded mean.
+// One CTA: K or V of one page of one sequence and head, the tokens of this call
+// that fall into it.  A row is held by D / 16 lanes, and the next row's load is
+// in flight while one is quantised.  When the call fills the page the CTA of K
+// adds up the page's decoded keys (those of earlier calls are read back) and
+// writes their rounded mean.
 template <int D, int GL>
-__global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kRowThreads, 6) kv4_append_kernel(const AppendParams p) {
   constexpr int L = D / 16, NG = L / GL, kRows = kRowThreads / L;  // rows the CTA holds at once
-  const int h = blockIdx.y, b = blockIdx.z;
+  const bool is_k = blockIdx.y < p.c.Hkv;
+  const int h = is_k ? blockIdx.y : blockIdx.y - p.c.Hkv, b = blockIdx.z;
   wait_for_previous_launch();
   allow_next_launch();
   const int len = __ldg(p.lengths + b);
@@ -154,64 +158,61 @@ __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const AppendPar
   const int64_t end = min((int64_t)len + cnt, (logical + 1) << p.c.log_page);
   const int64_t begin = max((int64_t)len, logical << p.c.log_page);
   if (begin >= end) return;
+  const int n = (int)(end - begin), place0 = (int)(begin & (p.c.page - 1));
+  const int sub = threadIdx.x / L, cl = threadIdx.x % L;
+  // the first row is on its way while the table is asked
+  const int64_t token = is_k ? p.kt : p.vt;
+  const uint16_t* src = (is_k ? p.k + b * p.kb + h * p.kh : p.v + b * p.vb + h * p.vh) +
+                        (begin - len + sub) * token + cl * 16;
+  uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+  if (sub < n) {
+    lo = __ldg(reinterpret_cast<const uint4*>(src));
+    hi = __ldg(reinterpret_cast<const uint4*>(src) + 1);
+  }
   const int pg = page_at(p.c, p.table + b * p.table_stride, p.columns, logical);
   if (pg < 0) return;
-  const bool fills = end == (logical + 1) << p.c.log_page;
-  const int n = (int)(end - begin), place0 = (int)(begin & (p.c.page - 1));
-  const int t0 = (int)(begin - len);
-  const int sub = threadIdx.x / L, cl = threadIdx.x % L;
+  const bool sums = is_k && end == (logical + 1) << p.c.log_page;
   const int64_t row0 = p.c.row(pg, h, 0);
 
   Sum2x2 s[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) s[i].hi = s[i].lo = f2(0.0f);
   const int rounds = (n + kRows - 1) / kRows;
-#pragma unroll
-  for (int kv = 0; kv < 2; ++kv) {
-    const int64_t stride = kv ? p.vt : p.kt;
-    const uint16_t* src = (kv ? p.v + b * p.vb + h * p.vh : p.k + b * p.kb + h * p.kh) +
-                          (t0 + sub) * stride + cl * 16;
-    const int64_t row = row0 + place0 + sub;
-    uint2* codes = reinterpret_cast<uint2*>(kv ? p.c.v_codes : p.c.k_codes) + row * L + cl;
-    uint32_t* scales =
-        reinterpret_cast<uint32_t*>(kv ? p.c.v_scales : p.c.k_scales) + row * NG + cl / GL;
-    uint4 a = make_uint4(0, 0, 0, 0), c = a;
-    if (sub < n) {
-      a = __ldg(reinterpret_cast<const uint4*>(src));
-      c = __ldg(reinterpret_cast<const uint4*>(src) + 1);
+  const int64_t row = row0 + place0 + sub;
+  uint2* codes = reinterpret_cast<uint2*>(is_k ? p.c.k_codes : p.c.v_codes) + row * L + cl;
+  uint32_t* scales =
+      reinterpret_cast<uint32_t*>(is_k ? p.c.k_scales : p.c.v_scales) + row * NG + cl / GL;
+  for (int i = 0; i < rounds; ++i) {  // (as many for every lane: shuffles)
+    const bool there = i * kRows + sub < n;
+    const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    src += kRows * token;
+    if ((i + 1) * kRows + sub < n) {
+      lo = __ldg(reinterpret_cast<const uint4*>(src));
+      hi = __ldg(reinterpret_cast<const uint4*>(src) + 1);
     }
-    for (int i = 0; i < rounds; ++i) {  // (as many for every lane: shuffles)
-      const bool there = i * kRows + sub < n;
-      const uint32_t w[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
-      src += kRows * stride;
-      if ((i + 1) * kRows + sub < n) {
-        a = __ldg(reinterpret_cast<const uint4*>(src));
-        c = __ldg(reinterpret_cast<const uint4*>(src) + 1);
-      }
-      F2 x[8];
-      float step, least;
-      const uint2 packed = quantise<GL>(w, x, step, least);
-      if (there) {
-        *codes = packed;
-        if (cl % GL == 0) *scales = pack_bf16(step, least);
-        if (kv == 0 && fills) {
+    F2 x[8];
+    float step, least;
+    const uint2 packed = quantise<GL>(w, x, step, least);
+    if (there) {
+      *codes = packed;
+      if (cl % GL == 0) *scales = pack_bf16(step, least);
+      if (sums) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) add_exact(s[k], fma2(x[k], f2(step), f2(least)));
-        }
+        for (int k = 0; k < 8; ++k) add_exact(s[k], fma2(x[k], f2(step), f2(least)));
       }
-      codes += kRows * L;
-      scales += kRows * NG;
     }
+    codes += kRows * L;
+    scales += kRows * NG;
   }
-  if (!fills) return;
+  if (!sums) return;
   for (int r = sub; r < place0; r += kRows) {
-    const int64_t row = row0 + r;
-    const uint2 codes = reinterpret_cast<const uint2*>(p.c.k_codes)[row * L + cl];
-    const uint32_t sc = reinterpret_cast<const uint32_t*>(p.c.k_scales)[row * NG + cl / GL];
+    const int64_t at = row0 + r;
+    const uint2 packed = reinterpret_cast<const uint2*>(p.c.k_codes)[at * L + cl];
+    const uint32_t sc = reinterpret_cast<const uint32_t*>(p.c.k_scales)[at * NG + cl / GL];
     const Decoder dec(bf16_lo(sc), bf16_hi(sc));
     F2 x[8];
-    dec.decode8(codes.x, x);
-    dec.decode8(codes.y, x + 4);
+    dec.decode8(packed.x, x);
+    dec.decode8(packed.y, x + 4);
 #pragma unroll
     for (int k = 0; k < 8; ++k) add_exact(s[k], x[k]);
   }
@@ -287,10 +288,20 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const ReadParams 
 // of t . mean over those queries: a whole number times the page's power of
 // two, exact in 32 bits.  The last `recent` pages and the first `sink` are
 // always taken; of the others the best, the lowest index first among equals.
+//
+// Bound: memory, one row of D bf16 a page, or latency where there are few.  One
+// CTA scores a head's pages and chooses among them while that keeps the
+// machine busy or the list is short; else scores and choice are two launches.
 // ---------------------------------------------------------------------------
-constexpr int kScoreThreads = 256;
-constexpr int kScorePages = 64;  // a CTA: 8 warps, 8 pages each
+constexpr int kPageThreads = 512;
+constexpr int kPageWarps = kPageThreads / 32;
+constexpr int kChooseThreads = 128;
+constexpr int kChooseWarps = kChooseThreads / 32;
+constexpr int kAtOnce = 4;       // groups of 8 pages that a warp has in flight
 constexpr int kMostRows = 128;   // G * T
+constexpr int kSplitPages = kPageWarps * kAtOnce * 8;  // a CTA of the split form scores
+constexpr int kOneCtaPages = 2048;  // one CTA reads 512 KB of means in about 8 us
+constexpr int kMostShared = 8192;   // keys in shared memory
 constexpr uint32_t kForcedPage = 0xFFFFFFFFu;
 constexpr uint32_t kNoPage = 0u;
 
@@ -303,100 +314,158 @@ struct PagesParams {
   const int* lengths;
   int rows;  // G * T
   int keep, sink, recent;
-  uint32_t* keys;  // [B * Hkv][columns]
+  uint32_t* keys;  // [B * Hkv][columns] (the split form)
   int* out;        // [B * Hkv][keep]
 };
 
 __device__ __forceinline__ int pages_of(const PagesParams& p, int b) {
-  const int64_t n = ((int64_t)max(p.lengths[b], 0) + p.c.page - 1) >> p.c.log_page;
+  const int64_t n = ((int64_t)max(__ldg(p.lengths + b), 0) + p.c.page - 1) >> p.c.log_page;
   return (int)min(n, (int64_t)p.columns);
 }
 
+// Rounds the queries of (sequence, head) bh into `whole` ([16 tiles][D] bf16,
+// zero rows at the end).  All threads of the CTA.
 template <int D>
-__global__ void __launch_bounds__(kScoreThreads) page_scores_kernel(const PagesParams p) {
-  constexpr int C = D / 32;
-  __shared__ __align__(16) uint16_t whole[kMostRows * D];
-  __shared__ int top[kScoreThreads / 32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int h = blockIdx.y, b = blockIdx.z;
-  wait_for_previous_launch();
-  allow_next_launch();
-  const int n = pages_of(p, b);
-  const int first = blockIdx.x * kScorePages;
-  if (first >= n) return;
-  const int tiles = (p.rows + 15) / 16;
-  const int64_t bh = (int64_t)b * p.c.Hkv + h;
-  const uint16_t* q = p.q + bh * p.rows * D;
-
-  int e = kNoExponent;
-  for (int i = threadIdx.x; i < p.rows * D; i += kScoreThreads)
-    e = max(e, exponent_of(Sum2{__uint_as_float((uint32_t)__ldg(q + i) << 16), 0.0f}));
-  e = __reduce_max_sync(0xFFFFFFFFu, e);
-  if (lane == 0) top[warp] = e;
-  __syncthreads();
+__device__ __forceinline__ void round_queries(const PagesParams& p, int64_t bh, uint16_t* whole) {
+  constexpr int kVec = kMostRows * 128 / 8 / kPageThreads;  // 16-byte pieces a thread, at most
+  __shared__ uint32_t top[kPageWarps];
+  const uint4* q = reinterpret_cast<const uint4*>(p.q + bh * p.rows * D);
+  const int pieces = p.rows * D / 8, room = (p.rows + 15) / 16 * 16 * D / 8;
+  uint4 v[kVec];
+  uint32_t most = 0;  // bits of the largest finite |q|
 #pragma unroll
-  for (int w = 0; w < kScoreThreads / 32; ++w) e = max(e, top[w]);
-  for (int i = threadIdx.x; i < tiles * 16 * D; i += kScoreThreads) {
-    float t = 0.0f;
-    if (i < p.rows * D && e != kNoExponent)
-      t = rint_scaled(Sum2{__uint_as_float((uint32_t)__ldg(q + i) << 16), 0.0f}, 6 - e);
-    whole[i] = (uint16_t)(__float_as_uint(t) >> 16);
-  }
-  __syncthreads();
-
-  const int g = lane >> 2, j = lane & 3;
-  const int my_page = first + warp * 8 + g;
-  int pg = -1;
-  if (my_page < n) pg = page_at(p.c, p.table + b * p.table_stride, p.columns, my_page);
-  uint4 w[C];
+  for (int i = 0; i < kVec; ++i) {
+    const int at = threadIdx.x + i * kPageThreads;
+    v[i] = make_uint4(0, 0, 0, 0);
+    if (at >= pieces) continue;
+    v[i] = __ldg(q + at);
+    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
-  for (int c = 0; c < C; ++c)
-    w[c] = pg < 0 ? make_uint4(0, 0, 0, 0)
-                  : reinterpret_cast<const uint4*>(
-                        p.c.k_means + ((int64_t)pg * p.c.Hkv + h) * D)[4 * c + j];
-  float best[2] = {-INFINITY, -INFINITY};  // of pages 2j and 2j + 1, over the rows
-  for (int m = 0; m < tiles; ++m) {
-    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    const uint4* a = reinterpret_cast<const uint4*>(whole + (m * 16 + g) * D);
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const uint4 lo = a[4 * c + j], hi = a[D + 4 * c + j];  // row g + 8: 8 * D / 8 pieces on
-      const uint32_t a0[4] = {lo.x, hi.x, lo.y, hi.y};
-      const uint32_t a1[4] = {lo.z, hi.z, lo.w, hi.w};
-      mma_bf16(acc, a0, w[c].x, w[c].y);
-      mma_bf16(acc, a1, w[c].z, w[c].w);
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t lo = w[k] & 0x7FFFu, hi = (w[k] >> 16) & 0x7FFFu;
+      most = max(most, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
     }
+  }
+  most = __reduce_max_sync(0xFFFFFFFFu, most);
+  if ((threadIdx.x & 31) == 0) top[threadIdx.x >> 5] = most;
+  __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (m * 16 + g + 8 * (i >> 1) < p.rows) best[i & 1] = fmaxf(best[i & 1], acc[i]);
-  }
+  for (int w = 0; w < kPageWarps; ++w) most = max(most, top[w]);
+  // t = rint(q 2^(6 - e)), in two factors, for 2^(6 - e) may pass fp32's range
+  const int shift = most ? 6 - ilogbf(__uint_as_float(most << 16)) : 0;
+  const float f1 = ldexpf(1.0f, shift / 2), f2 = ldexpf(1.0f, shift - shift / 2);
+  auto round1 = [&](float x) { return fabsf(x) <= 3.4e38f ? rintf(x * f1 * f2) : 0.0f; };
+  auto round2 = [&](uint32_t w) { return pack_bf16(round1(bf16_lo(w)), round1(bf16_hi(w))); };
 #pragma unroll
-  for (int o = 4; o < 32; o <<= 1) {
-    best[0] = fmaxf(best[0], __shfl_xor_sync(0xFFFFFFFFu, best[0], o));
-    best[1] = fmaxf(best[1], __shfl_xor_sync(0xFFFFFFFFu, best[1], o));
+  for (int i = 0; i < kVec; ++i) {
+    const int at = threadIdx.x + i * kPageThreads;
+    if (at < room)
+      reinterpret_cast<uint4*>(whole)[at] =
+          make_uint4(round2(v[i].x), round2(v[i].y), round2(v[i].z), round2(v[i].w));
   }
-  // lane (g, j) writes page g: its score sits in lanes with j = g / 2
-  const float lo = __shfl_sync(0xFFFFFFFFu, best[0], g >> 1);
-  const float hi = __shfl_sync(0xFFFFFFFFu, best[1], g >> 1);
-  if (j == 0 && my_page < n) {
-    const bool forced = my_page < p.sink || my_page >= n - p.recent;
-    p.keys[bh * p.columns + my_page] =
-        pg < 0 ? kNoPage : forced ? kForcedPage : ordered_bits(g & 1 ? hi : lo);
-  }
+  __syncthreads();
 }
 
-// Sum over the CTA of one number a thread (two uses in a row need other slots).
+// Scores pages first .. end - 1 of a sequence with n pages into keys[page -
+// offset]: each warp 8 pages a tensor tile, kAtOnce tiles at once.  The loads of
+// a round are issued before `whole` is needed (it may be filled in between).
+template <int D, typename Ready>
+__device__ __forceinline__ void score_pages(const PagesParams& p, int b, int h, int n, int first,
+                                            int end, const uint16_t* whole, uint32_t* keys,
+                                            Ready ready) {
+  constexpr int C = D / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, j = lane & 3;
+  const int tiles = (p.rows + 15) / 16;
+  const int* table = p.table + b * p.table_stride;
+  bool waiting = true;
+  for (int base = first; base < end; base += kPageWarps * kAtOnce * 8) {
+    const int at = base + warp * (kAtOnce * 8) + g;
+    int pg[kAtOnce];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      pg[k] = -1;
+      if (at + 8 * k < end) pg[k] = __ldg(table + at + 8 * k);
+    }
+    uint4 w[kAtOnce][C];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const bool there = pg[k] >= 0 && pg[k] < p.c.pages;
+      if (!there && at + 8 * k < end) p.c.report();
+      if (!there) pg[k] = -1;
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        w[k][c] = there ? reinterpret_cast<const uint4*>(
+                              p.c.k_means + ((int64_t)pg[k] * p.c.Hkv + h) * D)[4 * c + j]
+                        : make_uint4(0, 0, 0, 0);
+    }
+    if (waiting) ready();
+    waiting = false;
+    float best[kAtOnce][2];  // of pages 2j and 2j + 1, over the rows
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) best[k][0] = best[k][1] = -INFINITY;
+    for (int m = 0; m < tiles; ++m) {
+      const uint4* row = reinterpret_cast<const uint4*>(whole + (m * 16 + g) * D);
+      float acc[kAtOnce][4];
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[k][i] = 0.0f;
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const uint4 lo = row[4 * c + j], hi = row[D + 4 * c + j];  // rows g, g + 8
+        const uint32_t a0[4] = {lo.x, hi.x, lo.y, hi.y};
+        const uint32_t a1[4] = {lo.z, hi.z, lo.w, hi.w};
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+          mma_bf16(acc[k], a0, w[k][c].x, w[k][c].y);
+          mma_bf16(acc[k], a1, w[k][c].z, w[k][c].w);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (m * 16 + g + 8 * (i >> 1) < p.rows) {
+#pragma unroll
+          for (int k = 0; k < kAtOnce; ++k) best[k][i & 1] = fmaxf(best[k][i & 1], acc[k][i]);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) {
+        best[k][0] = fmaxf(best[k][0], __shfl_xor_sync(0xFFFFFFFFu, best[k][0], o));
+        best[k][1] = fmaxf(best[k][1], __shfl_xor_sync(0xFFFFFFFFu, best[k][1], o));
+      }
+      // lane (g, 0) writes page g: its score sits in lanes with j = g / 2
+      const float lo = __shfl_sync(0xFFFFFFFFu, best[k][0], g >> 1);
+      const float hi = __shfl_sync(0xFFFFFFFFu, best[k][1], g >> 1);
+      const int page = at + 8 * k;
+      if (j == 0 && page < end) {
+        const bool forced = page < p.sink || page >= n - p.recent;
+        keys[page] = pg[k] < 0 ? kNoPage : forced ? kForcedPage : ordered_bits(g & 1 ? hi : lo);
+      }
+    }
+  }
+  if (waiting) ready();
+}
+
+// Barrier of the threads that choose (the first kChooseThreads of the CTA).
+__device__ __forceinline__ void choose_barrier() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kChooseThreads) : "memory");
+}
+
+// Sum over those threads of one number each (two uses in a row need other slots).
 __device__ __forceinline__ int block_sum(int v, int* slots) {
   v = __reduce_add_sync(0xFFFFFFFFu, v);
   if ((threadIdx.x & 31) == 0) slots[threadIdx.x >> 5] = v;
-  __syncthreads();
+  choose_barrier();
   int s = 0;
 #pragma unroll
-  for (int w = 0; w < kScoreThreads / 32; ++w) s += slots[w];
+  for (int w = 0; w < kChooseWarps; ++w) s += slots[w];
   return s;
 }
 
-// Exclusive prefix over the CTA's threads.
+// Exclusive prefix over them.
 __device__ __forceinline__ int block_prefix(int v, int* slots) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int s = v;
@@ -406,70 +475,112 @@ __device__ __forceinline__ int block_prefix(int v, int* slots) {
     if (lane >= o) s += t;
   }
   if (lane == 31) slots[warp] = s;
-  __syncthreads();
+  choose_barrier();
   int before = 0;
-  for (int w = 0; w < warp; ++w) before += slots[w];
+#pragma unroll
+  for (int w = 0; w < kChooseWarps; ++w) before += w < warp ? slots[w] : 0;
   return before + s - v;
 }
 
-// One CTA per (sequence, head): thread i holds KP consecutive keys (KP = 0:
-// reads them again each time, for more pages than registers hold).
-template <int KP>
+// The best of n keys, by the first kChooseThreads threads of the CTA of one
+// (sequence, head): thread i holds KP consecutive keys (KP = 0: reads them again
+// each time, for more pages than registers hold).  The threshold is searched
+// as in select.cu.  (Four warps: each step of the search is a barrier.)
+template <int KP, bool SHARED>
 __device__ __forceinline__ void choose_pages(const PagesParams& p, const uint32_t* keys, int n,
-                                             int* out, int (*slots)[kScoreThreads / 32]) {
-  const int per = KP > 0 ? KP : (n + kScoreThreads - 1) / kScoreThreads;
+                                             int* out) {
+  __shared__ int slots[4][kChooseWarps];
+  __shared__ uint32_t ends[2][kChooseWarps];
+  const int per = KP > 0 ? KP : (n + kChooseThreads - 1) / kChooseThreads;
   const int64_t base = (int64_t)threadIdx.x * per;
   uint32_t k[KP > 0 ? KP : 1];
   if (KP > 0) {
 #pragma unroll
-    for (int i = 0; i < KP; ++i) k[i] = base + i < n ? __ldcg(keys + base + i) : kNoPage;
+    for (int i = 0; i < KP; ++i)
+      k[i] = base + i < n ? (SHARED ? keys[base + i] : __ldcg(keys + base + i)) : kNoPage;
   }
   auto key = [&](int i) -> uint32_t {
     if (KP > 0) return k[i];
     return base + i < n ? __ldcg(keys + base + i) : kNoPage;
   };
-  int turn = 0;
-  auto at_least = [&](uint32_t t) {
-    int c = 0;
+  auto each = [&](auto f) {
     if (KP > 0) {
 #pragma unroll
-      for (int i = 0; i < KP; ++i) c += k[i] >= t ? 1 : 0;
+      for (int i = 0; i < KP; ++i) f(k[i]);
     } else {
-      for (int i = 0; i < per; ++i) c += key(i) >= t ? 1 : 0;
+      for (int i = 0; i < per; ++i) f(key(i));
     }
+  };
+  int turn = 0;
+  auto total = [&](int c) {
     turn ^= 1;
     return block_sum(c, slots[turn]);
   };
-  const int there = at_least(1u);
+  // largest and least of the keys that are neither forced nor ruled out
+  uint32_t top = 0, least = kForcedPage;
+  int c = 0, f = 0;
+  each([&](uint32_t x) {
+    c += x != kNoPage ? 1 : 0;
+    f += x == kForcedPage ? 1 : 0;
+    top = max(top, x == kForcedPage ? 0u : x);
+    least = min(least, x - 1u);  // 0 wraps: never the least
+  });
+  top = __reduce_max_sync(0xFFFFFFFFu, top);
+  least = __reduce_min_sync(0xFFFFFFFFu, least);
+  if ((threadIdx.x & 31) == 0) {
+    ends[0][threadIdx.x >> 5] = top;
+    ends[1][threadIdx.x >> 5] = least;
+  }
+  const int there = total(c), forced = total(f);
+#pragma unroll
+  for (int w = 0; w < kChooseWarps; ++w) {
+    top = max(top, ends[0][w]);
+    least = min(least, ends[1][w]);
+  }
   const int want = min(p.keep, there);
   uint32_t t = 1u;
   int have = there;
-  if (want < there) {
-    t = 0u;
-    for (int bit = 31; bit >= 0; --bit) {
-      const uint32_t c = t | (1u << bit);
-      const int cnt = at_least(c);
-      if (cnt >= want) {
-        t = c;
-        have = cnt;
-        if (cnt == want) break;
+  if (want == forced) {
+    t = kForcedPage;
+    have = forced;
+  } else if (want < there) {
+    t = least + 1u;
+    uint32_t hi = top + 1u;
+    int over = forced;
+    for (int step = 0; have != want && hi - t > 1u; ++step) {
+      uint32_t m = t + (hi - t) / 2u;
+      if (step < 8 || (step & 1)) {
+        const float low = from_ordered_bits(t), high = from_ordered_bits(hi - 1u);
+        const float share = ((float)(have - want) + 0.5f) / (float)(have - over);
+        m = ordered_bits(fmaf(high - low, share, low));
       }
+      m = min(max(m, t + 1u), hi - 1u);
+      int cnt = 0;
+      each([&](uint32_t x) { cnt += x >= m ? 1 : 0; });
+      cnt = total(cnt);
+      if (cnt >= want)
+        t = m, have = cnt;
+      else
+        hi = m, over = cnt;
     }
   }
   // all of those above t, and the first of those equal to it
   const bool all = have == want;
   int above = 0, equal = 0;
-  for (int i = 0; i < per; ++i) {
-    const uint32_t x = key(i);
+  each([&](uint32_t x) {
     above += (all ? x >= t : x > t) ? 1 : 0;
     equal += (!all && x == t) ? 1 : 0;
-  }
+  });
   const int before = block_prefix(above, slots[2]);
-  const int equal_before = block_prefix(equal, slots[3]);
-  turn ^= 1;
-  const int ties = all ? 0 : want - block_sum(above, slots[turn]);
-  int taken = min(equal_before, ties), pos = before + taken;
-  for (int i = 0; i < per; ++i) {
+  int taken = 0, ties = 0;
+  if (!all) {
+    const int equal_before = block_prefix(equal, slots[3]);
+    ties = want - total(above);
+    taken = min(equal_before, ties);
+  }
+  int pos = before + taken;
+#pragma unroll
+  for (int i = 0; i < (KP > 0 ? KP : per); ++i) {
     const uint32_t x = key(i);
     bool take = all ? x >= t : x > t;
     if (!all && x == t && taken < ties) {
@@ -478,23 +589,76 @@ __device__ __forceinline__ void choose_pages(const PagesParams& p, const uint32_
     }
     if (take) out[pos++] = (int)(base + i);
   }
-  for (int i = want + threadIdx.x; i < p.keep; i += kScoreThreads) out[i] = -1;
+  for (int i = want + threadIdx.x; i < p.keep; i += kChooseThreads) out[i] = -1;
 }
 
-__global__ void __launch_bounds__(kScoreThreads) choose_pages_kernel(const PagesParams p) {
-  __shared__ int slots[4][kScoreThreads / 32];
+template <bool SHARED>
+__device__ __forceinline__ void choose_pages(const PagesParams& p, const uint32_t* keys, int n,
+                                             int* out) {
+  if (n <= 4 * kChooseThreads)
+    choose_pages<4, SHARED>(p, keys, n, out);
+  else if (n <= 16 * kChooseThreads)
+    choose_pages<16, SHARED>(p, keys, n, out);
+  else
+    choose_pages<0, SHARED>(p, keys, n, out);
+}
+
+// The split form: scores of kSplitPages pages a CTA, then one CTA a head.
+template <int D>
+__global__ void __launch_bounds__(kPageThreads) page_scores_kernel(const PagesParams p) {
+  extern __shared__ __align__(16) uint16_t whole[];
+  wait_for_previous_launch();
+  allow_next_launch();
+  const int h = blockIdx.y, b = blockIdx.z;
+  const int n = pages_of(p, b), first = blockIdx.x * kSplitPages;
+  if (first >= n) return;
+  const int64_t bh = (int64_t)b * p.c.Hkv + h;
+  score_pages<D>(p, b, h, n, first, min(n, first + kSplitPages), whole, p.keys + bh * p.columns,
+                 [&] { round_queries<D>(p, bh, whole); });
+}
+
+__global__ void __launch_bounds__(kChooseThreads) choose_pages_kernel(const PagesParams p) {
   wait_for_previous_launch();
   allow_next_launch();
   const int64_t bh = blockIdx.x;
-  const int n = pages_of(p, (int)(bh / p.c.Hkv));
-  const uint32_t* keys = p.keys + bh * p.columns;
-  int* out = p.out + bh * p.keep;
-  if (n <= 4 * kScoreThreads)
-    choose_pages<4>(p, keys, n, out, slots);
-  else if (n <= 16 * kScoreThreads)
-    choose_pages<16>(p, keys, n, out, slots);
-  else
-    choose_pages<0>(p, keys, n, out, slots);
+  choose_pages<false>(p, p.keys + bh * p.columns, pages_of(p, (int)(bh / p.c.Hkv)),
+                      p.out + bh * p.keep);
+}
+
+// Both in one: a head a CTA, the keys in shared memory.
+template <int D>
+__global__ void __launch_bounds__(kPageThreads) select_pages_kernel(const PagesParams p) {
+  extern __shared__ __align__(16) uint16_t whole[];
+  wait_for_previous_launch();
+  allow_next_launch();
+  const int64_t bh = blockIdx.x;
+  const int b = (int)(bh / p.c.Hkv), h = (int)(bh - (int64_t)b * p.c.Hkv);
+  const int n = pages_of(p, b);
+  uint32_t* keys = reinterpret_cast<uint32_t*>(whole + (p.rows + 15) / 16 * 16 * D);
+  score_pages<D>(p, b, h, n, 0, n, whole, keys, [&] { round_queries<D>(p, bh, whole); });
+  __syncthreads();
+  if (threadIdx.x < kChooseThreads) choose_pages<true>(p, keys, n, p.out + bh * p.keep);
+}
+
+bool one_cta_a_head(int heads, int columns, int sms) {
+  return columns <= kOneCtaPages || (heads >= sms && columns <= kMostShared);
+}
+
+template <int D>
+cudaError_t launch_pages(const PagesParams& p, int B, int sms, cudaStream_t st) {
+  const size_t queries = (size_t)(p.rows + 15) / 16 * 16 * D * 2;
+  const int heads = B * p.c.Hkv;
+  if (one_cta_a_head(heads, p.columns, sms)) {
+    const size_t smem = queries + (size_t)p.columns * sizeof(uint32_t);
+    cudaError_t e = allow_shared_memory<select_pages_kernel<D>>(64 << 10);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(select_pages_kernel<D>, dim3(heads), dim3(kPageThreads), smem, st, p);
+  }
+  cudaError_t e = launch_dependent(
+      page_scores_kernel<D>, dim3((p.columns + kSplitPages - 1) / kSplitPages, p.c.Hkv, B),
+      dim3(kPageThreads), queries, st, p);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(choose_pages_kernel, dim3(heads), dim3(kChooseThreads), 0, st, p);
 }
 
 bool strides_ok(const int64_t (&s)[6]) {
@@ -531,7 +695,7 @@ bsattn_status check_cache(const bsattn_kv4_cache* c, Kv4View* view) {
   if (c->group > c->head_dim) return BSATTN_ERR_INVALID_ARG;
   const int ps = c->page_size;
   if (ps < 16 || ps > 256 || (ps & (ps - 1)) != 0) return BSATTN_ERR_UNSUPPORTED;
-  if (c->kv_heads > 65535) return BSATTN_ERR_UNSUPPORTED;
+  if (c->kv_heads > 32767) return BSATTN_ERR_UNSUPPORTED;
   view->k_codes = static_cast<uint8_t*>(c->k_codes);
   view->v_codes = static_cast<uint8_t*>(c->v_codes);
   view->k_scales = static_cast<uint16_t*>(c->k_scales);
@@ -582,7 +746,7 @@ bsattn_status bsattn_kv4_append(const bsattn_kv4_cache* cache, const void* k, in
   p.T = T;
   // T tokens touch at most this many pages
   const int touched = (T + cache->page_size - 2) / cache->page_size + 1;
-  const dim3 grid(touched, cache->kv_heads, B);
+  const dim3 grid(touched, 2 * cache->kv_heads, B);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
 #define BSATTN_CALL(D, GL) \
   e = launch_dependent(kv4_append_kernel<D, GL>, grid, dim3(kRowThreads), 0, st, p)
@@ -626,7 +790,11 @@ bsattn_status bsattn_kv4_read(const bsattn_kv4_cache* cache, int B, int T,
 
 size_t bsattn_kv4_select_workspace(int B, int kv_heads, int columns) {
   if (B <= 0 || kv_heads <= 0 || columns <= 0) return 0;
-  return (size_t)B * kv_heads * columns * sizeof(uint32_t);
+  const int64_t heads = (int64_t)B * kv_heads;
+  int dev = -1, sms = 1 << 30;
+  if (columns <= kMostShared && cudaGetDevice(&dev) == cudaSuccess) sms = device_sm_count(dev);
+  if (heads < (1ll << 31) && one_cta_a_head((int)heads, columns, sms)) return 0;
+  return (size_t)heads * columns * sizeof(uint32_t);
 }
 
 bsattn_status bsattn_kv4_select(const bsattn_kv4_cache* cache, const void* q, int B, int H, int T,
@@ -637,8 +805,7 @@ bsattn_status bsattn_kv4_select(const bsattn_kv4_cache* cache, const void* q, in
   PagesParams p{};
   const bsattn_status rc = check_cache(cache, &p.c);
   if (rc != BSATTN_OK) return rc;
-  if (!q || !aligned16(q) || !ints_ok(block_table) || !ints_ok(lengths) || !ints_ok(selected) ||
-      !ints_ok(workspace))
+  if (!q || !aligned16(q) || !ints_ok(block_table) || !ints_ok(lengths) || !ints_ok(selected))
     return BSATTN_ERR_INVALID_ARG;
   if (B <= 0 || H <= 0 || T <= 0 || columns <= 0 || table_stride < 0 || H % cache->kv_heads != 0)
     return BSATTN_ERR_INVALID_ARG;
@@ -646,7 +813,8 @@ bsattn_status bsattn_kv4_select(const bsattn_kv4_cache* cache, const void* q, in
   const int64_t rows = (int64_t)(H / cache->kv_heads) * T;
   if (rows > kMostRows || B > 65535 || (int64_t)B * cache->kv_heads >= (1ll << 31))
     return BSATTN_ERR_UNSUPPORTED;
-  if (workspace_bytes < bsattn_kv4_select_workspace(B, cache->kv_heads, columns))
+  const size_t need = bsattn_kv4_select_workspace(B, cache->kv_heads, columns);
+  if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need))
     return BSATTN_ERR_INVALID_ARG;
   p.q = static_cast<const uint16_t*>(q);
   p.table = block_table;
@@ -659,15 +827,12 @@ bsattn_status bsattn_kv4_select(const bsattn_kv4_cache* cache, const void* q, in
   p.recent = recent;
   p.keys = static_cast<uint32_t*>(workspace);
   p.out = selected;
-  const dim3 grid((columns + kScorePages - 1) / kScorePages, cache->kv_heads, B);
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return BSATTN_ERR_CUDA;
+  const int sms = device_sm_count(dev);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_dependent(
-      cache->head_dim == 64 ? page_scores_kernel<64> : page_scores_kernel<128>, grid,
-      dim3(kScoreThreads), 0, st, p);
-  if (e != cudaSuccess) return from_cuda(e);
-  e = launch_dependent(choose_pages_kernel, dim3(B * cache->kv_heads), dim3(kScoreThreads), 0, st,
-                       p);
-  return from_cuda(e);
+  return from_cuda(cache->head_dim == 64 ? launch_pages<64>(p, B, sms, st)
+                                         : launch_pages<128>(p, B, sms, st));
 }
 
 bsattn_status bsattn_kv4_status(const bsattn_kv4_cache* cache, void* stream) {

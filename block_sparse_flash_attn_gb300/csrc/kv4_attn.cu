@@ -47,16 +47,12 @@ constexpr int kAttnThreads = 256;
 constexpr int kAttnWarps = kAttnThreads / 32;
 constexpr int kTile = 16;                      // tokens a warp takes at once
 constexpr int kStep = kTile * kAttnWarps;      // tokens a CTA takes at once
-#ifndef ATTS
-#define ATTS 4
-#endif
-#ifndef ATTP
-#define ATTP 2
-#endif
-constexpr int kStages = ATTS;                     // tiles in a warp's ring
-constexpr int kPerSm = ATTP;  // CTAs an SM, 8 query rows
+constexpr int kStages = 4;                     // tiles in a warp's ring
+constexpr int kPerSm = 2;                      // CTAs an SM with up to 8 query rows
 constexpr int kMostSequences = 4096;
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 128;
+constexpr int kMostParts = 64;                 // CTAs that share a head, so that the join stays short
+constexpr int kSegmentSteps = 4;
 constexpr float kNoMax = -1e30f;               // running maximum before any score
 constexpr float kLag = 8.0f;                   // a score may pass the running maximum by 2^8
 
@@ -115,11 +111,14 @@ __device__ __forceinline__ float2 unpack_half(uint32_t x) {
 
 // Where each CTA's range of units begins.
 __device__ __forceinline__ int64_t range_begin(int64_t units, int ctas, int c) {
+  // (32-bit division where it does: a 64-bit one is some hundred instructions)
+  if (units < (1 << 20)) return (unsigned)units * (unsigned)c / (unsigned)ctas;
   return units * c / ctas;
 }
 // The CTA whose range holds unit u.
 __device__ __forceinline__ int range_of(int64_t units, int ctas, int64_t u) {
-  int c = (int)((u * ctas) / units);
+  int c = units < (1 << 20) ? (int)((unsigned)u * (unsigned)ctas / (unsigned)units)
+                            : (int)((u * ctas) / units);
   while (c + 1 < ctas && range_begin(units, ctas, c + 1) <= u) ++c;
   while (c > 0 && range_begin(units, ctas, c) > u) --c;
   return c;
@@ -149,13 +148,15 @@ __device__ __forceinline__ int tile_page(const AttnParams& p, int b, int h, int6
 }
 
 // One CTA: a range of units.  NG groups of channels share a step each, NT
-// tiles of 8 query rows.
-template <int D, int NG, int NT>
+// tiles of 8 query rows.  TWICE: up to 4 rows, each in two columns of the one
+// tile, of which the second carries the low halves of the weights: one product
+// for hi + lo instead of two.
+template <int D, int NG, int NT, bool TWICE>
 struct Attn {
   static constexpr int C = D / 32;        // 16-byte pieces (32 channels) of a row of codes
   static constexpr int CG = C / NG;       // pieces a group
   static constexpr int RB = D / 2;        // bytes of a row of codes
-  static constexpr int RP = 8 * NT;       // query rows a tile
+  static constexpr int RP = TWICE ? 4 : 8 * NT;  // query rows a tile
   static constexpr int kCodes = kTile * RB;
   static constexpr int kScales = kTile * NG * 4;
   static constexpr int kStage = 2 * kCodes + 2 * kScales;  // K, V codes, K, V scales
@@ -171,16 +172,16 @@ struct Attn {
   }
 };
 
-template <int D, int NG, int NT>
+template <int D, int NG, int NT, bool TWICE>
 __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
     kv4_attn_kernel(const AttnParams p) {
-  using A = Attn<D, NG, NT>;
+  using A = Attn<D, NG, NT, TWICE>;
   constexpr int C = A::C, RB = A::RB, RP = A::RP, KW = A::CG;
   constexpr bool kWide = D / NG >= 64;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int warp_sums[kAttnWarps];
   __shared__ uint4 queries[NT][C][32];        // operands of S^T = K Q^T, a lane's four words
-  __shared__ int2 tiles[kAttnWarps][4][32];  // (row / 16, position) of four batches of tiles
+  __shared__ int2 tiles[kAttnWarps][128];  // (row / 16, position) of four batches of tiles
   int* prefix = reinterpret_cast<int*>(smem + A::kSmem);  // [B + 1]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, j = lane & 3;
@@ -243,7 +244,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
   const uint32_t k_at = g * RB + (4 * KW * j & 15) + 16 * (A::swizzle(g) ^ (KW * j / 4));
   const uint32_t v_at = 2 * j * RB + 4 * (g & 3) + 16 * (A::swizzle(2 * j) ^ (kWide ? g >> 2 : 0));
   const uint32_t half = g < 4 ? 0x5410u : 0x7632u;
-  int2(*my_tiles)[32] = tiles[warp];
+  int2* my_tiles = tiles[warp];
   // this lane's pieces of a tile: codes (token, piece) = lane / C, lane % C, and
   // for D = 128 eight tokens on; one piece of the scales
   const uint32_t code_at = ring + lane / C * RB + 16 * ((lane % C) ^ A::swizzle(lane / C));
@@ -289,36 +290,37 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
       }
     };
     look_up(0);
+    uint32_t to = 0;  // the ring's place for the next copy
     auto issue = [&](int i) {
       if ((i & 31) == 0) {
-        my_tiles[(i >> 5) & 3][lane] = next_tile;
+        my_tiles[(i & 127) + lane] = next_tile;
         __syncwarp();
         look_up((i >> 5) + 1);
       }
-      const int row16 = my_tiles[(i >> 5) & 3][i & 31].x;
+      const int row16 = my_tiles[i & 127].x;
       if (row16 >= 0) {
-        const uint32_t stage = (i % kStages) * A::kStage;
         const uint8_t* kc = k_src + (int64_t)row16 * A::kCodes;
         const uint8_t* vc = v_src + (int64_t)row16 * A::kCodes;
-        copy16(code_at + stage, kc);
-        copy16(code_at + stage + A::kCodes, vc);
+        copy16(code_at + to, kc);
+        copy16(code_at + to + A::kCodes, vc);
         if (D == 128) {
-          copy16(code_at + stage + 8 * RB, kc + 512);
-          copy16(code_at + stage + A::kCodes + 8 * RB, vc + 512);
+          copy16(code_at + to + 8 * RB, kc + 512);
+          copy16(code_at + to + A::kCodes + 8 * RB, vc + 512);
         }
-        if (lane < 8 * NG) copy16(scale_at + stage, scale_src + (int64_t)row16 * A::kScales);
+        if (lane < 8 * NG) copy16(scale_at + to, scale_src + (int64_t)row16 * A::kScales);
       }
       copy_commit();
+      to = to == (kStages - 1) * A::kStage ? 0 : to + A::kStage;
     };
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < kStages - 1; ++i) issue(i);
 
     // ---- queries: operands, the factor of the code product, the group sums
-    float mul[NT][2], qs[NT][NG][2];
-    int lim[NT][2];  // last position that the row sees
+    F2 mul[NT], qs[NT][NG];  // of rows 2j, 2j + 1 of the accumulators
+    int lim[NT][2];          // last position that the row sees
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int r = row0 + nt * 8 + g;
+      const int r = row0 + nt * 8 + (TWICE ? g & 3 : g);
       float x[C][8], top = 0.0f, sum[NG];
 #pragma unroll
       for (int c = 0; c < C; ++c) {
@@ -353,29 +355,28 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
               pack_half(x[c][1] * f16, x[c][5] * f16), pack_half(x[c][3] * f16, x[c][7] * f16));
       }
       const float m = p.scale_log2 * ldexpf(1.0f, 24 - sh);
+      auto rows2 = [&](float v) {  // of rows 2j and 2j + 1, from the lanes that loaded them
+        return f2(__shfl_sync(0xFFFFFFFFu, v, 8 * j), __shfl_sync(0xFFFFFFFFu, v, 8 * j + 4));
+      };
+      mul[nt] = rows2(m);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {  // rows 2j, 2j + 1 of the accumulators
-        const int src = 8 * j + 4 * e;
-        mul[nt][e] = __shfl_sync(0xFFFFFFFFu, m, src);
+      for (int n = 0; n < NG; ++n) qs[nt][n] = rows2(sum[n] * p.scale_log2);
 #pragma unroll
-        for (int n = 0; n < NG; ++n)
-          qs[nt][n][e] = __shfl_sync(0xFFFFFFFFu, sum[n], src) * p.scale_log2;
-        const int rr = row0 + nt * 8 + 2 * j + e;
+      for (int e = 0; e < 2; ++e) {
+        const int rr = row0 + nt * 8 + (TWICE ? (2 * j + e) & 3 : 2 * j + e);
         lim[nt][e] = rr < p.rows ? len - p.T + rr % p.T : -1;
       }
     }
 
     __syncthreads();
-    float mx[NT][2], l[NT][2], vm[NT][NG][2], o[C][2][NT][4];
+    F2 mx[NT], l[NT], vm[NT][NG];  // -maximum, sum of weights, sum of weights * least
+    float o[C][2][NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
+      mx[nt] = f2(-kNoMax);
+      l[nt] = f2(0.0f);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        mx[nt][e] = kNoMax;
-        l[nt][e] = 0.0f;
-#pragma unroll
-        for (int n = 0; n < NG; ++n) vm[nt][n][e] = 0.0f;
-      }
+      for (int n = 0; n < NG; ++n) vm[nt][n] = f2(0.0f);
 #pragma unroll
       for (int c = 0; c < C; ++c)
 #pragma unroll
@@ -388,21 +389,19 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
     float top_step = 7.888609e-31f;  // 2^-100
     float inv_top = 1.2676506e30f;   // 2^100
 
+    uint32_t from = 0;  // the ring's place of the tile
+#pragma unroll 1
     for (int i = 0; i < n_tiles; ++i) {
       copy_wait<kStages - 2>();
       __syncwarp();
       issue(i + kStages - 1);
-      const int st = i % kStages;
-      const int pos = my_tiles[(i >> 5) & 3][i & 31].y;
+      const uint8_t* stage = my_ring + from;
+      from = from == (kStages - 1) * A::kStage ? 0 : from + A::kStage;
+      const int pos = my_tiles[i & 127].y;
       if (pos < 0) continue;
-      const uint8_t* stage = my_ring + st * A::kStage;
 
-      // ---- scores (base 2): tokens g and g + 8, rows 2j and 2j + 1
-      float s[NT][4];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[nt][e] = 0.0f;
+      // ---- scores (base 2): token g (t = 0) and g + 8, rows 2j and 2j + 1 as a pair
+      F2 s[NT][2];
 #pragma unroll
       for (int n = 0; n < NG; ++n) {
         float acc[NT][4], acc16[NT][4];  // (two chains of products, half as long)
@@ -429,51 +428,55 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
           }
         }
         const uint8_t* ks = stage + 2 * A::kCodes + (g * NG + n) * 4;
-        const uint32_t k0 = word(ks), k1 = word(ks + 8 * NG * 4);
+        const uint32_t k[2] = {word(ks), word(ks + 8 * NG * 4)};
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t sc = e < 2 ? k0 : k1;
-            s[nt][e] = fmaf((acc[nt][e] + acc16[nt][e]) * bf16_lo(sc), mul[nt][e & 1],
-                            fmaf(bf16_hi(sc), qs[nt][n][e & 1], s[nt][e]));
+          for (int t = 0; t < 2; ++t) {
+            const F2 dot = f2(acc[nt][2 * t], acc[nt][2 * t + 1]) +
+                           f2(acc16[nt][2 * t], acc16[nt][2 * t + 1]);
+            const F2 by_least = f2(bf16_hi(k[t])) * qs[nt][n];
+            s[nt][t] = fma2(dot, mul[nt] * f2(bf16_lo(k[t])),
+                            n == 0 ? by_least : by_least + s[nt][t]);
           }
       }
       // ---- V's steps and minima; what a row does not see weighs nothing
-      float vs[NG][NT][4], vl[NG][NT][4], most = 0.0f;
+      uint32_t v[NG][2];
+      float most = 0.0f;
 #pragma unroll
       for (int n = 0; n < NG; ++n) {
         const uint8_t* sc = stage + 2 * A::kCodes + A::kScales + (g * NG + n) * 4;
-        const uint32_t v0 = word(sc), v1 = word(sc + 8 * NG * 4);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            vs[n][nt][e] = bf16_lo(e < 2 ? v0 : v1);
-            vl[n][nt][e] = bf16_hi(e < 2 ? v0 : v1);
-          }
-        most = fmaxf(most, fmaxf(bf16_lo(v0), bf16_lo(v1)));
+        v[n][0] = word(sc);
+        v[n][1] = word(sc + 8 * NG * 4);
       }
+      uint32_t hidden = 0;  // bits 4 nt + 2 t + e
       if (pos > seen_by_all) {
-        most = 0.0f;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int t = 0; t < 2; ++t) {
+          bool any = false;
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (pos + g + (e < 2 ? 0 : 8) > lim[nt][e & 1]) {
-              s[nt][e] = -INFINITY;
+          for (int nt = 0; nt < NT; ++nt) {
+            float2 x = split(s[nt][t]);
+            const bool h0 = pos + g + 8 * t > lim[nt][0], h1 = pos + g + 8 * t > lim[nt][1];
+            if (h0) x.x = -INFINITY;
+            if (h1) x.y = -INFINITY;
+            s[nt][t] = f2(x.x, x.y);
+            hidden |= (h0 ? 1u : 0u) << (4 * nt + 2 * t) | (h1 ? 2u : 0u) << (4 * nt + 2 * t);
+            any = any || !h0 || !h1;
+          }
 #pragma unroll
-              for (int n = 0; n < NG; ++n) vs[n][nt][e] = vl[n][nt][e] = 0.0f;
-            } else {
-#pragma unroll
-              for (int n = 0; n < NG; ++n) most = fmaxf(most, vs[n][nt][e]);
-            }
+          for (int n = 0; n < NG; ++n)
+            if (!any) v[n][t] = 0u;
+        }
       }
+#pragma unroll
+      for (int n = 0; n < NG; ++n) most = fmaxf(most, fmaxf(bf16_lo(v[n][0]), bf16_lo(v[n][1])));
       float over = kNoMax;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) over = fmaxf(over, s[nt][e] - mx[nt][e & 1]);
+      for (int nt = 0; nt < NT; ++nt) {
+        const float2 a = split(s[nt][0] + mx[nt]), c = split(s[nt][1] + mx[nt]);
+        over = fmaxf(over, fmaxf(fmaxf(a.x, a.y), fmaxf(c.x, c.y)));
+      }
       // ---- rare: a score far above the running maximum, or a larger step
       if (__any_sync(0xFFFFFFFFu, over > kLag || most > top_step)) {
 #pragma unroll
@@ -490,52 +493,62 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
           inv_top = 1.0f / t;
         }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
+          const float2 a = split(s[nt][0]), c = split(s[nt][1]), old = split(mx[nt]);
+          float top[2] = {fmaxf(a.x, c.x), fmaxf(a.y, c.y)};
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float t = fmaxf(s[nt][e], s[nt][e + 2]);
 #pragma unroll
             for (int sft = 4; sft < 32; sft <<= 1)
-              t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, sft));
-            t = fmaxf(t, mx[nt][e]);
-            const float f = exp2_fast(mx[nt][e] - t);
-            mx[nt][e] = t;
-            l[nt][e] *= f;
-#pragma unroll
-            for (int n = 0; n < NG; ++n) vm[nt][n][e] *= f;
-#pragma unroll
-            for (int c = 0; c < C; ++c)
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                o[c][k][nt][e] *= f * fs;
-                o[c][k][nt][e + 2] *= f * fs;
-              }
+              top[e] = fmaxf(top[e], __shfl_xor_sync(0xFFFFFFFFu, top[e], sft));
+            top[e] = fmaxf(top[e], e ? -old.y : -old.x);
           }
+          const F2 f = f2(exp2_fast(-old.x - top[0]), exp2_fast(-old.y - top[1]));
+          mx[nt] = f2(-top[0], -top[1]);
+          l[nt] = l[nt] * f;
+#pragma unroll
+          for (int n = 0; n < NG; ++n) vm[nt][n] = vm[nt][n] * f;
+          const float2 of = split(f * f2(fs));
+#pragma unroll
+          for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              o[c][k][nt][0] *= of.x, o[c][k][nt][1] *= of.y;
+              o[c][k][nt][2] *= of.x, o[c][k][nt][3] *= of.y;
+            }
+        }
       }
       // ---- weights p step, as fp16 hi + lo, turned to the operand layout
       uint32_t wh[NG][NT][2], wl[NG][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float pr[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          pr[e] = exp2_fast(s[nt][e] - mx[nt][e & 1]);
-          l[nt][e & 1] += pr[e];
-        }
+        for (int t = 0; t < 2; ++t) {
+          const float2 x = split(s[nt][t] + mx[nt]);
+          const F2 pr = f2(exp2_fast(x.x), exp2_fast(x.y));
+          l[nt] = l[nt] + pr;
 #pragma unroll
-        for (int n = 0; n < NG; ++n) {
-          float w[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            vm[nt][n][e & 1] = fmaf(pr[e], vl[n][nt][e], vm[nt][n][e & 1]);
-            w[e] = pr[e] * (vs[n][nt][e] * inv_top);
-          }
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const uint32_t hi16 = pack_half(w[2 * t], w[2 * t + 1]);
+          for (int n = 0; n < NG; ++n) {
+            F2 least = f2(bf16_hi(v[n][t])), step = f2(bf16_lo(v[n][t]) * inv_top);
+            if (hidden) {  // 0 * NaN must stay 0
+              const float2 a = split(least), c = split(step);
+              const bool h0 = hidden >> (4 * nt + 2 * t) & 1, h1 = hidden >> (4 * nt + 2 * t) & 2;
+              least = f2(h0 ? 0.0f : a.x, h1 ? 0.0f : a.y);
+              step = f2(h0 ? 0.0f : c.x, h1 ? 0.0f : c.y);
+            }
+            vm[nt][n] = fma2(pr, least, vm[nt][n]);
+            const F2 w = pr * step;
+            const float2 ws = split(w);
+            const uint32_t hi16 = pack_half(ws.x, ws.y);
             const float2 back = unpack_half(hi16);
-            wh[n][nt][t] = transpose8x8(hi16);
-            wl[n][nt][t] = transpose8x8(pack_half(w[2 * t] - back.x, w[2 * t + 1] - back.y));
+            const float2 rest = split(fma2(f2(back.x, back.y), f2(-1.0f), w));
+            const uint32_t lo16 = pack_half(rest.x, rest.y);
+            if (TWICE) {
+              wh[n][nt][t] = transpose8x8(j < 2 ? hi16 : lo16);
+            } else {
+              wh[n][nt][t] = transpose8x8(hi16);
+              wl[n][nt][t] = transpose8x8(lo16);
+            }
           }
         }
       }
@@ -565,8 +578,10 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
         for (int nt = 0; nt < NT; ++nt) {
           mma_f16(o[c][0][nt], a, wh[n][nt][0], wh[n][nt][1]);
           mma_f16(o[c][1][nt], bytes, wh[n][nt][0], wh[n][nt][1]);
-          mma_f16(o[c][0][nt], a, wl[n][nt][0], wl[n][nt][1]);
-          mma_f16(o[c][1][nt], bytes, wl[n][nt][0], wl[n][nt][1]);
+          if (!TWICE) {
+            mma_f16(o[c][0][nt], a, wl[n][nt][0], wl[n][nt][1]);
+            mma_f16(o[c][1][nt], bytes, wl[n][nt][0], wl[n][nt][1]);
+          }
         }
       }
     }
@@ -579,34 +594,51 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
     float* so = sl + kAttnWarps * RP;            // [warp][RP][D]
     float* sf = so + kAttnWarps * RP * D;        // [warp][RP] factors
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt) {
+      if (TWICE) {  // the columns of the low halves onto those of the high ones
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              o[c][k][nt][e] += __shfl_xor_sync(0xFFFFFFFFu, o[c][k][nt][e], 2);
+      }
+      const float2 m2 = split(mx[nt]);
+      float2 l2 = split(l[nt]), vm2[NG];
+#pragma unroll
+      for (int n = 0; n < NG; ++n) vm2[n] = split(vm[nt][n]);
+#pragma unroll
+      for (int sft = 4; sft < 32; sft <<= 1) {
+        l2.x += __shfl_xor_sync(0xFFFFFFFFu, l2.x, sft);
+        l2.y += __shfl_xor_sync(0xFFFFFFFFu, l2.y, sft);
+#pragma unroll
+        for (int n = 0; n < NG; ++n) {
+          vm2[n].x += __shfl_xor_sync(0xFFFFFFFFu, vm2[n].x, sft);
+          vm2[n].y += __shfl_xor_sync(0xFFFFFFFFu, vm2[n].y, sft);
+        }
+      }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int r = nt * 8 + 2 * j + e;
-#pragma unroll
-        for (int sft = 4; sft < 32; sft <<= 1) {
-          l[nt][e] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][e], sft);
-#pragma unroll
-          for (int n = 0; n < NG; ++n)
-            vm[nt][n][e] += __shfl_xor_sync(0xFFFFFFFFu, vm[nt][n][e], sft);
-        }
+        if (r >= RP) continue;
         if (g == 0) {
-          sm[warp * RP + r] = mx[nt][e];
-          sl[warp * RP + r] = l[nt][e];
+          sm[warp * RP + r] = -(e ? m2.y : m2.x);
+          sl[warp * RP + r] = e ? l2.y : l2.x;
         }
         const float f = 16777216.0f * top_step, f16 = 1048576.0f * top_step;  // 2^24, 2^20
 #pragma unroll
         for (int c = 0; c < C; ++c) {
           const int ch = kWide ? 64 * (c / 2) + 8 * g + 4 * (c & 1)
                                : 32 * c + 8 * (g & 3) + 4 * (g >> 2);
-          float* dst = so + (warp * RP + r) * D + ch;
-          const float base = vm[nt][c / A::CG][e];
-          dst[0] = fmaf(o[c][0][nt][e], f, base);
-          dst[1] = fmaf(o[c][1][nt][e] - o[c][0][nt][e], f16, base);
-          dst[2] = fmaf(o[c][0][nt][e + 2], f, base);
-          dst[3] = fmaf(o[c][1][nt][e + 2] - o[c][0][nt][e + 2], f16, base);
+          const float base = e ? vm2[c / A::CG].y : vm2[c / A::CG].x;
+          *reinterpret_cast<float4*>(so + (warp * RP + r) * D + ch) = make_float4(
+              fmaf(o[c][0][nt][e], f, base), fmaf(o[c][1][nt][e] - o[c][0][nt][e], f16, base),
+              fmaf(o[c][0][nt][e + 2], f, base),
+              fmaf(o[c][1][nt][e + 2] - o[c][0][nt][e + 2], f16, base));
         }
       }
+    }
     __syncthreads();
     if (tid < RP) {
       float top = kNoMax, sum = 0.0f;
@@ -630,8 +662,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
       if (!whole) {
         slot[2 * RP + x] = t;
       } else if (row0 + r < p.rows) {
-        const float sum = sl[r];
-        t = sum == 0.0f ? 0.0f : t / sum;
+        t *= sl[r] == 0.0f ? 0.0f : 1.0f / sl[r];
         const int64_t at = (bh * p.rows + row0 + r) * D + ch;
         if (p.out_f32)
           static_cast<float*>(p.out)[at] = t;
@@ -654,36 +685,38 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
 }
 
 // One CTA per (row of a tile, row tile, head, sequence): joins the partial
-// results of a head that several CTAs shared, in their order; writes the empty
-// result where there is nothing to see.
-template <int D, int NT>
+// results of a head that several CTAs shared, in their order (a lane group
+// reads a slot's row, 16 bytes a lane; the groups' sums are added in a fixed
+// order); writes the empty result where there is nothing to see.
+template <int D, int RP>
 __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const AttnParams p) {
-  constexpr int RP = 8 * NT, kSlot = RP * (D + 2);
-  constexpr int kParts = kJoinThreads / D;  // slots read at once
-  __shared__ float red[kJoinThreads];
+  constexpr int kSlot = RP * (D + 2);
+  constexpr int L = D / 4, kParts = kJoinThreads / L;  // slots read at once
+  __shared__ float4 red[kParts][L];
+  __shared__ float sums[kParts];
   __shared__ float tops[kJoinThreads / 32];
   wait_for_previous_launch();
   allow_next_launch();
   const int heads = p.c.Hkv * p.mt;
-  const int64_t hh = blockIdx.x;
-  const int b = (int)(hh / heads), hm = (int)(hh - (int64_t)b * heads);
+  const int b = blockIdx.x / heads, hm = blockIdx.x - b * heads;
   const int h = hm / p.mt, r = blockIdx.y;
   const int row = (hm - h * p.mt) * RP + r;
   if (row >= p.rows) return;
   const int64_t before = __ldcg(p.prefix + b), steps = __ldcg(p.prefix + b + 1) - before;
   const int64_t units = (int64_t)__ldcg(p.prefix + p.B) * heads;
   const int64_t out_row = ((int64_t)b * p.c.Hkv + h) * p.rows + row;
-  const int ch = threadIdx.x % D, part = threadIdx.x / D;
-  if (steps == 0) {
-    if (part == 0) {
-      if (p.out_f32)
-        static_cast<float*>(p.out)[out_row * D + ch] = 0.0f;
-      else
-        static_cast<uint16_t*>(p.out)[out_row * D + ch] = 0;
-    }
-    if (threadIdx.x == 0) p.lse[out_row] = -INFINITY;
-    return;
-  }
+  const int cl = threadIdx.x % L, part = threadIdx.x / L;
+  auto write = [&](float4 v, float lse) {
+    if (part != 0) return;
+    const int64_t at = out_row * D + cl * 4;
+    if (p.out_f32)
+      *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = v;
+    else
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) =
+          make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+    if (cl == 0) p.lse[out_row] = lse;
+  };
+  if (steps == 0) return write(make_float4(0, 0, 0, 0), -INFINITY);
   const int ctas = (int)min((int64_t)p.ctas, units);
   const int64_t u0 = before * heads + hm * steps;
   const int c0 = range_of(units, ctas, u0), c1 = range_of(units, ctas, u0 + steps - 1);
@@ -694,62 +727,66 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const AttnParams
     return p.partial + (int64_t)(2 * c + (first ? 0 : 1)) * kSlot;
   };
   float top = kNoMax;
-  for (int c = c0 + threadIdx.x; c <= c1; c += kJoinThreads) top = fmaxf(top, __ldcg(slot_of(c) + r));
+  for (int c = c0 + threadIdx.x; c <= c1; c += kJoinThreads)
+    top = fmaxf(top, __ldcg(slot_of(c) + r));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
   if ((threadIdx.x & 31) == 0) tops[threadIdx.x / 32] = top;
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kJoinThreads / 32; ++w) top = fmaxf(top, tops[w]);
-  float t = 0.0f, sum = 0.0f;
+  float4 t = make_float4(0, 0, 0, 0);
+  float sum = 0.0f;
 #pragma unroll 4
   for (int c = c0 + part; c <= c1; c += kParts) {
     const float* s = slot_of(c);
     const float f = exp2_fast(__ldcg(s + r) - top);
+    const float4 v = __ldcg(reinterpret_cast<const float4*>(s + 2 * RP + r * D) + cl);
     sum = fmaf(__ldcg(s + RP + r), f, sum);
-    t = fmaf(__ldcg(s + 2 * RP + r * D + ch), f, t);
+    t.x = fmaf(v.x, f, t.x), t.y = fmaf(v.y, f, t.y);
+    t.z = fmaf(v.z, f, t.z), t.w = fmaf(v.w, f, t.w);
   }
-  red[threadIdx.x] = t;
+  red[part][cl] = t;
+  if (cl == 0) sums[part] = sum;
   __syncthreads();
-  float total = 0.0f;
-  for (int w = 0; w < kParts; ++w) total += red[w * D + ch];
-  __syncthreads();
-  red[threadIdx.x] = sum;
-  __syncthreads();
+  if (part != 0) return;
+  t = make_float4(0, 0, 0, 0);
   sum = 0.0f;
-  for (int w = 0; w < kParts; ++w) sum += red[w * D + ch];
-  if (part == 0) {
-    const float v = sum == 0.0f ? 0.0f : total / sum;
-    if (p.out_f32)
-      static_cast<float*>(p.out)[out_row * D + ch] = v;
-    else
-      static_cast<__nv_bfloat16*>(p.out)[out_row * D + ch] = __float2bfloat16_rn(v);
+#pragma unroll
+  for (int w = 0; w < kParts; ++w) {
+    const float4 v = red[w][cl];
+    t.x += v.x, t.y += v.y, t.z += v.z, t.w += v.w;
+    sum += sums[w];
   }
-  if (threadIdx.x == 0) p.lse[out_row] = (top + log2f(sum)) * kLn2;
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  write(make_float4(t.x * inv, t.y * inv, t.z * inv, t.w * inv), (top + log2f(sum)) * kLn2);
 }
 
 // CTAs of the attention launch: as many as run at once
 int attn_ctas(int nt, int sms) { return nt == 1 ? kPerSm * sms : sms; }
 
-template <int D, int NG, int NT>
+template <int D, int NG, int NT, bool TWICE>
 cudaError_t launch_attn(const AttnParams& p, int grid, cudaStream_t st) {
-  using A = Attn<D, NG, NT>;
+  using A = Attn<D, NG, NT, TWICE>;
   const size_t smem = A::kSmem + (size_t)(p.B + 1) * sizeof(int);
   constexpr size_t most = A::kSmem + (size_t)(kMostSequences + 1) * sizeof(int);
-  static_assert(most <= 227 * 1024, "shared memory");
-  cudaError_t e = cudaFuncSetAttribute(kv4_attn_kernel<D, NG, NT>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+  static_assert(most <= 210 * 1024, "shared memory");
+  cudaError_t e = allow_shared_memory<kv4_attn_kernel<D, NG, NT, TWICE>>((int)most);
   if (e != cudaSuccess) return e;
-  e = launch_dependent(kv4_attn_kernel<D, NG, NT>, dim3(grid), dim3(kAttnThreads), smem, st, p);
+  e = launch_dependent(kv4_attn_kernel<D, NG, NT, TWICE>, dim3(grid), dim3(kAttnThreads), smem, st,
+                       p);
   if (e != cudaSuccess) return e;
-  const int rows = p.rows < 8 * NT ? p.rows : 8 * NT;
-  return launch_dependent(kv4_join_kernel<D, NT>, dim3(p.B * p.c.Hkv * p.mt, rows),
+  return launch_dependent(kv4_join_kernel<D, A::RP>,
+                          dim3(p.B * p.c.Hkv * p.mt, p.rows < A::RP ? p.rows : A::RP),
                           dim3(kJoinThreads), 0, st, p);
 }
 
+// Up to 4 rows a head: each row twice; up to 8: one tile; more: tiles of 16.
 template <int D, int NG>
-cudaError_t launch_attn(const AttnParams& p, int nt, int grid, cudaStream_t st) {
-  return nt == 1 ? launch_attn<D, NG, 1>(p, grid, st) : launch_attn<D, NG, 2>(p, grid, st);
+cudaError_t launch_attn(const AttnParams& p, int grid, cudaStream_t st) {
+  if (p.rows <= 4) return launch_attn<D, NG, 1, true>(p, grid, st);
+  if (p.rows <= 8) return launch_attn<D, NG, 1, false>(p, grid, st);
+  return launch_attn<D, NG, 2, false>(p, grid, st);
 }
 
 size_t prefix_bytes(int B) { return ((size_t)(B + 1) * sizeof(int) + 15) / 16 * 16; }
@@ -824,17 +861,27 @@ bsattn_status bsattn_kv4_attn(const bsattn_kv4_cache* cache, const void* q, int 
   p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + prefix_bytes(B));
   p.ctas = attn_ctas(nt, device_sm_count(dev));
   const int64_t most = steps * B * cache->kv_heads * mt;  // units, at most
+  const int64_t heads = (int64_t)B * cache->kv_heads * mt;
+  if (heads * kMostParts < p.ctas) p.ctas = (int)(heads * kMostParts);
+  if (selected && heads <= p.ctas) {
+    // Every head has the same steps: whole CTAs a head, unless that leaves each
+    // of them with more to do than cutting through heads (which costs most CTAs
+    // a second start and join, about kSegmentSteps steps) would.
+    const int64_t share = p.ctas / heads < steps ? p.ctas / heads : steps;
+    if ((steps + share - 1) / share <= steps * heads / p.ctas + kSegmentSteps)
+      p.ctas = (int)(heads * share);
+  }
   const int grid = (int)(most < p.ctas ? most : p.ctas);
   p.ctas = grid;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int groups = cache->head_dim / cache->group;
   cudaError_t e;
   if (cache->head_dim == 64)
-    e = groups == 1 ? launch_attn<64, 1>(p, nt, grid, st) : launch_attn<64, 2>(p, nt, grid, st);
+    e = groups == 1 ? launch_attn<64, 1>(p, grid, st) : launch_attn<64, 2>(p, grid, st);
   else
-    e = groups == 1   ? launch_attn<128, 1>(p, nt, grid, st)
-        : groups == 2 ? launch_attn<128, 2>(p, nt, grid, st)
-                      : launch_attn<128, 4>(p, nt, grid, st);
+    e = groups == 1   ? launch_attn<128, 1>(p, grid, st)
+        : groups == 2 ? launch_attn<128, 2>(p, grid, st)
+                      : launch_attn<128, 4>(p, grid, st);
   return from_cuda(e);
 }
 

@@ -2,6 +2,7 @@
 // (rope.cu, select.cu, kv4.cu): bf16 packing, exact sums, block floating point.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -28,6 +29,19 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
                     pack_bf16(f[6], f[7]));
+}
+
+// Lets a kernel have `bytes` of dynamic shared memory; asks once a device.
+template <auto Kernel>
+inline cudaError_t allow_shared_memory(int bytes) {
+  static std::atomic<int> allowed[64];
+  int dev = -1;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < 64 && allowed[dev].load(std::memory_order_relaxed) >= bytes))
+    return e;
+  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) allowed[dev].store(bytes, std::memory_order_relaxed);
+  return e;
 }
 
 // ---------------------------------------------------------------------------
@@ -253,6 +267,10 @@ __device__ __forceinline__ void store32(void* dst, const uint32_t (&v)[8], bool 
     static_cast<uint4*>(dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
     static_cast<uint4*>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
   }
+}
+
+__device__ __forceinline__ float from_ordered_bits(uint32_t u) {
+  return __uint_as_float((u & 0x80000000u) ? u ^ 0x80000000u : ~u);
 }
 
 // D += A B, 16 x 8 x 16: bf16 in, 32-bit sums (A row-major, B column-major)

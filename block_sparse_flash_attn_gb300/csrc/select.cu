@@ -82,7 +82,7 @@ struct SelectParams {
   const uint8_t* allow;  // [B][H or 1][nb][nk], null: all
   int64_t allow_b, allow_h;
   uint8_t* mask;  // [B][H][nb][nk]
-  int H, Hkv, nb, nk, kdiv;
+  int H, Hkv, nb, nk, kdiv, kshift;  // kdiv = 1 << kshift key blocks a query block
   int keep, sink, local, causal;
   int rows;  // query blocks a CTA: 16, or 4 when 16 rows of keys do not fit
 };
@@ -103,15 +103,14 @@ struct RowKeys {
     if (KP > 0) {
 #pragma unroll
       for (int i = 0; i < KP / 4; ++i) {
-        const uint4 v = piece_from_shared(i, n);
+        const uint4 v = piece(i, n);
         k[4 * i] = v.x, k[4 * i + 1] = v.y, k[4 * i + 2] = v.z, k[4 * i + 3] = v.w;
       }
     }
   }
-  __device__ __forceinline__ uint4 piece_from_shared(int i, int n) const {
+  __device__ __forceinline__ uint4 piece(int i, int n) const {
     return i * 128 + lane * 4 < n ? sh[i * 32 + lane] : make_uint4(0, 0, 0, 0);
   }
-  __device__ __forceinline__ uint4 piece(int i, int n) const { return piece_from_shared(i, n); }
 
   template <typename F>
   __device__ __forceinline__ void each(int n, F f) const {
@@ -120,7 +119,7 @@ struct RowKeys {
       for (int i = 0; i < KP; ++i) f(k[i]);
     } else {
       for (int i = 0; i < pieces; ++i) {
-        const uint4 v = piece_from_shared(i, n);
+        const uint4 v = piece(i, n);
         f(v.x), f(v.y), f(v.z), f(v.w);
       }
     }
@@ -128,9 +127,10 @@ struct RowKeys {
 };
 
 // Marks the best keys of a row: `keep` of them, or all that are forced if those
-// are more.  The threshold is searched between the row's least and largest key,
-// in turn by interpolating the counts (scores spread smoothly: a few steps
-// do) and by halving (so that it ends, in 64 steps at most).
+// are more.  The threshold is searched between the row's least and largest key
+// by interpolating the counts between the two scores (they spread smoothly: six
+// to eight steps do); from the ninth step on every other one halves the
+// interval of bit patterns instead, so that 72 steps always end it.
 template <int KP>
 __device__ __forceinline__ void choose_row(const uint32_t* row, int n, int nk, int keep,
                                            uint8_t* out, int lane) {
@@ -159,11 +159,14 @@ __device__ __forceinline__ void choose_row(const uint32_t* row, int n, int nk, i
     t = least;
     uint32_t hi = top + 1u;
     int over = forced;
-    bool halve = false;
-    while (have != want && hi - t > 1u) {
-      const float share = halve ? 0.5f : ((float)(have - want) + 0.5f) / (float)(have - over);
-      const uint32_t step = (uint32_t)((float)(hi - t) * share);
-      const uint32_t c = t + min(max(step, 1u), hi - t - 1u);
+    for (int step = 0; have != want && hi - t > 1u; ++step) {
+      uint32_t c = t + (hi - t) / 2u;
+      if (step < 8 || (step & 1)) {
+        const float low = from_ordered_bits(t), high = from_ordered_bits(hi - 1u);
+        const float share = ((float)(have - want) + 0.5f) * __frcp_rn((float)(have - over));
+        c = ordered_bits(fmaf(high - low, share, low));
+      }
+      c = min(max(c, t + 1u), hi - 1u);
       int cnt = 0;
       keys.each(n, [&](uint32_t x) { cnt += x >= c ? 1 : 0; });
       cnt = __reduce_add_sync(0xFFFFFFFFu, cnt);
@@ -171,7 +174,6 @@ __device__ __forceinline__ void choose_row(const uint32_t* row, int n, int nk, i
         t = c, have = cnt;
       else
         hi = c, over = cnt;
-      halve = !halve;
     }
   }
   // more keys >= t than wanted: those equal to t go in from the left
@@ -190,14 +192,18 @@ __device__ __forceinline__ void choose_row(const uint32_t* row, int n, int nk, i
     }
   }
   if (((nk | (int)reinterpret_cast<uintptr_t>(out)) & 3) == 0) {
+    // (keys behind n read as ruled out, below any threshold)
+    const uint32_t least_in = drop_from == 0x7FFFFFFF ? t : t + 1u;
     for (int i = 0; i * 128 + lane * 4 < nk; ++i) {
-      const uint4 v = keys.piece(i, n);
       const int col = i * 128 + lane * 4;
-      auto in = [&](uint32_t x, int at) {
-        return (x > t || (x == t && at < drop_from)) && at < n ? 1u : 0u;
-      };
-      *reinterpret_cast<uint32_t*>(out + col) = in(v.x, col) | in(v.y, col + 1) << 8 |
-                                                in(v.z, col + 2) << 16 | in(v.w, col + 3) << 24;
+      const uint4 v = keys.piece(i, n);
+      uint32_t in = (v.x >= least_in ? 1u : 0u) | (v.y >= least_in ? 0x100u : 0u) |
+                    (v.z >= least_in ? 0x10000u : 0u) | (v.w >= least_in ? 0x1000000u : 0u);
+      if (col < drop_from && least_in != t)
+        in |= (v.x == t ? 1u : 0u) | (v.y == t && col + 1 < drop_from ? 0x100u : 0u) |
+              (v.z == t && col + 2 < drop_from ? 0x10000u : 0u) |
+              (v.w == t && col + 3 < drop_from ? 0x1000000u : 0u);
+      *reinterpret_cast<uint32_t*>(out + col) = in;
     }
   } else {
     for (int i = lane; i < nk; i += 32) {
@@ -256,7 +262,7 @@ __global__ void __launch_bounds__(kSelThreads, 4) choose_blocks_kernel(const Sel
     for (int i = 0; i < 4; ++i) {
       const int r = g + 8 * (i >> 1), col = n0 + 2 * j + (i & 1);
       if (r < rows && col < reach) {
-        const int q128 = q0 + r, k128 = col / p.kdiv;
+        const int q128 = q0 + r, k128 = col >> p.kshift;
         bool ok = !p.causal || k128 <= q128;
         if (allow) ok = ok && allow[(int64_t)r * p.nk + col] != 0;
         const bool must = col < p.sink || abs(k128 - q128) < p.local;
@@ -292,12 +298,8 @@ cudaError_t launch_select(const void* q, const void* k, int q_blocks, int k_bloc
                           uint16_t* mq, uint16_t* mk, const SelectParams& p, int B,
                           cudaStream_t st) {
   const size_t smem = (size_t)p.rows * ((p.nk + 3) & ~3) * sizeof(uint32_t);
-  cudaError_t e = cudaSuccess;
-  if (smem > (48 << 10)) {
-    e = cudaFuncSetAttribute(choose_blocks_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kSelKeyBytes);
-    if (e != cudaSuccess) return e;
-  }
+  cudaError_t e = allow_shared_memory<choose_blocks_kernel<D>>(kSelKeyBytes);
+  if (e != cudaSuccess) return e;
   e = launch_dependent(block_mean_kernel<D>, dim3(q_blocks + k_blocks), dim3(kPoolThreads),
                        (size_t)kBlock * D * 2, st, static_cast<const uint16_t*>(q),
                        static_cast<const uint16_t*>(k), q_blocks, key_block, mq, mk);
@@ -357,6 +359,7 @@ bsattn_status bsattn_select_blocks(const void* q, const void* k, int B, int H, i
   p.H = H;
   p.Hkv = Hkv;
   p.kdiv = kdiv;
+  p.kshift = kdiv - 1;
   p.keep = keep;
   p.sink = sink;
   p.local = local;

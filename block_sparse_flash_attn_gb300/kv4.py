@@ -76,6 +76,11 @@ def _attn_workspace(device, *sizes):  # a function of the sizes and the (current
     return _bs.load().bsattn_kv4_attn_workspace(*sizes)
 
 
+@functools.lru_cache(maxsize=256)
+def _select_workspace(device, *sizes):
+    return _bs.load().bsattn_kv4_select_workspace(*sizes)
+
+
 def _cache(cache) -> Kv4Cache:
     if not isinstance(cache, Kv4Cache):
         raise TypeError("cache must be a Kv4Cache")
@@ -177,11 +182,11 @@ def kv4_select(cache: Kv4Cache, q: torch.Tensor, block_table: torch.Tensor, leng
             tensor("out", out, (_I32,), (B, cache.kv_heads, keep), cache.device)
         if B:
             lib = _bs.load()
-            nbytes = 4 * B * cache.kv_heads * columns  # bsattn_kv4_select_workspace
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=cache.device)
+            nbytes = _select_workspace(cache.device.index, B, cache.kv_heads, columns)
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=cache.device) if nbytes else None
             _bs._check(lib.bsattn_kv4_select(
                 cache._ref, q.data_ptr(), B, H, T, block_table.data_ptr(), stride, columns,
-                lengths.data_ptr(), keep, sink, recent, out.data_ptr(), ws.data_ptr(), nbytes,
+                lengths.data_ptr(), keep, sink, recent, out.data_ptr(), pointer(ws), nbytes,
                 on), "bsattn_kv4_select")
     return out
 

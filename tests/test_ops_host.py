@@ -103,7 +103,7 @@ ATTN = dict(cache=None, q=FAKE, B=1, H=4, T=1, table=FAKE, stride=4, columns=4, 
 
 @pytest.mark.parametrize("change,status", [
     (dict(k_codes=None), 1), (dict(v_scales=0x10008), 1), (dict(status=None), 1), (dict(status=0x10002), 1),
-    (dict(pages=0), 1), (dict(kv_heads=0), 1), (dict(kv_heads=65536), 2), (dict(page_size=8), 2),
+    (dict(pages=0), 1), (dict(kv_heads=0), 1), (dict(kv_heads=32768), 2), (dict(page_size=8), 2),
     (dict(page_size=48), 2), (dict(page_size=512), 2), (dict(head_dim=96), 2), (dict(group=16), 2),
     (dict(group=128), 1)], ids=lambda c: str(c))
 def test_caches(bs, change, status):
@@ -127,7 +127,7 @@ def test_caches(bs, change, status):
     ("read", READ, dict(T=0), 1), ("read", READ, dict(B=1 << 16), 2), ("read", READ, dict(T=(1 << 30) + 1), 2),
     ("select", PAGES, dict(q=ODD), 1), ("select", PAGES, dict(H=3), 1), ("select", PAGES, dict(T=65), 2),
     ("select", PAGES, dict(keep=1), 1), ("select", PAGES, dict(recent=0), 1), ("select", PAGES, dict(sink=-1), 1),
-    ("select", PAGES, dict(nbytes=8), 1), ("select", PAGES, dict(out=None), 1),
+    ("select", PAGES, dict(columns=20000, stride=20000, nbytes=8), 1), ("select", PAGES, dict(out=None), 1),
     ("attn", ATTN, dict(q=None), 1), ("attn", ATTN, dict(out=ODD), 1), ("attn", ATTN, dict(lse=None), 1),
     ("attn", ATTN, dict(T=65), 2), ("attn", ATTN, dict(scale=float("nan")), 1), ("attn", ATTN, dict(flags=1), 1),
     ("attn", ATTN, dict(selected=FAKE), 1), ("attn", ATTN, dict(n=3), 1), ("attn", ATTN, dict(nbytes=0), 1),

@@ -50,6 +50,7 @@ def select_blocks(q: torch.Tensor, k: torch.Tensor, keep: int, causal: bool = Fa
     if keep <= 0 or sink < 0 or local < 0:
         raise ValueError("keep must be positive, sink and local not negative")
     Hkv, nb, nk = k.shape[1], S // 128, S // key_block
+    keep, sink, local = min(keep, nk), min(sink, nk), min(local, nb)  # (C ints)
     allow_heads = 0
     if allow is not None:
         tensor("allow", allow, (torch.uint8,), device=q.device)

@@ -19,10 +19,7 @@ namespace bsattn {
 namespace {
 
 constexpr int kRowThreads = 128;  // write_rounded_mean takes a CTA of 128
-#ifndef RDR
-#define RDR 2
-#endif
-constexpr int kReadRows = RDR;      // rows a lane group reads back at once
+constexpr int kReadRows = 2;      // rows a lane group reads back at once
 constexpr float kLeastStep = 7.888609e-31f;  // 2^-100
 
 struct AppendParams {

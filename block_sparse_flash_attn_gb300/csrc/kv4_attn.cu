@@ -834,6 +834,7 @@ bsattn_status bsattn_kv4_attn(const bsattn_kv4_cache* cache, const void* q, int 
   const int nt = rows <= 8 ? 1 : 2;
   const int mt = (int)((rows + 8 * nt - 1) / (8 * nt));
   if (rows > 128 || B > kMostSequences || steps * B >= (1ll << 31) ||
+      (int64_t)columns * cache->page_size > (1ll << 31) - kStep ||  // positions are 32-bit
       (int64_t)B * cache->kv_heads * mt >= (1ll << 31) ||
       (int64_t)cache->pages * cache->kv_heads * cache->page_size / kTile >= (1ll << 31))
     return BSATTN_ERR_UNSUPPORTED;

@@ -30,7 +30,8 @@ class _CacheStruct(ctypes.Structure):  # bsattn_kv4_cache
 
 
 class Kv4Cache:
-    """The cache's tensors (all CUDA, one device), zero at first:
+    """The cache's tensors (all CUDA, one device), zero at first, to be changed in
+    place only:
 
     k_codes, v_codes    uint8 [pages, kv_heads, page_size, head_dim/2], even channel in the low bits
     k_scales, v_scales  bf16 [pages, kv_heads, page_size, head_dim/group, 2]: (step, least)
@@ -110,6 +111,10 @@ def _queries(cache, q, B):
     return H, T
 
 
+def _strides(t):  # of batch, head and token; none where there is only one
+    return [s if n > 1 else 0 for s, n in zip(t.stride(), t.shape[:3])]
+
+
 def kv4_append(cache: Kv4Cache, k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor,
                lengths: torch.Tensor, counts: torch.Tensor | None = None, stream=None) -> None:
     """Write new tokens: k, v CUDA bf16 [B, kv_heads, T, head_dim] (channels
@@ -123,8 +128,8 @@ def kv4_append(cache: Kv4Cache, k: torch.Tensor, v: torch.Tensor, block_table: t
         if t.dim() != 4 or t.shape[:2] != (B, cache.kv_heads) or t.shape[3] != cache.head_dim \
                 or t.shape != k.shape:
             raise ValueError("k, v must be [B, kv_heads, T, head_dim]")
-        if t.numel() and (t.stride(3) != 1 or any(s % 8 for s in t.stride()[:3])
-                          or t.data_ptr() % 16):
+        if t.numel() and (t.stride(3) != 1 or t.data_ptr() % 16 or
+                          any(s % 8 and n > 1 for s, n in zip(t.stride(), t.shape[:3]))):
             raise ValueError(f"{name}: channels must be contiguous, other strides multiples of 8 "
                              "elements, the data 16-byte aligned")
     T = k.shape[2]
@@ -132,7 +137,7 @@ def kv4_append(cache: Kv4Cache, k: torch.Tensor, v: torch.Tensor, block_table: t
         return
     with launch_on(cache.device, stream) as on:
         _bs._check(_bs.load().bsattn_kv4_append(
-            cache._ref, k.data_ptr(), *k.stride()[:3], v.data_ptr(), *v.stride()[:3], B, T,
+            cache._ref, k.data_ptr(), *_strides(k), v.data_ptr(), *_strides(v), B, T,
             block_table.data_ptr(), stride, columns, lengths.data_ptr(), pointer(counts),
             on), "bsattn_kv4_append")
 

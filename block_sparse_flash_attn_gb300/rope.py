@@ -64,7 +64,7 @@ def _common(x, heads, kv_heads, q_weight, k_weight, table, positions, interleave
     if D not in (64, 128):
         raise ValueError("D must be 64 or 128")
     sb, ss, sh, sd = x.stride()
-    if sd != 1 or sh != D or ss % 8 or sb % 8 or x.data_ptr() % 16:
+    if sd != 1 or sh != D or (ss % 8 and S > 1) or (sb % 8 and B > 1) or x.data_ptr() % 16:
         raise ValueError("the rows of a token must be contiguous, tokens and batch entries a "
                          "multiple of 8 elements apart, x 16-byte aligned")
     flags = ROPE_INTERLEAVED if interleaved else 0
@@ -89,7 +89,7 @@ def _common(x, heads, kv_heads, q_weight, k_weight, table, positions, interleave
         raise ValueError("positions need a table")
     if positions is not None:
         tensor("positions", positions, (torch.int32,), (B, S), x.device)
-    return B, S, D, n_pos, rotary, flags
+    return B, S, D, n_pos, rotary, flags, sb if B > 1 else 0, ss if S > 1 else 0
 
 
 def qk_norm_rope(x: torch.Tensor, heads: int, kv_heads: int, q_weight: torch.Tensor | None = None,
@@ -107,8 +107,8 @@ def qk_norm_rope(x: torch.Tensor, heads: int, kv_heads: int, q_weight: torch.Ten
     (2i, 2i + 1) with interleaved.  positions: CUDA int32 [B, S] (default 0 .. S-1); one
     outside the table gives NaN.  Weights: bf16 or fp32 [D].  S need not be a
     multiple of 128 here."""
-    B, S, D, n_pos, rotary, flags = _common(x, heads, kv_heads, q_weight, k_weight, table,
-                                            positions, interleaved)
+    B, S, D, n_pos, rotary, flags, sb, ss = _common(x, heads, kv_heads, q_weight, k_weight, table,
+                                                    positions, interleaved)
     with launch_on(x.device, stream) as on:
         outs = []
         for name, t, h in (("q", q, heads), ("k", k, kv_heads), ("v", v, kv_heads)):
@@ -120,7 +120,7 @@ def qk_norm_rope(x: torch.Tensor, heads: int, kv_heads: int, q_weight: torch.Ten
         q, k, v = outs
         if B * S:
             _bs._check(_bs.load().bsattn_qk_norm_rope(
-                x.data_ptr(), x.stride(0), x.stride(1), B, S, heads, kv_heads, D,
+                x.data_ptr(), sb, ss, B, S, heads, kv_heads, D,
                 pointer(q_weight), pointer(k_weight), pointer(table), n_pos, rotary,
                 pointer(positions), float(eps), flags, q.data_ptr(), k.data_ptr(), v.data_ptr(),
                 on), "bsattn_qk_norm_rope")
@@ -142,8 +142,8 @@ def qk_norm_rope_bwd(x: torch.Tensor, dq: torch.Tensor, dk: torch.Tensor, dv: to
         if t.dim() != 4:
             raise ValueError(f"{name} must be [B, H, S, D]")
     heads, kv_heads = dq.shape[1], dk.shape[1]
-    B, S, D, n_pos, rotary, flags = _common(x, heads, kv_heads, q_weight, k_weight, table,
-                                            positions, interleaved)
+    B, S, D, n_pos, rotary, flags, sb, ss = _common(x, heads, kv_heads, q_weight, k_weight, table,
+                                                    positions, interleaved)
     for name, t, h in (("dq", dq, heads), ("dk", dk, kv_heads), ("dv", dv, kv_heads)):
         tensor(name, t, (_F32,), (B, h, S, D), x.device)
     with launch_on(x.device, stream) as on:
@@ -164,7 +164,7 @@ def qk_norm_rope_bwd(x: torch.Tensor, dq: torch.Tensor, dk: torch.Tensor, dv: to
                 nbytes = _workspace(x.device.index, B, S, heads, kv_heads, D)
                 ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
             _bs._check(lib.bsattn_qk_norm_rope_bwd(
-                x.data_ptr(), x.stride(0), x.stride(1), dq.data_ptr(), dk.data_ptr(),
+                x.data_ptr(), sb, ss, dq.data_ptr(), dk.data_ptr(),
                 dv.data_ptr(), B, S, heads, kv_heads, D, pointer(q_weight), pointer(k_weight),
                 pointer(table), n_pos, rotary, pointer(positions), float(eps), flags,
                 dx.data_ptr(), dx.stride(0), dx.stride(1), pointer(dwq), pointer(dwk),

@@ -469,7 +469,8 @@ bsattn_status bsattn_qk_norm_rope_bwd(const void* x, int64_t x_batch_stride, int
  *              towards `keep`; if they are more than `keep` they are all kept.
  *   q, k       device bf16 [B][H][S][D], [B][Hkv][S][D], as for bsattn_fwd_gqa
  *              (query head h scores against key head h / (H / Hkv)).  Sums of a
- *              block's entries must stay below 3e38 in magnitude.
+ *              block's entries must stay below 3e38 in magnitude; a block whose
+ *              means are all below 2^-119 is scored with fewer bits.
  *   mask       device uint8 [B][H][S/128][S/128 (S/64)], written in full.
  *   workspace  bsattn_select_blocks_workspace bytes, 16-byte aligned.
  * Errors: INVALID_ARG, UNSUPPORTED (D, sizes as bsattn_plan), CUDA.
@@ -563,7 +564,8 @@ bsattn_status bsattn_kv4_select(const bsattn_kv4_cache* cache, const void* q, in
  * cached tokens at positions up to its own: all, or those of the listed pages.
  * A query that sees none gets O = 0, LSE = -inf.
  *   q          device bf16 [B][H][T][head_dim], 16-byte aligned; query head h reads
- *              key/value head h / (H / kv_heads); (H / kv_heads) * T <= 128; B <= 4096.
+ *              key/value head h / (H / kv_heads); (H / kv_heads) * T <= 128; B <= 4096;
+ *              columns * page_size at most 2^31 - 128.
  *   lengths    cached tokens, the T new ones included.
  *   selected   device int32 [B][kv_heads][n_selected], strictly ascending pages, then
  *              negative entries (as bsattn_kv4_select writes it), or null with

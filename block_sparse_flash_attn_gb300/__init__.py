@@ -135,7 +135,7 @@ def load():
             ("kv4_select_workspace", [i32] * 3, size),
             ("kv4_attn", [vp, vp, i32, i32, i32] + table + [vp, vp, i32, f32, u32, vp, vp, vp, size,
                                                             vp], i32),
-            ("kv4_attn_workspace", [i32] * 5, size),
+            ("kv4_attn_workspace", [i32] * 8, size),
             ("kv4_status", [vp, vp], i32)):
         fn = getattr(lib, "bsattn_" + name)
         fn.argtypes, fn.restype = args, res

@@ -27,12 +27,16 @@
 // registers) is ample.  Each warp streams 16-token tiles through its own ring
 // of cp.async stages, with no CTA barrier in the loop.
 //
-// Work: the (sequence, head, 128-token step) units in order are cut into equal
-// ranges, one a CTA, from the device's lengths (so a captured graph follows
-// them).  A range that ends inside a sequence's head leaves a partial result
-// (maximum, sum, O) in the workspace, and a second launch joins those in a fixed
-// order: ragged batches and single long sequences fill the machine alike, and
-// results repeat bit for bit.
+// Work, split from the device's lengths (so a captured graph follows them):
+// - Long or ragged contexts: the (sequence, head, 128-token step) units in order
+//   are cut into equal ranges, one a CTA.  A range that ends inside a sequence's
+//   head leaves a partial result (maximum, sum, O) in the workspace, and a second
+//   launch joins those: ragged batches and single long sequences fill the
+//   machine alike.
+// - Short contexts and lists: a head is a cluster of up to 8 CTAs, which share
+//   its steps and join their results through each other's shared memory, in one
+//   launch without a workspace.
+// Both join in a fixed order: results repeat bit for bit.
 #include <cmath>
 #include <cstdint>
 
@@ -53,6 +57,7 @@ constexpr int kMostSequences = 4096;
 constexpr int kJoinThreads = 128;
 constexpr int kMostParts = 64;                 // CTAs that share a head, so that the join stays short
 constexpr int kSegmentSteps = 4;
+constexpr int kMostCluster = 8;
 constexpr float kNoMax = -1e30f;               // running maximum before any score
 constexpr float kLag = 8.0f;                   // a score may pass the running maximum by 2^8
 
@@ -74,6 +79,7 @@ struct AttnParams {
   int* prefix;     // [B + 1] steps before each sequence (written by CTA 0 for the join)
   float* partial;  // [2 * CTAs][RP * (D + 2)]
   int ctas;
+  int cluster;  // CTAs a head, 0: ranges
 };
 
 __device__ __forceinline__ uint32_t word(const uint8_t* shared) {
@@ -107,6 +113,20 @@ __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
 }
 __device__ __forceinline__ float2 unpack_half(uint32_t x) {
   return __half22float2(*reinterpret_cast<__half2*>(&x));
+}
+
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile(
+      "barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+          : "memory");
+}
+// This CTA's shared-memory word in another CTA of the cluster.
+__device__ __forceinline__ float peer_word(const float* shared, int rank) {
+  uint32_t at;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(shared_address(shared)), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return v;
 }
 
 // Where each CTA's range of units begins.
@@ -172,7 +192,7 @@ struct Attn {
   }
 };
 
-template <int D, int NG, int NT, bool TWICE>
+template <int D, int NG, int NT, bool TWICE, bool CLUSTER>
 __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
     kv4_attn_kernel(const AttnParams p) {
   using A = Attn<D, NG, NT, TWICE>;
@@ -187,20 +207,25 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
   const int g = lane >> 2, j = lane & 3;
 
   wait_for_previous_launch();
-  // steps before each sequence
-  {
+  const int heads = p.c.Hkv * p.mt;
+  const int64_t most = (int64_t)p.columns * p.c.page;  // tokens that the table has room for
+  auto steps_of = [&](int b) -> int {
+    if (p.selected) return (int)(((int64_t)p.n_selected * p.c.page + kStep - 1) / kStep);
+    int64_t n = max(__ldg(p.lengths + b), 0);
+    if (n > most) {
+      p.c.report();
+      n = most;
+    }
+    return (int)((n + kStep - 1) / kStep);
+  };
+  int64_t units = 0, u = 0, u_end = 1;
+  bool first_segment = true;
+  if (CLUSTER) {
+    allow_next_launch();
+  } else {
+    // steps before each sequence
     const int per = (p.B + kAttnThreads - 1) / kAttnThreads;
     const int b0 = tid * per;
-    const int64_t most = (int64_t)p.columns * p.c.page;
-    auto steps_of = [&](int b) -> int {
-      if (p.selected) return (int)(((int64_t)p.n_selected * p.c.page + kStep - 1) / kStep);
-      int64_t n = max(__ldg(p.lengths + b), 0);
-      if (n > most) {
-        p.c.report();
-        n = most;
-      }
-      return (int)((n + kStep - 1) / kStep);
-    };
     int sum = 0;
     for (int i = 0; i < per; ++i)
       if (b0 + i < p.B) sum += steps_of(b0 + i);
@@ -223,16 +248,14 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
     __syncthreads();
     if (blockIdx.x == 0)
       for (int i = tid; i <= p.B; i += kAttnThreads) p.prefix[i] = prefix[i];
+    allow_next_launch();
+    units = (int64_t)prefix[p.B] * heads;
+    if (units == 0) return;
+    const int ctas = (int)min((int64_t)p.ctas, units);
+    if ((int)blockIdx.x >= ctas) return;
+    u = range_begin(units, ctas, blockIdx.x);
+    u_end = range_begin(units, ctas, blockIdx.x + 1);
   }
-  allow_next_launch();
-  const int heads = p.c.Hkv * p.mt;
-  const int64_t units = (int64_t)prefix[p.B] * heads;
-  if (units == 0) return;
-  const int ctas = (int)min((int64_t)p.ctas, units);
-  if ((int)blockIdx.x >= ctas) return;
-  int64_t u = range_begin(units, ctas, blockIdx.x);
-  const int64_t u_end = range_begin(units, ctas, blockIdx.x + 1);
-  bool first_segment = true;
 
   const uint32_t ring = shared_address(smem) + warp * (kStages * A::kStage);
   const uint8_t* my_ring = smem + warp * (kStages * A::kStage);
@@ -258,17 +281,27 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
 
   while (u < u_end) {
     // the segment: steps [s0, s1) of row tile m of head h of sequence b
-    int lo = 0, hi = p.B;  // last b with prefix[b] * heads <= u
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if ((int64_t)prefix[mid] * heads <= u) lo = mid; else hi = mid;
+    int b, hm, steps, s0, s1;
+    if (CLUSTER) {
+      const int hh = blockIdx.x / p.cluster, rank = blockIdx.x - hh * p.cluster;
+      b = hh / heads;
+      hm = hh - b * heads;
+      steps = steps_of(b);
+      s0 = (int)((int64_t)steps * rank / p.cluster);
+      s1 = (int)((int64_t)steps * (rank + 1) / p.cluster);
+    } else {
+      int lo = 0, hi = p.B;  // last b with prefix[b] * heads <= u
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if ((int64_t)prefix[mid] * heads <= u) lo = mid; else hi = mid;
+      }
+      b = lo;
+      steps = prefix[b + 1] - prefix[b];
+      const int64_t off = u - (int64_t)prefix[b] * heads;
+      hm = (int)(off / steps);
+      s0 = (int)(off - (int64_t)hm * steps);
+      s1 = (int)min((int64_t)steps, s0 + (u_end - u));
     }
-    const int b = lo;
-    const int steps = prefix[b + 1] - prefix[b];
-    const int64_t off = u - (int64_t)prefix[b] * heads;
-    const int hm = (int)(off / steps);
-    const int s0 = (int)(off - (int64_t)hm * steps);
-    const int s1 = (int)min((int64_t)steps, s0 + (u_end - u));
     const int h = hm / p.mt, row0 = (hm - h * p.mt) * RP;
     const int len = max(__ldg(p.lengths + b), 0);
     const int64_t bh = (int64_t)b * p.c.Hkv + h;
@@ -652,23 +685,50 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
       sl[tid] = sum;
     }
     __syncthreads();
+    auto write = [&](int r, int ch, float v) {
+      const int64_t at = (bh * p.rows + row0 + r) * D + ch;
+      if (p.out_f32)
+        static_cast<float*>(p.out)[at] = v;
+      else
+        static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v);
+    };
+    auto sum_of_warps = [&](int x) {
+      const int r = x / D;
+      float t = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kAttnWarps; ++w) t = fmaf(so[w * RP * D + x], sf[w * RP + r], t);
+      return t;
+    };
+    if (CLUSTER) {
+      // the CTA's O in place of its first warp's; then each CTA joins a share of it
+      for (int x = tid; x < RP * D; x += kAttnThreads) so[x] = sum_of_warps(x);
+      cluster_barrier();
+      const int rank = blockIdx.x % p.cluster;
+      const int n = min(RP, p.rows - row0) * D;
+      for (int x = rank * kAttnThreads + tid; x < n; x += p.cluster * kAttnThreads) {
+        const int r = x / D, ch = x % D;
+        float top = kNoMax, sum = 0.0f, t = 0.0f;
+        for (int k = 0; k < p.cluster; ++k) top = fmaxf(top, peer_word(sm + r, k));
+        for (int k = 0; k < p.cluster; ++k) {
+          const float f = exp2_fast(peer_word(sm + r, k) - top);
+          sum = fmaf(peer_word(sl + r, k), f, sum);
+          t = fmaf(peer_word(so + x, k), f, t);
+        }
+        write(r, ch, t * (sum == 0.0f ? 0.0f : 1.0f / sum));
+        if (ch == 0) p.lse[bh * p.rows + row0 + r] = (top + log2f(sum)) * kLn2;
+      }
+      cluster_barrier();  // no CTA leaves while another reads its memory
+      return;
+    }
     const bool whole = s0 == 0 && s1 == steps;
     float* slot = p.partial + (int64_t)(2 * blockIdx.x + (first_segment ? 0 : 1)) * A::kSlot;
     for (int x = tid; x < RP * D; x += kAttnThreads) {
-      const int r = x / D, ch = x % D;
-      float t = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kAttnWarps; ++w) t = fmaf(so[(w * RP + r) * D + ch], sf[w * RP + r], t);
-      if (!whole) {
+      const int r = x / D;
+      const float t = sum_of_warps(x);
+      if (!whole)
         slot[2 * RP + x] = t;
-      } else if (row0 + r < p.rows) {
-        t *= sl[r] == 0.0f ? 0.0f : 1.0f / sl[r];
-        const int64_t at = (bh * p.rows + row0 + r) * D + ch;
-        if (p.out_f32)
-          static_cast<float*>(p.out)[at] = t;
-        else
-          static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(t);
-      }
+      else if (row0 + r < p.rows)
+        write(r, x % D, t * (sl[r] == 0.0f ? 0.0f : 1.0f / sl[r]));
     }
     if (tid < RP) {
       if (!whole) {
@@ -762,19 +822,22 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const AttnParams
   write(make_float4(t.x * inv, t.y * inv, t.z * inv, t.w * inv), (top + log2f(sum)) * kLn2);
 }
 
-// CTAs of the attention launch: as many as run at once
-int attn_ctas(int nt, int sms) { return nt == 1 ? kPerSm * sms : sms; }
-
 template <int D, int NG, int NT, bool TWICE>
 cudaError_t launch_attn(const AttnParams& p, int grid, cudaStream_t st) {
   using A = Attn<D, NG, NT, TWICE>;
-  const size_t smem = A::kSmem + (size_t)(p.B + 1) * sizeof(int);
   constexpr size_t most = A::kSmem + (size_t)(kMostSequences + 1) * sizeof(int);
   static_assert(most <= 210 * 1024, "shared memory");
-  cudaError_t e = allow_shared_memory<kv4_attn_kernel<D, NG, NT, TWICE>>((int)most);
+  if (p.cluster) {
+    cudaError_t e = allow_shared_memory<kv4_attn_kernel<D, NG, NT, TWICE, true>>(A::kSmem);
+    if (e != cudaSuccess) return e;
+    return launch_dependent_clusters(kv4_attn_kernel<D, NG, NT, TWICE, true>, dim3(grid),
+                                     dim3(kAttnThreads), p.cluster, A::kSmem, st, p);
+  }
+  const size_t smem = A::kSmem + (size_t)(p.B + 1) * sizeof(int);
+  cudaError_t e = allow_shared_memory<kv4_attn_kernel<D, NG, NT, TWICE, false>>((int)most);
   if (e != cudaSuccess) return e;
-  e = launch_dependent(kv4_attn_kernel<D, NG, NT, TWICE>, dim3(grid), dim3(kAttnThreads), smem, st,
-                       p);
+  e = launch_dependent(kv4_attn_kernel<D, NG, NT, TWICE, false>, dim3(grid), dim3(kAttnThreads),
+                       smem, st, p);
   if (e != cudaSuccess) return e;
   return launch_dependent(kv4_join_kernel<D, A::RP>,
                           dim3(p.B * p.c.Hkv * p.mt, p.rows < A::RP ? p.rows : A::RP),
@@ -789,7 +852,44 @@ cudaError_t launch_attn(const AttnParams& p, int grid, cudaStream_t st) {
   return launch_attn<D, NG, 2, false>(p, grid, st);
 }
 
-size_t prefix_bytes(int B) { return ((size_t)(B + 1) * sizeof(int) + 15) / 16 * 16; }
+// How a call is split: by its sizes only, so that the workspace's size is known
+// beforehand.
+struct AttnSplit {
+  int nt, mt;      // tiles of 8 rows a CTA, row tiles a head
+  int64_t steps;   // of a sequence, by the room of its table or list
+  int ctas, grid, cluster;
+  size_t prefix_bytes, workspace;
+};
+AttnSplit attn_split(int B, int kv_heads, int64_t rows, int64_t tokens, int D, int sms) {
+  AttnSplit s{};
+  s.nt = rows <= 8 ? 1 : 2;
+  s.mt = (int)((rows + 8 * s.nt - 1) / (8 * s.nt));
+  s.steps = (tokens + kStep - 1) / kStep;
+  s.ctas = s.nt == 1 ? kPerSm * sms : sms;  // as many as run at once
+  const int64_t heads = (int64_t)B * kv_heads * s.mt;
+  // A cluster a head where that leaves no CTA with more to do than ranges over
+  // all CTAs would: those cost most CTAs a second start and everyone the second
+  // launch, about kSegmentSteps steps.
+  int64_t share = s.ctas / heads < kMostCluster ? s.ctas / heads : kMostCluster;
+  if (share > s.steps) share = s.steps;
+  if (share >= 1 && (s.steps + share - 1) / share <= s.steps * heads / s.ctas + kSegmentSteps) {
+    s.cluster = (int)share;
+    s.grid = (int)(heads * share);
+    return s;
+  }
+  if (heads * kMostParts < s.ctas) s.ctas = (int)(heads * kMostParts);
+  if (s.steps * heads < s.ctas) s.ctas = (int)(s.steps * heads);  // no more than units
+  s.grid = s.ctas;
+  s.prefix_bytes = ((size_t)(B + 1) * sizeof(int) + 15) / 16 * 16;
+  s.workspace = s.prefix_bytes + (size_t)2 * s.ctas * 8 * s.nt * (D + 2) * sizeof(float);
+  return s;
+}
+
+// Tokens that a call may see of a sequence; 0 for sizes that no call takes.
+int64_t attn_tokens(int page_size, int columns, int n_selected) {
+  if (page_size <= 0 || columns <= 0 || n_selected < 0) return 0;
+  return (int64_t)page_size * (n_selected > 0 ? n_selected : columns);
+}
 
 }  // namespace
 }  // namespace bsattn
@@ -798,14 +898,14 @@ using namespace bsattn;
 
 extern "C" {
 
-size_t bsattn_kv4_attn_workspace(int B, int H, int kv_heads, int T, int D) {
-  if (B <= 0 || H <= 0 || kv_heads <= 0 || T <= 0 || H % kv_heads != 0 || (D != 64 && D != 128))
-    return 0;
+size_t bsattn_kv4_attn_workspace(int B, int H, int kv_heads, int T, int D, int page_size,
+                                 int columns, int n_selected) {
+  const int64_t tokens = attn_tokens(page_size, columns, n_selected);
+  if (B <= 0 || H <= 0 || kv_heads <= 0 || T <= 0 || H % kv_heads != 0 || tokens == 0) return 0;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  const int nt = (int64_t)(H / kv_heads) * T <= 8 ? 1 : 2;
-  return prefix_bytes(B) +
-         (size_t)2 * attn_ctas(nt, device_sm_count(dev)) * 8 * nt * (D + 2) * sizeof(float);
+  return attn_split(B, kv_heads, (int64_t)(H / kv_heads) * T, tokens, D, device_sm_count(dev))
+      .workspace;
 }
 
 bsattn_status bsattn_kv4_attn(const bsattn_kv4_cache* cache, const void* q, int B, int H, int T,
@@ -816,7 +916,7 @@ bsattn_status bsattn_kv4_attn(const bsattn_kv4_cache* cache, const void* q, int 
   AttnParams p{};
   const bsattn_status rc = check_cache(cache, &p.c);
   if (rc != BSATTN_OK) return rc;
-  if (!q || !out || !lse || !workspace || !aligned16(q) || !aligned16(out) || !aligned16(lse) ||
+  if (!q || !out || !lse || !aligned16(q) || !aligned16(out) || !aligned16(lse) ||
       !aligned16(workspace))
     return BSATTN_ERR_INVALID_ARG;
   if (!block_table || !lengths || ((reinterpret_cast<uintptr_t>(block_table) |
@@ -829,20 +929,19 @@ bsattn_status bsattn_kv4_attn(const bsattn_kv4_cache* cache, const void* q, int 
   if (flags & ~(unsigned)BSATTN_OUT_F32) return BSATTN_ERR_INVALID_ARG;
   if (!std::isfinite(scale)) return BSATTN_ERR_INVALID_ARG;
   const int64_t rows = (int64_t)(H / cache->kv_heads) * T;
-  const int64_t listed = selected ? n_selected : columns;  // pages a sequence
-  const int64_t steps = (listed * cache->page_size + kStep - 1) / kStep;
-  const int nt = rows <= 8 ? 1 : 2;
-  const int mt = (int)((rows + 8 * nt - 1) / (8 * nt));
-  if (rows > 128 || B > kMostSequences || steps * B >= (1ll << 31) ||
+  if (rows > 128 || B > kMostSequences ||
       (int64_t)columns * cache->page_size > (1ll << 31) - kStep ||  // positions are 32-bit
-      (int64_t)B * cache->kv_heads * mt >= (1ll << 31) ||
       (int64_t)cache->pages * cache->kv_heads * cache->page_size / kTile >= (1ll << 31))
     return BSATTN_ERR_UNSUPPORTED;
-  if (workspace_bytes < bsattn_kv4_attn_workspace(B, H, cache->kv_heads, T, cache->head_dim) ||
-      workspace_bytes == 0)
-    return BSATTN_ERR_INVALID_ARG;
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) return BSATTN_ERR_CUDA;
+  const AttnSplit split =
+      attn_split(B, cache->kv_heads, rows, attn_tokens(cache->page_size, columns, n_selected),
+                 cache->head_dim, device_sm_count(dev));
+  if (split.steps * B >= (1ll << 31) || (int64_t)B * cache->kv_heads * split.mt >= (1ll << 31))
+    return BSATTN_ERR_UNSUPPORTED;
+  if (split.workspace > 0 && (!workspace || workspace_bytes < split.workspace))
+    return BSATTN_ERR_INVALID_ARG;
   p.q = static_cast<const uint16_t*>(q);
   p.table = block_table;
   p.table_stride = table_stride;
@@ -853,27 +952,16 @@ bsattn_status bsattn_kv4_attn(const bsattn_kv4_cache* cache, const void* q, int 
   p.B = B;
   p.T = T;
   p.rows = (int)rows;
-  p.mt = mt;
+  p.mt = split.mt;
   p.scale_log2 = (float)((double)scale * 1.4426950408889634074);
   p.out = out;
   p.lse = lse;
   p.out_f32 = (flags & BSATTN_OUT_F32) ? 1 : 0;
   p.prefix = static_cast<int*>(workspace);
-  p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + prefix_bytes(B));
-  p.ctas = attn_ctas(nt, device_sm_count(dev));
-  const int64_t most = steps * B * cache->kv_heads * mt;  // units, at most
-  const int64_t heads = (int64_t)B * cache->kv_heads * mt;
-  if (heads * kMostParts < p.ctas) p.ctas = (int)(heads * kMostParts);
-  if (selected && heads <= p.ctas) {
-    // Every head has the same steps: whole CTAs a head, unless that leaves each
-    // of them with more to do than cutting through heads (which costs most CTAs
-    // a second start and join, about kSegmentSteps steps) would.
-    const int64_t share = p.ctas / heads < steps ? p.ctas / heads : steps;
-    if ((steps + share - 1) / share <= steps * heads / p.ctas + kSegmentSteps)
-      p.ctas = (int)(heads * share);
-  }
-  const int grid = (int)(most < p.ctas ? most : p.ctas);
-  p.ctas = grid;
+  p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + split.prefix_bytes);
+  p.ctas = split.ctas;
+  p.cluster = split.cluster;
+  const int grid = split.grid;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int groups = cache->head_dim / cache->group;
   cudaError_t e;

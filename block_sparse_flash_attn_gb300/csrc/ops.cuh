@@ -31,6 +31,28 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
                     pack_bf16(f[6], f[7]));
 }
 
+// The same in clusters of `cluster` CTAs (along x).
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_dependent_clusters(void (*kernel)(KArgs...), dim3 grid, dim3 block,
+                                             int cluster, size_t smem, cudaStream_t stream,
+                                             Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, KArgs(args)...);
+}
+
 // Lets a kernel have `bytes` of dynamic shared memory; asks once a device.
 template <auto Kernel>
 inline cudaError_t allow_shared_memory(int bytes) {

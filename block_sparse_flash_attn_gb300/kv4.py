@@ -230,12 +230,13 @@ def kv4_attn(cache: Kv4Cache, q: torch.Tensor, block_table: torch.Tensor, length
             tensor("lse", lse, (torch.float32,), q.shape[:3], cache.device)
         if B:
             lib = _bs.load()
-            nbytes = _attn_workspace(cache.device.index, B, H, cache.kv_heads, T, cache.head_dim)
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=cache.device)
+            nbytes = _attn_workspace(cache.device.index, B, H, cache.kv_heads, T, cache.head_dim,
+                                     cache.page_size, columns, n_selected)
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=cache.device) if nbytes else None
             _bs._check(lib.bsattn_kv4_attn(
                 cache._ref, q.data_ptr(), B, H, T, block_table.data_ptr(), stride, columns,
                 lengths.data_ptr(), pointer(selected), n_selected, float(scale),
-                _bs.OUT_F32 if out_f32 else 0, out.data_ptr(), lse.data_ptr(), ws.data_ptr(),
+                _bs.OUT_F32 if out_f32 else 0, out.data_ptr(), lse.data_ptr(), pointer(ws),
                 nbytes, on), "bsattn_kv4_attn")
     return out, lse
 

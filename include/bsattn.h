@@ -547,7 +547,7 @@ bsattn_status bsattn_kv4_read(const bsattn_kv4_cache* cache, int B, int T,
  *   lengths    cached tokens, the T new ones included.
  *   keep       >= sink + recent;  sink >= 0;  recent >= 1.
  *   selected   device int32 [B][kv_heads][keep]: pages (p / page_size) ascending, then -1.
- *   workspace  bsattn_kv4_select_workspace bytes, 16-byte aligned.
+ *   workspace  bsattn_kv4_select_workspace bytes (may be none), 16-byte aligned.
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA.
  */
 size_t bsattn_kv4_select_workspace(int B, int kv_heads, int columns);
@@ -574,10 +574,11 @@ bsattn_status bsattn_kv4_select(const bsattn_kv4_cache* cache, const void* q, in
  *   scale      finite; multiplies q.k.
  *   flags      BSATTN_OUT_F32.
  *   out        device bf16 (fp32) [B][H][T][head_dim];  lse  device fp32 [B][H][T].
- *   workspace  bsattn_kv4_attn_workspace bytes, 16-byte aligned.
+ *   workspace  bsattn_kv4_attn_workspace bytes (may be none), 16-byte aligned.
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA.
  */
-size_t bsattn_kv4_attn_workspace(int B, int H, int kv_heads, int T, int D);
+size_t bsattn_kv4_attn_workspace(int B, int H, int kv_heads, int T, int D, int page_size,
+                                 int columns, int n_selected);
 bsattn_status bsattn_kv4_attn(const bsattn_kv4_cache* cache, const void* q, int B, int H, int T,
                               const int32_t* block_table, int64_t table_stride, int columns,
                               const int32_t* lengths, const int32_t* selected, int n_selected,

@@ -415,3 +415,49 @@ def test_refusals(bs):
         bs.kv4_read(cache, table, n, 1, _i32([1, 2]))
     with pytest.raises(bs.BsattnError):
         bs.kv4_attn(cache, q, table, n, scale=float("inf"))
+
+
+def test_workspaces_too_small_are_refused(bs):
+    """Long contexts and long page lists need a workspace; without enough of it nothing is launched."""
+    cache = bs.Kv4Cache(3000, 1, 64, page_size=16)
+    table = torch.arange(3000, dtype=torch.int32, device="cuda").expand(1, -1).repeat(1, 4).contiguous()
+    q = torch.zeros(1, 1, 1, 64, dtype=torch.bfloat16, device="cuda")
+    n, lib = _i32([100]), bs.load()
+    out, lse = torch.full_like(q, 7.0), torch.zeros(1, 1, 1, device="cuda")
+    sel = torch.full((1, 1, 4), 7, dtype=torch.int32, device="cuda")
+    need = lib.bsattn_kv4_attn_workspace(1, 1, 1, 1, 64, 16, 12000, 0)
+    pages = lib.bsattn_kv4_select_workspace(1, 1, 12000)
+    assert need > 0 and pages == 4 * 12000
+    ws = torch.zeros(max(need, pages), dtype=torch.uint8, device="cuda")
+    on = torch.cuda.current_stream().cuda_stream
+    for ptr, size in ((ws.data_ptr(), need - 1), (None, need), (ws.data_ptr() + 8, need)):
+        assert lib.bsattn_kv4_attn(cache._ref, q.data_ptr(), 1, 1, 1, table.data_ptr(), 12000, 12000, n.data_ptr(),
+                                   None, 0, 0.1, 0, out.data_ptr(), lse.data_ptr(), ptr, size, on) == bs.ERR_INVALID_ARG
+    for ptr, size in ((ws.data_ptr(), pages - 1), (None, pages), (ws.data_ptr() + 8, pages)):
+        assert lib.bsattn_kv4_select(cache._ref, q.data_ptr(), 1, 1, 1, table.data_ptr(), 12000, 12000, n.data_ptr(),
+                                     4, 1, 1, sel.data_ptr(), ptr, size, on) == bs.ERR_INVALID_ARG
+    torch.cuda.synchronize()
+    assert bool((out == 7).all()) and bool((sel == 7).all())
+
+
+#          Hkv G  D    page group T  lengths, table columns behind them: on both sides of each split
+SPLITS = [
+    (1, 4, 128, 64, 128, 1, [20000], 0),             # one head over many CTAs
+    (1, 2, 64, 16, 32, 1, [129, 5000, 1, 0, 640], 900),   # a wide table, short sequences
+    (8, 8, 128, 16, 128, 1, [300] * 30 + [2500], 0),      # heads more than CTAs, ragged
+    (2, 4, 128, 32, 64, 2, [1000, 900], 0),          # clusters of 8
+    (8, 1, 64, 64, 64, 1, [700] * 9, 0),             # clusters of 4
+    (2, 4, 128, 16, 32, 4, [513, 90], 800),          # 16 rows, ranges
+]
+
+
+@pytest.mark.parametrize("case", SPLITS, ids=str)
+def test_splits(bs, case):
+    *rest, extra = case
+    cache, table, q, n = _attn_case(bs, tuple(rest))
+    if extra:
+        table = torch.cat([table, torch.full((table.shape[0], extra), -1, dtype=torch.int32, device="cuda")], 1)
+    lengths = rest[-1]
+    o, lse = bs.kv4_attn(cache, q, table, n, out_f32=True)
+    bs.kv4_status(cache)
+    _check_attn(o, lse, ref.attn(cache, q, table, lengths), True)

@@ -130,7 +130,7 @@ def test_caches(bs, change, status):
     ("select", PAGES, dict(columns=20000, stride=20000, nbytes=8), 1), ("select", PAGES, dict(out=None), 1),
     ("attn", ATTN, dict(q=None), 1), ("attn", ATTN, dict(out=ODD), 1), ("attn", ATTN, dict(lse=None), 1),
     ("attn", ATTN, dict(T=65), 2), ("attn", ATTN, dict(scale=float("nan")), 1), ("attn", ATTN, dict(flags=1), 1),
-    ("attn", ATTN, dict(selected=FAKE), 1), ("attn", ATTN, dict(n=3), 1), ("attn", ATTN, dict(nbytes=0), 1),
+    ("attn", ATTN, dict(selected=FAKE), 1), ("attn", ATTN, dict(n=3), 1), ("attn", ATTN, dict(H=0), 1),
     ("attn", ATTN, dict(table=None), 1), ("attn", ATTN, dict(columns=1 << 27), 2), ("attn", ATTN, dict(B=4097), 2),
     ("attn", ATTN, dict(H=5), 1)], ids=lambda c: str(c) if len(str(c)) < 40 else "")
 def test_cache_calls(bs, call, good, change, status):

@@ -376,14 +376,19 @@ __device__ __forceinline__ void score_pages(const PagesParams& p, int b, int h, 
   const int tiles = (p.rows + 15) / 16;
   const int* table = p.table + b * p.table_stride;
   bool waiting = true;
-  for (int base = first; base < end; base += kPageWarps * kAtOnce * 8) {
+  constexpr int kRound = kPageWarps * kAtOnce * 8;
+  int next[kAtOnce];  // the table's answers for the next round
+  auto look_up = [&](int at) {
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) next[k] = at + 8 * k < end ? __ldg(table + at + 8 * k) : -1;
+  };
+  look_up(first + warp * (kAtOnce * 8) + g);
+  for (int base = first; base < end; base += kRound) {
     const int at = base + warp * (kAtOnce * 8) + g;
     int pg[kAtOnce];
 #pragma unroll
-    for (int k = 0; k < kAtOnce; ++k) {
-      pg[k] = -1;
-      if (at + 8 * k < end) pg[k] = __ldg(table + at + 8 * k);
-    }
+    for (int k = 0; k < kAtOnce; ++k) pg[k] = next[k];
+    look_up(at + kRound);
     uint4 w[kAtOnce][C];
 #pragma unroll
     for (int k = 0; k < kAtOnce; ++k) {

@@ -124,7 +124,7 @@ __device__ __forceinline__ void cluster_barrier() {
 __device__ __forceinline__ float peer_word(const float* shared, int rank) {
   uint32_t at;
   float v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(shared_address(shared)), "r"(rank));
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(shared_address(shared)), "r"(rank));
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
   return v;
 }
@@ -707,12 +707,22 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
       const int n = min(RP, p.rows - row0) * D;
       for (int x = rank * kAttnThreads + tid; x < n; x += p.cluster * kAttnThreads) {
         const int r = x / D, ch = x % D;
+        float m[kMostCluster], l8[kMostCluster], v[kMostCluster];
+#pragma unroll
+        for (int k = 0; k < kMostCluster; ++k) {  // (all loads at once)
+          const bool there = k < p.cluster;
+          m[k] = there ? peer_word(sm + r, k) : kNoMax;
+          l8[k] = there ? peer_word(sl + r, k) : 0.0f;
+          v[k] = there ? peer_word(so + x, k) : 0.0f;
+        }
         float top = kNoMax, sum = 0.0f, t = 0.0f;
-        for (int k = 0; k < p.cluster; ++k) top = fmaxf(top, peer_word(sm + r, k));
-        for (int k = 0; k < p.cluster; ++k) {
-          const float f = exp2_fast(peer_word(sm + r, k) - top);
-          sum = fmaf(peer_word(sl + r, k), f, sum);
-          t = fmaf(peer_word(so + x, k), f, t);
+#pragma unroll
+        for (int k = 0; k < kMostCluster; ++k) top = fmaxf(top, m[k]);
+#pragma unroll
+        for (int k = 0; k < kMostCluster; ++k) {
+          const float f = exp2_fast(m[k] - top);
+          sum = fmaf(l8[k], f, sum);
+          t = fmaf(v[k], f, t);
         }
         write(r, ch, t * (sum == 0.0f ? 0.0f : 1.0f / sum));
         if (ch == 0) p.lse[bh * p.rows + row0 + r] = (top + log2f(sum)) * kLn2;

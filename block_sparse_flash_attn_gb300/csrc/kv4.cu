@@ -19,7 +19,7 @@ namespace bsattn {
 namespace {
 
 constexpr int kRowThreads = 128;  // write_rounded_mean takes a CTA of 128
-constexpr int kReadRows = 2;      // rows a lane group reads back at once
+constexpr int kReadRows = 4;      // rows a lane group reads back at once
 constexpr float kLeastStep = 7.888609e-31f;  // 2^-100
 
 struct AppendParams {
@@ -243,22 +243,31 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const ReadParams 
   const int count = p.counts ? min(__ldg(p.counts + b), p.T) : p.T;
   const int64_t start = __ldg(p.start + b);
   const int* table = p.table + b * p.table_stride;
+  // the table's answers for all rows, then all rows' loads
+  int pg[kReadRows];
+#pragma unroll
+  for (int u = 0; u < kReadRows; ++u) {
+    const int t = t0 + u * kGroups;
+    const int64_t logical = (start + t) >> p.c.log_page;
+    pg[u] = -2;  // nothing to read
+    if (t < count) pg[u] = logical >= 0 && logical < p.columns ? __ldg(table + logical) : -1;
+  }
   uint2 code[kReadRows][2];
   uint32_t sc[kReadRows][2];
 #pragma unroll
   for (int u = 0; u < kReadRows; ++u) {
-    const int t = t0 + u * kGroups;
+    const bool there = pg[u] >= 0 && pg[u] < p.c.pages;
+    if (!there && pg[u] != -2) p.c.report();
+    const int64_t row =
+        p.c.row(there ? pg[u] : 0, h, (int)((start + t0 + u * kGroups) & (p.c.page - 1)));
     code[u][0] = code[u][1] = make_uint2(0, 0);
     sc[u][0] = sc[u][1] = 0u;
-    if (t >= count) continue;
-    const int64_t pos = start + t;
-    const int pg = page_at(p.c, table, p.columns, pos >> p.c.log_page);
-    if (pg < 0) continue;
-    const int64_t row = p.c.row(pg, h, (int)(pos & (p.c.page - 1)));
-    code[u][0] = reinterpret_cast<const uint2*>(p.c.k_codes)[row * L + cl];
-    code[u][1] = reinterpret_cast<const uint2*>(p.c.v_codes)[row * L + cl];
-    sc[u][0] = reinterpret_cast<const uint32_t*>(p.c.k_scales)[row * NG + cl / GL];
-    sc[u][1] = reinterpret_cast<const uint32_t*>(p.c.v_scales)[row * NG + cl / GL];
+    if (there) {
+      code[u][0] = reinterpret_cast<const uint2*>(p.c.k_codes)[row * L + cl];
+      code[u][1] = reinterpret_cast<const uint2*>(p.c.v_codes)[row * L + cl];
+      sc[u][0] = reinterpret_cast<const uint32_t*>(p.c.k_scales)[row * NG + cl / GL];
+      sc[u][1] = reinterpret_cast<const uint32_t*>(p.c.v_scales)[row * NG + cl / GL];
+    }
   }
   const int64_t out = (((int64_t)b * p.c.Hkv + h) * p.T + t0) * D + cl * 16;
 #pragma unroll

@@ -94,34 +94,14 @@ __device__ __forceinline__ uint32_t shared_address(const void* p) {
 // with one instruction, each rounded as the single instruction rounds.
 // ---------------------------------------------------------------------------
 struct F2 {
-  unsigned long long v;
+  float2 v;
 };
-__device__ __forceinline__ F2 f2(float lo, float hi) {
-  F2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
-  return r;
-}
+__device__ __forceinline__ F2 f2(float lo, float hi) { return F2{make_float2(lo, hi)}; }
 __device__ __forceinline__ F2 f2(float both) { return f2(both, both); }
-__device__ __forceinline__ float2 split(F2 a) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
-  return r;
-}
-__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
-  F2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
+__device__ __forceinline__ float2 split(F2 a) { return a.v; }
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) { return F2{__fadd2_rn(a.v, b.v)}; }
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) { return F2{__fmul2_rn(a.v, b.v)}; }
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) { return F2{__ffma2_rn(a.v, b.v, c.v)}; }
 __device__ __forceinline__ F2 bf16_pair(uint32_t w) { return f2(bf16_lo(w), bf16_hi(w)); }
 __device__ __forceinline__ uint32_t pack_bf16(F2 a) {
   const float2 s = split(a);

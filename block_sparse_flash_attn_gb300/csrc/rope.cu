@@ -350,12 +350,21 @@ __global__ void __launch_bounds__(1024)
   const float* from = partial + (is_q ? 0 : (size_t)q_rows * D) + col;
   const int rows = is_q ? q_rows : k_rows;
   double t = 0.0;
-  for (int r = threadIdx.y; r < rows; r += 32) t += __ldcg(from + (size_t)r * D);
+  int r = threadIdx.y;
+  for (; r + 7 * 32 < rows; r += 8 * 32) {  // (eight loads at once)
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __ldcg(from + (size_t)(r + i * 32) * D);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t += v[i];
+  }
+  for (; r < rows; r += 32) t += __ldcg(from + (size_t)r * D);
   sh[threadIdx.y][threadIdx.x] = t;
   __syncthreads();
   if (threadIdx.y == 0) {
     double s = 0.0;
-    for (int r = 0; r < 32; ++r) s += sh[r][threadIdx.x];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) s += sh[i][threadIdx.x];
     (is_q ? dwq : dwk)[col] = (float)s;
   }
 }

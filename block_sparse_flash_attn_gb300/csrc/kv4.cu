@@ -326,6 +326,7 @@ struct PagesParams {
 
 __device__ __forceinline__ int pages_of(const PagesParams& p, int b) {
   const int64_t n = ((int64_t)max(__ldg(p.lengths + b), 0) + p.c.page - 1) >> p.c.log_page;
+  if (n > p.columns && threadIdx.x == 0) p.c.report();
   return (int)min(n, (int64_t)p.columns);
 }
 

@@ -503,7 +503,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
         }
       }
 #pragma unroll
-      for (int n = 0; n < NG; ++n) most = fmaxf(most, fmaxf(bf16_lo(v[n][0]), bf16_lo(v[n][1])));
+      for (int n = 0; n < NG; ++n) most = fmaxf(most, fmaxf(fabsf(bf16_lo(v[n][0])), fabsf(bf16_lo(v[n][1]))));
       float over = kNoMax;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {

@@ -339,34 +339,41 @@ __global__ void __launch_bounds__(32 * kBwdWarps, kBwdPerSm) rope_bwd_kernel(con
 }
 
 // Adds up the CTAs' partial weight gradients in a fixed order: 32 channels of
-// one weight a CTA, 32 rows at a time.  (A few hundred rows, in 64 bits.)
+// one weight a CTA, 32 rows at a time, a few hundred rows.  The sums carry their
+// errors along (hi + lo): as good as 64 bits, which this machine adds at 1/64 of
+// the rate.
 __global__ void __launch_bounds__(1024)
     rope_weight_kernel(const float* __restrict__ partial, int q_rows, int k_rows, int D,
                        float* __restrict__ dwq, float* __restrict__ dwk) {
-  __shared__ double sh[32][33];
+  __shared__ Sum2 sh[32][33];
   wait_for_previous_launch();
   const int col = blockIdx.x * 32 + threadIdx.x;
   const bool is_q = blockIdx.y == 0;
   const float* from = partial + (is_q ? 0 : (size_t)q_rows * D) + col;
   const int rows = is_q ? q_rows : k_rows;
-  double t = 0.0;
+  Sum2 t{0.0f, 0.0f};
   int r = threadIdx.y;
   for (; r + 7 * 32 < rows; r += 8 * 32) {  // (eight loads at once)
     float v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = __ldcg(from + (size_t)(r + i * 32) * D);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t += v[i];
+    for (int i = 0; i < 8; ++i) add_exact(t, v[i]);
   }
-  for (; r < rows; r += 32) t += __ldcg(from + (size_t)r * D);
+  for (; r < rows; r += 32) add_exact(t, __ldcg(from + (size_t)r * D));
   sh[threadIdx.y][threadIdx.x] = t;
   __syncthreads();
-  if (threadIdx.y == 0) {
-    double s = 0.0;
+  t = sh[threadIdx.x][threadIdx.y];  // warp y: channel y's 32 sums
 #pragma unroll
-    for (int i = 0; i < 32; ++i) s += sh[i][threadIdx.x];
-    (is_q ? dwq : dwk)[col] = (float)s;
+  for (int o = 16; o > 0; o >>= 1) {
+    Sum2 other;
+    other.hi = __shfl_xor_sync(0xFFFFFFFFu, t.hi, o);
+    other.lo = __shfl_xor_sync(0xFFFFFFFFu, t.lo, o);
+    add_exact(t, other);
   }
+  // (an infinite sum has no rest)
+  if (threadIdx.x == 0)
+    (is_q ? dwq : dwk)[blockIdx.x * 32 + threadIdx.y] = isfinite(t.lo) ? t.hi + t.lo : t.hi;
 }
 
 __global__ void rope_table_kernel(const double* __restrict__ inv_freq, int n_pos, int half,

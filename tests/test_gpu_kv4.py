@@ -461,3 +461,40 @@ def test_splits(bs, case):
     o, lse = bs.kv4_attn(cache, q, table, n, out_f32=True)
     bs.kv4_status(cache)
     _check_attn(o, lse, ref.attn(cache, q, table, lengths), True)
+
+
+def test_lengths_behind_the_table(bs):
+    """A length that the table has no pages for: reported; the queries see all that there is."""
+    case = (2, 4, 64, 16, 64, 2, [112, 50])
+    cache, table, q, n = _attn_case(bs, case)
+    far = _i32([5000, 50])
+    sel = bs.kv4_select(cache, q, table, far, 3)
+    with pytest.raises(bs.BsattnError):
+        bs.kv4_status(cache)
+    assert sel[0, :, -1].tolist() == [6, 6] and sel[1].tolist() == bs.kv4_select(cache, q, table, n, 3)[1].tolist()
+    o, lse = bs.kv4_attn(cache, q, table, far, out_f32=True)
+    with pytest.raises(bs.BsattnError):
+        bs.kv4_status(cache)
+    # the last query of the right length sees the same tokens
+    want, want_l = bs.kv4_attn(cache, q[:, :, 1:].contiguous(), table, n, out_f32=True)
+    assert float((o[0, :, 1:] - want[0]).abs().max()) < 1e-5 and float((lse[0, :, 1:] - want_l[0]).abs().max()) < 1e-5
+    bs.kv4_status(cache)
+
+
+def test_many_sequences(bs):
+    """The most sequences that one call takes; copies of a few give the same results."""
+    B, case = 4096, (1, 4, 64, 16, 32, 1, [37, 0, 140, 16, 1])
+    cache, table, q, n = _attn_case(bs, case)
+    at = torch.arange(B, device="cuda") % 5
+    want = bs.kv4_attn(cache, q, table, n, out_f32=True)
+    _check_attn(*want, ref.attn(cache, q, table, case[-1]), True)
+    o, lse = bs.kv4_attn(cache, q[at], table[at], n[at], out_f32=True)
+    bs.kv4_status(cache)
+    # (split otherwise: sums in another order)
+    assert torch.equal(lse.isneginf(), want[1][at].isneginf())
+    assert float((o - want[0][at]).abs().max()) < 1e-5
+    with pytest.raises(bs.BsattnError, match="unsupported"):
+        bs.kv4_attn(cache, q[at[:1]].expand(B + 1, -1, -1, -1).contiguous(), table[at[:1]].expand(B + 1, -1).contiguous(),
+                    n[at[:1]].expand(B + 1).contiguous())
+    sel = bs.kv4_select(cache, q[at], table[at], n[at], 3)
+    assert torch.equal(sel, bs.kv4_select(cache, q, table, n, 3)[at])

@@ -183,6 +183,16 @@ def test_extreme_rows(bs):
     assert not bool(dx[0, 0].isnan().any()) and not bool(dx[0, 3].isnan().any())
 
 
+def test_infinities_pass_where_nothing_turns_them(bs):
+    """Without norm, channels that are not rotated are copied, infinities too."""
+    x = torch.randn(1, 3, 3, 64, generator=ref.gen(8), device="cuda").bfloat16()
+    x[0, 1, 0, 40] = float("inf")
+    for table in (None, bs.rope_table(3, 32)):
+        for inter in (False, True):
+            q, _, _ = bs.qk_norm_rope(x, 1, 1, table=table, interleaved=inter)
+            assert float(q[0, 0, 1, 40]) == float("inf") and int(q.isfinite().sum()) == q.numel() - 1
+
+
 def test_no_tokens(bs):
     table = bs.rope_table(4, 64)
     x = torch.empty(2, 0, 6, 64, dtype=torch.bfloat16, device="cuda")

@@ -551,7 +551,14 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
             }
         }
       }
-      // ---- weights p step, as fp16 hi + lo, turned to the operand layout
+      // ---- weights p step, as fp16 hi + lo, turned to the operand layout.
+      // Every other tile takes the codes' complements: p step n + p least =
+      // -p step (15 - n) + p (15 step + least).  Codes are positive and least
+      // mostly not, so sums of either alone grow with the context while the
+      // output shrinks; in turn they stay near zero, and so do their roundings.
+      const bool odd = i & 1;
+      const uint32_t flip = odd ? 0xFFFFFFFFu : 0u;
+      const float signed_inv = odd ? -inv_top : inv_top, fifteen = odd ? 15.0f : 0.0f;
       uint32_t wh[NG][NT][2], wl[NG][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -562,7 +569,8 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
           l[nt] = l[nt] + pr;
 #pragma unroll
           for (int n = 0; n < NG; ++n) {
-            F2 least = f2(bf16_hi(v[n][t])), step = f2(bf16_lo(v[n][t]) * inv_top);
+            F2 least = f2(fmaf(bf16_lo(v[n][t]), fifteen, bf16_hi(v[n][t])));
+            F2 step = f2(bf16_lo(v[n][t]) * signed_inv);
             if (hidden) {  // 0 * NaN must stay 0
               const float2 a = split(least), c = split(step);
               const bool h0 = hidden >> (4 * nt + 2 * t) & 1, h1 = hidden >> (4 * nt + 2 * t) & 2;
@@ -587,8 +595,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
       }
       // ---- O^T += V^T P^T: of each half word, M tile 0 is made of codes 0 (rows
       // g) and 2 (rows g + 8), M tile 1 of the whole bytes, codes 0 + 16 1 and
-      // 2 + 16 3, from which tile 0 is taken off at the end: a byte is one
-      // mask, a code by itself a shift and a mask
+      // 2 + 16 3, from which tile 0 is taken off at the end.
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         uint32_t x0, x1;
@@ -602,10 +609,11 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
           x0 = __byte_perm(word(at), word(at + RB), half);
           x1 = __byte_perm(word(at + 8 * RB), word(at + 9 * RB), half);
         }
-        const uint32_t bytes[4] = {x0 & 0x00FF00FFu, __byte_perm(x0, 0u, 0x4341),
-                                   x1 & 0x00FF00FFu, __byte_perm(x1, 0u, 0x4341)};
-        const uint32_t a[4] = {x0 & 0x000F000Fu, bytes[1] & 0x000F000Fu, x1 & 0x000F000Fu,
-                               bytes[3] & 0x000F000Fu};
+        const uint32_t y0 = x0 >> 8, y1 = x1 >> 8;
+        const uint32_t bytes[4] = {(x0 ^ flip) & 0x00FF00FFu, (y0 ^ flip) & 0x00FF00FFu,
+                                   (x1 ^ flip) & 0x00FF00FFu, (y1 ^ flip) & 0x00FF00FFu};
+        const uint32_t a[4] = {(x0 ^ flip) & 0x000F000Fu, (y0 ^ flip) & 0x000F000Fu,
+                               (x1 ^ flip) & 0x000F000Fu, (y1 ^ flip) & 0x000F000Fu};
         const int n = c / A::CG;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {

@@ -39,6 +39,7 @@
 // Both join in a fixed order: results repeat bit for bit.
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda_fp16.h>
 
@@ -423,15 +424,15 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
     float inv_top = 1.2676506e30f;   // 2^100
 
     uint32_t from = 0;  // the ring's place of the tile
-#pragma unroll 1
-    for (int i = 0; i < n_tiles; ++i) {
+    auto tile = [&](int i, auto parity) {
+      constexpr bool odd = decltype(parity)::value;
       copy_wait<kStages - 2>();
       __syncwarp();
       issue(i + kStages - 1);
       const uint8_t* stage = my_ring + from;
       from = from == (kStages - 1) * A::kStage ? 0 : from + A::kStage;
       const int pos = my_tiles[i & 127].y;
-      if (pos < 0) continue;
+      if (pos < 0) return;
 
       // ---- scores (base 2): token g (t = 0) and g + 8, rows 2j and 2j + 1 as a pair
       F2 s[NT][2];
@@ -556,9 +557,8 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
       // -p step (15 - n) + p (15 step + least).  Codes are positive and least
       // mostly not, so sums of either alone grow with the context while the
       // output shrinks; in turn they stay near zero, and so do their roundings.
-      const bool odd = i & 1;
-      const uint32_t flip = odd ? 0xFFFFFFFFu : 0u;
-      const float signed_inv = odd ? -inv_top : inv_top, fifteen = odd ? 15.0f : 0.0f;
+      constexpr uint32_t flip = odd ? 0xFFFFFFFFu : 0u;
+      const float signed_inv = odd ? -inv_top : inv_top;
       uint32_t wh[NG][NT][2], wl[NG][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -569,7 +569,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
           l[nt] = l[nt] + pr;
 #pragma unroll
           for (int n = 0; n < NG; ++n) {
-            F2 least = f2(fmaf(bf16_lo(v[n][t]), fifteen, bf16_hi(v[n][t])));
+            F2 least = f2(odd ? fmaf(bf16_lo(v[n][t]), 15.0f, bf16_hi(v[n][t])) : bf16_hi(v[n][t]));
             F2 step = f2(bf16_lo(v[n][t]) * signed_inv);
             if (hidden) {  // 0 * NaN must stay 0
               const float2 a = split(least), c = split(step);
@@ -609,9 +609,10 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
           x0 = __byte_perm(word(at), word(at + RB), half);
           x1 = __byte_perm(word(at + 8 * RB), word(at + 9 * RB), half);
         }
-        const uint32_t y0 = x0 >> 8, y1 = x1 >> 8;
-        const uint32_t bytes[4] = {(x0 ^ flip) & 0x00FF00FFu, (y0 ^ flip) & 0x00FF00FFu,
-                                   (x1 ^ flip) & 0x00FF00FFu, (y1 ^ flip) & 0x00FF00FFu};
+        const uint32_t y0 = odd ? x0 >> 8 : __byte_perm(x0, 0u, 0x4341);
+        const uint32_t y1 = odd ? x1 >> 8 : __byte_perm(x1, 0u, 0x4341);
+        const uint32_t bytes[4] = {(x0 ^ flip) & 0x00FF00FFu, odd ? ~y0 & 0x00FF00FFu : y0,
+                                   (x1 ^ flip) & 0x00FF00FFu, odd ? ~y1 & 0x00FF00FFu : y1};
         const uint32_t a[4] = {(x0 ^ flip) & 0x000F000Fu, (y0 ^ flip) & 0x000F000Fu,
                                (x1 ^ flip) & 0x000F000Fu, (y1 ^ flip) & 0x000F000Fu};
         const int n = c / A::CG;
@@ -625,6 +626,11 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
           }
         }
       }
+    };
+#pragma unroll 1
+    for (int i = 0; i < n_tiles; i += 2) {
+      tile(i, std::false_type());
+      if (i + 1 < n_tiles) tile(i + 1, std::true_type());
     }
     copy_wait<0>();
 

@@ -30,6 +30,13 @@ def tensor(name: str, t, dtypes, shape=None, device=None, contiguous: bool = Tru
     return t
 
 
+def output(name: str, t, dtype, shape, device):
+    """t, checked, or a new tensor (inside launch_on)."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    return tensor(name, t, (dtype,), shape, device)
+
+
 class _Here:
     """The current device and stream are the launch's: nothing to switch."""
 

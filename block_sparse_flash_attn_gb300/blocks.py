@@ -11,7 +11,7 @@ import torch
 
 import block_sparse_flash_attn_gb300 as _bs
 
-from ._args import launch_on, pointer, tensor
+from ._args import launch_on, output, pointer, tensor
 
 
 @functools.lru_cache(maxsize=256)
@@ -60,10 +60,7 @@ def select_blocks(q: torch.Tensor, k: torch.Tensor, keep: int, causal: bool = Fa
         allow_heads = allow.shape[1]
     flags = (_bs.CAUSAL if causal else 0) | (_bs.KEY_BLOCK_64 if key_block == 64 else 0)
     with launch_on(q.device, stream) as on:
-        if out is None:
-            out = torch.empty((B, H, nb, nk), dtype=torch.uint8, device=q.device)
-        else:
-            tensor("out", out, (torch.uint8,), (B, H, nb, nk), q.device)
+        out = output("out", out, torch.uint8, (B, H, nb, nk), q.device)
         lib = _bs.load()
         nbytes = _workspace(B, H, Hkv, S, D, flags)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)

@@ -18,7 +18,7 @@ import torch
 
 import block_sparse_flash_attn_gb300 as _bs
 
-from ._args import launch_on, pointer, tensor
+from ._args import launch_on, output, pointer, tensor
 
 _I32, _BF16 = torch.int32, torch.bfloat16
 
@@ -111,8 +111,16 @@ def _queries(cache, q, B):
     return H, T
 
 
-def _strides(t):  # of batch, head and token; none where there is only one
-    return [s if n > 1 else 0 for s, n in zip(t.stride(), t.shape[:3])]
+def _rows(name, t, cache, B, T):
+    """Checks new keys or values; returns their strides of batch, head and token."""
+    tensor(name, t, (_BF16,), (B, cache.kv_heads, T, cache.head_dim), cache.device, False)
+    sb, sh, st, sd = t.stride()
+    if (sb | sh | st) % 8:  # a stride along a single entry does not matter
+        sb, sh, st = (s if n > 1 else 0 for s, n in zip((sb, sh, st), t.shape))
+    if t.numel() and (sd != 1 or (sb | sh | st) % 8 or t.data_ptr() % 16):
+        raise ValueError(f"{name}: channels must be contiguous, other strides multiples of 8 "
+                         "elements, the data 16-byte aligned")
+    return sb, sh, st
 
 
 def kv4_append(cache: Kv4Cache, k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor,
@@ -123,21 +131,15 @@ def kv4_append(cache: Kv4Cache, k: torch.Tensor, v: torch.Tensor, block_table: t
     a sequence]; lengths, counts: int32 [B].  lengths is not changed."""
     _cache(cache)
     B, stride, columns = _table(cache, block_table, lengths, counts)
-    for name, t in (("k", k), ("v", v)):
-        tensor(name, t, (_BF16,), device=cache.device, contiguous=False)
-        if t.dim() != 4 or t.shape[:2] != (B, cache.kv_heads) or t.shape[3] != cache.head_dim \
-                or t.shape != k.shape:
-            raise ValueError("k, v must be [B, kv_heads, T, head_dim]")
-        if t.numel() and (t.stride(3) != 1 or t.data_ptr() % 16 or
-                          any(s % 8 and n > 1 for s, n in zip(t.stride(), t.shape[:3]))):
-            raise ValueError(f"{name}: channels must be contiguous, other strides multiples of 8 "
-                             "elements, the data 16-byte aligned")
+    if not isinstance(k, torch.Tensor) or k.dim() != 4:
+        raise ValueError("k, v must be [B, kv_heads, T, head_dim]")
     T = k.shape[2]
+    k_strides, v_strides = _rows("k", k, cache, B, T), _rows("v", v, cache, B, T)
     if B * T == 0:
         return
     with launch_on(cache.device, stream) as on:
         _bs._check(_bs.load().bsattn_kv4_append(
-            cache._ref, k.data_ptr(), *_strides(k), v.data_ptr(), *_strides(v), B, T,
+            cache._ref, k.data_ptr(), *k_strides, v.data_ptr(), *v_strides, B, T,
             block_table.data_ptr(), stride, columns, lengths.data_ptr(), pointer(counts),
             on), "bsattn_kv4_append")
 
@@ -153,19 +155,14 @@ def kv4_read(cache: Kv4Cache, block_table: torch.Tensor, start: torch.Tensor, to
         raise ValueError("tokens must not be negative")
     shape = (B, cache.kv_heads, tokens, cache.head_dim)
     with launch_on(cache.device, stream) as on:
-        outs = []
-        for name, t in (("k", k), ("v", v)):
-            if t is None:
-                t = torch.empty(shape, dtype=_BF16, device=cache.device)
-            else:
-                tensor(name, t, (_BF16,), shape, cache.device)
-            outs.append(t)
+        k = output("k", k, _BF16, shape, cache.device)
+        v = output("v", v, _BF16, shape, cache.device)
         if B * tokens:
             _bs._check(_bs.load().bsattn_kv4_read(
                 cache._ref, B, tokens, block_table.data_ptr(), stride, columns, start.data_ptr(),
-                pointer(counts), outs[0].data_ptr(), outs[1].data_ptr(), on),
+                pointer(counts), k.data_ptr(), v.data_ptr(), on),
                 "bsattn_kv4_read")
-    return outs[0], outs[1]
+    return k, v
 
 
 def kv4_select(cache: Kv4Cache, q: torch.Tensor, block_table: torch.Tensor, lengths: torch.Tensor,
@@ -181,10 +178,7 @@ def kv4_select(cache: Kv4Cache, q: torch.Tensor, block_table: torch.Tensor, leng
     if sink < 0 or recent < 1 or keep < sink + recent:
         raise ValueError("sink must not be negative, recent at least 1, keep at least sink + recent")
     with launch_on(cache.device, stream) as on:
-        if out is None:
-            out = torch.empty((B, cache.kv_heads, keep), dtype=_I32, device=cache.device)
-        else:
-            tensor("out", out, (_I32,), (B, cache.kv_heads, keep), cache.device)
+        out = output("out", out, _I32, (B, cache.kv_heads, keep), cache.device)
         if B:
             lib = _bs.load()
             nbytes = _select_workspace(cache.device.index, B, cache.kv_heads, columns)
@@ -220,14 +214,8 @@ def kv4_attn(cache: Kv4Cache, q: torch.Tensor, block_table: torch.Tensor, length
         scale = 1.0 / math.sqrt(cache.head_dim)
     odt = torch.float32 if out_f32 else _BF16
     with launch_on(cache.device, stream) as on:
-        if out is None:
-            out = torch.empty(q.shape, dtype=odt, device=cache.device)
-        else:
-            tensor("out", out, (odt,), q.shape, cache.device)
-        if lse is None:
-            lse = torch.empty(q.shape[:3], dtype=torch.float32, device=cache.device)
-        else:
-            tensor("lse", lse, (torch.float32,), q.shape[:3], cache.device)
+        out = output("out", out, odt, q.shape, cache.device)
+        lse = output("lse", lse, torch.float32, q.shape[:3], cache.device)
         if B:
             lib = _bs.load()
             nbytes = _attn_workspace(cache.device.index, B, H, cache.kv_heads, T, cache.head_dim,

@@ -15,7 +15,7 @@ import torch
 
 import block_sparse_flash_attn_gb300 as _bs
 
-from ._args import launch_on, pointer, tensor
+from ._args import launch_on, output, pointer, tensor
 
 ROPE_INTERLEAVED, WEIGHT_F32 = 1, 2
 
@@ -110,14 +110,9 @@ def qk_norm_rope(x: torch.Tensor, heads: int, kv_heads: int, q_weight: torch.Ten
     B, S, D, n_pos, rotary, flags, sb, ss = _common(x, heads, kv_heads, q_weight, k_weight, table,
                                                     positions, interleaved)
     with launch_on(x.device, stream) as on:
-        outs = []
-        for name, t, h in (("q", q, heads), ("k", k, kv_heads), ("v", v, kv_heads)):
-            if t is None:
-                t = torch.empty((B, h, S, D), dtype=_BF16, device=x.device)
-            else:
-                tensor(name, t, (_BF16,), (B, h, S, D), x.device)
-            outs.append(t)
-        q, k, v = outs
+        q = output("q", q, _BF16, (B, heads, S, D), x.device)
+        k = output("k", k, _BF16, (B, kv_heads, S, D), x.device)
+        v = output("v", v, _BF16, (B, kv_heads, S, D), x.device)
         if B * S:
             _bs._check(_bs.load().bsattn_qk_norm_rope(
                 x.data_ptr(), sb, ss, B, S, heads, kv_heads, D,
@@ -147,10 +142,7 @@ def qk_norm_rope_bwd(x: torch.Tensor, dq: torch.Tensor, dk: torch.Tensor, dv: to
     for name, t, h in (("dq", dq, heads), ("dk", dk, kv_heads), ("dv", dv, kv_heads)):
         tensor(name, t, (_F32,), (B, h, S, D), x.device)
     with launch_on(x.device, stream) as on:
-        if dx is None:
-            dx = torch.empty(x.shape, dtype=_BF16, device=x.device)
-        else:
-            tensor("dx", dx, (_BF16,), x.shape, x.device)
+        dx = output("dx", dx, _BF16, x.shape, x.device)
         dwq = dwk = ws = None
         lib = _bs.load()
         if q_weight is not None:

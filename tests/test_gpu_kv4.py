@@ -404,7 +404,7 @@ def test_refusals(bs):
         bs.kv4_select(cache, q, table, n, 1, sink=1, recent=1)
     with pytest.raises(ValueError, match="recent"):
         bs.kv4_select(cache, q, table, n, 3, recent=0)
-    with pytest.raises(ValueError, match="k, v"):
+    with pytest.raises(ValueError, match="k must have shape|k, v"):
         bs.kv4_append(cache, k[..., :32], k, table, n)
     with pytest.raises(ValueError, match="contiguous"):
         wide = torch.zeros(1, 2, 64, 2, dtype=torch.bfloat16, device="cuda").transpose(2, 3)[:, :, :1]

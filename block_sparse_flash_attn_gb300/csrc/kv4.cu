@@ -303,9 +303,9 @@ constexpr int kPageThreads = 512;
 constexpr int kPageWarps = kPageThreads / 32;
 constexpr int kChooseThreads = 128;
 constexpr int kChooseWarps = kChooseThreads / 32;
-constexpr int kAtOnce = 4;       // groups of 8 pages that a warp has in flight
+constexpr int kTiles = 2;        // tiles of 16 pages that a warp has in flight
 constexpr int kMostRows = 128;   // G * T
-constexpr int kSplitPages = kPageWarps * kAtOnce * 8;  // a CTA of the split form scores
+constexpr int kRoundPages = kPageWarps * kTiles * 16;  // a CTA's; all of one in the split form
 constexpr int kOneCtaPages = 2048;  // one CTA reads 512 KB of means in about 8 us
 constexpr int kMostShared = 8192;   // keys in shared memory
 constexpr uint32_t kForcedPage = 0xFFFFFFFFu;
@@ -330,14 +330,14 @@ __device__ __forceinline__ int pages_of(const PagesParams& p, int b) {
   return (int)min(n, (int64_t)p.columns);
 }
 
-// Rounds the queries of (sequence, head) bh into `whole` ([16 tiles][D] bf16,
-// zero rows at the end).  All threads of the CTA.
+// Rounds the queries of (sequence, head) bh into `whole` ([rows, to a multiple
+// of 8][D] bf16, zero rows at the end).  All threads of the CTA.
 template <int D>
 __device__ __forceinline__ void round_queries(const PagesParams& p, int64_t bh, uint16_t* whole) {
   constexpr int kVec = kMostRows * 128 / 8 / kPageThreads;  // 16-byte pieces a thread, at most
   __shared__ uint32_t top[kPageWarps];
   const uint4* q = reinterpret_cast<const uint4*>(p.q + bh * p.rows * D);
-  const int pieces = p.rows * D / 8, room = (p.rows + 15) / 16 * 16 * D / 8;
+  const int pieces = p.rows * D / 8, room = (p.rows + 7) / 8 * 8 * D / 8;
   uint4 v[kVec];
   uint32_t most = 0;  // bits of the largest finite |q|
 #pragma unroll
@@ -373,9 +373,10 @@ __device__ __forceinline__ void round_queries(const PagesParams& p, int64_t bh, 
   __syncthreads();
 }
 
-// Scores pages first .. end - 1 of a sequence with n pages into keys[page -
-// offset]: each warp 8 pages a tensor tile, kAtOnce tiles at once.  The loads of
-// a round are issued before `whole` is needed (it may be filled in between).
+// Scores pages first .. end - 1 of a sequence with n pages into keys[page]: each
+// warp kTiles tiles of 16 pages at once, pages as the product's rows and
+// queries as its columns, so that a page's best query is two shuffles away.
+// The loads of a round are issued before `whole` is needed (ready() fills it).
 template <int D, typename Ready>
 __device__ __forceinline__ void score_pages(const PagesParams& p, int b, int h, int n, int first,
                                             int end, const uint16_t* whole, uint32_t* keys,
@@ -383,78 +384,72 @@ __device__ __forceinline__ void score_pages(const PagesParams& p, int b, int h, 
   constexpr int C = D / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, j = lane & 3;
-  const int tiles = (p.rows + 15) / 16;
   const int* table = p.table + b * p.table_stride;
   bool waiting = true;
-  constexpr int kRound = kPageWarps * kAtOnce * 8;
-  int next[kAtOnce];  // the table's answers for the next round
+  int next[2 * kTiles];  // the table's answers for the next round
   auto look_up = [&](int at) {
 #pragma unroll
-    for (int k = 0; k < kAtOnce; ++k) next[k] = at + 8 * k < end ? __ldg(table + at + 8 * k) : -1;
+    for (int k = 0; k < 2 * kTiles; ++k)
+      next[k] = at + 8 * k < end ? __ldg(table + at + 8 * k) : -1;
   };
-  look_up(first + warp * (kAtOnce * 8) + g);
-  for (int base = first; base < end; base += kRound) {
-    const int at = base + warp * (kAtOnce * 8) + g;
-    int pg[kAtOnce];
+  look_up(first + warp * (kTiles * 16) + g);
+  for (int base = first; base < end; base += kRoundPages) {
+    const int at = base + warp * (kTiles * 16) + g;  // this lane's pages: at + 8 k
+    bool there[2 * kTiles];
+    uint4 w[2 * kTiles][C];
 #pragma unroll
-    for (int k = 0; k < kAtOnce; ++k) pg[k] = next[k];
-    look_up(at + kRound);
-    uint4 w[kAtOnce][C];
+    for (int k = 0; k < 2 * kTiles; ++k) {
+      there[k] = next[k] >= 0 && next[k] < p.c.pages;
+      if (!there[k] && at + 8 * k < end) p.c.report();
+      // (a page that is not there: the first one's mean, and no key below)
+      const uint4* mean = reinterpret_cast<const uint4*>(
+          p.c.k_means + ((int64_t)(there[k] ? next[k] : 0) * p.c.Hkv + h) * D);
 #pragma unroll
-    for (int k = 0; k < kAtOnce; ++k) {
-      const bool there = pg[k] >= 0 && pg[k] < p.c.pages;
-      if (!there && at + 8 * k < end) p.c.report();
-      if (!there) pg[k] = -1;
-#pragma unroll
-      for (int c = 0; c < C; ++c)
-        w[k][c] = there ? reinterpret_cast<const uint4*>(
-                              p.c.k_means + ((int64_t)pg[k] * p.c.Hkv + h) * D)[4 * c + j]
-                        : make_uint4(0, 0, 0, 0);
+      for (int c = 0; c < C; ++c) w[k][c] = mean[4 * c + j];
     }
+    look_up(at + kRoundPages);
     if (waiting) ready();
     waiting = false;
-    float best[kAtOnce][2];  // of pages 2j and 2j + 1, over the rows
+    float best[2 * kTiles];
 #pragma unroll
-    for (int k = 0; k < kAtOnce; ++k) best[k][0] = best[k][1] = -INFINITY;
-    for (int m = 0; m < tiles; ++m) {
-      const uint4* row = reinterpret_cast<const uint4*>(whole + (m * 16 + g) * D);
-      float acc[kAtOnce][4];
+    for (int k = 0; k < 2 * kTiles; ++k) best[k] = -INFINITY;
+    for (int row0 = 0; row0 < p.rows; row0 += 8) {
+      const uint4* row = reinterpret_cast<const uint4*>(whole + (row0 + g) * D);
+      float acc[kTiles][4];
 #pragma unroll
-      for (int k = 0; k < kAtOnce; ++k)
+      for (int k = 0; k < kTiles; ++k)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[k][i] = 0.0f;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        const uint4 lo = row[4 * c + j], hi = row[D + 4 * c + j];  // rows g, g + 8
-        const uint32_t a0[4] = {lo.x, hi.x, lo.y, hi.y};
-        const uint32_t a1[4] = {lo.z, hi.z, lo.w, hi.w};
+        const uint4 q = row[4 * c + j];
 #pragma unroll
-        for (int k = 0; k < kAtOnce; ++k) {
-          mma_bf16(acc[k], a0, w[k][c].x, w[k][c].y);
-          mma_bf16(acc[k], a1, w[k][c].z, w[k][c].w);
+        for (int k = 0; k < kTiles; ++k) {
+          const uint4 lo = w[2 * k][c], hi = w[2 * k + 1][c];
+          const uint32_t a0[4] = {lo.x, hi.x, lo.y, hi.y};
+          const uint32_t a1[4] = {lo.z, hi.z, lo.w, hi.w};
+          mma_bf16(acc[k], a0, q.x, q.y);
+          mma_bf16(acc[k], a1, q.z, q.w);
         }
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (m * 16 + g + 8 * (i >> 1) < p.rows) {
+      for (int e = 0; e < 2; ++e)
+        if (row0 + 2 * j + e < p.rows) {
 #pragma unroll
-          for (int k = 0; k < kAtOnce; ++k) best[k][i & 1] = fmaxf(best[k][i & 1], acc[k][i]);
+          for (int k = 0; k < kTiles; ++k) {
+            best[2 * k] = fmaxf(best[2 * k], acc[k][e]);
+            best[2 * k + 1] = fmaxf(best[2 * k + 1], acc[k][2 + e]);
+          }
         }
     }
 #pragma unroll
-    for (int k = 0; k < kAtOnce; ++k) {
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) {
-        best[k][0] = fmaxf(best[k][0], __shfl_xor_sync(0xFFFFFFFFu, best[k][0], o));
-        best[k][1] = fmaxf(best[k][1], __shfl_xor_sync(0xFFFFFFFFu, best[k][1], o));
-      }
-      // lane (g, 0) writes page g: its score sits in lanes with j = g / 2
-      const float lo = __shfl_sync(0xFFFFFFFFu, best[k][0], g >> 1);
-      const float hi = __shfl_sync(0xFFFFFFFFu, best[k][1], g >> 1);
+    for (int k = 0; k < 2 * kTiles; ++k) {
+      best[k] = fmaxf(best[k], __shfl_xor_sync(0xFFFFFFFFu, best[k], 1));
+      best[k] = fmaxf(best[k], __shfl_xor_sync(0xFFFFFFFFu, best[k], 2));
       const int page = at + 8 * k;
-      if (j == 0 && page < end) {
+      if (j == (k & 3) && page < end) {
         const bool forced = page < p.sink || page >= n - p.recent;
-        keys[page] = pg[k] < 0 ? kNoPage : forced ? kForcedPage : ordered_bits(g & 1 ? hi : lo);
+        keys[page] = !there[k] ? kNoPage : forced ? kForcedPage : ordered_bits(best[k]);
       }
     }
   }
@@ -496,8 +491,8 @@ __device__ __forceinline__ int block_prefix(int v, int* slots) {
 
 // The best of n keys, by the first kChooseThreads threads of the CTA of one
 // (sequence, head): thread i holds KP consecutive keys (KP = 0: reads them again
-// each time, for more pages than registers hold).  The threshold is searched
-// as in select.cu.  (Four warps: each step of the search is a barrier.)
+// each time, for more pages than registers hold).  Four warps: each step of the
+// search is a barrier.
 template <int KP, bool SHARED>
 __device__ __forceinline__ void choose_pages(const PagesParams& p, const uint32_t* keys, int n,
                                              int* out) {
@@ -556,25 +551,15 @@ __device__ __forceinline__ void choose_pages(const PagesParams& p, const uint32_
     t = kForcedPage;
     have = forced;
   } else if (want < there) {
-    t = least + 1u;
-    uint32_t hi = top + 1u;
-    int over = forced;
-    for (int step = 0; have != want && hi - t > 1u; ++step) {
-      uint32_t m = t + (hi - t) / 2u;
-      if (step < 8 || (step & 1)) {
-        const float low = from_ordered_bits(t), high = from_ordered_bits(hi - 1u);
-        const float share = ((float)(have - want) + 0.5f) / (float)(have - over);
-        m = ordered_bits(fmaf(high - low, share, low));
-      }
-      m = min(max(m, t + 1u), hi - 1u);
+    KeySearch search(least + 1u, top, there, forced, want);
+    while (search.open()) {
+      const uint32_t c = search.probe();
       int cnt = 0;
-      each([&](uint32_t x) { cnt += x >= m ? 1 : 0; });
-      cnt = total(cnt);
-      if (cnt >= want)
-        t = m, have = cnt;
-      else
-        hi = m, over = cnt;
+      each([&](uint32_t x) { cnt += x >= c ? 1 : 0; });
+      search.count(c, total(cnt));
     }
+    t = search.t;
+    have = search.have;
   }
   // all of those above t, and the first of those equal to it
   const bool all = have == want;
@@ -615,17 +600,17 @@ __device__ __forceinline__ void choose_pages(const PagesParams& p, const uint32_
     choose_pages<0, SHARED>(p, keys, n, out);
 }
 
-// The split form: scores of kSplitPages pages a CTA, then one CTA a head.
+// The split form: scores of kRoundPages pages a CTA, then one CTA a head.
 template <int D>
 __global__ void __launch_bounds__(kPageThreads) page_scores_kernel(const PagesParams p) {
   extern __shared__ __align__(16) uint16_t whole[];
   wait_for_previous_launch();
   allow_next_launch();
   const int h = blockIdx.y, b = blockIdx.z;
-  const int n = pages_of(p, b), first = blockIdx.x * kSplitPages;
+  const int n = pages_of(p, b), first = blockIdx.x * kRoundPages;
   if (first >= n) return;
   const int64_t bh = (int64_t)b * p.c.Hkv + h;
-  score_pages<D>(p, b, h, n, first, min(n, first + kSplitPages), whole, p.keys + bh * p.columns,
+  score_pages<D>(p, b, h, n, first, min(n, first + kRoundPages), whole, p.keys + bh * p.columns,
                  [&] { round_queries<D>(p, bh, whole); });
 }
 
@@ -646,7 +631,7 @@ __global__ void __launch_bounds__(kPageThreads) select_pages_kernel(const PagesP
   const int64_t bh = blockIdx.x;
   const int b = (int)(bh / p.c.Hkv), h = (int)(bh - (int64_t)b * p.c.Hkv);
   const int n = pages_of(p, b);
-  uint32_t* keys = reinterpret_cast<uint32_t*>(whole + (p.rows + 15) / 16 * 16 * D);
+  uint32_t* keys = reinterpret_cast<uint32_t*>(whole + (p.rows + 7) / 8 * 8 * D);
   score_pages<D>(p, b, h, n, 0, n, whole, keys, [&] { round_queries<D>(p, bh, whole); });
   __syncthreads();
   if (threadIdx.x < kChooseThreads) choose_pages<true>(p, keys, n, p.out + bh * p.keep);
@@ -658,7 +643,7 @@ bool one_cta_a_head(int heads, int columns, int sms) {
 
 template <int D>
 cudaError_t launch_pages(const PagesParams& p, int B, int sms, cudaStream_t st) {
-  const size_t queries = (size_t)(p.rows + 15) / 16 * 16 * D * 2;
+  const size_t queries = (size_t)(p.rows + 7) / 8 * 8 * D * 2;
   const int heads = B * p.c.Hkv;
   if (one_cta_a_head(heads, p.columns, sms)) {
     const size_t smem = queries + (size_t)p.columns * sizeof(uint32_t);
@@ -667,7 +652,7 @@ cudaError_t launch_pages(const PagesParams& p, int B, int sms, cudaStream_t st) 
     return launch_dependent(select_pages_kernel<D>, dim3(heads), dim3(kPageThreads), smem, st, p);
   }
   cudaError_t e = launch_dependent(
-      page_scores_kernel<D>, dim3((p.columns + kSplitPages - 1) / kSplitPages, p.c.Hkv, B),
+      page_scores_kernel<D>, dim3((p.columns + kRoundPages - 1) / kRoundPages, p.c.Hkv, B),
       dim3(kPageThreads), queries, st, p);
   if (e != cudaSuccess) return e;
   return launch_dependent(choose_pages_kernel, dim3(heads), dim3(kChooseThreads), 0, st, p);

@@ -275,6 +275,55 @@ __device__ __forceinline__ float from_ordered_bits(uint32_t u) {
   return __uint_as_float((u & 0x80000000u) ? u ^ 0x80000000u : ~u);
 }
 
+__device__ __forceinline__ float log2_fast(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Search for a threshold t among ordered keys with exactly `want` keys >= t,
+// or, where equal keys leave none, for the want-th largest key.  Each step
+// probes between a key with too many at or above it (t, `have`) and one with too
+// few (hi, `over`), by interpolating the logarithm of the count between the two
+// scores: a linear tail of that is what scores have (5 to 8 steps for 768 or
+// 512 of them, against 9 by halving and up to 35 by interpolating the count).
+// An end that stays put twice counts half (the Illinois rule), and from the
+// thirteenth step on every other one halves the interval of bit patterns, so
+// that 76 steps always end it.
+struct KeySearch {
+  uint32_t t, hi;
+  int have, over, want, step, last;
+  float goal, at_t, at_hi;
+
+  // keys between least and top; `all` keys >= least, `more` of them above top
+  __device__ __forceinline__ KeySearch(uint32_t least, uint32_t top, int all, int more, int n)
+      : t(least), hi(top + 1u), have(all), over(more), want(n), step(0), last(0),
+        goal(log2_fast((float)n)), at_t(1.0f), at_hi(1.0f) {}
+  __device__ __forceinline__ bool open() const { return have != want && hi - t > 1u; }
+  __device__ __forceinline__ uint32_t probe() {
+    uint32_t c = t + (hi - t) / 2u;
+    if (step < 12 || (step & 1)) {
+      const float low = from_ordered_bits(t), high = from_ordered_bits(hi - 1u);
+      const float a = (log2_fast((float)have + 0.5f) - goal) * at_t;
+      const float b = (goal - log2_fast((float)over + 0.5f)) * at_hi;
+      c = ordered_bits(fmaf(high - low, __fdividef(a, a + b), low));
+    }
+    ++step;
+    return min(max(c, t + 1u), hi - 1u);
+  }
+  __device__ __forceinline__ void count(uint32_t c, int n) {
+    if (n >= want) {
+      t = c, have = n, at_t = 1.0f;
+      if (last > 0) at_hi *= 0.5f;
+      last = 1;
+    } else {
+      hi = c, over = n, at_hi = 1.0f;
+      if (last < 0) at_t *= 0.5f;
+      last = -1;
+    }
+  }
+};
+
 // D += A B, 16 x 8 x 16: bf16 in, 32-bit sums (A row-major, B column-major)
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {

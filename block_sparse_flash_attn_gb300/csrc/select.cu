@@ -127,10 +127,7 @@ struct RowKeys {
 };
 
 // Marks the best keys of a row: `keep` of them, or all that are forced if those
-// are more.  The threshold is searched between the row's least and largest key
-// by interpolating the counts between the two scores (they spread smoothly: six
-// to eight steps do); from the ninth step on every other one halves the
-// interval of bit patterns instead, so that 72 steps always end it.
+// are more.
 template <int KP>
 __device__ __forceinline__ void choose_row(const uint32_t* row, int n, int nk, int keep,
                                            uint8_t* out, int lane) {
@@ -149,32 +146,22 @@ __device__ __forceinline__ void choose_row(const uint32_t* row, int n, int nk, i
   least = __reduce_min_sync(0xFFFFFFFFu, least) + 1u;
   const int allowed = counts & 0xFFFF, forced = counts >> 16;
   const int want = min(max(keep, forced), allowed);
-  // at least `want` keys are >= t, fewer are >= hi; `have` of them are >= t
+  // `have` >= want keys are >= t
   uint32_t t = 1u;
   int have = allowed;
   if (want == forced) {
     t = kForced;
     have = forced;
   } else if (want < allowed) {
-    t = least;
-    uint32_t hi = top + 1u;
-    int over = forced;
-    for (int step = 0; have != want && hi - t > 1u; ++step) {
-      uint32_t c = t + (hi - t) / 2u;
-      if (step < 8 || (step & 1)) {
-        const float low = from_ordered_bits(t), high = from_ordered_bits(hi - 1u);
-        const float share = ((float)(have - want) + 0.5f) * __frcp_rn((float)(have - over));
-        c = ordered_bits(fmaf(high - low, share, low));
-      }
-      c = min(max(c, t + 1u), hi - 1u);
+    KeySearch search(least, top, allowed, forced, want);
+    while (search.open()) {
+      const uint32_t c = search.probe();
       int cnt = 0;
       keys.each(n, [&](uint32_t x) { cnt += x >= c ? 1 : 0; });
-      cnt = __reduce_add_sync(0xFFFFFFFFu, cnt);
-      if (cnt >= want)
-        t = c, have = cnt;
-      else
-        hi = c, over = cnt;
+      search.count(c, __reduce_add_sync(0xFFFFFFFFu, cnt));
     }
+    t = search.t;
+    have = search.have;
   }
   // more keys >= t than wanted: those equal to t go in from the left
   int drop_from = 0x7FFFFFFF;  // column from which keys equal to t stay out

@@ -136,6 +136,12 @@ struct Decoder {
 // in flight while one is quantised.  When the call fills the page the CTA of K
 // adds up the page's decoded keys (those of earlier calls are read back) and
 // writes their rounded mean.
+//
+// 512 bytes read and 160 written a token and head (groups of 32): the bound is
+// memory on paper, instructions in fact, some 20 a channel's lane.  8 x 4096
+// tokens (three quarters of them there), 8 heads of 128: 43 us, 69% of issue
+// slots, 2.9 TB/s; with conversions and comparisons a code 104 us, with a lane
+// for 8 channels instead of 16 59 us.
 template <int D, int GL>
 __global__ void __launch_bounds__(kRowThreads, 6) kv4_append_kernel(const AppendParams p) {
   constexpr int L = D / 16, NG = L / GL, kRows = kRowThreads / L;  // rows the CTA holds at once
@@ -231,6 +237,7 @@ struct ReadParams {
 
 // One CTA: consecutive rows of one sequence and head; a lane group (D / 16
 // lanes) decodes kReadRows of them, K and V.  Rows behind the count are zero.
+// Bound by its stores: the tokens above in 26 us, 5.1 TB/s.
 template <int D, int GL>
 __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const ReadParams p) {
   constexpr int L = D / 16, NG = L / GL;
@@ -301,13 +308,14 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const ReadParams 
 // ---------------------------------------------------------------------------
 constexpr int kPageThreads = 512;
 constexpr int kPageWarps = kPageThreads / 32;
-constexpr int kChooseThreads = 128;
-constexpr int kChooseWarps = kChooseThreads / 32;
 constexpr int kTiles = 2;        // tiles of 16 pages that a warp has in flight
 constexpr int kMostRows = 128;   // G * T
 constexpr int kRoundPages = kPageWarps * kTiles * 16;  // a CTA's; all of one in the split form
-constexpr int kOneCtaPages = 2048;  // one CTA reads 512 KB of means in about 8 us
-constexpr int kMostShared = 8192;   // keys in shared memory
+// One launch for lists up to this room: 8 heads of 500 pages 8 us (two launches 10),
+// of 2000 pages 15 us (12, but another launch for the host); 128 heads of 1000
+// pages 13 us (19).
+constexpr int kOneCtaPages = 2048;
+constexpr int kMostShared = 16 * kPageThreads;  // keys in shared memory
 constexpr uint32_t kForcedPage = 0xFFFFFFFFu;
 constexpr uint32_t kNoPage = 0u;
 
@@ -456,23 +464,26 @@ __device__ __forceinline__ void score_pages(const PagesParams& p, int b, int h, 
   if (waiting) ready();
 }
 
-// Barrier of the threads that choose (the first kChooseThreads of the CTA).
+// Barrier of the CTA's first CT threads.
+template <int CT>
 __device__ __forceinline__ void choose_barrier() {
-  asm volatile("bar.sync 1, %0;" ::"n"(kChooseThreads) : "memory");
+  asm volatile("bar.sync 1, %0;" ::"n"(CT) : "memory");
 }
 
 // Sum over those threads of one number each (two uses in a row need other slots).
+template <int CT>
 __device__ __forceinline__ int block_sum(int v, int* slots) {
   v = __reduce_add_sync(0xFFFFFFFFu, v);
   if ((threadIdx.x & 31) == 0) slots[threadIdx.x >> 5] = v;
-  choose_barrier();
+  choose_barrier<CT>();
   int s = 0;
 #pragma unroll
-  for (int w = 0; w < kChooseWarps; ++w) s += slots[w];
+  for (int w = 0; w < CT / 32; ++w) s += slots[w];
   return s;
 }
 
 // Exclusive prefix over them.
+template <int CT>
 __device__ __forceinline__ int block_prefix(int v, int* slots) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int s = v;
@@ -482,46 +493,44 @@ __device__ __forceinline__ int block_prefix(int v, int* slots) {
     if (lane >= o) s += t;
   }
   if (lane == 31) slots[warp] = s;
-  choose_barrier();
+  choose_barrier<CT>();
   int before = 0;
 #pragma unroll
-  for (int w = 0; w < kChooseWarps; ++w) before += w < warp ? slots[w] : 0;
+  for (int w = 0; w < CT / 32; ++w) before += w < warp ? slots[w] : 0;
   return before + s - v;
 }
 
-// The best of n keys, by the first kChooseThreads threads of the CTA of one
+// The best of n keys, by the first CT threads of the CTA of one
 // (sequence, head): thread i holds KP consecutive keys (KP = 0: reads them again
-// each time, for more pages than registers hold).  Four warps: each step of the
-// search is a barrier.
-template <int KP, bool SHARED>
+// each time, for more pages than registers hold).  `keys` may be shared or global
+// memory.  Each step of the search is a barrier of those threads.
+template <int KP, int CT>
 __device__ __forceinline__ void choose_pages(const PagesParams& p, const uint32_t* keys, int n,
                                              int* out) {
-  __shared__ int slots[4][kChooseWarps];
-  __shared__ uint32_t ends[2][kChooseWarps];
-  const int per = KP > 0 ? KP : (n + kChooseThreads - 1) / kChooseThreads;
+  __shared__ int slots[4][CT / 32];
+  __shared__ uint32_t ends[2][CT / 32];
+  const int per = KP > 0 ? KP : (n + CT - 1) / CT;
   const int64_t base = (int64_t)threadIdx.x * per;
+  auto read = [&](int i) -> uint32_t { return base + i < n ? keys[base + i] : kNoPage; };
   uint32_t k[KP > 0 ? KP : 1];
   if (KP > 0) {
 #pragma unroll
-    for (int i = 0; i < KP; ++i)
-      k[i] = base + i < n ? (SHARED ? keys[base + i] : __ldcg(keys + base + i)) : kNoPage;
+    for (int i = 0; i < KP; ++i) k[i] = read(i);
   }
-  auto key = [&](int i) -> uint32_t {
-    if (KP > 0) return k[i];
-    return base + i < n ? __ldcg(keys + base + i) : kNoPage;
-  };
+  auto key = [&](int i) -> uint32_t { return KP > 0 ? k[i] : read(i); };
   auto each = [&](auto f) {
     if (KP > 0) {
 #pragma unroll
       for (int i = 0; i < KP; ++i) f(k[i]);
     } else {
-      for (int i = 0; i < per; ++i) f(key(i));
+#pragma unroll 8
+      for (int i = 0; i < per; ++i) f(read(i));
     }
   };
   int turn = 0;
   auto total = [&](int c) {
     turn ^= 1;
-    return block_sum(c, slots[turn]);
+    return block_sum<CT>(c, slots[turn]);
   };
   // largest and least of the keys that are neither forced nor ruled out
   uint32_t top = 0, least = kForcedPage;
@@ -540,7 +549,7 @@ __device__ __forceinline__ void choose_pages(const PagesParams& p, const uint32_
   }
   const int there = total(c), forced = total(f);
 #pragma unroll
-  for (int w = 0; w < kChooseWarps; ++w) {
+  for (int w = 0; w < CT / 32; ++w) {
     top = max(top, ends[0][w]);
     least = min(least, ends[1][w]);
   }
@@ -568,10 +577,10 @@ __device__ __forceinline__ void choose_pages(const PagesParams& p, const uint32_
     above += (all ? x >= t : x > t) ? 1 : 0;
     equal += (!all && x == t) ? 1 : 0;
   });
-  const int before = block_prefix(above, slots[2]);
+  const int before = block_prefix<CT>(above, slots[2]);
   int taken = 0, ties = 0;
   if (!all) {
-    const int equal_before = block_prefix(equal, slots[3]);
+    const int equal_before = block_prefix<CT>(equal, slots[3]);
     ties = want - total(above);
     taken = min(equal_before, ties);
   }
@@ -586,18 +595,23 @@ __device__ __forceinline__ void choose_pages(const PagesParams& p, const uint32_
     }
     if (take) out[pos++] = (int)(base + i);
   }
-  for (int i = want + threadIdx.x; i < p.keep; i += kChooseThreads) out[i] = -1;
+  for (int i = want + threadIdx.x; i < p.keep; i += CT) out[i] = -1;
 }
 
-template <bool SHARED>
+// As many of the CTA's threads as the list needs, 4 warps for up to 2048 pages.
 __device__ __forceinline__ void choose_pages(const PagesParams& p, const uint32_t* keys, int n,
                                              int* out) {
-  if (n <= 4 * kChooseThreads)
-    choose_pages<4, SHARED>(p, keys, n, out);
-  else if (n <= 16 * kChooseThreads)
-    choose_pages<16, SHARED>(p, keys, n, out);
-  else
-    choose_pages<0, SHARED>(p, keys, n, out);
+  if (n <= 16 * 128) {
+    if (threadIdx.x >= 128) return;
+    if (n <= 4 * 128)
+      choose_pages<4, 128>(p, keys, n, out);
+    else
+      choose_pages<16, 128>(p, keys, n, out);
+  } else if (n <= 16 * kPageThreads) {
+    choose_pages<16, kPageThreads>(p, keys, n, out);
+  } else {
+    choose_pages<0, kPageThreads>(p, keys, n, out);
+  }
 }
 
 // The split form: scores of kRoundPages pages a CTA, then one CTA a head.
@@ -614,11 +628,11 @@ __global__ void __launch_bounds__(kPageThreads) page_scores_kernel(const PagesPa
                  [&] { round_queries<D>(p, bh, whole); });
 }
 
-__global__ void __launch_bounds__(kChooseThreads) choose_pages_kernel(const PagesParams p) {
+__global__ void __launch_bounds__(kPageThreads) choose_pages_kernel(const PagesParams p) {
   wait_for_previous_launch();
   allow_next_launch();
   const int64_t bh = blockIdx.x;
-  choose_pages<false>(p, p.keys + bh * p.columns, pages_of(p, (int)(bh / p.c.Hkv)),
+  choose_pages(p, p.keys + bh * p.columns, pages_of(p, (int)(bh / p.c.Hkv)),
                       p.out + bh * p.keep);
 }
 
@@ -634,7 +648,7 @@ __global__ void __launch_bounds__(kPageThreads) select_pages_kernel(const PagesP
   uint32_t* keys = reinterpret_cast<uint32_t*>(whole + (p.rows + 7) / 8 * 8 * D);
   score_pages<D>(p, b, h, n, 0, n, whole, keys, [&] { round_queries<D>(p, bh, whole); });
   __syncthreads();
-  if (threadIdx.x < kChooseThreads) choose_pages<true>(p, keys, n, p.out + bh * p.keep);
+  choose_pages(p, keys, n, p.out + bh * p.keep);
 }
 
 bool one_cta_a_head(int heads, int columns, int sms) {
@@ -655,7 +669,7 @@ cudaError_t launch_pages(const PagesParams& p, int B, int sms, cudaStream_t st) 
       page_scores_kernel<D>, dim3((p.columns + kRoundPages - 1) / kRoundPages, p.c.Hkv, B),
       dim3(kPageThreads), queries, st, p);
   if (e != cudaSuccess) return e;
-  return launch_dependent(choose_pages_kernel, dim3(heads), dim3(kChooseThreads), 0, st, p);
+  return launch_dependent(choose_pages_kernel, dim3(heads), dim3(kPageThreads), 0, st, p);
 }
 
 bool strides_ok(const int64_t (&s)[6]) {

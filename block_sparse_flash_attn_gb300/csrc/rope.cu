@@ -20,6 +20,11 @@
 // and all its rows' loads are in flight at once.  A CTA's eight warps take
 // eight consecutive tokens of the same heads, 2 KB and more of every head-major
 // row run.  The arithmetic is on register pairs (two floats an instruction).
+//
+// Measured, of a plain copy's rate: forward, 2 x 16384 tokens, 32 + 2 x 8 heads of
+// 128: 138 us, 5.9 TB/s, 88%; backward, 4 x 4096 tokens, 16 + 2 x 16 heads of 128:
+// 127 us, 6.3 TB/s, 95%.  64 tokens of a decoding step: 6 us, the launch and
+// three loads in a row (position, angles, x beside them).
 #include <cmath>
 #include <cstdint>
 

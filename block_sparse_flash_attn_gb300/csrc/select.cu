@@ -16,8 +16,12 @@
 // Cost: Q and K are read once (2 bytes an element; the bound: memory), each
 // element costs one exact addition (6 operations).  The scores are one small
 // matrix product per head on bf16 tensor instructions (whole numbers up to 128
-// are exact in bf16), the rows' k-th best is found by bisection over the
-// scores' order-preserving bit patterns, held in registers, steered by the counts.
+// are exact in bf16); a row's k-th best is searched among the scores'
+// order-preserving bit patterns, held in a warp's registers.
+//
+// Measured at 65536 tokens, 32 + 8 heads of 128, causal: means 107 us (6.3 TB/s,
+// 94% of a plain copy's rate), choice 38 us (16384 rows of up to 512 scores,
+// bound by instructions: 63% of issue slots), 143 us together.
 #include <cstdint>
 
 #include "internal.h"

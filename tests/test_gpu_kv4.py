@@ -292,6 +292,20 @@ def test_select_many_pages(bs, pages):
     assert torch.equal(got, ref.select_pages(cache, q, table, lengths, 1, 0, 1))
 
 
+@pytest.mark.parametrize("pages", [1500, 2100, 8192, 8200])
+def test_select_many_heads(bs, pages):
+    """Enough heads for one CTA each, lists on both sides of what that keeps."""
+    page, D, B, Hkv = 16, 64, 20, 8
+    cache = bs.Kv4Cache(64, Hkv, D, page_size=page, group=64)
+    ref.fill(cache, 4)
+    g = ref.gen(5)
+    table = torch.randint(0, 64, (B, pages), generator=g, device="cuda").to(torch.int32)
+    lengths = [max(1, pages * page - 5 * i * page) for i in range(B)]
+    q = torch.randn(B, Hkv, 1, D, generator=g, device="cuda").bfloat16()
+    got = bs.kv4_select(cache, q, table, _i32(lengths), 33, sink=1, recent=2)
+    assert torch.equal(got, ref.select_pages(cache, q, table, lengths, 33, 1, 2))
+
+
 def test_select_zero_queries(bs):
     cache, table, q, n = _attn_case(bs, (2, 4, 128, 16, 128, 1, [300, 40]))
     q.zero_()

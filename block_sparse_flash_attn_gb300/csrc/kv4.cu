@@ -149,9 +149,9 @@ __global__ void __launch_bounds__(kRowThreads, 6) kv4_append_kernel(const Append
   const int h = is_k ? blockIdx.y : blockIdx.y - p.c.Hkv, b = blockIdx.z;
   wait_for_previous_launch();
   allow_next_launch();
-  const int len = __ldg(p.lengths + b);
+  const int len = load(p.lengths + b);
   int cnt = p.T;
-  if (p.counts) cnt = min(max(__ldg(p.counts + b), 0), p.T);
+  if (p.counts) cnt = min(max(load(p.counts + b), 0), p.T);
   if (cnt == 0) return;
   if (len < 0) {
     if (threadIdx.x == 0) p.c.report();
@@ -169,8 +169,8 @@ __global__ void __launch_bounds__(kRowThreads, 6) kv4_append_kernel(const Append
                         (begin - len + sub) * token + cl * 16;
   uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
   if (sub < n) {
-    lo = __ldg(reinterpret_cast<const uint4*>(src));
-    hi = __ldg(reinterpret_cast<const uint4*>(src) + 1);
+    lo = load(reinterpret_cast<const uint4*>(src));
+    hi = load(reinterpret_cast<const uint4*>(src) + 1);
   }
   const int pg = page_at(p.c, p.table + b * p.table_stride, p.columns, logical);
   if (pg < 0) return;
@@ -190,8 +190,8 @@ __global__ void __launch_bounds__(kRowThreads, 6) kv4_append_kernel(const Append
     const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
     src += kRows * token;
     if ((i + 1) * kRows + sub < n) {
-      lo = __ldg(reinterpret_cast<const uint4*>(src));
-      hi = __ldg(reinterpret_cast<const uint4*>(src) + 1);
+      lo = load(reinterpret_cast<const uint4*>(src));
+      hi = load(reinterpret_cast<const uint4*>(src) + 1);
     }
     F2 x[8];
     float step, least;
@@ -247,8 +247,8 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const ReadParams 
   const int t0 = blockIdx.x * (kGroups * kReadRows) + group;
   wait_for_previous_launch();
   allow_next_launch();
-  const int count = p.counts ? min(__ldg(p.counts + b), p.T) : p.T;
-  const int64_t start = __ldg(p.start + b);
+  const int count = p.counts ? min(load(p.counts + b), p.T) : p.T;
+  const int64_t start = load(p.start + b);
   const int* table = p.table + b * p.table_stride;
   // the table's answers for all rows, then all rows' loads
   int pg[kReadRows];
@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const ReadParams 
     const int t = t0 + u * kGroups;
     const int64_t logical = (start + t) >> p.c.log_page;
     pg[u] = -2;  // nothing to read
-    if (t < count) pg[u] = logical >= 0 && logical < p.columns ? __ldg(table + logical) : -1;
+    if (t < count) pg[u] = logical >= 0 && logical < p.columns ? load(table + logical) : -1;
   }
   uint2 code[kReadRows][2];
   uint32_t sc[kReadRows][2];
@@ -333,7 +333,7 @@ struct PagesParams {
 };
 
 __device__ __forceinline__ int pages_of(const PagesParams& p, int b) {
-  const int64_t n = ((int64_t)max(__ldg(p.lengths + b), 0) + p.c.page - 1) >> p.c.log_page;
+  const int64_t n = ((int64_t)max(load(p.lengths + b), 0) + p.c.page - 1) >> p.c.log_page;
   if (n > p.columns && threadIdx.x == 0) p.c.report();
   return (int)min(n, (int64_t)p.columns);
 }
@@ -353,7 +353,7 @@ __device__ __forceinline__ void round_queries(const PagesParams& p, int64_t bh, 
     const int at = threadIdx.x + i * kPageThreads;
     v[i] = make_uint4(0, 0, 0, 0);
     if (at >= pieces) continue;
-    v[i] = __ldg(q + at);
+    v[i] = load(q + at);
     const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -398,7 +398,7 @@ __device__ __forceinline__ void score_pages(const PagesParams& p, int b, int h, 
   auto look_up = [&](int at) {
 #pragma unroll
     for (int k = 0; k < 2 * kTiles; ++k)
-      next[k] = at + 8 * k < end ? __ldg(table + at + 8 * k) : -1;
+      next[k] = at + 8 * k < end ? load(table + at + 8 * k) : -1;
   };
   look_up(first + warp * (kTiles * 16) + g);
   for (int base = first; base < end; base += kRoundPages) {
@@ -738,7 +738,7 @@ bsattn_status bsattn_kv4_append(const bsattn_kv4_cache* cache, const void* k, in
   if (!ints_ok(block_table) || !ints_ok(lengths) || (counts && !ints_ok(counts)))
     return BSATTN_ERR_INVALID_ARG;
   if (B <= 0 || T <= 0 || columns <= 0 || table_stride < 0) return BSATTN_ERR_INVALID_ARG;
-  if (B > 65535) return BSATTN_ERR_UNSUPPORTED;
+  if (B > 65535 || T > (1 << 30)) return BSATTN_ERR_UNSUPPORTED;
   if (!strides_ok({k_batch, k_head, k_token, v_batch, v_head, v_token}))
     return BSATTN_ERR_INVALID_ARG;
   p.k = static_cast<const uint16_t*>(k);

@@ -36,7 +36,7 @@ struct Kv4View {
 __device__ __forceinline__ int page_at(const Kv4View& c, const int* table, int columns,
                                        int64_t logical) {
   int pg = -1;
-  if (logical >= 0 && logical < columns) pg = __ldg(table + logical);
+  if (logical >= 0 && logical < columns) pg = load(table + logical);
   if (pg < 0 || pg >= c.pages) {
     c.report();
     pg = -1;

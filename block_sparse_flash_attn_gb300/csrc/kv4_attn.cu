@@ -46,6 +46,7 @@
 // row.
 #include <cmath>
 #include <cstdint>
+#include <mutex>
 #include <type_traits>
 
 #include <cuda_fp16.h>
@@ -168,9 +169,9 @@ __device__ __forceinline__ int tile_page(const AttnParams& p, int b, int h, int6
     if (logical >= p.n_selected) return -1;
     const int* sel = p.selected + ((int64_t)b * p.c.Hkv + h) * p.n_selected;
     const int64_t e = logical;
-    logical = __ldg(sel + e);
+    logical = load(sel + e);
     if (logical < 0) return -1;
-    if (e > 0 && logical <= __ldg(sel + e - 1)) {  // a page named twice, or out of order
+    if (e > 0 && logical <= load(sel + e - 1)) {  // a page named twice, or out of order
       p.c.report();
       return -1;
     }
@@ -225,7 +226,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
   const int64_t most = (int64_t)p.columns * p.c.page;  // tokens that the table has room for
   auto steps_of = [&](int b) -> int {
     if (p.selected) return (int)(((int64_t)p.n_selected * p.c.page + kStep - 1) / kStep);
-    int64_t n = max(__ldg(p.lengths + b), 0);
+    int64_t n = max(load(p.lengths + b), 0);
     if (n > most) {
       p.c.report();
       n = most;
@@ -317,7 +318,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
       s1 = (int)min((int64_t)steps, s0 + (u_end - u));
     }
     const int h = hm / p.mt, row0 = (hm - h * p.mt) * RP;
-    const int len = max(__ldg(p.lengths + b), 0);
+    const int len = max(load(p.lengths + b), 0);
     const int64_t bh = (int64_t)b * p.c.Hkv + h;
     const int n_tiles = s1 - s0;  // this warp's, one a step
     const int seen_by_all = len - p.T - (kTile - 1);  // tiles that begin later need the mask
@@ -373,7 +374,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
       for (int c = 0; c < C; ++c) {
         uint4 raw = make_uint4(0, 0, 0, 0);
         if (r < p.rows)
-          raw = __ldg(reinterpret_cast<const uint4*>(p.q + (bh * p.rows + r) * D) +
+          raw = load(reinterpret_cast<const uint4*>(p.q + (bh * p.rows + r) * D) +
                       (c / KW * 4 + j) * KW + c % KW);
         unpack8(raw, x[c]);
         if (c % A::CG == 0) sum[c / A::CG] = 0.0f;
@@ -883,8 +884,8 @@ cudaError_t launch_attn(const AttnParams& p, int grid, cudaStream_t st) {
 
 // Up to 4 rows a head: each row twice (32 x 8 heads of 32768 tokens: 219 us, one
 // tile of 8 for them 234 us); up to 8: one tile; more: tiles of 16 rows, which
-// decode the codes once for both halves (16 rows: 630 us for 49152 tokens, as
-// two tiles of 8 680 us).
+// decode the codes once for both halves (16 rows, 8 x 8 heads of 49152 tokens:
+// 163 us, as two tiles of 8 183 us; one sequence: 33 and 37 us).
 template <int D, int NG>
 cudaError_t launch_attn(const AttnParams& p, int grid, cudaStream_t st) {
   if (p.rows <= 4) return launch_attn<D, NG, 1, true>(p, grid, st);
@@ -892,8 +893,56 @@ cudaError_t launch_attn(const AttnParams& p, int grid, cudaStream_t st) {
   return launch_attn<D, NG, 2, false>(p, grid, st);
 }
 
-// How a call is split: by its sizes only, so that the workspace's size is known
-// beforehand.
+// How many clusters of 1 to kMostCluster CTAs run at once, by tiles of 8 rows a
+// CTA.  A cluster stays inside one of the chip's groups of SMs, so these are
+// fewer than the CTAs that the SMs hold: with 16 rows 15 clusters of 8 on 152
+// SMs, not 19.  One too many costs a second wave (16 heads of 16 rows, 8192
+// tokens: 33 us as clusters of 8, 21 us of 6).  Asked once a device, of the
+// kernels with the most shared memory.
+struct ActiveClusters {
+  int n[2][kMostCluster + 1];
+};
+template <int NT>
+void ask_active_clusters(int sms, int (&n)[kMostCluster + 1]) {
+  using A = Attn<128, 4, NT, false>;
+  const auto kernel = kv4_attn_kernel<128, 4, NT, false, true>;
+  n[0] = 0;
+  for (int c = 1; c <= kMostCluster; ++c) {
+    n[c] = (NT == 1 ? kPerSm : 1) * sms / (2 * c);  // where the question fails
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(c);
+    cfg.blockDim = dim3(kAttnThreads);
+    cfg.dynamicSmemBytes = A::kSmem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = c;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int most = 0;
+    if (allow_shared_memory<kv4_attn_kernel<128, 4, NT, false, true>>(A::kSmem) == cudaSuccess &&
+        cudaOccupancyMaxActiveClusters(&most, kernel, &cfg) == cudaSuccess)
+      n[c] = most;
+    else
+      cudaGetLastError();
+  }
+}
+const int (&active_clusters(int nt, int sms))[kMostCluster + 1] {
+  constexpr int kDevices = 64;
+  static ActiveClusters known[kDevices];
+  static std::once_flag asked[kDevices];
+  int dev = 0;
+  cudaGetDevice(&dev);
+  dev = dev < kDevices ? dev : kDevices - 1;
+  std::call_once(asked[dev], [&] {
+    ask_active_clusters<1>(sms, known[dev].n[0]);
+    ask_active_clusters<2>(sms, known[dev].n[1]);
+  });
+  return known[dev].n[nt - 1];
+}
+
+// How a call is split: by its sizes and the device only, so that the workspace's
+// size is known beforehand.
 struct AttnSplit {
   int nt, mt;      // tiles of 8 rows a CTA, row tiles a head
   int64_t steps;   // of a sequence, by the room of its table or list
@@ -907,10 +956,12 @@ AttnSplit attn_split(int B, int kv_heads, int64_t rows, int64_t tokens, int D, i
   s.steps = (tokens + kStep - 1) / kStep;
   s.ctas = s.nt == 1 ? kPerSm * sms : sms;  // as many as run at once
   const int64_t heads = (int64_t)B * kv_heads * s.mt;
-  // A cluster a head where that leaves no CTA with more to do than ranges over
-  // all CTAs would: those cost most CTAs a second start and everyone the second
-  // launch, about kSegmentSteps steps.
-  int64_t share = s.ctas / heads < kMostCluster ? s.ctas / heads : kMostCluster;
+  // A cluster a head, the largest of which all run at once, where that leaves no
+  // CTA with more to do than ranges over all CTAs would: those cost most CTAs a
+  // second start and everyone the second launch, about kSegmentSteps steps.
+  const auto& active = active_clusters(s.nt, sms);
+  int64_t share = kMostCluster;
+  while (share > 0 && heads > active[share]) --share;
   if (share > s.steps) share = s.steps;
   if (share >= 1 && (s.steps + share - 1) / share <= s.steps * heads / s.ctas + kSegmentSteps) {
     s.cluster = (int)share;

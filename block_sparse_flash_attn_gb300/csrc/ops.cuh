@@ -117,6 +117,15 @@ __device__ __forceinline__ void allow_next_launch() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// An ordinary load, and no read-only one (ld.global.nc): a kernel launched early
+// lives while the launch before it still writes, and the gradient of
+// qk_norm_rope may be written over its input; the read-only path is for data
+// that nothing writes during the kernel's life.
+template <typename T>
+__device__ __forceinline__ T load(const T* p) {
+  return *p;
+}
+
 // Launch with programmatic stream serialisation: the kernel may start while
 // the one before it in the stream drains, and waits for it itself.
 template <typename... KArgs, typename... Args>

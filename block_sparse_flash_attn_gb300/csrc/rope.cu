@@ -91,11 +91,11 @@ __device__ __forceinline__ void load_weights(const void* w, int f32, int c0, flo
     for (int i = 0; i < 8; ++i) out[i] = 1.0f;
   } else if (f32) {
     const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(w) + c0);
-    const float4 a = __ldg(f), b = __ldg(f + 1);
+    const float4 a = load(f), b = load(f + 1);
     out[0] = a.x, out[1] = a.y, out[2] = a.z, out[3] = a.w;
     out[4] = b.x, out[5] = b.y, out[6] = b.z, out[7] = b.w;
   } else {
-    unpack8(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(w) + c0)), out);
+    unpack8(load(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(w) + c0)), out);
   }
 }
 
@@ -108,7 +108,7 @@ __device__ __forceinline__ void load_angles(const RopeParams& p, int token, int 
 #pragma unroll
   for (int i = 0; i < 8; ++i) cs[i] = 1.0f, sn[i] = 0.0f;
   if (c0 >= 2 * p.half) return;
-  const int pos = p.pos ? __ldg(p.pos + token) : s;
+  const int pos = p.pos ? load(p.pos + token) : s;
   if (pos < 0 || pos >= p.n_pos) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) cs[i] = sn[i] = __int_as_float(0x7FC00000);
@@ -119,7 +119,7 @@ __device__ __forceinline__ void load_angles(const RopeParams& p, int token, int 
   const float sign = c0 < p.half ? -1.0f : 1.0f;
 #pragma unroll
   for (int i = 0; i < (INTER ? 2 : 4); ++i) {
-    const float4 f = __ldg(t + i);
+    const float4 f = load(t + i);
     if (INTER) {  // two pairs of channels
       cs[4 * i] = cs[4 * i + 1] = f.x;
       cs[4 * i + 2] = cs[4 * i + 3] = f.z;
@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_fwd_kernel(const RopeParams
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     raw[u] = make_uint4(0, 0, 0, 0);
-    if (h0 + u * R < c.end) raw[u] = __ldg(reinterpret_cast<const uint4*>(xr + u * R * D));
+    if (h0 + u * R < c.end) raw[u] = load(reinterpret_cast<const uint4*>(xr + u * R * D));
   }
   const int heads = c.kind == 0 ? p.H : p.Hkv;
   uint16_t* out = static_cast<uint16_t*>(c.kind == 0 ? p.q : c.kind == 1 ? p.k : p.v) +
@@ -265,9 +265,9 @@ __global__ void __launch_bounds__(32 * kBwdWarps, kBwdPerSm) rope_bwd_kernel(con
       raw[u] = make_uint4(0, 0, 0, 0);
       dy[u][0] = dy[u][1] = make_float4(0, 0, 0, 0);
       if (h0 + u * R < c.end) {
-        dy[u][0] = __ldg(reinterpret_cast<const float4*>(d + u * next));
-        dy[u][1] = __ldg(reinterpret_cast<const float4*>(d + u * next) + 1);
-        if (norm) raw[u] = __ldg(reinterpret_cast<const uint4*>(xr + u * R * D));
+        dy[u][0] = load(reinterpret_cast<const float4*>(d + u * next));
+        dy[u][1] = load(reinterpret_cast<const float4*>(d + u * next) + 1);
+        if (norm) raw[u] = load(reinterpret_cast<const uint4*>(xr + u * R * D));
       }
     }
     float cs[8], sn[8];

@@ -91,7 +91,8 @@ def _cache(cache) -> Kv4Cache:
 def _table(cache, block_table, lengths, counts=None, name="lengths"):
     """Checks the shared index tensors; returns (B, row stride, columns)."""
     tensor("block_table", block_table, (_I32,), device=cache.device, contiguous=False)
-    if block_table.dim() != 2 or block_table.shape[1] == 0 or block_table.stride(1) != 1:
+    if block_table.dim() != 2 or block_table.shape[1] == 0 or \
+            (block_table.stride(1) != 1 and block_table.shape[1] > 1):
         raise ValueError("block_table must be [B, pages a sequence], rows contiguous")
     B, columns = block_table.shape
     tensor(name, lengths, (_I32,), (B,), cache.device)

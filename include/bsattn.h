@@ -468,9 +468,9 @@ bsattn_status bsattn_qk_norm_rope_bwd(const void* x, int64_t x_batch_stride, int
  *              query block are kept where allowed (1: its own).  These count
  *              towards `keep`; if they are more than `keep` they are all kept.
  *   q, k       device bf16 [B][H][S][D], [B][Hkv][S][D], as for bsattn_fwd_gqa
- *              (query head h scores against key head h / (H / Hkv)).  Sums of a
- *              block's entries must stay below 3e38 in magnitude; a block whose
- *              means are all below 2^-119 is scored with fewer bits.
+ *              (query head h scores against key head h / (H / Hkv)).  Means must
+ *              stay below 2^112 in magnitude (a score overflows above); a block
+ *              whose means are all below 2^-119 is scored with fewer bits.
  *   mask       device uint8 [B][H][S/128][S/128 (S/64)], written in full.
  *   workspace  bsattn_select_blocks_workspace bytes, 16-byte aligned.
  * Errors: INVALID_ARG, UNSUPPORTED (D, sizes as bsattn_plan), CUDA.
@@ -539,8 +539,9 @@ bsattn_status bsattn_kv4_read(const bsattn_kv4_cache* cache, int B, int T,
  * the single-token form of bsattn_select_blocks.
  *
  * The queries of one key/value head (H / kv_heads heads, T tokens) are rounded
- * to 7 bits beside their largest entry; a page scores the largest of query . page
- * mean over them.  The first `sink` and the last `recent` pages of the sequence
+ * to 7 bits beside their largest entry, entries that are not finite counting as
+ * zero; a page scores the largest of query . page mean over them (means below
+ * 2^112, as there).  The first `sink` and the last `recent` pages of the sequence
  * are always taken, the best others fill up to `keep`, the lower page first
  * among equals.
  *   q          device bf16 [B][H][T][head_dim]; (H / kv_heads) * T <= 128.
@@ -563,7 +564,9 @@ bsattn_status bsattn_kv4_select(const bsattn_kv4_cache* cache, const void* q, in
  * Query t of a sequence of length n sits at position n - T + t and sees the
  * cached tokens at positions up to its own: all, or those of the listed pages.
  * A query that sees none gets O = 0, LSE = -inf.
- *   q          device bf16 [B][H][T][head_dim], 16-byte aligned; query head h reads
+ *   q          device bf16 [B][H][T][head_dim], 16-byte aligned, entries below 2^100
+ *              in magnitude (one that is not finite spoils its own query only);
+ *              query head h reads
  *              key/value head h / (H / kv_heads); (H / kv_heads) * T <= 128; B <= 4096;
  *              columns * page_size at most 2^31 - 128.
  *   lengths    cached tokens, the T new ones included.

@@ -219,6 +219,40 @@ def test_attn_wide_steps(bs):
     _check_attn(o, lse, ref.attn(cache, q, table, case[-1]), True)
 
 
+@pytest.mark.parametrize("power", [99, 40, -60, -120])
+def test_attn_sizes_of_queries(bs, power):
+    """Queries far from 1, up to the documented 2^100, and keys that make up for it."""
+    for case in ((1, 4, 128, 16, 32, 1, [300]), (2, 8, 64, 16, 64, 2, [100, 37])):
+        cache, table, q, n = _attn_case(bs, case)
+        q.mul_(2.0 ** (power - 3))
+        cache.k_scales.mul_(2.0 ** min(-power, 100))
+        o, lse = bs.kv4_attn(cache, q, table, n, out_f32=True)
+        _check_attn(o, lse, ref.attn(cache, q, table, case[-1]), True)
+
+
+@pytest.mark.parametrize("case", [(1, 4, 128, 16, 32, 2, [300]), (1, 2, 64, 16, 64, 2, [9000])], ids=str)
+def test_attn_query_that_is_not_finite_spoils_its_own_row_only(bs, case):
+    cache, table, q, n = _attn_case(bs, case)
+    want = bs.kv4_attn(cache, q, table, n)
+    for bad in (float("nan"), float("inf")):
+        spoilt = q.clone()
+        spoilt[0, 1, 0, 5] = bad
+        for got, old in zip(bs.kv4_attn(cache, spoilt, table, n), want):
+            same = got == old
+            same[0, 1, 0] = True
+            assert bool(same.all())
+
+
+def test_tables_of_one_page_with_any_stride(bs):
+    """A single column cut out of a wider table, whatever its stride."""
+    cache, table, q, n = _attn_case(bs, (1, 2, 64, 16, 64, 1, [9, 16]))
+    wide = torch.full((2, 6), -1, dtype=torch.int32, device="cuda")
+    wide[:, 3:4] = table
+    for got, want in zip(bs.kv4_attn(cache, q, wide[:, 3::3], n), bs.kv4_attn(cache, q, table, n)):
+        assert torch.equal(got, want)
+    bs.kv4_status(cache)
+
+
 def test_attn_growing_scores(bs):
     """Scores that rise along the sequence by far more than a running maximum may lag, and fall."""
     case = (1, 2, 64, 16, 64, 1, [400])
@@ -462,6 +496,12 @@ SPLITS = [
     (2, 4, 128, 32, 64, 2, [1000, 900], 0),          # clusters of 8
     (8, 1, 64, 64, 64, 1, [700] * 9, 0),             # clusters of 4
     (2, 4, 128, 16, 32, 4, [513, 90], 800),          # 16 rows, ranges
+    (37, 2, 64, 64, 64, 1, [1000], 0),               # clusters of 7, 6, 5 and 3
+    (22, 4, 128, 64, 128, 1, [1100, 130], 0),
+    (25, 1, 64, 16, 32, 1, [900, 17], 0),
+    (20, 4, 128, 64, 128, 1, [1000, 500, 0, 3], 0),
+    (16, 16, 64, 64, 64, 1, [800], 0),               # 16 rows, clusters of 6 and 4
+    (15, 12, 128, 32, 64, 1, [700, 90], 0),
 ]
 
 

@@ -89,7 +89,7 @@ def test_ties_go_to_the_lowest_index(bs):
                        ref.select_blocks(q, k, 3, key_block=64, local=0))
 
 
-@pytest.mark.parametrize("scale", [1e-30, 1e-3, 1.0, 1e10])
+@pytest.mark.parametrize("scale", [1e-30, 1e-3, 1.0, 1e10, 1e31])
 def test_sizes_of_values(bs, scale):
     """Wide ranges of values, means on rounding borders."""
     q, k = _qk(1, 2, 1, 1024, 64, seed=3, topic=0.0)

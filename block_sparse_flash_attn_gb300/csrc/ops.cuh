@@ -179,6 +179,19 @@ __device__ __forceinline__ void add_exact(Sum2& s, const Sum2& o) {
   s.lo = __fadd_rn(s.lo, o.lo);
 }
 
+__device__ __forceinline__ void add_exact(Sum2x2& s, const Sum2x2& o) {
+  add_exact(s, o.hi);
+  s.lo = s.lo + o.lo;
+}
+
+// the sums of the lane `o` places away
+__device__ __forceinline__ Sum2x2 exchanged(const Sum2x2& s, int o) {
+  const float2 hi = split(s.hi), lo = split(s.lo);
+  constexpr unsigned all = 0xFFFFFFFFu;
+  return Sum2x2{f2(__shfl_xor_sync(all, hi.x, o), __shfl_xor_sync(all, hi.y, o)),
+                f2(__shfl_xor_sync(all, lo.x, o), __shfl_xor_sync(all, lo.y, o))};
+}
+
 // hi takes everything it can hold: |lo| <= half a step of hi
 __device__ __forceinline__ Sum2 renormalised(const Sum2& s) {
   Sum2 r{s.hi, 0.0f};
@@ -212,6 +225,24 @@ __device__ __forceinline__ float rint_scaled(const Sum2& s, int shift) {
   return n;
 }
 
+// Sums of a warp's rows, which lie O lanes apart: of two lanes each passes half
+// of its HELD sums on and adds up the other half.
+template <int O, int HELD, int N>
+__device__ __forceinline__ void add_over_rows(Sum2x2 (&s)[N], int& first) {
+  if constexpr (O < 32) {
+    constexpr int kHalf = HELD / 2;
+    const bool upper = (threadIdx.x & O) != 0;
+    first += upper ? kHalf : 0;
+#pragma unroll
+    for (int i = 0; i < kHalf; ++i) {
+      const Sum2x2 low = s[i], high = s[i + kHalf];
+      s[i] = upper ? high : low;
+      add_exact(s[i], exchanged(upper ? low : high, O));
+    }
+    add_over_rows<2 * O, kHalf>(s, first);
+  }
+}
+
 // The mean of `rows` rows of a block (rows a power of two), rounded to 7 bits
 // beside its largest entry, by a CTA of 128 threads: a row is held by D / (2 N)
 // lanes, pairs[i] are this thread's sums of channels (lane % L) * 2N + 2i and
@@ -221,21 +252,18 @@ template <int D, int N>
 __device__ __forceinline__ void write_rounded_mean(const Sum2x2 (&pairs)[N], int rows, bool whole,
                                                    uint16_t* out) {
   constexpr int L = D / (2 * N), W = 4;
-  __shared__ Sum2 part[W][D];
+  __shared__ __align__(16) Sum2 part[W][D];
   __shared__ int top[W];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  Sum2x2 s[N];
 #pragma unroll
-  for (int i = 0; i < 2 * N; ++i) {
-    const float2 hi = split(pairs[i / 2].hi), lo = split(pairs[i / 2].lo);
-    Sum2 s = i % 2 ? Sum2{hi.y, lo.y} : Sum2{hi.x, lo.x};
+  for (int i = 0; i < N; ++i) s[i] = pairs[i];
+  int first = lane % L * N;  // the first pair that this lane still holds
+  add_over_rows<L, N>(s, first);
 #pragma unroll
-    for (int o = L; o < 32; o <<= 1) {
-      Sum2 other;
-      other.hi = __shfl_xor_sync(0xFFFFFFFFu, s.hi, o);
-      other.lo = __shfl_xor_sync(0xFFFFFFFFu, s.lo, o);
-      add_exact(s, other);
-    }
-    if (lane < L) part[warp][lane * 2 * N + i] = s;
+  for (int i = 0; i < N * L / 32; ++i) {
+    const float2 hi = split(s[i].hi), lo = split(s[i].lo);
+    *reinterpret_cast<float4*>(&part[warp][2 * (first + i)]) = make_float4(hi.x, lo.x, hi.y, lo.y);
   }
   __syncthreads();
   const int c = threadIdx.x;

@@ -9,6 +9,9 @@ is missing, every call raises.
     plan = bsattn.plan(mask_u8_cuda, causal=False)   # once per mask
     o, lse = bsattn.fwd(q, k, v, plan, scale)        # q/k/v bf16 [B,H,S,D] on cuda
 
+Around it: qk_norm_rope and its gradient (rope.py), select_blocks (blocks.py)
+and the 4-bit cache, Kv4Cache and kv4_* (kv4.py).
+
 The operation: "Writing Pallas Kernels for JAX: Stepping Outside the XLA
 Safety Net" (sections "Designing the Block Specification" and "Writing the
 Kernel Logic: Load, Compute, Store"), computed exactly across key blocks as in

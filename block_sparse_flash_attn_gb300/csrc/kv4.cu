@@ -139,9 +139,10 @@ struct Decoder {
 //
 // 512 bytes read and 160 written a token and head (groups of 32): the bound is
 // memory on paper, instructions in fact, some 20 a channel's lane.  8 x 4096
-// tokens (three quarters of them there), 8 heads of 128: 43 us, 69% of issue
-// slots, 2.9 TB/s; with conversions and comparisons a code 104 us, with a lane
-// for 8 channels instead of 16 59 us.
+// tokens (three quarters of them there), 8 heads of 128: 40 us, 67% of issue
+// slots, 3.6 TB/s; with conversions and comparisons a code 104 us, with a lane
+// for 8 channels instead of 16 59 us, with the next two rows in flight no less,
+// with 8 CTAs an SM (64 registers, spilling) 47 us.
 template <int D, int GL>
 __global__ void __launch_bounds__(kRowThreads, 6) kv4_append_kernel(const AppendParams p) {
   constexpr int L = D / 16, NG = L / GL, kRows = kRowThreads / L;  // rows the CTA holds at once

@@ -19,9 +19,9 @@
 // are exact in bf16); a row's k-th best is searched among the scores'
 // order-preserving bit patterns, held in a warp's registers.
 //
-// Measured at 65536 tokens, 32 + 8 heads of 128, causal: means 107 us (6.3 TB/s,
-// 94% of a plain copy's rate), choice 38 us (16384 rows of up to 512 scores,
-// bound by instructions: 63% of issue slots), 143 us together.
+// Measured at 65536 tokens, 32 + 8 heads of 128, causal: means 104 us (6.4 TB/s,
+// 97% of a plain copy's rate), choice 36 us (16384 rows of up to 512 scores,
+// bound by instructions: 63% of issue slots), 140 us together.
 #include <cstdint>
 
 #include "internal.h"

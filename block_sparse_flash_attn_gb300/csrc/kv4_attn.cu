@@ -34,9 +34,10 @@
 //   launch joins those: ragged batches and single long sequences fill the
 //   machine alike.
 // - Short contexts and lists: a head is a cluster of up to 8 CTAs, which share
-//   its steps and join their results through each other's shared memory, in one
-//   launch without a workspace.
-// Both join in a fixed order: results repeat bit for bit.
+//   its steps and join their results through each other's shared memory; where
+//   there are more heads than CTAs, 8, 4, 2 or 1 warps of a CTA.  One launch
+//   without a workspace.
+// All join in a fixed order: results repeat bit for bit.
 //
 // Measured: 32 sequences of 32768 to 65536 tokens, 8 heads of 128, 4 query heads
 // each: 318 us, 5.4 TB/s, 81% of a plain copy's rate, and the same when all pages
@@ -72,6 +73,14 @@ constexpr int kMostParts = 64;
 // tokens: 13 us as clusters of 8, 18 us as ranges; 128 heads: 40 and 45 us;
 // 16 heads of 16384 tokens: 23 and 21 us.
 constexpr int kSegmentSteps = 8;
+// What a head costs a group of warps beside its steps, and a segment a CTA of
+// ranges (which is a chain of loads, barriers and stores too, with less beside it
+// to run meanwhile; once more for the second launch).
+constexpr int kGroupStart = 4;
+constexpr int kSegmentStart = 6;
+// The most steps that a group of warps or a CTA of a cluster is given: a sequence
+// much longer than the others holds the call up by no more.
+constexpr int kMostGroupSteps = 64;
 constexpr int kMostCluster = 8;  // CTAs, the portable most
 constexpr float kNoMax = -1e30f;               // running maximum before any score
 constexpr float kLag = 8.0f;                   // a score may pass the running maximum by 2^8
@@ -94,7 +103,9 @@ struct AttnParams {
   int* prefix;     // [B + 1] steps before each sequence (written by CTA 0 for the join)
   float* partial;  // [2 * CTAs][RP * (D + 2)]
   int ctas;
-  int cluster;  // CTAs a head, 0: ranges
+  int cluster;  // CTAs a head
+  int group;    // or warps a head; both 0: ranges
+  int tiles;    // row tiles of all heads and sequences
 };
 
 __device__ __forceinline__ uint32_t word(const uint8_t* shared) {
@@ -182,7 +193,11 @@ __device__ __forceinline__ int tile_page(const AttnParams& p, int b, int h, int6
   return page_at(p.c, p.table + b * p.table_stride, p.columns, logical);
 }
 
-// One CTA: a range of units.  NG groups of channels share a step each, NT
+// What a CTA takes: a range of units, a share of one head (the CTAs of a cluster
+// share it), or a head for each group of p.group warps.
+enum : int { kRanges, kClusters, kGroups };
+
+// NG groups of channels share a step each, NT
 // tiles of 8 query rows.  TWICE: up to 4 rows, each in two columns of the one
 // tile, of which the second carries the low halves of the weights: one product
 // for hi + lo instead of two.
@@ -195,9 +210,10 @@ struct Attn {
   static constexpr int kCodes = kTile * RB;
   static constexpr int kScales = kTile * NG * 4;
   static constexpr int kStage = 2 * kCodes + 2 * kScales;  // K, V codes, K, V scales
-  static constexpr int kRing = kAttnWarps * kStages * kStage;
-  static constexpr int kJoin = kAttnWarps * RP * (D + 2) * 4 + kAttnWarps * RP * 4;
-  static constexpr int kSmem = (kRing > kJoin ? kRing : kJoin);
+  static constexpr int kWarpRing = kStages * kStage;
+  static constexpr int kSmem = kAttnWarps * kWarpRing;
+  // (the join of a warp's results takes the place of its ring)
+  static_assert(RP * (D + 3) * 4 <= kWarpRing, "shared memory");
   static constexpr int kSlot = RP * (D + 2);  // floats of a partial result
 
   // pieces of a row are stored permuted by its token, so that the 32-bit reads
@@ -207,7 +223,7 @@ struct Attn {
   }
 };
 
-template <int D, int NG, int NT, bool TWICE, bool CLUSTER>
+template <int D, int NG, int NT, bool TWICE, int MODE>
 __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
     kv4_attn_kernel(const AttnParams p) {
   using A = Attn<D, NG, NT, TWICE>;
@@ -215,27 +231,40 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
   constexpr bool kWide = D / NG >= 64;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int warp_sums[kAttnWarps];
-  __shared__ uint4 queries[NT][C][32];        // operands of S^T = K Q^T, a lane's four words
+  constexpr int kMostGroups = MODE == kGroups ? kAttnWarps : 1;
+  __shared__ uint4 queries_of[kMostGroups][NT][C][32];  // operands of S^T = K Q^T, a lane's four words
   __shared__ int2 tiles[kAttnWarps][128];  // (row / 16, position) of four batches of tiles
   int* prefix = reinterpret_cast<int*>(smem + A::kSmem);  // [B + 1]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, j = lane & 3;
+  // this warp's group, its place there, and this thread's
+  const int warps = MODE == kGroups ? p.group : kAttnWarps;
+  const int group = MODE == kGroups ? warp / warps : 0;
+  const int gwarp = warp - group * warps, gtid = tid - group * warps * 32, threads = warps * 32;
+  auto group_barrier = [&] {
+    if (MODE == kGroups)
+      asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(threads) : "memory");
+    else
+      __syncthreads();
+  };
+  auto& queries = queries_of[group];
 
   wait_for_previous_launch();
   const int heads = p.c.Hkv * p.mt;
   const int64_t most = (int64_t)p.columns * p.c.page;  // tokens that the table has room for
   auto steps_of = [&](int b) -> int {
-    if (p.selected) return (int)(((int64_t)p.n_selected * p.c.page + kStep - 1) / kStep);
+    const int step = kTile * warps;
+    if (p.selected) return (int)(((int64_t)p.n_selected * p.c.page + step - 1) / step);
     int64_t n = max(load(p.lengths + b), 0);
     if (n > most) {
       p.c.report();
       n = most;
     }
-    return (int)((n + kStep - 1) / kStep);
+    return (int)((n + step - 1) / step);
   };
   int64_t units = 0, u = 0, u_end = 1;
   bool first_segment = true;
-  if (CLUSTER) {
+  if (MODE != kRanges) {
     allow_next_launch();
   } else {
     // steps before each sequence
@@ -272,8 +301,8 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
     u_end = range_begin(units, ctas, blockIdx.x + 1);
   }
 
-  const uint32_t ring = shared_address(smem) + warp * (kStages * A::kStage);
-  const uint8_t* my_ring = smem + warp * (kStages * A::kStage);
+  const uint32_t ring = shared_address(smem) + warp * A::kWarpRing;
+  const uint8_t* my_ring = smem + warp * A::kWarpRing;
   // Where this lane's words begin.  K: tokens g and g + 8, words j KW .. j KW +
   // KW - 1 of each group.  V: tokens 2j, 2j + 1 and 8 on, word g of each 64
   // channels; where a group has 32 channels, word g mod 4 of each 32, its half
@@ -297,7 +326,14 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
   while (u < u_end) {
     // the segment: steps [s0, s1) of row tile m of head h of sequence b
     int b, hm, steps, s0, s1;
-    if (CLUSTER) {
+    if (MODE == kGroups) {
+      const int hh = blockIdx.x * (kAttnWarps / warps) + group;
+      if (hh >= p.tiles) return;  // (the whole group)
+      b = hh / heads;
+      hm = hh - b * heads;
+      steps = s1 = steps_of(b);
+      s0 = 0;
+    } else if (MODE == kClusters) {
       const int hh = blockIdx.x / p.cluster, rank = blockIdx.x - hh * p.cluster;
       b = hh / heads;
       hm = hh - b * heads;
@@ -332,7 +368,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
       if (i < n_tiles) {
         int pos = 0;
         const int pg =
-            tile_page(p, b, h, ((int64_t)(s0 + i) * kAttnWarps + warp) * kTile, len, pos);
+            tile_page(p, b, h, ((int64_t)(s0 + i) * warps + gwarp) * kTile, len, pos);
         if (pg >= 0)
           next_tile = make_int2((int)(p.c.row(pg, h, pos & (p.c.page - 1)) / kTile), pos);
       }
@@ -397,7 +433,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
       const float f = ldexpf(1.0f, sh), f16 = f * 0.0625f;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        if (warp == 0)  // (the same for all warps)
+        if (gwarp == 0)  // (the same for all warps)
           queries[nt][c][lane] = make_uint4(
               pack_half(x[c][0] * f, x[c][4] * f), pack_half(x[c][2] * f, x[c][6] * f),
               pack_half(x[c][1] * f16, x[c][5] * f16), pack_half(x[c][3] * f16, x[c][7] * f16));
@@ -416,7 +452,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
       }
     }
 
-    __syncthreads();
+    group_barrier();
     F2 mx[NT], l[NT], vm[NT][NG];  // -maximum, sum of weights, sum of weights * least
     float o[C][2][NT][4];
 #pragma unroll
@@ -648,12 +684,12 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
     }
     copy_wait<0>();
 
-    // ---- join the warps (the ring is free): maxima, sums, O in 32 bits
-    __syncthreads();
-    float* sm = reinterpret_cast<float*>(smem);  // [warp][RP] maxima
-    float* sl = sm + kAttnWarps * RP;            // [warp][RP] sums
-    float* so = sl + kAttnWarps * RP;            // [warp][RP][D]
-    float* sf = so + kAttnWarps * RP * D;        // [warp][RP] factors
+    // ---- join the group's warps (their rings are free): maxima, sums, O in 32 bits
+    group_barrier();
+    float* sm = reinterpret_cast<float*>(smem + group * warps * A::kWarpRing);  // [warp][RP] maxima
+    float* sl = sm + warps * RP;      // [warp][RP] sums
+    float* so = sl + warps * RP;      // [warp][RP][D]
+    float* sf = so + warps * RP * D;  // [warp][RP] factors
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       if (TWICE) {  // the columns of the low halves onto those of the high ones
@@ -684,8 +720,8 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
         const int r = nt * 8 + 2 * j + e;
         if (r >= RP) continue;
         if (g == 0) {
-          sm[warp * RP + r] = -(e ? m2.y : m2.x);
-          sl[warp * RP + r] = e ? l2.y : l2.x;
+          sm[gwarp * RP + r] = -(e ? m2.y : m2.x);
+          sl[gwarp * RP + r] = e ? l2.y : l2.x;
         }
         const float f = 16777216.0f * top_step, f16 = 1048576.0f * top_step;  // 2^24, 2^20
 #pragma unroll
@@ -693,26 +729,26 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
           const int ch = kWide ? 64 * (c / 2) + 8 * g + 4 * (c & 1)
                                : 32 * c + 8 * (g & 3) + 4 * (g >> 2);
           const float base = e ? vm2[c / A::CG].y : vm2[c / A::CG].x;
-          *reinterpret_cast<float4*>(so + (warp * RP + r) * D + ch) = make_float4(
+          *reinterpret_cast<float4*>(so + (gwarp * RP + r) * D + ch) = make_float4(
               fmaf(o[c][0][nt][e], f, base), fmaf(o[c][1][nt][e] - o[c][0][nt][e], f16, base),
               fmaf(o[c][0][nt][e + 2], f, base),
               fmaf(o[c][1][nt][e + 2] - o[c][0][nt][e + 2], f16, base));
         }
       }
     }
-    __syncthreads();
-    if (tid < RP) {
+    group_barrier();
+    if (gtid < RP) {
       float top = kNoMax, sum = 0.0f;
-      for (int w = 0; w < kAttnWarps; ++w) top = fmaxf(top, sm[w * RP + tid]);
-      for (int w = 0; w < kAttnWarps; ++w) {
-        const float f = exp2_fast(sm[w * RP + tid] - top);
-        sf[w * RP + tid] = f;
-        sum += sl[w * RP + tid] * f;
+      for (int w = 0; w < warps; ++w) top = fmaxf(top, sm[w * RP + gtid]);
+      for (int w = 0; w < warps; ++w) {
+        const float f = exp2_fast(sm[w * RP + gtid] - top);
+        sf[w * RP + gtid] = f;
+        sum += sl[w * RP + gtid] * f;
       }
-      sm[tid] = top;  // (this thread's column only)
-      sl[tid] = sum;
+      sm[gtid] = top;  // (this thread's column only)
+      sl[gtid] = sum;
     }
-    __syncthreads();
+    group_barrier();
     auto write = [&](int r, int ch, float v) {
       const int64_t at = (bh * p.rows + row0 + r) * D + ch;
       if (p.out_f32)
@@ -724,10 +760,21 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
       const int r = x / D;
       float t = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kAttnWarps; ++w) t = fmaf(so[w * RP * D + x], sf[w * RP + r], t);
+      for (int w = 0; w < kAttnWarps; ++w) {
+        if (w < warps) t = fmaf(so[w * RP * D + x], sf[w * RP + r], t);
+      }
       return t;
     };
-    if (CLUSTER) {
+    auto write_whole = [&] {
+      for (int x = gtid; x < min(RP, p.rows - row0) * D; x += threads) {
+        const int r = x / D;
+        write(r, x % D, sum_of_warps(x) * (sl[r] == 0.0f ? 0.0f : 1.0f / sl[r]));
+      }
+      if (gtid < min(RP, p.rows - row0))
+        p.lse[bh * p.rows + row0 + gtid] = (sm[gtid] + log2f(sl[gtid])) * kLn2;
+    };
+    if (MODE == kGroups) return write_whole();
+    if (MODE == kClusters) {
       // the CTA's O in place of its first warp's; then each CTA joins a share of it
       for (int x = tid; x < RP * D; x += kAttnThreads) so[x] = sum_of_warps(x);
       cluster_barrier();
@@ -758,22 +805,14 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
       cluster_barrier();  // no CTA leaves while another reads its memory
       return;
     }
-    const bool whole = s0 == 0 && s1 == steps;
-    float* slot = p.partial + (int64_t)(2 * blockIdx.x + (first_segment ? 0 : 1)) * A::kSlot;
-    for (int x = tid; x < RP * D; x += kAttnThreads) {
-      const int r = x / D;
-      const float t = sum_of_warps(x);
-      if (!whole)
-        slot[2 * RP + x] = t;
-      else if (row0 + r < p.rows)
-        write(r, x % D, t * (sl[r] == 0.0f ? 0.0f : 1.0f / sl[r]));
-    }
-    if (tid < RP) {
-      if (!whole) {
+    if (s0 == 0 && s1 == steps) {
+      write_whole();
+    } else {
+      float* slot = p.partial + (int64_t)(2 * blockIdx.x + (first_segment ? 0 : 1)) * A::kSlot;
+      for (int x = tid; x < RP * D; x += kAttnThreads) slot[2 * RP + x] = sum_of_warps(x);
+      if (tid < RP) {
         slot[tid] = sm[tid];
         slot[RP + tid] = sl[tid];
-      } else if (row0 + tid < p.rows) {
-        p.lse[bh * p.rows + row0 + tid] = (sm[tid] + log2f(sl[tid])) * kLn2;
       }
     }
     __syncthreads();
@@ -865,16 +904,23 @@ cudaError_t launch_attn(const AttnParams& p, int grid, cudaStream_t st) {
   using A = Attn<D, NG, NT, TWICE>;
   constexpr size_t most = A::kSmem + (size_t)(kMostSequences + 1) * sizeof(int);
   static_assert(most <= 210 * 1024, "shared memory");
-  if (p.cluster) {
-    cudaError_t e = allow_shared_memory<kv4_attn_kernel<D, NG, NT, TWICE, true>>(A::kSmem);
+  if (p.group) {
+    constexpr auto kernel = kv4_attn_kernel<D, NG, NT, TWICE, kGroups>;
+    cudaError_t e = allow_shared_memory<kernel>(A::kSmem);
     if (e != cudaSuccess) return e;
-    return launch_dependent_clusters(kv4_attn_kernel<D, NG, NT, TWICE, true>, dim3(grid),
-                                     dim3(kAttnThreads), p.cluster, A::kSmem, st, p);
+    return launch_dependent(kernel, dim3(grid), dim3(kAttnThreads), A::kSmem, st, p);
+  }
+  if (p.cluster) {
+    constexpr auto kernel = kv4_attn_kernel<D, NG, NT, TWICE, kClusters>;
+    cudaError_t e = allow_shared_memory<kernel>(A::kSmem);
+    if (e != cudaSuccess) return e;
+    return launch_dependent_clusters(kernel, dim3(grid), dim3(kAttnThreads), p.cluster, A::kSmem,
+                                     st, p);
   }
   const size_t smem = A::kSmem + (size_t)(p.B + 1) * sizeof(int);
-  cudaError_t e = allow_shared_memory<kv4_attn_kernel<D, NG, NT, TWICE, false>>((int)most);
+  cudaError_t e = allow_shared_memory<kv4_attn_kernel<D, NG, NT, TWICE, kRanges>>((int)most);
   if (e != cudaSuccess) return e;
-  e = launch_dependent(kv4_attn_kernel<D, NG, NT, TWICE, false>, dim3(grid), dim3(kAttnThreads),
+  e = launch_dependent(kv4_attn_kernel<D, NG, NT, TWICE, kRanges>, dim3(grid), dim3(kAttnThreads),
                        smem, st, p);
   if (e != cudaSuccess) return e;
   return launch_dependent(kv4_join_kernel<D, A::RP>,
@@ -905,7 +951,7 @@ struct ActiveClusters {
 template <int NT>
 void ask_active_clusters(int sms, int (&n)[kMostCluster + 1]) {
   using A = Attn<128, 4, NT, false>;
-  const auto kernel = kv4_attn_kernel<128, 4, NT, false, true>;
+  constexpr auto kernel = kv4_attn_kernel<128, 4, NT, false, kClusters>;
   n[0] = 0;
   for (int c = 1; c <= kMostCluster; ++c) {
     n[c] = (NT == 1 ? kPerSm : 1) * sms / (2 * c);  // where the question fails
@@ -920,7 +966,7 @@ void ask_active_clusters(int sms, int (&n)[kMostCluster + 1]) {
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     int most = 0;
-    if (allow_shared_memory<kv4_attn_kernel<128, 4, NT, false, true>>(A::kSmem) == cudaSuccess &&
+    if (allow_shared_memory<kernel>(A::kSmem) == cudaSuccess &&
         cudaOccupancyMaxActiveClusters(&most, kernel, &cfg) == cudaSuccess)
       n[c] = most;
     else
@@ -946,7 +992,7 @@ const int (&active_clusters(int nt, int sms))[kMostCluster + 1] {
 struct AttnSplit {
   int nt, mt;      // tiles of 8 rows a CTA, row tiles a head
   int64_t steps;   // of a sequence, by the room of its table or list
-  int ctas, grid, cluster;
+  int ctas, grid, cluster, group;
   size_t prefix_bytes, workspace;
 };
 AttnSplit attn_split(int B, int kv_heads, int64_t rows, int64_t tokens, int D, int sms) {
@@ -956,17 +1002,43 @@ AttnSplit attn_split(int B, int kv_heads, int64_t rows, int64_t tokens, int D, i
   s.steps = (tokens + kStep - 1) / kStep;
   s.ctas = s.nt == 1 ? kPerSm * sms : sms;  // as many as run at once
   const int64_t heads = (int64_t)B * kv_heads * s.mt;
-  // A cluster a head, the largest of which all run at once, where that leaves no
-  // CTA with more to do than ranges over all CTAs would: those cost most CTAs a
-  // second start and everyone the second launch, about kSegmentSteps steps.
+  // Up to as many heads as CTAs: a cluster a head, the largest of which all run at
+  // once, where that leaves no CTA with more to do than ranges over all CTAs would:
+  // those cost most CTAs a second start and everyone the second launch, about
+  // kSegmentSteps steps.
   const auto& active = active_clusters(s.nt, sms);
   int64_t share = kMostCluster;
   while (share > 0 && heads > active[share]) --share;
   if (share > s.steps) share = s.steps;
-  if (share >= 1 && (s.steps + share - 1) / share <= s.steps * heads / s.ctas + kSegmentSteps) {
-    s.cluster = (int)share;
-    s.grid = (int)(heads * share);
-    return s;
+  if (share >= 1) {
+    const int64_t most = (s.steps + share - 1) / share;
+    if (most <= kMostGroupSteps && most <= s.steps * heads / s.ctas + kSegmentSteps) {
+      if (share == 1)
+        s.group = kAttnWarps;
+      else
+        s.cluster = (int)share;
+      s.grid = (int)(heads * share);
+      return s;
+    }
+  } else {
+    // More heads than CTAs: a group of 8, 4, 2 or 1 warps a head.  Fewer warps a
+    // head take fewer waves of CTAs, each with a start of its own, of more steps.
+    // 2048 heads of 128 tokens, 4 rows each: 45, 30, 23, 19 us, as ranges 54;
+    // of 512 tokens 68, 52, 47, 41 (83); of 2048 140, 123, 129, 127 (158); 384
+    // heads of 4096 tokens 60, 68, 84, 160 (68).
+    double best = (double)s.steps * heads / s.ctas +
+                  kSegmentStart * ((double)heads / s.ctas + 2);
+    for (int warps = kAttnWarps; warps >= 1; warps /= 2) {
+      const int64_t a_cta = kAttnWarps / warps, steps = (tokens + kTile * warps - 1) / (kTile * warps);
+      const int64_t grid = (heads + a_cta - 1) / a_cta, waves = (grid + s.ctas - 1) / s.ctas;
+      const double cost = (double)waves * (steps + kGroupStart);
+      if (steps <= kMostGroupSteps && cost < best) {
+        best = cost;
+        s.group = warps;
+        s.grid = (int)grid;
+      }
+    }
+    if (s.group) return s;
   }
   if (heads * kMostParts < s.ctas) s.ctas = (int)(heads * kMostParts);
   if (s.steps * heads < s.ctas) s.ctas = (int)(s.steps * heads);  // no more than units
@@ -1052,6 +1124,8 @@ bsattn_status bsattn_kv4_attn(const bsattn_kv4_cache* cache, const void* q, int 
   p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + split.prefix_bytes);
   p.ctas = split.ctas;
   p.cluster = split.cluster;
+  p.group = split.group;
+  p.tiles = (int)(B * cache->kv_heads * split.mt);
   const int grid = split.grid;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int groups = cache->head_dim / cache->group;

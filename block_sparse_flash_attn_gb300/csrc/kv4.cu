@@ -19,6 +19,7 @@ namespace bsattn {
 namespace {
 
 constexpr int kRowThreads = 128;  // write_rounded_mean takes a CTA of 128
+constexpr int kFewTokens = 8;
 constexpr int kReadRows = 4;      // rows a lane group reads back at once
 constexpr float kLeastStep = 7.888609e-31f;  // 2^-100
 
@@ -131,6 +132,36 @@ struct Decoder {
   }
 };
 
+// Rows first .. of the cnt new tokens of sequence b, token by token, the heads of
+// K and then of V: a lane group a row.
+template <int D, int GL>
+__device__ __forceinline__ void append_rows(const AppendParams& p, int b, int len, int cnt,
+                                            int first, int sub, int cl) {
+  constexpr int L = D / 16, NG = L / GL;
+  const int heads = 2 * p.c.Hkv, r = first + sub, t = r / heads, place = r - t * heads;
+  const bool is_k = place < p.c.Hkv;
+  const int h = is_k ? place : place - p.c.Hkv;
+  uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+  int pg = -1;
+  if (t < cnt) {
+    const uint16_t* src = is_k ? p.k + b * p.kb + h * p.kh + t * p.kt
+                               : p.v + b * p.vb + h * p.vh + t * p.vt;
+    lo = load(reinterpret_cast<const uint4*>(src) + 2 * cl);
+    hi = load(reinterpret_cast<const uint4*>(src) + 2 * cl + 1);
+    pg = page_at(p.c, p.table + b * p.table_stride, p.columns, ((int64_t)len + t) >> p.c.log_page);
+  }
+  const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  F2 x[8];
+  float step, least;
+  const uint2 packed = quantise<GL>(w, x, step, least);  // (every lane: shuffles)
+  if (pg < 0) return;
+  const int64_t row = p.c.row(pg, h, (int)(((int64_t)len + t) & (p.c.page - 1)));
+  reinterpret_cast<uint2*>(is_k ? p.c.k_codes : p.c.v_codes)[row * L + cl] = packed;
+  if (cl % GL == 0)
+    reinterpret_cast<uint32_t*>(is_k ? p.c.k_scales : p.c.v_scales)[row * NG + cl / GL] =
+        pack_bf16(step, least);
+}
+
 // One CTA: K or V of one page of one sequence and head, the tokens of this call
 // that fall into it.  A row is held by D / 16 lanes, and the next row's load is
 // in flight while one is quantised.  When the call fills the page the CTA of K
@@ -143,7 +174,13 @@ struct Decoder {
 // slots, 3.6 TB/s; with conversions and comparisons a code 104 us, with a lane
 // for 8 channels instead of 16 59 us, with the next two rows in flight no less,
 // with 8 CTAs an SM (64 registers, spilling) 47 us.
-template <int D, int GL>
+//
+// FEW tokens (up to kFewTokens, decoding steps): CTAs behind those of the heads of
+// K write all rows, as many a CTA as it holds, and those of the heads only see to
+// the means of pages that fill, which one token in a page's does.
+// 512 sequences, 8 heads of 128, of one token: 9 us (a CTA for each head's K and
+// V: 17 us), of 8 tokens: 13 us (21 us).
+template <int D, int GL, bool FEW>
 __global__ void __launch_bounds__(kRowThreads, 6) kv4_append_kernel(const AppendParams p) {
   constexpr int L = D / 16, NG = L / GL, kRows = kRowThreads / L;  // rows the CTA holds at once
   const bool is_k = blockIdx.y < p.c.Hkv;
@@ -158,12 +195,16 @@ __global__ void __launch_bounds__(kRowThreads, 6) kv4_append_kernel(const Append
     if (threadIdx.x == 0) p.c.report();
     return;
   }
+  const int sub = threadIdx.x / L, cl = threadIdx.x % L;
+  if (FEW) {
+    if (!is_k) return append_rows<D, GL>(p, b, len, cnt, h * kRows, sub, cl);
+    if ((((int64_t)len + cnt) >> p.c.log_page) == (len >> p.c.log_page)) return;
+  }
   const int64_t logical = (len >> p.c.log_page) + (int64_t)blockIdx.x;
   const int64_t end = min((int64_t)len + cnt, (logical + 1) << p.c.log_page);
   const int64_t begin = max((int64_t)len, logical << p.c.log_page);
   if (begin >= end) return;
   const int n = (int)(end - begin), place0 = (int)(begin & (p.c.page - 1));
-  const int sub = threadIdx.x / L, cl = threadIdx.x % L;
   // the first row is on its way while the table is asked
   const int64_t token = is_k ? p.kt : p.vt;
   const uint16_t* src = (is_k ? p.k + b * p.kb + h * p.kh : p.v + b * p.vb + h * p.vh) +
@@ -198,8 +239,10 @@ __global__ void __launch_bounds__(kRowThreads, 6) kv4_append_kernel(const Append
     float step, least;
     const uint2 packed = quantise<GL>(w, x, step, least);
     if (there) {
-      *codes = packed;
-      if (cl % GL == 0) *scales = pack_bf16(step, least);
+      if (!FEW) {
+        *codes = packed;
+        if (cl % GL == 0) *scales = pack_bf16(step, least);
+      }
       if (sums) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) add_exact(s[k], fma2(x[k], f2(step), f2(least)));
@@ -308,16 +351,27 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const ReadParams 
 // machine busy or the list is short; else scores and choice are two launches.
 // ---------------------------------------------------------------------------
 constexpr int kPageThreads = 512;
-constexpr int kPageWarps = kPageThreads / 32;
+// More heads than SMs: CTAs of 128 threads, four of which an SM holds, so that the
+// starts, barriers and searches of one pass beside the others.  2048 heads of 64
+// pages: 21 us, with 512 threads 64 us; of 1024 pages 88 and 131 us; 256 heads of
+// 16 pages 7 and 11 us.
+constexpr int kFewPageThreads = 128;
 constexpr int kTiles = 2;        // tiles of 16 pages that a warp has in flight
 constexpr int kMostRows = 128;   // G * T
-constexpr int kRoundPages = kPageWarps * kTiles * 16;  // a CTA's; all of one in the split form
+constexpr int kVec = 4;          // 16-byte pieces of the queries a thread
+template <int THREADS>
+constexpr int kRound = THREADS / 32 * kTiles * 16;  // pages that a CTA scores at once
+constexpr int kRoundPages = kRound<kPageThreads>;  // all of a CTA's in the split form
 // One launch for lists up to this room: 8 heads of 500 pages 8 us (two launches 10),
 // of 2000 pages 15 us (12, but another launch for the host); 128 heads of 1000
 // pages 13 us (19).
 constexpr int kOneCtaPages = 2048;
 constexpr int kMostShared = 16 * kPageThreads;  // keys in shared memory
 constexpr uint32_t kForcedPage = 0xFFFFFFFFu;
+static_assert(kMostRows * 128 <= kPageThreads * kVec * 8, "queries");
+// (a call with kFewPageThreads asks for no more than the usual shared memory: rows to a
+// multiple of 8)
+static_assert(kFewPageThreads * kVec * 16 + 7 * 256 + kOneCtaPages * 4 <= 48 << 10, "shared memory");
 constexpr uint32_t kNoPage = 0u;
 
 struct PagesParams {
@@ -341,17 +395,17 @@ __device__ __forceinline__ int pages_of(const PagesParams& p, int b) {
 
 // Rounds the queries of (sequence, head) bh into `whole` ([rows, to a multiple
 // of 8][D] bf16, zero rows at the end).  All threads of the CTA.
-template <int D>
+template <int D, int THREADS>
 __device__ __forceinline__ void round_queries(const PagesParams& p, int64_t bh, uint16_t* whole) {
-  constexpr int kVec = kMostRows * 128 / 8 / kPageThreads;  // 16-byte pieces a thread, at most
-  __shared__ uint32_t top[kPageWarps];
+  constexpr int kWarps = THREADS / 32;
+  __shared__ uint32_t top[kWarps];
   const uint4* q = reinterpret_cast<const uint4*>(p.q + bh * p.rows * D);
   const int pieces = p.rows * D / 8, room = (p.rows + 7) / 8 * 8 * D / 8;
   uint4 v[kVec];
   uint32_t most = 0;  // bits of the largest finite |q|
 #pragma unroll
   for (int i = 0; i < kVec; ++i) {
-    const int at = threadIdx.x + i * kPageThreads;
+    const int at = threadIdx.x + i * THREADS;
     v[i] = make_uint4(0, 0, 0, 0);
     if (at >= pieces) continue;
     v[i] = load(q + at);
@@ -366,7 +420,7 @@ __device__ __forceinline__ void round_queries(const PagesParams& p, int64_t bh, 
   if ((threadIdx.x & 31) == 0) top[threadIdx.x >> 5] = most;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kPageWarps; ++w) most = max(most, top[w]);
+  for (int w = 0; w < kWarps; ++w) most = max(most, top[w]);
   // t = rint(q 2^(6 - e)), in two factors, for 2^(6 - e) may pass fp32's range
   const int shift = most ? 6 - ilogbf(__uint_as_float(most << 16)) : 0;
   const float f1 = ldexpf(1.0f, shift / 2), f2 = ldexpf(1.0f, shift - shift / 2);
@@ -374,7 +428,7 @@ __device__ __forceinline__ void round_queries(const PagesParams& p, int64_t bh, 
   auto round2 = [&](uint32_t w) { return pack_bf16(round1(bf16_lo(w)), round1(bf16_hi(w))); };
 #pragma unroll
   for (int i = 0; i < kVec; ++i) {
-    const int at = threadIdx.x + i * kPageThreads;
+    const int at = threadIdx.x + i * THREADS;
     if (at < room)
       reinterpret_cast<uint4*>(whole)[at] =
           make_uint4(round2(v[i].x), round2(v[i].y), round2(v[i].z), round2(v[i].w));
@@ -386,7 +440,7 @@ __device__ __forceinline__ void round_queries(const PagesParams& p, int64_t bh, 
 // warp kTiles tiles of 16 pages at once, pages as the product's rows and
 // queries as its columns, so that a page's best query is two shuffles away.
 // The loads of a round are issued before `whole` is needed (ready() fills it).
-template <int D, typename Ready>
+template <int D, int THREADS, typename Ready>
 __device__ __forceinline__ void score_pages(const PagesParams& p, int b, int h, int n, int first,
                                             int end, const uint16_t* whole, uint32_t* keys,
                                             Ready ready) {
@@ -402,7 +456,7 @@ __device__ __forceinline__ void score_pages(const PagesParams& p, int b, int h, 
       next[k] = at + 8 * k < end ? load(table + at + 8 * k) : -1;
   };
   look_up(first + warp * (kTiles * 16) + g);
-  for (int base = first; base < end; base += kRoundPages) {
+  for (int base = first; base < end; base += kRound<THREADS>) {
     const int at = base + warp * (kTiles * 16) + g;  // this lane's pages: at + 8 k
     bool there[2 * kTiles];
     uint4 w[2 * kTiles][C];
@@ -416,7 +470,7 @@ __device__ __forceinline__ void score_pages(const PagesParams& p, int b, int h, 
 #pragma unroll
       for (int c = 0; c < C; ++c) w[k][c] = mean[4 * c + j];
     }
-    look_up(at + kRoundPages);
+    look_up(at + kRound<THREADS>);
     if (waiting) ready();
     waiting = false;
     float best[2 * kTiles];
@@ -600,6 +654,7 @@ __device__ __forceinline__ void choose_pages(const PagesParams& p, const uint32_
 }
 
 // As many of the CTA's threads as the list needs, 4 warps for up to 2048 pages.
+template <int THREADS>
 __device__ __forceinline__ void choose_pages(const PagesParams& p, const uint32_t* keys, int n,
                                              int* out) {
   if (n <= 16 * 128) {
@@ -608,10 +663,11 @@ __device__ __forceinline__ void choose_pages(const PagesParams& p, const uint32_
       choose_pages<4, 128>(p, keys, n, out);
     else
       choose_pages<16, 128>(p, keys, n, out);
-  } else if (n <= 16 * kPageThreads) {
-    choose_pages<16, kPageThreads>(p, keys, n, out);
-  } else {
-    choose_pages<0, kPageThreads>(p, keys, n, out);
+  } else if constexpr (THREADS == kPageThreads) {  // (kFewPageThreads: no longer lists)
+    if (n <= 16 * kPageThreads)
+      choose_pages<16, kPageThreads>(p, keys, n, out);
+    else
+      choose_pages<0, kPageThreads>(p, keys, n, out);
   }
 }
 
@@ -625,21 +681,22 @@ __global__ void __launch_bounds__(kPageThreads) page_scores_kernel(const PagesPa
   const int n = pages_of(p, b), first = blockIdx.x * kRoundPages;
   if (first >= n) return;
   const int64_t bh = (int64_t)b * p.c.Hkv + h;
-  score_pages<D>(p, b, h, n, first, min(n, first + kRoundPages), whole, p.keys + bh * p.columns,
-                 [&] { round_queries<D>(p, bh, whole); });
+  score_pages<D, kPageThreads>(p, b, h, n, first, min(n, first + kRoundPages), whole,
+                               p.keys + bh * p.columns,
+                               [&] { round_queries<D, kPageThreads>(p, bh, whole); });
 }
 
 __global__ void __launch_bounds__(kPageThreads) choose_pages_kernel(const PagesParams p) {
   wait_for_previous_launch();
   allow_next_launch();
   const int64_t bh = blockIdx.x;
-  choose_pages(p, p.keys + bh * p.columns, pages_of(p, (int)(bh / p.c.Hkv)),
-                      p.out + bh * p.keep);
+  choose_pages<kPageThreads>(p, p.keys + bh * p.columns, pages_of(p, (int)(bh / p.c.Hkv)),
+                             p.out + bh * p.keep);
 }
 
 // Both in one: a head a CTA, the keys in shared memory.
-template <int D>
-__global__ void __launch_bounds__(kPageThreads) select_pages_kernel(const PagesParams p) {
+template <int D, int THREADS>
+__global__ void __launch_bounds__(THREADS) select_pages_kernel(const PagesParams p) {
   extern __shared__ __align__(16) uint16_t whole[];
   wait_for_previous_launch();
   allow_next_launch();
@@ -647,9 +704,10 @@ __global__ void __launch_bounds__(kPageThreads) select_pages_kernel(const PagesP
   const int b = (int)(bh / p.c.Hkv), h = (int)(bh - (int64_t)b * p.c.Hkv);
   const int n = pages_of(p, b);
   uint32_t* keys = reinterpret_cast<uint32_t*>(whole + (p.rows + 7) / 8 * 8 * D);
-  score_pages<D>(p, b, h, n, 0, n, whole, keys, [&] { round_queries<D>(p, bh, whole); });
+  score_pages<D, THREADS>(p, b, h, n, 0, n, whole, keys,
+                          [&] { round_queries<D, THREADS>(p, bh, whole); });
   __syncthreads();
-  choose_pages(p, keys, n, p.out + bh * p.keep);
+  choose_pages<THREADS>(p, keys, n, p.out + bh * p.keep);
 }
 
 bool one_cta_a_head(int heads, int columns, int sms) {
@@ -662,9 +720,13 @@ cudaError_t launch_pages(const PagesParams& p, int B, int sms, cudaStream_t st) 
   const int heads = B * p.c.Hkv;
   if (one_cta_a_head(heads, p.columns, sms)) {
     const size_t smem = queries + (size_t)p.columns * sizeof(uint32_t);
-    cudaError_t e = allow_shared_memory<select_pages_kernel<D>>(64 << 10);
+    if (heads > sms && p.columns <= kOneCtaPages && p.rows * D <= kFewPageThreads * kVec * 8)
+      return launch_dependent(select_pages_kernel<D, kFewPageThreads>, dim3(heads),
+                              dim3(kFewPageThreads), smem, st, p);
+    constexpr auto kernel = select_pages_kernel<D, kPageThreads>;
+    cudaError_t e = allow_shared_memory<kernel>(64 << 10);
     if (e != cudaSuccess) return e;
-    return launch_dependent(select_pages_kernel<D>, dim3(heads), dim3(kPageThreads), smem, st, p);
+    return launch_dependent(kernel, dim3(heads), dim3(kPageThreads), smem, st, p);
   }
   cudaError_t e = launch_dependent(
       page_scores_kernel<D>, dim3((p.columns + kRoundPages - 1) / kRoundPages, p.c.Hkv, B),
@@ -758,10 +820,14 @@ bsattn_status bsattn_kv4_append(const bsattn_kv4_cache* cache, const void* k, in
   p.T = T;
   // T tokens touch at most this many pages
   const int touched = (T + cache->page_size - 2) / cache->page_size + 1;
-  const dim3 grid(touched, 2 * cache->kv_heads, B);
+  const bool few = T <= kFewTokens && cache->kv_heads <= 2048;  // (one page fills at most)
+  const int rows = kRowThreads / (cache->head_dim / 16), all = few ? 2 * T * cache->kv_heads : 0;
+  const dim3 grid(few ? 1 : touched,
+                  cache->kv_heads + (few ? (all + rows - 1) / rows : cache->kv_heads), B);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-#define BSATTN_CALL(D, GL) \
-  e = launch_dependent(kv4_append_kernel<D, GL>, grid, dim3(kRowThreads), 0, st, p)
+#define BSATTN_CALL(D, GL)                                                                  \
+  e = few ? launch_dependent(kv4_append_kernel<D, GL, true>, grid, dim3(kRowThreads), 0, st, p) \
+          : launch_dependent(kv4_append_kernel<D, GL, false>, grid, dim3(kRowThreads), 0, st, p)
   cudaError_t e;
   BSATTN_KV4_DISPATCH(cache, BSATTN_CALL);
 #undef BSATTN_CALL

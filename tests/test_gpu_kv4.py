@@ -596,3 +596,46 @@ def test_attn_long_context(bs):
     err = (o.double() - o_ref).square().mean((1, 2, 3)).sqrt() / o_ref.square().mean((1, 2, 3)).sqrt()
     assert float(err.max()) < 2.0 ** -10, err
     assert float((lse.double() - l_ref).abs().max()) < 1e-5
+
+
+@pytest.mark.parametrize("T", [1, 5, 8, 9])
+def test_append_a_few_tokens(bs, T):
+    """Decoding steps across page borders, pages that fill and pages that do not exist among them."""
+    Hkv, D, page = 3, 64, 16
+    lengths = [0, 7, 8, 15, 16, 31, 30, 100, 11]
+    cache = bs.Kv4Cache(60, Hkv, D, page_size=page, group=32)
+    ref.fill(cache, 4)
+    table = ref.table(cache, [n + T for n in lengths], 8, 5)
+    g = ref.gen(6)
+    k, v = (torch.randn(len(lengths), Hkv, T, D, generator=g, device="cuda").bfloat16() for _ in "kv")
+    for counts in (None, [T, 0, T, 1, T - 1, T, T, T, 0]):
+        before = _state(cache)
+        bs.kv4_append(cache, k, v, table, _i32(lengths), None if counts is None else _i32(counts))
+        bs.kv4_status(cache)
+        want = _append_ref(cache, before, k, v, table, lengths, counts or [T] * len(lengths))
+        assert all(torch.equal(a, b) for a, b in zip(_state(cache), want))
+        k, v = v, k
+    # a page that is not there: its tokens are skipped, the others written
+    before, bad = _state(cache), table.clone()
+    bad[3, 0] = -1  # position 15's
+    bs.kv4_append(cache, k, v, bad, _i32(lengths))
+    with pytest.raises(bs.BsattnError):
+        bs.kv4_status(cache)
+    rest = [b for b in range(len(lengths)) if b != 3]
+    want = _append_ref(cache, before, k[rest], v[rest], table[rest], [lengths[b] for b in rest], [T] * len(rest))
+    want = _append_ref(cache, want, k[3:4, :, 1:], v[3:4, :, 1:], table[3:4], [16], [T - 1])
+    assert all(torch.equal(a, b) for a, b in zip(_state(cache), want))
+
+
+@pytest.mark.parametrize("D, G, T, pages", [(128, 4, 1, 40), (128, 8, 4, 40), (128, 8, 5, 40), (64, 16, 4, 300), (128, 1, 1, 1500)])
+def test_select_more_heads_than_sms(bs, D, G, T, pages):
+    """On both sides of what the small CTAs take: rows, pages."""
+    Hkv, page, B = 4, 16, 50
+    few = [pages * page, 0, 1, 37, pages * page // 2 + 3]
+    cache = bs.Kv4Cache(2 * pages + 8, Hkv, D, page_size=page)
+    ref.fill(cache, 9)
+    table = ref.table(cache, few, pages, 3)
+    q = torch.randn(5, Hkv * G, T, D, generator=ref.gen(5), device="cuda").bfloat16()
+    at = torch.arange(B, device="cuda") % 5
+    got = bs.kv4_select(cache, q[at], table[at], _i32(few)[at], 7, sink=1, recent=2)
+    assert torch.equal(got, ref.select_pages(cache, q, table, few, 7, 1, 2)[at])

@@ -2,6 +2,10 @@
 (projection -> norm + rotation -> chosen blocks -> attention -> gradients),
 serving (prompt into the cache, then tokens), captured into graphs, on other
 streams and several at once."""
+import pathlib
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -163,6 +167,45 @@ def test_decoding_step_in_a_graph(bs):
         for a, b in zip(out, want[i]):
             assert torch.equal(a, b), i
     bs.kv4_status(cache)
+
+
+FIRST_USE = """
+import torch
+import block_sparse_flash_attn_gb300 as bs
+cache = bs.Kv4Cache(64, 4, 128)
+table = torch.arange(64, dtype=torch.int32, device="cuda").view(2, 32)
+n = torch.tensor([100, 700], dtype=torch.int32, device="cuda")
+x = torch.randn(2, 256, 24, 128, device="cuda").bfloat16()
+w = torch.ones(128, device="cuda")
+dy = [torch.randn(2, h, 256, 128, device="cuda") for h in (16, 4, 4)]
+rope = torch.randn(256, 64, 2, device="cuda")
+
+
+def step():
+    q, k, v = bs.qk_norm_rope(x, 16, 4, w, w, rope)
+    mask = bs.select_blocks(q, k, 2)
+    grads = bs.qk_norm_rope_bwd(x, *dy, w, w, rope)
+    bs.kv4_append(cache, k, v, table, n)
+    one = q[:, :, -1:].contiguous()
+    pages = bs.kv4_select(cache, one, table, n + 256, 4)
+    return (mask, pages) + grads + bs.kv4_attn(cache, one, table, n + 256, pages) + bs.kv4_attn(cache, one, table, n)
+
+
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = step()
+graph.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in got]
+assert all(torch.equal(a, b) for a, b in zip(got, step()))
+bs.kv4_status(cache)
+"""
+
+
+def test_first_use_inside_a_capture(bs):
+    """A process whose first calls are captured into a graph."""
+    root = pathlib.Path(__file__).resolve().parents[1]
+    subprocess.run([sys.executable, "-c", FIRST_USE], cwd=root, check=True, timeout=120)
 
 
 def test_training_step_in_a_graph(bs):

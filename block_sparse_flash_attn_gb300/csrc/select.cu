@@ -88,7 +88,7 @@ struct SelectParams {
   uint8_t* mask;  // [B][H][nb][nk]
   int H, Hkv, nb, nk, kdiv, kshift;  // kdiv = 1 << kshift key blocks a query block
   int keep, sink, local, causal;
-  int rows;  // query blocks a CTA: 16, or 4 when 16 rows of keys do not fit
+  int rows;  // query blocks a CTA: 16, 8 or 4 (select_rows)
 };
 
 // A row of n keys held by one warp, four consecutive ones a lane and piece of
@@ -280,9 +280,14 @@ __global__ void __launch_bounds__(kSelThreads, 4) choose_blocks_kernel(const Sel
 }
 
 // 16 query blocks a CTA (the tensor instruction's rows) while their keys fit
-// 128 KB of shared memory, 4 above (4 rows of at most 8192 keys).
+// 128 KB of shared memory, 4 above (4 rows of at most 8192 keys); 8, a row a warp,
+// where tiles of 16 would leave SMs idle (8 heads of 4096 tokens: 11 us, with 16
+// rows 13; 32 heads: 17 and 19; 4 x 32 heads: 39 and 40).
 constexpr int kSelKeyBytes = 128 << 10;
-int select_rows(int nk) { return 16 * ((nk + 3) & ~3) * 4 <= kSelKeyBytes ? 16 : 4; }
+int select_rows(int nk, int nb, int64_t heads, int sms) {
+  if (16 * ((nk + 3) & ~3) * 4 > kSelKeyBytes) return 4;
+  return (nb + 15) / 16 * heads <= sms ? kSelWarps : 16;
+}
 
 template <int D>
 cudaError_t launch_select(const void* q, const void* k, int q_blocks, int k_blocks, int key_block,
@@ -355,7 +360,9 @@ bsattn_status bsattn_select_blocks(const void* q, const void* k, int B, int H, i
   p.sink = sink;
   p.local = local;
   p.causal = (flags & BSATTN_CAUSAL) ? 1 : 0;
-  p.rows = select_rows(p.nk);
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return BSATTN_ERR_CUDA;
+  p.rows = select_rows(p.nk, nb, (int64_t)B * H, device_sm_count(dev));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int kb = kBlock / kdiv;
   return from_cuda(D == 64

@@ -40,6 +40,8 @@ CASES = [
     (1, 1, 1, 65664, 128, 128, 52, True, 1, 2),    # 513 query blocks
     (1, 2, 2, 1024, 128, 128, 100, True, 0, 1),    # more than there are
     (1, 2, 2, 1024, 128, 128, 1, False, 3, 2),     # fewer than are forced
+    (2, 40, 8, 2176, 64, 128, 3, True, 1, 1),      # tiles of 16 rows, and of one
+    (1, 80, 4, 2688, 128, 64, 6, False, 0, 1),     # of 16 and 5
 ]
 
 

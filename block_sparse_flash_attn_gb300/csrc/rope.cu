@@ -404,7 +404,9 @@ int rows_per_lane(int H, int D, int most) {
 }
 
 // The backward pass's split: CTAs a chunk, so that kBwdPerSm CTAs run on each SM
-// and none is without tokens.
+// and none is without tokens.  (As many for a chunk of few heads as for a full one:
+// a token costs a warp its latency.  3 x 1021 tokens, 16 + 2 x 4 heads of 64: 15 us,
+// with CTAs by the number of heads 19.)
 struct BwdSplit {
   int u, q_chunks, k_chunks, groups;
 };

@@ -1,5 +1,6 @@
 // Small device helpers shared by the operators around the attention kernels
-// (rope.cu, select.cu, kv4.cu): bf16 packing, exact sums, block floating point.
+// (rope.cu, select.cu, kv4.cu, kv4_attn.cu): bf16 packing, launches, pairs of
+// floats, exact sums, block floating point, threshold search, matrix products.
 #pragma once
 
 #include <atomic>
@@ -9,7 +10,6 @@
 
 namespace bsattn {
 
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // two bf16 of a 32-bit word, the lower half first
@@ -24,33 +24,6 @@ __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&h);
-}
-
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
-                    pack_bf16(f[6], f[7]));
-}
-
-// The same in clusters of `cluster` CTAs (along x).
-template <typename... KArgs, typename... Args>
-inline cudaError_t launch_dependent_clusters(void (*kernel)(KArgs...), dim3 grid, dim3 block,
-                                             int cluster, size_t smem, cudaStream_t stream,
-                                             Args... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = cluster;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, KArgs(args)...);
 }
 
 // Lets a kernel have `bytes` of dynamic shared memory; asks once a device.
@@ -141,6 +114,28 @@ inline cudaError_t launch_dependent(void (*kernel)(KArgs...), dim3 grid, dim3 bl
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, KArgs(args)...);
+}
+
+// The same in clusters of `cluster` CTAs (along x).
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_dependent_clusters(void (*kernel)(KArgs...), dim3 grid, dim3 block,
+                                             int cluster, size_t smem, cudaStream_t stream,
+                                             Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, KArgs(args)...);
 }
 

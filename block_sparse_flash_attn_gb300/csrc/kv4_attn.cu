@@ -18,8 +18,12 @@
 //
 // Tokens are the MMA's M (16 a tile), queries its N (8 a tile): S^T = K Q^T and
 // O^T = V^T P^T, since a key/value head has few query rows (G T <= 16 a tile).
-// P goes from S^T's accumulator layout to O^T's operand layout with movmatrix,
-// as an fp16 pair hi + lo (22 bits), so its rounding is below fp32 sums' own.
+// P step goes from S^T's accumulator layout to O^T's operand layout with
+// movmatrix, as an fp16 pair hi + lo.  Each query row and group of channels has
+// its own power of two beside the largest p step that it has met: that one lies
+// between 2^6 and 2^15, and the pair ends at fp16's 2^-24, so a weight is off by
+// 2^-23 of itself or by 2^-31 of the largest, whatever is larger.  A token of a
+// wide step and no weight takes no bits from the others.
 //
 // Bound: memory.  D + 8 bytes (groups of D) a token and head for 4 D G T
 // operations: at G T = 8 some 30 operations a byte, a tenth of the card's
@@ -83,7 +87,11 @@ constexpr int kSegmentStart = 6;
 constexpr int kMostGroupSteps = 64;
 constexpr int kMostCluster = 8;  // CTAs, the portable most
 constexpr float kNoMax = -1e30f;               // running maximum before any score
-constexpr float kLag = 8.0f;                   // a score may pass the running maximum by 2^8
+// Weights are taken beside 2^8 times the largest one so far: later scores may pass
+// the running maximum by that, and no weight is above 1.
+constexpr float kLag = 8.0f;
+// p step is brought to [2^6, 2^7) and may grow to 2^15 (as fp16 bits)
+constexpr uint32_t kMostWeight = 0x7800u;
 
 struct AttnParams {
   Kv4View c;
@@ -139,6 +147,22 @@ __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
 }
 __device__ __forceinline__ float2 unpack_half(uint32_t x) {
   return __half22float2(*reinterpret_cast<__half2*>(&x));
+}
+
+// The larger magnitudes of two fp16 pairs; a NaN gives way to a number.
+__device__ __forceinline__ uint32_t larger_halves(uint32_t a, uint32_t b) {
+  const __half2 m = __hmax2(*reinterpret_cast<__half2*>(&a), __habs2(*reinterpret_cast<__half2*>(&b)));
+  return *reinterpret_cast<const uint32_t*>(&m);
+}
+
+// The power of two that brings x > 0 to [2^6, 2^7), 2^106 for x below 2^-100; and
+// the lower end of what such a scale brings there, 2^6 / scale.
+__device__ __forceinline__ float scale_beside(float x) {
+  const int e = max((int)(__float_as_uint(x) >> 23), 27);
+  return __uint_as_float((uint32_t)(254 + 6 - e) << 23);
+}
+__device__ __forceinline__ float largest_beside(float scale) {
+  return __uint_as_float((254u + 6u << 23) - __float_as_uint(scale));
 }
 
 __device__ __forceinline__ void cluster_barrier() {
@@ -453,14 +477,15 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
     }
 
     group_barrier();
-    F2 mx[NT], l[NT], vm[NT][NG];  // -maximum, sum of weights, sum of weights * least
+    F2 mx[NT], l[NT], vm[NT][NG];  // -(maximum + kLag), sum of weights, of weights * least
+    F2 inv[NT][NG];                // the powers of two that p step is multiplied by
     float o[C][2][NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       mx[nt] = f2(-kNoMax);
       l[nt] = f2(0.0f);
 #pragma unroll
-      for (int n = 0; n < NG; ++n) vm[nt][n] = f2(0.0f);
+      for (int n = 0; n < NG; ++n) vm[nt][n] = f2(0.0f), inv[nt][n] = f2(scale_beside(0.0f));
 #pragma unroll
       for (int c = 0; c < C; ++c)
 #pragma unroll
@@ -468,10 +493,6 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[c][t][nt][e] = 0.0f;
     }
-    // steps are held beside a power of two not below any seen, so that p step
-    // stays inside fp16 (|p| <= 2^8)
-    float top_step = 7.888609e-31f;  // 2^-100
-    float inv_top = 1.2676506e30f;   // 2^100
 
     uint32_t from = 0;  // the ring's place of the tile
     auto tile = [&](int i, auto parity) {
@@ -526,7 +547,6 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
       }
       // ---- V's steps and minima; what a row does not see weighs nothing
       uint32_t v[NG][2];
-      float most = 0.0f;
 #pragma unroll
       for (int n = 0; n < NG; ++n) {
         const uint8_t* sc = stage + 2 * A::kCodes + A::kScales + (g * NG + n) * 4;
@@ -553,29 +573,42 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
             if (!any) v[n][t] = 0u;
         }
       }
+      // ---- weights p and p step.  Every other tile takes the codes'
+      // complements: p step n + p least = -p step (15 - n) + p (15 step + least).
+      // Codes are positive and least mostly not, so sums of either alone grow with
+      // the context while the output shrinks; in turn they stay near zero, and so
+      // do their roundings.
+      F2 pr[NT][2], w[NG][NT][2];
+      auto step_of = [&](int nt, int t, int n) {  // 0 * NaN must stay 0
+        const float step = bf16_lo(odd ? v[n][t] ^ 0x8000u : v[n][t]);
+        if (!hidden) return f2(step);
+        return f2(hidden >> (4 * nt + 2 * t) & 1 ? 0.0f : step,
+                  hidden >> (4 * nt + 2 * t) & 2 ? 0.0f : step);
+      };
+      uint32_t wh[NG][NT][2];
+      auto weigh = [&] {  // whether a weight passes its bound
+        float most = 0.0f;
+        uint32_t most16 = 0u;
 #pragma unroll
-      for (int n = 0; n < NG; ++n) most = fmaxf(most, fmaxf(fabsf(bf16_lo(v[n][0])), fabsf(bf16_lo(v[n][1]))));
-      float over = kNoMax;
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const float2 a = split(s[nt][0] + mx[nt]), c = split(s[nt][1] + mx[nt]);
-        over = fmaxf(over, fmaxf(fmaxf(a.x, a.y), fmaxf(c.x, c.y)));
-      }
-      // ---- rare: a score far above the running maximum, or a larger step
-      if (__any_sync(0xFFFFFFFFu, over > kLag || most > top_step)) {
+          for (int t = 0; t < 2; ++t) {
+            const float2 x = split(s[nt][t] + mx[nt]);
+            const float p0 = exp2_fast(x.x), p1 = exp2_fast(x.y);
+            most = fmaxf(most, fmaxf(p0, p1));
+            pr[nt][t] = f2(p0, p1);
 #pragma unroll
-        for (int sft = 16; sft > 0; sft >>= 1)
-          most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, sft));
-        float fs = 1.0f;
-        if (most > top_step) {
-          // the next power of two (2^127 at most: p step then passes 2^8 by 2)
-          uint32_t bits = (__float_as_uint(most) + 0x007FFFFFu) & 0x7F800000u;
-          bits = min(bits, 0x7F000000u);
-          const float t = __uint_as_float(bits);
-          fs = top_step / t;
-          top_step = t;
-          inv_top = 1.0f / t;
-        }
+            for (int n = 0; n < NG; ++n) {
+              w[n][nt][t] = pr[nt][t] * step_of(nt, t, n) * inv[nt][n];
+              const float2 ws = split(w[n][nt][t]);
+              wh[n][nt][t] = pack_half(ws.x, ws.y);
+              most16 = larger_halves(most16, wh[n][nt][t]);
+            }
+          }
+        return most > 1.0f || (most16 & 0xFFFFu) > kMostWeight || (most16 >> 16) > kMostWeight;
+      };
+      // ---- rare: a score far above the running maximum, or p step of its own scale
+      if (__any_sync(0xFFFFFFFFu, weigh())) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const float2 a = split(s[nt][0]), c = split(s[nt][1]), old = split(mx[nt]);
@@ -585,54 +618,63 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
 #pragma unroll
             for (int sft = 4; sft < 32; sft <<= 1)
               top[e] = fmaxf(top[e], __shfl_xor_sync(0xFFFFFFFFu, top[e], sft));
-            top[e] = fmaxf(top[e], e ? -old.y : -old.x);
+            top[e] = fmaxf(top[e] + kLag, e ? -old.y : -old.x);
           }
           const F2 f = f2(exp2_fast(-old.x - top[0]), exp2_fast(-old.y - top[1]));
           mx[nt] = f2(-top[0], -top[1]);
           l[nt] = l[nt] * f;
+          const float2 p0 = split(s[nt][0] + mx[nt]), p1 = split(s[nt][1] + mx[nt]);
+          const F2 q0 = f2(exp2_fast(p0.x), exp2_fast(p0.y)), q1 = f2(exp2_fast(p1.x), exp2_fast(p1.y));
 #pragma unroll
-          for (int n = 0; n < NG; ++n) vm[nt][n] = vm[nt][n] * f;
-          const float2 of = split(f * f2(fs));
+          for (int n = 0; n < NG; ++n) {
+            vm[nt][n] = vm[nt][n] * f;
+            // beside the largest of this tile, or of the ones before it
+            const float2 b0 = split(q0 * step_of(nt, 0, n)), b1 = split(q1 * step_of(nt, 1, n));
+            const float2 was = split(inv[nt][n]), fs = split(f);
+            float large[2] = {fmaxf(fabsf(b0.x), fabsf(b1.x)), fmaxf(fabsf(b0.y), fabsf(b1.y))};
 #pragma unroll
-          for (int c = 0; c < C; ++c)
+            for (int e = 0; e < 2; ++e) {
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              o[c][k][nt][0] *= of.x, o[c][k][nt][1] *= of.y;
-              o[c][k][nt][2] *= of.x, o[c][k][nt][3] *= of.y;
+              for (int sft = 4; sft < 32; sft <<= 1)
+                large[e] = fmaxf(large[e], __shfl_xor_sync(0xFFFFFFFFu, large[e], sft));
+              const float before = (e ? fs.y : fs.x) * largest_beside(e ? was.y : was.x);
+              large[e] = scale_beside(fmaxf(large[e], before));
             }
+            inv[nt][n] = f2(large[0], large[1]);
+            // f new / old, at most 2 (f new first: new / old alone may overflow)
+            const float2 of = split(f * inv[nt][n] * f2(largest_beside(was.x), largest_beside(was.y)) *
+                                    f2(0.015625f));
+#pragma unroll
+            for (int c = n * A::CG; c < (n + 1) * A::CG; ++c)
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                o[c][k][nt][0] *= of.x, o[c][k][nt][1] *= of.y;
+                o[c][k][nt][2] *= of.x, o[c][k][nt][3] *= of.y;
+              }
+          }
         }
+        weigh();
       }
-      // ---- weights p step, as fp16 hi + lo, turned to the operand layout.
-      // Every other tile takes the codes' complements: p step n + p least =
-      // -p step (15 - n) + p (15 step + least).  Codes are positive and least
-      // mostly not, so sums of either alone grow with the context while the
-      // output shrinks; in turn they stay near zero, and so do their roundings.
+      // ---- hi + lo, turned to the operand layout
       constexpr uint32_t flip = odd ? 0xFFFFFFFFu : 0u;
-      const float signed_inv = odd ? -inv_top : inv_top;
-      uint32_t wh[NG][NT][2], wl[NG][NT][2];
+      uint32_t wl[NG][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          const float2 x = split(s[nt][t] + mx[nt]);
-          const F2 pr = f2(exp2_fast(x.x), exp2_fast(x.y));
-          l[nt] = l[nt] + pr;
+          l[nt] = l[nt] + pr[nt][t];
 #pragma unroll
           for (int n = 0; n < NG; ++n) {
             F2 least = f2(odd ? fmaf(bf16_lo(v[n][t]), 15.0f, bf16_hi(v[n][t])) : bf16_hi(v[n][t]));
-            F2 step = f2(bf16_lo(v[n][t]) * signed_inv);
-            if (hidden) {  // 0 * NaN must stay 0
-              const float2 a = split(least), c = split(step);
-              const bool h0 = hidden >> (4 * nt + 2 * t) & 1, h1 = hidden >> (4 * nt + 2 * t) & 2;
-              least = f2(h0 ? 0.0f : a.x, h1 ? 0.0f : a.y);
-              step = f2(h0 ? 0.0f : c.x, h1 ? 0.0f : c.y);
+            if (hidden) {
+              const float2 a = split(least);
+              least = f2(hidden >> (4 * nt + 2 * t) & 1 ? 0.0f : a.x,
+                         hidden >> (4 * nt + 2 * t) & 2 ? 0.0f : a.y);
             }
-            vm[nt][n] = fma2(pr, least, vm[nt][n]);
-            const F2 w = pr * step;
-            const float2 ws = split(w);
-            const uint32_t hi16 = pack_half(ws.x, ws.y);
+            vm[nt][n] = fma2(pr[nt][t], least, vm[nt][n]);
+            const uint32_t hi16 = wh[n][nt][t];
             const float2 back = unpack_half(hi16);
-            const float2 rest = split(fma2(f2(back.x, back.y), f2(-1.0f), w));
+            const float2 rest = split(fma2(f2(back.x, back.y), f2(-1.0f), w[n][nt][t]));
             const uint32_t lo16 = pack_half(rest.x, rest.y);
             if (TWICE) {
               wh[n][nt][t] = transpose8x8(j < 2 ? hi16 : lo16);
@@ -723,9 +765,11 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
           sm[gwarp * RP + r] = -(e ? m2.y : m2.x);
           sl[gwarp * RP + r] = e ? l2.y : l2.x;
         }
-        const float f = 16777216.0f * top_step, f16 = 1048576.0f * top_step;  // 2^24, 2^20
 #pragma unroll
         for (int c = 0; c < C; ++c) {
+          const float2 iv = split(inv[nt][c / A::CG]);
+          const float top = 0.015625f * largest_beside(e ? iv.y : iv.x);
+          const float f = 16777216.0f * top, f16 = 1048576.0f * top;  // 2^24, 2^20
           const int ch = kWide ? 64 * (c / 2) + 8 * g + 4 * (c & 1)
                                : 32 * c + 8 * (g & 3) + 4 * (g >> 2);
           const float base = e ? vm2[c / A::CG].y : vm2[c / A::CG].x;

@@ -639,3 +639,116 @@ def test_select_more_heads_than_sms(bs, D, G, T, pages):
     at = torch.arange(B, device="cuda") % 5
     got = bs.kv4_select(cache, q[at], table[at], _i32(few)[at], 7, sink=1, recent=2)
     assert torch.equal(got, ref.select_pages(cache, q, table, few, 7, 1, 2)[at])
+
+
+#          Hkv G  D    page group T  lengths, table columns behind them, copies of the batch
+WEIGHTED = [
+    (2, 4, 128, 16, 128, 1, [1024, 300], 0, 1),          # clusters
+    (1, 2, 64, 16, 32, 1, [1024], 900, 1),               # ranges
+    (2, 8, 128, 32, 32, 1, [1000, 77], 0, 1),            # 8 rows
+    (4, 4, 128, 64, 64, 4, [600], 0, 1),                 # 16 rows
+    (8, 4, 64, 16, 64, 1, [700, 1024, 0, 33], 0, 60),    # a few warps a head
+    (8, 8, 128, 16, 128, 1, [130, 90], 0, 150),
+]
+
+
+class _Weighted:
+    """A case whose queries are positive, so that keys of one sign have weight or none."""
+
+    def __init__(self, bs, case):
+        *rest, extra, copies = case
+        self.cache, self.table, self.q, self.n = _attn_case(bs, tuple(rest))
+        self.q.abs_()
+        self.lengths, self.copies = rest[-1], copies
+        self.table = torch.cat([self.table, torch.full((len(self.lengths), extra), -1, dtype=torch.int32,
+                                                       device="cuda")], 1)
+
+    def places(self, first, last=None, step=1):
+        """(page, place) of every sequence's tokens first(n), first(n) + step ... below last(n)."""
+        page = self.cache.page_size
+        for b, n in enumerate(self.lengths):
+            for pos in range(first(n), n if last is None else last(n), step):
+                yield int(self.table[b, pos // page]), pos % page
+
+    def key(self, at, value):
+        self.cache.k_scales[at[0], :, at[1], :, 0] = 0
+        self.cache.k_scales[at[0], :, at[1], :, 1] = value
+
+    def call(self, bs):
+        at = torch.arange(len(self.lengths) * self.copies, device="cuda") % len(self.lengths)
+        got = bs.kv4_attn(self.cache, self.q[at], self.table[at], self.n[at], out_f32=True)
+        bs.kv4_status(self.cache)
+        return at, *got
+
+    def sizes(self):
+        """Per output channel the size of the terms that it is the sum of: sum_i p_i (15 step_i + |least_i|)."""
+        cache, (B, H, T, D) = self.cache, self.q.shape
+        Hkv, page, G = cache.kv_heads, cache.page_size, H // cache.kv_heads
+        out = torch.zeros(B, H, T, D, dtype=torch.float64, device="cuda")
+        for b, n in enumerate(self.lengths):
+            pg, pos = self.table[b, :-(-n // page)].long(), torch.arange(n, device="cuda")
+            for h in range(Hkv if n else 0):
+                k = ref.values(cache.k_codes[pg, h], cache.k_scales[pg, h]).reshape(-1, D)[:n]
+                vs = cache.v_scales[pg, h].double().reshape(-1, D // cache.group, 2)[:n]
+                size = (15 * vs[..., 0] + vs[..., 1].abs()).repeat_interleave(cache.group, -1)
+                for t in range(T):
+                    s = self.q[b, h * G:(h + 1) * G, t].double() @ k.T * D ** -0.5
+                    s = s.masked_fill(pos > n - T + t, float("-inf"))
+                    if n - T + t >= 0:
+                        out[b, h * G:(h + 1) * G, t] = torch.softmax(s, -1) @ size
+        return out
+
+    def check(self, bs):
+        """Every term's relative error is within _ops_ref.attn's bound for a weight (twice: of the
+        weight, and of the sum of weights), so an output is off by that part of its own terms' sizes.
+        (The pair of halves ends at 2^-31 of a row's largest p step: over m tokens less than the
+        m U32 that the bound has for the sums.)"""
+        o_ref, _, _, dp = ref.attn(self.cache, self.q, self.table, self.lengths)
+        tol = 2 * dp[..., None] * self.sizes() + U32 * o_ref.abs()
+        at, o, _ = self.call(bs)
+        err = (o.double() - o_ref[at]).abs()
+        assert bool((err <= tol[at]).all()), float((err / (tol[at] + 1e-300)).max())
+
+
+@pytest.mark.parametrize("power", [20, 60])
+@pytest.mark.parametrize("case", WEIGHTED, ids=str)
+def test_attn_wide_values_without_weight(bs, case, power):
+    """Tokens that the queries give no weight (exp(-100)), their values 2^power times the others'."""
+    w = _Weighted(bs, case)
+    for at in w.places(lambda n: 5, step=97):
+        w.key(at, -8.0)
+        w.cache.v_scales[at[0], :, at[1]] *= 2.0 ** power
+    w.check(bs)
+
+
+@pytest.mark.parametrize("power", [-20, 0, 90])
+@pytest.mark.parametrize("case", WEIGHTED, ids=str)
+def test_attn_wide_values_whose_weight_vanishes(bs, case, power):
+    """The first three quarters of a context weigh nothing once the rest, with values far smaller, is seen."""
+    w = _Weighted(bs, case)
+    for at in w.places(lambda n: 0, lambda n: 3 * n // 4):
+        w.key(at, -8.0 if power < 50 else -16.0)
+        w.cache.v_scales[at[0], :, at[1]] *= 2.0 ** power
+    for at in w.places(lambda n: 3 * n // 4):
+        w.cache.v_scales[at[0], :, at[1]] *= 2.0 ** -40
+    w.check(bs)
+
+
+@pytest.mark.parametrize("case", WEIGHTED, ids=str)
+def test_attn_small_weights_beside_a_value_of_zero(bs, case):
+    """One token has nearly all the weight, and its value is zero: the others make the output."""
+    w = _Weighted(bs, case)
+    w.cache.k_scales.mul_(0.1)
+    for at in w.places(lambda n: 0, lambda n: min(n, 1)):
+        w.key(at, 1.6)
+        w.cache.v_scales[at[0], :, at[1]] = 0
+    w.check(bs)
+
+
+@pytest.mark.parametrize("case", [c for c in WEIGHTED if c[4] < c[2]], ids=str)
+def test_attn_groups_of_other_sizes(bs, case):
+    """Each group of channels 2^-20 times the one before: every output beside its own group."""
+    w = _Weighted(bs, case)
+    for n in range(w.cache.head_dim // w.cache.group):
+        w.cache.v_scales[..., n, :] *= 2.0 ** (-20 * n)
+    w.check(bs)

@@ -10,11 +10,25 @@
 //   q . k_i = step_i (q . n_i) + least_i sum(q)           (per group of channels)
 //   sum_i p_i v_i = sum_i (p_i step_i) n_i + sum_i p_i least_i
 // so both products run on the codes themselves, and steps and minima touch
-// one number a (token, query, group).  A code masked out of a 32-bit word IS an
-// fp16 number: the bits 0x000F hold n as the subnormal n 2^-24, the bits
-// 0x00F0 as 16 n 2^-24, both exact operands of an fp16 MMA.  One AND makes two
-// operands; the factor 16 goes into the queries (divided by 16) and the
-// output, the 2^-24 into a final factor.
+// one number a (token, query, group).  A code masked out of a 32-bit word IS a
+// 16-bit float: the low bits of one hold n as a subnormal, an exact operand.  One
+// AND makes two operands; powers of two go into the queries and a final factor.
+// But the tensor instruction lines products up by their operands' exponents and
+// cuts them 25 bits below the largest, and a subnormal has the exponent of 1
+// times its type's least normal number, however small it is (seen with single
+// products): a code in the low bits of an fp16 loses up to 10 of those bits.  So
+// - K's codes are bf16 operands, in its bits 0-3 and 4-7 (the latter reach the
+//   exponent's last bit, where bf16 is linear still): 2^-18 and 2^-22 of a code
+//   beside a row's largest query; queries are bf16 themselves;
+// - V's are fp16 operands, for the weights' sake, moved to the mantissa's top, bits
+//   6-9: 2^-21 of a code beside a row's largest weight.
+// Every other token's codes are taken as complements: p step n + p least =
+// -p step (15 - n) + p (15 step + least).  Codes are positive and least mostly not,
+// so sums of either alone grow with the context while the output shrinks, and what
+// is cut off adds up; in turn the sums stay near zero and the cuts cancel.
+// Off the 64-bit result, of the output's norm (norm of the difference): 777 tokens
+// 4e-7, 32768 to 65536 tokens 1.9e-6; with all codes as fp16 subnormals in place
+// and complements by tiles 4.5e-5 and 3.7e-5.
 //
 // Tokens are the MMA's M (16 a tile), queries its N (8 a tile): S^T = K Q^T and
 // O^T = V^T P^T, since a key/value head has few query rows (G T <= 16 a tile).
@@ -52,7 +66,6 @@
 #include <cmath>
 #include <cstdint>
 #include <mutex>
-#include <type_traits>
 
 #include <cuda_fp16.h>
 
@@ -136,6 +149,13 @@ __device__ __forceinline__ float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// Four 8 x 8 matrices of 16-bit words, transposed: of each pair of pieces (16
+// bytes) this lane's word of rows 2j and 2j + 1, and of those 8 on.
+__device__ __forceinline__ void load_transposed(uint32_t at, uint32_t (&a)[2], uint32_t (&b)[2]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(a[0]), "=r"(a[1]), "=r"(b[0]), "=r"(b[1])
+               : "r"(at));
+}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -149,6 +169,16 @@ __device__ __forceinline__ float2 unpack_half(uint32_t x) {
   return __half22float2(*reinterpret_cast<__half2*>(&x));
 }
 
+// Of a pair of tokens' codes in bits 6-9 and 22-25 the even token's code and the
+// odd one's complement.  One instruction, if one of its two constants comes from a
+// register: the long contexts above 332 us (by twos), with two instructions 372,
+// with the loaded words turned over first 338.
+__device__ __forceinline__ uint32_t complements(uint32_t x, uint32_t flip) {
+  uint32_t y;  // (x ^ flip) & mask
+  asm("lop3.b32 %0, %1, %2, %3, 0x48;" : "=r"(y) : "r"(x), "n"(0x03C003C0u), "r"(flip));
+  return y;
+}
+
 // The larger magnitudes of two fp16 pairs; a NaN gives way to a number.
 __device__ __forceinline__ uint32_t larger_halves(uint32_t a, uint32_t b) {
   const __half2 m = __hmax2(*reinterpret_cast<__half2*>(&a), __habs2(*reinterpret_cast<__half2*>(&b)));
@@ -156,13 +186,13 @@ __device__ __forceinline__ uint32_t larger_halves(uint32_t a, uint32_t b) {
 }
 
 // The power of two that brings x > 0 to [2^6, 2^7), 2^106 for x below 2^-100; and
-// the lower end of what such a scale brings there, 2^6 / scale.
+// the lower end of what such a scale brings there, 2^6 / |scale|.
 __device__ __forceinline__ float scale_beside(float x) {
   const int e = max((int)(__float_as_uint(x) >> 23), 27);
   return __uint_as_float((uint32_t)(254 + 6 - e) << 23);
 }
 __device__ __forceinline__ float largest_beside(float scale) {
-  return __uint_as_float((254u + 6u << 23) - __float_as_uint(scale));
+  return __uint_as_float((254u + 6u << 23) - (__float_as_uint(scale) & 0x7FFFFFFFu));
 }
 
 __device__ __forceinline__ void cluster_barrier() {
@@ -239,6 +269,11 @@ struct Attn {
   // (the join of a warp's results takes the place of its ring)
   static_assert(RP * (D + 3) * 4 <= kWarpRing, "shared memory");
   static constexpr int kSlot = RP * (D + 2);  // floats of a partial result
+  // Tiles a pass of the loop: a turn of the ring, whose places are constants then;
+  // two where registers run out.  32 sequences of 32768 to 65536 tokens, groups of
+  // 128: 318 us, by twos 332, one by one 355; 64 heads of 16 rows and 49152 tokens,
+  // groups of 32: 241 us, by twos 225.
+  static constexpr int kUnroll = NG == 4 && NT == 2 ? 2 : kStages;
 
   // pieces of a row are stored permuted by its token, so that the 32-bit reads
   // of both products meet 32 banks
@@ -252,7 +287,6 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
     kv4_attn_kernel(const AttnParams p) {
   using A = Attn<D, NG, NT, TWICE>;
   constexpr int C = A::C, RB = A::RB, RP = A::RP, KW = A::CG;
-  constexpr bool kWide = D / NG >= 64;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int warp_sums[kAttnWarps];
   constexpr int kMostGroups = MODE == kGroups ? kAttnWarps : 1;
@@ -328,13 +362,12 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
   const uint32_t ring = shared_address(smem) + warp * A::kWarpRing;
   const uint8_t* my_ring = smem + warp * A::kWarpRing;
   // Where this lane's words begin.  K: tokens g and g + 8, words j KW .. j KW +
-  // KW - 1 of each group.  V: tokens 2j, 2j + 1 and 8 on, word g of each 64
-  // channels; where a group has 32 channels, word g mod 4 of each 32, its half
-  // g / 4.  A row's 16-byte piece c is at the offset with 16 c in its swizzled
-  // bits.
+  // KW - 1 of each group.  V: the row that it points out to the transposing load,
+  // piece lane / 16 of token lane mod 16.  A row's 16-byte piece c is at the offset
+  // with 16 c in its swizzled bits.
   const uint32_t k_at = g * RB + (4 * KW * j & 15) + 16 * (A::swizzle(g) ^ (KW * j / 4));
-  const uint32_t v_at = 2 * j * RB + 4 * (g & 3) + 16 * (A::swizzle(2 * j) ^ (kWide ? g >> 2 : 0));
-  const uint32_t half = g < 4 ? 0x5410u : 0x7632u;
+  const uint32_t v_at =
+      ring + A::kCodes + lane % 16 * RB + 16 * (A::swizzle(lane % 16) ^ (lane / 16));
   int2* my_tiles = tiles[warp];
   // this lane's pieces of a tile: codes (token, piece) = lane / C, lane % C, and
   // for D = 128 eight tokens on; one piece of the scales
@@ -450,19 +483,24 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
 #pragma unroll
         for (int n = 0; n < NG; ++n) sum[n] += __shfl_xor_sync(0xFFFFFFFFu, sum[n], o);
       }
-      // the row's largest query goes to [2^13, 2^14): fp16 then holds bf16
-      // queries 2^27 times smaller exactly, a sixteenth of them included
-      int sh = 0;
-      if (top > 0.0f && top <= 3.4e38f) sh = min(13 - ilogbf(top), 120);
-      const float f = ldexpf(1.0f, sh), f16 = f * 0.0625f;
+      // the row's largest query goes to [2^116, 2^117), so that products with codes
+      // (n 2^-133) are normal numbers; in two factors, for 2^sh may pass fp32's range
+      int sh = 120;
+      if (top > 0.0f && top <= 3.4e38f) sh = 116 - ilogbf(top);
+      const float fa = ldexpf(1.0f, sh / 2), fb = ldexpf(1.0f, sh - sh / 2);
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[c][i] = x[c][i] * fa * fb;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         if (gwarp == 0)  // (the same for all warps)
           queries[nt][c][lane] = make_uint4(
-              pack_half(x[c][0] * f, x[c][4] * f), pack_half(x[c][2] * f, x[c][6] * f),
-              pack_half(x[c][1] * f16, x[c][5] * f16), pack_half(x[c][3] * f16, x[c][7] * f16));
+              pack_bf16(x[c][0], x[c][4]), pack_bf16(x[c][2], x[c][6]),
+              pack_bf16(x[c][1] * 0.0625f, x[c][5] * 0.0625f),
+              pack_bf16(x[c][3] * 0.0625f, x[c][7] * 0.0625f));
       }
-      const float m = p.scale_log2 * ldexpf(1.0f, 24 - sh);
+      const float m = p.scale_log2 * ldexpf(1.0f, 133 - sh);
       auto rows2 = [&](float v) {  // of rows 2j and 2j + 1, from the lanes that loaded them
         return f2(__shfl_sync(0xFFFFFFFFu, v, 8 * j), __shfl_sync(0xFFFFFFFFu, v, 8 * j + 4));
       };
@@ -478,14 +516,15 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
 
     group_barrier();
     F2 mx[NT], l[NT], vm[NT][NG];  // -(maximum + kLag), sum of weights, of weights * least
-    F2 inv[NT][NG];                // the powers of two that p step is multiplied by
+    F2 inv[NT][NG];  // what p step is multiplied by: a power of two, below 0 for complements
+    const float sign = g & 1 ? -1.0f : 1.0f, fifteen = g & 1 ? 15.0f : 0.0f;
     float o[C][2][NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       mx[nt] = f2(-kNoMax);
       l[nt] = f2(0.0f);
 #pragma unroll
-      for (int n = 0; n < NG; ++n) vm[nt][n] = f2(0.0f), inv[nt][n] = f2(scale_beside(0.0f));
+      for (int n = 0; n < NG; ++n) vm[nt][n] = f2(0.0f), inv[nt][n] = f2(sign * scale_beside(0.0f));
 #pragma unroll
       for (int c = 0; c < C; ++c)
 #pragma unroll
@@ -495,15 +534,18 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
     }
 
     uint32_t from = 0;  // the ring's place of the tile
-    auto tile = [&](int i, auto parity) {
-      constexpr bool odd = decltype(parity)::value;
+    uint32_t flip;      // the odd tokens' halves (kept in a register: see complements)
+    asm volatile("mov.b32 %0, 0xFFFF0000;" : "=r"(flip));
+#pragma unroll A::kUnroll
+    for (int i = 0; i < n_tiles; ++i) {
       copy_wait<kStages - 2>();
       __syncwarp();
       issue(i + kStages - 1);
-      const uint8_t* stage = my_ring + from;
+      const uint32_t at_stage = from;
+      const uint8_t* stage = my_ring + at_stage;
       from = from == (kStages - 1) * A::kStage ? 0 : from + A::kStage;
       const int pos = my_tiles[i & 127].y;
-      if (pos < 0) return;
+      if (pos < 0) continue;
 
       // ---- scores (base 2): token g (t = 0) and g + 8, rows 2j and 2j + 1 as a pair
       F2 s[NT][2];
@@ -528,8 +570,8 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             const uint4 qf = queries[nt][n * KW + k][lane];
-            mma_f16(acc[nt], a, qf.x, qf.y);
-            mma_f16(acc16[nt], a16, qf.z, qf.w);
+            mma_bf16(acc[nt], a, qf.x, qf.y);
+            mma_bf16(acc16[nt], a16, qf.z, qf.w);
           }
         }
         const uint8_t* ks = stage + 2 * A::kCodes + (g * NG + n) * 4;
@@ -573,14 +615,10 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
             if (!any) v[n][t] = 0u;
         }
       }
-      // ---- weights p and p step.  Every other tile takes the codes'
-      // complements: p step n + p least = -p step (15 - n) + p (15 step + least).
-      // Codes are positive and least mostly not, so sums of either alone grow with
-      // the context while the output shrinks; in turn they stay near zero, and so
-      // do their roundings.
+      // ---- weights p and p step
       F2 pr[NT][2], w[NG][NT][2];
       auto step_of = [&](int nt, int t, int n) {  // 0 * NaN must stay 0
-        const float step = bf16_lo(odd ? v[n][t] ^ 0x8000u : v[n][t]);
+        const float step = bf16_lo(v[n][t]);
         if (!hidden) return f2(step);
         return f2(hidden >> (4 * nt + 2 * t) & 1 ? 0.0f : step,
                   hidden >> (4 * nt + 2 * t) & 2 ? 0.0f : step);
@@ -640,10 +678,10 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
               const float before = (e ? fs.y : fs.x) * largest_beside(e ? was.y : was.x);
               large[e] = scale_beside(fmaxf(large[e], before));
             }
-            inv[nt][n] = f2(large[0], large[1]);
+            inv[nt][n] = f2(sign * large[0], sign * large[1]);
             // f new / old, at most 2 (f new first: new / old alone may overflow)
-            const float2 of = split(f * inv[nt][n] * f2(largest_beside(was.x), largest_beside(was.y)) *
-                                    f2(0.015625f));
+            const float2 of = split(f * f2(large[0], large[1]) *
+                                    f2(largest_beside(was.x), largest_beside(was.y)) * f2(0.015625f));
 #pragma unroll
             for (int c = n * A::CG; c < (n + 1) * A::CG; ++c)
 #pragma unroll
@@ -656,7 +694,6 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
         weigh();
       }
       // ---- hi + lo, turned to the operand layout
-      constexpr uint32_t flip = odd ? 0xFFFFFFFFu : 0u;
       uint32_t wl[NG][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -665,7 +702,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
           l[nt] = l[nt] + pr[nt][t];
 #pragma unroll
           for (int n = 0; n < NG; ++n) {
-            F2 least = f2(odd ? fmaf(bf16_lo(v[n][t]), 15.0f, bf16_hi(v[n][t])) : bf16_hi(v[n][t]));
+            F2 least = f2(fmaf(bf16_lo(v[n][t]), fifteen, bf16_hi(v[n][t])));
             if (hidden) {
               const float2 a = split(least);
               least = f2(hidden >> (4 * nt + 2 * t) & 1 ? 0.0f : a.x,
@@ -685,44 +722,30 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
           }
         }
       }
-      // ---- O^T += V^T P^T: of each half word, M tile 0 is made of codes 0 (rows
-      // g) and 2 (rows g + 8), M tile 1 of the whole bytes, codes 0 + 16 1 and
-      // 2 + 16 3, from which tile 0 is taken off at the end.
+      // ---- O^T += V^T P^T: of each half word (channels 32 c + 4 g on, tokens 2j
+      // and 2j + 1, and 8 on), M tile 0 is made of codes 0 (rows g) and 2 (rows
+      // g + 8), M tile 1 of codes 1 and 3
+      uint32_t x[C][2];
+#pragma unroll
+      for (int c = 0; c < C; c += 2) load_transposed((v_at + at_stage) ^ (16 * c), x[c], x[c + 1]);
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        uint32_t x0, x1;
-        if (kWide) {
-          const uint8_t* at = stage + A::kCodes + (v_at ^ (16 * (c & ~1)));
-          const uint32_t sel = c & 1 ? 0x7632u : 0x5410u;
-          x0 = __byte_perm(word(at), word(at + RB), sel);
-          x1 = __byte_perm(word(at + 8 * RB), word(at + 9 * RB), sel);
-        } else {
-          const uint8_t* at = stage + A::kCodes + (v_at ^ (16 * c));
-          x0 = __byte_perm(word(at), word(at + RB), half);
-          x1 = __byte_perm(word(at + 8 * RB), word(at + 9 * RB), half);
-        }
-        const uint32_t y0 = odd ? x0 >> 8 : __byte_perm(x0, 0u, 0x4341);
-        const uint32_t y1 = odd ? x1 >> 8 : __byte_perm(x1, 0u, 0x4341);
-        const uint32_t bytes[4] = {(x0 ^ flip) & 0x00FF00FFu, odd ? ~y0 & 0x00FF00FFu : y0,
-                                   (x1 ^ flip) & 0x00FF00FFu, odd ? ~y1 & 0x00FF00FFu : y1};
-        const uint32_t a[4] = {(x0 ^ flip) & 0x000F000Fu, (y0 ^ flip) & 0x000F000Fu,
-                               (x1 ^ flip) & 0x000F000Fu, (y1 ^ flip) & 0x000F000Fu};
+        const uint32_t x0 = x[c][0], x1 = x[c][1];
+        const uint32_t a[2][4] = {
+            {complements(x0 << 6, flip), complements(x0 >> 2, flip), complements(x1 << 6, flip),
+             complements(x1 >> 2, flip)},
+            {complements(x0 << 2, flip), complements(x0 >> 6, flip), complements(x1 << 2, flip),
+             complements(x1 >> 6, flip)}};
         const int n = c / A::CG;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          mma_f16(o[c][0][nt], a, wh[n][nt][0], wh[n][nt][1]);
-          mma_f16(o[c][1][nt], bytes, wh[n][nt][0], wh[n][nt][1]);
-          if (!TWICE) {
-            mma_f16(o[c][0][nt], a, wl[n][nt][0], wl[n][nt][1]);
-            mma_f16(o[c][1][nt], bytes, wl[n][nt][0], wl[n][nt][1]);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            mma_f16(o[c][k][nt], a[k], wh[n][nt][0], wh[n][nt][1]);
+            if (!TWICE) mma_f16(o[c][k][nt], a[k], wl[n][nt][0], wl[n][nt][1]);
           }
         }
       }
-    };
-#pragma unroll 1
-    for (int i = 0; i < n_tiles; i += 2) {
-      tile(i, std::false_type());
-      if (i + 1 < n_tiles) tile(i + 1, std::true_type());
     }
     copy_wait<0>();
 
@@ -769,14 +792,12 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
         for (int c = 0; c < C; ++c) {
           const float2 iv = split(inv[nt][c / A::CG]);
           const float top = 0.015625f * largest_beside(e ? iv.y : iv.x);
-          const float f = 16777216.0f * top, f16 = 1048576.0f * top;  // 2^24, 2^20
-          const int ch = kWide ? 64 * (c / 2) + 8 * g + 4 * (c & 1)
-                               : 32 * c + 8 * (g & 3) + 4 * (g >> 2);
+          const float f = 262144.0f * top;  // 2^18
+          const int ch = 32 * c + 4 * g;
           const float base = e ? vm2[c / A::CG].y : vm2[c / A::CG].x;
           *reinterpret_cast<float4*>(so + (gwarp * RP + r) * D + ch) = make_float4(
-              fmaf(o[c][0][nt][e], f, base), fmaf(o[c][1][nt][e] - o[c][0][nt][e], f16, base),
-              fmaf(o[c][0][nt][e + 2], f, base),
-              fmaf(o[c][1][nt][e + 2] - o[c][0][nt][e + 2], f16, base));
+              fmaf(o[c][0][nt][e], f, base), fmaf(o[c][1][nt][e], f, base),
+              fmaf(o[c][0][nt][e + 2], f, base), fmaf(o[c][1][nt][e + 2], f, base));
         }
       }
     }

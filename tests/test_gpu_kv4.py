@@ -752,3 +752,50 @@ def test_attn_groups_of_other_sizes(bs, case):
     for n in range(w.cache.head_dim // w.cache.group):
         w.cache.v_scales[..., n, :] *= 2.0 ** (-20 * n)
     w.check(bs)
+
+
+#         Hkv G  D    page group
+CUTS = [(1, 4, 128, 16, 128), (2, 8, 64, 16, 32), (1, 8, 128, 64, 64), (2, 16, 128, 16, 32), (1, 2, 64, 32, 64),
+        (1, 16, 64, 16, 64), (1, 3, 128, 16, 32)]
+
+
+@pytest.mark.parametrize("case", CUTS, ids=str)
+def test_attn_small_products_beside_a_large_one(bs, case):
+    """One token of weight 1 and fifteen of weight 2^-15.5, all with the same step.
+
+    A tensor instruction lines products up and cuts them: at 2^-21 of a code beside the largest
+    weight, 16 products.  Beside that some 24 roundings in 32 bits (weight, its halves, sums) of at
+    most 15 steps.  (Operands cut at 2^-15 are off by ten times the bound.)"""
+    Hkv, G, D, page, group = case
+    cache, table, q, n = _attn_case(bs, (Hkv, G, D, page, group, 1, [16]))
+    q.fill_(1.0)
+    pg = int(table[0, 0])
+    cache.k_scales[pg, ..., 0] = 0
+    cache.k_scales[pg, :, 0, :, 1] = 0
+    cache.k_scales[pg, :, 1:, :, 1] = -10.75 * D ** -0.5
+    cache.v_scales[pg, ..., 0] = 1
+    cache.v_scales[pg, ..., 1] = 0
+    o, _ = bs.kv4_attn(cache, q, table, n, out_f32=True)
+    want = ref.attn(cache, q, table, [16])[0]
+    assert float((o.double() - want).abs().max()) <= 16 * 2.0 ** -21 + 24 * U32 * 15
+
+
+@pytest.mark.parametrize("case", CUTS, ids=str)
+def test_attn_small_queries_beside_a_large_one(bs, case):
+    """A single cached token, whose LSE is the score: one query channel of 1, the others 1.75 2^-19.
+
+    32-bit sums as in _ops_ref.attn, and the cuts of the 16 products that share an instruction with
+    the large one, and of their sum: 2^-18 of a step beside the largest query.  (Cut at 2^-15: twice
+    the bound.)"""
+    Hkv, G, D, page, group = case
+    cache, table, q, n = _attn_case(bs, (Hkv, G, D, page, group, 1, [1]))
+    q.fill_(1.75 * 2.0 ** -19)
+    q[..., 4] = 1.0
+    pg = int(table[0, 0])
+    cache.k_codes[pg] = 0x99
+    cache.k_scales[pg, ..., 0] = 1
+    cache.k_scales[pg, ..., 1] = 0
+    _, lse = bs.kv4_attn(cache, q, table, n)
+    s = q.double().sum(-1) * 9 * D ** -0.5
+    assert float((lse - s).abs().max()) <= D ** -0.5 * (
+        (D + 8) * U32 * 15 * float(q[0, 0].double().sum()) + 17 * 2.0 ** -18)

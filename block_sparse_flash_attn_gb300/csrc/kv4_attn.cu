@@ -483,10 +483,11 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
 #pragma unroll
         for (int n = 0; n < NG; ++n) sum[n] += __shfl_xor_sync(0xFFFFFFFFu, sum[n], o);
       }
-      // the row's largest query goes to [2^116, 2^117), so that products with codes
-      // (n 2^-133) are normal numbers; in two factors, for 2^sh may pass fp32's range
+      // the row's largest query goes to [2^120, 2^121), so that products with codes
+      // (n 2^-133) are normal numbers and the factor below is small; in two factors,
+      // for 2^sh may pass fp32's range
       int sh = 120;
-      if (top > 0.0f && top <= 3.4e38f) sh = 116 - ilogbf(top);
+      if (top > 0.0f && top <= 3.4e38f) sh = 120 - ilogbf(top);
       const float fa = ldexpf(1.0f, sh / 2), fb = ldexpf(1.0f, sh - sh / 2);
 #pragma unroll
       for (int c = 0; c < C; ++c)
@@ -790,14 +791,15 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
         }
 #pragma unroll
         for (int c = 0; c < C; ++c) {
+          // 2^18 / |inv| in two factors, 2^12 and 2^6 / |inv|: it may pass fp32's range
+          // where the value does not
           const float2 iv = split(inv[nt][c / A::CG]);
-          const float top = 0.015625f * largest_beside(e ? iv.y : iv.x);
-          const float f = 262144.0f * top;  // 2^18
-          const int ch = 32 * c + 4 * g;
           const float base = e ? vm2[c / A::CG].y : vm2[c / A::CG].x;
-          *reinterpret_cast<float4*>(so + (gwarp * RP + r) * D + ch) = make_float4(
-              fmaf(o[c][0][nt][e], f, base), fmaf(o[c][1][nt][e], f, base),
-              fmaf(o[c][0][nt][e + 2], f, base), fmaf(o[c][1][nt][e + 2], f, base));
+          const float top = largest_beside(e ? iv.y : iv.x);
+          auto value = [&](float sum) { return fmaf(sum * 4096.0f, top, base); };
+          *reinterpret_cast<float4*>(so + (gwarp * RP + r) * D + 32 * c + 4 * g) =
+              make_float4(value(o[c][0][nt][e]), value(o[c][1][nt][e]), value(o[c][0][nt][e + 2]),
+                          value(o[c][1][nt][e + 2]));
         }
       }
     }

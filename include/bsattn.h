@@ -566,9 +566,11 @@ bsattn_status bsattn_kv4_select(const bsattn_kv4_cache* cache, const void* q, in
  * A query that sees none gets O = 0, LSE = -inf.
  *   q          device bf16 [B][H][T][head_dim], 16-byte aligned, entries below 2^100
  *              in magnitude (one that is not finite spoils its own query only);
- *              query head h reads
- *              key/value head h / (H / kv_heads); (H / kv_heads) * T <= 128; B <= 4096;
- *              columns * page_size at most 2^31 - 128.
+ *              query head h reads key/value head h / (H / kv_heads);
+ *              (H / kv_heads) * T <= 128; B <= 4096; columns * page_size at most
+ *              2^31 - 128.
+ *   cache      sums are 32-bit ones: values below 2^104 in magnitude (2^23 tokens of them
+ *              can be added up), |scale| sum |q k| of a query and a key below 2^112.
  *   lengths    cached tokens, the T new ones included.
  *   selected   device int32 [B][kv_heads][n_selected], strictly ascending pages, then
  *              negative entries (as bsattn_kv4_select writes it), or null with

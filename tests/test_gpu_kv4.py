@@ -799,3 +799,33 @@ def test_attn_small_queries_beside_a_large_one(bs, case):
     s = q.double().sum(-1) * 9 * D ** -0.5
     assert float((lse - s).abs().max()) <= D ** -0.5 * (
         (D + 8) * U32 * 15 * float(q[0, 0].double().sum()) + 17 * 2.0 ** -18)
+
+
+@pytest.mark.parametrize("power", [101, 109, 116])
+@pytest.mark.parametrize("case", WEIGHTED, ids=str)
+def test_attn_large_values(bs, case, power):
+    """Values up to the documented 2^104, and beyond where their sums still fit 32 bits."""
+    w = _Weighted(bs, case)
+    w.cache.v_scales.mul_(2.0 ** power)
+    w.check(bs)
+
+
+@pytest.mark.parametrize("case", WEIGHTED[:3], ids=str)
+def test_attn_large_scores(bs, case):
+    """Products of queries and keys up to the documented 2^112, one key a little above the others."""
+    w = _Weighted(bs, case)
+    D, s = w.cache.head_dim, w.cache.head_dim ** -0.5
+    w.q.fill_(2.0 ** 99)
+    w.cache.k_scales[..., 0] = 2.0
+    w.cache.k_scales[..., 1] = 0.0
+    for at in w.places(lambda n: n // 2, lambda n: n // 2 + 1):
+        w.cache.k_codes[at[0], :, at[1]] = 0xFF
+    w.cache.k_codes[w.cache.k_codes != 0xFF] = 0xEE
+    at, o, lse = w.call(bs)
+    for b, n in enumerate(w.lengths):
+        pos = n // 2
+        pg, place, group = int(w.table[b, pos // w.cache.page_size]), pos % w.cache.page_size, w.cache.group
+        v = ref.values(w.cache.v_codes[pg, :, place], w.cache.v_scales[pg, :, place])
+        v = v.repeat_interleave(o.shape[1] // v.shape[0], 0)
+        assert float(((o[b, :, 0].double() - v).abs() - 24 * U32 * 15 * w.cache.v_scales[..., 0].max()).max()) <= 0
+        assert float((lse[b, :, 0].double() / (2.0 ** 99 * 30 * D * s) - 1).abs().max()) <= (D + 16) * U32

@@ -99,7 +99,9 @@ constexpr int kSegmentStart = 6;
 // much longer than the others holds the call up by no more.
 constexpr int kMostGroupSteps = 64;
 constexpr int kMostCluster = 8;  // CTAs, the portable most
-constexpr float kNoMax = -1e30f;               // running maximum before any score
+// Running maximum before any score: no finite score lies below it, and differences
+// of it are 0 or infinite, never NaN.
+constexpr float kNoMax = -3.402823466e38f;
 // Weights are taken beside 2^8 times the largest one so far: later scores may pass
 // the running maximum by that, and no weight is above 1.
 constexpr float kLag = 8.0f;

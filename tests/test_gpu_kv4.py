@@ -829,3 +829,28 @@ def test_attn_large_scores(bs, case):
         v = v.repeat_interleave(o.shape[1] // v.shape[0], 0)
         assert float(((o[b, :, 0].double() - v).abs() - 24 * U32 * 15 * w.cache.v_scales[..., 0].max()).max()) <= 0
         assert float((lse[b, :, 0].double() / (2.0 ** 99 * 30 * D * s) - 1).abs().max()) <= (D + 16) * U32
+
+
+@pytest.mark.parametrize("case", WEIGHTED, ids=str)
+def test_attn_very_negative_scores(bs, case):
+    """Equal scores of some -2^121: every visible token has the same weight, whatever the scores' size.
+
+    The LSE is that score (the logarithm of the count is far below its last bit): D + 16 roundings of
+    equal terms.  The output is a mean: the bound of _Weighted.check with exact scores."""
+    w = _Weighted(bs, case)
+    D, U = w.cache.head_dim, 2.0 ** 60
+    w.q.fill_(U)
+    w.cache.k_scales[..., 0] = 0
+    w.cache.k_scales[..., 1] = -U / 2
+    at, o, lse = w.call(bs)
+    page, T = w.cache.page_size, w.q.shape[2]
+    for b, n in enumerate(w.lengths):
+        pg = w.table[b, :-(-n // page)].long()
+        for t in range(T if n else 0):
+            m = n - T + t + 1
+            v = ref.values(w.cache.v_codes[pg], w.cache.v_scales[pg]).transpose(1, 2).flatten(0, 1)[:m]
+            vs = w.cache.v_scales[pg].double().transpose(1, 2).flatten(0, 1)[:m]
+            size = (15 * vs[..., 0] + vs[..., 1].abs()).amax((0, 2))[:, None]
+            heads = o[b, :, t].unflatten(0, (w.cache.kv_heads, -1)).double()
+            assert bool(((heads - v.mean(0)[:, None]).abs() <= 2 * (2.0 ** -20 + (m + 8) * U32) * size[..., None]).all())
+            assert float((lse[b, :, t].double() / (-U * U / 2 * D ** 0.5) - 1).abs().max()) <= (D + 16) * U32

@@ -260,9 +260,12 @@ __global__ void __launch_bounds__(32 * kBwdWarps, kBwdPerSm) rope_bwd_kernel(con
     const float* d = up + (((int64_t)b * heads + h0) * p.S + s) * D + c0;
     uint4 raw[U];
     float4 dy[U][2];
+    constexpr uint32_t kOnes = 0x3F803F80u;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      raw[u] = make_uint4(0, 0, 0, 0);
+      // behind the last head: dy = 0 and x = 1, so that r is finite with eps = 0 too and
+      // the row adds 0 to the weights' gradient
+      raw[u] = make_uint4(kOnes, kOnes, kOnes, kOnes);
       dy[u][0] = dy[u][1] = make_float4(0, 0, 0, 0);
       if (h0 + u * R < c.end) {
         dy[u][0] = load(reinterpret_cast<const float4*>(d + u * next));

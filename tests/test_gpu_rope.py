@@ -236,3 +236,21 @@ def test_refusals(bs):
         bs.rope_table(10, 24)
     with pytest.raises(bs.BsattnError):
         bs.qk_norm_rope(x, 2, 2, w, w, eps=float("nan"))
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-30, 0.01])
+@pytest.mark.parametrize("H, Hkv, D", [(32, 4, 128), (16, 4, 64), (5, 5, 128), (5, 1, 64), (1, 1, 64), (3, 3, 128)], ids=str)
+def test_other_eps(bs, H, Hkv, D, eps):
+    """eps from zero on, with numbers of heads that leave a warp's rows empty."""
+    B, S = 2, 37
+    x, w, _ = _inputs(B, S, H, Hkv, D, torch.float32, False, 0)
+    g = ref.gen(7)
+    dq, dk, dv = (torch.randn(B, h, S, D, generator=g, device="cuda") for h in (H, Hkv, Hkv))
+    q, k, _ = bs.qk_norm_rope(x, H, Hkv, *w, eps=eps)
+    dx, dwq, dwk = bs.qk_norm_rope_bwd(x, dq, dk, dv, *w, eps=eps)
+    for lo, hi, y, d, wt, dw in ((0, H, q, dq, w[0], dwq), (H, H + Hkv, k, dk, w[1], dwk)):
+        want, size = ref.norm_rope(x[:, :, lo:hi], wt, eps, None)
+        _close(y, want.transpose(1, 2), (UBF * want.abs() + 24 * U32 * size).transpose(1, 2), eps)
+        want, want_w, size, size_w = ref.norm_rope_bwd(x[:, :, lo:hi], d.transpose(1, 2), wt, eps, None)
+        _close(dx[:, :, lo:hi], want, UBF * want.abs() + 48 * U32 * size, eps)
+        _close(dw, want_w, (B * S * (hi - lo) + 48) * U32 * size_w, eps)

@@ -48,6 +48,15 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
   return *reinterpret_cast<uint32_t*>(&r);
 }
 
+// A pair with its magnitudes brought up to `least`; zeros stay.
+__device__ __forceinline__ uint32_t at_least(uint32_t a, __nv_bfloat162 least) {
+  const __nv_bfloat162 v = *reinterpret_cast<__nv_bfloat162*>(&a);
+  const __nv_bfloat162 m = __hmax2(__habs2(v), least);
+  const uint32_t up = *reinterpret_cast<const uint32_t*>(&m) | (a & 0x80008000u);
+  const unsigned there = __hne2_mask(v, __float2bfloat162_rn(0.0f));
+  return (a & ~there) | (up & there);
+}
+
 // Sixteen channels of one group's row -> codes (a nibble each, the first
 // lowest; n[i]: channels 2i, 2i + 1 as floats), and the group's step and least.
 // GL lanes hold a group.
@@ -55,14 +64,19 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
 // d / step, d = x - least, is estimated with the reciprocal and corrected by its
 // exact remainder: q = q0 + (d - q0 step) / step, good to 2^-46 before its one
 // rounding; adding 1.5 2^23 then rounds it half to even with no conversion
-// instruction.  The codes are those of the real quotient: at a border it is
+// instruction.  The codes are those of the real quotient of d: at a border it is
 // k + 1/2 exactly, which 32 bits hold, and next to one d differs from
 // (k + 1/2) step, a number of 13 bits, by a step of d at least, so the quotient
-// by more than its own rounding.  The step's (most - least) / 15 is taken the
-// same way, and is the 32-bit quotient: no a / 15 comes closer to the middle
-// between two floats than 2^-29 of itself.
+// by more than its own rounding.  d itself would be rounded where x and least are
+// more than 2^16 apart, which matters at a border: d = (k + 1/2) step would stand
+// for numbers on both sides of it.  Either least is the small one, or x is and
+// -least lies on the border; the small one then counts as 2^-15 of the other, of
+// its own sign: d is exact, on its side of the border, and as far from others
+// (2^-12 of the range at least) as before.  The step's (most - least) / 15 is
+// taken the same way, and is the 32-bit quotient: no a / 15 comes closer to the
+// middle between two floats than 2^-29 of itself.
 template <int GL>
-__device__ __forceinline__ uint2 quantise(const uint32_t (&w)[8], F2 (&n)[8], float& step,
+__device__ __forceinline__ uint2 quantise(uint32_t (&w)[8], F2 (&n)[8], float& step,
                                           float& least) {
   uint32_t lo = w[0], hi = w[0];
 #pragma unroll
@@ -81,7 +95,16 @@ __device__ __forceinline__ uint2 quantise(const uint32_t (&w)[8], F2 (&n)[8], fl
   const bool finite = range <= 3.4028234e38f, flat = step < kLeastStep;
   float inv;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(step));
-  const F2 vinv = f2(inv), vstep = f2(-step), vleast = f2(-least);
+  constexpr float kFar = 3.0517578125e-5f;  // 2^-15
+  float from = least;
+  if (least != 0.0f && fabsf(least) < kFar * range)
+    from = copysignf(kFar * __uint_as_float(__float_as_uint(range) & 0x7F800000u), least);
+  if (least != 0.0f && fmaf(rintf(-2.0f * least * inv), step, 2.0f * least) == 0.0f) {
+    const __nv_bfloat162 far = __float2bfloat162_rn(kFar * fabsf(least));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = at_least(w[i], far);
+  }
+  const F2 vinv = f2(inv), vstep = f2(-step), vleast = f2(-from);
   const F2 magic = f2(12582912.0f), unmagic = f2(-12582912.0f);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -150,7 +173,7 @@ __device__ __forceinline__ void append_rows(const AppendParams& p, int b, int le
     hi = load(reinterpret_cast<const uint4*>(src) + 2 * cl + 1);
     pg = page_at(p.c, p.table + b * p.table_stride, p.columns, ((int64_t)len + t) >> p.c.log_page);
   }
-  const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
   F2 x[8];
   float step, least;
   const uint2 packed = quantise<GL>(w, x, step, least);  // (every lane: shuffles)
@@ -229,7 +252,7 @@ __global__ void __launch_bounds__(kRowThreads, 6) kv4_append_kernel(const Append
       reinterpret_cast<uint32_t*>(is_k ? p.c.k_scales : p.c.v_scales) + row * NG + cl / GL;
   for (int i = 0; i < rounds; ++i) {  // (as many for every lane: shuffles)
     const bool there = i * kRows + sub < n;
-    const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
     src += kRows * token;
     if ((i + 1) * kRows + sub < n) {
       lo = load(reinterpret_cast<const uint4*>(src));

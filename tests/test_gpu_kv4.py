@@ -854,3 +854,31 @@ def test_attn_very_negative_scores(bs, case):
             heads = o[b, :, t].unflatten(0, (w.cache.kv_heads, -1)).double()
             assert bool(((heads - v.mean(0)[:, None]).abs() <= 2 * (2.0 ** -20 + (m + 8) * U32) * size[..., None]).all())
             assert float((lse[b, :, t].double() / (-U * U / 2 * D ** 0.5) - 1).abs().max()) <= (D + 16) * U32
+
+
+@pytest.mark.parametrize("T", [16, 5])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_append_values_of_far_sizes(bs, group, T):
+    """Differences x - least that 32 bits round, on borders between two codes: tiny x of both signs
+    beside a least value of -(k + 1/2) steps, and x of k + 1/2 steps beside a tiny least value."""
+    D = 128
+    tiny = 2.0 ** -torch.arange(15, 39, device="cuda").float()
+    x = torch.zeros(1, 4, 16, D, device="cuda")
+    x[..., :24], x[..., 32:56], x[..., 64:88], x[..., 96:120] = tiny, -tiny, tiny * 1.5, -tiny * 1.25
+    border = torch.arange(16, device="cuda") * 0.25 + 0.125
+    steps = torch.cat([border[:15], border.new_tensor([3.75])])
+    for g in range(0, D, 32):
+        x[0, 0, :, g + 24], x[0, 0, :, g + 25] = -border, 3.75 - border          # step 1/4
+        x[0, 1, :, g + 24], x[0, 1, :, g + 25] = -border * 3, (3.75 - border) * 3
+        x[0, 2, :, g + 8:g + 24] = steps
+        x[0, 2, :, g + 24], x[0, 2, :, g:g + 8] = -tiny[4:20], 0                  # the least: tiny, below 0
+        x[0, 3, :, g + 8:g + 24] = steps
+        x[0, 3, :, g:g + 8], x[0, 3, :, g + 24:g + 32] = tiny[4:20, None], tiny[4:20, None]  # above 0
+    x = x.bfloat16()[:, :, :T].contiguous()
+    for k, v in ((x, -x), (-x, x)):
+        cache = bs.Kv4Cache(2, 4, D, page_size=16, group=group)
+        before = _state(cache)
+        bs.kv4_append(cache, k, v, _i32([[1]]), _i32([0]))
+        want = _append_ref(cache, before, k, v, _i32([[1]]), [0], [T])
+        for got, w in zip(_state(cache), want):
+            assert torch.equal(got, w), int((got != w).sum())

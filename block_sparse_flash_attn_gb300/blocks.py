@@ -61,11 +61,12 @@ def select_blocks(q: torch.Tensor, k: torch.Tensor, keep: int, causal: bool = Fa
     flags = (_bs.CAUSAL if causal else 0) | (_bs.KEY_BLOCK_64 if key_block == 64 else 0)
     with launch_on(q.device, stream) as on:
         out = output("out", out, torch.uint8, (B, H, nb, nk), q.device)
-        lib = _bs.load()
-        nbytes = _workspace(B, H, Hkv, S, D, flags)
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-        _bs._check(lib.bsattn_select_blocks(
-            q.data_ptr(), k.data_ptr(), B, H, Hkv, S, D, keep, sink, local, flags, pointer(allow),
-            allow_heads, out.data_ptr(), ws.data_ptr(), nbytes, on),
-            "bsattn_select_blocks")
+        if B * H:
+            lib = _bs.load()
+            nbytes = _workspace(B, H, Hkv, S, D, flags)
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+            _bs._check(lib.bsattn_select_blocks(
+                q.data_ptr(), k.data_ptr(), B, H, Hkv, S, D, keep, sink, local, flags,
+                pointer(allow), allow_heads, out.data_ptr(), ws.data_ptr(), nbytes, on),
+                "bsattn_select_blocks")
     return out

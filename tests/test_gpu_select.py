@@ -136,3 +136,15 @@ def test_given_output_and_refusals(bs):
         bs.select_blocks(q, k, 1, allow=torch.ones(1, 1, 2, 2, device="cuda"))
     with pytest.raises(TypeError):
         bs.select_blocks(q.float(), k.float(), 1)
+
+
+@pytest.mark.parametrize("key_block", [128, 64])
+def test_empty_batch(bs, key_block):
+    """No batch entries: an empty mask, as the operators around it give empty results."""
+    q, k = (torch.zeros(0, h, 256, 64, dtype=torch.bfloat16, device="cuda") for h in (4, 2))
+    mask = bs.select_blocks(q, k, 1, key_block=key_block)
+    assert mask.shape == (0, 4, 2, 256 // key_block) and mask.dtype == torch.uint8
+    allow = torch.zeros(0, 1, 2, 256 // key_block, dtype=torch.uint8, device="cuda")
+    assert bs.select_blocks(q, k, 1, key_block=key_block, allow=allow, out=mask) is mask
+    with pytest.raises(ValueError, match="keep"):
+        bs.select_blocks(q, k, 0)

@@ -944,10 +944,15 @@ bsattn_status bsattn_kv4_status(const bsattn_kv4_cache* cache, void* stream) {
   int word = 0;
   if (cudaMemcpyAsync(&word, view.status, sizeof(word), cudaMemcpyDeviceToHost, st) !=
           cudaSuccess ||
-      cudaMemsetAsync(view.status, 0, sizeof(word), st) != cudaSuccess ||
       cudaStreamSynchronize(st) != cudaSuccess)
     return BSATTN_ERR_CUDA;
-  return (word & kStatusPage) ? BSATTN_ERR_PAGE : BSATTN_OK;
+  if (!(word & kStatusPage)) return BSATTN_OK;
+  // (cleared only after a report was seen: one that another stream makes in between is
+  // in this answer, and none is lost)
+  if (cudaMemsetAsync(view.status, 0, sizeof(word), st) != cudaSuccess ||
+      cudaStreamSynchronize(st) != cudaSuccess)
+    return BSATTN_ERR_CUDA;
+  return BSATTN_ERR_PAGE;
 }
 
 }  // extern "C"

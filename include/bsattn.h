@@ -591,7 +591,8 @@ bsattn_status bsattn_kv4_attn(const bsattn_kv4_cache* cache, const void* q, int 
                               size_t workspace_bytes, void* stream);
 
 /* Wait for `stream`, then report and clear the cache's status word: OK or PAGE
-   (CUDA if the wait failed). */
+   (CUDA if the wait failed).  What calls on other streams report meanwhile is in
+   this answer or in the next one's. */
 bsattn_status bsattn_kv4_status(const bsattn_kv4_cache* cache, void* stream);
 
 #ifdef __cplusplus

@@ -882,3 +882,26 @@ def test_append_values_of_far_sizes(bs, group, T):
         want = _append_ref(cache, before, k, v, _i32([[1]]), [0], [T])
         for got, w in zip(_state(cache), want):
             assert torch.equal(got, w), int((got != w).sum())
+
+
+def test_report_while_the_status_is_asked(bs):
+    """A call on another stream that reports at any time around a check is in that check's answer
+    or in the next one's."""
+    cache, table, q, n = _attn_case(bs, (1, 4, 64, 16, 64, 1, [100]))
+    broken, other = torch.full_like(table, -1), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for i in range(1500):
+        with torch.cuda.stream(other):
+            torch.cuda._sleep(30000 + i % 500 * 400)  # some 15 to 115 us, the check a few after the call
+            bs.kv4_attn(cache, q, broken, n)
+        answers = []
+        for wait in (False, True):
+            if wait:
+                other.synchronize()
+            try:
+                bs.kv4_status(cache)
+                answers.append(bs.OK)
+            except bs.BsattnError as e:
+                answers.append(e.status)
+        assert bs.ERR_PAGE in answers, i
+    bs.kv4_status(cache)

@@ -238,9 +238,12 @@ __device__ __forceinline__ int tile_page(const AttnParams& p, int b, int h, int6
     const int64_t e = logical;
     logical = load(sel + e);
     if (logical < 0) return -1;
-    if (e > 0 && logical <= load(sel + e - 1)) {  // a page named twice, or out of order
-      p.c.report();
-      return -1;
+    if (e > 0) {  // a page named twice, out of order or behind a negative entry
+      const int64_t before = load(sel + e - 1);
+      if (before < 0 || logical <= before) {
+        p.c.report();
+        return -1;
+      }
     }
   }
   const int64_t first = (logical << p.c.log_page) + place;

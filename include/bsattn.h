@@ -574,8 +574,9 @@ bsattn_status bsattn_kv4_select(const bsattn_kv4_cache* cache, const void* q, in
  *   lengths    cached tokens, the T new ones included.
  *   selected   device int32 [B][kv_heads][n_selected], strictly ascending pages, then
  *              negative entries (as bsattn_kv4_select writes it), or null with
- *              n_selected 0.  A page not above the one before it is skipped and
- *              reported; pages behind the length are skipped.
+ *              n_selected 0.  A page not above the entry before it, or directly behind
+ *              a negative one, is skipped and reported; pages behind the length
+ *              are skipped.
  *   scale      finite; multiplies q.k.
  *   flags      BSATTN_OUT_F32.
  *   out        device bf16 (fp32) [B][H][T][head_dim];  lse  device fp32 [B][H][T].

@@ -905,3 +905,22 @@ def test_report_while_the_status_is_asked(bs):
                 answers.append(e.status)
         assert bs.ERR_PAGE in answers, i
     bs.kv4_status(cache)
+
+
+@pytest.mark.parametrize("lengths", [[100], [100, 40, 9] * 120], ids=["clusters", "groups"])
+def test_pages_behind_a_negative_entry(bs, lengths):
+    """A page directly behind a negative entry is skipped and reported, and so not counted twice."""
+    cache, table, q, n = _attn_case(bs, (1, 4, 64, 16, 64, 1, lengths))
+    B = len(lengths)
+
+    def call(pages):
+        return bs.kv4_attn(cache, q, table, n, _i32(pages).expand(B, 1, -1).contiguous(), out_f32=True)
+
+    for pages, same in (([1, -1, 1], [1, -1, -1]), ([0, -1, 2], [0, -1, -1]), ([0, 2, -5, 0], [0, 2, -1, -1]),
+                        ([-1, 1], [-1, -1])):
+        want = call(same)
+        bs.kv4_status(cache)
+        got = call(pages)
+        with pytest.raises(bs.BsattnError, match="page"):
+            bs.kv4_status(cache)
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), pages

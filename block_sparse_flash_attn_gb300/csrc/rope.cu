@@ -452,6 +452,33 @@ bsattn_status check_rope(const void* x, int64_t xb, int64_t xs, int B, int S, in
   return BSATTN_OK;
 }
 
+// Whether B x S rows of `row` elements at x and at dx share memory, other than each
+// row with its own: dx may be x itself.
+bool rows_overlap(const void* x, int64_t xb, int64_t xs, const void* dx, int64_t dxb, int64_t dxs,
+                  int B, int S, int64_t row) {
+  if (B == 1) xb = dxb = 0;
+  if (S == 1) xs = dxs = 0;
+  const int64_t apart =
+      static_cast<int64_t>(reinterpret_cast<intptr_t>(dx) - reinterpret_cast<intptr_t>(x)) / 2;
+  const bool same = xb == dxb && xs == dxs;
+  if (apart == 0 && same) return false;
+  const int64_t x_end = (B - 1) * xb + (S - 1) * xs + row;
+  const int64_t dx_end = apart + (B - 1) * dxb + (S - 1) * dxs + row;
+  if (apart >= x_end || dx_end <= 0) return false;
+  if (!same) return true;
+  // the same strides, one between the other's rows: the distance of a row of dx to the
+  // nearest row of x in each other batch entry
+  for (int64_t b = 1 - B; b < B; ++b) {
+    const int64_t from = apart + b * xb;
+    const int64_t near = xs ? -from / xs : 0;
+    for (int64_t t = near - 1; t <= near + 1; ++t) {
+      const int64_t off = from + t * xs;
+      if (t > -S && t < S && off > -row && off < row) return true;
+    }
+  }
+  return false;
+}
+
 RopeParams rope_params(const void* x, int64_t xb, int64_t xs, int B, int S, int H, int Hkv,
                        const void* wq, const void* wk, unsigned flags, const float* table,
                        int n_pos, int rotary_dim, const int32_t* pos, float eps) {
@@ -566,6 +593,10 @@ bsattn_status bsattn_qk_norm_rope_bwd(const void* x, int64_t x_batch_stride, int
   const int64_t row = (int64_t)(H + 2 * Hkv) * D;  // rows of dx must not overlap
   if (!multiple8(dx_batch_stride) || !multiple8(dx_token_stride) || dx_token_stride < row ||
       dx_batch_stride < 0 || (B > 1 && dx_batch_stride < (S - 1) * dx_token_stride + row))
+    return BSATTN_ERR_INVALID_ARG;
+  // (x is read with weights only)
+  if (q_weight && rows_overlap(x, x_batch_stride, x_token_stride, dx, dx_batch_stride,
+                               dx_token_stride, B, S, row))
     return BSATTN_ERR_INVALID_ARG;
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) return BSATTN_ERR_CUDA;

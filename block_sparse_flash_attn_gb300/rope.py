@@ -130,7 +130,8 @@ def qk_norm_rope_bwd(x: torch.Tensor, dq: torch.Tensor, dk: torch.Tensor, dv: to
     """dx (bf16, like x), dq_weight, dk_weight (fp32 [D]; None without weights):
     the gradient of qk_norm_rope, from dq [B, H, S, D], dk, dv [B, Hkv, S, D]
     (CUDA fp32, as bwd returns them) and the forward call's other arguments.
-    Repeated calls give the same bits."""
+    dx may be x itself, but must not overlap it otherwise.  Repeated calls give the
+    same bits."""
     for name, t in (("dq", dq), ("dk", dk)):
         if not isinstance(t, torch.Tensor) or t.dtype != _F32:
             raise TypeError(f"{name} must be a tensor of {_F32}")

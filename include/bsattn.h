@@ -431,7 +431,9 @@ bsattn_status bsattn_qk_norm_rope(const void* x, int64_t x_batch_stride, int64_t
  *   dq, dk, dv device fp32 [B][H][S][D], [B][Hkv][S][D] twice (as bsattn_bwd_gqa
  *              writes them), 16-byte aligned.
  *   dx         device bf16, shaped like x, with strides of its own (multiples of 8;
- *              tokens must not overlap); may be x itself.
+ *              tokens must not overlap); may be x itself.  With weights it is refused
+ *              if it overlaps x in any other way (lying between x's rows needs the
+ *              same strides).
  *   dq_weight, dk_weight  device fp32 [D], written in full; ignored without weights.
  *   workspace  bsattn_qk_norm_rope_bwd_workspace bytes, 16-byte aligned; ignored
  *              without weights.

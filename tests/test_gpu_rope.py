@@ -254,3 +254,37 @@ def test_other_eps(bs, H, Hkv, D, eps):
         want, want_w, size, size_w = ref.norm_rope_bwd(x[:, :, lo:hi], d.transpose(1, 2), wt, eps, None)
         _close(dx[:, :, lo:hi], want, UBF * want.abs() + 48 * U32 * size, eps)
         _close(dw, want_w, (B * S * (hi - lo) + 48) * U32 * size_w, eps)
+
+
+def test_gradient_between_the_rows_of_its_input(bs):
+    """dx beside x in one buffer, row by row: allowed where the rows lie apart, refused elsewhere."""
+    B, S, H, Hkv, D = 3, 50, 4, 2, 64
+    row = (H + 2 * Hkv) * D
+    x, w, _ = _inputs(B, S, H, Hkv, D, torch.float32, False, 0)
+    g = ref.gen(7)
+    grads = [torch.randn(B, h, S, D, generator=g, device="cuda") for h in (H, Hkv, Hkv)]
+    want = bs.qk_norm_rope_bwd(x, *grads, *w)
+    lib, on = bs.load(), torch.cuda.current_stream().cuda_stream
+    ws = torch.empty(lib.bsattn_qk_norm_rope_bwd_workspace(B, S, H, Hkv, D), dtype=torch.uint8, device="cuda")
+    dw = torch.empty(2, D, device="cuda")
+    both = torch.zeros(B, S, 2, row, dtype=torch.bfloat16, device="cuda")
+    both[:, :, 0] = x.flatten(2)
+
+    def call(dx):
+        t = both.data_ptr()
+        return lib.bsattn_qk_norm_rope_bwd(
+            t, 2 * S * row, 2 * row, *(d.data_ptr() for d in grads), B, S, H, Hkv, D, *(v.data_ptr() for v in w), None,
+            0, 0, None, 1e-6, bs_weight_f32, t + 2 * dx, 2 * S * row, 2 * row, dw[0].data_ptr(), dw[1].data_ptr(),
+            ws.data_ptr(), ws.numel(), on)
+
+    from block_sparse_flash_attn_gb300.rope import WEIGHT_F32 as bs_weight_f32
+    assert call(row) == bs.OK
+    assert torch.equal(both[:, :, 1].view_as(x), want[0]) and torch.equal(both[:, :, 0].view_as(x), x)
+    assert torch.equal(dw[0], want[1]) and torch.equal(dw[1], want[2])
+    for near in (8, row - 8, row + 8):
+        assert call(near) == bs.ERR_INVALID_ARG
+    flat = torch.empty(x.numel() + 8, dtype=torch.bfloat16, device="cuda")
+    flat[:-8] = x.flatten()
+    with pytest.raises(bs.BsattnError, match="invalid argument"):
+        bs.qk_norm_rope_bwd(flat[:-8].view_as(x), *grads, *w, dx=flat[8:].view_as(x))
+    assert torch.equal(bs.qk_norm_rope_bwd(flat[:-8].view_as(x), *grads, *w, dx=flat[:-8].view_as(x))[0], want[0])

@@ -165,3 +165,22 @@ def test_wrappers_check_before_the_library(bs, monkeypatch):
         bs.Kv4Cache(1, 1, 64, device="cpu")
     with pytest.raises(ValueError, match="multiple of 16"):
         bs.rope_table(4, 24)
+
+
+BASE = 0x100000
+OVERLAPS = [  # dx's distance in elements, B, S, strides of x, strides of dx (rows of 512 elements)
+    (8, 1, 4, (2048, 512), (2048, 512)), (-8, 1, 4, (2048, 512), (2048, 512)), (512, 1, 4, (2048, 512), (2048, 512)),
+    (2040, 1, 4, (2048, 512), (2048, 512)), (-2040, 1, 4, (2048, 512), (2048, 512)),
+    (0, 1, 4, (0, 512), (0, 1024)), (0, 1, 4, (0, 0), (0, 512)), (0, 3, 4, (0, 512), (2048, 512)),  # x broadcast
+    (504, 1, 4, (0, 1024), (0, 1024)), (1032, 1, 4, (0, 1024), (0, 1024)),  # between the rows, but too near
+    (1024, 2, 2, (1544, 1024), (1544, 1024)), (1560, 2, 2, (1536, 512), (1536, 512)), (8, 1, 1, (0, 0), (0, 512))]
+
+
+@pytest.mark.parametrize("case", OVERLAPS, ids=str)
+def test_gradient_over_its_input(bs, case):
+    """dx that overlaps x without being x itself: rows would be read after they were overwritten."""
+    apart, B, S, (xb, xs), (dxb, dxs) = case
+    dxb = max(dxb, (S - 1) * dxs + 512)
+    args = [vp(BASE), xb, xs, FAKE, FAKE, FAKE, B, S, 4, 2, 64, FAKE, FAKE, None, 0, 0, None, 1e-6, 0,
+            vp(BASE + 2 * apart), dxb, dxs, FAKE, FAKE, FAKE, 1 << 30, None]
+    assert bs.load().bsattn_qk_norm_rope_bwd(*args) == bs.ERR_INVALID_ARG

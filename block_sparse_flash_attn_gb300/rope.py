@@ -145,6 +145,7 @@ def qk_norm_rope_bwd(x: torch.Tensor, dq: torch.Tensor, dk: torch.Tensor, dv: to
     with launch_on(x.device, stream) as on:
         dx = output("dx", dx, _BF16, x.shape, x.device)
         dwq = dwk = ws = None
+        row = x.shape[2] * D  # dx is contiguous (the strides of its axes of one entry may be anything)
         lib = _bs.load()
         if q_weight is not None:
             dwq = torch.empty(D, dtype=_F32, device=x.device)
@@ -160,6 +161,6 @@ def qk_norm_rope_bwd(x: torch.Tensor, dq: torch.Tensor, dk: torch.Tensor, dv: to
                 x.data_ptr(), sb, ss, dq.data_ptr(), dk.data_ptr(),
                 dv.data_ptr(), B, S, heads, kv_heads, D, pointer(q_weight), pointer(k_weight),
                 pointer(table), n_pos, rotary, pointer(positions), float(eps), flags,
-                dx.data_ptr(), dx.stride(0), dx.stride(1), pointer(dwq), pointer(dwk),
+                dx.data_ptr(), S * row, row, pointer(dwq), pointer(dwk),
                 pointer(ws), nbytes, on), "bsattn_qk_norm_rope_bwd")
     return dx, dwq, dwk

@@ -288,3 +288,18 @@ def test_gradient_between_the_rows_of_its_input(bs):
     with pytest.raises(bs.BsattnError, match="invalid argument"):
         bs.qk_norm_rope_bwd(flat[:-8].view_as(x), *grads, *w, dx=flat[8:].view_as(x))
     assert torch.equal(bs.qk_norm_rope_bwd(flat[:-8].view_as(x), *grads, *w, dx=flat[:-8].view_as(x))[0], want[0])
+
+
+@pytest.mark.parametrize("B, S", [(1, 3), (3, 1), (1, 1)], ids=str)
+def test_given_dx_with_any_stride_along_one_entry(bs, B, S):
+    """A contiguous dx; the stride of an axis of one entry means nothing."""
+    x, w, _ = _inputs(B, S, 2, 2, 64, torch.float32, False, 0)
+    dy = [torch.randn(B, 2, S, 64, generator=ref.gen(2), device="cuda") for _ in range(3)]
+    want = bs.qk_norm_rope_bwd(x, *dy, *w)
+    dx = torch.empty(B * S * 384, dtype=torch.bfloat16, device="cuda")
+    dx = dx.as_strided((B, S, 6, 64), (384 * S if B > 1 else 3, 384 if S > 1 else 5, 64, 1))
+    assert dx.is_contiguous()
+    got = bs.qk_norm_rope_bwd(x, *dy, *w, dx=dx)
+    assert got[0] is dx and all(torch.equal(a, b) for a, b in zip(got, want))
+    own = x.clone().as_strided(x.shape, dx.stride())
+    assert torch.equal(bs.qk_norm_rope_bwd(own, *dy, *w, dx=own)[0], want[0])

@@ -58,9 +58,9 @@
 // All join in a fixed order: results repeat bit for bit.
 //
 // Measured: 32 sequences of 32768 to 65536 tokens, 8 heads of 128, 4 query heads
-// each: 318 us, 5.4 TB/s, 81% of a plain copy's rate, and the same when all pages
-// lie in L2: what is left is instructions (58% of issue slots, half of them
-// masks and shifts of codes), not bandwidth.  CUDA-core products on decoded
+// each: 311 us, 5.5 TB/s, 82% of a plain copy's rate, and 303 of 306 us when all pages
+// lie in L2: what is left is instructions (59% of issue slots, the integer pipe,
+// masks and shifts of codes, 58%), not bandwidth.  CUDA-core products on decoded
 // values: 10 ms.  One sequence of 777 tokens: 8 us, launch and five loads in a
 // row.
 #include <cmath>
@@ -173,7 +173,7 @@ __device__ __forceinline__ float2 unpack_half(uint32_t x) {
 
 // Of a pair of tokens' codes in bits 6-9 and 22-25 the even token's code and the
 // odd one's complement.  One instruction, if one of its two constants comes from a
-// register: the long contexts above 332 us (by twos), with two instructions 372,
+// register: the long contexts below 332 us (by twos), with two instructions 372,
 // with the loaded words turned over first 338.
 __device__ __forceinline__ uint32_t complements(uint32_t x, uint32_t flip) {
   uint32_t y;  // (x ^ flip) & mask
@@ -275,10 +275,12 @@ struct Attn {
   static_assert(RP * (D + 3) * 4 <= kWarpRing, "shared memory");
   static constexpr int kSlot = RP * (D + 2);  // floats of a partial result
   // Tiles a pass of the loop: a turn of the ring, whose places are constants then;
-  // two where registers run out.  32 sequences of 32768 to 65536 tokens, groups of
-  // 128: 318 us, by twos 332, one by one 355; 64 heads of 16 rows and 49152 tokens,
-  // groups of 32: 241 us, by twos 225.
-  static constexpr int kUnroll = NG == 4 && NT == 2 ? 2 : kStages;
+  // fewer where registers run out and code is long.  32 sequences of 32768 to 65536
+  // tokens, groups of 128: 311 us, by twos 332, one by one 355; 64 heads of 16 rows
+  // and 49152 tokens, groups of 32: 241 us, by twos 232; 12 heads of 16 rows over 24
+  // pages of 32 tokens, page choice included: 19 us one by one, by twos 21.
+  template <int MODE>
+  static constexpr int kUnroll = NG < 4 || NT < 2 ? kStages : MODE == kRanges ? 2 : 1;
 
   // pieces of a row are stored permuted by its token, so that the 32-bit reads
   // of both products meet 32 banks
@@ -292,6 +294,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
     kv4_attn_kernel(const AttnParams p) {
   using A = Attn<D, NG, NT, TWICE>;
   constexpr int C = A::C, RB = A::RB, RP = A::RP, KW = A::CG;
+  constexpr int kUnroll = A::template kUnroll<MODE>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int warp_sums[kAttnWarps];
   constexpr int kMostGroups = MODE == kGroups ? kAttnWarps : 1;
@@ -542,7 +545,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
     uint32_t from = 0;  // the ring's place of the tile
     uint32_t flip;      // the odd tokens' halves (kept in a register: see complements)
     asm volatile("mov.b32 %0, 0xFFFF0000;" : "=r"(flip));
-#pragma unroll A::kUnroll
+#pragma unroll kUnroll
     for (int i = 0; i < n_tiles; ++i) {
       copy_wait<kStages - 2>();
       __syncwarp();
@@ -651,8 +654,10 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
           }
         return most > 1.0f || (most16 & 0xFFFFu) > kMostWeight || (most16 >> 16) > kMostWeight;
       };
-      // ---- rare: a score far above the running maximum, or p step of its own scale
-      if (__any_sync(0xFFFFFFFFu, weigh())) {
+      // ---- rare: a score far above the running maximum, or p step of another scale;
+      // then once more with the scales that hold them (one copy of the code)
+#pragma unroll 1
+      for (bool again = false; __any_sync(0xFFFFFFFFu, weigh()) && !again; again = true) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const float2 a = split(s[nt][0]), c = split(s[nt][1]), old = split(mx[nt]);
@@ -697,7 +702,6 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
               }
           }
         }
-        weigh();
       }
       // ---- hi + lo, turned to the operand layout
       uint32_t wl[NG][NT][2];

@@ -655,7 +655,8 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
         return most > 1.0f || (most16 & 0xFFFFu) > kMostWeight || (most16 >> 16) > kMostWeight;
       };
       // ---- rare: a score far above the running maximum, or p step of another scale;
-      // then once more with the scales that hold them (one copy of the code)
+      // then once more with the scales that hold them (one copy of the code).  A row
+      // that has neither stays as it is, whatever the others have.
 #pragma unroll 1
       for (bool again = false; __any_sync(0xFFFFFFFFu, weigh()) && !again; again = true) {
 #pragma unroll
@@ -667,7 +668,8 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
 #pragma unroll
             for (int sft = 4; sft < 32; sft <<= 1)
               top[e] = fmaxf(top[e], __shfl_xor_sync(0xFFFFFFFFu, top[e], sft));
-            top[e] = fmaxf(top[e] + kLag, e ? -old.y : -old.x);
+            const float reference = e ? -old.y : -old.x;
+            top[e] = top[e] > reference ? top[e] + kLag : reference;
           }
           const F2 f = f2(exp2_fast(-old.x - top[0]), exp2_fast(-old.y - top[1]));
           mx[nt] = f2(-top[0], -top[1]);
@@ -686,8 +688,10 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
 #pragma unroll
               for (int sft = 4; sft < 32; sft <<= 1)
                 large[e] = fmaxf(large[e], __shfl_xor_sync(0xFFFFFFFFu, large[e], sft));
-              const float before = (e ? fs.y : fs.x) * largest_beside(e ? was.y : was.x);
-              large[e] = scale_beside(fmaxf(large[e], before));
+              const float fe = e ? fs.y : fs.x, scale = fabsf(e ? was.y : was.x);
+              large[e] = fe == 1.0f && large[e] * scale <= 32768.0f
+                             ? scale
+                             : scale_beside(fmaxf(large[e], fe * largest_beside(scale)));
             }
             inv[nt][n] = f2(sign * large[0], sign * large[1]);
             // f new / old, at most 2 (f new first: new / old alone may overflow)

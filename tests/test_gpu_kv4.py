@@ -924,3 +924,21 @@ def test_pages_behind_a_negative_entry(bs, lengths):
         with pytest.raises(bs.BsattnError, match="page"):
             bs.kv4_status(cache)
         assert all(torch.equal(a, b) for a, b in zip(got, want)), pages
+
+
+@pytest.mark.parametrize("case", [(1, 4, 128, 16, 128, 1, [300]), (1, 2, 64, 16, 32, 3, [9000]), (2, 8, 64, 32, 64, 1, [700, 20]),
+                                  (1, 16, 128, 16, 32, 1, [200])], ids=str)
+def test_attn_rows_do_not_touch_one_another(bs, case):
+    """The bits of a query's result are the same whatever the other queries of its head are: scores
+    that rise far above their running maximum, or that are infinite, rescale their own row only."""
+    cache, table, q, n = _attn_case(bs, case)
+    cache.k_scales[..., 1].abs_()  # keys above zero
+    cache.k_codes |= 0x11
+    G, rows = case[1], [h for h in range(q.shape[1]) if h % case[1]]
+    want = bs.kv4_attn(cache, q, table, n, out_f32=True)
+    for value in (float("inf"), 2.0 ** 90, 300.0, -300.0, 0.0, float("nan")):
+        other = q.clone()
+        other[:, ::G] = value
+        got = bs.kv4_attn(cache, other, table, n, out_f32=True)
+        for a, b in zip(got, want):
+            assert torch.equal(a[:, rows], b[:, rows]), value

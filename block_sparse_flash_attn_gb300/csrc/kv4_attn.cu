@@ -58,7 +58,7 @@
 // All join in a fixed order: results repeat bit for bit.
 //
 // Measured: 32 sequences of 32768 to 65536 tokens, 8 heads of 128, 4 query heads
-// each: 311 us, 5.5 TB/s, 82% of a plain copy's rate, and 303 of 306 us when all pages
+// each: 310 us, 5.5 TB/s, 83% of a plain copy's rate, and 303 of 306 us when all pages
 // lie in L2: what is left is instructions (59% of issue slots, the integer pipe,
 // masks and shifts of codes, 58%), not bandwidth.  CUDA-core products on decoded
 // values: 10 ms.  One sequence of 777 tokens: 8 us, launch and five loads in a
@@ -275,12 +275,13 @@ struct Attn {
   static_assert(RP * (D + 3) * 4 <= kWarpRing, "shared memory");
   static constexpr int kSlot = RP * (D + 2);  // floats of a partial result
   // Tiles a pass of the loop: a turn of the ring, whose places are constants then;
-  // fewer where registers run out and code is long.  32 sequences of 32768 to 65536
-  // tokens, groups of 128: 311 us, by twos 332, one by one 355; 64 heads of 16 rows
-  // and 49152 tokens, groups of 32: 241 us, by twos 232; 12 heads of 16 rows over 24
-  // pages of 32 tokens, page choice included: 19 us one by one, by twos 21.
+  // fewer in four groups, where registers run out and code is long.  32 sequences of
+  // 32768 to 65536 tokens, groups of 128: 310 us, by twos 332, one by one 355; 256
+  // heads of 32768 tokens, groups of 32: 342 us, by twos 334; 64 heads of 16 rows and
+  // 49152 tokens: 241 and 232; 12 heads of 16 rows over 24 pages of 32 tokens, page
+  // choice included: by twos 21, one by one 19.
   template <int MODE>
-  static constexpr int kUnroll = NG < 4 || NT < 2 ? kStages : MODE == kRanges ? 2 : 1;
+  static constexpr int kUnroll = NG < 4 ? kStages : MODE == kRanges ? 2 : 1;
 
   // pieces of a row are stored permuted by its token, so that the 32-bit reads
   // of both products meet 32 banks
@@ -688,10 +689,10 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
 #pragma unroll
               for (int sft = 4; sft < 32; sft <<= 1)
                 large[e] = fmaxf(large[e], __shfl_xor_sync(0xFFFFFFFFu, large[e], sft));
-              const float fe = e ? fs.y : fs.x, scale = fabsf(e ? was.y : was.x);
-              large[e] = fe == 1.0f && large[e] * scale <= 32768.0f
-                             ? scale
-                             : scale_beside(fmaxf(large[e], fe * largest_beside(scale)));
+              const float before = largest_beside(e ? was.y : was.x), fe = e ? fs.y : fs.x;
+              // (512 = 2^15 / 2^6: what the scale leaves room for)
+              if (fe == 1.0f && large[e] <= 512.0f * before) large[e] = 0.0f;
+              large[e] = scale_beside(fmaxf(large[e], fe * before));
             }
             inv[nt][n] = f2(sign * large[0], sign * large[1]);
             // f new / old, at most 2 (f new first: new / old alone may overflow)
@@ -1008,10 +1009,10 @@ cudaError_t launch_attn(const AttnParams& p, int grid, cudaStream_t st) {
                           dim3(kJoinThreads), 0, st, p);
 }
 
-// Up to 4 rows a head: each row twice (32 x 8 heads of 32768 tokens: 219 us, one
-// tile of 8 for them 234 us); up to 8: one tile; more: tiles of 16 rows, which
-// decode the codes once for both halves (16 rows, 8 x 8 heads of 49152 tokens:
-// 163 us, as two tiles of 8 183 us; one sequence: 33 and 37 us).
+// Up to 4 rows a head: each row twice (32 x 8 heads of 32768 tokens: 211 us, one
+// tile of 8 230 us); up to 8: one tile; more: tiles of 16 rows, which decode the
+// codes once for both halves (16 rows, 8 x 8 heads of 49152 tokens: 163 us when two
+// tiles of 8 took 183 us, 157 us now; one sequence: 33 and 37 us).
 template <int D, int NG>
 cudaError_t launch_attn(const AttnParams& p, int grid, cudaStream_t st) {
   if (p.rows <= 4) return launch_attn<D, NG, 1, true>(p, grid, st);

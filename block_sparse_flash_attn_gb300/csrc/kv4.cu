@@ -193,8 +193,8 @@ __device__ __forceinline__ void append_rows(const AppendParams& p, int b, int le
 //
 // 512 bytes read and 160 written a token and head (groups of 32): the bound is
 // memory on paper, instructions in fact, some 20 a channel's lane.  8 x 4096
-// tokens (three quarters of them there), 8 heads of 128: 40 us, 67% of issue
-// slots, 3.6 TB/s; with conversions and comparisons a code 104 us, with a lane
+// tokens (three quarters of them there), 8 heads of 128: 43 us, 70% of issue
+// slots, 3.4 TB/s (42 us without the care for far values); with conversions and comparisons a code 104 us, with a lane
 // for 8 channels instead of 16 59 us, with the next two rows in flight no less,
 // with 8 CTAs an SM (64 registers, spilling) 47 us.
 //

@@ -60,7 +60,7 @@
 // Measured: 32 sequences of 32768 to 65536 tokens, 8 heads of 128, 4 query heads
 // each: 310 us, 5.5 TB/s, 83% of a plain copy's rate, and 303 of 306 us when all pages
 // lie in L2: what is left is instructions (59% of issue slots, the integer pipe,
-// masks and shifts of codes, 58%), not bandwidth.  CUDA-core products on decoded
+// masks and shifts of codes, 57%), not bandwidth.  CUDA-core products on decoded
 // values: 10 ms.  One sequence of 777 tokens: 8 us, launch and five loads in a
 // row.
 #include <cmath>

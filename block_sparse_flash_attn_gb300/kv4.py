@@ -6,7 +6,7 @@
     pages = bsattn.kv4_select(cache, q, block_table, lengths, keep=64)  # optional
     o, lse = bsattn.kv4_attn(cache, q, block_table, lengths, pages)
     bsattn.kv4_status(cache)                                   # raises if a table named a bad page
-    k, v = bsattn.kv4_read(cache, block_table, start, tokens)  # a cached prefix, for fwd
+    k, v = bsattn.kv4_read(cache, block_table, start, tokens)  # cached tokens as bf16
 """
 from __future__ import annotations
 

@@ -65,9 +65,9 @@ typedef enum {
                                   every V entry must be finite with |v| <= 65504; reported
                                   after the launch, by the status calls */
   BSATTN_ERR_PAGE = 9          /* bsattn_kv4_*: a block table names a page outside the cache,
-                                  a position lies behind the table, a length is negative, or
-                                  a page list is out of order; reported after the launch, by
-                                  bsattn_kv4_status */
+                                  a position to write or read lies behind the table or below
+                                  0, or a page list is out of order; reported after the
+                                  launch, by bsattn_kv4_status */
 } bsattn_status;
 
 /* Opaque plan: the per-query-tile list of live key blocks and the tile order. */
@@ -402,7 +402,8 @@ bsattn_status bsattn_rope_table(const double* inv_freq, int n_pos, int rotary_di
  *   y_i = n_i cos - n_j sin, y_j = n_j cos + n_i sin for the channel pairs
  *   (i, j) of the first rotary_dim channels, the angles taken from the table at
  *   the token's position (table null: y = n); the other channels y = n.
- * V rows are copied.  32-bit arithmetic, one rounding to bf16.
+ * V rows are copied.  32-bit arithmetic, one rounding to bf16: with weights, x below
+ * 2^60 in magnitude (the sum of squares overflows above).
  *
  *   x          device bf16 [B][S][H + 2 Hkv][D]: heads of Q, then K, then V; rows of
  *              one token contiguous, token and batch strides in elements, multiples
@@ -510,7 +511,8 @@ typedef struct {
 /*
  * Arguments that the bsattn_kv4_* calls share:
  *   block_table device int32, `columns` pages a sequence, rows table_stride apart.
- *   lengths     device int32 [B].
+ *   lengths     device int32 [B]; a sequence of the attention or the page choice whose
+ *               length is below 0 is empty.
  *   counts      device int32 [B] (taken as 0 below 0, T above T), or null: T each.
  * A page that the table does not have, or that lies outside the cache, is
  * skipped (its tokens are not written, read as zero, not attended to) and

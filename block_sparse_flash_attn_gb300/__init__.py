@@ -10,7 +10,7 @@ is missing, every call raises.
     o, lse = bsattn.fwd(q, k, v, plan, scale)        # q/k/v bf16 [B,H,S,D] on cuda
 
 Around it: qk_norm_rope and its gradient (rope.py), select_blocks (blocks.py)
-and the 4-bit cache, Kv4Cache and kv4_* (kv4.py).
+and the 4-bit cache, Kv4Cache and kv4_* (kv4.py), with its pages (kv4_pages.py).
 
 The operation: "Writing Pallas Kernels for JAX: Stepping Outside the XLA
 Safety Net" (sections "Designing the Block Specification" and "Writing the
@@ -44,7 +44,10 @@ EXPORTS = ["bsattn_plan", "bsattn_plan_csr", "bsattn_plan_schedule", "bsattn_fwd
            "bsattn_qk_norm_rope_bwd", "bsattn_qk_norm_rope_bwd_workspace",
            "bsattn_select_blocks", "bsattn_select_blocks_workspace", "bsattn_kv4_append",
            "bsattn_kv4_read", "bsattn_kv4_select", "bsattn_kv4_select_workspace",
-           "bsattn_kv4_attn", "bsattn_kv4_attn_workspace", "bsattn_kv4_status"]
+           "bsattn_kv4_attn", "bsattn_kv4_attn_workspace", "bsattn_kv4_status",
+           "bsattn_kv4_attn_chunk", "bsattn_kv4_attn_chunk_workspace", "bsattn_kv4_copy",
+           "bsattn_kv4_fork", "bsattn_kv4_fork_workspace", "bsattn_kv4_reserve",
+           "bsattn_kv4_compact", "bsattn_kv4_compact_workspace"]
 
 
 class BsattnError(RuntimeError):
@@ -139,6 +142,15 @@ def load():
             ("kv4_attn", [vp, vp, i32, i32, i32] + table + [vp, vp, i32, f32, u32, vp, vp, vp, size,
                                                             vp], i32),
             ("kv4_attn_workspace", [i32] * 8, size),
+            ("kv4_attn_chunk", [vp, vp, i32, i32, i32] + table + [vp, vp, vp, f32, f32, vp, u32, vp,
+                                                                  vp, vp, size, vp], i32),
+            ("kv4_attn_chunk_workspace", [i32] * 7, size),
+            ("kv4_copy", [vp, vp, vp, vp, i32, vp], i32),
+            ("kv4_fork", [vp, vp] + table + [vp, i32, vp, i32, vp, vp, vp, vp, size, vp], i32),
+            ("kv4_fork_workspace", [i32], size),
+            ("kv4_reserve", [vp, vp] + table + [vp, vp, i32, i32, vp, i64, vp, vp], i32),
+            ("kv4_compact", [vp, vp] + table + [i32, vp, i64, vp, vp, vp, size, vp], i32),
+            ("kv4_compact_workspace", [i32], size),
             ("kv4_status", [vp, vp], i32)):
         fn = getattr(lib, "bsattn_" + name)
         fn.argtypes, fn.restype = args, res
@@ -536,6 +548,7 @@ def attention(q, k, v, mask, causal: bool = False, scale: float | None = None,
 
 # the operators around the attention (they use the names above)
 from .blocks import select_blocks  # noqa: E402
-from .kv4 import (Kv4Cache, kv4_append, kv4_attn, kv4_read, kv4_select,  # noqa: E402
-                  kv4_status)
+from .kv4 import (Kv4Cache, kv4_append, kv4_attn, kv4_attn_chunk, kv4_read,  # noqa: E402
+                  kv4_select, kv4_status)
+from .kv4_pages import kv4_compact, kv4_copy, kv4_fork, kv4_reserve  # noqa: E402
 from .rope import qk_norm_rope, qk_norm_rope_bwd, rope_table  # noqa: E402

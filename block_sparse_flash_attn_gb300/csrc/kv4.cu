@@ -946,13 +946,13 @@ bsattn_status bsattn_kv4_status(const bsattn_kv4_cache* cache, void* stream) {
           cudaSuccess ||
       cudaStreamSynchronize(st) != cudaSuccess)
     return BSATTN_ERR_CUDA;
-  if (!(word & kStatusPage)) return BSATTN_OK;
+  if (!(word & (kStatusPage | kStatusTimeout))) return BSATTN_OK;
   // (cleared only after a report was seen: one that another stream makes in between is
   // in this answer, and none is lost)
   if (cudaMemsetAsync(view.status, 0, sizeof(word), st) != cudaSuccess ||
       cudaStreamSynchronize(st) != cudaSuccess)
     return BSATTN_ERR_CUDA;
-  return BSATTN_ERR_PAGE;
+  return word & kStatusTimeout ? BSATTN_ERR_TIMEOUT : BSATTN_ERR_PAGE;
 }
 
 }  // extern "C"

@@ -197,11 +197,6 @@ __device__ __forceinline__ float largest_beside(float scale) {
   return __uint_as_float((254u + 6u << 23) - (__float_as_uint(scale) & 0x7FFFFFFFu));
 }
 
-__device__ __forceinline__ void cluster_barrier() {
-  asm volatile(
-      "barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-          : "memory");
-}
 // This CTA's shared-memory word in another CTA of the cluster.
 __device__ __forceinline__ float peer_word(const float* shared, int rank) {
   uint32_t at;

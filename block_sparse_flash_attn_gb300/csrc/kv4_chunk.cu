@@ -1,0 +1,1165 @@
+// Attention of a chunk of new tokens over the 4-bit cache, one token to whole
+// prompts, with scores that may be capped, biased by distance and opened to a
+// prefix.
+//
+// Query t of the count c new tokens of a sequence of length n sits at i = n - c + t
+// and sees the cached tokens j <= i, and those of the prefix, j < f.  With keys and
+// values decoded as step * code + least (kv4.cu):
+//   x_j = scale q . k_j;  x_j = cap tanh(x_j / cap);  x_j -= slope |i - j|
+//   p = softmax(x),  o = sum_j p_j v_j,  lse = ln sum_j exp(x_j)
+//   a query that sees nothing, or lies behind the count: o = 0, lse = -inf.
+//
+// Bound: the tensor cores where there are many rows (4 D multiply-adds a query and
+// key), the codes' expansion where there are few.  So a CTA takes 256 query rows of
+// one key/value head, its G query heads' tokens interleaved (row = token G + head:
+// a tile ends where its last token does), and expands each tile of 128 tokens
+// once for all of them, to operands of tcgen05 in shared memory:
+//
+// - K without a rounding that counts.  An fp16 holds step (code - 8) exactly (8 bits
+//   times 3), and the rest of a key is one number a group, c = least + 8 step:
+//     q . k = sum_d q_d step (code_d - 8) + sum_groups c sum_d q_d.
+//   The second sum is one more 16-channel step of the same product: c and the sums
+//   of q are split into two fp16 each, (q hi, q lo, q hi) beside (c hi, c hi, c lo),
+//   off by 2^-22 of a product.  Queries are bf16, exact in fp16 beside their
+//   row's largest; keys are taken beside the largest of 32 tokens (what is 2^-22 of
+//   it and less loses bits); both are powers of two that the softmax puts back.  So
+//   scores and lse are those of 32-bit products, at the cost of a ninth step for 8.
+// - V in fp16, rounded once (2^-11), where all values of 32 tokens lie in its range
+//   (groups of up to 2^15, and of 2^-4 at least or zero), else in bf16 (2^-8); the weights
+//   in the same type.  Weights are off by that rounding, or by 2^-25 of a number that
+//   the row's largest weight is at least 2^-8 of.
+//
+// Work of a CTA (512 threads, one CTA an SM, 211 KB of shared memory):
+//   warps 0-3, 4-7   softmax of the first and the second 128 rows: a thread a row
+//   warps 8-11       the codes' expansion, 32 tokens a warp
+//   warp 12          issues S = Q K^T, owns the tensor memory
+//   warp 13          issues O += P V
+// Tensor memory: S of both row tiles (128 columns each; the weights replace the
+// scores they come from) and O of both.  While one tile's softmax runs, the tensor
+// core works for the other.
+//
+// Few rows and long contexts: the tokens are cut into `splits` ranges, a CTA each,
+// whose partial results (maximum, sum, O) a second launch joins, in order.
+// Every wait is bounded; a wait that runs out is reported by bsattn_kv4_status.
+#include <cmath>
+#include <cstdint>
+
+#include <cuda_fp16.h>
+
+#include "kv4.cuh"
+#include "ptx.cuh"
+
+namespace bsattn {
+namespace {
+
+constexpr int kChunkThreads = 512;
+constexpr int kTileRows = 128;              // rows of a softmax tile: lanes of tensor memory
+constexpr int kCtaRows = 2 * kTileRows;
+constexpr int kKeys = 128;                  // tokens a step
+constexpr int kStages = 2;                  // of the expanded K and V
+constexpr int kInfos = 4;                   // steps whose ChunkInfo is kept
+constexpr int kWarpExpand = 8, kWarpScores = 12, kWarpValues = 13;
+// 256 x 184 + 128 x 96 + 128 x 48 = 512 x 128 registers
+constexpr int kSoftmaxRegs = 184, kExpandRegs = 96, kIssueRegs = 48;
+constexpr uint32_t kTmemColumns = 512;
+constexpr float kLagBits = 8.0f;            // a row's reference may lie 2^8 below its maximum
+constexpr float kMostSum = 32768.0f;        // of a step's weights: each then fits fp16
+constexpr int kJoinWarps = 4;
+constexpr unsigned long long kDrainLimitNs = 200ull * 1000 * 1000;
+
+struct ChunkParams {
+  Kv4View c;
+  const uint16_t* q;  // [B][H][T][D]
+  const int* table;
+  int64_t table_stride;
+  int columns;
+  const int* lengths;
+  const int* counts;   // null: T each
+  const int* prefix;   // null: none
+  const float* slopes; // null: none
+  int B, H, T, G;
+  int items;           // row tiles (of kCtaRows) a key/value head
+  int splits;
+  float scale_log2;    // |scale| log2 e, above 0
+  float sign;          // of the scale
+  float cap_log2;      // cap log2 e; 0: no cap
+  void* out;
+  float* lse;
+  int out_f32;
+  float* partial;      // [B * Hkv * items * splits][kCtaRows * (D + 2)]
+  unsigned long long timeout_ns;
+};
+
+// What the softmax needs of 32 tokens of a step.
+struct TokenInfo {
+  float factor;   // the keys' power of two
+  uint32_t bits;  // 0, 1: the first, the second 16 tokens are there; 2: V is bf16
+};
+
+struct __align__(16) ChunkBars {
+  uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+  uint64_t q_full[2], s_full[2], p_full[2], pv_done[2];
+  // (a step's slot is taken again four steps on: two steps after its scores were read)
+  uint64_t info_full[kInfos];
+  uint64_t drain;
+  TokenInfo info[kInfos][4];
+  int nan_from[4];  // by group of channels: the first token whose values are not numbers
+  uint32_t tmem_base;
+  int abort_flag;
+  int query_shift[kCtaRows];
+};
+
+template <int D>
+struct ChunkCfg {
+  static constexpr int kBoxes = D / 64;  // of 64 channels, 128 bytes a row, swizzled
+  static constexpr int kBoxBytes = 128 * 128;
+  static constexpr int kTileBytes = kBoxes * kBoxBytes;
+  static constexpr int kSumBytes = 128 * 32;  // the 16 channels of the group sums
+  static constexpr int kQ = 0;
+  static constexpr int kQSums = kQ + 2 * kTileBytes;
+  static constexpr int kKSums = kQSums + 2 * kSumBytes;
+  static constexpr int kK = kKSums + kStages * kSumBytes;
+  static constexpr int kV = kK + kStages * kTileBytes;
+  static constexpr int kBars = kV + kStages * kTileBytes;
+  static constexpr int kSmem = kBars + (int)sizeof(ChunkBars) + 1024;
+  static_assert(kSmem <= 232448, "shared memory");
+  static_assert(kKSums % 1024 == 0 && kK % 1024 == 0, "swizzled tiles begin at multiples of 1024");
+  static constexpr uint32_t kTmemS = 0, kTmemO = 256;
+  static constexpr uint32_t kIdescS = idesc_f16kind_f32(128, 128, false, false, true);
+  static constexpr uint32_t kIdescO16 = idesc_f16kind_f32(128, D, true, false, true);
+  static constexpr uint32_t kIdescOBf = idesc_f16kind_f32(128, D, true, false, false);
+};
+
+// K-major operand of 16 channels without a swizzle: 8 rows of 16 bytes are a core
+// matrix; the next 8 rows follow 128 bytes on, the next 8 channels 2048.
+__device__ __forceinline__ uint64_t sums_desc(uint32_t at) {
+  uint64_t d = 0;
+  d |= (uint64_t)((at >> 4) & 0x3FFFu);
+  d |= (uint64_t)(2048 >> 4) << 16;
+  d |= (uint64_t)(128 >> 4) << 32;
+  d |= 1ull << 46;
+  return d;
+}
+
+// What a CTA works on.
+struct ChunkWork {
+  int b, h, split;
+  int len, count, first_pos;  // tokens, new ones, position of the first new one
+  int open;                   // positions below it are seen by all
+  int keys;                   // tokens that the table has room for
+  int rows;                   // G * count: rows that have a query
+  int row0;                   // the CTA's first
+  int64_t slot;               // partial result
+  int j0;                     // first step
+  int steps[2];               // of each row tile
+  int total;
+
+  __device__ __forceinline__ int limit(int t) const {  // last position that token t sees
+    return min(max(first_pos + t, open - 1), keys - 1);
+  }
+};
+
+__device__ __forceinline__ ChunkWork chunk_work(const ChunkParams& p) {
+  ChunkWork w;
+  // row tiles with the longest contexts first
+  const int heads = p.B * p.c.Hkv;
+  int at = blockIdx.x;
+  w.split = at % p.splits;
+  at /= p.splits;
+  const int item = p.items - 1 - at / heads;
+  const int bh = at % heads;
+  w.b = bh / p.c.Hkv;
+  w.h = bh - w.b * p.c.Hkv;
+  w.slot = ((int64_t)bh * p.items + item) * p.splits + w.split;
+  w.len = max(load(p.lengths + w.b), 0);
+  w.count = p.T;
+  if (p.counts) w.count = min(max(load(p.counts + w.b), 0), p.T);
+  w.first_pos = w.len - w.count;
+  w.open = p.prefix ? load(p.prefix + w.b) : 0;
+  const int64_t room = (int64_t)p.columns * p.c.page;
+  w.keys = (int)min((int64_t)w.len, room);
+  if (w.len > room && threadIdx.x == 0) p.c.report();
+  w.rows = p.G * w.count;
+  w.row0 = item * kCtaRows;
+  int most[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int first = w.row0 + i * kTileRows;
+    const int last = min(first + kTileRows, w.rows) - 1;
+    const int lim = first < w.rows ? w.limit(last / p.G) : -1;
+    most[i] = lim >= 0 ? lim / kKeys + 1 : 0;
+  }
+  const int all = max(most[0], most[1]);
+  w.j0 = (int)((int64_t)all * w.split / p.splits);
+  const int j1 = (int)((int64_t)all * (w.split + 1) / p.splits);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) w.steps[i] = max(min(j1, most[i]) - w.j0, 0);
+  w.total = max(w.steps[0], w.steps[1]);
+  return w;
+}
+
+__device__ __forceinline__ bool wait_all(const uint64_t* bar, uint32_t parity,
+                                         volatile int* abort_flag, const ChunkParams& p) {
+  const bool ok = wait_bounded(smem_u32(bar), parity, abort_flag, p.c.status, p.timeout_ns);
+  return __all_sync(0xffffffffu, ok);
+}
+
+// Waits, with a limit of its own, for all products that this warp issued.
+__device__ __forceinline__ void drain(ChunkBars* bars) {
+  if (elect_one()) mma_commit(smem_u32(&bars->drain));
+  __syncwarp();
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(smem_u32(&bars->drain), 0)) {
+    if (globaltimer_ns() - t0 > kDrainLimitNs) return;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// warps 8-11: codes to operands
+// ---------------------------------------------------------------------------
+// A word of eight codes as four pairs of fp16 (codes 0 and 4, 1 and 5, ...): the
+// codes are put into the mantissas of 1024 and 64, and `off` takes those away.
+__device__ __forceinline__ void open_codes(uint32_t w, __half2 off1024, __half2 off64,
+                                           __half2 (&x)[4]) {
+  const uint32_t y = w >> 8;
+  const uint32_t n[4] = {(w & 0x000F000Fu) | 0x64006400u, (w & 0x00F000F0u) | 0x54005400u,
+                         (y & 0x000F000Fu) | 0x64006400u, (y & 0x00F000F0u) | 0x54005400u};
+  x[0] = __hadd2(*reinterpret_cast<const __half2*>(&n[0]), off1024);
+  x[1] = __hadd2(*reinterpret_cast<const __half2*>(&n[1]), off64);
+  x[2] = __hadd2(*reinterpret_cast<const __half2*>(&n[2]), off1024);
+  x[3] = __hadd2(*reinterpret_cast<const __half2*>(&n[3]), off64);
+}
+__device__ __forceinline__ uint32_t half_bits(__half2 x) { return *reinterpret_cast<uint32_t*>(&x); }
+__device__ __forceinline__ uint32_t half_pair(__half lo, __half hi) {
+  return half_bits(__halves2half2(lo, hi));
+}
+
+// A group's scales; a group with one that is not finite stands for NaN.
+struct Scales {
+  float step, least;
+  bool finite;
+  __device__ __forceinline__ explicit Scales(uint32_t word)
+      : step(bf16_lo(word)), least(bf16_hi(word)),
+        finite((word & 0x7F80u) != 0x7F80u && (word & 0x7F800000u) != 0x7F800000u) {
+    if (!finite) step = least = 0.0f;
+  }
+  // the largest magnitude that the group stands for
+  __device__ __forceinline__ float most() const {
+    return fmaxf(fabsf(least), fabsf(fmaf(15.0f, step, least)));
+  }
+};
+
+template <int D, int NG>
+__device__ void run_expand(const ChunkParams& p, const ChunkWork& w, ChunkBars* bars,
+                           uint32_t base, volatile int* abort_flag) {
+  using C = ChunkCfg<D>;
+  constexpr int LR = D / 32;           // lanes a row: 16 bytes, 32 codes each
+  constexpr int RL = 32 / LR;          // rows a load
+  constexpr int NL = 32 / RL;          // loads a warp and step
+  constexpr int GL = D / NG / 32;      // lanes a group
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - kWarpExpand;
+  const int piece = lane % LR, group = piece / GL;
+  const int* table = p.table + w.b * p.table_stride;
+  const uint4* k_codes = reinterpret_cast<const uint4*>(p.c.k_codes);
+  const uint4* v_codes = reinterpret_cast<const uint4*>(p.c.v_codes);
+  const uint32_t* k_scales = reinterpret_cast<const uint32_t*>(p.c.k_scales);
+  const uint32_t* v_scales = reinterpret_cast<const uint32_t*>(p.c.v_scales);
+
+  // Lanes 0 and 1: where the first and the second 16 of the warp's tokens of step s
+  // are, in units of 16 rows; -1: nowhere.
+  auto look_up = [&](int s) -> int {
+    if (lane > 1 || s >= w.total) return -1;
+    const int pos = (w.j0 + s) * kKeys + warp * 32 + lane * 16;
+    if (pos >= w.keys) return -1;
+    const int pg = page_at(p.c, table, p.columns, pos >> p.c.log_page);
+    return pg < 0 ? -1 : (int)(p.c.row(pg, w.h, pos & (p.c.page - 1)) >> 4);
+  };
+  // the row of the warp's token t of step s; -1 where there is none
+  auto row_of = [&](int where, int s, int t) -> int64_t {
+    const int r16 = __shfl_sync(0xffffffffu, where, t >> 4);
+    const int pos = (w.j0 + s) * kKeys + warp * 32 + t;
+    return r16 < 0 || pos >= w.keys ? -1 : (int64_t)r16 * 16 + (t & 15);
+  };
+  uint4 kc[NL], vc[NL];
+  uint32_t ks[NL], vs[NL], sums[NG];  // (sums: the scales of token `lane`'s keys)
+  auto load_k = [&](int where, int s) {
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      const int64_t row = row_of(where, s, i * RL + lane / LR);
+      kc[i] = make_uint4(0, 0, 0, 0);
+      ks[i] = 0;
+      if (row >= 0) {
+        kc[i] = load(k_codes + row * LR + piece);
+        ks[i] = load(k_scales + row * NG + group);
+      }
+    }
+    const int64_t row = row_of(where, s, lane);
+#pragma unroll
+    for (int g = 0; g < NG; ++g) sums[g] = row >= 0 ? load(k_scales + row * NG + g) : 0u;
+  };
+  auto load_v = [&](int where, int s) {
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      const int64_t row = row_of(where, s, i * RL + lane / LR);
+      vc[i] = make_uint4(0, 0, 0, 0);
+      vs[i] = 0;
+      if (row >= 0) {
+        vc[i] = load(v_codes + row * LR + piece);
+        vs[i] = load(v_scales + row * NG + group);
+      }
+    }
+  };
+
+  // A row's 32 codes are four 16-byte pieces of its tile; lanes of the second box
+  // begin with the other two, so that the eight lanes of a store meet 32 banks.
+  const int turned = D == 128 ? lane & 2 : 0;
+  auto word_of = [&](const uint4& v, int i) -> uint32_t {
+    const uint32_t a = i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+    const uint32_t b = i == 0 ? v.z : i == 1 ? v.w : i == 2 ? v.x : v.y;
+    return turned ? b : a;
+  };
+  const int row_in = warp * 32 + lane / LR;
+  uint32_t piece_at[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int c = 4 * (lane & 1) + (i ^ turned);  // of the box's eight
+    piece_at[i] = (D == 128 ? (uint32_t)(piece >> 1) * C::kBoxBytes : 0u) + row_in * 128 +
+                  ((c ^ (row_in & 7)) << 4);
+  }
+
+  int where = look_up(0), next = look_up(1);
+  load_k(where, 0);
+  load_v(where, 0);
+  const __half2 k1024 = __float2half2_rn(-1032.0f), k64 = __float2half2_rn(-72.0f);
+  const __half2 v1024 = __float2half2_rn(-1024.0f), v64 = __float2half2_rn(-64.0f);
+  for (int s = 0; s < w.total; ++s) {
+    const int st = s % kStages;
+    const uint32_t parity = ((uint32_t)(s / kStages) & 1u) ^ 1u;
+    // ---- the keys' power of two, the values' type
+    float most = 0.0f;
+    bool fits = true;
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      most = fmaxf(most, Scales(ks[i]).most());
+      const Scales v(vs[i]);
+      const float vm = v.most();
+      fits = fits && vm <= 32768.0f && (vm >= 0.0625f || vm == 0.0f);
+      if (!v.finite)
+        atomicMin(&bars->nan_from[group],
+                  (w.j0 + s) * kKeys + warp * 32 + i * RL + lane / LR);
+    }
+    const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
+    // the largest goes to [2^7, 2^8) (below 2^-119: times 2^126)
+    const int e = min(max((int)(top >> 23), 8), 253);
+    const float scale = __uint_as_float((uint32_t)(254 + 7 - e) << 23);
+    const bool v_bf16 = !__all_sync(0xffffffffu, fits);
+    const uint32_t there = __ballot_sync(0xffffffffu, where >= 0) & 3u;
+    if (!wait_all(&bars->k_empty[st], parity, abort_flag, p)) return;
+    if (lane == 0) {
+      TokenInfo* info = &bars->info[s % kInfos][warp];
+      info->factor = 1.0f / scale;
+      info->bits = there | (v_bf16 ? 4u : 0u);
+    }
+    // ---- K
+    const uint32_t k_at = base + C::kK + st * C::kTileBytes;
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      const __half2 step = __float2half2_rn(Scales(ks[i]).step * scale);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        __half2 x[4];
+        open_codes(word_of(kc[i], c), k1024, k64, x);
+        st_shared_v4(k_at + piece_at[c] + i * (RL * 128), half_bits(__hmul2(x[0], step)),
+                     half_bits(__hmul2(x[1], step)), half_bits(__hmul2(x[2], step)),
+                     half_bits(__hmul2(x[3], step)));
+      }
+    }
+    {  // c of each group, twice its high half and once its low one
+      __half x[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = __ushort_as_half(0);
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        const Scales k(sums[g]);
+        float c = fmaf(8.0f, k.step, k.least) * scale * 128.0f;
+        if (!k.finite) c = __int_as_float(0x7FC00000);
+        const __half hi = __float2half_rn(c);
+        x[g] = x[NG + g] = hi;
+        x[2 * NG + g] = __float2half_rn(c - __half2float(hi));
+      }
+      const uint32_t at = base + C::kKSums + st * C::kSumBytes + (warp * 32 + lane) * 16;
+      st_shared_v4(at, half_pair(x[0], x[1]), half_pair(x[2], x[3]), half_pair(x[4], x[5]),
+                   half_pair(x[6], x[7]));
+      st_shared_v4(at + 2048, half_pair(x[8], x[9]), half_pair(x[10], x[11]),
+                   half_pair(x[12], x[13]), half_pair(x[14], x[15]));
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(smem_u32(&bars->info_full[s % kInfos]));
+      mbar_arrive(smem_u32(&bars->k_full[st]));
+    }
+    where = next;
+    next = look_up(s + 2);
+    load_k(where, s + 1);
+    // ---- V
+    if (!wait_all(&bars->v_empty[st], parity, abort_flag, p)) return;
+    const uint32_t v_at = base + C::kV + st * C::kTileBytes;
+    if (!v_bf16) {
+#pragma unroll
+      for (int i = 0; i < NL; ++i) {
+        const Scales v(vs[i]);
+        const __half2 step = __float2half2_rn(v.step), least = __float2half2_rn(v.least);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          __half2 x[4];
+          open_codes(word_of(vc[i], c), v1024, v64, x);
+          st_shared_v4(v_at + piece_at[c] + i * (RL * 128), half_bits(__hfma2(x[0], step, least)),
+                       half_bits(__hfma2(x[1], step, least)),
+                       half_bits(__hfma2(x[2], step, least)),
+                       half_bits(__hfma2(x[3], step, least)));
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NL; ++i) {
+        const Scales v(vs[i]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint32_t n = word_of(vc[i], c);
+          uint32_t y[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            y[k] = pack_bf16x2(fmaf((float)(n >> (4 * k) & 15u), v.step, v.least),
+                               fmaf((float)(n >> (4 * k + 16) & 15u), v.step, v.least));
+          st_shared_v4(v_at + piece_at[c] + i * (RL * 128), y[0], y[1], y[2], y[3]);
+        }
+      }
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&bars->v_full[st]));
+    load_v(where, s + 1);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// warps 12 and 13: the two products
+// ---------------------------------------------------------------------------
+// S(s) of a row tile replaces what P(s - 1) V read, so it waits for that product.
+template <int D>
+__device__ void run_scores(const ChunkParams& p, const ChunkWork& w, ChunkBars* bars,
+                           uint32_t tmem, uint32_t base, volatile int* abort_flag) {
+  using C = ChunkCfg<D>;
+  bool ok = true;
+  for (int i = 0; i < 2 && ok; ++i)
+    if (w.steps[i] > 0) ok = wait_all(&bars->q_full[i], 0, abort_flag, p);
+  for (int s = 0; s < w.total && ok; ++s) {
+    const int st = s % kStages;
+    ok = wait_all(&bars->k_full[st], (uint32_t)(s / kStages) & 1u, abort_flag, p);
+    for (int i = 0; i < 2 && ok; ++i) {
+      if (s >= w.steps[i]) continue;
+      if (s > 0) ok = wait_all(&bars->pv_done[i], (uint32_t)(s - 1) & 1u, abort_flag, p);
+      if (!ok) break;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t qd = smem_desc_sw128(base + C::kQ + i * C::kTileBytes, 16, 1024);
+        const uint64_t kd = smem_desc_sw128(base + C::kK + st * C::kTileBytes, 16, 1024);
+        const uint32_t to = tmem + C::kTmemS + i * 128;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = ((k >> 2) * C::kBoxBytes + (k & 3) * 32) >> 4;
+          mma_ss(to, qd + off, kd + off, C::kIdescS, k > 0 ? 1u : 0u);
+        }
+        mma_ss(to, sums_desc(base + C::kQSums + i * C::kSumBytes),
+               sums_desc(base + C::kKSums + st * C::kSumBytes), C::kIdescS, 1u);
+        mma_commit(smem_u32(&bars->s_full[i]));
+      }
+      __syncwarp();
+    }
+    if (ok && elect_one()) mma_commit(smem_u32(&bars->k_empty[st]));
+    __syncwarp();
+  }
+  drain(bars);
+}
+
+template <int D>
+__device__ void run_values(const ChunkParams& p, const ChunkWork& w, ChunkBars* bars,
+                           uint32_t tmem, uint32_t base, volatile int* abort_flag) {
+  using C = ChunkCfg<D>;
+  bool ok = true;
+  for (int s = 0; s < w.total && ok; ++s) {
+    const int st = s % kStages;
+    ok = wait_all(&bars->v_full[st], (uint32_t)(s / kStages) & 1u, abort_flag, p);
+    for (int i = 0; i < 2 && ok; ++i) {
+      if (s >= w.steps[i]) continue;
+      ok = wait_all(&bars->p_full[i], (uint32_t)s & 1u, abort_flag, p);
+      if (!ok) break;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t vd =
+            smem_desc_sw128(base + C::kV + st * C::kTileBytes, C::kBoxBytes, 1024);
+        const uint32_t from = tmem + C::kTmemS + i * 128, to = tmem + C::kTmemO + i * D;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {  // 16 tokens each
+          const bool bf = bars->info[s % kInfos][k >> 1].bits & 4u;
+          mma_ts(to, from + k * 8, vd + (uint32_t)(k * 2048 >> 4),
+                 bf ? C::kIdescOBf : C::kIdescO16, s > 0 || k > 0 ? 1u : 0u);
+        }
+        mma_commit(smem_u32(&bars->pv_done[i]));
+      }
+      __syncwarp();
+    }
+    if (ok && elect_one()) mma_commit(smem_u32(&bars->v_empty[st]));
+    __syncwarp();
+  }
+  drain(bars);
+}
+
+// ---------------------------------------------------------------------------
+// warps 0-7: queries, softmax, results
+// ---------------------------------------------------------------------------
+// This warp's 32 rows of Q as fp16 beside each row's largest (which goes to [2^14,
+// 2^15)), channels in the codes' order, and the sums of their groups.
+template <int D, int NG>
+__device__ __forceinline__ void load_queries(const ChunkParams& p, const ChunkWork& w,
+                                             ChunkBars* bars, uint32_t base, int tile, int sub) {
+  using C = ChunkCfg<D>;
+  constexpr int LQ = D / 8, RQ = 32 / LQ;  // lanes a row, rows at once
+  constexpr int GL = LQ / NG;              // lanes a group
+  constexpr int kBatch = 8;
+  const int lane = threadIdx.x & 31, piece = lane % LQ;
+  const uint32_t q_at = base + C::kQ + tile * C::kTileBytes + piece / 8 * C::kBoxBytes;
+  const uint32_t sums_at = base + C::kQSums + tile * C::kSumBytes + (sub * 32) * 16;
+  st_shared_v4(sums_at + lane * 16, 0, 0, 0, 0);
+  st_shared_v4(sums_at + lane * 16 + 2048, 0, 0, 0, 0);
+  __syncwarp();
+#pragma unroll 1
+  for (int r0 = 0; r0 < 32; r0 += kBatch * RQ) {
+    uint4 raw[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int row = w.row0 + tile * kTileRows + sub * 32 + r0 + i * RQ + lane / LQ;
+      raw[i] = make_uint4(0, 0, 0, 0);
+      if (row < w.rows) {
+        const int t = row / p.G, g = row - t * p.G;
+        raw[i] = load(reinterpret_cast<const uint4*>(
+                          p.q + (((int64_t)w.b * p.H + w.h * p.G + g) * p.T + t) * D) +
+                      piece);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int r = sub * 32 + r0 + i * RQ + lane / LQ;
+      float x[8], most = 0.0f, sum = 0.0f;
+      unpack8(raw[i], x);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float a = fabsf(x[k]);
+        most = fmaxf(most, a <= 3.4e38f ? a : 0.0f);
+      }
+#pragma unroll
+      for (int o = 1; o < LQ; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+      const int sh = most > 0.0f ? 14 - ilogbf(most) : 0;
+      // in two factors: 2^sh may pass fp32's range
+      const float fa = ldexpf(p.sign, sh / 2), fb = ldexpf(1.0f, sh - sh / 2);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        x[k] = x[k] * fa * fb;
+        sum += x[k];
+      }
+      st_shared_v4(q_at + r * 128 + ((piece % 8 ^ (r & 7)) << 4), pack_f16x2(x[0], x[4]),
+                   pack_f16x2(x[1], x[5]), pack_f16x2(x[2], x[6]), pack_f16x2(x[3], x[7]));
+#pragma unroll
+      for (int o = 1; o < GL; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      sum *= 0.0078125f;
+      if (piece % GL == 0) {
+        const int g = piece / GL;
+        const __half hi = __float2half_rn(sum), lo = __float2half_rn(sum - __half2float(hi));
+        auto put = [&](int k, __half v) {
+          asm volatile("st.shared.b16 [%0], %1;" ::"r"(sums_at + (r - sub * 32) * 16 +
+                                                       (k >> 3) * 2048 + (k & 7) * 2),
+                       "h"(__half_as_ushort(v))
+                       : "memory");
+        };
+        put(g, hi);
+        put(NG + g, lo);
+        put(2 * NG + g, hi);
+      }
+      if (piece == 0) bars->query_shift[tile * kTileRows + r] = sh;
+    }
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(smem_u32(&bars->q_full[tile]));
+}
+
+__device__ __forceinline__ float largest32(const uint32_t (&x)[32]) {
+  float a[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) a[i] = fmaxf(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+#pragma unroll
+  for (int c = 8; c < 32; c += 8) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      a[i] = max3(a[i], __uint_as_float(x[c + 2 * i]), __uint_as_float(x[c + 2 * i + 1]));
+  }
+  return fmaxf(max3(a[0], a[1], a[2]), a[3]);
+}
+
+// tanh(y) / y by y^2 for |y| <= 0.8, off by 5e-8 relative: least maximal relative
+// error, by Lawson's iteration.
+constexpr float kTanh0 = 0.99999994f, kTanh1 = -0.333326757f, kTanh2 = 0.13321048f,
+                kTanh3 = -0.0531143136f, kTanh4 = 0.0190932993f, kTanh5 = -0.00435529929f;
+constexpr float kTanhRange = 0.8f;
+
+// tanh(y): (1 - e) / (1 + e), e = exp(-2 |y|); off by 2^-22 of one or less.
+__device__ __forceinline__ float tanh_any(float y) {
+  const float e = ex2_approx(-2.8853900817779268f * fabsf(y));
+  return copysignf(__fdividef(1.0f - e, 1.0f + e), y);
+}
+
+// The row's results to `out` and `lse`, or to the partial result.
+template <int D>
+__device__ __forceinline__ void write_row(const ChunkParams& p, int64_t at, const float (&x)[16],
+                                          int c0) {
+  const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
+  if (p.out_f32) {
+    uint32_t y[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(x[i]);
+    float* dst = static_cast<float*>(p.out) + at * D + c0;
+    store32(dst, *reinterpret_cast<const uint32_t(*)[8]>(y), wide);
+    store32(dst + 8, *reinterpret_cast<const uint32_t(*)[8]>(y + 8), wide);
+  } else {
+    uint32_t y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+    store32(static_cast<uint16_t*>(p.out) + at * D + c0, y, wide);
+  }
+}
+
+// What there is to write where a row tile has nothing to see.
+template <int D>
+__device__ __forceinline__ void write_nothing(const ChunkParams& p, const ChunkWork& w, int tile,
+                                              int r) {
+  const int row = w.row0 + tile * kTileRows + r;
+  if (row >= p.G * p.T) return;
+  if (p.splits > 1 && row < w.rows) {
+    float* slot = p.partial + w.slot * (kCtaRows * (D + 2)) + tile * kTileRows + r;
+    slot[0] = -INFINITY;
+    slot[kCtaRows] = 0.0f;
+    return;
+  }
+  if (w.split != 0) return;
+  const int t = row / p.G, g = row - t * p.G;
+  const int64_t at = ((int64_t)w.b * p.H + w.h * p.G + g) * p.T + t;
+  const float zero[16] = {};
+#pragma unroll 1
+  for (int c = 0; c < D; c += 16) write_row<D>(p, at, zero, c);
+  p.lse[at] = -INFINITY;
+}
+
+template <int D, int NG, bool SCORED>
+__device__ void run_softmax(const ChunkParams& p, const ChunkWork& w, ChunkBars* bars,
+                            uint32_t tmem, uint32_t base, volatile int* abort_flag) {
+  using C = ChunkCfg<D>;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int tile = warp >> 2, sub = warp & 3;
+  const int r = sub * 32 + lane;
+  const int steps = w.steps[tile];
+  if (steps == 0) return write_nothing<D>(p, w, tile, r);
+  load_queries<D, NG>(p, w, bars, base, tile, sub);
+  const int row = w.row0 + tile * kTileRows + r;
+  const int t = row / p.G, g = row - t * p.G;
+  const bool there = row < w.rows;
+  // (rows without a query: all keys, with scores of zero)
+  const int lim = there ? w.limit(t) : 0x7FFFFFFF;
+  const int pos = w.first_pos + t;
+  const float row_factor = ldexpf(p.scale_log2, -bars->query_shift[tile * kTileRows + r]);
+  float slope = 0.0f;
+  if constexpr (SCORED) {
+    if (p.slopes && there) slope = load(p.slopes + w.h * p.G + g) * 1.4426950408889634f;
+  }
+  const float inv_cap = SCORED && p.cap_log2 > 0.0f ? 1.0f / p.cap_log2 : 0.0f;
+  const uint32_t lanes = (uint32_t)(sub * 32) << 16;
+  const uint32_t tS = tmem + C::kTmemS + tile * 128 + lanes;
+  const uint32_t tO = tmem + C::kTmemO + tile * D + lanes;
+  const uint32_t kNegInf = 0xff800000u;
+
+  float m = -INFINITY;  // reference: a maximum of scores (base 2) so far, or up to kLagBits below
+  uint64_t sum2 = 0;
+  for (int s = 0; s < steps; ++s) {
+    if (!wait_all(&bars->info_full[s % kInfos], (uint32_t)(s / kInfos) & 1u, abort_flag, p)) return;
+    if (!wait_all(&bars->s_full[tile], (uint32_t)s & 1u, abort_flag, p)) return;
+    tc_fence_after();
+    const int key0 = (w.j0 + s) * kKeys;
+    const int rel = lim - key0;  // keys c <= rel of the step are seen
+    float factor[4];
+    uint32_t bits = 0;  // 16-token pieces that are there
+    uint32_t bf16s = 0;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const TokenInfo info = bars->info[s % kInfos][c];
+      // (not zero: what is hidden is -inf times it)
+      factor[c] = fmaxf(row_factor * info.factor, 1.17549435e-38f);
+      bits |= (info.bits & 3u) << (2 * c);
+      bf16s |= (info.bits >> 2 & 1u) << c;
+    }
+    const bool masked = __any_sync(0xffffffffu, rel < kKeys - 1) || bits != 0xFFu;
+    bool beyond = false;  // a key behind the query's own position is seen
+    if constexpr (SCORED)
+      beyond = __any_sync(0xffffffffu, slope != 0.0f && min(lim, key0 + kKeys - 1) > pos);
+    uint32_t weights[64];
+    uint64_t step_sum = 0;
+
+    // 32 scores as they are to be multiplied by `f` (SCORED: by one)
+    auto finish = [&](int c, uint32_t (&x)[32]) -> float {
+      float f = factor[c];
+      if constexpr (SCORED) {
+        const uint64_t f2 = f2_pack(f, f);
+        bool capped = false;
+        if (p.cap_log2 > 0.0f) {
+          const float k = f * inv_cap;
+          float big = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 32; i += 2)
+            big = max3(big, fabsf(__uint_as_float(x[i])), fabsf(__uint_as_float(x[i + 1])));
+          capped = true;
+          if (__any_sync(0xffffffffu, !(big * k <= kTanhRange))) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              x[i] = __float_as_uint(p.cap_log2 * tanh_any(__uint_as_float(x[i]) * k));
+          } else {
+            const uint64_t k2 = f2_pack(k, k);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const uint64_t raw = f2_pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+              const uint64_t y = f2_mul(raw, k2), u = f2_mul(y, y);
+              uint64_t a = f2_fma(f2_pack(kTanh5, kTanh5), u, f2_pack(kTanh4, kTanh4));
+              a = f2_fma(a, u, f2_pack(kTanh3, kTanh3));
+              a = f2_fma(a, u, f2_pack(kTanh2, kTanh2));
+              a = f2_fma(a, u, f2_pack(kTanh1, kTanh1));
+              a = f2_fma(a, u, f2_pack(kTanh0, kTanh0));
+              a = f2_mul(a, f2_mul(raw, f2));
+              float lo, hi;
+              f2_unpack(a, lo, hi);
+              x[i] = __float_as_uint(lo), x[i + 1] = __float_as_uint(hi);
+            }
+          }
+        }
+        if (!capped) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
+        }
+        if (p.slopes) {
+          const int d0 = key0 + 32 * c - pos;  // of key 0 from the query
+          if (beyond) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              x[i] = __float_as_uint(
+                  fmaf(-slope, fabsf((float)(d0 + i)), __uint_as_float(x[i])));
+          } else {
+            const float b0 = slope * (float)d0;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              x[i] = __float_as_uint(__uint_as_float(x[i]) + fmaf(slope, (float)i, b0));
+          }
+        }
+        f = 1.0f;
+      }
+      if (masked) {
+        const int last = rel - 32 * c;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          x[i] = i > last || !(bits >> (2 * c + i / 16) & 1u) ? kNegInf : x[i];
+      }
+      return f;
+    };
+    // The step's weights beside the reference, and their sum.
+    auto weigh = [&](float reference) {
+      const uint64_t nm2 = f2_pack(-reference, -reference);
+      step_sum = 0;
+      uint32_t x[2][32];
+      tmem_ld32(tS, x[0]);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t(&now)[32] = x[c & 1];
+        tmem_wait_ld();
+        reg_fence(now, 32);
+        if (c < 3) tmem_ld32(tS + 32 * (c + 1), x[(c + 1) & 1]);
+        const float f = finish(c, now);
+        const uint64_t f2 = f2_pack(f, f);
+        const bool bf = bf16s >> c & 1u;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const uint64_t v = f2_pack(__uint_as_float(now[2 * i]), __uint_as_float(now[2 * i + 1]));
+          float a, b;
+          f2_unpack(SCORED ? f2_add(v, nm2) : f2_fma(v, f2, nm2), a, b);
+          a = ex2_approx(a), b = ex2_approx(b);
+          step_sum = f2_add(step_sum, f2_pack(a, b));
+          weights[16 * c + i] = bf ? pack_bf16x2(a, b) : pack_f16x2(a, b);
+        }
+      }
+    };
+    // A step's weights are formed beside the reference of the steps before; where
+    // their sum shows that scores rose far above it (or there is none yet), again
+    // beside the new maximum.
+    bool again = __any_sync(0xffffffffu, m == -INFINITY);
+    if (!again) {
+      weigh(m);
+      float a, b;
+      f2_unpack(step_sum, a, b);
+      again = __any_sync(0xffffffffu, !(a + b <= kMostSum));  // (NaN too)
+    }
+    if (again) {
+      float top = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t x[32];
+        tmem_ld32(tS + 32 * c, x);
+        tmem_wait_ld();
+        reg_fence(x, 32);
+        const float f = finish(c, x);
+        top = fmaxf(top, largest32(x) * f);
+      }
+      const bool moves = top > m + kLagBits;
+      float f = 1.0f;
+      if (moves) {
+        f = ex2_approx(m - top);  // (0 from no reference)
+        m = top;
+        sum2 = f2_mul(sum2, f2_pack(f, f));
+      }
+      // O is complete: the scores of this step waited for the last step's product
+      if (s > 0 && __any_sync(0xffffffffu, moves)) {
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          tmem_ld32(tO + c, o);
+          tmem_wait_ld();
+          reg_fence(o, 32);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+          tmem_st32_16(tO + c, o);
+          tmem_st32_16(tO + c + 16, o + 16);
+        }
+        tmem_wait_st();
+      }
+      weigh(m == -INFINITY ? 0.0f : m);
+    }
+    sum2 = f2_add(sum2, step_sum);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) tmem_st32_16(tS + 16 * c, weights + 16 * c);
+    tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&bars->p_full[tile]));
+  }
+
+  if (!wait_all(&bars->pv_done[tile], (uint32_t)(steps - 1) & 1u, abort_flag, p)) return;
+  tc_fence_after();
+  float s0, s1;
+  f2_unpack(sum2, s0, s1);
+  const float sum = s0 + s1;
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  float* slot = p.partial + w.slot * (kCtaRows * (D + 2)) + tile * kTileRows + r;
+  const bool partial = p.splits > 1;
+  const int64_t at = ((int64_t)w.b * p.H + w.h * p.G + g) * p.T + t;
+  if (there) {
+    if (partial) {
+      slot[0] = m;
+      slot[kCtaRows] = sum;
+    } else {
+      p.lse[at] = (m + __log2f(sum)) * kLn2;
+    }
+  }
+#pragma unroll 1
+  for (int c = 0; c < D; c += 16) {
+    uint32_t o[16];
+    tmem_ld32_16(tO + c, o);
+    tmem_wait_ld();
+    reg_fence(o, 16);
+    // channels from the codes' order
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int k = i & 7;
+      x[i] = __uint_as_float(o[(i & 8) + (k < 4 ? 2 * k : 2 * k - 7)]) * (partial ? 1.0f : inv);
+    }
+    const int nan_from = bars->nan_from[c / (D / NG)];
+    if (lim >= nan_from) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = __int_as_float(0x7FC00000);
+    }
+    if (there && partial) {
+      float4* dst = reinterpret_cast<float4*>(p.partial + w.slot * (kCtaRows * (D + 2)) +
+                                              2 * kCtaRows + (tile * kTileRows + r) * D + c);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        dst[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+    } else if (there) {
+      write_row<D>(p, at, x, c);
+    }
+  }
+  if (!there) write_nothing<D>(p, w, tile, r);  // behind the count
+}
+
+template <int D, int NG, bool SCORED>
+__global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const ChunkParams p) {
+  using C = ChunkCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;  // swizzled tiles begin at multiples of 1024
+  ChunkBars* bars = reinterpret_cast<ChunkBars*>(smem_raw + (base - raw) + C::kBars);
+  const int warp = threadIdx.x >> 5;
+
+  wait_for_previous_launch();
+  const ChunkWork w = chunk_work(p);
+  if (w.total == 0) {  // (the whole CTA)
+    allow_next_launch();
+    if (threadIdx.x < kCtaRows)
+      write_nothing<D>(p, w, threadIdx.x / kTileRows, threadIdx.x % kTileRows);
+    return;
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(smem_u32(&bars->k_full[i]), 4);
+      mbar_init(smem_u32(&bars->k_empty[i]), 1);
+      mbar_init(smem_u32(&bars->v_full[i]), 4);
+      mbar_init(smem_u32(&bars->v_empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&bars->q_full[i]), 4);
+      mbar_init(smem_u32(&bars->s_full[i]), 1);
+      mbar_init(smem_u32(&bars->p_full[i]), 4);
+      mbar_init(smem_u32(&bars->pv_done[i]), 1);
+    }
+    for (int i = 0; i < kInfos; ++i) mbar_init(smem_u32(&bars->info_full[i]), 4);
+    mbar_init(smem_u32(&bars->drain), 2);
+    for (int i = 0; i < 4; ++i) bars->nan_from[i] = 0x7FFFFFFF;
+    bars->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kWarpScores) {
+    tmem_alloc(smem_u32(&bars->tmem_base), kTmemColumns);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  allow_next_launch();
+  const uint32_t tmem = bars->tmem_base;
+  volatile int* abort_flag = &bars->abort_flag;
+
+  if (warp < kWarpExpand) {
+    regs_inc<kSoftmaxRegs>();
+    run_softmax<D, NG, SCORED>(p, w, bars, tmem, base, abort_flag);
+  } else if (warp < kWarpScores) {
+    regs_dec<kExpandRegs>();
+    run_expand<D, NG>(p, w, bars, base, abort_flag);
+  } else {
+    regs_dec<kIssueRegs>();
+    if (warp == kWarpScores) run_scores<D>(p, w, bars, tmem, base, abort_flag);
+    if (warp == kWarpValues) run_values<D>(p, w, bars, tmem, base, abort_flag);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpScores) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemColumns);
+  }
+}
+
+// A warp a row: joins the splits' results in their order.
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) kv4_chunk_join_kernel(const ChunkParams p) {
+  constexpr int V = D / 32;  // channels a lane
+  wait_for_previous_launch();
+  allow_next_launch();
+  const int lane = threadIdx.x & 31;
+  const int row = blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
+  const int bh = blockIdx.y, b = bh / p.c.Hkv, h = bh - b * p.c.Hkv;
+  int count = p.T;
+  if (p.counts) count = min(max(load(p.counts + b), 0), p.T);
+  if (row >= p.G * count) return;  // (written by the first split)
+  const float* slot = p.partial + ((int64_t)bh * p.items + row / kCtaRows) * p.splits *
+                                      (int64_t)(kCtaRows * (D + 2));
+  const int r = row % kCtaRows;
+  const int64_t next = kCtaRows * (D + 2);
+  float top = -INFINITY;
+  for (int s = 0; s < p.splits; ++s) top = fmaxf(top, __ldcg(slot + s * next + r));
+  float sum = 0.0f, x[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) x[i] = 0.0f;
+  bool seen = false;
+  for (int s = 0; s < p.splits; ++s) {
+    const float m = __ldcg(slot + s * next + r), l = __ldcg(slot + s * next + kCtaRows + r);
+    if (m == -INFINITY && l == 0.0f) continue;  // (nothing was written behind them)
+    seen = true;
+    const float f = ex2_approx(m - top);
+    sum = fmaf(l, f, sum);
+    const float* o = slot + s * next + 2 * kCtaRows + r * D + lane * V;
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = fmaf(__ldcg(o + i), f, x[i]);
+  }
+  const float inv = seen ? 1.0f / sum : 0.0f;
+  const int t = row / p.G, g = row - t * p.G;
+  const int64_t at = ((int64_t)b * p.H + h * p.G + g) * p.T + t;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int64_t to = at * D + lane * V + i;
+    if (p.out_f32)
+      static_cast<float*>(p.out)[to] = x[i] * inv;
+    else
+      static_cast<__nv_bfloat16*>(p.out)[to] = __float2bfloat16_rn(x[i] * inv);
+  }
+  if (lane == 0) p.lse[at] = seen ? (top + __log2f(sum)) * kLn2 : -INFINITY;
+}
+
+// How many ranges the tokens of a row tile are cut into, by sizes that the host
+// knows: waves of CTAs times the steps of each, a CTA's start counted as kStart
+// steps and the join as kJoin.
+constexpr int kMostSplits = 64;
+constexpr double kStart = 3.0, kJoin = 4.0;
+int chunk_splits(int64_t ctas, int64_t steps, int sms) {
+  int best = 1;
+  double least = 0.0;
+  for (int n = 1; n <= kMostSplits && n <= steps; ++n) {
+    const double waves = (double)((ctas * n + sms - 1) / sms);
+    const double cost = waves * ((double)((steps + n - 1) / n) + kStart) + (n > 1 ? kJoin : 0.0);
+    if (n == 1 || cost < least) best = n, least = cost;
+    if (ctas * n > 8 * (int64_t)sms) break;
+  }
+  return best;
+}
+
+struct ChunkSplit {
+  int64_t items, ctas;
+  int splits;
+  size_t workspace;
+};
+ChunkSplit chunk_split(int B, int kv_heads, int64_t rows, int64_t tokens, int D, int sms) {
+  ChunkSplit s{};
+  s.items = (rows + kCtaRows - 1) / kCtaRows;
+  const int64_t tiles = s.items * B * kv_heads;
+  s.splits = chunk_splits(tiles, (tokens + kKeys - 1) / kKeys, sms);
+  s.ctas = tiles * s.splits;
+  if (s.splits > 1) s.workspace = (size_t)s.ctas * kCtaRows * (D + 2) * sizeof(float);
+  return s;
+}
+
+template <int D, int NG>
+cudaError_t launch_chunk(const ChunkParams& p, bool scored, int64_t ctas, cudaStream_t st) {
+  using C = ChunkCfg<D>;
+  cudaError_t e;
+  if (scored) {
+    constexpr auto kernel = kv4_chunk_kernel<D, NG, true>;
+    e = allow_shared_memory<kernel>(C::kSmem);
+    if (e != cudaSuccess) return e;
+    e = launch_dependent(kernel, dim3((unsigned)ctas), dim3(kChunkThreads), C::kSmem, st, p);
+  } else {
+    constexpr auto kernel = kv4_chunk_kernel<D, NG, false>;
+    e = allow_shared_memory<kernel>(C::kSmem);
+    if (e != cudaSuccess) return e;
+    e = launch_dependent(kernel, dim3((unsigned)ctas), dim3(kChunkThreads), C::kSmem, st, p);
+  }
+  if (e != cudaSuccess || p.splits == 1) return e;
+  const int64_t rows = (int64_t)p.G * p.T;
+  return launch_dependent(kv4_chunk_join_kernel<D>,
+                          dim3((unsigned)((rows + kJoinWarps - 1) / kJoinWarps), p.B * p.c.Hkv),
+                          dim3(kJoinWarps * 32), 0, st, p);
+}
+
+}  // namespace
+}  // namespace bsattn
+
+using namespace bsattn;
+
+extern "C" {
+
+size_t bsattn_kv4_attn_chunk_workspace(int B, int H, int kv_heads, int T, int D, int page_size,
+                                       int columns) {
+  if (B <= 0 || H <= 0 || kv_heads <= 0 || T <= 0 || H % kv_heads != 0 || page_size <= 0 ||
+      columns <= 0)
+    return 0;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  return chunk_split(B, kv_heads, (int64_t)(H / kv_heads) * T, (int64_t)columns * page_size, D,
+                     device_sm_count(dev))
+      .workspace;
+}
+
+bsattn_status bsattn_kv4_attn_chunk(const bsattn_kv4_cache* cache, const void* q, int B, int H,
+                                    int T, const int32_t* block_table, int64_t table_stride,
+                                    int columns, const int32_t* lengths, const int32_t* counts,
+                                    const int32_t* prefix, float scale, float cap,
+                                    const float* slopes, unsigned flags, void* out, float* lse,
+                                    void* workspace, size_t workspace_bytes, void* stream) {
+  ChunkParams p{};
+  const bsattn_status rc = check_cache(cache, &p.c);
+  if (rc != BSATTN_OK) return rc;
+  if (!q || !out || !lse || !aligned16(q) || !aligned16(out) || !aligned16(lse) ||
+      !aligned16(workspace))
+    return BSATTN_ERR_INVALID_ARG;
+  if (!block_table || !lengths ||
+      ((reinterpret_cast<uintptr_t>(block_table) | reinterpret_cast<uintptr_t>(lengths) |
+        reinterpret_cast<uintptr_t>(counts) | reinterpret_cast<uintptr_t>(prefix) |
+        reinterpret_cast<uintptr_t>(slopes)) & 3u))
+    return BSATTN_ERR_INVALID_ARG;
+  if (B <= 0 || H <= 0 || T <= 0 || columns <= 0 || table_stride < 0 || H % cache->kv_heads != 0)
+    return BSATTN_ERR_INVALID_ARG;
+  if (flags & ~(unsigned)BSATTN_OUT_F32) return BSATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || !std::isfinite(cap) || cap < 0.0f) return BSATTN_ERR_INVALID_ARG;
+  // (a cap that underflows in the kernel's units would cap nothing)
+  if (cap > 0.0f && (cap < 1e-30f || cap > 1e30f)) return BSATTN_ERR_UNSUPPORTED;
+  const int64_t rows = (int64_t)(H / cache->kv_heads) * T;
+  if (B > 65535 || rows > (1 << 30) || (int64_t)B * cache->kv_heads > 65535 ||
+      (int64_t)columns * cache->page_size > (1ll << 31) - 2 * kKeys ||  // positions are 32-bit
+      (int64_t)cache->pages * cache->kv_heads * cache->page_size / 16 >= (1ll << 31))
+    return BSATTN_ERR_UNSUPPORTED;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return BSATTN_ERR_CUDA;
+  const ChunkSplit split =
+      chunk_split(B, cache->kv_heads, rows, (int64_t)columns * cache->page_size, cache->head_dim,
+                  device_sm_count(dev));
+  if (split.ctas >= (1ll << 31)) return BSATTN_ERR_UNSUPPORTED;
+  if (split.workspace > 0 && (!workspace || workspace_bytes < split.workspace))
+    return BSATTN_ERR_INVALID_ARG;
+  p.q = static_cast<const uint16_t*>(q);
+  p.table = block_table;
+  p.table_stride = table_stride;
+  p.columns = columns;
+  p.lengths = lengths;
+  p.counts = counts;
+  p.prefix = prefix;
+  p.slopes = slopes;
+  p.B = B;
+  p.H = H;
+  p.T = T;
+  p.G = H / cache->kv_heads;
+  p.items = (int)split.items;
+  p.splits = split.splits;
+  p.scale_log2 = (float)(std::fabs((double)scale) * 1.4426950408889634074);
+  p.sign = scale < 0.0f ? -1.0f : 1.0f;
+  p.cap_log2 = (float)((double)cap * 1.4426950408889634074);
+  p.out = out;
+  p.lse = lse;
+  p.out_f32 = (flags & BSATTN_OUT_F32) ? 1 : 0;
+  p.partial = static_cast<float*>(workspace);
+  p.timeout_ns = kDefaultWaitTimeoutNs;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool scored = cap > 0.0f || slopes;
+  const int groups = cache->head_dim / cache->group;
+  cudaError_t e;
+  if (cache->head_dim == 64)
+    e = groups == 1 ? launch_chunk<64, 1>(p, scored, split.ctas, st)
+                    : launch_chunk<64, 2>(p, scored, split.ctas, st);
+  else
+    e = groups == 1   ? launch_chunk<128, 1>(p, scored, split.ctas, st)
+        : groups == 2 ? launch_chunk<128, 2>(p, scored, split.ctas, st)
+                      : launch_chunk<128, 4>(p, scored, split.ctas, st);
+  return from_cuda(e);
+}
+
+}  // extern "C"

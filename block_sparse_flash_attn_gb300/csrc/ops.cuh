@@ -1,5 +1,5 @@
 // Small device helpers shared by the operators around the attention kernels
-// (rope.cu, select.cu, kv4.cu, kv4_attn.cu): bf16 packing, launches, pairs of
+// (rope.cu, select.cu, kv4.cu, kv4_attn.cu, kv4_chunk.cu, kv4_pages.cu): bf16 packing, launches, pairs of
 // floats, exact sums, block floating point, threshold search, matrix products.
 #pragma once
 
@@ -137,6 +137,12 @@ inline cudaError_t launch_dependent_clusters(void (*kernel)(KArgs...), dim3 grid
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, KArgs(args)...);
+}
+
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile(
+      "barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+          : "memory");
 }
 
 // ---------------------------------------------------------------------------

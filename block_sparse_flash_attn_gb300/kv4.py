@@ -5,6 +5,7 @@
     lengths += k.shape[2]
     pages = bsattn.kv4_select(cache, q, block_table, lengths, keep=64)  # optional
     o, lse = bsattn.kv4_attn(cache, q, block_table, lengths, pages)
+    o, lse = bsattn.kv4_attn_chunk(cache, q, block_table, lengths, counts)  # any number of new tokens
     bsattn.kv4_status(cache)                                   # raises if a table named a bad page
     k, v = bsattn.kv4_read(cache, block_table, start, tokens)  # cached tokens as bf16
 """
@@ -75,6 +76,11 @@ class Kv4Cache:
 @functools.lru_cache(maxsize=256)
 def _attn_workspace(device, *sizes):  # a function of the sizes and the (current) device
     return _bs.load().bsattn_kv4_attn_workspace(*sizes)
+
+
+@functools.lru_cache(maxsize=256)
+def _chunk_workspace(device, *sizes):
+    return _bs.load().bsattn_kv4_attn_chunk_workspace(*sizes)
 
 
 @functools.lru_cache(maxsize=256)
@@ -227,6 +233,54 @@ def kv4_attn(cache: Kv4Cache, q: torch.Tensor, block_table: torch.Tensor, length
                 lengths.data_ptr(), pointer(selected), n_selected, float(scale),
                 _bs.OUT_F32 if out_f32 else 0, out.data_ptr(), lse.data_ptr(), pointer(ws),
                 nbytes, on), "bsattn_kv4_attn")
+    return out, lse
+
+
+def kv4_attn_chunk(cache: Kv4Cache, q: torch.Tensor, block_table: torch.Tensor,
+                   lengths: torch.Tensor, counts: torch.Tensor | None = None,
+                   prefix: torch.Tensor | None = None, cap: float | None = None,
+                   slopes: torch.Tensor | None = None, scale: float | None = None,
+                   out_f32: bool = False, out: torch.Tensor | None = None,
+                   lse: torch.Tensor | None = None, stream=None):
+    """O [B, H, T, head_dim] (bf16, or fp32 with out_f32), LSE fp32 [B, H, T] of a chunk of
+    new tokens against the cache: single tokens, drafts, prompts, parts of prompts.
+
+    q: CUDA bf16 [B, H, T, head_dim]; query t < counts[b] (default T) sits at position
+    lengths[b] - counts[b] + t (lengths counts the new tokens too) and sees the cached
+    tokens up to there, and those at positions below prefix[b].  A query behind the
+    count has O = 0, LSE = -inf.  counts, prefix: int32 [B].
+    cap: scores become cap * tanh(score / cap).  slopes: fp32 [H]; slopes[h] times the
+    distance of query and key is taken off the (capped) scores.  scale: default
+    1/sqrt(head_dim)."""
+    _cache(cache)
+    B, stride, columns = _table(cache, block_table, lengths, counts)
+    tensor("q", q, (_BF16,), device=cache.device)
+    if q.dim() != 4 or q.shape[0] != B or q.shape[3] != cache.head_dim or not q.shape[1] \
+            or q.shape[1] % cache.kv_heads:
+        raise ValueError("q must be [B, H, T, head_dim] with H a multiple of the cache's kv_heads")
+    H, T = q.shape[1:3]
+    if prefix is not None:
+        tensor("prefix", prefix, (_I32,), (B,), cache.device)
+    if slopes is not None:
+        tensor("slopes", slopes, (torch.float32,), (H,), cache.device)
+    if cap is not None and not cap > 0.0:
+        raise ValueError("cap must be positive")
+    if scale is None:
+        scale = 1.0 / math.sqrt(cache.head_dim)
+    odt = torch.float32 if out_f32 else _BF16
+    with launch_on(cache.device, stream) as on:
+        out = output("out", out, odt, q.shape, cache.device)
+        lse = output("lse", lse, torch.float32, q.shape[:3], cache.device)
+        if B * T:
+            nbytes = _chunk_workspace(cache.device.index, B, H, cache.kv_heads, T, cache.head_dim,
+                                      cache.page_size, columns)
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=cache.device) if nbytes else None
+            _bs._check(_bs.load().bsattn_kv4_attn_chunk(
+                cache._ref, q.data_ptr(), B, H, T, block_table.data_ptr(), stride, columns,
+                lengths.data_ptr(), pointer(counts), pointer(prefix), float(scale),
+                0.0 if cap is None else float(cap), pointer(slopes),
+                _bs.OUT_F32 if out_f32 else 0, out.data_ptr(), lse.data_ptr(), pointer(ws), nbytes,
+                on), "bsattn_kv4_attn_chunk")
     return out, lse
 
 

@@ -595,7 +595,103 @@ bsattn_status bsattn_kv4_attn(const bsattn_kv4_cache* cache, const void* q, int 
                               float scale, unsigned flags, void* out, float* lse, void* workspace,
                               size_t workspace_bytes, void* stream);
 
-/* Wait for `stream`, then report and clear the cache's status word: OK or PAGE
+/*
+ * bsattn_kv4_attn_chunk -- O, LSE of a chunk of new tokens a sequence against the
+ * cache: one token to whole prompts, with anything cached before them.
+ *
+ * Query t < counts[b] of a sequence of length n sits at i = n - counts[b] + t and
+ * sees the cached tokens j < n with j <= i or j < prefix[b]:
+ *   x_j = scale q.k_j;  x_j = cap tanh(x_j / cap);  x_j -= slopes[head] |i - j|;
+ *   O = softmax(x) V;  LSE = ln sum exp(x_j).
+ * A query that sees none, or lies behind the count (t >= counts[b]), gets O = 0,
+ * LSE = -inf.
+ *   q          device bf16 [B][H][T][head_dim], 16-byte aligned, entries below 2^100 in
+ *              magnitude (one that is not finite spoils its own query only); query head
+ *              h reads key/value head h / (H / kv_heads).  B * kv_heads at most 65535,
+ *              H / kv_heads * T at most 2^30, columns * page_size at most 2^31 - 256.
+ *   cache      values below 2^104 in magnitude, |scale| sum |q k| of a query and a key
+ *              below 2^112.  Scores are as good as 32-bit products; a key's channels
+ *              below 2^-22 of the largest key of 32 tokens (positions 32 i to 32 i + 31)
+ *              count with fewer bits.  Values are rounded to fp16 where those of 32
+ *              tokens fit it (the largest of each group of channels up to 2^15, and zero
+ *              or at least 2^-4), else to bf16; weights to the same type.
+ *   lengths    cached tokens, the new ones included.
+ *   counts     new tokens of each sequence, or null: T.
+ *   prefix     device int32 [B]: positions below it are seen by every query; or null.
+ *   scale      finite.  cap: 0 (none), or 1e-30 to 1e30.
+ *   slopes     device fp32 [H], or null.
+ *   flags, out, lse  as bsattn_kv4_attn.
+ *   workspace  bsattn_kv4_attn_chunk_workspace bytes (may be none), 16-byte aligned.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA.  A wait inside the kernel that runs out (2 s)
+ * is reported by bsattn_kv4_status as TIMEOUT.
+ */
+size_t bsattn_kv4_attn_chunk_workspace(int B, int H, int kv_heads, int T, int D, int page_size,
+                                       int columns);
+bsattn_status bsattn_kv4_attn_chunk(const bsattn_kv4_cache* cache, const void* q, int B, int H,
+                                    int T, const int32_t* block_table, int64_t table_stride,
+                                    int columns, const int32_t* lengths, const int32_t* counts,
+                                    const int32_t* prefix, float scale, float cap,
+                                    const float* slopes, unsigned flags, void* out, float* lse,
+                                    void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The pages of a cache.
+ *
+ *   refs       device int32 [pages]: the rows of the block table that hold a page (as far
+ *              as their lengths reach).  A page that none holds is free.
+ * A page that is not full belongs to one row.  What is given out is the lowest free
+ * page, rows in ascending order and in each its columns.  Where there are too few, the
+ * last ones get -1 and bsattn_kv4_status reports it, as it does bad pages and lengths
+ * behind the table.  new_* receive the books after the call; `refs` may be updated in
+ * place (new_refs = refs), and so may the table where that is said.  At most 16384 rows.
+ *
+ * bsattn_kv4_copy -- page src[i] of `from` to page dst[i] of `to` (one cache, or two of the
+ * same sizes): codes, scales, means.  A pair with a negative page is no move.  A page
+ * must not be written twice in one call, nor be read where it is written.
+ *
+ * bsattn_kv4_fork -- new row i continues row parents[i] of the old table: several rows
+ * may continue one (samples, beams), rows may change places, and rows that none
+ * continues end.  Row i is empty where parents[i] is negative.  Full pages are shared;
+ * of a last page that is not full the first child keeps the parent's, the others get
+ * copies of the tokens in it.  Pages of rows that end are free for those copies.
+ *   block_table, lengths [B]  the old rows, all that refs counts.
+ *   new_table  device int32 [n][columns], -1 behind a row's pages; not the old one.
+ *   new_lengths, new_refs  device int32 [n], [pages]; new_refs 16-byte aligned.
+ *   workspace  bsattn_kv4_fork_workspace bytes, 16-byte aligned.
+ *
+ * bsattn_kv4_reserve -- pages for counts[b] (null: T) more tokens of every row: columns
+ * ceil(lengths / page_size) up to ceil((lengths + counts) / page_size) - 1 get one each,
+ * whatever they held.  The table may be updated in place (new_table = block_table).
+ *   new_table  device int32 [B][columns], rows new_stride apart; new_refs 16-byte aligned.
+ *
+ * bsattn_kv4_compact -- with n pages in use, those at n and above move to the free ones
+ * below n, both in ascending order.  The table may be updated in place.
+ *   new_table  as for reserve: every entry's new page (negative ones as they were).
+ *   page_map   device int32 [pages]: the new place of each page, -1 for a free one.
+ *   workspace  bsattn_kv4_compact_workspace bytes, 16-byte aligned.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA.
+ */
+bsattn_status bsattn_kv4_copy(const bsattn_kv4_cache* from, const bsattn_kv4_cache* to,
+                              const int32_t* src, const int32_t* dst, int n, void* stream);
+size_t bsattn_kv4_fork_workspace(int n);
+bsattn_status bsattn_kv4_fork(const bsattn_kv4_cache* cache, const int32_t* refs,
+                              const int32_t* block_table, int64_t table_stride, int columns,
+                              const int32_t* lengths, int B, const int32_t* parents, int n,
+                              int32_t* new_table, int32_t* new_lengths, int32_t* new_refs,
+                              void* workspace, size_t workspace_bytes, void* stream);
+bsattn_status bsattn_kv4_reserve(const bsattn_kv4_cache* cache, const int32_t* refs,
+                                 const int32_t* block_table, int64_t table_stride, int columns,
+                                 const int32_t* lengths, const int32_t* counts, int T, int B,
+                                 int32_t* new_table, int64_t new_stride, int32_t* new_refs,
+                                 void* stream);
+size_t bsattn_kv4_compact_workspace(int pages);
+bsattn_status bsattn_kv4_compact(const bsattn_kv4_cache* cache, const int32_t* refs,
+                                 const int32_t* block_table, int64_t table_stride, int columns,
+                                 int B, int32_t* new_table, int64_t new_stride, int32_t* new_refs,
+                                 int32_t* page_map, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+
+/* Wait for `stream`, then report and clear the cache's status word: OK, PAGE or TIMEOUT
    (CUDA if the wait failed).  What calls on other streams report meanwhile is in
    this answer or in the next one's. */
 bsattn_status bsattn_kv4_status(const bsattn_kv4_cache* cache, void* stream);

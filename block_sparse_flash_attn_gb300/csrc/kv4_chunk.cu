@@ -15,25 +15,30 @@
 // a tile ends where its last token does), and expands each tile of 128 tokens
 // once for all of them, to operands of tcgen05 in shared memory:
 //
+// - A code in bits 0-3 or 4-7 of an fp16 is a subnormal number; so a mask and one fused
+//   multiply-add with a power of two more take two codes to two operands.
 // - K without a rounding that counts.  An fp16 holds step (code - 8) exactly (8 bits
 //   times 3), and the rest of a key is one number a group, c = least + 8 step:
 //     q . k = sum_d q_d step (code_d - 8) + sum_groups c sum_d q_d.
 //   The second sum is one more 16-channel step of the same product: c and the sums
 //   of q are split into two fp16 each, (q hi, q lo, q hi) beside (c hi, c hi, c lo),
 //   off by 2^-22 of a product.  Queries are bf16, exact in fp16 beside their
-//   row's largest; keys are taken beside the largest of 32 tokens (what is 2^-22 of
+//   row's largest; keys are taken beside the largest of 32 tokens (what is 2^-17 of
 //   it and less loses bits); both are powers of two that the softmax puts back.  So
 //   scores and lse are those of 32-bit products, at the cost of a ninth step for 8.
-// - V in fp16, rounded once (2^-11), where all values of 32 tokens lie in its range
-//   (groups of up to 2^15, and of 2^-4 at least or zero), else in bf16 (2^-8); the weights
-//   in the same type.  Weights are off by that rounding, or by 2^-25 of a number that
-//   the row's largest weight is at least 2^-8 of.
+// - V in fp16, rounded once (2^-11), beside a power of two that the CTA takes from its
+//   first step: the mean exponent of its groups of channels goes to 2^-10.  Where a
+//   group of 32 tokens passes 2^-6 there, or 2^-14 the other way, those tokens are taken
+//   in bf16 (2^-8), their weights too.  Weights are off by that rounding, or by 2^-25 of
+//   a number that the row's largest weight is at least 2^-8 of.
 //
-// Work of a CTA (512 threads, one CTA an SM, 211 KB of shared memory):
-//   warps 0-3, 4-7   softmax of the first and the second 128 rows: a thread a row
-//   warps 8-11       the codes' expansion, 32 tokens a warp
-//   warp 12          issues S = Q K^T, owns the tensor memory
-//   warp 13          issues O += P V
+// Work of a CTA (896 threads, one CTA an SM, 211 KB of shared memory):
+//   warps 0-7, 8-15   softmax of the first and the second 128 rows: 16 rows a warp, two
+//                     threads a row, a half of the tokens and of the channels each
+//   warps 16-19       the keys' expansion, 32 tokens a warp
+//   warps 20-23       the values'
+//   warps 24, 25      issue S = Q K^T of a row tile each; 24 owns the tensor memory
+//   warps 26, 27      issue O += P V
 // Tensor memory: S of both row tiles (128 columns each; the weights replace the
 // scores they come from) and O of both.  While one tile's softmax runs, the tensor
 // core works for the other.
@@ -43,6 +48,7 @@
 // Every wait is bounded; a wait that runs out is reported by bsattn_kv4_status.
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda_fp16.h>
 
@@ -52,15 +58,16 @@
 namespace bsattn {
 namespace {
 
-constexpr int kChunkThreads = 512;
+constexpr int kChunkThreads = 896;
+constexpr int kSoftmaxWarps = 8;            // a row tile
 constexpr int kTileRows = 128;              // rows of a softmax tile: lanes of tensor memory
 constexpr int kCtaRows = 2 * kTileRows;
 constexpr int kKeys = 128;                  // tokens a step
 constexpr int kStages = 2;                  // of the expanded K and V
 constexpr int kInfos = 4;                   // steps whose ChunkInfo is kept
-constexpr int kWarpExpand = 8, kWarpScores = 12, kWarpValues = 13;
-// 256 x 184 + 128 x 96 + 128 x 48 = 512 x 128 registers
-constexpr int kSoftmaxRegs = 184, kExpandRegs = 96, kIssueRegs = 48;
+constexpr int kWarpK = 16, kWarpV = 20, kWarpScores = 24, kWarpValues = 26;
+// 512 x 88 + 256 x 64 + 128 x 24 = 896 x 72 registers
+constexpr int kSoftmaxRegs = 88, kExpandRegs = 64, kIssueRegs = 24;
 constexpr uint32_t kTmemColumns = 512;
 constexpr float kLagBits = 8.0f;            // a row's reference may lie 2^8 below its maximum
 constexpr float kMostSum = 32768.0f;        // of a step's weights: each then fits fp16
@@ -92,20 +99,25 @@ struct ChunkParams {
 
 // What the softmax needs of 32 tokens of a step.
 struct TokenInfo {
-  float factor;   // the keys' power of two
-  uint32_t bits;  // 0, 1: the first, the second 16 tokens are there; 2: V is bf16
+  float factor;     // the keys' power of two
+  uint32_t there;   // bits 0, 1: the first, the second 16 tokens are there
+  uint32_t v_bf16;  // the values' type
+  uint32_t unused;
 };
 
 struct __align__(16) ChunkBars {
   uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
   uint64_t q_full[2], s_full[2], p_full[2], pv_done[2];
+  uint64_t turn[2];  // the other row tile's softmax of a step is over
   // (a step's slot is taken again four steps on: two steps after its scores were read)
   uint64_t info_full[kInfos];
-  uint64_t drain;
+  uint64_t drain[4];
   TokenInfo info[kInfos][4];
   int nan_from[4];  // by group of channels: the first token whose values are not numbers
   uint32_t tmem_base;
   int abort_flag;
+  float v_scale;      // what O is multiplied by
+  int v_exponents[4][2];  // of each V warp's first step: sum, number
   int query_shift[kCtaRows];
 };
 
@@ -204,32 +216,39 @@ __device__ __forceinline__ bool wait_all(const uint64_t* bar, uint32_t parity,
   return __all_sync(0xffffffffu, ok);
 }
 
+// Both barriers, odd lanes the second.
+__device__ __forceinline__ bool wait_both(const uint64_t* a, uint32_t parity_a, const uint64_t* b,
+                                          uint32_t parity_b, volatile int* abort_flag,
+                                          const ChunkParams& p) {
+  const bool second = threadIdx.x & 1;
+  return wait_all(second ? b : a, second ? parity_b : parity_a, abort_flag, p);
+}
+
 // Waits, with a limit of its own, for all products that this warp issued.
-__device__ __forceinline__ void drain(ChunkBars* bars) {
-  if (elect_one()) mma_commit(smem_u32(&bars->drain));
+__device__ __forceinline__ void drain(uint64_t* bar) {
+  if (elect_one()) mma_commit(smem_u32(bar));
   __syncwarp();
   const uint64_t t0 = globaltimer_ns();
-  while (!mbar_try_wait(smem_u32(&bars->drain), 0)) {
+  while (!mbar_try_wait(smem_u32(bar), 0)) {
     if (globaltimer_ns() - t0 > kDrainLimitNs) return;
   }
 }
 
 // ---------------------------------------------------------------------------
-// warps 8-11: codes to operands
+// warps 16-23: codes to operands
 // ---------------------------------------------------------------------------
-// A word of eight codes as four pairs of fp16 (codes 0 and 4, 1 and 5, ...): the
-// codes are put into the mantissas of 1024 and 64, and `off` takes those away.
-__device__ __forceinline__ void open_codes(uint32_t w, __half2 off1024, __half2 off64,
-                                           __half2 (&x)[4]) {
-  const uint32_t y = w >> 8;
-  const uint32_t n[4] = {(w & 0x000F000Fu) | 0x64006400u, (w & 0x00F000F0u) | 0x54005400u,
-                         (y & 0x000F000Fu) | 0x64006400u, (y & 0x00F000F0u) | 0x54005400u};
-  x[0] = __hadd2(*reinterpret_cast<const __half2*>(&n[0]), off1024);
-  x[1] = __hadd2(*reinterpret_cast<const __half2*>(&n[1]), off64);
-  x[2] = __hadd2(*reinterpret_cast<const __half2*>(&n[2]), off1024);
-  x[3] = __hadd2(*reinterpret_cast<const __half2*>(&n[3]), off64);
-}
 __device__ __forceinline__ uint32_t half_bits(__half2 x) { return *reinterpret_cast<uint32_t*>(&x); }
+__device__ __forceinline__ __half2 half2_of(uint32_t x) { return *reinterpret_cast<__half2*>(&x); }
+// The eight codes of a word times a step and plus a number, as four pairs of fp16 (codes
+// 0 and 4, 1 and 5, ...): low = 2^24 step, high = 2^20 step.
+__device__ __forceinline__ void expand_codes(uint32_t w, __half2 low, __half2 high, __half2 plus,
+                                             uint32_t (&x)[4]) {
+  const uint32_t y = w >> 8;
+  x[0] = half_bits(__hfma2(half2_of(w & 0x000F000Fu), low, plus));
+  x[1] = half_bits(__hfma2(half2_of(w & 0x00F000F0u), high, plus));
+  x[2] = half_bits(__hfma2(half2_of(y & 0x000F000Fu), low, plus));
+  x[3] = half_bits(__hfma2(half2_of(y & 0x00F000F0u), high, plus));
+}
 __device__ __forceinline__ uint32_t half_pair(__half lo, __half hi) {
   return half_bits(__halves2half2(lo, hi));
 }
@@ -249,297 +268,357 @@ struct Scales {
   }
 };
 
+// What a warp of either kind needs to expand its 32 tokens of a step.
 template <int D, int NG>
-__device__ void run_expand(const ChunkParams& p, const ChunkWork& w, ChunkBars* bars,
-                           uint32_t base, volatile int* abort_flag) {
+struct Expander {
   using C = ChunkCfg<D>;
-  constexpr int LR = D / 32;           // lanes a row: 16 bytes, 32 codes each
-  constexpr int RL = 32 / LR;          // rows a load
-  constexpr int NL = 32 / RL;          // loads a warp and step
-  constexpr int GL = D / NG / 32;      // lanes a group
-  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - kWarpExpand;
-  const int piece = lane % LR, group = piece / GL;
-  const int* table = p.table + w.b * p.table_stride;
-  const uint4* k_codes = reinterpret_cast<const uint4*>(p.c.k_codes);
-  const uint4* v_codes = reinterpret_cast<const uint4*>(p.c.v_codes);
-  const uint32_t* k_scales = reinterpret_cast<const uint32_t*>(p.c.k_scales);
-  const uint32_t* v_scales = reinterpret_cast<const uint32_t*>(p.c.v_scales);
+  static constexpr int LR = D / 32;       // lanes a row: 16 bytes, 32 codes each
+  static constexpr int RL = 32 / LR;      // rows a load
+  static constexpr int NL = 32 / RL;      // loads a warp and step
+  static constexpr int GL = D / NG / 32;  // lanes a group
+  const ChunkParams& p;
+  const ChunkWork& w;
+  const uint4* codes;
+  const uint32_t* scales;
+  int lane, warp, turned;
+  uint32_t at[2];     // where pieces 0 and 1 go; 2 and 3: 64 bytes the other way
+  uint4 word[NL];
+  uint32_t scale[NL];
 
+  __device__ __forceinline__ Expander(const ChunkParams& pp, const ChunkWork& ww, bool keys)
+      : p(pp), w(ww), lane(threadIdx.x & 31), warp((threadIdx.x >> 5) & 3) {
+    codes = reinterpret_cast<const uint4*>(keys ? p.c.k_codes : p.c.v_codes) + lane % LR;
+    scales = reinterpret_cast<const uint32_t*>(keys ? p.c.k_scales : p.c.v_scales) + lane % LR / GL;
+    // A row's 32 codes are four 16-byte pieces of its tile; lanes of the second box
+    // begin with the other two, so that the eight lanes of a store meet 32 banks.
+    turned = D == 128 ? lane & 2 : 0;
+    const int row = warp * 32 + lane / LR;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      at[i] = (D == 128 ? (uint32_t)(lane % LR >> 1) * C::kBoxBytes : 0u) + row * 128 +
+              ((4 * (lane & 1) + (i ^ turned) ^ (row & 7)) << 4);
+  }
   // Lanes 0 and 1: where the first and the second 16 of the warp's tokens of step s
   // are, in units of 16 rows; -1: nowhere.
-  auto look_up = [&](int s) -> int {
+  __device__ __forceinline__ int look_up(int s) const {
     if (lane > 1 || s >= w.total) return -1;
     const int pos = (w.j0 + s) * kKeys + warp * 32 + lane * 16;
     if (pos >= w.keys) return -1;
-    const int pg = page_at(p.c, table, p.columns, pos >> p.c.log_page);
+    const int pg = page_at(p.c, p.table + w.b * p.table_stride, p.columns, pos >> p.c.log_page);
     return pg < 0 ? -1 : (int)(p.c.row(pg, w.h, pos & (p.c.page - 1)) >> 4);
-  };
+  }
   // the row of the warp's token t of step s; -1 where there is none
-  auto row_of = [&](int where, int s, int t) -> int64_t {
+  __device__ __forceinline__ int64_t row_of(int where, int s, int t) const {
     const int r16 = __shfl_sync(0xffffffffu, where, t >> 4);
     const int pos = (w.j0 + s) * kKeys + warp * 32 + t;
     return r16 < 0 || pos >= w.keys ? -1 : (int64_t)r16 * 16 + (t & 15);
-  };
-  uint4 kc[NL], vc[NL];
-  uint32_t ks[NL], vs[NL], sums[NG];  // (sums: the scales of token `lane`'s keys)
-  auto load_k = [&](int where, int s) {
-#pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      const int64_t row = row_of(where, s, i * RL + lane / LR);
-      kc[i] = make_uint4(0, 0, 0, 0);
-      ks[i] = 0;
-      if (row >= 0) {
-        kc[i] = load(k_codes + row * LR + piece);
-        ks[i] = load(k_scales + row * NG + group);
-      }
-    }
-    const int64_t row = row_of(where, s, lane);
-#pragma unroll
-    for (int g = 0; g < NG; ++g) sums[g] = row >= 0 ? load(k_scales + row * NG + g) : 0u;
-  };
-  auto load_v = [&](int where, int s) {
-#pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      const int64_t row = row_of(where, s, i * RL + lane / LR);
-      vc[i] = make_uint4(0, 0, 0, 0);
-      vs[i] = 0;
-      if (row >= 0) {
-        vc[i] = load(v_codes + row * LR + piece);
-        vs[i] = load(v_scales + row * NG + group);
-      }
-    }
-  };
-
-  // A row's 32 codes are four 16-byte pieces of its tile; lanes of the second box
-  // begin with the other two, so that the eight lanes of a store meet 32 banks.
-  const int turned = D == 128 ? lane & 2 : 0;
-  auto word_of = [&](const uint4& v, int i) -> uint32_t {
-    const uint32_t a = i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
-    const uint32_t b = i == 0 ? v.z : i == 1 ? v.w : i == 2 ? v.x : v.y;
-    return turned ? b : a;
-  };
-  const int row_in = warp * 32 + lane / LR;
-  uint32_t piece_at[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int c = 4 * (lane & 1) + (i ^ turned);  // of the box's eight
-    piece_at[i] = (D == 128 ? (uint32_t)(piece >> 1) * C::kBoxBytes : 0u) + row_in * 128 +
-                  ((c ^ (row_in & 7)) << 4);
   }
+  __device__ __forceinline__ void load_step(int where, int s) {
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      const int64_t row = row_of(where, s, i * RL + lane / LR);
+      word[i] = make_uint4(0, 0, 0, 0);
+      scale[i] = 0;
+      if (row >= 0) {
+        word[i] = load(codes + row * LR);
+        scale[i] = load(scales + row * NG);
+      }
+    }
+  }
+  // f(x, piece's place) for the four words of load i: turned, the other two first
+  template <typename F>
+  __device__ __forceinline__ void each(int i, uint32_t tile, F f) const {
+    const uint4 v = word[i];
+    const uint32_t n[4] = {turned ? v.z : v.x, turned ? v.w : v.y, turned ? v.x : v.z,
+                           turned ? v.y : v.w};
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      f(n[c], tile + ((c & 2 ? at[c & 1] ^ 32u : at[c & 1]) + i * (RL * 128)));
+  }
+};
 
-  int where = look_up(0), next = look_up(1);
-  load_k(where, 0);
-  load_v(where, 0);
-  const __half2 k1024 = __float2half2_rn(-1032.0f), k64 = __float2half2_rn(-72.0f);
-  const __half2 v1024 = __float2half2_rn(-1024.0f), v64 = __float2half2_rn(-64.0f);
+template <int D, int NG>
+__device__ void run_expand_keys(const ChunkParams& p, const ChunkWork& w, ChunkBars* bars, uint32_t base,
+                         volatile int* abort_flag) {
+  using C = ChunkCfg<D>;
+  using E = Expander<D, NG>;
+  E e(p, w, true);
+  const int lane = e.lane, warp = e.warp;
+  uint32_t sums[NG];  // the scales of token `lane`
+  auto load_sums = [&](int where, int s) {
+    const int64_t row = e.row_of(where, s, lane);
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+      sums[g] = row >= 0 ? load(reinterpret_cast<const uint32_t*>(p.c.k_scales) + row * NG + g) : 0u;
+  };
+  int where = e.look_up(0), next = e.look_up(1);
+  e.load_step(where, 0);
+  load_sums(where, 0);
+#pragma unroll 1
   for (int s = 0; s < w.total; ++s) {
     const int st = s % kStages;
-    const uint32_t parity = ((uint32_t)(s / kStages) & 1u) ^ 1u;
-    // ---- the keys' power of two, the values' type
+    // ---- the keys' power of two
     float most = 0.0f;
-    bool fits = true;
 #pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      most = fmaxf(most, Scales(ks[i]).most());
-      const Scales v(vs[i]);
-      const float vm = v.most();
-      fits = fits && vm <= 32768.0f && (vm >= 0.0625f || vm == 0.0f);
-      if (!v.finite)
-        atomicMin(&bars->nan_from[group],
-                  (w.j0 + s) * kKeys + warp * 32 + i * RL + lane / LR);
-    }
+    for (int i = 0; i < E::NL; ++i) most = fmaxf(most, Scales(e.scale[i]).most());
     const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
-    // the largest goes to [2^7, 2^8) (below 2^-119: times 2^126)
-    const int e = min(max((int)(top >> 23), 8), 253);
-    const float scale = __uint_as_float((uint32_t)(254 + 7 - e) << 23);
-    const bool v_bf16 = !__all_sync(0xffffffffu, fits);
+    // the largest goes to [2^-7, 2^-6): 2^24 of a step to 2^15.1 at most (below 2^-112:
+    // times 2^105)
+    const int x = min(max((int)(top >> 23), 15), 246);
+    const float scale = __uint_as_float((uint32_t)(254 - 7 - x) << 23);
     const uint32_t there = __ballot_sync(0xffffffffu, where >= 0) & 3u;
-    if (!wait_all(&bars->k_empty[st], parity, abort_flag, p)) return;
+    if (!wait_all(&bars->k_empty[st], ((uint32_t)(s / kStages) & 1u) ^ 1u, abort_flag, p)) return;
     if (lane == 0) {
       TokenInfo* info = &bars->info[s % kInfos][warp];
       info->factor = 1.0f / scale;
-      info->bits = there | (v_bf16 ? 4u : 0u);
+      info->there = there;
+      mbar_arrive(smem_u32(&bars->info_full[s % kInfos]));
     }
-    // ---- K
-    const uint32_t k_at = base + C::kK + st * C::kTileBytes;
+    const uint32_t tile = base + C::kK + st * C::kTileBytes;
 #pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      const __half2 step = __float2half2_rn(Scales(ks[i]).step * scale);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        __half2 x[4];
-        open_codes(word_of(kc[i], c), k1024, k64, x);
-        st_shared_v4(k_at + piece_at[c] + i * (RL * 128), half_bits(__hmul2(x[0], step)),
-                     half_bits(__hmul2(x[1], step)), half_bits(__hmul2(x[2], step)),
-                     half_bits(__hmul2(x[3], step)));
-      }
+    for (int i = 0; i < E::NL; ++i) {
+      const float step = Scales(e.scale[i]).step * scale;
+      const __half2 low = __float2half2_rn(step * 16777216.0f),
+                    high = __float2half2_rn(step * 1048576.0f),
+                    plus = __float2half2_rn(step * -8.0f);
+      e.each(i, tile, [&](uint32_t n, uint32_t to) {
+        uint32_t y[4];
+        expand_codes(n, low, high, plus, y);
+        st_shared_v4(to, y[0], y[1], y[2], y[3]);
+      });
     }
     {  // c of each group, twice its high half and once its low one
-      __half x[16];
+      __half y[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = __ushort_as_half(0);
+      for (int i = 0; i < 16; ++i) y[i] = __ushort_as_half(0);
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         const Scales k(sums[g]);
-        float c = fmaf(8.0f, k.step, k.least) * scale * 128.0f;
+        float c = fmaf(8.0f, k.step, k.least) * scale * 16384.0f;
         if (!k.finite) c = __int_as_float(0x7FC00000);
         const __half hi = __float2half_rn(c);
-        x[g] = x[NG + g] = hi;
-        x[2 * NG + g] = __float2half_rn(c - __half2float(hi));
+        y[g] = y[NG + g] = hi;
+        y[2 * NG + g] = __float2half_rn(c - __half2float(hi));
       }
-      const uint32_t at = base + C::kKSums + st * C::kSumBytes + (warp * 32 + lane) * 16;
-      st_shared_v4(at, half_pair(x[0], x[1]), half_pair(x[2], x[3]), half_pair(x[4], x[5]),
-                   half_pair(x[6], x[7]));
-      st_shared_v4(at + 2048, half_pair(x[8], x[9]), half_pair(x[10], x[11]),
-                   half_pair(x[12], x[13]), half_pair(x[14], x[15]));
+      const uint32_t to = base + C::kKSums + st * C::kSumBytes + (warp * 32 + lane) * 16;
+      st_shared_v4(to, half_pair(y[0], y[1]), half_pair(y[2], y[3]), half_pair(y[4], y[5]),
+                   half_pair(y[6], y[7]));
+      st_shared_v4(to + 2048, half_pair(y[8], y[9]), half_pair(y[10], y[11]),
+                   half_pair(y[12], y[13]), half_pair(y[14], y[15]));
     }
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) {
-      mbar_arrive(smem_u32(&bars->info_full[s % kInfos]));
-      mbar_arrive(smem_u32(&bars->k_full[st]));
-    }
+    if (lane == 0) mbar_arrive(smem_u32(&bars->k_full[st]));
     where = next;
-    next = look_up(s + 2);
-    load_k(where, s + 1);
-    // ---- V
-    if (!wait_all(&bars->v_empty[st], parity, abort_flag, p)) return;
-    const uint32_t v_at = base + C::kV + st * C::kTileBytes;
-    if (!v_bf16) {
+    next = e.look_up(s + 2);
+    e.load_step(where, s + 1);
+    load_sums(where, s + 1);
+  }
+}
+
+template <int D, int NG>
+__device__ void run_expand_values(const ChunkParams& p, const ChunkWork& w, ChunkBars* bars,
+                                    uint32_t base, volatile int* abort_flag) {
+  using C = ChunkCfg<D>;
+  using E = Expander<D, NG>;
+  E e(p, w, false);
+  const int lane = e.lane, warp = e.warp;
+  int where = e.look_up(0), next = e.look_up(1);
+  float v_scale;
+  e.load_step(where, 0);
+  // ---- the CTA's power of two
+  {
+    int sum = 0, n = 0;
 #pragma unroll
-      for (int i = 0; i < NL; ++i) {
-        const Scales v(vs[i]);
-        const __half2 step = __float2half2_rn(v.step), least = __float2half2_rn(v.least);
+    for (int i = 0; i < E::NL; ++i) {
+      const float most = Scales(e.scale[i]).most();
+      if (most > 0.0f) sum += (int)(__float_as_uint(most) >> 23), ++n;
+    }
+    sum = __reduce_add_sync(0xffffffffu, sum);
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (lane == 0) bars->v_exponents[warp][0] = sum, bars->v_exponents[warp][1] = n;
+    named_bar_sync(1, 128);
+    sum = n = 0;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          __half2 x[4];
-          open_codes(word_of(vc[i], c), v1024, v64, x);
-          st_shared_v4(v_at + piece_at[c] + i * (RL * 128), half_bits(__hfma2(x[0], step, least)),
-                       half_bits(__hfma2(x[1], step, least)),
-                       half_bits(__hfma2(x[2], step, least)),
-                       half_bits(__hfma2(x[3], step, least)));
-        }
+    for (int i = 0; i < 4; ++i) sum += bars->v_exponents[i][0], n += bars->v_exponents[i][1];
+    const int mean = n > 0 ? min(max(sum / n, 20), 240) : 127;
+    v_scale = __uint_as_float((uint32_t)(254 - 10 - mean) << 23);
+    if (lane == 0 && warp == 0) bars->v_scale = 1.0f / v_scale;
+  }
+#pragma unroll 1
+  for (int s = 0; s < w.total; ++s) {
+    const int st = s % kStages;
+    bool fits = true;
+#pragma unroll
+    for (int i = 0; i < E::NL; ++i) {
+      const Scales v(e.scale[i]);
+      const float most = v.most() * v_scale;
+      fits = fits && most <= 0.015625f && (most >= 6.103515625e-5f || most == 0.0f);
+      if (!v.finite)
+        atomicMin(&bars->nan_from[lane % E::LR / E::GL],
+                  (w.j0 + s) * kKeys + warp * 32 + i * E::RL + lane / E::LR);
+    }
+    const bool bf16 = !__all_sync(0xffffffffu, fits);
+    // (the step four before this one is read: its values' stage was free a step ago)
+    if (lane == 0) {
+      bars->info[s % kInfos][warp].v_bf16 = bf16 ? 1u : 0u;
+      mbar_arrive(smem_u32(&bars->info_full[s % kInfos]));
+    }
+    if (!wait_all(&bars->v_empty[st], ((uint32_t)(s / kStages) & 1u) ^ 1u, abort_flag, p)) return;
+    const uint32_t tile = base + C::kV + st * C::kTileBytes;
+    if (!bf16) {
+#pragma unroll
+      for (int i = 0; i < E::NL; ++i) {
+        const Scales v(e.scale[i]);
+        const float step = v.step * v_scale;
+        const __half2 low = __float2half2_rn(step * 16777216.0f),
+                      high = __float2half2_rn(step * 1048576.0f),
+                      plus = __float2half2_rn(v.least * v_scale);
+        e.each(i, tile, [&](uint32_t n, uint32_t to) {
+          uint32_t y[4];
+          expand_codes(n, low, high, plus, y);
+          st_shared_v4(to, y[0], y[1], y[2], y[3]);
+        });
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < NL; ++i) {
-        const Scales v(vs[i]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const uint32_t n = word_of(vc[i], c);
+      for (int i = 0; i < E::NL; ++i) {
+        const Scales v(e.scale[i]);
+        const float step = v.step * v_scale, least = v.least * v_scale;
+        e.each(i, tile, [&](uint32_t n, uint32_t to) {
           uint32_t y[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            y[k] = pack_bf16x2(fmaf((float)(n >> (4 * k) & 15u), v.step, v.least),
-                               fmaf((float)(n >> (4 * k + 16) & 15u), v.step, v.least));
-          st_shared_v4(v_at + piece_at[c] + i * (RL * 128), y[0], y[1], y[2], y[3]);
-        }
+            y[k] = pack_bf16x2(fmaf((float)(n >> (4 * k) & 15u), step, least),
+                               fmaf((float)(n >> (4 * k + 16) & 15u), step, least));
+          st_shared_v4(to, y[0], y[1], y[2], y[3]);
+        });
       }
     }
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&bars->v_full[st]));
-    load_v(where, s + 1);
+    where = next;
+    next = e.look_up(s + 2);
+    e.load_step(where, s + 1);
   }
 }
 
 // ---------------------------------------------------------------------------
-// warps 12 and 13: the two products
+// warps 24 and 25: the two products
 // ---------------------------------------------------------------------------
+// A warp a product and row tile, so that none waits behind another tile's issue.  (What the
+// loops turn on is broadcast: the instruction's operands are uniform registers.)
+//
 // S(s) of a row tile replaces what P(s - 1) V read, so it waits for that product.
 template <int D>
 __device__ void run_scores(const ChunkParams& p, const ChunkWork& w, ChunkBars* bars,
-                           uint32_t tmem, uint32_t base, volatile int* abort_flag) {
+                           uint32_t tmem, uint32_t base, volatile int* abort_flag, int tile) {
   using C = ChunkCfg<D>;
-  bool ok = true;
-  for (int i = 0; i < 2 && ok; ++i)
-    if (w.steps[i] > 0) ok = wait_all(&bars->q_full[i], 0, abort_flag, p);
-  for (int s = 0; s < w.total && ok; ++s) {
+  const int total = __shfl_sync(0xffffffffu, w.total, 0);
+  const int steps = __shfl_sync(0xffffffffu, w.steps[tile], 0);
+  const uint32_t to = __shfl_sync(0xffffffffu, tmem, 0) + C::kTmemS + tile * 128;
+  const uint64_t qd = smem_desc_sw128(base + C::kQ + tile * C::kTileBytes, 16, 1024);
+  const uint64_t qs = sums_desc(base + C::kQSums + tile * C::kSumBytes);
+  bool ok = steps == 0 || wait_all(&bars->q_full[tile], 0, abort_flag, p);
+  for (int s = 0; s < total && ok; ++s) {
     const int st = s % kStages;
     ok = wait_all(&bars->k_full[st], (uint32_t)(s / kStages) & 1u, abort_flag, p);
-    for (int i = 0; i < 2 && ok; ++i) {
-      if (s >= w.steps[i]) continue;
-      if (s > 0) ok = wait_all(&bars->pv_done[i], (uint32_t)(s - 1) & 1u, abort_flag, p);
-      if (!ok) break;
-      tc_fence_after();
-      if (elect_one()) {
-        const uint64_t qd = smem_desc_sw128(base + C::kQ + i * C::kTileBytes, 16, 1024);
-        const uint64_t kd = smem_desc_sw128(base + C::kK + st * C::kTileBytes, 16, 1024);
-        const uint32_t to = tmem + C::kTmemS + i * 128;
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = ((k >> 2) * C::kBoxBytes + (k & 3) * 32) >> 4;
-          mma_ss(to, qd + off, kd + off, C::kIdescS, k > 0 ? 1u : 0u);
-        }
-        mma_ss(to, sums_desc(base + C::kQSums + i * C::kSumBytes),
-               sums_desc(base + C::kKSums + st * C::kSumBytes), C::kIdescS, 1u);
-        mma_commit(smem_u32(&bars->s_full[i]));
-      }
+    if (!ok) break;
+    if (s >= steps) {
+      if (elect_one()) mbar_arrive(smem_u32(&bars->k_empty[st]));
       __syncwarp();
+      continue;
     }
-    if (ok && elect_one()) mma_commit(smem_u32(&bars->k_empty[st]));
+    if (s > 0) ok = wait_all(&bars->pv_done[tile], (uint32_t)(s - 1) & 1u, abort_flag, p);
+    if (!ok) break;
+    tc_fence_after();
+    const uint64_t kd = smem_desc_sw128(base + C::kK + st * C::kTileBytes, 16, 1024);
+    const uint64_t ks = sums_desc(base + C::kKSums + st * C::kSumBytes);
+    if (elect_one()) {
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const uint32_t off = ((k >> 2) * C::kBoxBytes + (k & 3) * 32) >> 4;
+        mma_ss(to, qd + off, kd + off, C::kIdescS, k > 0 ? 1u : 0u);
+      }
+      mma_ss(to, qs, ks, C::kIdescS, 1u);
+      mma_commit(smem_u32(&bars->s_full[tile]));
+      mma_commit(smem_u32(&bars->k_empty[st]));
+    }
     __syncwarp();
   }
-  drain(bars);
+  drain(&bars->drain[tile]);
 }
 
 template <int D>
 __device__ void run_values(const ChunkParams& p, const ChunkWork& w, ChunkBars* bars,
-                           uint32_t tmem, uint32_t base, volatile int* abort_flag) {
+                           uint32_t tmem, uint32_t base, volatile int* abort_flag, int tile) {
   using C = ChunkCfg<D>;
+  const int total = __shfl_sync(0xffffffffu, w.total, 0);
+  const int steps = __shfl_sync(0xffffffffu, w.steps[tile], 0);
+  tmem = __shfl_sync(0xffffffffu, tmem, 0);
+  const uint32_t from = tmem + C::kTmemS + tile * 128, to = tmem + C::kTmemO + tile * D;
   bool ok = true;
-  for (int s = 0; s < w.total && ok; ++s) {
+  for (int s = 0; s < total && ok; ++s) {
     const int st = s % kStages;
     ok = wait_all(&bars->v_full[st], (uint32_t)(s / kStages) & 1u, abort_flag, p);
-    for (int i = 0; i < 2 && ok; ++i) {
-      if (s >= w.steps[i]) continue;
-      ok = wait_all(&bars->p_full[i], (uint32_t)s & 1u, abort_flag, p);
-      if (!ok) break;
-      tc_fence_after();
-      if (elect_one()) {
-        const uint64_t vd =
-            smem_desc_sw128(base + C::kV + st * C::kTileBytes, C::kBoxBytes, 1024);
-        const uint32_t from = tmem + C::kTmemS + i * 128, to = tmem + C::kTmemO + i * D;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {  // 16 tokens each
-          const bool bf = bars->info[s % kInfos][k >> 1].bits & 4u;
-          mma_ts(to, from + k * 8, vd + (uint32_t)(k * 2048 >> 4),
-                 bf ? C::kIdescOBf : C::kIdescO16, s > 0 || k > 0 ? 1u : 0u);
-        }
-        mma_commit(smem_u32(&bars->pv_done[i]));
-      }
+    if (!ok) break;
+    if (s >= steps) {
+      if (elect_one()) mbar_arrive(smem_u32(&bars->v_empty[st]));
       __syncwarp();
+      continue;
     }
-    if (ok && elect_one()) mma_commit(smem_u32(&bars->v_empty[st]));
+    uint32_t bf16 = 0;  // by 32 tokens
+#pragma unroll
+    for (int c = 0; c < 4; ++c) bf16 |= bars->info[s % kInfos][c].v_bf16 << c;
+    bf16 = __shfl_sync(0xffffffffu, bf16, 0);
+    const uint64_t vd = smem_desc_sw128(base + C::kV + st * C::kTileBytes, C::kBoxBytes, 1024);
+    ok = wait_all(&bars->p_full[tile], (uint32_t)s & 1u, abort_flag, p);
+    if (!ok) break;
+    tc_fence_after();
+    if (elect_one()) {
+      // 16 tokens each (tokens 64 on: 64 columns on)
+      if (bf16 == 0u) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          mma_ts(to, from + (k & 3) * 8 + (k >> 2) * 64, vd + (uint32_t)(k * 2048 >> 4),
+                 C::kIdescO16, s > 0 || k > 0 ? 1u : 0u);
+      } else {
+        for (int k = 0; k < 8; ++k)
+          mma_ts(to, from + (k & 3) * 8 + (k >> 2) * 64, vd + (uint32_t)(k * 2048 >> 4),
+                 bf16 >> (k >> 1) & 1u ? C::kIdescOBf : C::kIdescO16, s > 0 || k > 0 ? 1u : 0u);
+      }
+      mma_commit(smem_u32(&bars->pv_done[tile]));
+      mma_commit(smem_u32(&bars->v_empty[st]));
+    }
     __syncwarp();
   }
-  drain(bars);
+  drain(&bars->drain[2 + tile]);
 }
 
 // ---------------------------------------------------------------------------
-// warps 0-7: queries, softmax, results
+// warps 0-15: queries, softmax, results
 // ---------------------------------------------------------------------------
-// This warp's 32 rows of Q as fp16 beside each row's largest (which goes to [2^14,
+// This warp's 16 rows of Q as fp16 beside each row's largest (which goes to [2^14,
 // 2^15)), channels in the codes' order, and the sums of their groups.
 template <int D, int NG>
 __device__ __forceinline__ void load_queries(const ChunkParams& p, const ChunkWork& w,
-                                             ChunkBars* bars, uint32_t base, int tile, int sub) {
+                                             ChunkBars* bars, uint32_t base, int tile, int row_in) {
   using C = ChunkCfg<D>;
   constexpr int LQ = D / 8, RQ = 32 / LQ;  // lanes a row, rows at once
   constexpr int GL = LQ / NG;              // lanes a group
-  constexpr int kBatch = 8;
+  constexpr int kBatch = 4;
   const int lane = threadIdx.x & 31, piece = lane % LQ;
   const uint32_t q_at = base + C::kQ + tile * C::kTileBytes + piece / 8 * C::kBoxBytes;
-  const uint32_t sums_at = base + C::kQSums + tile * C::kSumBytes + (sub * 32) * 16;
-  st_shared_v4(sums_at + lane * 16, 0, 0, 0, 0);
-  st_shared_v4(sums_at + lane * 16 + 2048, 0, 0, 0, 0);
+  const uint32_t sums_at = base + C::kQSums + tile * C::kSumBytes + row_in * 16;
+  st_shared_v4(sums_at + (lane & 15) * 16 + (lane >> 4) * 2048, 0, 0, 0, 0);
   __syncwarp();
 #pragma unroll 1
-  for (int r0 = 0; r0 < 32; r0 += kBatch * RQ) {
+  for (int r0 = 0; r0 < 16; r0 += kBatch * RQ) {
     uint4 raw[kBatch];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      const int row = w.row0 + tile * kTileRows + sub * 32 + r0 + i * RQ + lane / LQ;
+      const int row = w.row0 + tile * kTileRows + row_in + r0 + i * RQ + lane / LQ;
       raw[i] = make_uint4(0, 0, 0, 0);
       if (row < w.rows) {
         const int t = row / p.G, g = row - t * p.G;
@@ -550,7 +629,7 @@ __device__ __forceinline__ void load_queries(const ChunkParams& p, const ChunkWo
     }
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      const int r = sub * 32 + r0 + i * RQ + lane / LQ;
+      const int r = row_in + r0 + i * RQ + lane / LQ;
       float x[8], most = 0.0f, sum = 0.0f;
       unpack8(raw[i], x);
 #pragma unroll
@@ -572,12 +651,12 @@ __device__ __forceinline__ void load_queries(const ChunkParams& p, const ChunkWo
                    pack_f16x2(x[1], x[5]), pack_f16x2(x[2], x[6]), pack_f16x2(x[3], x[7]));
 #pragma unroll
       for (int o = 1; o < GL; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      sum *= 0.0078125f;
+      sum *= 6.103515625e-5f;  // (2^-14: c has 2^14)
       if (piece % GL == 0) {
         const int g = piece / GL;
         const __half hi = __float2half_rn(sum), lo = __float2half_rn(sum - __half2float(hi));
         auto put = [&](int k, __half v) {
-          asm volatile("st.shared.b16 [%0], %1;" ::"r"(sums_at + (r - sub * 32) * 16 +
+          asm volatile("st.shared.b16 [%0], %1;" ::"r"(sums_at + (r - row_in) * 16 +
                                                        (k >> 3) * 2048 + (k & 7) * 2),
                        "h"(__half_as_ushort(v))
                        : "memory");
@@ -664,12 +743,19 @@ template <int D, int NG, bool SCORED>
 __device__ void run_softmax(const ChunkParams& p, const ChunkWork& w, ChunkBars* bars,
                             uint32_t tmem, uint32_t base, volatile int* abort_flag) {
   using C = ChunkCfg<D>;
+  constexpr int DH = D / 2;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int tile = warp >> 2, sub = warp & 3;
-  const int r = sub * 32 + lane;
-  const int steps = w.steps[tile];
-  if (steps == 0) return write_nothing<D>(p, w, tile, r);
-  load_queries<D, NG>(p, w, bars, base, tile, sub);
+  const int tile = warp / kSoftmaxWarps;
+  // 16 of the 32 rows of this warp's part of tensor memory; lanes 16 on take the same
+  // rows' tokens 64 to 127 and the second half of the channels
+  const int row_in = (warp & 3) * 32 + (warp >> 2 & 1) * 16, half = lane >> 4;
+  const int r = row_in + (lane & 15);
+  const int steps = w.steps[tile], both = min(w.steps[0], w.steps[1]);
+  if (steps == 0) {
+    if (half == 0) write_nothing<D>(p, w, tile, r);
+    return;
+  }
+  load_queries<D, NG>(p, w, bars, base, tile, row_in);
   const int row = w.row0 + tile * kTileRows + r;
   const int t = row / p.G, g = row - t * p.G;
   const bool there = row < w.rows;
@@ -682,190 +768,210 @@ __device__ void run_softmax(const ChunkParams& p, const ChunkWork& w, ChunkBars*
     if (p.slopes && there) slope = load(p.slopes + w.h * p.G + g) * 1.4426950408889634f;
   }
   const float inv_cap = SCORED && p.cap_log2 > 0.0f ? 1.0f / p.cap_log2 : 0.0f;
-  const uint32_t lanes = (uint32_t)(sub * 32) << 16;
+  const uint32_t lanes = (uint32_t)row_in << 16;
   const uint32_t tS = tmem + C::kTmemS + tile * 128 + lanes;
   const uint32_t tO = tmem + C::kTmemO + tile * D + lanes;
   const uint32_t kNegInf = 0xff800000u;
+  constexpr unsigned kAll = 0xffffffffu;
+
+  // SCORED: 32 products to scores in base 2: `f` is their factor, d0 the distance of the
+  // first key from the query, `past` whether keys behind the query are seen.
+  auto score = [&](uint32_t (&x)[32], float f, int d0, bool past) {
+    if (p.cap_log2 > 0.0f) {
+      const float k = f * inv_cap;
+      float big = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 32; i += 2)
+        big = max3(big, fabsf(__uint_as_float(x[i])), fabsf(__uint_as_float(x[i + 1])));
+      if (__any_sync(0xffffffffu, !(big * k <= kTanhRange))) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          x[i] = __float_as_uint(p.cap_log2 * tanh_any(__uint_as_float(x[i]) * k));
+      } else {
+        const uint64_t k2 = f2_pack(k, k), f2 = f2_pack(f, f);
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          const uint64_t raw = f2_pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+          const uint64_t y = f2_mul(raw, k2), u = f2_mul(y, y);
+          uint64_t a = f2_fma(f2_pack(kTanh5, kTanh5), u, f2_pack(kTanh4, kTanh4));
+          a = f2_fma(a, u, f2_pack(kTanh3, kTanh3));
+          a = f2_fma(a, u, f2_pack(kTanh2, kTanh2));
+          a = f2_fma(a, u, f2_pack(kTanh1, kTanh1));
+          a = f2_fma(a, u, f2_pack(kTanh0, kTanh0));
+          a = f2_mul(a, f2_mul(raw, f2));
+          float lo, hi;
+          f2_unpack(a, lo, hi);
+          x[i] = __float_as_uint(lo), x[i + 1] = __float_as_uint(hi);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
+    }
+    if (p.slopes) {
+      if (__any_sync(0xffffffffu, slope != 0.0f && past)) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          x[i] = __float_as_uint(fmaf(-slope, fabsf((float)(d0 + i)), __uint_as_float(x[i])));
+      } else {
+        const float b0 = slope * (float)d0;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          x[i] = __float_as_uint(__uint_as_float(x[i]) + fmaf(slope, (float)i, b0));
+      }
+    }
+  };
 
   float m = -INFINITY;  // reference: a maximum of scores (base 2) so far, or up to kLagBits below
-  uint64_t sum2 = 0;
-  for (int s = 0; s < steps; ++s) {
-    if (!wait_all(&bars->info_full[s % kInfos], (uint32_t)(s / kInfos) & 1u, abort_flag, p)) return;
-    if (!wait_all(&bars->s_full[tile], (uint32_t)s & 1u, abort_flag, p)) return;
-    tc_fence_after();
-    const int key0 = (w.j0 + s) * kKeys;
-    const int rel = lim - key0;  // keys c <= rel of the step are seen
-    float factor[4];
-    uint32_t bits = 0;  // 16-token pieces that are there
-    uint32_t bf16s = 0;
+  uint64_t sum2 = 0;    // of the weights of this half
+  // What a step needs besides its scores: read while the tensor core works on them.
+  TokenInfo info[2];
+  float factor[2];
+  bool whole = false, any_bf16 = false, look = true;
+  auto prepare = [&](int s) -> bool {
+    if (!wait_all(&bars->info_full[s % kInfos], (uint32_t)(s / kInfos) & 1u, abort_flag, p))
+      return false;
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const TokenInfo info = bars->info[s % kInfos][c];
+    for (int c = 0; c < 2; ++c) {
+      info[c] = bars->info[s % kInfos][2 * half + c];
       // (not zero: what is hidden is -inf times it)
-      factor[c] = fmaxf(row_factor * info.factor, 1.17549435e-38f);
-      bits |= (info.bits & 3u) << (2 * c);
-      bf16s |= (info.bits >> 2 & 1u) << c;
+      factor[c] = fmaxf(row_factor * info[c].factor, 1.17549435e-38f);
     }
-    const bool masked = __any_sync(0xffffffffu, rel < kKeys - 1) || bits != 0xFFu;
-    bool beyond = false;  // a key behind the query's own position is seen
-    if constexpr (SCORED)
-      beyond = __any_sync(0xffffffffu, slope != 0.0f && min(lim, key0 + kKeys - 1) > pos);
-    uint32_t weights[64];
-    uint64_t step_sum = 0;
-
-    // 32 scores as they are to be multiplied by `f` (SCORED: by one)
-    auto finish = [&](int c, uint32_t (&x)[32]) -> float {
-      float f = factor[c];
-      if constexpr (SCORED) {
-        const uint64_t f2 = f2_pack(f, f);
-        bool capped = false;
-        if (p.cap_log2 > 0.0f) {
-          const float k = f * inv_cap;
-          float big = 0.0f;
+    const int rel = lim - ((w.j0 + s) * kKeys + 64 * half);
+    whole = __all_sync(kAll, rel >= 63 && (info[0].there & info[1].there) == 3u);
+    any_bf16 = __any_sync(kAll, (info[0].v_bf16 | info[1].v_bf16) != 0u);
+    // Weights are formed beside the reference of the steps before, without a look for
+    // the maximum; with one where their sum shows that scores rose far above it, where
+    // there is no reference yet, and where scores are to be masked, capped or biased
+    // first (they go back to tensor memory for that).
+    look = SCORED || !whole || __any_sync(kAll, m == -INFINITY);
+    return true;
+  };
+  if (!prepare(0)) return;
+#pragma unroll 1
+  for (int s = 0; s < steps; ++s) {
+    // The row tiles' softmaxes take turns: while one has the issue slots, the tensor core
+    // works for the other.
+    const bool turns = s < both && (tile == 1 || s > 0);
+    if (!wait_both(&bars->s_full[tile], (uint32_t)s & 1u,
+                   turns ? &bars->turn[tile] : &bars->s_full[tile],
+                   (uint32_t)(turns && tile == 0 ? s - 1 : s) & 1u, abort_flag, p))
+      return;
+    tc_fence_after();
+    const int key0 = (w.j0 + s) * kKeys + 64 * half;
+    const int rel = lim - key0;  // of this half's keys those up to rel are seen
+    uint32_t weights[32];
+    bool hand = s < both;  // the other tile's turn is to come
+    uint64_t part;
+    for (;;) {
+      if (look) {
+        float top = -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+          uint32_t x[32];
+          tmem_ld16x2_32<64>(tS + 32 * c, x);
+          const float f = c ? factor[1] : factor[0];
+          tmem_wait_ld();
+          reg_fence(x, 32);
+          if constexpr (SCORED)
+            score(x, f, key0 + 32 * c - pos, min(lim, key0 + 32 * c + 31) > pos);
+          if (!whole) {
+            const int last = rel - 32 * c;
+            const uint32_t there16 = c ? info[1].there : info[0].there;
+            uint32_t seen = last >= 31 ? 0xFFFFFFFFu : last < 0 ? 0u : (2u << last) - 1u;
+            if (!(there16 & 1u)) seen &= 0xFFFF0000u;
+            if (!(there16 & 2u)) seen &= 0x0000FFFFu;
 #pragma unroll
-          for (int i = 0; i < 32; i += 2)
-            big = max3(big, fabsf(__uint_as_float(x[i])), fabsf(__uint_as_float(x[i + 1])));
-          capped = true;
-          if (__any_sync(0xffffffffu, !(big * k <= kTanhRange))) {
+            for (int i = 0; i < 32; ++i) x[i] = seen >> i & 1u ? x[i] : kNegInf;
+          }
+          if (SCORED || !whole) tmem_st16x2_32<64>(tS + 32 * c, x);
+          top = fmaxf(top, largest32(x) * (SCORED ? 1.0f : f));
+        }
+        if (SCORED || !whole) tmem_wait_st();
+        top = fmaxf(top, __shfl_xor_sync(kAll, top, 16));
+        const bool moves = top > m + kLagBits;
+        if (__any_sync(kAll, moves)) {
+          float f = 1.0f;
+          if (moves) {
+            f = ex2_approx(m - top);  // (0 from no reference)
+            m = top;
+            sum2 = f2_mul(sum2, f2_pack(f, f));
+          }
+          if (s > 0) {  // (O is complete: the step's scores waited for the last step's product)
+#pragma unroll 1
+            for (int k = 0; k < DH; k += 16) {
+              uint32_t o[16];
+              tmem_ld16x2_16<DH>(tO + k, o);
+              tmem_wait_ld();
+              reg_fence(o, 16);
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              x[i] = __float_as_uint(p.cap_log2 * tanh_any(__uint_as_float(x[i]) * k));
-          } else {
-            const uint64_t k2 = f2_pack(k, k);
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              const uint64_t raw = f2_pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1]));
-              const uint64_t y = f2_mul(raw, k2), u = f2_mul(y, y);
-              uint64_t a = f2_fma(f2_pack(kTanh5, kTanh5), u, f2_pack(kTanh4, kTanh4));
-              a = f2_fma(a, u, f2_pack(kTanh3, kTanh3));
-              a = f2_fma(a, u, f2_pack(kTanh2, kTanh2));
-              a = f2_fma(a, u, f2_pack(kTanh1, kTanh1));
-              a = f2_fma(a, u, f2_pack(kTanh0, kTanh0));
-              a = f2_mul(a, f2_mul(raw, f2));
-              float lo, hi;
-              f2_unpack(a, lo, hi);
-              x[i] = __float_as_uint(lo), x[i + 1] = __float_as_uint(hi);
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_st16x2_16<DH>(tO + k, o);
             }
           }
         }
-        if (!capped) {
+      }
+      const float reference = m == -INFINITY ? 0.0f : m;
+      const uint64_t nm2 = f2_pack(-reference, -reference);
+      auto weigh = [&](auto type) {
+        uint64_t parts[2] = {0, 0};
+        uint32_t x[2][16];
+        tmem_ld16x2_16<64>(tS, x[0]);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
-        }
-        if (p.slopes) {
-          const int d0 = key0 + 32 * c - pos;  // of key 0 from the query
-          if (beyond) {
+        for (int c = 0; c < 4; ++c) {  // 16 at once, the next 16 on their way
+          uint32_t(&now)[16] = x[c & 1];
+          if (c == 3) {  // (the others hear of it about when this is done)
+            if (lane == 0 && hand) mbar_arrive(smem_u32(&bars->turn[1 - tile]));
+            hand = false;
+          }
+          tmem_wait_ld();
+          reg_fence(now, 16);
+          if (c < 3) tmem_ld16x2_16<64>(tS + 16 * (c + 1), x[(c + 1) & 1]);
+          const uint64_t f2 = f2_pack(factor[c / 2], factor[c / 2]);
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              x[i] = __float_as_uint(
-                  fmaf(-slope, fabsf((float)(d0 + i)), __uint_as_float(x[i])));
-          } else {
-            const float b0 = slope * (float)d0;
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              x[i] = __float_as_uint(__uint_as_float(x[i]) + fmaf(slope, (float)i, b0));
+          for (int i = 0; i < 16; i += 2) {
+            const uint64_t v = f2_pack(__uint_as_float(now[i]), __uint_as_float(now[i + 1]));
+            float a, b;
+            f2_unpack(SCORED ? f2_add(v, nm2) : f2_fma(v, f2, nm2), a, b);
+            a = ex2_approx(a), b = ex2_approx(b);
+            parts[i / 2 & 1] = f2_add(parts[i / 2 & 1], f2_pack(a, b));
+            weights[8 * c + i / 2] = pack_f16x2(a, b);
+            if (decltype(type)::value && info[c / 2].v_bf16)
+              weights[8 * c + i / 2] = pack_bf16x2(a, b);
           }
         }
-        f = 1.0f;
-      }
-      if (masked) {
-        const int last = rel - 32 * c;
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          x[i] = i > last || !(bits >> (2 * c + i / 16) & 1u) ? kNegInf : x[i];
-      }
-      return f;
-    };
-    // The step's weights beside the reference, and their sum.
-    auto weigh = [&](float reference) {
-      const uint64_t nm2 = f2_pack(-reference, -reference);
-      step_sum = 0;
-      uint32_t x[2][32];
-      tmem_ld32(tS, x[0]);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t(&now)[32] = x[c & 1];
-        tmem_wait_ld();
-        reg_fence(now, 32);
-        if (c < 3) tmem_ld32(tS + 32 * (c + 1), x[(c + 1) & 1]);
-        const float f = finish(c, now);
-        const uint64_t f2 = f2_pack(f, f);
-        const bool bf = bf16s >> c & 1u;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const uint64_t v = f2_pack(__uint_as_float(now[2 * i]), __uint_as_float(now[2 * i + 1]));
-          float a, b;
-          f2_unpack(SCORED ? f2_add(v, nm2) : f2_fma(v, f2, nm2), a, b);
-          a = ex2_approx(a), b = ex2_approx(b);
-          step_sum = f2_add(step_sum, f2_pack(a, b));
-          weights[16 * c + i] = bf ? pack_bf16x2(a, b) : pack_f16x2(a, b);
-        }
-      }
-    };
-    // A step's weights are formed beside the reference of the steps before; where
-    // their sum shows that scores rose far above it (or there is none yet), again
-    // beside the new maximum.
-    bool again = __any_sync(0xffffffffu, m == -INFINITY);
-    if (!again) {
-      weigh(m);
+        part = f2_add(parts[0], parts[1]);
+      };
+      if (any_bf16)
+        weigh(std::true_type{});
+      else
+        weigh(std::false_type{});
       float a, b;
-      f2_unpack(step_sum, a, b);
-      again = __any_sync(0xffffffffu, !(a + b <= kMostSum));  // (NaN too)
+      f2_unpack(part, a, b);
+      if (look || !__any_sync(kAll, !(a + b <= kMostSum))) break;  // (NaN: look, too)
+      look = true;
     }
-    if (again) {
-      float top = -INFINITY;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t x[32];
-        tmem_ld32(tS + 32 * c, x);
-        tmem_wait_ld();
-        reg_fence(x, 32);
-        const float f = finish(c, x);
-        top = fmaxf(top, largest32(x) * f);
-      }
-      const bool moves = top > m + kLagBits;
-      float f = 1.0f;
-      if (moves) {
-        f = ex2_approx(m - top);  // (0 from no reference)
-        m = top;
-        sum2 = f2_mul(sum2, f2_pack(f, f));
-      }
-      // O is complete: the scores of this step waited for the last step's product
-      if (s > 0 && __any_sync(0xffffffffu, moves)) {
-#pragma unroll
-        for (int c = 0; c < D; c += 32) {
-          uint32_t o[32];
-          tmem_ld32(tO + c, o);
-          tmem_wait_ld();
-          reg_fence(o, 32);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-          tmem_st32_16(tO + c, o);
-          tmem_st32_16(tO + c + 16, o + 16);
-        }
-        tmem_wait_st();
-      }
-      weigh(m == -INFINITY ? 0.0f : m);
-    }
-    sum2 = f2_add(sum2, step_sum);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) tmem_st32_16(tS + 16 * c, weights + 16 * c);
+    sum2 = f2_add(sum2, part);
+    tmem_st16x2_32<64>(tS, weights);
     tmem_wait_st();
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&bars->p_full[tile]));
+    if (s + 1 < steps && !prepare(s + 1)) return;
   }
 
   if (!wait_all(&bars->pv_done[tile], (uint32_t)(steps - 1) & 1u, abort_flag, p)) return;
   tc_fence_after();
   float s0, s1;
   f2_unpack(sum2, s0, s1);
-  const float sum = s0 + s1;
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  float sum = s0 + s1;
+  sum += __shfl_xor_sync(kAll, sum, 16);
+  const float v_scale = bars->v_scale;
+  const float inv = sum == 0.0f ? 0.0f : v_scale / sum;
   float* slot = p.partial + w.slot * (kCtaRows * (D + 2)) + tile * kTileRows + r;
   const bool partial = p.splits > 1;
   const int64_t at = ((int64_t)w.b * p.H + w.h * p.G + g) * p.T + t;
-  if (there) {
+  if (there && half == 0) {
     if (partial) {
       slot[0] = m;
       slot[kCtaRows] = sum;
@@ -874,17 +980,18 @@ __device__ void run_softmax(const ChunkParams& p, const ChunkWork& w, ChunkBars*
     }
   }
 #pragma unroll 1
-  for (int c = 0; c < D; c += 16) {
+  for (int k = 0; k < DH; k += 16) {
     uint32_t o[16];
-    tmem_ld32_16(tO + c, o);
+    tmem_ld16x2_16<DH>(tO + k, o);
     tmem_wait_ld();
     reg_fence(o, 16);
+    const int c = half * DH + k;
     // channels from the codes' order
     float x[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const int k = i & 7;
-      x[i] = __uint_as_float(o[(i & 8) + (k < 4 ? 2 * k : 2 * k - 7)]) * (partial ? 1.0f : inv);
+      const int k8 = i & 7;
+      x[i] = __uint_as_float(o[(i & 8) + (k8 < 4 ? 2 * k8 : 2 * k8 - 7)]) * (partial ? v_scale : inv);
     }
     const int nan_from = bars->nan_from[c / (D / NG)];
     if (lim >= nan_from) {
@@ -901,7 +1008,7 @@ __device__ void run_softmax(const ChunkParams& p, const ChunkWork& w, ChunkBars*
       write_row<D>(p, at, x, c);
     }
   }
-  if (!there) write_nothing<D>(p, w, tile, r);  // behind the count
+  if (!there && half == 0) write_nothing<D>(p, w, tile, r);  // behind the count
 }
 
 template <int D, int NG, bool SCORED>
@@ -911,7 +1018,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Chunk
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;  // swizzled tiles begin at multiples of 1024
   ChunkBars* bars = reinterpret_cast<ChunkBars*>(smem_raw + (base - raw) + C::kBars);
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);  // (the same for the warp)
 
   wait_for_previous_launch();
   const ChunkWork w = chunk_work(p);
@@ -924,18 +1031,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Chunk
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(smem_u32(&bars->k_full[i]), 4);
-      mbar_init(smem_u32(&bars->k_empty[i]), 1);
+      mbar_init(smem_u32(&bars->k_empty[i]), 2);
       mbar_init(smem_u32(&bars->v_full[i]), 4);
-      mbar_init(smem_u32(&bars->v_empty[i]), 1);
+      mbar_init(smem_u32(&bars->v_empty[i]), 2);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&bars->q_full[i]), 4);
+      mbar_init(smem_u32(&bars->q_full[i]), kSoftmaxWarps);
       mbar_init(smem_u32(&bars->s_full[i]), 1);
-      mbar_init(smem_u32(&bars->p_full[i]), 4);
+      mbar_init(smem_u32(&bars->p_full[i]), kSoftmaxWarps);
       mbar_init(smem_u32(&bars->pv_done[i]), 1);
+      mbar_init(smem_u32(&bars->turn[i]), kSoftmaxWarps);
     }
-    for (int i = 0; i < kInfos; ++i) mbar_init(smem_u32(&bars->info_full[i]), 4);
-    mbar_init(smem_u32(&bars->drain), 2);
+    for (int i = 0; i < kInfos; ++i) mbar_init(smem_u32(&bars->info_full[i]), 8);
+    for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&bars->drain[i]), 1);
     for (int i = 0; i < 4; ++i) bars->nan_from[i] = 0x7FFFFFFF;
     bars->abort_flag = 0;
     fence_mbar_init();
@@ -951,16 +1059,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Chunk
   const uint32_t tmem = bars->tmem_base;
   volatile int* abort_flag = &bars->abort_flag;
 
-  if (warp < kWarpExpand) {
+  if (warp < kWarpK) {
     regs_inc<kSoftmaxRegs>();
     run_softmax<D, NG, SCORED>(p, w, bars, tmem, base, abort_flag);
   } else if (warp < kWarpScores) {
     regs_dec<kExpandRegs>();
-    run_expand<D, NG>(p, w, bars, base, abort_flag);
+    if (warp < kWarpV)
+      run_expand_keys<D, NG>(p, w, bars, base, abort_flag);
+    else
+      run_expand_values<D, NG>(p, w, bars, base, abort_flag);
   } else {
     regs_dec<kIssueRegs>();
-    if (warp == kWarpScores) run_scores<D>(p, w, bars, tmem, base, abort_flag);
-    if (warp == kWarpValues) run_values<D>(p, w, bars, tmem, base, abort_flag);
+    if (warp < kWarpValues)
+      run_scores<D>(p, w, bars, tmem, base, abort_flag, warp - kWarpScores);
+    else
+      run_values<D>(p, w, bars, tmem, base, abort_flag, warp - kWarpValues);
   }
   __syncwarp();
   tc_fence_before();

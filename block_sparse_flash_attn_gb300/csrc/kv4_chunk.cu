@@ -62,12 +62,28 @@ constexpr int kChunkThreads = 896;
 constexpr int kSoftmaxWarps = 8;            // a row tile
 constexpr int kTileRows = 128;              // rows of a softmax tile: lanes of tensor memory
 constexpr int kCtaRows = 2 * kTileRows;
-constexpr int kKeys = 128;                  // tokens a step
+constexpr int kKeys = 128;                  // tokens that are expanded at once: a step
+// Tokens of a score product: a step, or a half of it (SCORED).  With whole steps a row tile's
+// chain of products and softmax is hidden by the other tile's, which takes turns with it;
+// with halves by its own other half too, and scores stay in registers while they are
+// capped and biased, at a third more shared-memory reads (Q is read for 64 tokens).  4096
+// tokens behind 61440: 3.5 ms as steps, 4.0 as halves; capped scores, 1024 behind 15360:
+// 541 and 432 us.
+template <bool SCORED>
+constexpr int kPiece = SCORED ? 64 : 128;
+template <bool SCORED>
+constexpr int kPieces = kKeys / kPiece<SCORED>;
 constexpr int kStages = 2;                  // of the expanded K and V
 constexpr int kInfos = 4;                   // steps whose ChunkInfo is kept
 constexpr int kWarpK = 16, kWarpV = 20, kWarpScores = 24, kWarpValues = 26;
-// 512 x 88 + 256 x 64 + 128 x 24 = 896 x 72 registers
-constexpr int kSoftmaxRegs = 88, kExpandRegs = 64, kIssueRegs = 24;
+// 512 x 96 + 256 x 48 + 128 x 24 = 896 x 72 registers; the expansion of four groups a row
+// wants more: 512 x 88 + 256 x 64 + 128 x 24.  4096 tokens behind 61440 in groups of 32:
+// 3.6 ms, with the former 4.0; 1024 behind 15360 in groups of 128: 275 us, with the latter 309.
+template <int NG, bool SCORED>
+constexpr int kSoftmaxRegs = SCORED && NG < 4 ? 96 : 88;
+template <int NG, bool SCORED>
+constexpr int kExpandRegs = SCORED && NG < 4 ? 48 : 64;
+constexpr int kIssueRegs = 24;
 constexpr uint32_t kTmemColumns = 512;
 constexpr float kLagBits = 8.0f;            // a row's reference may lie 2^8 below its maximum
 constexpr float kMostSum = 32768.0f;        // of a step's weights: each then fits fp16
@@ -107,8 +123,9 @@ struct TokenInfo {
 
 struct __align__(16) ChunkBars {
   uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
-  uint64_t q_full[2], s_full[2], p_full[2], pv_done[2];
-  uint64_t turn[2];  // the other row tile's softmax of a step is over
+  uint64_t q_full[2];
+  uint64_t turn[2];  // the other row tile's softmax of a step is about over
+  uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // by row tile and piece of a step
   // (a step's slot is taken again four steps on: two steps after its scores were read)
   uint64_t info_full[kInfos];
   uint64_t drain[4];
@@ -119,6 +136,7 @@ struct __align__(16) ChunkBars {
   float v_scale;      // what O is multiplied by
   int v_exponents[4][2];  // of each V warp's first step: sum, number
   int query_shift[kCtaRows];
+  uint2 factors[8][4 * 32];  // by warp, group and token: what codes are multiplied by, and a summand
 };
 
 template <int D>
@@ -137,7 +155,6 @@ struct ChunkCfg {
   static_assert(kSmem <= 232448, "shared memory");
   static_assert(kKSums % 1024 == 0 && kK % 1024 == 0, "swizzled tiles begin at multiples of 1024");
   static constexpr uint32_t kTmemS = 0, kTmemO = 256;
-  static constexpr uint32_t kIdescS = idesc_f16kind_f32(128, 128, false, false, true);
   static constexpr uint32_t kIdescO16 = idesc_f16kind_f32(128, D, true, false, true);
   static constexpr uint32_t kIdescOBf = idesc_f16kind_f32(128, D, true, false, false);
 };
@@ -162,10 +179,11 @@ struct ChunkWork {
   int rows;                   // G * count: rows that have a query
   int row0;                   // the CTA's first
   int64_t slot;               // partial result
-  int j0;                     // first step
-  int steps[2];               // of each row tile
+  int j0;                     // the range's first 128 tokens: step s has j0 + total - 1 - s
+  int steps[2];               // of each row tile: the last ones
   int total;
 
+  __device__ __forceinline__ int first_key(int s) const { return (j0 + total - 1 - s) * kKeys; }
   __device__ __forceinline__ int limit(int t) const {  // last position that token t sees
     return min(max(first_pos + t, open - 1), keys - 1);
   }
@@ -216,14 +234,6 @@ __device__ __forceinline__ bool wait_all(const uint64_t* bar, uint32_t parity,
   return __all_sync(0xffffffffu, ok);
 }
 
-// Both barriers, odd lanes the second.
-__device__ __forceinline__ bool wait_both(const uint64_t* a, uint32_t parity_a, const uint64_t* b,
-                                          uint32_t parity_b, volatile int* abort_flag,
-                                          const ChunkParams& p) {
-  const bool second = threadIdx.x & 1;
-  return wait_all(second ? b : a, second ? parity_b : parity_a, abort_flag, p);
-}
-
 // Waits, with a limit of its own, for all products that this warp issued.
 __device__ __forceinline__ void drain(uint64_t* bar) {
   if (elect_one()) mma_commit(smem_u32(bar));
@@ -268,11 +278,13 @@ struct Scales {
   }
 };
 
-// What a warp of either kind needs to expand its 32 tokens of a step.
+// What a warp of either kind needs to expand its 32 tokens of a step.  A lane is a token
+// where steps and minima are concerned, and a 16-byte piece (32 codes) of a row where
+// codes are; what it works out of the former passes through shared memory.
 template <int D, int NG>
 struct Expander {
   using C = ChunkCfg<D>;
-  static constexpr int LR = D / 32;       // lanes a row: 16 bytes, 32 codes each
+  static constexpr int LR = D / 32;       // lanes a row
   static constexpr int RL = 32 / LR;      // rows a load
   static constexpr int NL = 32 / RL;      // loads a warp and step
   static constexpr int GL = D / NG / 32;  // lanes a group
@@ -280,158 +292,194 @@ struct Expander {
   const ChunkWork& w;
   const uint4* codes;
   const uint32_t* scales;
-  int lane, warp, turned;
-  uint32_t at[2];     // where pieces 0 and 1 go; 2 and 3: 64 bytes the other way
+  uint2* factors;
+  int lane, warp, row, log16;
+  uint32_t at;         // where its first 16 bytes go
   uint4 word[NL];
-  uint32_t scale[NL];
+  uint32_t scale[NG];  // of token `lane`
 
-  __device__ __forceinline__ Expander(const ChunkParams& pp, const ChunkWork& ww, bool keys)
+  __device__ __forceinline__ Expander(const ChunkParams& pp, const ChunkWork& ww, ChunkBars* bars,
+                                      bool keys)
       : p(pp), w(ww), lane(threadIdx.x & 31), warp((threadIdx.x >> 5) & 3) {
-    codes = reinterpret_cast<const uint4*>(keys ? p.c.k_codes : p.c.v_codes) + lane % LR;
-    scales = reinterpret_cast<const uint32_t*>(keys ? p.c.k_scales : p.c.v_scales) + lane % LR / GL;
-    // A row's 32 codes are four 16-byte pieces of its tile; lanes of the second box
-    // begin with the other two, so that the eight lanes of a store meet 32 banks.
-    turned = D == 128 ? lane & 2 : 0;
-    const int row = warp * 32 + lane / LR;
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      at[i] = (D == 128 ? (uint32_t)(lane % LR >> 1) * C::kBoxBytes : 0u) + row * 128 +
-              ((4 * (lane & 1) + (i ^ turned) ^ (row & 7)) << 4);
+    // eight lanes in a row hold eight rows' same piece: their stores meet 32 banks
+    row = lane % RL;
+    const int piece = lane / RL;
+    codes = reinterpret_cast<const uint4*>(keys ? p.c.k_codes : p.c.v_codes) + row * LR + piece;
+    scales = reinterpret_cast<const uint32_t*>(keys ? p.c.k_scales : p.c.v_scales);
+    factors = bars->factors[(keys ? 0 : 4) + warp];
+    log16 = p.c.log_page - 4;
+    const int r = warp * 32 + row;
+    at = (D == 128 ? (uint32_t)(piece >> 1) * C::kBoxBytes : 0u) + r * 128 +
+         ((4 * (piece & 1) ^ (r & 7)) << 4);
   }
-  // Lanes 0 and 1: where the first and the second 16 of the warp's tokens of step s
-  // are, in units of 16 rows; -1: nowhere.
+  // Lanes 0 to 15: where the first 16 of the warp's tokens of step s are, in units of 16
+  // rows; the others: the second 16; -1: nowhere.
   __device__ __forceinline__ int look_up(int s) const {
-    if (lane > 1 || s >= w.total) return -1;
-    const int pos = (w.j0 + s) * kKeys + warp * 32 + lane * 16;
+    if (s >= w.total) return -1;
+    const int pos = w.first_key(s) + warp * 32 + (lane & 16);
     if (pos >= w.keys) return -1;
-    const int pg = page_at(p.c, p.table + w.b * p.table_stride, p.columns, pos >> p.c.log_page);
-    return pg < 0 ? -1 : (int)(p.c.row(pg, w.h, pos & (p.c.page - 1)) >> 4);
+    const int pg = load(p.table + w.b * p.table_stride + (pos >> p.c.log_page));  // (keys end with it)
+    if (pg < 0 || pg >= p.c.pages) {
+      p.c.report();
+      return -1;
+    }
+    return ((pg * p.c.Hkv + w.h) << log16) + ((pos & (p.c.page - 1)) >> 4);
   }
-  // the row of the warp's token t of step s; -1 where there is none
-  __device__ __forceinline__ int64_t row_of(int where, int s, int t) const {
-    const int r16 = __shfl_sync(0xffffffffu, where, t >> 4);
-    const int pos = (w.j0 + s) * kKeys + warp * 32 + t;
-    return r16 < 0 || pos >= w.keys ? -1 : (int64_t)r16 * 16 + (t & 15);
+  // Where a step's codes are (look_up's answer, for the warp).
+  struct Place {
+    int r16[2], there;  // 16 rows each; tokens that there are, or more
+    bool all;
+  };
+  __device__ __forceinline__ Place place_of(int where, int s) const {
+    Place x;
+    x.there = s < w.total ? w.keys - (w.first_key(s) + warp * 32) : 0;
+    x.r16[0] = __shfl_sync(0xffffffffu, where, 0);
+    x.r16[1] = __shfl_sync(0xffffffffu, where, 16);
+    x.all = x.there >= 32 && (x.r16[0] | x.r16[1]) >= 0;
+    return x;
   }
-  __device__ __forceinline__ void load_step(int where, int s) {
-#pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      const int64_t row = row_of(where, s, i * RL + lane / LR);
-      word[i] = make_uint4(0, 0, 0, 0);
-      scale[i] = 0;
-      if (row >= 0) {
-        word[i] = load(codes + row * LR);
-        scale[i] = load(scales + row * NG);
-      }
+  __device__ __forceinline__ void load_word(const Place& x, int i) {
+    const int h = i * RL / 16;  // (RL divides 16)
+    word[i] = make_uint4(0, 0, 0, 0);
+    if (x.all || (x.r16[h] >= 0 && i * RL + row < x.there))
+      word[i] = load(codes + (int64_t)x.r16[h] * (16 * LR) + (i * RL & 15) * LR);
+  }
+  __device__ __forceinline__ void load_scales(int where, int s) {
+    const int there = s < w.total ? w.keys - (w.first_key(s) + warp * 32) : 0;
+    const uint32_t* mine = scales + ((int64_t)where * 16 + (lane & 15)) * NG;
+    const bool seen = where >= 0 && lane < there;
+    if constexpr (NG == 4) {
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (seen) v = load(reinterpret_cast<const uint4*>(mine));
+      scale[0] = v.x, scale[1] = v.y, scale[2] = v.z, scale[3] = v.w;
+    } else if constexpr (NG == 2) {
+      uint2 v = make_uint2(0, 0);
+      if (seen) v = load(reinterpret_cast<const uint2*>(mine));
+      scale[0] = v.x, scale[1] = v.y;
+    } else {
+      scale[0] = seen ? load(mine) : 0u;
     }
   }
-  // f(x, piece's place) for the four words of load i: turned, the other two first
+  __device__ __forceinline__ void load_step(int where, int s) {
+    const Place x = place_of(where, s);
+#pragma unroll
+    for (int i = 0; i < NL; ++i) load_word(x, i);
+    load_scales(where, s);
+  }
+  // of this lane's codes of load i
+  __device__ __forceinline__ uint2 factors_of(int i) const {
+    return factors[(NG > 1 ? lane / RL / GL * 32 : 0) + i * RL + row];
+  }
+  // f(word, place) for the four words of load i
   template <typename F>
   __device__ __forceinline__ void each(int i, uint32_t tile, F f) const {
-    const uint4 v = word[i];
-    const uint32_t n[4] = {turned ? v.z : v.x, turned ? v.w : v.y, turned ? v.x : v.z,
-                           turned ? v.y : v.w};
+    const uint32_t n[4] = {word[i].x, word[i].y, word[i].z, word[i].w};
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-      f(n[c], tile + ((c & 2 ? at[c & 1] ^ 32u : at[c & 1]) + i * (RL * 128)));
+    for (int c = 0; c < 4; ++c) f(n[c], tile + ((at ^ (c << 4)) + i * (RL * 128)));
+  }
+  // all codes, in fp16: token `lane` has factors (2^24 step, 2^20 step), summand
+  __device__ __forceinline__ void put(int g, float step, float plus) {
+    const uint32_t both = pack_f16x2(step * 16777216.0f, step * 1048576.0f);
+    factors[g * 32 + lane] = make_uint2(both, pack_f16x2(plus, plus));
+  }
+  // (each word's place is taken at once by the next step's)
+  __device__ __forceinline__ void expand(uint32_t tile, const Place& next) {
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      const uint2 v = factors_of(i);
+      const __half2 low = half2_of(__byte_perm(v.x, v.x, 0x1010)),
+                    high = half2_of(__byte_perm(v.x, v.x, 0x3232)), plus = half2_of(v.y);
+      each(i, tile, [&](uint32_t n, uint32_t to) {
+        uint32_t y[4];
+        expand_codes(n, low, high, plus, y);
+        st_shared_v4(to, y[0], y[1], y[2], y[3]);
+      });
+      load_word(next, i);
+    }
   }
 };
 
 template <int D, int NG>
-__device__ void run_expand_keys(const ChunkParams& p, const ChunkWork& w, ChunkBars* bars, uint32_t base,
-                         volatile int* abort_flag) {
+__device__ void run_expand_keys(const ChunkParams& p, const ChunkWork& w, ChunkBars* bars,
+                                uint32_t base, volatile int* abort_flag) {
   using C = ChunkCfg<D>;
-  using E = Expander<D, NG>;
-  E e(p, w, true);
+  Expander<D, NG> e(p, w, bars, true);
   const int lane = e.lane, warp = e.warp;
-  uint32_t sums[NG];  // the scales of token `lane`
-  auto load_sums = [&](int where, int s) {
-    const int64_t row = e.row_of(where, s, lane);
-#pragma unroll
-    for (int g = 0; g < NG; ++g)
-      sums[g] = row >= 0 ? load(reinterpret_cast<const uint32_t*>(p.c.k_scales) + row * NG + g) : 0u;
-  };
   int where = e.look_up(0), next = e.look_up(1);
   e.load_step(where, 0);
-  load_sums(where, 0);
 #pragma unroll 1
   for (int s = 0; s < w.total; ++s) {
     const int st = s % kStages;
     // ---- the keys' power of two
     float most = 0.0f;
 #pragma unroll
-    for (int i = 0; i < E::NL; ++i) most = fmaxf(most, Scales(e.scale[i]).most());
+    for (int g = 0; g < NG; ++g) most = fmaxf(most, Scales(e.scale[g]).most());
     const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
     // the largest goes to [2^-7, 2^-6): 2^24 of a step to 2^15.1 at most (below 2^-112:
     // times 2^105)
     const int x = min(max((int)(top >> 23), 15), 246);
     const float scale = __uint_as_float((uint32_t)(254 - 7 - x) << 23);
-    const uint32_t there = __ballot_sync(0xffffffffu, where >= 0) & 3u;
+    const uint32_t there = __ballot_sync(0xffffffffu, where >= 0);
     if (!wait_all(&bars->k_empty[st], ((uint32_t)(s / kStages) & 1u) ^ 1u, abort_flag, p)) return;
     if (lane == 0) {
       TokenInfo* info = &bars->info[s % kInfos][warp];
       info->factor = 1.0f / scale;
-      info->there = there;
+      info->there = (there & 1u) | (there >> 15 & 2u);
       mbar_arrive(smem_u32(&bars->info_full[s % kInfos]));
     }
-    const uint32_t tile = base + C::kK + st * C::kTileBytes;
-#pragma unroll
-    for (int i = 0; i < E::NL; ++i) {
-      const float step = Scales(e.scale[i]).step * scale;
-      const __half2 low = __float2half2_rn(step * 16777216.0f),
-                    high = __float2half2_rn(step * 1048576.0f),
-                    plus = __float2half2_rn(step * -8.0f);
-      e.each(i, tile, [&](uint32_t n, uint32_t to) {
-        uint32_t y[4];
-        expand_codes(n, low, high, plus, y);
-        st_shared_v4(to, y[0], y[1], y[2], y[3]);
-      });
-    }
     {  // c of each group, twice its high half and once its low one
-      __half y[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) y[i] = __ushort_as_half(0);
+      __half hi[4] = {}, lo[4] = {};
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
-        const Scales k(sums[g]);
-        float c = fmaf(8.0f, k.step, k.least) * scale * 16384.0f;
+        const Scales k(e.scale[g]);
+        const float step = k.step * scale;
+        e.put(g, step, step * -8.0f);
+        float c = fmaf(8.0f, step, k.least * scale) * 16384.0f;
         if (!k.finite) c = __int_as_float(0x7FC00000);
-        const __half hi = __float2half_rn(c);
-        y[g] = y[NG + g] = hi;
-        y[2 * NG + g] = __float2half_rn(c - __half2float(hi));
+        hi[g] = __float2half_rn(c);
+        lo[g] = __float2half_rn(c - __half2float(hi[g]));
       }
       const uint32_t to = base + C::kKSums + st * C::kSumBytes + (warp * 32 + lane) * 16;
-      st_shared_v4(to, half_pair(y[0], y[1]), half_pair(y[2], y[3]), half_pair(y[4], y[5]),
-                   half_pair(y[6], y[7]));
-      st_shared_v4(to + 2048, half_pair(y[8], y[9]), half_pair(y[10], y[11]),
-                   half_pair(y[12], y[13]), half_pair(y[14], y[15]));
+      if constexpr (NG == 4) {
+        const uint32_t h01 = half_pair(hi[0], hi[1]), h23 = half_pair(hi[2], hi[3]);
+        st_shared_v4(to, h01, h23, h01, h23);
+        st_shared_v4(to + 2048, half_pair(lo[0], lo[1]), half_pair(lo[2], lo[3]), 0, 0);
+      } else if constexpr (NG == 2) {
+        const uint32_t h01 = half_pair(hi[0], hi[1]);
+        st_shared_v4(to, h01, h01, half_pair(lo[0], lo[1]), 0);
+        st_shared_v4(to + 2048, 0, 0, 0, 0);
+      } else {
+        st_shared_v4(to, half_pair(hi[0], hi[0]), half_pair(lo[0], lo[1]), 0, 0);
+        st_shared_v4(to + 2048, 0, 0, 0, 0);
+      }
     }
+    e.load_scales(next, s + 1);
+    __syncwarp();
+    e.expand(base + C::kK + st * C::kTileBytes, e.place_of(next, s + 1));
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&bars->k_full[st]));
     where = next;
     next = e.look_up(s + 2);
-    e.load_step(where, s + 1);
-    load_sums(where, s + 1);
   }
 }
 
 template <int D, int NG>
 __device__ void run_expand_values(const ChunkParams& p, const ChunkWork& w, ChunkBars* bars,
-                                    uint32_t base, volatile int* abort_flag) {
+                                  uint32_t base, volatile int* abort_flag) {
   using C = ChunkCfg<D>;
   using E = Expander<D, NG>;
-  E e(p, w, false);
+  E e(p, w, bars, false);
   const int lane = e.lane, warp = e.warp;
-  int where = e.look_up(0), next = e.look_up(1);
+  int next = e.look_up(1);
+  e.load_step(e.look_up(0), 0);
   float v_scale;
-  e.load_step(where, 0);
   // ---- the CTA's power of two
   {
     int sum = 0, n = 0;
 #pragma unroll
-    for (int i = 0; i < E::NL; ++i) {
-      const float most = Scales(e.scale[i]).most();
+    for (int g = 0; g < NG; ++g) {
+      const float most = Scales(e.scale[g]).most();
       if (most > 0.0f) sum += (int)(__float_as_uint(most) >> 23), ++n;
     }
     sum = __reduce_add_sync(0xffffffffu, sum);
@@ -450,15 +498,22 @@ __device__ void run_expand_values(const ChunkParams& p, const ChunkWork& w, Chun
     const int st = s % kStages;
     bool fits = true;
 #pragma unroll
-    for (int i = 0; i < E::NL; ++i) {
-      const Scales v(e.scale[i]);
+    for (int g = 0; g < NG; ++g) {
+      const Scales v(e.scale[g]);
       const float most = v.most() * v_scale;
       fits = fits && most <= 0.015625f && (most >= 6.103515625e-5f || most == 0.0f);
-      if (!v.finite)
-        atomicMin(&bars->nan_from[lane % E::LR / E::GL],
-                  (w.j0 + s) * kKeys + warp * 32 + i * E::RL + lane / E::LR);
+      if (!v.finite) atomicMin(&bars->nan_from[g], w.first_key(s) + warp * 32 + lane);
     }
     const bool bf16 = !__all_sync(0xffffffffu, fits);
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      const Scales v(e.scale[g]);
+      if (bf16)
+        e.factors[g * 32 + lane] =
+            make_uint2(__float_as_uint(v.step * v_scale), __float_as_uint(v.least * v_scale));
+      else
+        e.put(g, v.step * v_scale, v.least * v_scale);
+    }
     // (the step four before this one is read: its values' stage was free a step ago)
     if (lane == 0) {
       bars->info[s % kInfos][warp].v_bf16 = bf16 ? 1u : 0u;
@@ -466,25 +521,16 @@ __device__ void run_expand_values(const ChunkParams& p, const ChunkWork& w, Chun
     }
     if (!wait_all(&bars->v_empty[st], ((uint32_t)(s / kStages) & 1u) ^ 1u, abort_flag, p)) return;
     const uint32_t tile = base + C::kV + st * C::kTileBytes;
+    e.load_scales(next, s + 1);
+    const auto place = e.place_of(next, s + 1);
+    __syncwarp();
     if (!bf16) {
-#pragma unroll
-      for (int i = 0; i < E::NL; ++i) {
-        const Scales v(e.scale[i]);
-        const float step = v.step * v_scale;
-        const __half2 low = __float2half2_rn(step * 16777216.0f),
-                      high = __float2half2_rn(step * 1048576.0f),
-                      plus = __float2half2_rn(v.least * v_scale);
-        e.each(i, tile, [&](uint32_t n, uint32_t to) {
-          uint32_t y[4];
-          expand_codes(n, low, high, plus, y);
-          st_shared_v4(to, y[0], y[1], y[2], y[3]);
-        });
-      }
+      e.expand(tile, place);
     } else {
 #pragma unroll
       for (int i = 0; i < E::NL; ++i) {
-        const Scales v(e.scale[i]);
-        const float step = v.step * v_scale, least = v.least * v_scale;
+        const uint2 v = e.factors_of(i);
+        const float step = __uint_as_float(v.x), least = __uint_as_float(v.y);
         e.each(i, tile, [&](uint32_t n, uint32_t to) {
           uint32_t y[4];
 #pragma unroll
@@ -493,14 +539,13 @@ __device__ void run_expand_values(const ChunkParams& p, const ChunkWork& w, Chun
                                fmaf((float)(n >> (4 * k + 16) & 15u), step, least));
           st_shared_v4(to, y[0], y[1], y[2], y[3]);
         });
+        e.load_word(place, i);
       }
     }
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&bars->v_full[st]));
-    where = next;
     next = e.look_up(s + 2);
-    e.load_step(where, s + 1);
   }
 }
 
@@ -510,87 +555,92 @@ __device__ void run_expand_values(const ChunkParams& p, const ChunkWork& w, Chun
 // A warp a product and row tile, so that none waits behind another tile's issue.  (What the
 // loops turn on is broadcast: the instruction's operands are uniform registers.)
 //
-// S(s) of a row tile replaces what P(s - 1) V read, so it waits for that product.
-template <int D>
+// The scores of a piece replace what the product with V of the same piece read a step
+// before, so they wait for that; another's softmax runs meanwhile.
+template <int D, bool SCORED>
 __device__ void run_scores(const ChunkParams& p, const ChunkWork& w, ChunkBars* bars,
                            uint32_t tmem, uint32_t base, volatile int* abort_flag, int tile) {
   using C = ChunkCfg<D>;
+  constexpr int N = kPiece<SCORED>;
   const int total = __shfl_sync(0xffffffffu, w.total, 0);
-  const int steps = __shfl_sync(0xffffffffu, w.steps[tile], 0);
-  const uint32_t to = __shfl_sync(0xffffffffu, tmem, 0) + C::kTmemS + tile * 128;
+  const int skip = total - __shfl_sync(0xffffffffu, w.steps[tile], 0);
+  const uint32_t to = __shfl_sync(0xffffffffu, tmem, 0) + C::kTmemS + tile * kKeys;
+  constexpr uint32_t kIdesc = idesc_f16kind_f32(128, N, false, false, true);
   const uint64_t qd = smem_desc_sw128(base + C::kQ + tile * C::kTileBytes, 16, 1024);
   const uint64_t qs = sums_desc(base + C::kQSums + tile * C::kSumBytes);
-  bool ok = steps == 0 || wait_all(&bars->q_full[tile], 0, abort_flag, p);
+  bool ok = skip == total || wait_all(&bars->q_full[tile], 0, abort_flag, p);
   for (int s = 0; s < total && ok; ++s) {
     const int st = s % kStages;
     ok = wait_all(&bars->k_full[st], (uint32_t)(s / kStages) & 1u, abort_flag, p);
-    if (!ok) break;
-    if (s >= steps) {
-      if (elect_one()) mbar_arrive(smem_u32(&bars->k_empty[st]));
-      __syncwarp();
-      continue;
-    }
-    if (s > 0) ok = wait_all(&bars->pv_done[tile], (uint32_t)(s - 1) & 1u, abort_flag, p);
-    if (!ok) break;
-    tc_fence_after();
     const uint64_t kd = smem_desc_sw128(base + C::kK + st * C::kTileBytes, 16, 1024);
     const uint64_t ks = sums_desc(base + C::kKSums + st * C::kSumBytes);
-    if (elect_one()) {
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        const uint32_t off = ((k >> 2) * C::kBoxBytes + (k & 3) * 32) >> 4;
-        mma_ss(to, qd + off, kd + off, C::kIdescS, k > 0 ? 1u : 0u);
+    for (int h = 0; h < kPieces<SCORED>; ++h) {
+      if (!ok || s < skip) break;
+      if (s > skip)
+        ok = wait_all(&bars->pv_done[tile][h], (uint32_t)(s - 1 - skip) & 1u, abort_flag, p);
+      if (!ok) break;
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = ((k >> 2) * C::kBoxBytes + (k & 3) * 32) >> 4;
+          mma_ss(to + h * N, qd + off, kd + off + (h * N * 128 >> 4), kIdesc, k > 0 ? 1u : 0u);
+        }
+        mma_ss(to + h * N, qs, ks + (h * N * 16 >> 4), kIdesc, 1u);
+        mma_commit(smem_u32(&bars->s_full[tile][h]));
       }
-      mma_ss(to, qs, ks, C::kIdescS, 1u);
-      mma_commit(smem_u32(&bars->s_full[tile]));
-      mma_commit(smem_u32(&bars->k_empty[st]));
+      __syncwarp();
     }
+    if (ok && elect_one()) mma_commit(smem_u32(&bars->k_empty[st]));
     __syncwarp();
   }
   drain(&bars->drain[tile]);
 }
 
-template <int D>
+template <int D, bool SCORED>
 __device__ void run_values(const ChunkParams& p, const ChunkWork& w, ChunkBars* bars,
                            uint32_t tmem, uint32_t base, volatile int* abort_flag, int tile) {
   using C = ChunkCfg<D>;
+  constexpr int N = kPiece<SCORED>;
   const int total = __shfl_sync(0xffffffffu, w.total, 0);
-  const int steps = __shfl_sync(0xffffffffu, w.steps[tile], 0);
+  const int skip = total - __shfl_sync(0xffffffffu, w.steps[tile], 0);
   tmem = __shfl_sync(0xffffffffu, tmem, 0);
-  const uint32_t from = tmem + C::kTmemS + tile * 128, to = tmem + C::kTmemO + tile * D;
+  const uint32_t from = tmem + C::kTmemS + tile * kKeys, to = tmem + C::kTmemO + tile * D;
   bool ok = true;
   for (int s = 0; s < total && ok; ++s) {
     const int st = s % kStages;
     ok = wait_all(&bars->v_full[st], (uint32_t)(s / kStages) & 1u, abort_flag, p);
-    if (!ok) break;
-    if (s >= steps) {
-      if (elect_one()) mbar_arrive(smem_u32(&bars->v_empty[st]));
-      __syncwarp();
-      continue;
-    }
     uint32_t bf16 = 0;  // by 32 tokens
 #pragma unroll
     for (int c = 0; c < 4; ++c) bf16 |= bars->info[s % kInfos][c].v_bf16 << c;
     bf16 = __shfl_sync(0xffffffffu, bf16, 0);
     const uint64_t vd = smem_desc_sw128(base + C::kV + st * C::kTileBytes, C::kBoxBytes, 1024);
-    ok = wait_all(&bars->p_full[tile], (uint32_t)s & 1u, abort_flag, p);
-    if (!ok) break;
-    tc_fence_after();
-    if (elect_one()) {
-      // 16 tokens each (tokens 64 on: 64 columns on)
-      if (bf16 == 0u) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          mma_ts(to, from + (k & 3) * 8 + (k >> 2) * 64, vd + (uint32_t)(k * 2048 >> 4),
-                 C::kIdescO16, s > 0 || k > 0 ? 1u : 0u);
-      } else {
-        for (int k = 0; k < 8; ++k)
-          mma_ts(to, from + (k & 3) * 8 + (k >> 2) * 64, vd + (uint32_t)(k * 2048 >> 4),
-                 bf16 >> (k >> 1) & 1u ? C::kIdescOBf : C::kIdescO16, s > 0 || k > 0 ? 1u : 0u);
+    for (int h = 0; h < kPieces<SCORED>; ++h) {
+      if (!ok || s < skip) break;
+      ok = wait_all(&bars->p_full[tile][h], (uint32_t)(s - skip) & 1u, abort_flag, p);
+      if (!ok) break;
+      tc_fence_after();
+      if (elect_one()) {
+        // 16 tokens each; whole steps have tokens 64 on 64 columns on
+        auto product = [&](int k, uint32_t idesc) {
+          const int at = N == 64 ? h * N + k * 8 : (k & 3) * 8 + (k >> 2) * 64;
+          mma_ts(to, from + at, vd + (uint32_t)((h * N / 16 + k) * 2048 >> 4), idesc,
+                 s > skip || h > 0 || k > 0 ? 1u : 0u);
+        };
+        if (bf16 == 0u) {
+#pragma unroll
+          for (int k = 0; k < N / 16; ++k) product(k, C::kIdescO16);
+        } else {
+          for (int k = 0; k < N / 16; ++k)
+            product(k, bf16 >> (h * N / 32 + (k >> 1)) & 1u ? C::kIdescOBf : C::kIdescO16);
+        }
+        mma_commit(smem_u32(&bars->pv_done[tile][h]));
       }
-      mma_commit(smem_u32(&bars->pv_done[tile]));
-      mma_commit(smem_u32(&bars->v_empty[st]));
+      __syncwarp();
     }
+    if (ok && elect_one()) mma_commit(smem_u32(&bars->v_empty[st]));
     __syncwarp();
   }
   drain(&bars->drain[2 + tile]);
@@ -739,91 +789,112 @@ __device__ __forceinline__ void write_nothing(const ChunkParams& p, const ChunkW
   p.lse[at] = -INFINITY;
 }
 
-template <int D, int NG, bool SCORED>
-__device__ void run_softmax(const ChunkParams& p, const ChunkWork& w, ChunkBars* bars,
-                            uint32_t tmem, uint32_t base, volatile int* abort_flag) {
-  using C = ChunkCfg<D>;
-  constexpr int DH = D / 2;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int tile = warp / kSoftmaxWarps;
-  // 16 of the 32 rows of this warp's part of tensor memory; lanes 16 on take the same
-  // rows' tokens 64 to 127 and the second half of the channels
-  const int row_in = (warp & 3) * 32 + (warp >> 2 & 1) * 16, half = lane >> 4;
-  const int r = row_in + (lane & 15);
-  const int steps = w.steps[tile], both = min(w.steps[0], w.steps[1]);
-  if (steps == 0) {
-    if (half == 0) write_nothing<D>(p, w, tile, r);
-    return;
-  }
-  load_queries<D, NG>(p, w, bars, base, tile, row_in);
-  const int row = w.row0 + tile * kTileRows + r;
-  const int t = row / p.G, g = row - t * p.G;
-  const bool there = row < w.rows;
-  // (rows without a query: all keys, with scores of zero)
-  const int lim = there ? w.limit(t) : 0x7FFFFFFF;
-  const int pos = w.first_pos + t;
-  const float row_factor = ldexpf(p.scale_log2, -bars->query_shift[tile * kTileRows + r]);
-  float slope = 0.0f;
-  if constexpr (SCORED) {
-    if (p.slopes && there) slope = load(p.slopes + w.h * p.G + g) * 1.4426950408889634f;
-  }
-  const float inv_cap = SCORED && p.cap_log2 > 0.0f ? 1.0f / p.cap_log2 : 0.0f;
-  const uint32_t lanes = (uint32_t)row_in << 16;
-  const uint32_t tS = tmem + C::kTmemS + tile * 128 + lanes;
-  const uint32_t tO = tmem + C::kTmemO + tile * D + lanes;
-  const uint32_t kNegInf = 0xff800000u;
-  constexpr unsigned kAll = 0xffffffffu;
+// A softmax thread's row.
+struct ChunkRow {
+  int tile, half, row_in, row, t, g;  // row_in: the warp's first row of the tile
+  bool there;                         // there is a query
+  int lim, pos;                       // last position that it sees, its own
+  float factor;                       // of the products, but for the keys' power of two
+  float slope, inv_cap;
+  uint32_t s, o;                      // its warp's part of tensor memory
+  float m;       // reference: a maximum of scores (base 2) so far, or up to kLagBits below
+  uint64_t sum;  // of the weights of this half, two partial sums
 
-  // SCORED: 32 products to scores in base 2: `f` is their factor, d0 the distance of the
-  // first key from the query, `past` whether keys behind the query are seen.
-  auto score = [&](uint32_t (&x)[32], float f, int d0, bool past) {
-    if (p.cap_log2 > 0.0f) {
-      const float k = f * inv_cap;
-      float big = 0.0f;
+  // the row's new maximum: what was weighed before is to be multiplied by this
+  __device__ __forceinline__ float move_to(float top, bool moves) {
+    if (!moves) return 1.0f;
+    const float f = ex2_approx(m - top);  // (0 from no reference)
+    m = top;
+    sum = f2_mul(sum, f2_pack(f, f));
+    return f;
+  }
+  __device__ __forceinline__ float reference() const { return m == -INFINITY ? 0.0f : m; }
+  // of tokens first .. first + 31 those that the row sees (pieces: bits 0, 1: 16 tokens are there)
+  __device__ __forceinline__ uint32_t seen(int first, uint32_t pieces) const {
+    const int last = lim - first;
+    uint32_t m32 = last >= 31 ? 0xFFFFFFFFu : last < 0 ? 0u : (2u << last) - 1u;
+    if (!(pieces & 1u)) m32 &= 0xFFFF0000u;
+    if (!(pieces & 2u)) m32 &= 0x0000FFFFu;
+    return m32;
+  }
+  template <int DH>
+  __device__ __forceinline__ void rescale(float f) const {
+#pragma unroll 1
+    for (int k = 0; k < DH; k += 16) {
+      uint32_t x[16];
+      tmem_ld16x2_16<DH>(o + k, x);
+      tmem_wait_ld();
+      reg_fence(x, 16);
 #pragma unroll
-      for (int i = 0; i < 32; i += 2)
-        big = max3(big, fabsf(__uint_as_float(x[i])), fabsf(__uint_as_float(x[i + 1])));
-      if (__any_sync(0xffffffffu, !(big * k <= kTanhRange))) {
+      for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
+      tmem_st16x2_16<DH>(o + k, x);
+    }
+  }
+};
+__device__ __forceinline__ void hide(uint32_t (&x)[32], uint32_t seen) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-          x[i] = __float_as_uint(p.cap_log2 * tanh_any(__uint_as_float(x[i]) * k));
+  for (int i = 0; i < 32; ++i) x[i] = seen >> i & 1u ? x[i] : 0xff800000u;  // -inf
+}
+// (not zero: what is hidden is -inf times it)
+__device__ __forceinline__ float at_least_normal(float x) { return fmaxf(x, 1.17549435e-38f); }
+
+// 32 products to scores in base 2: `f` is their factor, d0 the distance of the first key
+// from the query, `past` whether keys behind the query are seen.
+__device__ __forceinline__ void score(const ChunkParams& p, const ChunkRow& r, uint32_t (&x)[32],
+                                      float f, int d0, bool past) {
+      if (p.cap_log2 > 0.0f) {
+        const float k = f * r.inv_cap;
+        float big = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 32; i += 2)
+          big = max3(big, fabsf(__uint_as_float(x[i])), fabsf(__uint_as_float(x[i + 1])));
+        if (__any_sync(0xffffffffu, !(big * k <= kTanhRange))) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            x[i] = __float_as_uint(p.cap_log2 * tanh_any(__uint_as_float(x[i]) * k));
+        } else {
+          const uint64_t k2 = f2_pack(k, k), f2 = f2_pack(f, f);
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const uint64_t raw = f2_pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+            const uint64_t y = f2_mul(raw, k2), u = f2_mul(y, y);
+            uint64_t a = f2_fma(f2_pack(kTanh5, kTanh5), u, f2_pack(kTanh4, kTanh4));
+            a = f2_fma(a, u, f2_pack(kTanh3, kTanh3));
+            a = f2_fma(a, u, f2_pack(kTanh2, kTanh2));
+            a = f2_fma(a, u, f2_pack(kTanh1, kTanh1));
+            a = f2_fma(a, u, f2_pack(kTanh0, kTanh0));
+            a = f2_mul(a, f2_mul(raw, f2));
+            float lo, hi;
+            f2_unpack(a, lo, hi);
+            x[i] = __float_as_uint(lo), x[i + 1] = __float_as_uint(hi);
+          }
+        }
       } else {
-        const uint64_t k2 = f2_pack(k, k), f2 = f2_pack(f, f);
 #pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          const uint64_t raw = f2_pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1]));
-          const uint64_t y = f2_mul(raw, k2), u = f2_mul(y, y);
-          uint64_t a = f2_fma(f2_pack(kTanh5, kTanh5), u, f2_pack(kTanh4, kTanh4));
-          a = f2_fma(a, u, f2_pack(kTanh3, kTanh3));
-          a = f2_fma(a, u, f2_pack(kTanh2, kTanh2));
-          a = f2_fma(a, u, f2_pack(kTanh1, kTanh1));
-          a = f2_fma(a, u, f2_pack(kTanh0, kTanh0));
-          a = f2_mul(a, f2_mul(raw, f2));
-          float lo, hi;
-          f2_unpack(a, lo, hi);
-          x[i] = __float_as_uint(lo), x[i + 1] = __float_as_uint(hi);
+        for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
+      }
+      if (p.slopes) {
+        if (__any_sync(0xffffffffu, r.slope != 0.0f && past)) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            x[i] = __float_as_uint(fmaf(-r.slope, fabsf((float)(d0 + i)), __uint_as_float(x[i])));
+        } else {
+          const float b0 = r.slope * (float)d0;
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            x[i] = __float_as_uint(__uint_as_float(x[i]) + fmaf(r.slope, (float)i, b0));
         }
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
-    }
-    if (p.slopes) {
-      if (__any_sync(0xffffffffu, slope != 0.0f && past)) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          x[i] = __float_as_uint(fmaf(-slope, fabsf((float)(d0 + i)), __uint_as_float(x[i])));
-      } else {
-        const float b0 = slope * (float)d0;
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          x[i] = __float_as_uint(__uint_as_float(x[i]) + fmaf(slope, (float)i, b0));
-      }
-    }
-  };
+}
 
-  float m = -INFINITY;  // reference: a maximum of scores (base 2) so far, or up to kLagBits below
-  uint64_t sum2 = 0;    // of the weights of this half
+constexpr unsigned kAll = 0xffffffffu;
+
+// The softmax by whole steps: 64 of a row's 128 scores a thread (tokens 64 half on).
+template <int D>
+__device__ bool softmax_steps(const ChunkParams& p, const ChunkWork& w, ChunkBars* bars, ChunkRow& r,
+                              volatile int* abort_flag) {
+  const int lane = threadIdx.x & 31, tile = r.tile;
+  const int steps = w.steps[tile], skip = w.total - steps, both = min(w.steps[0], w.steps[1]);
   // What a step needs besides its scores: read while the tensor core works on them.
   TokenInfo info[2];
   float factor[2];
@@ -833,35 +904,34 @@ __device__ void run_softmax(const ChunkParams& p, const ChunkWork& w, ChunkBars*
       return false;
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      info[c] = bars->info[s % kInfos][2 * half + c];
-      // (not zero: what is hidden is -inf times it)
-      factor[c] = fmaxf(row_factor * info[c].factor, 1.17549435e-38f);
+      info[c] = bars->info[s % kInfos][2 * r.half + c];
+      factor[c] = at_least_normal(r.factor * info[c].factor);
     }
-    const int rel = lim - ((w.j0 + s) * kKeys + 64 * half);
+    const int rel = r.lim - (w.first_key(s) + 64 * r.half);
     whole = __all_sync(kAll, rel >= 63 && (info[0].there & info[1].there) == 3u);
     any_bf16 = __any_sync(kAll, (info[0].v_bf16 | info[1].v_bf16) != 0u);
     // Weights are formed beside the reference of the steps before, without a look for
     // the maximum; with one where their sum shows that scores rose far above it, where
-    // there is no reference yet, and where scores are to be masked, capped or biased
-    // first (they go back to tensor memory for that).
-    look = SCORED || !whole || __any_sync(kAll, m == -INFINITY);
+    // there is no reference yet, and where scores are to be masked first (they go back to
+    // tensor memory for that).
+    look = !whole || __any_sync(kAll, r.m == -INFINITY);
     return true;
   };
-  if (!prepare(0)) return;
+  if (!prepare(skip)) return false;
 #pragma unroll 1
-  for (int s = 0; s < steps; ++s) {
+  for (int n = 0; n < steps; ++n) {  // (steps from `skip` on)
     // The row tiles' softmaxes take turns: while one has the issue slots, the tensor core
-    // works for the other.
-    const bool turns = s < both && (tile == 1 || s > 0);
-    if (!wait_both(&bars->s_full[tile], (uint32_t)s & 1u,
-                   turns ? &bars->turn[tile] : &bars->s_full[tile],
-                   (uint32_t)(turns && tile == 0 ? s - 1 : s) & 1u, abort_flag, p))
-      return;
+    // works for the other.  (Odd lanes wait for the turn.)
+    const int first_turn = steps - both;  // steps before it are this tile's alone
+    const int k = n - first_turn;
+    const bool turns = k >= 0 && (tile == 1 || k > 0) && (threadIdx.x & 1);
+    if (!wait_all(turns ? &bars->turn[tile] : &bars->s_full[tile][0],
+                  (uint32_t)(turns ? (tile ? k : k - 1) : n) & 1u, abort_flag, p))
+      return false;
     tc_fence_after();
-    const int key0 = (w.j0 + s) * kKeys + 64 * half;
-    const int rel = lim - key0;  // of this half's keys those up to rel are seen
+    const int key0 = w.first_key(n + skip) + 64 * r.half;
     uint32_t weights[32];
-    bool hand = s < both;  // the other tile's turn is to come
+    bool hand = k >= 0;  // the other tile's turn is to come
     uint64_t part;
     for (;;) {
       if (look) {
@@ -869,54 +939,28 @@ __device__ void run_softmax(const ChunkParams& p, const ChunkWork& w, ChunkBars*
 #pragma unroll 1
         for (int c = 0; c < 2; ++c) {
           uint32_t x[32];
-          tmem_ld16x2_32<64>(tS + 32 * c, x);
-          const float f = c ? factor[1] : factor[0];
+          tmem_ld16x2_32<64>(r.s + 32 * c, x);
           tmem_wait_ld();
           reg_fence(x, 32);
-          if constexpr (SCORED)
-            score(x, f, key0 + 32 * c - pos, min(lim, key0 + 32 * c + 31) > pos);
           if (!whole) {
-            const int last = rel - 32 * c;
-            const uint32_t there16 = c ? info[1].there : info[0].there;
-            uint32_t seen = last >= 31 ? 0xFFFFFFFFu : last < 0 ? 0u : (2u << last) - 1u;
-            if (!(there16 & 1u)) seen &= 0xFFFF0000u;
-            if (!(there16 & 2u)) seen &= 0x0000FFFFu;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = seen >> i & 1u ? x[i] : kNegInf;
+            hide(x, r.seen(key0 + 32 * c, c ? info[1].there : info[0].there));
+            tmem_st16x2_32<64>(r.s + 32 * c, x);
           }
-          if (SCORED || !whole) tmem_st16x2_32<64>(tS + 32 * c, x);
-          top = fmaxf(top, largest32(x) * (SCORED ? 1.0f : f));
+          top = fmaxf(top, largest32(x) * (c ? factor[1] : factor[0]));
         }
-        if (SCORED || !whole) tmem_wait_st();
+        if (!whole) tmem_wait_st();
         top = fmaxf(top, __shfl_xor_sync(kAll, top, 16));
-        const bool moves = top > m + kLagBits;
-        if (__any_sync(kAll, moves)) {
-          float f = 1.0f;
-          if (moves) {
-            f = ex2_approx(m - top);  // (0 from no reference)
-            m = top;
-            sum2 = f2_mul(sum2, f2_pack(f, f));
-          }
-          if (s > 0) {  // (O is complete: the step's scores waited for the last step's product)
-#pragma unroll 1
-            for (int k = 0; k < DH; k += 16) {
-              uint32_t o[16];
-              tmem_ld16x2_16<DH>(tO + k, o);
-              tmem_wait_ld();
-              reg_fence(o, 16);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-              tmem_st16x2_16<DH>(tO + k, o);
-            }
-          }
-        }
+        const bool moves = top > r.m + kLagBits;
+        const bool any = __any_sync(kAll, moves);
+        const float f = r.move_to(top, moves);
+        // (O is complete: the step's scores waited for the last step's product)
+        if (any && n > 0) r.template rescale<D / 2>(f);
       }
-      const float reference = m == -INFINITY ? 0.0f : m;
-      const uint64_t nm2 = f2_pack(-reference, -reference);
+      const uint64_t nm2 = f2_pack(-r.reference(), -r.reference());
       auto weigh = [&](auto type) {
         uint64_t parts[2] = {0, 0};
         uint32_t x[2][16];
-        tmem_ld16x2_16<64>(tS, x[0]);
+        tmem_ld16x2_16<64>(r.s, x[0]);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {  // 16 at once, the next 16 on their way
           uint32_t(&now)[16] = x[c & 1];
@@ -926,13 +970,13 @@ __device__ void run_softmax(const ChunkParams& p, const ChunkWork& w, ChunkBars*
           }
           tmem_wait_ld();
           reg_fence(now, 16);
-          if (c < 3) tmem_ld16x2_16<64>(tS + 16 * (c + 1), x[(c + 1) & 1]);
+          if (c < 3) tmem_ld16x2_16<64>(r.s + 16 * (c + 1), x[(c + 1) & 1]);
           const uint64_t f2 = f2_pack(factor[c / 2], factor[c / 2]);
 #pragma unroll
           for (int i = 0; i < 16; i += 2) {
-            const uint64_t v = f2_pack(__uint_as_float(now[i]), __uint_as_float(now[i + 1]));
             float a, b;
-            f2_unpack(SCORED ? f2_add(v, nm2) : f2_fma(v, f2, nm2), a, b);
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(now[i]), __uint_as_float(now[i + 1])), f2, nm2),
+                      a, b);
             a = ex2_approx(a), b = ex2_approx(b);
             parts[i / 2 & 1] = f2_add(parts[i / 2 & 1], f2_pack(a, b));
             weights[8 * c + i / 2] = pack_f16x2(a, b);
@@ -951,41 +995,179 @@ __device__ void run_softmax(const ChunkParams& p, const ChunkWork& w, ChunkBars*
       if (look || !__any_sync(kAll, !(a + b <= kMostSum))) break;  // (NaN: look, too)
       look = true;
     }
-    sum2 = f2_add(sum2, part);
-    tmem_st16x2_32<64>(tS, weights);
+    r.sum = f2_add(r.sum, part);
+    tmem_st16x2_32<64>(r.s, weights);
     tmem_wait_st();
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&bars->p_full[tile]));
-    if (s + 1 < steps && !prepare(s + 1)) return;
+    if (lane == 0) mbar_arrive(smem_u32(&bars->p_full[tile][0]));
+    if (n + 1 < steps && !prepare(n + 1 + skip)) return false;
   }
+  return wait_all(&bars->pv_done[tile][0], (uint32_t)(steps - 1) & 1u, abort_flag, p);
+}
 
-  if (!wait_all(&bars->pv_done[tile], (uint32_t)(steps - 1) & 1u, abort_flag, p)) return;
+// The softmax by half steps, scores capped and biased: 32 of a row's 64 a thread (tokens 32
+// half on).
+template <int D>
+__device__ bool softmax_halves(const ChunkParams& p, const ChunkWork& w, ChunkBars* bars,
+                               ChunkRow& r, volatile int* abort_flag) {
+  constexpr int N = kPiece<true>;
+  const int lane = threadIdx.x & 31, tile = r.tile;
+  const int steps = w.steps[tile], skip = w.total - steps;
+  // What a step needs besides its scores, of this thread's 32 tokens of each half: read
+  // while the tensor core works on them.
+  float factor[2];
+  uint32_t bits = 0;  // by half: 0, 1: 16 tokens are there; 2: V is bf16
+  bool plain[2], bf16[2];  // all rows see all tokens; V is bf16 for some
+  auto prepare = [&](int s) -> bool {
+    if (!wait_all(&bars->info_full[s % kInfos], (uint32_t)(s / kInfos) & 1u, abort_flag, p))
+      return false;
+    const int rel = r.lim - (w.first_key(s) + 32 * r.half);
+    bits = 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const TokenInfo info = bars->info[s % kInfos][2 * h + r.half];
+      factor[h] = at_least_normal(r.factor * info.factor);
+      bits |= (info.there | info.v_bf16 << 2) << (4 * h);
+      plain[h] = __all_sync(kAll, rel - N * h >= 31 && info.there == 3u);
+      bf16[h] = __any_sync(kAll, info.v_bf16 != 0u);
+    }
+    return true;
+  };
+  if (!prepare(skip)) return false;
+#pragma unroll 1
+  for (int u = 0; u < 2 * steps; ++u) {
+    const int n = u >> 1, h = u & 1;  // the tile's n-th step, its half
+    if (!wait_all(&bars->s_full[tile][h], (uint32_t)n & 1u, abort_flag, p)) return false;
+    tc_fence_after();
+    uint32_t x[32];
+    tmem_ld16x2_32<32>(r.s + h * N, x);
+    const int key0 = w.first_key(n + skip) + h * N + 32 * r.half;
+    const float f = h ? factor[1] : factor[0];
+    const uint32_t my_bits = bits >> (4 * h);
+    tmem_wait_ld();
+    reg_fence(x, 32);
+    score(p, r, x, f, key0 - r.pos, min(r.lim, key0 + 31) > r.pos);
+    if (!(h ? plain[1] : plain[0])) hide(x, r.seen(key0, my_bits));
+    // Weights are formed beside the reference of the tokens before, without a look for
+    // the maximum; with one where their sum shows that scores rose far above it, or where
+    // there is no reference yet.
+    uint32_t weights[16];
+    uint64_t part;
+    auto weigh = [&](auto type) {
+      const uint64_t nm2 = f2_pack(-r.reference(), -r.reference());
+      uint64_t parts[2] = {0, 0};
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        const uint64_t v = f2_pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+        float a, b;
+        f2_unpack(f2_add(v, nm2), a, b);
+        a = ex2_approx(a), b = ex2_approx(b);
+        parts[i / 2 & 1] = f2_add(parts[i / 2 & 1], f2_pack(a, b));
+        weights[i / 2] = pack_f16x2(a, b);
+        if (decltype(type)::value && my_bits & 4u) weights[i / 2] = pack_bf16x2(a, b);
+      }
+      part = f2_add(parts[0], parts[1]);
+    };
+    for (;;) {
+      if (h ? bf16[1] : bf16[0])
+        weigh(std::true_type{});
+      else
+        weigh(std::false_type{});
+      float a, b;
+      f2_unpack(part, a, b);
+      // (a sum that is not a number too)
+      if (!__any_sync(kAll, r.m == -INFINITY || !(a + b <= kMostSum))) break;
+      float top = largest32(x);
+      top = fmaxf(top, __shfl_xor_sync(kAll, top, 16));
+      const bool moves = top > r.m + kLagBits;
+      if (!__any_sync(kAll, moves)) break;
+      const float g = r.move_to(top, moves);
+      if (u > 0) {  // O, once the product before is complete
+        if (!wait_all(&bars->pv_done[tile][1 - h], (uint32_t)(u - 1 >> 1) & 1u, abort_flag, p))
+          return false;
+        tc_fence_after();
+        r.template rescale<D / 2>(g);
+      }
+    }
+    r.sum = f2_add(r.sum, part);
+    tmem_st16x2_16<16>(r.s + h * N, weights);
+    tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&bars->p_full[tile][h]));
+    if (h == 1 && n + 1 < steps && !prepare(n + 1 + skip)) return false;
+  }
+  return wait_all(&bars->pv_done[tile][1], (uint32_t)(steps - 1) & 1u, abort_flag, p);
+}
+
+template <int D, int NG, bool SCORED>
+__device__ void run_softmax(const ChunkParams& p, const ChunkWork& w, ChunkBars* bars,
+                            uint32_t tmem, uint32_t base, volatile int* abort_flag) {
+  using C = ChunkCfg<D>;
+  constexpr int DH = D / 2;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  ChunkRow r;
+  r.tile = warp / kSoftmaxWarps;
+  // 16 of the 32 rows of this warp's part of tensor memory; lanes 16 on take the same
+  // rows' second half of a piece's tokens and of the channels
+  r.row_in = (warp & 3) * 32 + (warp >> 2 & 1) * 16;
+  r.half = lane >> 4;
+  const int in = r.row_in + (lane & 15);
+  if (w.steps[r.tile] == 0) {
+    if (r.half == 0) write_nothing<D>(p, w, r.tile, in);
+    return;
+  }
+  load_queries<D, NG>(p, w, bars, base, r.tile, r.row_in);
+  r.row = w.row0 + r.tile * kTileRows + in;
+  r.t = r.row / p.G;
+  r.g = r.row - r.t * p.G;
+  r.there = r.row < w.rows;
+  // (rows without a query: all keys, with scores of zero)
+  r.lim = r.there ? w.limit(r.t) : 0x7FFFFFFF;
+  r.pos = w.first_pos + r.t;
+  r.factor = ldexpf(p.scale_log2, -bars->query_shift[r.tile * kTileRows + in]);
+  r.slope = r.inv_cap = 0.0f;
+  if constexpr (SCORED) {
+    if (p.slopes && r.there) r.slope = load(p.slopes + w.h * p.G + r.g) * 1.4426950408889634f;
+    if (p.cap_log2 > 0.0f) r.inv_cap = 1.0f / p.cap_log2;
+  }
+  const uint32_t lanes = (uint32_t)r.row_in << 16;
+  r.s = tmem + C::kTmemS + r.tile * kKeys + lanes;
+  r.o = tmem + C::kTmemO + r.tile * D + lanes;
+  r.m = -INFINITY;
+  r.sum = 0;
+  if constexpr (SCORED) {
+    if (!softmax_halves<D>(p, w, bars, r, abort_flag)) return;
+  } else {
+    if (!softmax_steps<D>(p, w, bars, r, abort_flag)) return;
+  }
+  // ---- the results
   tc_fence_after();
   float s0, s1;
-  f2_unpack(sum2, s0, s1);
+  f2_unpack(r.sum, s0, s1);
   float sum = s0 + s1;
   sum += __shfl_xor_sync(kAll, sum, 16);
   const float v_scale = bars->v_scale;
   const float inv = sum == 0.0f ? 0.0f : v_scale / sum;
-  float* slot = p.partial + w.slot * (kCtaRows * (D + 2)) + tile * kTileRows + r;
+  float* slot = p.partial + w.slot * (kCtaRows * (D + 2)) + r.tile * kTileRows + in;
   const bool partial = p.splits > 1;
-  const int64_t at = ((int64_t)w.b * p.H + w.h * p.G + g) * p.T + t;
-  if (there && half == 0) {
+  const int64_t at = ((int64_t)w.b * p.H + w.h * p.G + r.g) * p.T + r.t;
+  if (r.there && r.half == 0) {
     if (partial) {
-      slot[0] = m;
+      slot[0] = r.m;
       slot[kCtaRows] = sum;
     } else {
-      p.lse[at] = (m + __log2f(sum)) * kLn2;
+      p.lse[at] = (r.m + __log2f(sum)) * kLn2;
     }
   }
 #pragma unroll 1
   for (int k = 0; k < DH; k += 16) {
     uint32_t o[16];
-    tmem_ld16x2_16<DH>(tO + k, o);
+    tmem_ld16x2_16<DH>(r.o + k, o);
     tmem_wait_ld();
     reg_fence(o, 16);
-    const int c = half * DH + k;
+    const int c = r.half * DH + k;
     // channels from the codes' order
     float x[16];
 #pragma unroll
@@ -994,21 +1176,21 @@ __device__ void run_softmax(const ChunkParams& p, const ChunkWork& w, ChunkBars*
       x[i] = __uint_as_float(o[(i & 8) + (k8 < 4 ? 2 * k8 : 2 * k8 - 7)]) * (partial ? v_scale : inv);
     }
     const int nan_from = bars->nan_from[c / (D / NG)];
-    if (lim >= nan_from) {
+    if (r.lim >= nan_from) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) x[i] = __int_as_float(0x7FC00000);
     }
-    if (there && partial) {
+    if (r.there && partial) {
       float4* dst = reinterpret_cast<float4*>(p.partial + w.slot * (kCtaRows * (D + 2)) +
-                                              2 * kCtaRows + (tile * kTileRows + r) * D + c);
+                                              2 * kCtaRows + (r.tile * kTileRows + in) * D + c);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         dst[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-    } else if (there) {
+    } else if (r.there) {
       write_row<D>(p, at, x, c);
     }
   }
-  if (!there && half == 0) write_nothing<D>(p, w, tile, r);  // behind the count
+  if (!r.there && r.half == 0) write_nothing<D>(p, w, r.tile, in);  // behind the count
 }
 
 template <int D, int NG, bool SCORED>
@@ -1037,10 +1219,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Chunk
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&bars->q_full[i]), kSoftmaxWarps);
-      mbar_init(smem_u32(&bars->s_full[i]), 1);
-      mbar_init(smem_u32(&bars->p_full[i]), kSoftmaxWarps);
-      mbar_init(smem_u32(&bars->pv_done[i]), 1);
       mbar_init(smem_u32(&bars->turn[i]), kSoftmaxWarps);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(smem_u32(&bars->s_full[i][h]), 1);
+        mbar_init(smem_u32(&bars->p_full[i][h]), kSoftmaxWarps);
+        mbar_init(smem_u32(&bars->pv_done[i][h]), 1);
+      }
     }
     for (int i = 0; i < kInfos; ++i) mbar_init(smem_u32(&bars->info_full[i]), 8);
     for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&bars->drain[i]), 1);
@@ -1060,10 +1244,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Chunk
   volatile int* abort_flag = &bars->abort_flag;
 
   if (warp < kWarpK) {
-    regs_inc<kSoftmaxRegs>();
+    regs_inc<kSoftmaxRegs<NG, SCORED>>();
     run_softmax<D, NG, SCORED>(p, w, bars, tmem, base, abort_flag);
   } else if (warp < kWarpScores) {
-    regs_dec<kExpandRegs>();
+    regs_dec<kExpandRegs<NG, SCORED>>();
     if (warp < kWarpV)
       run_expand_keys<D, NG>(p, w, bars, base, abort_flag);
     else
@@ -1071,9 +1255,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Chunk
   } else {
     regs_dec<kIssueRegs>();
     if (warp < kWarpValues)
-      run_scores<D>(p, w, bars, tmem, base, abort_flag, warp - kWarpScores);
+      run_scores<D, SCORED>(p, w, bars, tmem, base, abort_flag, warp - kWarpScores);
     else
-      run_values<D>(p, w, bars, tmem, base, abort_flag, warp - kWarpValues);
+      run_values<D, SCORED>(p, w, bars, tmem, base, abort_flag, warp - kWarpValues);
   }
   __syncwarp();
   tc_fence_before();

@@ -19,8 +19,8 @@ LIBDIR = os.path.join(_PKG, "_lib")
 LIB = os.path.join(LIBDIR, "libbsattn.so")
 
 SOURCES = ["api.cu", "plan.cu", "fwd_sm103.cu", "bwd_sm103.cu", "noalloc.cu", "pipeline.cu",
-           "rope.cu", "select.cu", "kv4.cu", "kv4_attn.cu", "kv4_chunk.cu", "kv4_pages.cu"]
-HEADERS = ["ptx.cuh", "internal.h", "bwd.h", "ops.cuh", "kv4.cuh"]
+           "rope.cu", "select.cu", "kv4.cu", "kv4_attn.cu", "kv4_attn_scored.cu", "kv4_chunk.cu", "kv4_pages.cu"]
+HEADERS = ["ptx.cuh", "internal.h", "bwd.h", "ops.cuh", "kv4.cuh", "kv4_attn.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -47,4 +47,38 @@ __device__ __forceinline__ int page_at(const Kv4View& c, const int* table, int c
 // Host side: the checks of a cache that every call makes.
 bsattn_status check_cache(const bsattn_kv4_cache* c, Kv4View* view);
 
+// kv4_attn_scored.cu: bsattn_kv4_attn_chunk's arguments, checked, for few rows.
+struct FewRows {
+  const bsattn_kv4_cache* cache;
+  const void* q;
+  int B, H, T;
+  const int32_t* block_table;
+  int64_t table_stride;
+  int columns;
+  const int32_t* lengths;
+  const int32_t* counts;
+  const int32_t* prefix;
+  float scale, cap;
+  const float* slopes;
+  int out_f32;
+  void* out;
+  float* lse;
+};
+size_t kv4_few_rows_workspace(int B, int kv_heads, int rows, int D, int64_t tokens);
+bsattn_status kv4_few_rows(const FewRows& f, void* workspace, size_t workspace_bytes,
+                           cudaStream_t stream);
+
+// tanh(y) / y by y^2 for |y| <= 0.8, off by 6e-8 relative: least maximal relative
+// error, by Lawson's iteration.
+constexpr float kTanh0 = 0.99999994f, kTanh1 = -0.333326757f, kTanh2 = 0.13321048f,
+                kTanh3 = -0.0531143136f, kTanh4 = 0.0190932993f, kTanh5 = -0.00435529929f;
+constexpr float kTanhRange = 0.8f;
+
+// tanh(y): (1 - e) / (1 + e), e = exp(-2 |y|); off by 2^-22 of one or less.
+__device__ __forceinline__ float tanh_any(float y) {
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-2.8853900817779268f * fabsf(y)));
+  return copysignf(__fdividef(1.0f - e, 1.0f + e), y);
+}
+
 }  // namespace bsattn

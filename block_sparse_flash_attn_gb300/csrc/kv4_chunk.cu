@@ -736,18 +736,6 @@ __device__ __forceinline__ float largest32(const uint32_t (&x)[32]) {
   return fmaxf(max3(a[0], a[1], a[2]), a[3]);
 }
 
-// tanh(y) / y by y^2 for |y| <= 0.8, off by 5e-8 relative: least maximal relative
-// error, by Lawson's iteration.
-constexpr float kTanh0 = 0.99999994f, kTanh1 = -0.333326757f, kTanh2 = 0.13321048f,
-                kTanh3 = -0.0531143136f, kTanh4 = 0.0190932993f, kTanh5 = -0.00435529929f;
-constexpr float kTanhRange = 0.8f;
-
-// tanh(y): (1 - e) / (1 + e), e = exp(-2 |y|); off by 2^-22 of one or less.
-__device__ __forceinline__ float tanh_any(float y) {
-  const float e = ex2_approx(-2.8853900817779268f * fabsf(y));
-  return copysignf(__fdividef(1.0f - e, 1.0f + e), y);
-}
-
 // The row's results to `out` and `lse`, or to the partial result.
 template <int D>
 __device__ __forceinline__ void write_row(const ChunkParams& p, int64_t at, const float (&x)[16],
@@ -1331,6 +1319,13 @@ int chunk_splits(int64_t ctas, int64_t steps, int sms) {
   return best;
 }
 
+// Up to so many rows a key/value head the kernels of kv4_attn.cuh take the call: they read
+// the cache once for 16 rows.  8 sequences of 49152 tokens, 8 heads of 128: 16 rows 158 us,
+// 32 rows 296; here 350 us for up to 256.
+constexpr int64_t kFewRows = 32;
+constexpr int kMostFewRowsBatch = 4096;
+bool few_rows(int B, int64_t rows) { return rows <= kFewRows && B <= kMostFewRowsBatch; }
+
 struct ChunkSplit {
   int64_t items, ctas;
   int splits;
@@ -1382,9 +1377,9 @@ size_t bsattn_kv4_attn_chunk_workspace(int B, int H, int kv_heads, int T, int D,
     return 0;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  return chunk_split(B, kv_heads, (int64_t)(H / kv_heads) * T, (int64_t)columns * page_size, D,
-                     device_sm_count(dev))
-      .workspace;
+  const int64_t rows = (int64_t)(H / kv_heads) * T, tokens = (int64_t)columns * page_size;
+  if (few_rows(B, rows)) return kv4_few_rows_workspace(B, kv_heads, (int)rows, D, tokens);
+  return chunk_split(B, kv_heads, rows, tokens, D, device_sm_count(dev)).workspace;
 }
 
 bsattn_status bsattn_kv4_attn_chunk(const bsattn_kv4_cache* cache, const void* q, int B, int H,
@@ -1415,6 +1410,11 @@ bsattn_status bsattn_kv4_attn_chunk(const bsattn_kv4_cache* cache, const void* q
       (int64_t)columns * cache->page_size > (1ll << 31) - 2 * kKeys ||  // positions are 32-bit
       (int64_t)cache->pages * cache->kv_heads * cache->page_size / 16 >= (1ll << 31))
     return BSATTN_ERR_UNSUPPORTED;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (few_rows(B, rows))
+    return kv4_few_rows({cache, q, B, H, T, block_table, table_stride, columns, lengths, counts,
+                         prefix, scale, cap, slopes, (flags & BSATTN_OUT_F32) ? 1 : 0, out, lse},
+                        workspace, workspace_bytes, st);
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) return BSATTN_ERR_CUDA;
   const ChunkSplit split =
@@ -1445,7 +1445,6 @@ bsattn_status bsattn_kv4_attn_chunk(const bsattn_kv4_cache* cache, const void* q
   p.out_f32 = (flags & BSATTN_OUT_F32) ? 1 : 0;
   p.partial = static_cast<float*>(workspace);
   p.timeout_ns = kDefaultWaitTimeoutNs;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool scored = cap > 0.0f || slopes;
   const int groups = cache->head_dim / cache->group;
   cudaError_t e;

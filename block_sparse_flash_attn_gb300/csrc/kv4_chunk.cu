@@ -43,8 +43,11 @@
 // scores they come from) and O of both.  While one tile's softmax runs, the tensor
 // core works for the other.
 //
-// Few rows and long contexts: the tokens are cut into `splits` ranges, a CTA each,
-// whose partial results (maximum, sum, O) a second launch joins, in order.
+// Up to 128 rows a key/value head both row tiles hold the same rows and take every other
+// step, so that one's chain of products and softmax runs beside the other's.
+// Few rows and long contexts: the tokens are cut into `splits` ranges, a CTA each.
+// Partial results (maximum, sum, O) of ranges and tiles are joined, in order, by a second
+// launch.
 // Every wait is bounded; a wait that runs out is reported by bsattn_kv4_status.
 #include <cmath>
 #include <cstdint>
@@ -103,13 +106,14 @@ struct ChunkParams {
   int B, H, T, G;
   int items;           // row tiles (of kCtaRows) a key/value head
   int splits;
+  int twin;            // both row tiles hold the same rows (up to kTileRows)
   float scale_log2;    // |scale| log2 e, above 0
   float sign;          // of the scale
   float cap_log2;      // cap log2 e; 0: no cap
   void* out;
   float* lse;
   int out_f32;
-  float* partial;      // [B * Hkv * items * splits][kCtaRows * (D + 2)]
+  float* partial;      // [B * Hkv * items * splits][2 tiles][kTileRows * (D + 2)]; null: none
   unsigned long long timeout_ns;
 };
 
@@ -180,8 +184,15 @@ struct ChunkWork {
   int row0;                   // the CTA's first
   int64_t slot;               // partial result
   int j0;                     // the range's first 128 tokens: step s has j0 + total - 1 - s
-  int steps[2];               // of each row tile: the last ones
+  int steps[2];               // of each row tile: the last ones, or every other one
   int total;
+  bool twin;
+
+  __device__ __forceinline__ int first_row(int tile) const { return row0 + (twin ? 0 : tile * kTileRows); }
+  // the tile's n-th step
+  __device__ __forceinline__ int step_of(int tile, int n) const {
+    return twin ? 2 * n + tile : total - steps[tile] + n;
+  }
 
   __device__ __forceinline__ int first_key(int s) const { return (j0 + total - 1 - s) * kKeys; }
   __device__ __forceinline__ int limit(int t) const {  // last position that token t sees
@@ -211,10 +222,11 @@ __device__ __forceinline__ ChunkWork chunk_work(const ChunkParams& p) {
   if (w.len > room && threadIdx.x == 0) p.c.report();
   w.rows = p.G * w.count;
   w.row0 = item * kCtaRows;
+  w.twin = p.twin != 0;
   int most[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int first = w.row0 + i * kTileRows;
+    const int first = w.first_row(i);
     const int last = min(first + kTileRows, w.rows) - 1;
     const int lim = first < w.rows ? w.limit(last / p.G) : -1;
     most[i] = lim >= 0 ? lim / kKeys + 1 : 0;
@@ -225,6 +237,7 @@ __device__ __forceinline__ ChunkWork chunk_work(const ChunkParams& p) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) w.steps[i] = max(min(j1, most[i]) - w.j0, 0);
   w.total = max(w.steps[0], w.steps[1]);
+  if (w.twin) w.steps[0] = (w.total + 1) / 2, w.steps[1] = w.total / 2;
   return w;
 }
 
@@ -563,22 +576,24 @@ __device__ void run_scores(const ChunkParams& p, const ChunkWork& w, ChunkBars* 
   using C = ChunkCfg<D>;
   constexpr int N = kPiece<SCORED>;
   const int total = __shfl_sync(0xffffffffu, w.total, 0);
-  const int skip = total - __shfl_sync(0xffffffffu, w.steps[tile], 0);
+  const int steps = __shfl_sync(0xffffffffu, w.steps[tile], 0), twin = p.twin;
+  const int skip = total - steps;
+  int n = 0;  // the tile's steps so far
   const uint32_t to = __shfl_sync(0xffffffffu, tmem, 0) + C::kTmemS + tile * kKeys;
   constexpr uint32_t kIdesc = idesc_f16kind_f32(128, N, false, false, true);
   const uint64_t qd = smem_desc_sw128(base + C::kQ + tile * C::kTileBytes, 16, 1024);
   const uint64_t qs = sums_desc(base + C::kQSums + tile * C::kSumBytes);
-  bool ok = skip == total || wait_all(&bars->q_full[tile], 0, abort_flag, p);
+  bool ok = steps == 0 || wait_all(&bars->q_full[tile], 0, abort_flag, p);
   for (int s = 0; s < total && ok; ++s) {
     const int st = s % kStages;
     ok = wait_all(&bars->k_full[st], (uint32_t)(s / kStages) & 1u, abort_flag, p);
     const uint64_t kd = smem_desc_sw128(base + C::kK + st * C::kTileBytes, 16, 1024);
     const uint64_t ks = sums_desc(base + C::kKSums + st * C::kSumBytes);
+    const bool mine = twin ? (s & 1) == tile : s >= skip;
 #pragma unroll
     for (int h = 0; h < kPieces<SCORED>; ++h) {
-      if (!ok || s < skip) break;
-      if (s > skip)
-        ok = wait_all(&bars->pv_done[tile][h], (uint32_t)(s - 1 - skip) & 1u, abort_flag, p);
+      if (!ok || !mine) break;
+      if (n > 0) ok = wait_all(&bars->pv_done[tile][h], (uint32_t)(n - 1) & 1u, abort_flag, p);
       if (!ok) break;
       tc_fence_after();
       if (elect_one()) {
@@ -592,6 +607,7 @@ __device__ void run_scores(const ChunkParams& p, const ChunkWork& w, ChunkBars* 
       }
       __syncwarp();
     }
+    n += mine ? 1 : 0;
     if (ok && elect_one()) mma_commit(smem_u32(&bars->k_empty[st]));
     __syncwarp();
   }
@@ -604,7 +620,9 @@ __device__ void run_values(const ChunkParams& p, const ChunkWork& w, ChunkBars* 
   using C = ChunkCfg<D>;
   constexpr int N = kPiece<SCORED>;
   const int total = __shfl_sync(0xffffffffu, w.total, 0);
-  const int skip = total - __shfl_sync(0xffffffffu, w.steps[tile], 0);
+  const int steps = __shfl_sync(0xffffffffu, w.steps[tile], 0), twin = p.twin;
+  const int skip = total - steps;
+  int n = 0;  // the tile's steps so far
   tmem = __shfl_sync(0xffffffffu, tmem, 0);
   const uint32_t from = tmem + C::kTmemS + tile * kKeys, to = tmem + C::kTmemO + tile * D;
   bool ok = true;
@@ -616,10 +634,11 @@ __device__ void run_values(const ChunkParams& p, const ChunkWork& w, ChunkBars* 
     for (int c = 0; c < 4; ++c) bf16 |= bars->info[s % kInfos][c].v_bf16 << c;
     bf16 = __shfl_sync(0xffffffffu, bf16, 0);
     const uint64_t vd = smem_desc_sw128(base + C::kV + st * C::kTileBytes, C::kBoxBytes, 1024);
+    const bool mine = twin ? (s & 1) == tile : s >= skip;
 #pragma unroll
     for (int h = 0; h < kPieces<SCORED>; ++h) {
-      if (!ok || s < skip) break;
-      ok = wait_all(&bars->p_full[tile][h], (uint32_t)(s - skip) & 1u, abort_flag, p);
+      if (!ok || !mine) break;
+      ok = wait_all(&bars->p_full[tile][h], (uint32_t)n & 1u, abort_flag, p);
       if (!ok) break;
       tc_fence_after();
       if (elect_one()) {
@@ -627,7 +646,7 @@ __device__ void run_values(const ChunkParams& p, const ChunkWork& w, ChunkBars* 
         auto product = [&](int k, uint32_t idesc) {
           const int at = N == 64 ? h * N + k * 8 : (k & 3) * 8 + (k >> 2) * 64;
           mma_ts(to, from + at, vd + (uint32_t)((h * N / 16 + k) * 2048 >> 4), idesc,
-                 s > skip || h > 0 || k > 0 ? 1u : 0u);
+                 n > 0 || h > 0 || k > 0 ? 1u : 0u);
         };
         if (bf16 == 0u) {
 #pragma unroll
@@ -640,6 +659,7 @@ __device__ void run_values(const ChunkParams& p, const ChunkWork& w, ChunkBars* 
       }
       __syncwarp();
     }
+    n += mine ? 1 : 0;
     if (ok && elect_one()) mma_commit(smem_u32(&bars->v_empty[st]));
     __syncwarp();
   }
@@ -668,7 +688,7 @@ __device__ __forceinline__ void load_queries(const ChunkParams& p, const ChunkWo
     uint4 raw[kBatch];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      const int row = w.row0 + tile * kTileRows + row_in + r0 + i * RQ + lane / LQ;
+      const int row = w.first_row(tile) + row_in + r0 + i * RQ + lane / LQ;
       raw[i] = make_uint4(0, 0, 0, 0);
       if (row < w.rows) {
         const int t = row / p.G, g = row - t * p.G;
@@ -760,15 +780,15 @@ __device__ __forceinline__ void write_row(const ChunkParams& p, int64_t at, cons
 template <int D>
 __device__ __forceinline__ void write_nothing(const ChunkParams& p, const ChunkWork& w, int tile,
                                               int r) {
-  const int row = w.row0 + tile * kTileRows + r;
+  const int row = w.first_row(tile) + r;
   if (row >= p.G * p.T) return;
-  if (p.splits > 1 && row < w.rows) {
-    float* slot = p.partial + w.slot * (kCtaRows * (D + 2)) + tile * kTileRows + r;
+  if (p.partial && row < w.rows) {
+    float* slot = p.partial + (w.slot * 2 + tile) * (kTileRows * (D + 2)) + r;
     slot[0] = -INFINITY;
-    slot[kCtaRows] = 0.0f;
+    slot[kTileRows] = 0.0f;
     return;
   }
-  if (w.split != 0) return;
+  if (w.split != 0 || (w.twin && tile != 0)) return;
   const int t = row / p.G, g = row - t * p.G;
   const int64_t at = ((int64_t)w.b * p.H + w.h * p.G + g) * p.T + t;
   const float zero[16] = {};
@@ -882,7 +902,7 @@ template <int D>
 __device__ bool softmax_steps(const ChunkParams& p, const ChunkWork& w, ChunkBars* bars, ChunkRow& r,
                               volatile int* abort_flag) {
   const int lane = threadIdx.x & 31, tile = r.tile;
-  const int steps = w.steps[tile], skip = w.total - steps, both = min(w.steps[0], w.steps[1]);
+  const int steps = w.steps[tile], both = min(w.steps[0], w.steps[1]);
   // What a step needs besides its scores: read while the tensor core works on them.
   TokenInfo info[2];
   float factor[2];
@@ -905,21 +925,23 @@ __device__ bool softmax_steps(const ChunkParams& p, const ChunkWork& w, ChunkBar
     look = !whole || __any_sync(kAll, r.m == -INFINITY);
     return true;
   };
-  if (!prepare(skip)) return false;
+  if (!prepare(w.step_of(tile, 0))) return false;
 #pragma unroll 1
-  for (int n = 0; n < steps; ++n) {  // (steps from `skip` on)
+  for (int n = 0; n < steps; ++n) {
     // The row tiles' softmaxes take turns: while one has the issue slots, the tensor core
     // works for the other.  (Odd lanes wait for the turn.)
-    const int first_turn = steps - both;  // steps before it are this tile's alone
-    const int k = n - first_turn;
-    const bool turns = k >= 0 && (tile == 1 || k > 0) && (threadIdx.x & 1);
+    // (Not where both hold the same few rows: 64 rows, 8 sequences of 49152 tokens, 323 us
+    // with turns, 288 without.)
+    const int k = n - (steps - both);  // of the steps that both have
+    const bool paired = k >= 0 && !w.twin;
+    const bool turns = paired && (tile == 1 || k > 0) && (threadIdx.x & 1);
     if (!wait_all(turns ? &bars->turn[tile] : &bars->s_full[tile][0],
                   (uint32_t)(turns ? (tile ? k : k - 1) : n) & 1u, abort_flag, p))
       return false;
     tc_fence_after();
-    const int key0 = w.first_key(n + skip) + 64 * r.half;
+    const int key0 = w.first_key(w.step_of(tile, n)) + 64 * r.half;
     uint32_t weights[32];
-    bool hand = k >= 0;  // the other tile's turn is to come
+    bool hand = paired;  // the other tile's turn is to come
     uint64_t part;
     for (;;) {
       if (look) {
@@ -989,7 +1011,7 @@ __device__ bool softmax_steps(const ChunkParams& p, const ChunkWork& w, ChunkBar
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&bars->p_full[tile][0]));
-    if (n + 1 < steps && !prepare(n + 1 + skip)) return false;
+    if (n + 1 < steps && !prepare(w.step_of(tile, n + 1))) return false;
   }
   return wait_all(&bars->pv_done[tile][0], (uint32_t)(steps - 1) & 1u, abort_flag, p);
 }
@@ -1001,7 +1023,7 @@ __device__ bool softmax_halves(const ChunkParams& p, const ChunkWork& w, ChunkBa
                                ChunkRow& r, volatile int* abort_flag) {
   constexpr int N = kPiece<true>;
   const int lane = threadIdx.x & 31, tile = r.tile;
-  const int steps = w.steps[tile], skip = w.total - steps;
+  const int steps = w.steps[tile];
   // What a step needs besides its scores, of this thread's 32 tokens of each half: read
   // while the tensor core works on them.
   float factor[2];
@@ -1022,7 +1044,7 @@ __device__ bool softmax_halves(const ChunkParams& p, const ChunkWork& w, ChunkBa
     }
     return true;
   };
-  if (!prepare(skip)) return false;
+  if (!prepare(w.step_of(tile, 0))) return false;
 #pragma unroll 1
   for (int u = 0; u < 2 * steps; ++u) {
     const int n = u >> 1, h = u & 1;  // the tile's n-th step, its half
@@ -1030,7 +1052,7 @@ __device__ bool softmax_halves(const ChunkParams& p, const ChunkWork& w, ChunkBa
     tc_fence_after();
     uint32_t x[32];
     tmem_ld16x2_32<32>(r.s + h * N, x);
-    const int key0 = w.first_key(n + skip) + h * N + 32 * r.half;
+    const int key0 = w.first_key(w.step_of(tile, n)) + h * N + 32 * r.half;
     const float f = h ? factor[1] : factor[0];
     const uint32_t my_bits = bits >> (4 * h);
     tmem_wait_ld();
@@ -1084,7 +1106,7 @@ __device__ bool softmax_halves(const ChunkParams& p, const ChunkWork& w, ChunkBa
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&bars->p_full[tile][h]));
-    if (h == 1 && n + 1 < steps && !prepare(n + 1 + skip)) return false;
+    if (h == 1 && n + 1 < steps && !prepare(w.step_of(tile, n + 1))) return false;
   }
   return wait_all(&bars->pv_done[tile][1], (uint32_t)(steps - 1) & 1u, abort_flag, p);
 }
@@ -1107,7 +1129,7 @@ __device__ void run_softmax(const ChunkParams& p, const ChunkWork& w, ChunkBars*
     return;
   }
   load_queries<D, NG>(p, w, bars, base, r.tile, r.row_in);
-  r.row = w.row0 + r.tile * kTileRows + in;
+  r.row = w.first_row(r.tile) + in;
   r.t = r.row / p.G;
   r.g = r.row - r.t * p.G;
   r.there = r.row < w.rows;
@@ -1138,13 +1160,13 @@ __device__ void run_softmax(const ChunkParams& p, const ChunkWork& w, ChunkBars*
   sum += __shfl_xor_sync(kAll, sum, 16);
   const float v_scale = bars->v_scale;
   const float inv = sum == 0.0f ? 0.0f : v_scale / sum;
-  float* slot = p.partial + w.slot * (kCtaRows * (D + 2)) + r.tile * kTileRows + in;
-  const bool partial = p.splits > 1;
+  const bool partial = p.partial != nullptr;
+  float* slot = p.partial + (w.slot * 2 + r.tile) * (kTileRows * (D + 2));
   const int64_t at = ((int64_t)w.b * p.H + w.h * p.G + r.g) * p.T + r.t;
   if (r.there && r.half == 0) {
     if (partial) {
-      slot[0] = r.m;
-      slot[kCtaRows] = sum;
+      slot[in] = r.m;
+      slot[kTileRows + in] = sum;
     } else {
       p.lse[at] = (r.m + __log2f(sum)) * kLn2;
     }
@@ -1169,8 +1191,7 @@ __device__ void run_softmax(const ChunkParams& p, const ChunkWork& w, ChunkBars*
       for (int i = 0; i < 16; ++i) x[i] = __int_as_float(0x7FC00000);
     }
     if (r.there && partial) {
-      float4* dst = reinterpret_cast<float4*>(p.partial + w.slot * (kCtaRows * (D + 2)) +
-                                              2 * kCtaRows + (r.tile * kTileRows + in) * D + c);
+      float4* dst = reinterpret_cast<float4*>(slot + 2 * kTileRows + in * D + c);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         dst[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
@@ -1268,23 +1289,26 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv4_chunk_join_kernel(const C
   int count = p.T;
   if (p.counts) count = min(max(load(p.counts + b), 0), p.T);
   if (row >= p.G * count) return;  // (written by the first split)
-  const float* slot = p.partial + ((int64_t)bh * p.items + row / kCtaRows) * p.splits *
-                                      (int64_t)(kCtaRows * (D + 2));
-  const int r = row % kCtaRows;
-  const int64_t next = kCtaRows * (D + 2);
+  // the ranges' results of the row's tile; of both, if they hold the same rows
+  constexpr int64_t kSlot = kTileRows * (D + 2);
+  const int r = row % kTileRows, parts = p.twin ? 2 * p.splits : p.splits;
+  const int64_t next = p.twin ? kSlot : 2 * kSlot;
+  const float* slot = p.partial + ((int64_t)bh * p.items + row / kCtaRows) * p.splits * 2 * kSlot +
+                      row / kTileRows % 2 * kSlot;
   float top = -INFINITY;
-  for (int s = 0; s < p.splits; ++s) top = fmaxf(top, __ldcg(slot + s * next + r));
+  for (int s = 0; s < parts; ++s) top = fmaxf(top, __ldcg(slot + s * next + r));
   float sum = 0.0f, x[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) x[i] = 0.0f;
   bool seen = false;
-  for (int s = 0; s < p.splits; ++s) {
-    const float m = __ldcg(slot + s * next + r), l = __ldcg(slot + s * next + kCtaRows + r);
+#pragma unroll 4
+  for (int s = 0; s < parts; ++s) {
+    const float m = __ldcg(slot + s * next + r), l = __ldcg(slot + s * next + kTileRows + r);
     if (m == -INFINITY && l == 0.0f) continue;  // (nothing was written behind them)
     seen = true;
     const float f = ex2_approx(m - top);
     sum = fmaf(l, f, sum);
-    const float* o = slot + s * next + 2 * kCtaRows + r * D + lane * V;
+    const float* o = slot + s * next + 2 * kTileRows + r * D + lane * V;
 #pragma unroll
     for (int i = 0; i < V; ++i) x[i] = fmaf(__ldcg(o + i), f, x[i]);
   }
@@ -1322,13 +1346,16 @@ int chunk_splits(int64_t ctas, int64_t steps, int sms) {
 // Up to so many rows a key/value head the kernels of kv4_attn.cuh take the call: they read
 // the cache once for 16 rows.  8 sequences of 49152 tokens, 8 heads of 128: 16 rows 158 us,
 // 32 rows 296; here 350 us for up to 256.
-constexpr int64_t kFewRows = 32;
+constexpr int64_t kFewRows = 16;
 constexpr int kMostFewRowsBatch = 4096;
 bool few_rows(int B, int64_t rows) { return rows <= kFewRows && B <= kMostFewRowsBatch; }
+
+constexpr int64_t kLeastTwin = 512;  // tokens from which the join is worth it
 
 struct ChunkSplit {
   int64_t items, ctas;
   int splits;
+  bool twin;
   size_t workspace;
 };
 ChunkSplit chunk_split(int B, int kv_heads, int64_t rows, int64_t tokens, int D, int sms) {
@@ -1337,7 +1364,8 @@ ChunkSplit chunk_split(int B, int kv_heads, int64_t rows, int64_t tokens, int D,
   const int64_t tiles = s.items * B * kv_heads;
   s.splits = chunk_splits(tiles, (tokens + kKeys - 1) / kKeys, sms);
   s.ctas = tiles * s.splits;
-  if (s.splits > 1) s.workspace = (size_t)s.ctas * kCtaRows * (D + 2) * sizeof(float);
+  s.twin = rows <= kTileRows && tokens > kLeastTwin;
+  if (s.splits > 1 || s.twin) s.workspace = (size_t)s.ctas * kCtaRows * (D + 2) * sizeof(float);
   return s;
 }
 
@@ -1356,7 +1384,7 @@ cudaError_t launch_chunk(const ChunkParams& p, bool scored, int64_t ctas, cudaSt
     if (e != cudaSuccess) return e;
     e = launch_dependent(kernel, dim3((unsigned)ctas), dim3(kChunkThreads), C::kSmem, st, p);
   }
-  if (e != cudaSuccess || p.splits == 1) return e;
+  if (e != cudaSuccess || !p.partial) return e;
   const int64_t rows = (int64_t)p.G * p.T;
   return launch_dependent(kv4_chunk_join_kernel<D>,
                           dim3((unsigned)((rows + kJoinWarps - 1) / kJoinWarps), p.B * p.c.Hkv),
@@ -1443,7 +1471,8 @@ bsattn_status bsattn_kv4_attn_chunk(const bsattn_kv4_cache* cache, const void* q
   p.out = out;
   p.lse = lse;
   p.out_f32 = (flags & BSATTN_OUT_F32) ? 1 : 0;
-  p.partial = static_cast<float*>(workspace);
+  p.twin = split.twin ? 1 : 0;
+  p.partial = split.workspace > 0 ? static_cast<float*>(workspace) : nullptr;
   p.timeout_ns = kDefaultWaitTimeoutNs;
   const bool scored = cap > 0.0f || slopes;
   const int groups = cache->head_dim / cache->group;

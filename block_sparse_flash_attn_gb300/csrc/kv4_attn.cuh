@@ -305,6 +305,15 @@ struct Attn {
   }
 };
 
+// A group's step and least; SCORED: NaN both where one is not finite (an infinity times the
+// sum of a query's channels would have a sign that the channels' own products have not).
+template <bool SCORED>
+__device__ __forceinline__ uint32_t scales_of(const uint8_t* shared) {
+  const uint32_t x = word(shared);
+  if (SCORED && ((x & 0x7F80u) == 0x7F80u || (x & 0x7F800000u) == 0x7F800000u)) return 0x7FC07FC0u;
+  return x;
+}
+
 // A pair of scores (base 2) capped.  32 sequences of up to 65536 tokens: see launch_attn.
 __device__ __forceinline__ F2 capped(F2 s, float cap, float inv_cap) {
   const F2 y = s * f2(inv_cap), u = y * y;
@@ -455,7 +464,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
     const int64_t bh = (int64_t)b * p.c.Hkv + h;
     const int n_tiles = s1 - s0;  // this warp's, one a step
     const int count = SCORED && p.counts ? min(max(load(p.counts + b), 0), p.T) : p.T;
-    const int open = SCORED && p.open ? min(load(p.open + b), len) : 0;
+    const int open = SCORED && p.open ? min(max(load(p.open + b), 0), len) : 0;
     // tiles that begin later need the mask (all, where rows are behind the count)
     const int seen_by_all = count < p.T ? -1 : max(len - p.T, open - 1) - (kTile - 1);
 
@@ -641,7 +650,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
           }
         }
         const uint8_t* ks = stage + 2 * A::kCodes + (g * NG + n) * 4;
-        const uint32_t k[2] = {word(ks), word(ks + 8 * NG * 4)};
+        const uint32_t k[2] = {scales_of<SCORED>(ks), scales_of<SCORED>(ks + 8 * NG * 4)};
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -676,8 +685,8 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kPerSm : 1)
 #pragma unroll
       for (int n = 0; n < NG; ++n) {
         const uint8_t* sc = stage + 2 * A::kCodes + A::kScales + (g * NG + n) * 4;
-        v[n][0] = word(sc);
-        v[n][1] = word(sc + 8 * NG * 4);
+        v[n][0] = scales_of<SCORED>(sc);
+        v[n][1] = scales_of<SCORED>(sc + 8 * NG * 4);
       }
       uint32_t hidden = 0;  // bits 4 nt + 2 t + e
       if (pos > seen_by_all) {

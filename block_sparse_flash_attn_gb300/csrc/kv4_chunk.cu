@@ -29,8 +29,8 @@
 // - V in fp16, rounded once (2^-11), beside a power of two that the CTA takes from its
 //   first step: the mean exponent of its groups of channels goes to 2^-10.  Where a
 //   group of 32 tokens passes 2^-6 there, or 2^-14 the other way, those tokens are taken
-//   in bf16 (2^-8), their weights too.  Weights are off by that rounding, or by 2^-25 of
-//   a number that the row's largest weight is at least 2^-8 of.
+//   in bf16 (2^-8), their weights too.  Weights are off by that rounding, or by 2^-25
+//   beside a row's largest weight of one or more.
 //
 // Work of a CTA (896 threads, one CTA an SM, 211 KB of shared memory):
 //   warps 0-7, 8-15   softmax of the first and the second 128 rows: 16 rows a warp, two
@@ -216,7 +216,7 @@ __device__ __forceinline__ ChunkWork chunk_work(const ChunkParams& p) {
   w.count = p.T;
   if (p.counts) w.count = min(max(load(p.counts + w.b), 0), p.T);
   w.first_pos = w.len - w.count;
-  w.open = p.prefix ? load(p.prefix + w.b) : 0;
+  w.open = p.prefix ? max(load(p.prefix + w.b), 0) : 0;
   const int64_t room = (int64_t)p.columns * p.c.page;
   w.keys = (int)min((int64_t)w.len, room);
   if (w.len > room && threadIdx.x == 0) p.c.report();
@@ -856,7 +856,8 @@ __device__ __forceinline__ void score(const ChunkParams& p, const ChunkRow& r, u
 #pragma unroll
         for (int i = 0; i < 32; i += 2)
           big = max3(big, fabsf(__uint_as_float(x[i])), fabsf(__uint_as_float(x[i + 1])));
-        if (__any_sync(0xffffffffu, !(big * k <= kTanhRange))) {
+        // (by the row's own scores: no vote, another row's leave its bits alone)
+        if (!(big * k <= kTanhRange)) {
 #pragma unroll
           for (int i = 0; i < 32; ++i)
             x[i] = __float_as_uint(p.cap_log2 * tanh_any(__uint_as_float(x[i]) * k));
@@ -906,7 +907,7 @@ __device__ bool softmax_steps(const ChunkParams& p, const ChunkWork& w, ChunkBar
   // What a step needs besides its scores: read while the tensor core works on them.
   TokenInfo info[2];
   float factor[2];
-  bool whole = false, any_bf16 = false, look = true;
+  bool whole = false, any_bf16 = false, find = true;
   auto prepare = [&](int s) -> bool {
     if (!wait_all(&bars->info_full[s % kInfos], (uint32_t)(s / kInfos) & 1u, abort_flag, p))
       return false;
@@ -921,8 +922,9 @@ __device__ bool softmax_steps(const ChunkParams& p, const ChunkWork& w, ChunkBar
     // Weights are formed beside the reference of the steps before, without a look for
     // the maximum; with one where their sum shows that scores rose far above it, where
     // there is no reference yet, and where scores are to be masked first (they go back to
-    // tensor memory for that).
-    look = !whole || __any_sync(kAll, r.m == -INFINITY);
+    // tensor memory for that).  A row that has no reason of its own (`find`) keeps its
+    // reference, and with it its bits, whatever the other rows of the warp have.
+    find = !whole || r.m == -INFINITY;
     return true;
   };
   if (!prepare(w.step_of(tile, 0))) return false;
@@ -944,7 +946,7 @@ __device__ bool softmax_steps(const ChunkParams& p, const ChunkWork& w, ChunkBar
     bool hand = paired;  // the other tile's turn is to come
     uint64_t part;
     for (;;) {
-      if (look) {
+      if (__any_sync(kAll, find)) {
         float top = -INFINITY;
 #pragma unroll 1
         for (int c = 0; c < 2; ++c) {
@@ -960,7 +962,7 @@ __device__ bool softmax_steps(const ChunkParams& p, const ChunkWork& w, ChunkBar
         }
         if (!whole) tmem_wait_st();
         top = fmaxf(top, __shfl_xor_sync(kAll, top, 16));
-        const bool moves = top > r.m + kLagBits;
+        const bool moves = find && top > r.m + kLagBits;
         const bool any = __any_sync(kAll, moves);
         const float f = r.move_to(top, moves);
         // (O is complete: the step's scores waited for the last step's product)
@@ -1002,8 +1004,11 @@ __device__ bool softmax_steps(const ChunkParams& p, const ChunkWork& w, ChunkBar
         weigh(std::false_type{});
       float a, b;
       f2_unpack(part, a, b);
-      if (look || !__any_sync(kAll, !(a + b <= kMostSum))) break;  // (NaN: look, too)
-      look = true;
+      const bool over = !(a + b <= kMostSum);  // (NaN, too)
+      if (!__any_sync(kAll, over && !find)) break;
+      // (by all lanes: no short circuit around the exchange)
+      const int others = __shfl_xor_sync(kAll, over ? 1 : 0, 16);
+      find = find || over || others != 0;
     }
     r.sum = f2_add(r.sum, part);
     tmem_st16x2_32<64>(r.s, weights);
@@ -1087,10 +1092,13 @@ __device__ bool softmax_halves(const ChunkParams& p, const ChunkWork& w, ChunkBa
       float a, b;
       f2_unpack(part, a, b);
       // (a sum that is not a number too)
-      if (!__any_sync(kAll, r.m == -INFINITY || !(a + b <= kMostSum))) break;
+      const bool find = r.m == -INFINITY || !(a + b <= kMostSum);
+      if (!__any_sync(kAll, find)) break;
       float top = largest32(x);
       top = fmaxf(top, __shfl_xor_sync(kAll, top, 16));
-      const bool moves = top > r.m + kLagBits;
+      // (a row without a reason of its own keeps its reference, and its bits)
+      const int others = __shfl_xor_sync(kAll, find ? 1 : 0, 16);
+      const bool moves = (find || others != 0) && top > r.m + kLagBits;
       if (!__any_sync(kAll, moves)) break;
       const float g = r.move_to(top, moves);
       if (u > 0) {  // O, once the product before is complete

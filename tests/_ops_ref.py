@@ -239,3 +239,130 @@ def attn(cache, q, block_table, lengths, selected=None, scale=None):
                 tol_l[b, h * G:(h + 1) * G, t] = dp
                 tol_o[b, h * G:(h + 1) * G, t] = 2 * dp * vbig
     return out, lse, tol_o, tol_l
+
+
+def attn_chunk(cache, q, block_table, lengths, counts=None, prefix=None, cap=None, slopes=None, scale=None,
+               value_bits=11):
+    """O, LSE of kv4_attn_chunk in 64 bits, and the bounds (on O, on LSE) of its arithmetic: 32-bit
+    products and sums, values and weights rounded to `value_bits` bits (11: fp16, 8: bf16)."""
+    B, H, T, D = q.shape
+    Hkv, page, dev = cache.kv_heads, cache.page_size, q.device
+    G = H // Hkv
+    scale = D ** -0.5 if scale is None else scale
+    out = torch.zeros(B, H, T, D, dtype=torch.float64, device=dev)
+    lse = torch.full((B, H, T), -math.inf, dtype=torch.float64, device=dev)
+    tol_o, tol_l = torch.zeros_like(lse), torch.zeros_like(lse)
+    for b, n in enumerate(lengths):
+        c = T if counts is None else max(0, min(T, counts[b]))
+        room = min(max(n, 0), block_table.shape[1] * page)
+        i = n - c + torch.arange(c, device=dev)
+        last = i if prefix is None else torch.maximum(i, torch.full_like(i, prefix[b] - 1))
+        j = torch.arange(room, device=dev)
+        pg = block_table[b, j // page].long()
+        there = (pg >= 0) & (pg < cache.pages)
+        j, pg = j[there], pg[there]
+        if j.numel() == 0 or c == 0:
+            continue
+        see = j[None] <= last[:, None]  # [c, n]
+        for h in range(Hkv):
+            at = (pg, h, j % page)
+            k, v = (values(getattr(cache, m + "_codes")[at], getattr(cache, m + "_scales")[at]) for m in "kv")
+            kbig, vbig = (float(t.abs().nan_to_num(0.0).max()) for t in (k, v))
+            for g in range(h * G, (h + 1) * G):
+                qq = q[b, g, :c].double()
+                s = qq @ k.T * scale
+                smax = torch.where(see, s.abs(), 0.0).amax(-1)
+                bias = 0.0
+                if cap is not None:
+                    s = cap * torch.tanh(s / cap)
+                if slopes is not None:
+                    far = slopes[g].double() * (i[:, None] - j[None]).abs()
+                    s = s - far
+                    bias = torch.where(see, far.abs(), 0.0).amax(-1)
+                s = s.masked_fill(~see, -math.inf)
+                some = see.any(-1)
+                s, m = s[some], see[some].sum(-1)
+                lse[b, g, :c][some] = torch.logsumexp(s, -1)
+                out[b, g, :c][some] = torch.softmax(s, -1) @ v
+                # a score: D products and a few sums of 32 bits, keys held to 2^-18 beside the largest of
+                # their neighbours, the groups' sums to 2^-20
+                ds = ((2 * D + 64) * U32 + 2.0 ** -18 + 2.0 ** -20) * abs(scale) * qq.abs().sum(-1) * kbig
+                if cap is not None:
+                    ds = ds + 2.0 ** -20 * torch.clamp(2 * smax, max=cap)
+                ds = (ds + 4 * U32 * (smax + bias))[some]
+                # exp2 of a 32-bit argument and sums of m terms
+                dp = ds + 2.0 ** -20 + (m + 8) * U32
+                tol_l[b, g, :c][some] = dp
+                half = 2.0 ** -value_bits
+                tol_o[b, g, :c][some] = (2 * dp + 2 * half + m * (2.0 ** -25 + U32)) * vbig
+    return out, lse, tol_o, tol_l
+
+
+# ------------------------------------------------------------- the cache's pages
+
+def _pages(n, page):
+    return -(-max(n, 0) // page)
+
+
+def count_refs(cache, table, lengths):
+    refs = [0] * cache.pages
+    for row, n in zip(table, lengths):
+        for p in row[:_pages(n, cache.page_size)]:
+            if 0 <= p < cache.pages:
+                refs[p] += 1
+    return refs
+
+
+def fork(refs, table, lengths, parents, page):
+    """table, lengths, refs (lists) and the copies [(from, to, tokens)]; -1 where pages ran out."""
+    refs, columns = list(refs), len(table[0])
+    for row, n in zip(table, lengths):
+        for p in row[:_pages(n, page)]:
+            refs[p] -= 1
+    new, new_lengths, keeps, wants = [], [], set(), []
+    for i, a in enumerate(parents):
+        n = lengths[a] if a >= 0 else 0
+        row = table[a][:_pages(n, page)] if a >= 0 else []
+        row = row + [-1] * (columns - len(row))
+        if n % page and a in keeps:
+            wants.append((i, n // page, row[n // page], n % page))
+            row[n // page] = -1
+        keeps.add(a)
+        for p in row:
+            if p >= 0:
+                refs[p] += 1
+        new.append(row)
+        new_lengths.append(n)
+    free = iter([p for p, r in enumerate(refs) if r == 0])
+    copies = []
+    for i, column, src, tokens in wants:
+        p = next(free, -1)
+        new[i][column] = p
+        if p >= 0:
+            refs[p] = 1
+            copies.append((src, p, tokens))
+    return new, new_lengths, refs, copies
+
+
+def reserve(refs, table, lengths, counts, page):
+    refs, table = list(refs), [list(row) for row in table]
+    free = iter([p for p, r in enumerate(refs) if r == 0])
+    for row, n, c in zip(table, lengths, counts):
+        for column in range(_pages(n, page), min(len(row), _pages(max(n, 0) + max(c, 0), page))):
+            row[column] = next(free, -1)
+            if row[column] >= 0:
+                refs[row[column]] = 1
+    return table, refs
+
+
+def compact(refs, table):
+    """table, refs, page_map"""
+    n = sum(r > 0 for r in refs)
+    high = [p for p, r in enumerate(refs) if r > 0 and p >= n]
+    low = [p for p, r in enumerate(refs) if r <= 0 and p < n]
+    to = dict(zip(high, low))
+    page_map = [to.get(p, p) if r > 0 else -1 for p, r in enumerate(refs)]
+    after = list(refs)
+    for a, b in to.items():
+        after[b], after[a] = refs[a], 0
+    return [[page_map[p] if p >= 0 else p for p in row] for row in table], after, page_map

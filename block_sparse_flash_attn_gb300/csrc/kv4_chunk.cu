@@ -139,7 +139,6 @@ struct __align__(16) ChunkBars {
   int abort_flag;
   float v_scale;      // what O is multiplied by
   int v_exponents[4][2];  // of each V warp's first step: sum, number
-  int query_shift[kCtaRows];
   uint2 factors[8][4 * 32];  // by warp, group and token: what codes are multiplied by, and a summand
 };
 
@@ -203,20 +202,19 @@ struct ChunkWork {
 __device__ __forceinline__ ChunkWork chunk_work(const ChunkParams& p) {
   ChunkWork w;
   // row tiles with the longest contexts first
-  const int heads = p.B * p.c.Hkv;
-  int at = blockIdx.x;
-  w.split = at % p.splits;
-  at /= p.splits;
-  const int item = p.items - 1 - at / heads;
-  const int bh = at % heads;
-  w.b = bh / p.c.Hkv;
+  const int item = p.items - 1 - (int)blockIdx.z;
+  const unsigned bh = blockIdx.y, splits = p.splits;
+  w.split = blockIdx.x;
+  w.b = bh / (unsigned)p.c.Hkv;
   w.h = bh - w.b * p.c.Hkv;
+  // (all loads at once, whatever there is)
+  const int len = load(p.lengths + w.b), count = load((p.counts ? p.counts : p.lengths) + w.b),
+            open = load((p.prefix ? p.prefix : p.lengths) + w.b);
   w.slot = ((int64_t)bh * p.items + item) * p.splits + w.split;
-  w.len = max(load(p.lengths + w.b), 0);
-  w.count = p.T;
-  if (p.counts) w.count = min(max(load(p.counts + w.b), 0), p.T);
+  w.len = max(len, 0);
+  w.count = p.counts ? min(max(count, 0), p.T) : p.T;
   w.first_pos = w.len - w.count;
-  w.open = p.prefix ? max(load(p.prefix + w.b), 0) : 0;
+  w.open = p.prefix ? max(open, 0) : 0;
   const int64_t room = (int64_t)p.columns * p.c.page;
   w.keys = (int)min((int64_t)w.len, room);
   if (w.len > room && threadIdx.x == 0) p.c.report();
@@ -232,8 +230,12 @@ __device__ __forceinline__ ChunkWork chunk_work(const ChunkParams& p) {
     most[i] = lim >= 0 ? lim / kKeys + 1 : 0;
   }
   const int all = max(most[0], most[1]);
-  w.j0 = (int)((int64_t)all * w.split / p.splits);
-  const int j1 = (int)((int64_t)all * (w.split + 1) / p.splits);
+  w.j0 = 0;
+  int j1 = all;
+  if (splits > 1) {  // (all: at most 2^24, splits: 2^6)
+    w.j0 = (unsigned)all * w.split / splits;
+    j1 = (unsigned)all * (w.split + 1) / splits;
+  }
 #pragma unroll
   for (int i = 0; i < 2; ++i) w.steps[i] = max(min(j1, most[i]) - w.j0, 0);
   w.total = max(w.steps[0], w.steps[1]);
@@ -669,78 +671,105 @@ __device__ void run_values(const ChunkParams& p, const ChunkWork& w, ChunkBars* 
 // ---------------------------------------------------------------------------
 // warps 0-15: queries, softmax, results
 // ---------------------------------------------------------------------------
-// This warp's 16 rows of Q as fp16 beside each row's largest (which goes to [2^14,
-// 2^15)), channels in the codes' order, and the sums of their groups.
+// A softmax thread's query: a half of the channels, lanes 16 on the second.  (A thread pair a
+// row, as the softmax has it.  With 16 lanes a row and maxima and sums by shuffles the first
+// product waited for the queries, 13000 clocks of a CTA; 10000 now.  8 prompts of up to 2048
+// tokens: 358 us, now 334.)
+template <int D>
+struct Query {
+  static constexpr int N = D / 16;
+  uint4 raw[N];
+  int row, t, g;  // row of the key/value head, token, head of the group
+  __device__ __forceinline__ void fetch(const ChunkParams& p, const ChunkWork& w, int first) {
+    const int lane = threadIdx.x & 31;
+    row = first + (lane & 15);
+    t = (unsigned)row / (unsigned)p.G;
+    g = row - t * p.G;
+    const uint4* from =
+        reinterpret_cast<const uint4*>(p.q + (((int64_t)w.b * p.H + w.h * p.G + g) * p.T + t) * D) +
+        (lane >> 4) * N;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      raw[i] = row < w.rows ? load(from + i) : make_uint4(0, 0, 0, 0);
+  }
+};
+
+// The queries as fp16 beside each row's largest (which goes to [2^14, 2^15)), channels in the
+// codes' order, and the sums of their groups.  Returns the row's power of two.
 template <int D, int NG>
-__device__ __forceinline__ void load_queries(const ChunkParams& p, const ChunkWork& w,
-                                             ChunkBars* bars, uint32_t base, int tile, int row_in) {
+__device__ __forceinline__ int load_queries(const ChunkParams& p, ChunkBars* bars, uint32_t base,
+                                            int tile, int row_in, const Query<D>& q) {
   using C = ChunkCfg<D>;
-  constexpr int LQ = D / 8, RQ = 32 / LQ;  // lanes a row, rows at once
-  constexpr int GL = LQ / NG;              // lanes a group
-  constexpr int kBatch = 4;
-  const int lane = threadIdx.x & 31, piece = lane % LQ;
-  const uint32_t q_at = base + C::kQ + tile * C::kTileBytes + piece / 8 * C::kBoxBytes;
-  const uint32_t sums_at = base + C::kQSums + tile * C::kSumBytes + row_in * 16;
-  st_shared_v4(sums_at + (lane & 15) * 16 + (lane >> 4) * 2048, 0, 0, 0, 0);
-  __syncwarp();
-#pragma unroll 1
-  for (int r0 = 0; r0 < 16; r0 += kBatch * RQ) {
-    uint4 raw[kBatch];
+  constexpr int N = Query<D>::N;
+  constexpr int SG = NG == 4 ? 2 : 1;  // sums of a half: of two groups, one, or half a group
+  const int lane = threadIdx.x & 31, half = lane >> 4, r = row_in + (lane & 15);
+  uint32_t top = 0;  // (magnitudes of bf16 compare as whole numbers)
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int row = w.first_row(tile) + row_in + r0 + i * RQ + lane / LQ;
-      raw[i] = make_uint4(0, 0, 0, 0);
-      if (row < w.rows) {
-        const int t = row / p.G, g = row - t * p.G;
-        raw[i] = load(reinterpret_cast<const uint4*>(
-                          p.q + (((int64_t)w.b * p.H + w.h * p.G + g) * p.T + t) * D) +
-                      piece);
-      }
+  for (int i = 0; i < N; ++i) {
+    top = __vmaxu2(top, __vmaxu2(q.raw[i].x & 0x7FFF7FFFu, q.raw[i].y & 0x7FFF7FFFu));
+    top = __vmaxu2(top, __vmaxu2(q.raw[i].z & 0x7FFF7FFFu, q.raw[i].w & 0x7FFF7FFFu));
+  }
+  top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 16));
+  const float most = __uint_as_float(max(top & 0xFFFFu, top >> 16) << 16);
+  // (a row with an infinity or NaN is spoiled whatever its power; one that is below 2^-112
+  // stays below 2^14)
+  const int sh = most > 0.0f ? min(14 + 127 - (int)(__float_as_uint(most) >> 23), 126) : 0;
+  const float f = p.sign * __uint_as_float((uint32_t)(127 + sh) << 23);
+  const uint64_t f2 = f2_pack(f, f);
+  uint64_t sums[SG] = {};
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const uint32_t u[4] = {q.raw[i].x, q.raw[i].y, q.raw[i].z, q.raw[i].w};
+    float x[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint64_t v = f2_mul(f2_pack(bf16_lo(u[k]), bf16_hi(u[k])), f2);
+      sums[i * SG / N] = f2_add(sums[i * SG / N], v);
+      f2_unpack(v, x[2 * k], x[2 * k + 1]);
     }
+    const int piece = half * N + i;
+    st_shared_v4(base + C::kQ + tile * C::kTileBytes + piece / 8 * C::kBoxBytes + r * 128 +
+                     ((piece % 8 ^ (r & 7)) << 4),
+                 pack_f16x2(x[0], x[4]), pack_f16x2(x[1], x[5]), pack_f16x2(x[2], x[6]),
+                 pack_f16x2(x[3], x[7]));
+  }
+  float all[4] = {};  // of each group
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int r = row_in + r0 + i * RQ + lane / LQ;
-      float x[8], most = 0.0f, sum = 0.0f;
-      unpack8(raw[i], x);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float a = fabsf(x[k]);
-        most = fmaxf(most, a <= 3.4e38f ? a : 0.0f);
-      }
-#pragma unroll
-      for (int o = 1; o < LQ; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-      const int sh = most > 0.0f ? 14 - ilogbf(most) : 0;
-      // in two factors: 2^sh may pass fp32's range
-      const float fa = ldexpf(p.sign, sh / 2), fb = ldexpf(1.0f, sh - sh / 2);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        x[k] = x[k] * fa * fb;
-        sum += x[k];
-      }
-      st_shared_v4(q_at + r * 128 + ((piece % 8 ^ (r & 7)) << 4), pack_f16x2(x[0], x[4]),
-                   pack_f16x2(x[1], x[5]), pack_f16x2(x[2], x[6]), pack_f16x2(x[3], x[7]));
-#pragma unroll
-      for (int o = 1; o < GL; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      sum *= 6.103515625e-5f;  // (2^-14: c has 2^14)
-      if (piece % GL == 0) {
-        const int g = piece / GL;
-        const __half hi = __float2half_rn(sum), lo = __float2half_rn(sum - __half2float(hi));
-        auto put = [&](int k, __half v) {
-          asm volatile("st.shared.b16 [%0], %1;" ::"r"(sums_at + (r - row_in) * 16 +
-                                                       (k >> 3) * 2048 + (k & 7) * 2),
-                       "h"(__half_as_ushort(v))
-                       : "memory");
-        };
-        put(g, hi);
-        put(NG + g, lo);
-        put(2 * NG + g, hi);
-      }
-      if (piece == 0) bars->query_shift[tile * kTileRows + r] = sh;
+  for (int i = 0; i < SG; ++i) {
+    float a, b;
+    f2_unpack(sums[i], a, b);
+    const float mine = (a + b) * 6.103515625e-5f;  // (2^-14: c has 2^14)
+    const float other = __shfl_xor_sync(0xffffffffu, mine, 16);
+    if constexpr (NG == 1) {
+      all[0] = mine + other;
+    } else {
+      all[i] = half ? other : mine;
+      all[SG + i] = half ? mine : other;
     }
   }
+  // (q hi, q lo, q hi) of NG groups each, then zeros: the lanes' halves 8 of the 16 each
+  uint32_t hi[4], lo[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half h = __float2half_rn(all[i]);
+    hi[i] = __half_as_ushort(h);
+    lo[i] = __half_as_ushort(__float2half_rn(all[i] - __half2float(h)));
+  }
+  uint32_t y[8] = {};
+#pragma unroll
+  for (int k = 0; k < 3 * NG; ++k) {
+    const uint32_t v = k < NG || k >= 2 * NG ? hi[k % NG] : lo[k % NG];
+    y[k / 2] |= k & 1 ? v << 16 : v;
+  }
+  const uint32_t to = base + C::kQSums + tile * C::kSumBytes + r * 16 + half * 2048;
+  if (half)
+    st_shared_v4(to, y[4], y[5], y[6], y[7]);
+  else
+    st_shared_v4(to, y[0], y[1], y[2], y[3]);
   fence_proxy_async_smem();
   __syncwarp();
   if (lane == 0) mbar_arrive(smem_u32(&bars->q_full[tile]));
+  return sh;
 }
 
 __device__ __forceinline__ float largest32(const uint32_t (&x)[32]) {
@@ -1136,15 +1165,17 @@ __device__ void run_softmax(const ChunkParams& p, const ChunkWork& w, ChunkBars*
     if (r.half == 0) write_nothing<D>(p, w, r.tile, in);
     return;
   }
-  load_queries<D, NG>(p, w, bars, base, r.tile, r.row_in);
-  r.row = w.first_row(r.tile) + in;
-  r.t = r.row / p.G;
-  r.g = r.row - r.t * p.G;
+  Query<D> query;
+  query.fetch(p, w, w.first_row(r.tile) + r.row_in);
+  const int shift = load_queries<D, NG>(p, bars, base, r.tile, r.row_in, query);
+  r.row = query.row;
+  r.t = query.t;
+  r.g = query.g;
   r.there = r.row < w.rows;
   // (rows without a query: all keys, with scores of zero)
   r.lim = r.there ? w.limit(r.t) : 0x7FFFFFFF;
   r.pos = w.first_pos + r.t;
-  r.factor = ldexpf(p.scale_log2, -bars->query_shift[r.tile * kTileRows + in]);
+  r.factor = ldexpf(p.scale_log2, -shift);
   r.slope = r.inv_cap = 0.0f;
   if constexpr (SCORED) {
     if (p.slopes && r.there) r.slope = load(p.slopes + w.h * p.G + r.g) * 1.4426950408889634f;
@@ -1352,12 +1383,19 @@ int chunk_splits(int64_t ctas, int64_t steps, int sms) {
 }
 
 // Up to so many rows a key/value head the kernels of kv4_attn.cuh take the call: they read
-// the cache once for 16 rows.  8 sequences of 49152 tokens, 8 heads of 128: 16 rows 158 us,
-// 32 rows 296; here 350 us for up to 256.
-constexpr int64_t kFewRows = 16;
+// the cache once for 16 rows, with less to set up.  8 sequences of 49152 tokens, 8 heads of
+// 128: 16 rows 161 us, 32 rows 276, 48 rows 430; here 240 to 270 us for 17 to 128.  Where there
+// is little to read in all (16 rows' tiles times tokens) they take more: 6 heads of 1000
+// tokens, 17 to 96 rows: 12 us, here 19; 128 rows 14 and 22; 128 heads of 1000 tokens, 32
+// rows: 24 and 27, 40 rows: 40 and 27.
+constexpr int64_t kFewRows = 16, kMostFewRows = 128, kLittle = 3 << 16;
 constexpr int kMostFewRowsBatch = 4096;
-bool few_rows(int B, int64_t rows) { return rows <= kFewRows && B <= kMostFewRowsBatch; }
+bool few_rows(int B, int kv_heads, int64_t rows, int64_t tokens) {
+  if (B > kMostFewRowsBatch || rows > kMostFewRows) return false;
+  return rows <= kFewRows || (rows + 15) / 16 * B * kv_heads * tokens <= kLittle;
+}
 
+constexpr int64_t kMostRows = 65535 * kCtaRows;  // a grid's third size
 constexpr int64_t kLeastTwin = 512;  // tokens from which the join is worth it
 
 struct ChunkSplit {
@@ -1378,19 +1416,20 @@ ChunkSplit chunk_split(int B, int kv_heads, int64_t rows, int64_t tokens, int D,
 }
 
 template <int D, int NG>
-cudaError_t launch_chunk(const ChunkParams& p, bool scored, int64_t ctas, cudaStream_t st) {
+cudaError_t launch_chunk(const ChunkParams& p, bool scored, cudaStream_t st) {
   using C = ChunkCfg<D>;
+  const dim3 grid(p.splits, p.B * p.c.Hkv, p.items);
   cudaError_t e;
   if (scored) {
     constexpr auto kernel = kv4_chunk_kernel<D, NG, true>;
     e = allow_shared_memory<kernel>(C::kSmem);
     if (e != cudaSuccess) return e;
-    e = launch_dependent(kernel, dim3((unsigned)ctas), dim3(kChunkThreads), C::kSmem, st, p);
+    e = launch_dependent(kernel, grid, dim3(kChunkThreads), C::kSmem, st, p);
   } else {
     constexpr auto kernel = kv4_chunk_kernel<D, NG, false>;
     e = allow_shared_memory<kernel>(C::kSmem);
     if (e != cudaSuccess) return e;
-    e = launch_dependent(kernel, dim3((unsigned)ctas), dim3(kChunkThreads), C::kSmem, st, p);
+    e = launch_dependent(kernel, grid, dim3(kChunkThreads), C::kSmem, st, p);
   }
   if (e != cudaSuccess || !p.partial) return e;
   const int64_t rows = (int64_t)p.G * p.T;
@@ -1414,7 +1453,7 @@ size_t bsattn_kv4_attn_chunk_workspace(int B, int H, int kv_heads, int T, int D,
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
   const int64_t rows = (int64_t)(H / kv_heads) * T, tokens = (int64_t)columns * page_size;
-  if (few_rows(B, rows)) return kv4_few_rows_workspace(B, kv_heads, (int)rows, D, tokens);
+  if (few_rows(B, kv_heads, rows, tokens)) return kv4_few_rows_workspace(B, kv_heads, (int)rows, D, tokens);
   return chunk_split(B, kv_heads, rows, tokens, D, device_sm_count(dev)).workspace;
 }
 
@@ -1442,12 +1481,12 @@ bsattn_status bsattn_kv4_attn_chunk(const bsattn_kv4_cache* cache, const void* q
   // (a cap that underflows in the kernel's units would cap nothing)
   if (cap > 0.0f && (cap < 1e-30f || cap > 1e30f)) return BSATTN_ERR_UNSUPPORTED;
   const int64_t rows = (int64_t)(H / cache->kv_heads) * T;
-  if (B > 65535 || rows > (1 << 30) || (int64_t)B * cache->kv_heads > 65535 ||
+  if (B > 65535 || rows > kMostRows || (int64_t)B * cache->kv_heads > 65535 ||
       (int64_t)columns * cache->page_size > (1ll << 31) - 2 * kKeys ||  // positions are 32-bit
       (int64_t)cache->pages * cache->kv_heads * cache->page_size / 16 >= (1ll << 31))
     return BSATTN_ERR_UNSUPPORTED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (few_rows(B, rows))
+  if (few_rows(B, cache->kv_heads, rows, (int64_t)columns * cache->page_size))
     return kv4_few_rows({cache, q, B, H, T, block_table, table_stride, columns, lengths, counts,
                          prefix, scale, cap, slopes, (flags & BSATTN_OUT_F32) ? 1 : 0, out, lse},
                         workspace, workspace_bytes, st);
@@ -1456,7 +1495,6 @@ bsattn_status bsattn_kv4_attn_chunk(const bsattn_kv4_cache* cache, const void* q
   const ChunkSplit split =
       chunk_split(B, cache->kv_heads, rows, (int64_t)columns * cache->page_size, cache->head_dim,
                   device_sm_count(dev));
-  if (split.ctas >= (1ll << 31)) return BSATTN_ERR_UNSUPPORTED;
   if (split.workspace > 0 && (!workspace || workspace_bytes < split.workspace))
     return BSATTN_ERR_INVALID_ARG;
   p.q = static_cast<const uint16_t*>(q);
@@ -1486,12 +1524,12 @@ bsattn_status bsattn_kv4_attn_chunk(const bsattn_kv4_cache* cache, const void* q
   const int groups = cache->head_dim / cache->group;
   cudaError_t e;
   if (cache->head_dim == 64)
-    e = groups == 1 ? launch_chunk<64, 1>(p, scored, split.ctas, st)
-                    : launch_chunk<64, 2>(p, scored, split.ctas, st);
+    e = groups == 1 ? launch_chunk<64, 1>(p, scored, st)
+                    : launch_chunk<64, 2>(p, scored, st);
   else
-    e = groups == 1   ? launch_chunk<128, 1>(p, scored, split.ctas, st)
-        : groups == 2 ? launch_chunk<128, 2>(p, scored, split.ctas, st)
-                      : launch_chunk<128, 4>(p, scored, split.ctas, st);
+    e = groups == 1   ? launch_chunk<128, 1>(p, scored, st)
+        : groups == 2 ? launch_chunk<128, 2>(p, scored, st)
+                      : launch_chunk<128, 4>(p, scored, st);
   return from_cuda(e);
 }
 

@@ -608,22 +608,23 @@ bsattn_status bsattn_kv4_attn(const bsattn_kv4_cache* cache, const void* q, int 
  *   q          device bf16 [B][H][T][head_dim], 16-byte aligned, entries below 2^100 in
  *              magnitude (one that is not finite spoils its own query only); query head
  *              h reads key/value head h / (H / kv_heads).  B * kv_heads at most 65535,
- *              H / kv_heads * T at most 2^30, columns * page_size at most 2^31 - 256.
+ *              H / kv_heads * T at most 2^24 - 256, columns * page_size at most 2^31 - 256.
  *   cache      values below 2^104 in magnitude, |scale| sum |q k| of a query and a key
  *              below 2^112; a group whose step or least value is not finite stands for
  *              NaN, which spoils its channels (values) or all of them (keys) of the
  *              queries that see it.
- *              Up to 16 rows (H / kv_heads * T; B at most 4096) all arithmetic is as in
- *              bsattn_kv4_attn.  More: scores are as good as 32-bit products; a key's
- *              channels below 2^-17 of the largest key of 32 tokens (positions 32 i to
- *              32 i + 31) count with fewer bits.  Values are rounded to fp16, beside a power
- *              of two taken from 128 tokens, where those of 32 tokens lie within 2^4 of
- *              those either way, else to bf16; weights to the same type.
+ *              Up to 16 rows (H / kv_heads * T), and up to 128 where the table has room for
+ *              few tokens, all arithmetic is as in bsattn_kv4_attn.  Else scores are as good
+ *              as 32-bit products; a key's channels below 2^-17 of the largest key of 32
+ *              tokens (positions 32 i to 32 i + 31) count with fewer bits.  Values are
+ *              rounded to fp16, beside a power of two taken from 128 tokens, where those of
+ *              32 tokens lie within 2^4 of those either way, else to bf16; weights to the
+ *              same type.
  *   lengths    cached tokens, the new ones included.
  *   counts     new tokens of each sequence, or null: T.
  *   prefix     device int32 [B]: positions below it are seen by every query; or null.
  *   scale      finite.  cap: 0 (none), or 1e-30 to 1e30.
- *   slopes     device fp32 [H], or null.
+ *   slopes     device fp32 [H], finite, or null.
  *   flags, out, lse  as bsattn_kv4_attn.
  *   workspace  bsattn_kv4_attn_chunk_workspace bytes (may be none), 16-byte aligned.
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA.  A wait inside the kernel that runs out (2 s)

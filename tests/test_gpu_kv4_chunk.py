@@ -25,6 +25,10 @@ def bs():
     return bs
 
 
+# with a table that has room for so many tokens up to 128 rows are taken as more are
+ROOM = 1 << 18
+
+
 def _i32(x):
     return torch.tensor(x, dtype=torch.int32, device="cuda")
 
@@ -85,11 +89,15 @@ def _options(name, H, lengths):
     return o, prefix
 
 
+CASES = [(c, False) for c in CHUNKS] + [(c, True) for c in CHUNKS if 16 < c[1] * c[5] <= 128]
+
+
 @pytest.mark.parametrize("option", OPTIONS)
-@pytest.mark.parametrize("case", CHUNKS, ids=lambda c: "-".join(str(x) for x in c[:6]))
-def test_chunk(bs, case, option):
+@pytest.mark.parametrize("case,room", CASES,
+                         ids=lambda c: "room" * c if isinstance(c, bool) else "-".join(str(x) for x in c[:6]))
+def test_chunk(bs, case, room, option):
     Hkv, G, D, page, group, T, lengths, counts = case
-    cache, table, q, n = _case(bs, *case[:-1])
+    cache, table, q, n = _case(bs, *case[:-1], columns=ROOM // page if room else None)
     o, prefix = _options(option, Hkv * G, lengths)
     args = dict(o, prefix=None if prefix is None else _i32(prefix))
     want = ref.attn_chunk(cache, q, table, lengths, counts, prefix, o.get("cap"), o.get("slopes"))
@@ -197,11 +205,11 @@ def test_values_that_are_not_numbers(bs, T):
     assert bool(o[:, :, sees].isnan().all()) and not bool(o[:, :, ~sees].isnan().any())
 
 
-@pytest.mark.parametrize("T", [2, 50])
+@pytest.mark.parametrize("T", [2, 50, 90])
 def test_nothing_behind_the_length_is_read(bs, T):
     """Rows of the last page behind the length hold NaN; so do all other pages."""
     n = 333
-    cache, table, q, lengths = _case(bs, 2, 2, 64, 64, 32, T, [n])
+    cache, table, q, lengths = _case(bs, 2, 2, 64, 64, 32, T, [n], columns=ROOM // 64 if T == 50 else None)
     want = bs.kv4_attn_chunk(cache, q, table, lengths)
     used = table[0, :6].long()
     for name in "kv":
@@ -214,10 +222,10 @@ def test_nothing_behind_the_length_is_read(bs, T):
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
-@pytest.mark.parametrize("T", [2, 50])
+@pytest.mark.parametrize("T", [2, 30, 42, 50])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), 3e38])
 def test_a_query_spoils_its_own_row_only(bs, T, bad):
-    cache, table, q, n = _case(bs, 1, 3, 64, 64, 32, T, [600])
+    cache, table, q, n = _case(bs, 1, 3, 64, 64, 32, T, [600], columns=ROOM // 64 if T == 42 else None)
     want = bs.kv4_attn_chunk(cache, q, table, n)
     q2 = q.clone()
     q2[0, 1, 1, 5] = bad
@@ -228,10 +236,10 @@ def test_a_query_spoils_its_own_row_only(bs, T, bad):
     assert torch.equal(got[1][0][others], want[1][0][others])
 
 
-@pytest.mark.parametrize("T", [2, 60])
+@pytest.mark.parametrize("T", [2, 40, 60, 70])
 def test_bad_pages_are_skipped_and_reported(bs, T):
     lengths = [500, 300]
-    cache, table, q, n = _case(bs, 1, 2, 64, 16, 32, T, lengths)
+    cache, table, q, n = _case(bs, 1, 2, 64, 16, 32, T, lengths, columns=ROOM // 16 if T == 60 else None)
     for entry in (-1, cache.pages, 1 << 30):
         t = table.clone()
         t[0, 3], t[1, 18] = entry, entry
@@ -248,11 +256,11 @@ def test_bad_pages_are_skipped_and_reported(bs, T):
     bs.kv4_status(cache)
 
 
-@pytest.mark.parametrize("T", [4, 50])
+@pytest.mark.parametrize("T", [4, 40, 50, 70])
 def test_sequences_that_are_empty(bs, T):
     """Lengths of zero and below, counts of zero and below, counts above T and above the length."""
     lengths, counts = [0, -5, 40, 40, 40, 2], [T, T, 0, -3, T + 9, T]
-    cache, table, q, n = _case(bs, 1, 2, 64, 16, 64, T, lengths)
+    cache, table, q, n = _case(bs, 1, 2, 64, 16, 64, T, lengths, columns=ROOM // 16 if T == 50 else None)
     _check(bs.kv4_attn_chunk(cache, q, table, n, _i32(counts)), ref.attn_chunk(cache, q, table, lengths, counts))
     bs.kv4_status(cache)
 
@@ -280,11 +288,11 @@ def test_offsets_past_32_bits(bs):
     bs.kv4_status(cache)
 
 
-@pytest.mark.parametrize("T", [2, 40, 200])
+@pytest.mark.parametrize("T", [2, 40, 50, 200])
 def test_captured_and_on_other_streams(bs, T):
     """Graphs follow lengths that grow; two of them, each with its workspace, at once."""
     lengths = [600, 900]
-    cache, table, q, _ = _case(bs, 1, 2, 64, 32, 64, T, lengths)
+    cache, table, q, _ = _case(bs, 1, 2, 64, 32, 64, T, lengths, columns=ROOM // 32 if T == 50 else None)
     n = _i32([500, 301])
     graphs, results = [], []
     side = torch.cuda.Stream()
@@ -365,10 +373,10 @@ def test_refusals(bs):
         bs.kv4_attn_chunk(cache, q, table, n, cap=1e35)
 
 
-@pytest.mark.parametrize("T", [3, 60])
+@pytest.mark.parametrize("T", [3, 12, 20, 60])
 def test_rows_do_not_touch_one_another(bs, T):
     """One row's wide scores leave the others' bits alone, with a cap and without."""
-    cache, table, q, n = _case(bs, 1, 4, 64, 64, 32, T, [700])
+    cache, table, q, n = _case(bs, 1, 4, 64, 64, 32, T, [700], columns=ROOM // 64 if T == 20 else None)
     for more in ({}, dict(cap=10.0), dict(slopes=_slopes(4))):
         want = bs.kv4_attn_chunk(cache, q, table, n, **more)
         q2 = q.clone()
@@ -378,3 +386,47 @@ def test_rows_do_not_touch_one_another(bs, T):
         others[2, 1] = False
         assert torch.equal(got[0][0][others], want[0][0][others])
         assert torch.equal(got[1][0][others], want[1][0][others])
+
+
+@pytest.mark.parametrize("T", [3, 90])
+@pytest.mark.parametrize("prefix", [-2 ** 31, -1, 2 ** 31 - 1])
+def test_prefixes_of_any_value(bs, T, prefix):
+    cache, table, q, n = _case(bs, 1, 2, 64, 64, 32, T, [200])
+    _check(bs.kv4_attn_chunk(cache, q, table, n, prefix=_i32([prefix])),
+           ref.attn_chunk(cache, q, table, [200], prefix=[prefix]))
+
+
+def test_chain(bs):
+    """As a server runs: pages reserved, prompts in ragged chunks, samples forked, drafts, ended
+    rows, compaction; each answer against 64 bits of what the cache holds."""
+    Hkv, H, D, page = 2, 6, 64, 16
+    cache = bs.Kv4Cache(96, Hkv, D, page_size=page, group=32)
+    refs = torch.zeros(96, dtype=torch.int32, device="cuda")
+    table = torch.full((2, 20), -1, dtype=torch.int32, device="cuda")
+    lengths = _i32([0, 0])
+    g = ref.gen(11)
+
+    def step(table, lengths, refs, T, counts, **more):
+        B = table.shape[0]
+        table, refs = bs.kv4_reserve(cache, refs, table, lengths, _i32(counts))
+        k, v = (torch.randn(B, Hkv, T, D, generator=g, device="cuda").bfloat16() for _ in "kv")
+        bs.kv4_append(cache, k, v, table, lengths, _i32(counts))
+        lengths = lengths + _i32(counts)
+        q = torch.randn(B, H, T, D, generator=g, device="cuda").bfloat16()
+        got = bs.kv4_attn_chunk(cache, q, table, lengths, _i32(counts), **more)
+        _check(got, ref.attn_chunk(cache, q, table, lengths.tolist(), counts, cap=more.get("cap"),
+                                   slopes=more.get("slopes")))
+        return table, lengths, refs
+
+    state = step(table, lengths, refs, 75, [75, 40])
+    state = step(*state, 33, [20, 33], cap=20.0)
+    table, lengths, refs = bs.kv4_fork(cache, state[2], state[0], state[1], _i32([0, 0, 1, 0, 1]))
+    state = step(table, lengths, refs, 1, [1] * 5, slopes=_slopes(H))
+    state = step(*state, 4, [4, 3, 0, 1, 2], cap=5.0, slopes=_slopes(H))
+    table, lengths, refs = bs.kv4_fork(cache, state[2], state[0], state[1], _i32([4, -1, 1]))
+    table, refs, page_map = bs.kv4_compact(cache, refs, table)
+    used = int((refs > 0).sum())
+    assert bool((refs[:used] > 0).all()) and not bool(refs[used:].any())
+    state = step(table, lengths, refs, 2, [2, 2, 1])
+    assert ref.count_refs(cache, state[0].tolist(), state[1].tolist()) == state[2].tolist()
+    bs.kv4_status(cache)

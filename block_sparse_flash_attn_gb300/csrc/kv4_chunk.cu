@@ -91,6 +91,8 @@ constexpr uint32_t kTmemColumns = 512;
 constexpr float kLagBits = 8.0f;            // a row's reference may lie 2^8 below its maximum
 constexpr float kMostSum = 32768.0f;        // of a step's weights: each then fits fp16
 constexpr int kJoinWarps = 4;
+constexpr int kMostSplits = 64;             // ranges of the tokens
+constexpr int kMostParts = 2 * kMostSplits;  // of a row: both row tiles may hold it
 constexpr unsigned long long kDrainLimitNs = 200ull * 1000 * 1000;
 
 struct ChunkParams {
@@ -1334,22 +1336,46 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv4_chunk_join_kernel(const C
   const int64_t next = p.twin ? kSlot : 2 * kSlot;
   const float* slot = p.partial + ((int64_t)bh * p.items + row / kCtaRows) * p.splits * 2 * kSlot +
                       row / kTileRows % 2 * kSlot;
-  float top = -INFINITY;
-  for (int s = 0; s < parts; ++s) top = fmaxf(top, __ldcg(slot + s * next + r));
-  float sum = 0.0f, x[V];
+  // Maxima and sums a lane a part, then the parts' O in their order, with all loads known
+  // beforehand: part by part, each behind the last one's maximum, 30 of them took 20 us.
+  float factor[kMostParts / 32], top = -INFINITY, sum = 0.0f;
+  bool seen = false;
+#pragma unroll
+  for (int k = 0; k < kMostParts / 32; ++k) {
+    const int s = k * 32 + lane;
+    factor[k] = s < parts ? __ldcg(slot + s * next + r) : -INFINITY;
+    top = fmaxf(top, factor[k]);
+  }
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+#pragma unroll
+  for (int k = 0; k < kMostParts / 32; ++k) {
+    const int s = k * 32 + lane;
+    const float l = s < parts ? __ldcg(slot + s * next + kTileRows + r) : 0.0f;
+    const bool there = !(factor[k] == -INFINITY && l == 0.0f);  // (else nothing was written behind)
+    seen = seen || there;
+    factor[k] = there ? ex2_approx(factor[k] - top) : 0.0f;
+    if (there) sum = fmaf(l, factor[k], sum);
+  }
+  seen = __any_sync(0xffffffffu, seen);
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  float x[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) x[i] = 0.0f;
-  bool seen = false;
-#pragma unroll 4
-  for (int s = 0; s < parts; ++s) {
-    const float m = __ldcg(slot + s * next + r), l = __ldcg(slot + s * next + kTileRows + r);
-    if (m == -INFINITY && l == 0.0f) continue;  // (nothing was written behind them)
-    seen = true;
-    const float f = ex2_approx(m - top);
-    sum = fmaf(l, f, sum);
-    const float* o = slot + s * next + 2 * kTileRows + r * D + lane * V;
+  const float* from = slot + 2 * kTileRows + r * D + lane * V;
 #pragma unroll
-    for (int i = 0; i < V; ++i) x[i] = fmaf(__ldcg(o + i), f, x[i]);
+  for (int k = 0; k < kMostParts / 32; ++k) {
+#pragma unroll 16
+    for (int s = k * 32; s < min(parts, k * 32 + 32); ++s) {
+      const float f = __shfl_sync(0xffffffffu, factor[k], s & 31);
+      using Piece = std::conditional_t<V == 4, float4, float2>;
+      Piece v{};
+      if (f != 0.0f) v = __ldcg(reinterpret_cast<const Piece*>(from + s * next));
+      const float* vs = reinterpret_cast<const float*>(&v);
+#pragma unroll
+      for (int i = 0; i < V; ++i) x[i] = fmaf(vs[i], f, x[i]);
+    }
   }
   const float inv = seen ? 1.0f / sum : 0.0f;
   const int t = row / p.G, g = row - t * p.G;
@@ -1368,7 +1394,6 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv4_chunk_join_kernel(const C
 // How many ranges the tokens of a row tile are cut into, by sizes that the host
 // knows: waves of CTAs times the steps of each, a CTA's start counted as kStart
 // steps and the join as kJoin.
-constexpr int kMostSplits = 64;
 constexpr double kStart = 3.0, kJoin = 4.0;
 int chunk_splits(int64_t ctas, int64_t steps, int sms) {
   int best = 1;

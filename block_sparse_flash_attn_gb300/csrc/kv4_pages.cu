@@ -20,6 +20,10 @@ constexpr int kRowsThreads = 128;
 constexpr int kGiveThreads = 1024, kGiveCtas = 8;  // one cluster
 constexpr int kGiveRound = 4 * kGiveThreads;       // pages that a CTA looks at once
 constexpr int kMostRows = 16384;
+// Entries of a table that the kernel that gives pages copies itself; more are copied by a
+// launch before it.  64 x 128 entries: 8.0 us, with the launch 8.8; 256 x 128: 9.3 and 9.1; 512 x
+// 256: 14.0 and 9.7.
+constexpr int64_t kFewEntries = 1 << 14;
 constexpr int kMoveThreads = 256;
 constexpr int kMoveLoads = 4;                      // 16-byte pieces a thread in flight
 constexpr int kMoveUnit = 16 * kMoveThreads * kMoveLoads;
@@ -130,6 +134,7 @@ struct BooksParams {
   const int* parents;  // fork: [n]
   const int* counts;   // reserve: [B], or null: T each
   int T, n;
+  int copy;            // reserve: what the kernel that gives copies: refs (bit 0), the table (1)
   int* new_table;      // [n][columns], rows new_stride apart
   int64_t new_stride;
   int* new_lengths;
@@ -262,22 +267,38 @@ __global__ void __launch_bounds__(kGiveThreads, 1) kv4_give_kernel(const BooksPa
     at += wants(i, column);
   }
   if (tid == 0) starts[p.n] = wanted;
+  if (!FORK && (p.copy & 2)) {  // (rows by CTAs; ordered before what is given by the barriers)
+    const int64_t entries = (int64_t)p.B * p.columns;
+    for (int64_t i = (int64_t)rank * kGiveThreads + tid; i < entries; i += kGiveCtas * kGiveThreads) {
+      const int64_t b = i / p.columns, k = i - b * p.columns;
+      p.new_table[b * p.new_stride + k] = load(p.table + b * p.table_stride + k);
+    }
+  }
   // this CTA's pages
+  const int* refs = !FORK && (p.copy & 1) ? p.refs : p.new_refs;
   const int64_t part = ((int64_t)p.c.pages + kGiveCtas * 4 - 1) / (kGiveCtas * 4) * 4;
   const int64_t begin = min((int64_t)p.c.pages, part * rank), end = min((int64_t)p.c.pages, begin + part);
+  const bool whole = (reinterpret_cast<uintptr_t>(refs) & 15u) == 0;
   auto free4 = [&](int64_t page) -> uint32_t {  // of pages page .. page + 3
     uint32_t m = 0;
     if (page + 4 <= end) {
-      const int4 v = load(reinterpret_cast<const int4*>(p.new_refs + page));
+      int4 v;
+      if (whole)
+        v = load(reinterpret_cast<const int4*>(refs + page));
+      else
+        v = make_int4(load(refs + page), load(refs + page + 1), load(refs + page + 2), load(refs + page + 3));
       m = (v.x == 0 ? 1u : 0u) | (v.y == 0 ? 2u : 0u) | (v.z == 0 ? 4u : 0u) | (v.w == 0 ? 8u : 0u);
     } else {
       for (int k = 0; k < 4; ++k)
-        if (page + k < end && load(p.new_refs + page + k) == 0) m |= 1u << k;
+        if (page + k < end && load(refs + page + k) == 0) m |= 1u << k;
     }
     return m;
   };
   int free = 0;
   for (int64_t page = begin + 4 * tid; page < end; page += kGiveRound) free += __popc(free4(page));
+  if (refs != p.new_refs)
+    for (int64_t page = begin + tid; page < end; page += kGiveThreads)
+      p.new_refs[page] = load(refs + page);
   int all_free = 0;
   prefix_of<kGiveThreads>(free, slots, all_free);
   if (tid == 0) mine = all_free;
@@ -402,7 +423,11 @@ __global__ void __launch_bounds__(kGiveThreads, 1) kv4_compact_kernel(const Book
     if (moving) p.src[high_before + (k >> 16)] = (int)page;
     low_before += sum & 0xFFFF;
     high_before += sum >> 16;
-    if (page < end) p.map[page] = in_use ? (int)page : -1;
+    if (page < end) {
+      const int holders = load(p.refs + page);
+      p.map[page] = in_use ? (int)page : -1;
+      if (p.new_refs != p.refs) p.new_refs[page] = holders;
+    }
   }
   __threadfence();
   cluster_barrier();
@@ -532,6 +557,8 @@ bsattn_status bsattn_kv4_fork(const bsattn_kv4_cache* cache, const int32_t* refs
   if (overlap(new_table, (int64_t)n * columns * 4, block_table,
               table_bytes(B, table_stride, columns)) ||
       overlap(new_lengths, (int64_t)n * 4, lengths, (int64_t)B * 4) ||
+      overlap(new_lengths, (int64_t)n * 4, parents, (int64_t)n * 4) ||
+      overlap(new_table, (int64_t)n * columns * 4, parents, (int64_t)n * 4) ||
       (new_refs != refs &&
        overlap(new_refs, (int64_t)cache->pages * 4, refs, (int64_t)cache->pages * 4)))
     return BSATTN_ERR_INVALID_ARG;
@@ -599,7 +626,10 @@ bsattn_status bsattn_kv4_reserve(const bsattn_kv4_cache* cache, const int32_t* r
   p.new_refs = new_refs;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
-  if (!same || new_refs != refs) e = launch_books_copy(p, !same, device_sm_count(dev), st);
+  if (same || (int64_t)B * columns <= kFewEntries)
+    p.copy = (same ? 0 : 2) | (new_refs != refs ? 1 : 0);
+  else
+    e = launch_books_copy(p, true, device_sm_count(dev), st);
   if (e == cudaSuccess) e = launch_give<false>(p, st);
   return from_cuda(e);
 }
@@ -654,8 +684,7 @@ bsattn_status bsattn_kv4_compact(const bsattn_kv4_cache* cache, const int32_t* r
   m.count = p.count;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
-  if (new_refs != refs) e = launch_books_copy(p, false, sms, st);
-  if (e == cudaSuccess) e = launch_cluster(kv4_compact_kernel, 0, st, p);
+  e = launch_cluster(kv4_compact_kernel, 0, st, p);
   // (at most half of the pages move)
   if (e == cudaSuccess)
     e = launch_dependent(kv4_compact_move_kernel,

@@ -16,6 +16,8 @@ the arguments themselves where that is said.  At most 16384 rows.
 """
 from __future__ import annotations
 
+import functools
+
 import torch
 
 import block_sparse_flash_attn_gb300 as _bs
@@ -24,6 +26,16 @@ from ._args import launch_on, output, pointer, tensor
 from .kv4 import Kv4Cache, _cache, _table
 
 _I32 = torch.int32
+
+
+@functools.lru_cache(maxsize=256)
+def _fork_workspace(n):
+    return _bs.load().bsattn_kv4_fork_workspace(n)
+
+
+@functools.lru_cache(maxsize=256)
+def _compact_workspace(pages):
+    return _bs.load().bsattn_kv4_compact_workspace(pages)
 
 
 def _refs(cache, refs):
@@ -97,10 +109,9 @@ def kv4_fork(cache: Kv4Cache, refs: torch.Tensor, block_table: torch.Tensor,
         new_refs = output("refs", new_refs, _I32, (cache.pages,), cache.device)
         if B == 0 or n == 0:
             raise ValueError("there must be rows")
-        lib = _bs.load()
-        nbytes = lib.bsattn_kv4_fork_workspace(n)
+        nbytes = _fork_workspace(n)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=cache.device)
-        _bs._check(lib.bsattn_kv4_fork(
+        _bs._check(_bs.load().bsattn_kv4_fork(
             cache._ref, refs.data_ptr(), block_table.data_ptr(), stride, columns,
             lengths.data_ptr(), B, parents.data_ptr(), n, table.data_ptr(), new_lengths.data_ptr(),
             new_refs.data_ptr(), ws.data_ptr(), nbytes, on), "bsattn_kv4_fork")
@@ -155,10 +166,9 @@ def kv4_compact(cache: Kv4Cache, refs: torch.Tensor, block_table: torch.Tensor, 
         table = _table_out("block_table", table, block_table)
         new_refs = output("refs", new_refs, _I32, (cache.pages,), cache.device)
         page_map = output("page_map", page_map, _I32, (cache.pages,), cache.device)
-        lib = _bs.load()
-        nbytes = lib.bsattn_kv4_compact_workspace(cache.pages)
+        nbytes = _compact_workspace(cache.pages)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=cache.device)
-        _bs._check(lib.bsattn_kv4_compact(
+        _bs._check(_bs.load().bsattn_kv4_compact(
             cache._ref, refs.data_ptr(), block_table.data_ptr(), block_table.stride(0), columns, B,
             table.data_ptr(), table.stride(0), new_refs.data_ptr(), page_map.data_ptr(),
             ws.data_ptr(), nbytes, on), "bsattn_kv4_compact")

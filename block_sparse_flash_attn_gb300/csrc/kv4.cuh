@@ -73,6 +73,9 @@ bsattn_status kv4_few_rows(const FewRows& f, void* workspace, size_t workspace_b
 constexpr float kTanh0 = 0.99999994f, kTanh1 = -0.333326757f, kTanh2 = 0.13321048f,
                 kTanh3 = -0.0531143136f, kTanh4 = 0.0190932993f, kTanh5 = -0.00435529929f;
 constexpr float kTanhRange = 0.8f;
+// The same for |y| <= 0.3, off by 6e-8.
+constexpr float kNear0 = 1.0f, kNear1 = -0.333329618f, kNear2 = 0.133125976f, kNear3 = -0.0502224378f;
+constexpr float kNearRange = 0.3f;
 
 // tanh(y): (1 - e) / (1 + e), e = exp(-2 |y|); off by 2^-22 of one or less.
 __device__ __forceinline__ float tanh_any(float y) {

@@ -887,12 +887,27 @@ __device__ __forceinline__ void score(const ChunkParams& p, const ChunkRow& r, u
 #pragma unroll
         for (int i = 0; i < 32; i += 2)
           big = max3(big, fabsf(__uint_as_float(x[i])), fabsf(__uint_as_float(x[i + 1])));
-        // (by the row's own scores: no vote, another row's leave its bits alone)
-        if (!(big * k <= kTanhRange)) {
+        // By the row's own scores: no vote, another row's leave its bits alone.  Most rows of
+        // most models are near zero; 1024 tokens behind 15360, capped: 437 us without a shorter
+        // polynomial for them, 390 with it (441 if it is not the first that is asked for).
+        // (Not where 1 / cap leaves the factor few bits.)
+        if (big * k <= kNearRange && k > 1e-30f) {
+          const uint64_t k2 = f2_pack(k, k);
+          const float n0 = kNear0 * p.cap_log2, n1 = kNear1 * p.cap_log2, n2 = kNear2 * p.cap_log2,
+                      n3 = kNear3 * p.cap_log2;
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            x[i] = __float_as_uint(p.cap_log2 * tanh_any(__uint_as_float(x[i]) * k));
-        } else {
+          for (int i = 0; i < 32; i += 2) {
+            const uint64_t y = f2_mul(f2_pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), k2),
+                           u = f2_mul(y, y);
+            uint64_t a = f2_fma(f2_pack(n3, n3), u, f2_pack(n2, n2));
+            a = f2_fma(a, u, f2_pack(n1, n1));
+            a = f2_fma(a, u, f2_pack(n0, n0));
+            a = f2_mul(a, y);
+            float lo, hi;
+            f2_unpack(a, lo, hi);
+            x[i] = __float_as_uint(lo), x[i + 1] = __float_as_uint(hi);
+          }
+        } else if (big * k <= kTanhRange) {
           const uint64_t k2 = f2_pack(k, k), f2 = f2_pack(f, f);
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
@@ -908,6 +923,10 @@ __device__ __forceinline__ void score(const ChunkParams& p, const ChunkRow& r, u
             f2_unpack(a, lo, hi);
             x[i] = __float_as_uint(lo), x[i + 1] = __float_as_uint(hi);
           }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            x[i] = __float_as_uint(p.cap_log2 * tanh_any(__uint_as_float(x[i]) * k));
         }
       } else {
 #pragma unroll

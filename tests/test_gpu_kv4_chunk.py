@@ -122,6 +122,16 @@ def test_scale(bs, scale, T):
                ref.attn_chunk(cache, q, table, [300, 100], scale=scale, **more))
 
 
+@pytest.mark.parametrize("cap", [1e-30, 1e-3, 0.5, 3.0, 1e6, 1e30])
+@pytest.mark.parametrize("T", [3, 80])
+@pytest.mark.parametrize("size", [1e-12, 1.0])
+def test_caps_of_any_size(bs, T, cap, size):
+    """All forms of the tanh, and caps that leave scores as they are."""
+    cache, table, q, n = _case(bs, 2, 2, 64, 32, 32, T, [300, 100])
+    q = (q.float() * size).bfloat16()
+    _check(bs.kv4_attn_chunk(cache, q, table, n, cap=cap), ref.attn_chunk(cache, q, table, [300, 100], cap=cap))
+
+
 def _put(cache, table, name, b, h, token, x):
     """Token `token` of sequence b holds x [D]."""
     code, scales = ref.quantise(x[None].bfloat16(), cache.group)

@@ -37,6 +37,14 @@ __device__ __forceinline__ int peer_int(const int* shared, int rank) {
   return v;
 }
 
+// A cluster's barrier in two halves.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 __device__ __forceinline__ int pages_for(int64_t tokens, int log_page) {
   return (int)((tokens + (1ll << log_page) - 1) >> log_page);
 }
@@ -224,6 +232,7 @@ __global__ void __launch_bounds__(kRowsThreads) kv4_fork_kernel(const BooksParam
 template <bool FORK>
 __global__ void __launch_bounds__(kGiveThreads, 1) kv4_give_kernel(const BooksParams p) {
   extern __shared__ int starts[];  // [n + 1] pages wanted by the rows before
+  int* columns = starts + p.n + 1;  // [n] the rows' first new columns
   __shared__ int slots[kGiveThreads / 32];
   __shared__ int mine;
   wait_for_previous_launch();
@@ -244,37 +253,8 @@ __global__ void __launch_bounds__(kGiveThreads, 1) kv4_give_kernel(const BooksPa
     column = (int)min(have, (int64_t)p.columns);
     return (int)(min(all, (int64_t)p.columns) - column);
   };
-  // rows: consecutive ones a thread
-  const int per = (p.n + kGiveThreads - 1) / kGiveThreads;
-  int sum = 0, column;
-  bool late = false;  // a row whose table is too short
-  for (int k = 0; k < per; ++k) {
-    const int i = tid * per + k;
-    if (i < p.n) sum += wants(i, column);
-    if (!FORK && i < p.n) {
-      const int64_t all = (int64_t)max(load(p.lengths + i), 0) +
-                          (p.counts ? max(load(p.counts + i), 0) : p.T);
-      late = late || all > (int64_t)p.columns << p.c.log_page;
-    }
-  }
-  if (late && rank == 0) p.c.report();
-  int wanted;
-  int at = prefix_of<kGiveThreads>(sum, slots, wanted);
-  for (int k = 0; k < per; ++k) {
-    const int i = tid * per + k;
-    if (i >= p.n) break;
-    starts[i] = at;
-    at += wants(i, column);
-  }
-  if (tid == 0) starts[p.n] = wanted;
-  if (!FORK && (p.copy & 2)) {  // (rows by CTAs; ordered before what is given by the barriers)
-    const int64_t entries = (int64_t)p.B * p.columns;
-    for (int64_t i = (int64_t)rank * kGiveThreads + tid; i < entries; i += kGiveCtas * kGiveThreads) {
-      const int64_t b = i / p.columns, k = i - b * p.columns;
-      p.new_table[b * p.new_stride + k] = load(p.table + b * p.table_stride + k);
-    }
-  }
-  // this CTA's pages
+  // this CTA's pages; those of the first round stay in registers, and are asked for before
+  // the rows
   const int* refs = !FORK && (p.copy & 1) ? p.refs : p.new_refs;
   const int64_t part = ((int64_t)p.c.pages + kGiveCtas * 4 - 1) / (kGiveCtas * 4) * 4;
   const int64_t begin = min((int64_t)p.c.pages, part * rank), end = min((int64_t)p.c.pages, begin + part);
@@ -294,8 +274,44 @@ __global__ void __launch_bounds__(kGiveThreads, 1) kv4_give_kernel(const BooksPa
     }
     return m;
   };
-  int free = 0;
-  for (int64_t page = begin + 4 * tid; page < end; page += kGiveRound) free += __popc(free4(page));
+  const uint32_t first_free = begin + 4 * tid < end ? free4(begin + 4 * tid) : 0u;
+  // rows: consecutive ones a thread
+  const int per = (p.n + kGiveThreads - 1) / kGiveThreads;
+  int sum = 0;
+  bool late = false;  // a row whose table is too short
+  for (int k = 0; k < per; ++k) {
+    const int i = tid * per + k;
+    if (i >= p.n) break;
+    const int wanted = wants(i, columns[i]);
+    starts[i] = wanted;
+    sum += wanted;
+    if (!FORK) {
+      const int64_t all = (int64_t)max(load(p.lengths + i), 0) +
+                          (p.counts ? max(load(p.counts + i), 0) : p.T);
+      late = late || all > (int64_t)p.columns << p.c.log_page;
+    }
+  }
+  if (late && rank == 0) p.c.report();
+  int wanted;
+  int at = prefix_of<kGiveThreads>(sum, slots, wanted);
+  for (int k = 0; k < per; ++k) {
+    const int i = tid * per + k;
+    if (i >= p.n) break;
+    const int mine = starts[i];
+    starts[i] = at;
+    at += mine;
+  }
+  if (tid == 0) starts[p.n] = wanted;
+  if (!FORK && (p.copy & 2)) {  // (rows by CTAs; ordered before what is given by the barriers)
+    const int64_t entries = (int64_t)p.B * p.columns;
+    for (int64_t i = (int64_t)rank * kGiveThreads + tid; i < entries; i += kGiveCtas * kGiveThreads) {
+      const int64_t b = i / p.columns, k = i - b * p.columns;
+      p.new_table[b * p.new_stride + k] = load(p.table + b * p.table_stride + k);
+    }
+  }
+  int free = __popc(first_free);
+  for (int64_t page = begin + 4 * tid + kGiveRound; page < end; page += kGiveRound)
+    free += __popc(free4(page));
   if (refs != p.new_refs)
     for (int64_t page = begin + tid; page < end; page += kGiveThreads)
       p.new_refs[page] = load(refs + page);
@@ -311,23 +327,21 @@ __global__ void __launch_bounds__(kGiveThreads, 1) kv4_give_kernel(const BooksPa
     before += k < rank ? x : 0;
     all_free += x;
   }
-  cluster_barrier();  // no CTA leaves while another reads its memory
+  cluster_arrive();  // no CTA leaves while another reads its memory
   auto give = [&](int k, int page) {  // the k-th wanted page
     int lo = 0, hi = p.n;             // last row with starts[row] <= k
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (starts[mid] <= k) lo = mid; else hi = mid;
     }
-    int column;
-    wants(lo, column);
-    p.new_table[lo * p.new_stride + column + (k - starts[lo])] = page;
+    p.new_table[lo * p.new_stride + columns[lo] + (k - starts[lo])] = page;
     if (FORK) p.dst[lo] = page;
     if (page >= 0) p.new_refs[page] = 1;
   };
   // (a round's pages are looked at by all threads before any of them is given)
   for (int64_t first = begin; first < end && before < wanted; first += kGiveRound) {
     const int64_t page = first + 4 * tid;
-    uint32_t m = page < end ? free4(page) : 0u;
+    uint32_t m = first == begin ? first_free : page < end ? free4(page) : 0u;
     int found;
     int k = before + prefix_of<kGiveThreads>(__popc(m), slots, found);
     before += found;
@@ -339,6 +353,8 @@ __global__ void __launch_bounds__(kGiveThreads, 1) kv4_give_kernel(const BooksPa
     for (int k = all_free + rank * kGiveThreads + tid; k < wanted; k += kGiveCtas * kGiveThreads)
       give(k, -1);
   }
+  __syncwarp();
+  cluster_wait();
 }
 
 // Copies of the pages that are not full, as far as they are filled: a CTA a row,
@@ -486,9 +502,9 @@ cudaError_t launch_cluster(Kernel kernel, size_t smem, cudaStream_t st, const Bo
 template <bool FORK>
 cudaError_t launch_give(const BooksParams& p, cudaStream_t st) {
   constexpr auto kernel = kv4_give_kernel<FORK>;
-  const cudaError_t e = allow_shared_memory<kernel>((kMostRows + 1) * (int)sizeof(int));
+  const cudaError_t e = allow_shared_memory<kernel>((2 * kMostRows + 1) * (int)sizeof(int));
   if (e != cudaSuccess) return e;
-  return launch_cluster(kernel, (size_t)(p.n + 1) * sizeof(int), st, p);
+  return launch_cluster(kernel, (size_t)(2 * p.n + 1) * sizeof(int), st, p);
 }
 
 cudaError_t launch_books_copy(const BooksParams& p, bool with_table, int sms, cudaStream_t st) {

@@ -71,7 +71,7 @@ constexpr int kKeys = 128;                  // tokens that are expanded at once:
 // with halves by its own other half too, and scores stay in registers while they are
 // capped and biased, at a third more shared-memory reads (Q is read for 64 tokens).  4096
 // tokens behind 61440: 3.5 ms as steps, 4.0 as halves; capped scores, 1024 behind 15360:
-// 541 and 432 us.
+// 541 and 432 us (390 since).
 template <bool SCORED>
 constexpr int kPiece = SCORED ? 64 : 128;
 template <bool SCORED>
@@ -1428,7 +1428,7 @@ int chunk_splits(int64_t ctas, int64_t steps, int sms) {
 
 // Up to so many rows a key/value head the kernels of kv4_attn.cuh take the call: they read
 // the cache once for 16 rows, with less to set up.  8 sequences of 49152 tokens, 8 heads of
-// 128: 16 rows 161 us, 32 rows 276, 48 rows 430; here 240 to 270 us for 17 to 128.  Where there
+// 128: 16 rows 161 us, 32 rows 276, 48 rows 430; here 215 to 245 us for 17 to 128.  Where there
 // is little to read in all (16 rows' tiles times tokens) they take more: 6 heads of 1000
 // tokens, 17 to 96 rows: 12 us, here 19; 128 rows 14 and 22; 128 heads of 1000 tokens, 32
 // rows: 24 and 27, 40 rows: 40 and 27.

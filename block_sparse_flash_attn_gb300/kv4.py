@@ -1,4 +1,4 @@
-"""A paged key/value cache in 4 bits, and attention over it token by token.
+"""A paged key/value cache in 4 bits, and attention over it: token by token, and of chunks.
 
     cache = bsattn.Kv4Cache(pages, kv_heads, head_dim)
     bsattn.kv4_append(cache, k, v, block_table, lengths)       # new tokens, prompts or single ones
@@ -249,9 +249,9 @@ def kv4_attn_chunk(cache: Kv4Cache, q: torch.Tensor, block_table: torch.Tensor,
     lengths[b] - counts[b] + t (lengths counts the new tokens too) and sees the cached
     tokens up to there, and those at positions below prefix[b].  A query behind the
     count has O = 0, LSE = -inf.  counts, prefix: int32 [B].
-    cap: scores become cap * tanh(score / cap).  slopes: fp32 [H]; slopes[h] times the
-    distance of query and key is taken off the (capped) scores.  scale: default
-    1/sqrt(head_dim)."""
+    cap: scores become cap * tanh(score / cap); 1e-30 to 1e30.  slopes: fp32 [H], finite;
+    slopes[h] times the distance of query and key is taken off the (capped) scores.
+    scale: default 1/sqrt(head_dim).  At most 2^24 - 256 queries a key/value head."""
     _cache(cache)
     B, stride, columns = _table(cache, block_table, lengths, counts)
     tensor("q", q, (_BF16,), device=cache.device)

@@ -4,6 +4,10 @@ Tolerances: the bounds that _ops_ref.attn_chunk derives (32-bit scores and sums,
 and weights of 11 bits, of 8 where the values of 32 tokens lie far apart), plus the
 output's own rounding."""
 import math
+import pathlib
+import subprocess
+import sys
+import threading
 
 import pytest
 import torch
@@ -181,7 +185,7 @@ def test_values_of_other_sizes(bs, T, power):
 
 
 @pytest.mark.parametrize("T", [3, 90])
-@pytest.mark.parametrize("power", [-40, 40])
+@pytest.mark.parametrize("power", [-98, -40, 40, 108])
 def test_keys_of_other_sizes(bs, T, power):
     """All keys very large or small, and queries the other way."""
     cache, table, q, n = _case(bs, 1, 2, 128, 32, 64, T, [300])
@@ -439,4 +443,75 @@ def test_chain(bs):
     assert bool((refs[:used] > 0).all()) and not bool(refs[used:].any())
     state = step(table, lengths, refs, 2, [2, 2, 1])
     assert ref.count_refs(cache, state[0].tolist(), state[1].tolist()) == state[2].tolist()
+    bs.kv4_status(cache)
+
+
+FIRST_USE = """
+import torch
+import block_sparse_flash_attn_gb300 as bs
+cache, other = (bs.Kv4Cache(200, 2, 64, page_size=32, group=32) for _ in range(2))
+refs = torch.zeros(200, dtype=torch.int32, device="cuda")
+empty = torch.full((3, 50), -1, dtype=torch.int32, device="cuda")
+zero = torch.zeros(3, dtype=torch.int32, device="cuda")
+counts = torch.tensor([700, 30, 333], dtype=torch.int32, device="cuda")
+parents = torch.tensor([2, 0, 0, -1], dtype=torch.int32, device="cuda")
+pages = torch.arange(200, dtype=torch.int32, device="cuda")
+k, v = (torch.randn(3, 2, 700, 64, device="cuda").bfloat16() for _ in "kv")
+q = torch.randn(3, 4, 700, 64, device="cuda").bfloat16()
+slopes = torch.rand(4, device="cuda")
+
+
+def step():
+    table, held = bs.kv4_reserve(cache, refs, empty, zero, counts)
+    bs.kv4_append(cache, k, v, table, zero, counts)
+    got = []
+    for T in (1, 4, 30, 700):
+        x = q[:, :, -T:].contiguous()
+        got += bs.kv4_attn_chunk(cache, x, table, counts, torch.clamp(counts, max=T))
+        got += bs.kv4_attn_chunk(cache, x, table, counts, torch.clamp(counts, max=T), cap=5.0, slopes=slopes)
+    table, lengths, held = bs.kv4_fork(cache, held, table, counts, parents)
+    table, held, moved = bs.kv4_compact(cache, held, table)
+    bs.kv4_copy(cache, pages, pages, to=other)
+    return got + [table, lengths, held, moved] + list(bs.kv4_read(other, table, torch.zeros_like(lengths), 700))
+
+
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = step()
+graph.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in got]
+assert all(torch.equal(a, b) for a, b in zip(got, step()))
+bs.kv4_status(cache)
+"""
+
+
+def test_first_use_inside_a_capture(bs):
+    """A process whose first calls are captured into a graph."""
+    root = pathlib.Path(__file__).resolve().parents[1]
+    subprocess.run([sys.executable, "-c", FIRST_USE], cwd=root, check=True, timeout=120)
+
+
+def test_calls_from_several_threads(bs):
+    """Each thread with its stream, one cache, calls of both kernels."""
+    cache, table, q, n = _case(bs, 2, 4, 64, 64, 32, 50, [700, 300])
+    few = q[:, :, -2:].contiguous()
+    want = [bs.kv4_attn_chunk(cache, x, table, n, cap=7.0) for x in (q, few)]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work():
+        stream = torch.cuda.Stream()
+        for _ in range(10):
+            for x, w in zip((q, few), want):
+                got = bs.kv4_attn_chunk(cache, x, table, n, cap=7.0, stream=stream)
+                stream.synchronize()
+                bad.extend(1 for a, b in zip(got, w) if not torch.equal(a, b))
+
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
     bs.kv4_status(cache)

@@ -1358,7 +1358,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv4_chunk_join_kernel(const C
   // Maxima and sums a lane a part, then the parts' O in their order, with all loads known
   // beforehand: part by part, each behind the last one's maximum, 30 of them took 20 us.
   float factor[kMostParts / 32], top = -INFINITY, sum = 0.0f;
-  bool seen = false;
+  uint32_t written[kMostParts / 32], seen = 0;  // parts that have an O
 #pragma unroll
   for (int k = 0; k < kMostParts / 32; ++k) {
     const int s = k * 32 + lane;
@@ -1371,12 +1371,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv4_chunk_join_kernel(const C
   for (int k = 0; k < kMostParts / 32; ++k) {
     const int s = k * 32 + lane;
     const float l = s < parts ? __ldcg(slot + s * next + kTileRows + r) : 0.0f;
-    const bool there = !(factor[k] == -INFINITY && l == 0.0f);  // (else nothing was written behind)
-    seen = seen || there;
+    const bool there = !(factor[k] == -INFINITY && l == 0.0f);
+    written[k] = __ballot_sync(0xffffffffu, there);
+    seen |= written[k];
     factor[k] = there ? ex2_approx(factor[k] - top) : 0.0f;
     if (there) sum = fmaf(l, factor[k], sum);
   }
-  seen = __any_sync(0xffffffffu, seen);
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   float x[V];
@@ -1390,13 +1390,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv4_chunk_join_kernel(const C
       const float f = __shfl_sync(0xffffffffu, factor[k], s & 31);
       using Piece = std::conditional_t<V == 4, float4, float2>;
       Piece v{};
-      if (f != 0.0f) v = __ldcg(reinterpret_cast<const Piece*>(from + s * next));
+      // (whatever its factor: a value that is not a number is not one times zero)
+      if (written[k] >> (s & 31) & 1u) v = __ldcg(reinterpret_cast<const Piece*>(from + s * next));
       const float* vs = reinterpret_cast<const float*>(&v);
 #pragma unroll
       for (int i = 0; i < V; ++i) x[i] = fmaf(vs[i], f, x[i]);
     }
   }
-  const float inv = seen ? 1.0f / sum : 0.0f;
+  const float inv = seen != 0u ? 1.0f / sum : 0.0f;
   const int t = row / p.G, g = row - t * p.G;
   const int64_t at = ((int64_t)b * p.H + h * p.G + g) * p.T + t;
 #pragma unroll
@@ -1407,7 +1408,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv4_chunk_join_kernel(const C
     else
       static_cast<__nv_bfloat16*>(p.out)[to] = __float2bfloat16_rn(x[i] * inv);
   }
-  if (lane == 0) p.lse[at] = seen ? (top + __log2f(sum)) * kLn2 : -INFINITY;
+  if (lane == 0) p.lse[at] = seen != 0u ? (top + __log2f(sum)) * kLn2 : -INFINITY;
 }
 
 // How many ranges the tokens of a row tile are cut into, by sizes that the host

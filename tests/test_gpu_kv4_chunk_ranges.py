@@ -1,0 +1,49 @@
+"""Chunk attention over the 4-bit cache where it can go wrong at the ends of its ranges: values that
+are not numbers far behind the queries."""
+import pytest
+import torch
+
+from test_gpu_kv4_chunk import ROOM, _case, bs  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("wide", [False, True], ids=["exact", "wide"])
+@pytest.mark.parametrize("T,B", [(2, 1), (8, 1), (20, 1), (60, 1), (300, 1), (300, 80)])
+def test_values_far_away_that_are_not_numbers(bs, T, B, wide):  # noqa: F811
+    """A group of channels that stands for NaN spoils those channels of all queries that see it, also
+    where a bias by distance leaves it no weight at all, in one range of tokens or in many."""
+    n, D, group = 2900, 128, 32
+    cache, table, q, lengths = _case(bs, 1, 2, D, 64, group, T, [n], columns=ROOM // 64 if wide else None)
+    table, q, lengths = table.expand(B, -1), q.expand(B, -1, -1, -1).contiguous(), lengths.expand(B).contiguous()
+    slopes = torch.tensor([0.5, 0.25], device="cuda")
+    clean = bs.kv4_attn_chunk(cache, q, table, lengths, slopes=slopes)
+    assert bool(clean[0].isfinite().all())
+    cache.v_scales[int(table[0, 0]), 0, 3, 2] = float("nan")
+    o, lse = bs.kv4_attn_chunk(cache, q, table, lengths, slopes=slopes)
+    bad = torch.zeros(D, dtype=torch.bool, device="cuda")
+    bad[2 * group:3 * group] = True
+    assert torch.equal(o.isnan(), bad.expand_as(o))
+    assert torch.equal(lse, clean[1])
+    # (the token's neighbours may be held otherwise: both are within their bounds of the same)
+    assert float((o - clean[0])[..., ~bad].abs().max()) < 0.1
+
+
+@pytest.mark.parametrize("T", [3, 5, 8])
+@pytest.mark.parametrize("more", [{}, dict(cap=20.0), dict(slopes=True)], ids=["plain", "cap", "slopes"])
+def test_few_rows_that_do_not_see_a_value(bs, T, more):  # noqa: F811
+    n, D, group = 700, 128, 32
+    cache, table, q, lengths = _case(bs, 1, 2, D, 64, group, T, [n])
+    if "slopes" in more:
+        more = dict(slopes=torch.tensor([0.5, 0.01], device="cuda"))
+    clean = bs.kv4_attn_chunk(cache, q, table, lengths, **more)
+    token = n - T // 2 - 1
+    cache.v_scales[int(table[0, token // 64]), 0, token % 64, 2] = float("nan")
+    o, lse = bs.kv4_attn_chunk(cache, q, table, lengths, **more)
+    sees = (n - T + torch.arange(T, device="cuda")) >= token
+    assert 0 < int(sees.sum()) < T
+    bad = torch.zeros(T, D, dtype=torch.bool, device="cuda")
+    bad[sees, 2 * group:3 * group] = True
+    assert torch.equal(o[0, 0].isnan(), bad) and torch.equal(o[0, 1].isnan(), bad)
+    assert torch.equal(lse, clean[1])
+    assert float((o[:, :, ~sees].double() - clean[0][:, :, ~sees].double()).abs().max()) < 0.1

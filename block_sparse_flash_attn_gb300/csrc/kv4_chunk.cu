@@ -27,7 +27,7 @@
 //   it and less loses bits); both are powers of two that the softmax puts back.  So
 //   scores and lse are those of 32-bit products, at the cost of a ninth step for 8.
 // - V in fp16, rounded once (2^-11), beside a power of two that the CTA takes from its
-//   first step: the mean exponent of its groups of channels goes to 2^-10.  Where a
+//   first step (1 to 2^-20): the mean exponent of its groups of channels goes to 2^-10.  Where a
 //   group of 32 tokens passes 2^-6 there, or 2^-14 the other way, those tokens are taken
 //   in bf16 (2^-8), their weights too.  Weights are off by that rounding, or by 2^-25
 //   beside a row's largest weight of one or more.
@@ -506,7 +506,9 @@ __device__ void run_expand_values(const ChunkParams& p, const ChunkWork& w, Chun
     sum = n = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) sum += bars->v_exponents[i][0], n += bars->v_exponents[i][1];
-    const int mean = n > 0 ? min(max(sum / n, 20), 240) : 127;
+    // Powers of 1 to 2^-20 only, for means of 2^-10 to 2^10: beside others the sums of large values
+    // (below 2^104, 2^13 tokens, weights of 2^10) would pass 2^127, and small ones (2^-100) 2^-126.
+    const int mean = n > 0 ? min(max(sum / n, 127 - 10), 127 + 10) : 127;
     v_scale = __uint_as_float((uint32_t)(254 - 10 - mean) << 23);
     if (lane == 0 && warp == 0) bars->v_scale = 1.0f / v_scale;
   }

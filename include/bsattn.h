@@ -609,7 +609,8 @@ bsattn_status bsattn_kv4_attn(const bsattn_kv4_cache* cache, const void* q, int 
  *              magnitude (one that is not finite spoils its own query only); query head
  *              h reads key/value head h / (H / kv_heads).  B * kv_heads at most 65535,
  *              H / kv_heads * T at most 2^24 - 256, columns * page_size at most 2^31 - 256.
- *   cache      values below 2^104 in magnitude, |scale| sum |q k| of a query and a key
+ *   cache      values below 2^104 in magnitude (2^13 tokens of them can be added up; what
+ *              is below 2^-100 may count as zero), |scale| sum |q k| of a query and a key
  *              below 2^112; a group whose step or least value is not finite stands for
  *              NaN, which spoils its channels (values) or all of them (keys) of the
  *              queries that see it.
@@ -617,9 +618,9 @@ bsattn_status bsattn_kv4_attn(const bsattn_kv4_cache* cache, const void* q, int 
  *              few tokens, all arithmetic is as in bsattn_kv4_attn.  Else scores are as good
  *              as 32-bit products; a key's channels below 2^-17 of the largest key of 32
  *              tokens (positions 32 i to 32 i + 31) count with fewer bits.  Values are
- *              rounded to fp16, beside a power of two taken from 128 tokens, where those of
- *              32 tokens lie within 2^4 of those either way, else to bf16; weights to the
- *              same type.
+ *              rounded to fp16, beside the mean magnitude of 128 tokens (2^-10 to 2^10), where
+ *              those of 32 tokens lie within 2^4 of it either way, else to bf16; weights to
+ *              the same type.
  *   lengths    cached tokens, the new ones included.
  *   counts     new tokens of each sequence, or null: T.
  *   prefix     device int32 [B]: positions below it are seen by every query; or null.

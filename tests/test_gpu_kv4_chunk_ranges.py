@@ -1,9 +1,11 @@
 """Chunk attention over the 4-bit cache where it can go wrong at the ends of its ranges: values that
-are not numbers far behind the queries."""
+are not numbers far behind the queries, values of very different sizes together."""
 import pytest
 import torch
 
-from test_gpu_kv4_chunk import ROOM, _case, bs  # noqa: F401
+import _ops_ref as ref
+from _ops_ref import UBF
+from test_gpu_kv4_chunk import ROOM, _case, _check, _put, bs  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -47,3 +49,36 @@ def test_few_rows_that_do_not_see_a_value(bs, T, more):  # noqa: F811
     assert torch.equal(o[0, 0].isnan(), bad) and torch.equal(o[0, 1].isnan(), bad)
     assert torch.equal(lse, clean[1])
     assert float((o[:, :, ~sees].double() - clean[0][:, :, ~sees].double()).abs().max()) < 0.1
+
+
+@pytest.mark.parametrize("T", [3, 90, 300])
+@pytest.mark.parametrize("slopes", [False, True])
+def test_one_value_far_above_the_others(bs, T, slopes):  # noqa: F811
+    """All values near 2^-60 but one token's near 2^100: the output is that token's.  It is off by the
+    rounding of its weight and of the value (2^-8 each), of the output, and by the score's error."""
+    n = 400
+    cache, table, q, lengths = _case(bs, 1, 2, 64, 32, 32, T, [n])
+    cache.v_scales.mul_(2.0 ** -60)
+    _put(cache, table, "v", 0, 0, 5, torch.randn(64, generator=ref.gen(3), device="cuda") * 2.0 ** 100)
+    s = torch.tensor([0.01, 0.003], device="cuda") if slopes else None
+    o, _ = bs.kv4_attn_chunk(cache, q, table, lengths, slopes=s)
+    want, _, _, tol_l = ref.attn_chunk(cache, q, table, [n], slopes=s)
+    assert bool(o.isfinite().all())
+    tol = (2 * 2.0 ** -8 + UBF + 2 * tol_l[..., None]) * want.abs() + 2.0 ** -30 * want.abs().amax(-1, keepdim=True)
+    assert bool(((o.double() - want).abs() <= tol).all()), float(((o.double() - want).abs() / tol).max())
+
+
+@pytest.mark.parametrize("slopes", [False, True])
+def test_values_far_below_those_of_later_tokens(bs, slopes):  # noqa: F811
+    """Queries that see small values only, beside queries (of the same tiles) that see very large ones."""
+    n = 200
+    cache, table, q, lengths = _case(bs, 1, 1, 64, 64, 32, n, [n])
+    cache.v_scales[table[0, :2].long()] *= 2.0 ** -30
+    cache.v_scales[table[0, 2:4].long()] *= 2.0 ** 100
+    s = torch.tensor([0.01], device="cuda") if slopes else None
+    o, lse = bs.kv4_attn_chunk(cache, q, table, lengths, slopes=s)
+    early = slice(0, 128)
+    want = ref.attn_chunk(cache, q[:, :, early].contiguous(), table, [128], slopes=s, value_bits=8)
+    _check((o[:, :, early], lse[:, :, early]), want)
+    want = ref.attn_chunk(cache, q, table, [n], slopes=s, value_bits=8)
+    assert bool(((o.double() - want[0]).abs()[:, :, 128:] <= (want[2][..., None] + UBF * want[0].abs())[:, :, 128:]).all())

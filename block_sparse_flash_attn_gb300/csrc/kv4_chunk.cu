@@ -935,7 +935,7 @@ __device__ __forceinline__ void score(const ChunkParams& p, const ChunkRow& r, u
         for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
       }
       if (p.slopes) {
-        if (__any_sync(0xffffffffu, r.slope != 0.0f && past)) {
+        if (past) {  // (by the row's own place, no vote: the two forms round otherwise)
 #pragma unroll
           for (int i = 0; i < 32; ++i)
             x[i] = __float_as_uint(fmaf(-r.slope, fabsf((float)(d0 + i)), __uint_as_float(x[i])));

@@ -1,11 +1,12 @@
 """Chunk attention over the 4-bit cache where it can go wrong at the ends of its ranges: values that
-are not numbers far behind the queries, values of very different sizes together."""
+are not numbers far behind the queries, values of very different sizes together, and what one
+row's bits depend on."""
 import pytest
 import torch
 
 import _ops_ref as ref
 from _ops_ref import UBF
-from test_gpu_kv4_chunk import ROOM, _case, _check, _put, bs  # noqa: F401
+from test_gpu_kv4_chunk import ROOM, _case, _check, _i32, _put, bs  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -82,3 +83,20 @@ def test_values_far_below_those_of_later_tokens(bs, slopes):  # noqa: F811
     _check((o[:, :, early], lse[:, :, early]), want)
     want = ref.attn_chunk(cache, q, table, [n], slopes=s, value_bits=8)
     assert bool(((o.double() - want[0]).abs()[:, :, 128:] <= (want[2][..., None] + UBF * want[0].abs())[:, :, 128:]).all())
+
+
+def test_another_heads_slope_leaves_a_row_alone(bs):  # noqa: F811
+    """12 heads: 16 rows in a row are 8 heads of one token and 8 of the next.  The prefix ends
+    behind the first of the two tokens, so that only it sees keys behind itself."""
+    G, T, B = 12, 12, 8
+    lengths = [701 + 3 * b for b in range(B)]
+    cache, table, q, n = _case(bs, 1, G, 64, 64, 32, T, lengths)
+    prefix = _i32([m - T + 3 for m in lengths])  # token 1 sees token 2, which sees itself
+    slopes = torch.tensor([0.37, 0.21, 0.13, 0.09] + [0.0] * 8, device="cuda")
+    want = bs.kv4_attn_chunk(cache, q, table, n, prefix=prefix, slopes=slopes, out_f32=True)
+    slopes[9] = 0.3
+    got = bs.kv4_attn_chunk(cache, q, table, n, prefix=prefix, slopes=slopes, out_f32=True)
+    assert not torch.equal(got[0][:, 9], want[0][:, 9])
+    others = [h for h in range(G) if h != 9]
+    assert torch.equal(got[1][:, others], want[1][:, others])
+    assert torch.equal(got[0][:, others], want[0][:, others])

@@ -47,7 +47,7 @@ EXPORTS = ["bsattn_plan", "bsattn_plan_csr", "bsattn_plan_schedule", "bsattn_fwd
            "bsattn_kv4_attn", "bsattn_kv4_attn_workspace", "bsattn_kv4_status",
            "bsattn_kv4_attn_chunk", "bsattn_kv4_attn_chunk_workspace", "bsattn_kv4_copy",
            "bsattn_kv4_fork", "bsattn_kv4_fork_workspace", "bsattn_kv4_reserve",
-           "bsattn_kv4_compact", "bsattn_kv4_compact_workspace"]
+           "bsattn_kv4_release", "bsattn_kv4_compact", "bsattn_kv4_compact_workspace"]
 
 
 class BsattnError(RuntimeError):
@@ -149,6 +149,7 @@ def load():
             ("kv4_fork", [vp, vp] + table + [vp, i32, vp, i32, vp, vp, vp, vp, size, vp], i32),
             ("kv4_fork_workspace", [i32], size),
             ("kv4_reserve", [vp, vp] + table + [vp, vp, i32, i32, vp, i64, vp, vp], i32),
+            ("kv4_release", [vp, vp] + table + [vp, vp, i32, vp, i64, vp, vp], i32),
             ("kv4_compact", [vp, vp] + table + [i32, vp, i64, vp, vp, vp, size, vp], i32),
             ("kv4_compact_workspace", [i32], size),
             ("kv4_status", [vp, vp], i32)):

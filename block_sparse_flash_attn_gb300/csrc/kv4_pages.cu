@@ -9,6 +9,7 @@
 //
 // Bound: launches and dependent loads for the books (refs and tables are some
 // hundred KB at most), memory for the pages that move.
+#include <algorithm>
 #include <cstdint>
 
 #include "kv4.cuh"
@@ -141,6 +142,7 @@ struct BooksParams {
   int B;
   const int* parents;  // fork: [n]
   const int* counts;   // reserve: [B], or null: T each
+  const int* held;     // release: [B]
   int T, n;
   int copy;            // reserve: what the kernel that gives copies: refs (bit 0), the table (1)
   int* new_table;      // [n][columns], rows new_stride apart
@@ -153,18 +155,38 @@ struct BooksParams {
   int* count;          // compact: the number of moves
 };
 
-// new_refs and new_table begin as refs and table (reserve, compact; fork: refs).
+// new_refs and new_table begin as refs and table (fork: refs; reserve, release: both).
 __global__ void __launch_bounds__(kRowsThreads) kv4_books_copy_kernel(const BooksParams p,
-                                                                      int with_table) {
+                                                                      int with_refs, int with_table) {
   wait_for_previous_launch();
   allow_next_launch();
   const int64_t at = (int64_t)blockIdx.x * kRowsThreads + threadIdx.x;
   const int64_t threads = (int64_t)gridDim.x * kRowsThreads;
-  for (int64_t i = at; i < p.c.pages; i += threads) p.new_refs[i] = load(p.refs + i);
+  if (with_refs)
+    for (int64_t i = at; i < p.c.pages; i += threads) p.new_refs[i] = load(p.refs + i);
   if (!with_table) return;
   for (int64_t i = at; i < (int64_t)p.B * p.columns; i += threads) {
     const int64_t b = i / p.columns, column = i - b * p.columns;
     p.new_table[b * p.new_stride + column] = load(p.table + b * p.table_stride + column);
+  }
+}
+
+// A CTA a row: what it holds behind its length is given back.  (Launches before it copied
+// new_refs and new_table; without a table the entries are the old one's.)
+__global__ void __launch_bounds__(kRowsThreads) kv4_release_kernel(const BooksParams p) {
+  wait_for_previous_launch();
+  allow_next_launch();
+  const int b = blockIdx.x;
+  const int64_t tokens = max(load(p.lengths + b), 0), most = (int64_t)p.columns << p.c.log_page;
+  const int64_t held = max(load(p.held + b), 0);
+  if (held > most && threadIdx.x == 0) p.c.report();
+  const int first = pages_for(min(tokens, most), p.c.log_page), end = pages_for(min(held, most), p.c.log_page);
+  const int* from = p.new_table ? p.new_table + b * p.new_stride : p.table + b * p.table_stride;
+  for (int k = first + threadIdx.x; k < end; k += kRowsThreads) {
+    const int pg = load(from + k);
+    if (pg >= p.c.pages) p.c.report();
+    if (pg >= 0 && pg < p.c.pages) atomicAdd(p.new_refs + pg, -1);
+    if (p.new_table) p.new_table[b * p.new_stride + k] = -1;
   }
 }
 
@@ -507,13 +529,12 @@ cudaError_t launch_give(const BooksParams& p, cudaStream_t st) {
   return launch_cluster(kernel, (size_t)(2 * p.n + 1) * sizeof(int), st, p);
 }
 
-cudaError_t launch_books_copy(const BooksParams& p, bool with_table, int sms, cudaStream_t st) {
-  const int64_t most = with_table && (int64_t)p.B * p.columns > p.c.pages
-                           ? (int64_t)p.B * p.columns
-                           : p.c.pages;
-  const int64_t ctas = (most + kRowsThreads - 1) / kRowsThreads, cap = (int64_t)sms * 16;
-  return launch_dependent(kv4_books_copy_kernel, dim3((unsigned)(ctas < cap ? ctas : cap)),
-                          dim3(kRowsThreads), 0, st, p, with_table ? 1 : 0);
+cudaError_t launch_books_copy(const BooksParams& p, bool with_refs, bool with_table, int sms,
+                              cudaStream_t st) {
+  const int64_t refs = with_refs ? p.c.pages : 0, entries = with_table ? (int64_t)p.B * p.columns : 0;
+  const int64_t ctas = (std::max(refs, entries) + kRowsThreads - 1) / kRowsThreads;
+  return launch_dependent(kv4_books_copy_kernel, dim3((unsigned)std::min(ctas, (int64_t)sms * 16)),
+                          dim3(kRowsThreads), 0, st, p, with_refs ? 1 : 0, with_table ? 1 : 0);
 }
 
 bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
@@ -596,7 +617,7 @@ bsattn_status bsattn_kv4_fork(const bsattn_kv4_cache* cache, const int32_t* refs
   p.dst = p.src + n;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
-  if (new_refs != refs) e = launch_books_copy(p, false, device_sm_count(dev), st);
+  if (new_refs != refs) e = launch_books_copy(p, true, false, device_sm_count(dev), st);
   if (e == cudaSuccess)
     e = launch_dependent(kv4_fork_kernel, dim3(n + B), dim3(kRowsThreads), 0, st, p);
   if (e == cudaSuccess) e = launch_give<true>(p, st);
@@ -645,8 +666,47 @@ bsattn_status bsattn_kv4_reserve(const bsattn_kv4_cache* cache, const int32_t* r
   if (same || (int64_t)B * columns <= kFewEntries)
     p.copy = (same ? 0 : 2) | (new_refs != refs ? 1 : 0);
   else
-    e = launch_books_copy(p, true, device_sm_count(dev), st);
+    e = launch_books_copy(p, new_refs != refs, true, device_sm_count(dev), st);
   if (e == cudaSuccess) e = launch_give<false>(p, st);
+  return from_cuda(e);
+}
+
+bsattn_status bsattn_kv4_release(const bsattn_kv4_cache* cache, const int32_t* refs,
+                                 const int32_t* block_table, int64_t table_stride, int columns,
+                                 const int32_t* lengths, const int32_t* held, int B,
+                                 int32_t* new_table, int64_t new_stride, int32_t* new_refs,
+                                 void* stream) {
+  BooksParams p{};
+  const bsattn_status rc = check_cache(cache, &p.c);
+  if (rc != BSATTN_OK) return rc;
+  if (!ints_ok(refs) || !ints_ok(block_table) || !ints_ok(lengths) || !ints_ok(held) ||
+      (new_table && !ints_ok(new_table)) || !ints_ok(new_refs) || !aligned16(new_refs))
+    return BSATTN_ERR_INVALID_ARG;
+  if (B <= 0 || columns <= 0 || table_stride < 0 || (new_table && B > 1 && new_stride < columns))
+    return BSATTN_ERR_INVALID_ARG;
+  if (B > kMostRows) return BSATTN_ERR_UNSUPPORTED;
+  const bool same = !new_table || (new_table == block_table && (new_stride == table_stride || B == 1));
+  if ((!same && overlap(new_table, table_bytes(B, new_stride, columns), block_table,
+                        table_bytes(B, table_stride, columns))) ||
+      (new_refs != refs &&
+       overlap(new_refs, (int64_t)cache->pages * 4, refs, (int64_t)cache->pages * 4)))
+    return BSATTN_ERR_INVALID_ARG;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return BSATTN_ERR_CUDA;
+  p.refs = refs;
+  p.table = block_table;
+  p.table_stride = table_stride;
+  p.columns = columns;
+  p.lengths = lengths;
+  p.held = held;
+  p.B = B;
+  p.new_table = new_table;
+  p.new_stride = new_stride;
+  p.new_refs = new_refs;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  if (!same || new_refs != refs) e = launch_books_copy(p, new_refs != refs, !same, device_sm_count(dev), st);
+  if (e == cudaSuccess) e = launch_dependent(kv4_release_kernel, dim3(B), dim3(kRowsThreads), 0, st, p);
   return from_cuda(e);
 }
 

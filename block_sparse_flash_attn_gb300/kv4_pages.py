@@ -10,9 +10,17 @@ that fork, copied, and moved together.
     bsattn.kv4_status(cache)                       # raises if pages ran out or a page was bad
 
 refs counts the table's rows that hold a page; one that none holds is free.  A page
-that is not full belongs to one row.  The lowest free page is given out first, in the
-order of rows and columns.  Results are new tensors, or those of `out`, which may be
-the arguments themselves where that is said.  At most 16384 rows.
+that is not full belongs to one row (so no row becomes shorter than where it forked).
+Where rows did become shorter than pages were reserved for (drafts that were refused),
+the next call that takes `held` needs it, or those pages are lost:
+
+    table, refs = bsattn.kv4_reserve(cache, refs, table, lengths, counts, held=held)
+    held = lengths + counts                        # what the rows have pages for
+    lengths += accepted                            # at most counts
+
+The lowest free page is given out first, in the order of rows and columns.  Results
+are new tensors, or those of `out`, which may be the arguments themselves where that
+is said.  At most 16384 rows.
 """
 from __future__ import annotations
 
@@ -60,6 +68,15 @@ def _table_out(name, t, block_table):
     return t
 
 
+def _release(cache, refs, block_table, stride, columns, lengths, held, table, new_refs, on):
+    """Pages behind the lengths, up to those of `held` tokens, lose their rows (table: None, or for the rows
+    without them)."""
+    _bs._check(_bs.load().bsattn_kv4_release(
+        cache._ref, refs.data_ptr(), block_table.data_ptr(), stride, columns, lengths.data_ptr(),
+        held.data_ptr(), block_table.shape[0], pointer(table), 0 if table is None else table.stride(0),
+        new_refs.data_ptr(), on), "bsattn_kv4_release")
+
+
 def kv4_copy(cache: Kv4Cache, src: torch.Tensor, dst: torch.Tensor, to: Kv4Cache | None = None,
              stream=None) -> None:
     """Copy pages src[i] of the cache to pages dst[i] of `to` (default: the same cache; another
@@ -84,7 +101,8 @@ def kv4_copy(cache: Kv4Cache, src: torch.Tensor, dst: torch.Tensor, to: Kv4Cache
 
 
 def kv4_fork(cache: Kv4Cache, refs: torch.Tensor, block_table: torch.Tensor,
-             lengths: torch.Tensor, parents: torch.Tensor, out=None, stream=None):
+             lengths: torch.Tensor, parents: torch.Tensor, out=None, stream=None,
+             held: torch.Tensor | None = None):
     """(block_table [n, columns], lengths [n], refs): new row i continues row parents[i] of the
     old table; a row that none continues ends, and row i is empty where parents[i] is
     negative.  So samples fork, beams change places, and ended sequences give their pages
@@ -94,13 +112,16 @@ def kv4_fork(cache: Kv4Cache, refs: torch.Tensor, block_table: torch.Tensor,
 
     refs: int32 [pages], block_table [B, columns] and lengths [B]: all rows that refs
     counts; parents: CUDA int32 [n].  out: (block_table, lengths, refs), of which refs may
-    be the argument itself."""
+    be the argument itself.  held: int32 [B], the tokens that the old rows have pages for,
+    where that is more than lengths: those behind the lengths are given back."""
     _cache(cache)
     B, stride, columns = _table(cache, block_table, lengths)
     _refs(cache, refs)
     tensor("parents", parents, (_I32,), device=cache.device)
     if parents.dim() != 1:
         raise ValueError("parents must be [n]")
+    if held is not None:
+        tensor("held", held, (_I32,), (B,), cache.device)
     n = parents.numel()
     table, new_lengths, new_refs = _outputs(out, ("block_table", "lengths", "refs"))
     with launch_on(cache.device, stream) as on:
@@ -109,6 +130,9 @@ def kv4_fork(cache: Kv4Cache, refs: torch.Tensor, block_table: torch.Tensor,
         new_refs = output("refs", new_refs, _I32, (cache.pages,), cache.device)
         if B == 0 or n == 0:
             raise ValueError("there must be rows")
+        if held is not None:
+            _release(cache, refs, block_table, stride, columns, lengths, held, None, new_refs, on)
+            refs = new_refs
         nbytes = _fork_workspace(n)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=cache.device)
         _bs._check(_bs.load().bsattn_kv4_fork(
@@ -119,11 +143,17 @@ def kv4_fork(cache: Kv4Cache, refs: torch.Tensor, block_table: torch.Tensor,
 
 
 def kv4_reserve(cache: Kv4Cache, refs: torch.Tensor, block_table: torch.Tensor,
-                lengths: torch.Tensor, counts: torch.Tensor | int, out=None, stream=None):
+                lengths: torch.Tensor, counts: torch.Tensor | int, out=None, stream=None,
+                held: torch.Tensor | None = None):
     """(block_table, refs) with pages for counts[b] (int32 [B], or one number) more tokens of
     every row: the columns behind those of lengths[b] tokens get new pages, whatever they
     held.  Where pages run out the last ones are -1.  out: (block_table, refs), which may be
-    the arguments themselves."""
+    the arguments themselves.
+
+    held: int32 [B], the tokens that the rows have pages for already, where that is more than
+    lengths: lengths + counts of the call before, if drafts were refused since, or of this very
+    call, if it ran out of pages and is tried again in place.  Those pages are given back
+    first, so that refs counts what the table holds behind the call."""
     _cache(cache)
     T = 0
     if isinstance(counts, int):
@@ -134,12 +164,17 @@ def kv4_reserve(cache: Kv4Cache, refs: torch.Tensor, block_table: torch.Tensor,
         raise TypeError("counts must be a tensor or an int")
     B, stride, columns = _table(cache, block_table, lengths, counts)
     _refs(cache, refs)
+    if held is not None:
+        tensor("held", held, (_I32,), (B,), cache.device)
     table, new_refs = _outputs(out, ("block_table", "refs"))
     if B == 0:
         raise ValueError("there must be rows")
     with launch_on(cache.device, stream) as on:
         table = _table_out("block_table", table, block_table)
         new_refs = output("refs", new_refs, _I32, (cache.pages,), cache.device)
+        if held is not None:
+            _release(cache, refs, block_table, stride, columns, lengths, held, table, new_refs, on)
+            refs, block_table, stride = new_refs, table, table.stride(0)
         _bs._check(_bs.load().bsattn_kv4_reserve(
             cache._ref, refs.data_ptr(), block_table.data_ptr(), stride, columns,
             lengths.data_ptr(), pointer(counts), T, B, table.data_ptr(), table.stride(0),

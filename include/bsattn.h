@@ -644,8 +644,10 @@ bsattn_status bsattn_kv4_attn_chunk(const bsattn_kv4_cache* cache, const void* q
  * The pages of a cache.
  *
  *   refs       device int32 [pages]: the rows of the block table that hold a page (as far
- *              as their lengths reach).  A page that none holds is free.
- * A page that is not full belongs to one row.  What is given out is the lowest free
+ *              as their lengths reach, those with pages reserved for more as far as these).
+ *              A page that none holds is free.
+ * A page that is not full belongs to one row (so no row becomes shorter than where it
+ * forked).  What is given out is the lowest free
  * page, rows in ascending order and in each its columns.  Where there are too few, the
  * last ones get -1 and bsattn_kv4_status reports it, as it does bad pages and lengths
  * behind the table.  new_* receive the books after the call; `refs` may be updated in
@@ -660,7 +662,8 @@ bsattn_status bsattn_kv4_attn_chunk(const bsattn_kv4_cache* cache, const void* q
  * continues end.  Row i is empty where parents[i] is negative.  Full pages are shared;
  * of a last page that is not full the first child keeps the parent's, the others get
  * copies of the tokens in it.  Pages of rows that end are free for those copies.
- *   block_table, lengths [B]  the old rows, all that refs counts.
+ *   block_table, lengths [B]  the old rows, all that refs counts; pages that they hold behind
+ *              their lengths are lost, if bsattn_kv4_release has not given them back.
  *   new_table  device int32 [n][columns], -1 behind a row's pages; not the old one.
  *   new_lengths, new_refs  device int32 [n], [pages]; new_refs 16-byte aligned.
  *   workspace  bsattn_kv4_fork_workspace bytes, 16-byte aligned.
@@ -669,6 +672,15 @@ bsattn_status bsattn_kv4_attn_chunk(const bsattn_kv4_cache* cache, const void* q
  * ceil(lengths / page_size) up to ceil((lengths + counts) / page_size) - 1 get one each,
  * whatever they held.  The table may be updated in place (new_table = block_table).
  *   new_table  device int32 [B][columns], rows new_stride apart; new_refs 16-byte aligned.
+ *
+ * bsattn_kv4_release -- rows that became shorter (drafts that were refused, a reservation that
+ * ran out and is tried again) give back what they hold behind their lengths: the pages of
+ * columns ceil(lengths / page_size) up to ceil(held / page_size) - 1 lose a holder, the
+ * columns become -1.  Those that are -1 already are skipped.  For bsattn_kv4_reserve and
+ * bsattn_kv4_fork, which count such pages in no row.
+ *   held       device int32 [B]: the tokens that a row has pages for: lengths + counts of the
+ *              reservation before.
+ *   new_table  as for reserve; or null, where refs alone are wanted (before a fork).
  *
  * bsattn_kv4_compact -- with n pages in use, those at n and above move to the free ones
  * below n, both in ascending order.  The table may be updated in place.
@@ -688,6 +700,11 @@ bsattn_status bsattn_kv4_fork(const bsattn_kv4_cache* cache, const int32_t* refs
 bsattn_status bsattn_kv4_reserve(const bsattn_kv4_cache* cache, const int32_t* refs,
                                  const int32_t* block_table, int64_t table_stride, int columns,
                                  const int32_t* lengths, const int32_t* counts, int T, int B,
+                                 int32_t* new_table, int64_t new_stride, int32_t* new_refs,
+                                 void* stream);
+bsattn_status bsattn_kv4_release(const bsattn_kv4_cache* cache, const int32_t* refs,
+                                 const int32_t* block_table, int64_t table_stride, int columns,
+                                 const int32_t* lengths, const int32_t* held, int B,
                                  int32_t* new_table, int64_t new_stride, int32_t* new_refs,
                                  void* stream);
 size_t bsattn_kv4_compact_workspace(int pages);

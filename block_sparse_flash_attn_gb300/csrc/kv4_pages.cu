@@ -101,7 +101,7 @@ __device__ __forceinline__ void move_unit(const PageMove& p, int64_t at) {
   const int from = load(p.src + i), to = load(p.dst + i);
   if (from < 0 || to < 0) return;  // (an entry of no move)
   if (from >= p.from.pages || to >= p.to.pages) {
-    if (threadIdx.x == 0) p.to.report();
+    if (threadIdx.x == 0) p.from.report(), p.to.report();
     return;
   }
   int b = 0;

@@ -82,7 +82,7 @@ def kv4_copy(cache: Kv4Cache, src: torch.Tensor, dst: torch.Tensor, to: Kv4Cache
     """Copy pages src[i] of the cache to pages dst[i] of `to` (default: the same cache; another
     one has the same sizes but for its number of pages).  src, dst: CUDA int32 [n]; a pair
     with a negative page is no move.  A page must not be written twice in one call, nor be
-    read where it is written."""
+    read where it is written.  A page that is not there is reported by both caches."""
     to = _cache(cache) if to is None else _cache(to)
     tensor("src", src, (_I32,), device=cache.device)
     if src.dim() != 1:

@@ -655,7 +655,8 @@ bsattn_status bsattn_kv4_attn_chunk(const bsattn_kv4_cache* cache, const void* q
  *
  * bsattn_kv4_copy -- page src[i] of `from` to page dst[i] of `to` (one cache, or two of the
  * same sizes): codes, scales, means.  A pair with a negative page is no move.  A page
- * must not be written twice in one call, nor be read where it is written.
+ * must not be written twice in one call, nor be read where it is written.  A page that is
+ * not there is reported by both caches.
  *
  * bsattn_kv4_fork -- new row i continues row parents[i] of the old table: several rows
  * may continue one (samples, beams), rows may change places, and rows that none

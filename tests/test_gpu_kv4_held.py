@@ -1,5 +1,5 @@
 """Pages behind a sequence that became shorter (drafts that were refused, reservations that ran out):
-given back, so that refs is what the tables hold."""
+given back, so that refs is what the tables hold; and who reports copies of bad pages."""
 import random
 
 import pytest
@@ -159,3 +159,14 @@ def test_refusals(bs):  # noqa: F811
     with pytest.raises(ValueError, match="held"):
         bs.kv4_fork(cache, refs, table, n, n, held=_i32([1, 2]))
     bs.kv4_status(cache)
+
+
+@pytest.mark.parametrize("src,dst", [(99, 1), (1, 99)])
+def test_copies_of_bad_pages_are_reported_by_both_caches(bs, src, dst):  # noqa: F811
+    cache, to = _cache(bs, 8), _cache(bs, 8, seed=2)
+    state = _state(to)
+    bs.kv4_copy(cache, _i32([src]), _i32([dst]), to=to)
+    for c in (cache, to):
+        with pytest.raises(bs.BsattnError, match="page"):
+            bs.kv4_status(c)
+    assert _same(to, state)

@@ -1,6 +1,6 @@
 """Chunk attention over the 4-bit cache where it can go wrong at the ends of its ranges: values that
-are not numbers far behind the queries, values of very different sizes together, and what one
-row's bits depend on."""
+are not numbers far behind the queries, values of very different sizes together, what one row's
+bits depend on, and errors by their norms (closer than bounds for each entry can be)."""
 import pytest
 import torch
 
@@ -100,3 +100,52 @@ def test_another_heads_slope_leaves_a_row_alone(bs):  # noqa: F811
     others = [h for h in range(G) if h != 9]
     assert torch.equal(got[1][:, others], want[1][:, others])
     assert torch.equal(got[0][:, others], want[0][:, others])
+
+
+@pytest.mark.parametrize("option", [{}, dict(cap=20.0)], ids=["plain", "cap"])
+def test_tables_much_wider_than_their_sequences(bs, option):  # noqa: F811
+    lengths = [150, 700, 161]
+    cache, table, q, n = _case(bs, 2, 2, 128, 64, 32, 150, lengths, columns=ROOM // 64)
+    _check(bs.kv4_attn_chunk(cache, q, table, n, **option), ref.attn_chunk(cache, q, table, lengths, cap=option.get("cap")))
+
+
+HEADS = [(64, 64), (64, 32), (128, 128), (128, 64), (128, 32)]
+
+
+@pytest.mark.parametrize("D,group", HEADS)
+@pytest.mark.parametrize("n", [150, 2000])
+@pytest.mark.parametrize("form", ["steps", "halves"])
+def test_errors_by_norm(bs, D, group, n, form):  # noqa: F811
+    """Weights and values are rounded to 11 bits each, independently: the root mean square of such a
+    rounding is at most 2^-11 / sqrt(3) of the number, 2.8e-4, of both 4.0e-4, and of a sum over tokens with
+    it.  (Rounded to 8 bits one of them alone would be 1.6e-3.)  A score sums D products in 9 steps of 32
+    bits: off by at most 9 * 2^-23 of sum |q k| scale, here about 10, so by 1.1e-5, and a lse, which is a
+    mean of those, by less."""
+    cache, table, q, lengths = _case(bs, 2, 2, D, 64, group, 150, [n])
+    more = dict(slopes=torch.zeros(4, device="cuda")) if form == "halves" else {}
+    o, lse = bs.kv4_attn_chunk(cache, q, table, lengths, out_f32=True, **more)
+    want, l_ref = ref.attn_chunk(cache, q, table, [n])[:2]
+    off = float((o - want).norm() / want.norm())
+    assert off <= 5e-4, off
+    off = float((lse - l_ref).square().mean().sqrt())
+    assert off <= 1.1e-5, off
+
+
+@pytest.mark.parametrize("D,group", HEADS)
+@pytest.mark.parametrize("form", ["steps", "halves"])
+def test_keys_with_a_common_offset(bs, D, group, form):  # noqa: F811
+    """Keys near 8, queries of one sign: scores near 100 are their groups' sums.  c and the sums of q are held
+    to 2^-22 each, their low halves' product is left out (2^-22), the sums of q are 32-bit ones (7 * 2^-24):
+    1.2e-6 of a score; 9 steps of 32 bits: 9 * 2^-23, 1.1e-6; the argument of exp2, its maximum and the lse: 5
+    roundings of 2^-24, 0.3e-6.  Of 110 at most: 2.9e-4.  (High halves alone: 2^-12 of a score and more.)"""
+    cache, table, q, lengths = _case(bs, 2, 2, D, 64, group, 150, [700])
+    x = (8 + 0.5 * torch.randn(cache.pages, 2, 64, D, generator=ref.gen(8), device="cuda")).bfloat16()
+    code, scales = ref.quantise(x, group)
+    cache.k_codes.copy_(ref.pack(code))
+    cache.k_scales.copy_(scales)
+    q = q.abs()
+    more = dict(slopes=torch.zeros(4, device="cuda")) if form == "halves" else {}
+    lse = bs.kv4_attn_chunk(cache, q, table, lengths, **more)[1]
+    l_ref = ref.attn_chunk(cache, q, table, [700])[1]
+    off = float((lse - l_ref).square().mean().sqrt())
+    assert off <= 3e-4, (off, float(l_ref.max()))

@@ -335,24 +335,6 @@ __device__ __forceinline__ void tmem_st16x2_16(uint32_t taddr, const uint32_t* r
 }
 
 template <int kSplit>
-__device__ __forceinline__ void tmem_ld16x2_8(uint32_t taddr, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x32bx2.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8], %9;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7])
-      : "r"(taddr), "n"(kSplit));
-}
-
-template <int kSplit>
-__device__ __forceinline__ void tmem_st16x2_8(uint32_t taddr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.16x32bx2.x8.b32 [%0], %9, {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "n"(kSplit)
-      : "memory");
-}
-
-template <int kSplit>
 __device__ __forceinline__ void tmem_ld16x2_1(uint32_t taddr, uint32_t* r) {
   asm volatile("tcgen05.ld.sync.aligned.16x32bx2.x1.b32 {%0}, [%1], %2;"
                : "=r"(r[0])

@@ -23,16 +23,17 @@
 //   The second sum is one more 16-channel step of the same product: c and the sums
 //   of q are split into two fp16 each, (q hi, q lo, q hi) beside (c hi, c hi, c lo),
 //   off by 2^-22 of a product.  Queries are bf16, exact in fp16 beside their
-//   row's largest; keys are taken beside the largest of 32 tokens (what is 2^-17 of
-//   it and less loses bits); both are powers of two that the softmax puts back.  So
-//   scores and lse are those of 32-bit products, at the cost of a ninth step for 8.
+//   row's largest; keys are taken beside the largest of 32 tokens (held to 2^-17 of it,
+//   exactly where a group's step is 2^-10 of it or more); both are powers of two that
+//   the softmax puts back.  So scores and lse are those of 32-bit products, at the cost of
+//   a ninth step for 8.
 // - V in fp16, rounded once (2^-11), beside a power of two that the CTA takes from its
-//   first step (1 to 2^-20): the mean exponent of its groups of channels goes to 2^-10.  Where a
-//   group of 32 tokens passes 2^-6 there, or 2^-14 the other way, those tokens are taken
-//   in bf16 (2^-8), their weights too.  Weights are off by that rounding, or by 2^-25
+//   first step (1 to 2^-20): the mean exponent of its groups of channels goes to 2^-10.
+//   Where a group of 32 tokens passes 2^-6 there, or 2^-14 the other way, those tokens are
+//   taken in bf16 (2^-8), their weights too.  Weights are off by that rounding, or by 2^-25
 //   beside a row's largest weight of one or more.
 //
-// Work of a CTA (896 threads, one CTA an SM, 211 KB of shared memory):
+// Work of a CTA (896 threads, one CTA an SM, 218 KB of shared memory for heads of 128):
 //   warps 0-7, 8-15   softmax of the first and the second 128 rows: 16 rows a warp, two
 //                     threads a row, a half of the tokens and of the channels each
 //   warps 16-19       the keys' expansion, 32 tokens a warp
@@ -1433,8 +1434,9 @@ int chunk_splits(int64_t ctas, int64_t steps, int sms) {
 // the cache once for 16 rows, with less to set up.  8 sequences of 49152 tokens, 8 heads of
 // 128: 16 rows 161 us, 32 rows 276, 48 rows 430; here 215 to 245 us for 17 to 128.  Where there
 // is little to read in all (16 rows' tiles times tokens) they take more: 6 heads of 1000
-// tokens, 17 to 96 rows: 12 us, here 19; 128 rows 14 and 22; 128 heads of 1000 tokens, 32
-// rows: 24 and 27, 40 rows: 40 and 27.
+// tokens, 17 to 96 rows: 12 us, here 19; 128 rows 14 and 22; 128 heads of 1000 tokens, 40
+// rows: 40 and 27.  (The border lies below where the two meet: the last ones' 32 rows, 256000
+// tiles times tokens, take 27 here, 24 there.)  Tokens are those that the table has room for.
 constexpr int64_t kFewRows = 16, kMostFewRows = 128, kLittle = 3 << 16;
 constexpr int kMostFewRowsBatch = 4096;
 bool few_rows(int B, int kv_heads, int64_t rows, int64_t tokens) {

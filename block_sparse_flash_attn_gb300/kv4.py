@@ -251,7 +251,12 @@ def kv4_attn_chunk(cache: Kv4Cache, q: torch.Tensor, block_table: torch.Tensor,
     count has O = 0, LSE = -inf.  counts, prefix: int32 [B].
     cap: scores become cap * tanh(score / cap); 1e-30 to 1e30.  slopes: fp32 [H], finite;
     slopes[h] times the distance of query and key is taken off the (capped) scores.
-    scale: default 1/sqrt(head_dim).  At most 2^24 - 256 queries a key/value head."""
+    scale: default 1/sqrt(head_dim).  At most 2^24 - 256 queries a key/value head.
+
+    Up to 16 queries a key/value head (and up to 128 where the table has room for few
+    tokens) the arithmetic is kv4_attn's; above, scores are 32-bit ones, but weights and values
+    are rounded to 11 bits (8 where the values of 32 tokens lie far from the others'), for
+    out_f32 too."""
     _cache(cache)
     B, stride, columns = _table(cache, block_table, lengths, counts)
     tensor("q", q, (_BF16,), device=cache.device)
@@ -285,7 +290,8 @@ def kv4_attn_chunk(cache: Kv4Cache, q: torch.Tensor, block_table: torch.Tensor,
 
 
 def kv4_status(cache: Kv4Cache, stream=None) -> None:
-    """Wait for the stream; raise if a call met a bad page or page list since the last check."""
+    """Wait for the stream; raise if since the last check a call met a bad page, page list or length,
+    ran out of pages, or gave up a wait."""
     _cache(cache)
     with launch_on(cache.device, stream) as on:
         _bs._check(_bs.load().bsattn_kv4_status(cache._ref, on),

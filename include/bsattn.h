@@ -616,11 +616,11 @@ bsattn_status bsattn_kv4_attn(const bsattn_kv4_cache* cache, const void* q, int 
  *              queries that see it.
  *              Up to 16 rows (H / kv_heads * T), and up to 128 where the table has room for
  *              few tokens, all arithmetic is as in bsattn_kv4_attn.  Else scores are as good
- *              as 32-bit products; a key's channels below 2^-17 of the largest key of 32
- *              tokens (positions 32 i to 32 i + 31) count with fewer bits.  Values are
- *              rounded to fp16, beside the mean magnitude of 128 tokens (2^-10 to 2^10), where
- *              those of 32 tokens lie within 2^4 of it either way, else to bf16; weights to
- *              the same type.
+ *              as 32-bit products of keys that are held to 2^-17 of the largest one of their 32
+ *              tokens (positions 32 i to 32 i + 31; exactly where a group's step is 2^-10 of
+ *              that or more).  Values are rounded to fp16, beside the mean magnitude of 128
+ *              tokens (2^-10 to 2^10), where those of 32 tokens lie within 2^4 of it either
+ *              way, else to bf16; weights to the same type.
  *   lengths    cached tokens, the new ones included.
  *   counts     new tokens of each sequence, or null: T.
  *   prefix     device int32 [B]: positions below it are seen by every query; or null.

@@ -10,7 +10,8 @@ that fork, copied, and moved together.
     bsattn.kv4_status(cache)                       # raises if pages ran out or a page was bad
 
 refs counts the table's rows that hold a page; one that none holds is free.  A page
-that is not full belongs to one row (so no row becomes shorter than where it forked).
+that is not full belongs to one row (so a row that becomes shorter does not end inside
+a page that it shares).
 Where rows did become shorter than pages were reserved for (drafts that were refused),
 the next call that takes `held` needs it, or those pages are lost:
 

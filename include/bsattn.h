@@ -646,8 +646,8 @@ bsattn_status bsattn_kv4_attn_chunk(const bsattn_kv4_cache* cache, const void* q
  *   refs       device int32 [pages]: the rows of the block table that hold a page (as far
  *              as their lengths reach, those with pages reserved for more as far as these).
  *              A page that none holds is free.
- * A page that is not full belongs to one row (so no row becomes shorter than where it
- * forked).  What is given out is the lowest free
+ * A page that is not full belongs to one row (so a row that becomes shorter does not end
+ * inside a page that it shares).  What is given out is the lowest free
  * page, rows in ascending order and in each its columns.  Where there are too few, the
  * last ones get -1 and bsattn_kv4_status reports it, as it does bad pages and lengths
  * behind the table.  new_* receive the books after the call; `refs` may be updated in
